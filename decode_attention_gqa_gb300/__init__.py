@@ -1,8 +1,8 @@
 """GB300 (sm_103a) split-KV grouped-query decode attention.
 
 Thin ctypes binding over ``libattn_decode.so`` (declared in
-``include/attn_decode.h``). Every function here has the name and argument order
-of the C entry point it calls and does argument marshalling only: pointers may
+``include/attn_decode.h`` and ``include/attn_paged.h``). Every ``attn_*``
+function here has the name and argument order of the C entry point it calls and does argument marshalling only: pointers may
 be given as integers or as tensors (their ``data_ptr()`` is passed), streams as
 integers, ``torch.cuda.Stream`` objects or ``None`` (the current torch stream).
 All arithmetic runs in the library's CUDA kernels; if the library has not been
@@ -30,6 +30,10 @@ __all__ = [
     "attn_workspace_size",
     "attn_read_device_error", "attn_selftest_bounded_wait", "attn_status_string",
     "attn_last_cuda_error", "attn_version",
+    "ATTN_DEVERR_BAD_PAGE", "ATTN_TYPE_F32", "ATTN_TYPE_F16", "ATTN_TYPE_BF16", "ATTN_TYPE_E4M3",
+    "ATTN_ROPE_PLAIN", "ATTN_ROPE_LINEAR", "ATTN_ROPE_BASE", "ATTN_ROPE_BANDS",
+    "PagedCache", "Rope", "rope_append", "paged_decode_attention",
+    "attn_rope_steps", "attn_rope_append", "attn_decode_paged", "attn_paged_plan",
 ]
 
 ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_WORKSPACE, ATTN_ERR_CUDA = range(5)
@@ -40,6 +44,9 @@ ATTN_VARIANT_TCGEN05_CLUSTER = 4
 ATTN_VARIANT_TC_TILE = 5
 ATTN_KV_BF16 = 0x10
 ATTN_KV_STABLE = 0x20
+ATTN_DEVERR_BAD_PAGE = 0x4
+ATTN_TYPE_F32, ATTN_TYPE_F16, ATTN_TYPE_BF16, ATTN_TYPE_E4M3 = range(4)
+ATTN_ROPE_PLAIN, ATTN_ROPE_LINEAR, ATTN_ROPE_BASE, ATTN_ROPE_BANDS = range(4)
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _lock = threading.Lock()
@@ -112,6 +119,18 @@ def load():
         lib.attn_last_cuda_error.argtypes = []
         lib.attn_version.restype = i32
         lib.attn_version.argtypes = []
+        f64 = ctypes.c_double
+        lib.attn_rope_steps.restype = i32
+        lib.attn_rope_steps.argtypes = [i32, f64, i32, f64, f64, f64, i64, vp]
+        lib.attn_rope_append.restype = i32
+        lib.attn_rope_append.argtypes = [vp, vp, i32, vp, vp, i32, i64, vp, vp, vp, i64, i64, i64,
+                                         i32, vp, i32, vp, vp]
+        lib.attn_decode_paged.restype = i32
+        lib.attn_decode_paged.argtypes = [vp, vp, i32, vp, vp, vp, i32, i32, i32, f32, vp, i32, vp,
+                                          sz, vp]
+        lib.attn_paged_plan.restype = i32
+        lib.attn_paged_plan.argtypes = [vp, i32, i32, i32, i32, i32, i32, i32, ctypes.POINTER(i32),
+                                        ctypes.POINTER(sz)]
         _lib = lib
         return lib
 
@@ -326,3 +345,284 @@ def attn_last_cuda_error() -> int:
 
 def attn_version() -> int:
     return load().attn_version()
+
+
+# ---------------------------------------------------------------------------
+# Paged cache (include/attn_paged.h).
+# ---------------------------------------------------------------------------
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_kv_head", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("kv_type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _RopeStruct(ctypes.Structure):
+    _fields_ = [("steps", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("mscale", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
+class _RulesStruct(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("slopes", ctypes.c_void_p), ("starts", ctypes.c_void_p)]
+
+
+def attn_rope_steps(rot_dim, base, scaling=ATTN_ROPE_PLAIN, factor=1.0, low_turns=0.0,
+                    high_turns=0.0, trained_len=0):
+    """The rotary steps per position as a list of rot_dim / 2 integers below 2^64 (host-only)."""
+    out = (ctypes.c_uint64 * max(1, min(int(rot_dim), 256) // 2))()
+    _check(load().attn_rope_steps(rot_dim, base, scaling, factor, low_turns, high_turns,
+                                  trained_len, ctypes.addressof(out)), "attn_rope_steps")
+    return list(out)
+
+
+def attn_rope_append(cache, block_table, max_pages, positions, cu_tokens, n_seq, n_tokens, q, k_new,
+                     v_new, q_stride, k_stride, v_stride, in_type, q_out, n_head, rope=None,
+                     stream=None):
+    """Rotate q and k by position and write k, v into the paged cache. `cache` and `rope` are a
+    PagedCache and a Rope (or addresses of the C structures)."""
+    _check(load().attn_rope_append(_struct(cache), _ptr(block_table), max_pages, _ptr(positions),
+                                   _ptr(cu_tokens), n_seq, n_tokens, _ptr(q), _ptr(k_new),
+                                   _ptr(v_new), q_stride, k_stride, v_stride, in_type, _ptr(q_out),
+                                   n_head, _struct(rope), _stream(stream)),
+           "attn_rope_append")
+
+
+def attn_paged_plan(cache, max_pages, n_seq, n_q, n_head, window=0, n_splits=0, sm_count=0):
+    """(split count, workspace bytes) of the attn_decode_paged call with these arguments."""
+    p, ws = ctypes.c_int(0), ctypes.c_size_t(0)
+    _check(load().attn_paged_plan(_struct(cache), max_pages, n_seq, n_q, n_head, window, n_splits,
+                                  sm_count, ctypes.byref(p), ctypes.byref(ws)), "attn_paged_plan")
+    return p.value, ws.value
+
+
+def attn_decode_paged(cache, block_table, max_pages, positions, q, out, n_seq, n_q, n_head, scale,
+                      rules=None, n_splits=0, workspace=None, workspace_bytes=0, stream=None):
+    """Decode attention over the paged cache. `rules` is None or the (softcap, window, slopes,
+    starts) of attn_score_rules."""
+    if workspace is not None and not workspace_bytes and hasattr(workspace, "nbytes"):
+        workspace_bytes = workspace.nbytes
+    if rules is not None:
+        softcap, window, slopes, starts = rules
+        rules = _RulesStruct(softcap, window, _ptr(slopes), _ptr(starts))
+        rules_p = ctypes.addressof(rules)
+    else:
+        rules_p = None
+    _check(load().attn_decode_paged(_struct(cache), _ptr(block_table), max_pages, _ptr(positions),
+                                    _ptr(q), _ptr(out), n_seq, n_q, n_head, scale, rules_p,
+                                    n_splits, _ptr(workspace), workspace_bytes, _stream(stream)),
+           "attn_decode_paged")
+
+
+def _struct(x):
+    if x is None or isinstance(x, int):
+        return x
+    return x._address
+
+
+def _on_device(name, t, dtype, device):
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s" % (name, str(dtype).replace("torch.", "")))
+    if t.device != device:
+        raise ValueError("%s must be on %s, the cache's device" % (name, device))
+
+
+def _dense(name, t):
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+class PagedCache:
+    """The pool of a paged cache: k, v [n_pages, page_size, n_kv_head, head_dim] float16, bfloat16
+    or float8_e4m3fn, as torch tensors of any strides over the first three dimensions (the same for
+    both; the last one dense); k_scale, v_scale float32 [n_pages, n_kv_head] for float8_e4m3fn.
+    Holds the tensors and the C structure that describes them."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+        types = {torch.float16: ATTN_TYPE_F16, torch.bfloat16: ATTN_TYPE_BF16,
+                 torch.float8_e4m3fn: ATTN_TYPE_E4M3}
+        if k.dtype not in types or v.dtype != k.dtype:
+            raise TypeError("k and v must both be float16, bfloat16 or float8_e4m3fn")
+        if k.dim() != 4 or k.shape != v.shape:
+            raise ValueError("k and v must be [n_pages, page_size, n_kv_head, head_dim]")
+        if k.stride() != v.stride() or k.stride(3) != 1:
+            raise ValueError("k and v must have the same strides, and dense rows")
+        if v.device != k.device:
+            raise ValueError("k and v must be on the same device")
+        e4m3 = k.dtype == torch.float8_e4m3fn
+        if e4m3 != (k_scale is not None) or e4m3 != (v_scale is not None):
+            raise ValueError("k_scale and v_scale belong to a float8_e4m3fn cache, and it needs both")
+        n_pages, page_size, n_kv_head, head_dim = k.shape
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is not None:
+                _on_device(name, t, torch.float32, k.device)
+                if t.shape != (n_pages, n_kv_head):
+                    raise ValueError("%s must be [n_pages, n_kv_head]" % name)
+                _dense(name, t)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_kv_head, self.head_dim, self.page_size = n_kv_head, head_dim, page_size
+        self.device = k.device
+        self._c = _CacheStruct(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale),
+                               k.stride(0), k.stride(1), k.stride(2), n_pages, page_size, n_kv_head,
+                               head_dim, types[k.dtype], 0)
+        self._address = ctypes.addressof(self._c)
+        self._plans = {}
+
+    def _plan(self, max_pages, n_seq, n_q, n_head, window, n_splits):
+        # the plan is a function of these numbers, the pool's shape and the device
+        key = (max_pages, n_seq, n_q, n_head, window, n_splits)
+        got = self._plans.get(key)
+        if got is None:
+            if len(self._plans) >= 4096:
+                self._plans.clear()
+            got = self._plans[key] = attn_paged_plan(self, max_pages, n_seq, n_q, n_head, window,
+                                                     n_splits)
+        return got
+
+
+class Rope:
+    """The rotation of rope_append: rotary steps on the device, made by attn_rope_steps, with the
+    rotated dimensions, the layout and the magnitude of attn_rope."""
+
+    def __init__(self, rot_dim, base=10000.0, scaling=ATTN_ROPE_PLAIN, factor=1.0, low_turns=0.0,
+                 high_turns=0.0, trained_len=0, interleaved=False, mscale=1.0, device="cuda"):
+        import torch
+        steps = attn_rope_steps(rot_dim, base, scaling, factor, low_turns, high_turns, trained_len)
+        self.steps = torch.tensor([s - (1 << 64) if s >> 63 else s for s in steps],
+                                  dtype=torch.int64, device=device)
+        self.rot_dim = rot_dim
+        self._c = _RopeStruct(self.steps.data_ptr(), rot_dim, 1 if interleaved else 0, mscale, 0)
+        self._address = ctypes.addressof(self._c)
+
+
+def _same_device(device):
+    import torch
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError("the cache must be on the current CUDA device")
+
+
+def _batch(cache, block_table, positions):
+    import torch
+    _on_device("block_table", block_table, torch.int32, cache.device)
+    _on_device("positions", positions, torch.int32, cache.device)
+    if block_table.dim() != 2 or positions.dim() != 1 or positions.shape[0] != block_table.shape[0]:
+        raise ValueError("block_table must be [n_seq, max_pages] and positions [n_seq]")
+    _dense("block_table", block_table)
+    _dense("positions", positions)
+    return block_table.shape
+
+
+def _tokens(name, t, n_tokens, heads, head_dim, dtype, device):
+    _on_device(name, t, dtype, device)
+    if t.dim() != 3 or t.shape[0] != n_tokens or t.shape[2] != head_dim or \
+            (heads is not None and t.shape[1] != heads):
+        raise ValueError("%s must be [n_tokens, heads, head_dim]" % name)
+    s = t.stride()
+    if s[2] != 1 or (s[1] != head_dim and t.shape[1] > 1):
+        raise ValueError("%s must be dense within a token" % name)
+    return s[0] if n_tokens > 1 else 0
+
+
+def rope_append(cache, block_table, positions, k_new, v_new, q=None, q_out=None, rope=None,
+                cu_tokens=None, stream=None):
+    """Convenience form of attn_rope_append for torch tensors: the sizes come from the shapes --
+    k_new, v_new [n_tokens, n_kv_head, head_dim] and q [n_tokens, n_head, head_dim] (or None) of one
+    type (float32, float16 or bfloat16), dense within a token and of any stride between tokens;
+    block_table int32 [n_seq, max_pages]; positions int32 [n_seq]; cu_tokens int32 [n_seq + 1], or
+    None for the same number of tokens in every sequence. `q_out` (float32) is allocated when not
+    given. Returns q_out (None without q)."""
+    import torch
+    _same_device(cache.device)
+    n_seq, max_pages = _batch(cache, block_table, positions)
+    types = {torch.float32: ATTN_TYPE_F32, torch.float16: ATTN_TYPE_F16,
+             torch.bfloat16: ATTN_TYPE_BF16}
+    dt = k_new.dtype
+    if dt not in types:
+        raise TypeError("k_new must be float32, float16 or bfloat16")
+    n_tokens, hd = k_new.shape[0], cache.head_dim
+    ks = _tokens("k_new", k_new, n_tokens, cache.n_kv_head, hd, dt, cache.device)
+    vs = _tokens("v_new", v_new, n_tokens, cache.n_kv_head, hd, dt, cache.device)
+    qs, n_head = 0, 0
+    if q is not None:
+        qs = _tokens("q", q, n_tokens, None, hd, dt, cache.device)
+        n_head = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty(n_tokens, n_head, hd, dtype=torch.float32, device=cache.device)
+        else:
+            _on_device("q_out", q_out, torch.float32, cache.device)
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must have the shape of q")
+            _dense("q_out", q_out)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if cu_tokens is not None:
+        _on_device("cu_tokens", cu_tokens, torch.int32, cache.device)
+        if cu_tokens.shape != (n_seq + 1,):
+            raise ValueError("cu_tokens must be [n_seq + 1]")
+        _dense("cu_tokens", cu_tokens)
+    if rope is not None and rope.steps.device != cache.device:
+        raise ValueError("rope must be on the cache's device")
+    attn_rope_append(cache, block_table, max_pages, positions, cu_tokens, n_seq, n_tokens, q, k_new,
+                     v_new, qs, ks, vs, types[dt], q_out, n_head, rope, stream)
+    return q_out
+
+
+def paged_decode_attention(cache, block_table, positions, q, scale=None, out=None, softcap=0.0,
+                           slopes=None, window=0, starts=None, n_splits=0, stream=None):
+    """Convenience form of attn_decode_paged for torch tensors: q float32 [n_seq, n_head, head_dim],
+    or [n_seq, n_q, n_head, head_dim] for several causal query rows; block_table int32 [n_seq,
+    max_pages]; positions int32 [n_seq]; slopes float32 [n_head] and starts int32 [n_seq] or None.
+    scale defaults to 1/sqrt(head_dim) and `out` is allocated when not given. The workspace comes
+    from torch's allocator on the current stream (pass that stream, or None: another one would
+    not be ordered with the workspace's reuse), so captured graphs hold workspaces of their own.
+    Returns out."""
+    import torch
+    _same_device(cache.device)
+    n_seq, max_pages = _batch(cache, block_table, positions)
+    _on_device("q", q, torch.float32, cache.device)
+    shape = q.shape
+    if len(shape) == 3:
+        n_q, (qs, n_head, hd) = 1, shape
+    elif len(shape) == 4:
+        qs, n_q, n_head, hd = shape
+    else:
+        raise ValueError("q must be [n_seq, n_head, head_dim] or [n_seq, n_q, n_head, head_dim]")
+    if qs != n_seq or hd != cache.head_dim:
+        raise ValueError("q, the cache and positions disagree on n_seq or head_dim")
+    _dense("q", q)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _on_device("out", out, torch.float32, cache.device)
+        if out.shape != shape:
+            raise ValueError("out must have the shape of q")
+        _dense("out", out)
+    rules = None
+    if softcap or window or slopes is not None or starts is not None:
+        if slopes is not None:
+            _on_device("slopes", slopes, torch.float32, cache.device)
+            if slopes.shape != (n_head,):
+                raise ValueError("slopes must be [n_head]")
+            _dense("slopes", slopes)
+        if starts is not None:
+            _on_device("starts", starts, torch.int32, cache.device)
+            if starts.shape != (n_seq,):
+                raise ValueError("starts must be [n_seq]")
+            _dense("starts", starts)
+        rules = (softcap, window, slopes, starts)
+    if scale is None:
+        scale = hd ** -0.5
+    if n_seq == 0:
+        return out
+    handle = torch.cuda.current_stream().cuda_stream
+    if stream is not None and _stream(stream) != handle:
+        raise ValueError("stream must be the current stream (torch.cuda.stream selects one)")
+    n_splits, need = cache._plan(max_pages, n_seq, n_q, n_head, window, n_splits)
+    ws = torch.empty(need, dtype=torch.uint8, device=cache.device) if need else None
+    attn_decode_paged(cache, block_table, max_pages, positions, q, out, n_seq, n_q, n_head, scale,
+                      rules, n_splits, ws, need, handle)
+    return out

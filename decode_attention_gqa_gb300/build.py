@@ -1,7 +1,7 @@
 """Build libattn_decode.so in-tree with nvcc for sm_103a.
 
-The translation units (one C-ABI unit plus one kernel unit per head_dim) are
-compiled in parallel; ptxas statistics (registers, spills, shared memory) of
+The translation units (C-ABI units plus kernel units per head_dim and cache
+type) are compiled in parallel; ptxas statistics (registers, spills, shared memory) of
 every kernel are written next to the objects in ``_build/ptxas_*.txt``.
 """
 from __future__ import annotations
@@ -19,7 +19,9 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libattn_decode.so")
 
 SOURCES = ["attn_api.cu", "attn_noalloc.cu"] + [
-    "attn_kernels_hd%d_%s.cu" % (hd, t) for hd in (8, 64, 128, 256) for t in ("f16", "bf16")]
+    "attn_kernels_hd%d_%s.cu" % (hd, t) for hd in (8, 64, 128, 256) for t in ("f16", "bf16")] + [
+    "attn_paged_api.cu", "attn_rope_append.cu"] + [
+    "attn_paged_hd%d_%s.cu" % (hd, t) for hd in (64, 128, 256) for t in ("f16", "bf16", "e4m3")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -49,7 +51,7 @@ def _stale() -> bool:
         return True
     t = os.path.getmtime(LIB)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    deps.append(os.path.join(ROOT, "include", "attn_decode.h"))
+    deps += [os.path.join(ROOT, "include", h) for h in ("attn_decode.h", "attn_paged.h")]
     deps.append(os.path.abspath(__file__))
     return any(os.path.getmtime(d) > t for d in deps)
 

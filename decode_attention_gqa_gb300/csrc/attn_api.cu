@@ -13,6 +13,7 @@
 
 #include "attn_decode.h"
 #include "attn_launch.h"
+#include "attn_paged_launch.h"
 
 namespace {
 
@@ -86,6 +87,31 @@ cudaError_t device_state(int dev, DeviceState **out)
         d.ready = true;
     }
     *out = &d;
+    return cudaSuccess;
+}
+
+// Grow the library-owned workspace to `need` bytes; ok false: it would have to
+// grow while `stream` captures. Called with g_mu held and the device current.
+cudaError_t grow_workspace(DeviceState &d, size_t need, cudaStream_t stream, bool &ok)
+{
+    ok = true;
+    if (d.ws_bytes >= need) return cudaSuccess;
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(stream, &cs);
+    if (e != cudaSuccess) return e;
+    if (cs != cudaStreamCaptureStatusNone) {
+        ok = false;
+        return cudaSuccess;
+    }
+    if (d.ws) {
+        e = cudaFree(d.ws);                       // synchronises with work using it
+        d.ws = nullptr;
+        d.ws_bytes = 0;
+        if (e != cudaSuccess) return e;
+    }
+    e = cudaMalloc(&d.ws, need);
+    if (e != cudaSuccess) return e;
+    d.ws_bytes = need;
     return cudaSuccess;
 }
 
@@ -400,21 +426,10 @@ attn_status decode_impl(const float *q, const void *k_cache, const void *v_cache
 
     if (!workspace && need > 0) {
         if (stages != (attn::kStagePartial | attn::kStageCombine)) return ATTN_ERR_INVALID_ARG;
-        if (ds->ws_bytes < need) {
-            cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-            e = cudaStreamIsCapturing(stream, &cs);
-            if (e != cudaSuccess) return cuda_fail(e);
-            if (cs != cudaStreamCaptureStatusNone) return ATTN_ERR_WORKSPACE;
-            if (ds->ws) {
-                e = cudaFree(ds->ws);                 // synchronises with work using it
-                ds->ws = nullptr;
-                ds->ws_bytes = 0;
-                if (e != cudaSuccess) return cuda_fail(e);
-            }
-            e = cudaMalloc(&ds->ws, need);
-            if (e != cudaSuccess) return cuda_fail(e);
-            ds->ws_bytes = need;
-        }
+        bool ok = false;
+        e = grow_workspace(*ds, need, stream, ok);
+        if (e != cudaSuccess) return cuda_fail(e);
+        if (!ok) return ATTN_ERR_WORKSPACE;
         workspace = ds->ws;
     } else if (workspace_bytes < need) {
         return ATTN_ERR_WORKSPACE;
@@ -524,6 +539,57 @@ cudaError_t encode_kv_map4(CUtensorMap *map, const void *base, int n_seq, int64_
                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
+
+cudaError_t encode_paged_map(CUtensorMap *map, const void *base, int elem_bytes, bool bf16, int head_dim,
+                             int n_kv_head, int page_size, int n_pages, int64_t head_bytes,
+                             int64_t row_bytes, int64_t page_bytes, int box_x, int box_rows)
+{
+    const cudaError_t le = load_encoder();
+    if (le != cudaSuccess) return le;
+    const cuuint64_t dims[4] = {(cuuint64_t)head_dim, (cuuint64_t)n_kv_head, (cuuint64_t)page_size,
+                                (cuuint64_t)n_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)head_bytes, (cuuint64_t)row_bytes, (cuuint64_t)page_bytes};
+    const cuuint32_t box[4] = {(cuuint32_t)box_x, 1u, (cuuint32_t)box_rows, 1u};
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    const CUtensorMapSwizzle sw = box_x * elem_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    const CUtensorMapDataType dt = elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : bf16          ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                   : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const CUresult r = g_encode(map, dt, 4, const_cast<void *>(base), dims, strides, box, estr,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t device_facts(int *sm_count, unsigned **err_word)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState *ds = nullptr;
+    e = device_state(dev, &ds);
+    if (e != cudaSuccess) return e;
+    *sm_count = ds->sm_count;
+    *err_word = ds->err_word;
+    return cudaSuccess;
+}
+
+cudaError_t owned_workspace(size_t need, cudaStream_t stream, void **ws, bool *ok)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState *ds = nullptr;
+    e = device_state(dev, &ds);
+    if (e != cudaSuccess) return e;
+    e = grow_workspace(*ds, need, stream, *ok);
+    *ws = ds->ws;
+    return e;
+}
+
+void note_cuda_error(cudaError_t e) { t_last_cuda_error = (int)e; }
 
 cudaError_t ensure_smem_attr(const void *func, int bytes)
 {

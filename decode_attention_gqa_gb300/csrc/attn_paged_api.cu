@@ -1,0 +1,363 @@
+// attn_paged_api.cu -- the C ABI of include/attn_paged.h: argument checks, the
+// rotary steps, the split plan and the dispatch to the kernels.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <initializer_list>
+
+#include "attn_launch.h"
+#include "attn_paged.h"
+#include "attn_paged_launch.h"
+
+namespace attn {
+
+PagedInfo paged_info(int head_dim, int kv_type, int)
+{
+    // the resident blocks of PagedShape (attn_paged_impl.cuh)
+    (void)kv_type;
+    return PagedInfo{64, head_dim == 256 ? 1 : 2};
+}
+
+} // namespace attn
+
+namespace {
+
+constexpr int kMaxPagedSplits = 4096;              // the combine's limit
+constexpr int64_t kMaxRows = (int64_t)0x7fffffff - 16384;
+constexpr int64_t kMaxStrideBytes = (int64_t)1 << 40;
+
+bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+attn_status fail(cudaError_t e)
+{
+    attn::note_cuda_error(e);
+    return ATTN_ERR_CUDA;
+}
+
+int type_bytes(int t) { return t == ATTN_TYPE_F32 ? 4 : t == ATTN_TYPE_E4M3 ? 1 : 2; }
+
+struct Strides {
+    int64_t page, row, head;
+};
+
+// Everything about the pool but its pointers.
+attn_status check_cache_shape(const attn_paged_cache *c, int max_pages, Strides &st)
+{
+    if (!c || c->reserved != 0 || c->n_pages < 1 || c->n_kv_head < 1 || c->head_dim < 1 || max_pages < 1)
+        return ATTN_ERR_INVALID_ARG;
+    if (c->page_size < 16 || c->page_size > 1024 || c->page_size % 16 != 0) return ATTN_ERR_INVALID_ARG;
+    if (c->kv_type != ATTN_TYPE_F16 && c->kv_type != ATTN_TYPE_BF16 && c->kv_type != ATTN_TYPE_E4M3)
+        return ATTN_ERR_INVALID_ARG;
+    if (c->n_kv_head > 65535 || (int64_t)max_pages * c->page_size > kMaxRows) return ATTN_ERR_INVALID_ARG;
+    st = Strides{c->page_stride, c->row_stride, c->head_stride};
+    if (st.page == 0 && st.row == 0 && st.head == 0) {
+        st.head = c->head_dim;
+        st.row = (int64_t)c->n_kv_head * c->head_dim;
+        st.page = (int64_t)c->page_size * st.row;
+    }
+    const int64_t es = type_bytes(c->kv_type);
+    for (int64_t x : {st.page, st.row, st.head})
+        if (x < c->head_dim || x >= kMaxStrideBytes / es || x * es % 16 != 0) return ATTN_ERR_INVALID_ARG;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
+
+attn_status check_cache_pointers(const attn_paged_cache *c)
+{
+    if (!c || !c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return ATTN_ERR_INVALID_ARG;
+    const bool scales = c->kv_type == ATTN_TYPE_E4M3;
+    if (scales != (c->k_scale != nullptr) || scales != (c->v_scale != nullptr)) return ATTN_ERR_INVALID_ARG;
+    if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)) return ATTN_ERR_INVALID_ARG;
+    return ATTN_OK;
+}
+
+struct PagedPlan {
+    int slots = 8, qgroups = 1, n_splits = 1;
+    size_t workspace = 0;
+};
+
+attn_status check_heads(const attn_paged_cache *c, int n_seq, int n_q, int n_head, int window, int n_splits)
+{
+    if (n_seq < 0 || n_seq > 65535 || n_q < 1 || n_q > 1024 || n_head < 1 || n_head % c->n_kv_head != 0 || window < 0 ||
+        n_splits < 0 || n_splits > kMaxPagedSplits)
+        return ATTN_ERR_INVALID_ARG;
+    if (n_head / c->n_kv_head > 64) return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
+
+// Split count from the shape and the capacity (the host never sees the lengths): the chunk that
+// fills one wave of resident blocks at full capacity for a single sequence, eight waves for a batch whose
+// ragged lengths then balance, in whole 64-row tiles; the device divides the rows that are there.
+void make_plan(const attn_paged_cache *c, int max_pages, int n_seq, int n_q, int n_head, int window, int n_splits,
+               int sm_count, PagedPlan &pl)
+{
+    const int group = n_head / c->n_kv_head;
+    pl.slots = attn::paged_slots(n_q, group);
+    pl.qgroups = (n_q * group + pl.slots - 1) / pl.slots;
+    if (n_splits > 0) {
+        pl.n_splits = n_splits;
+    } else {
+        const attn::PagedInfo ki = attn::paged_info(c->head_dim, c->kv_type, pl.slots);
+        int64_t rows = (int64_t)max_pages * c->page_size;
+        if (window > 0 && (int64_t)window + n_q + ki.tile_rows < rows) rows = (int64_t)window + n_q + ki.tile_rows;
+        const int64_t units = (int64_t)n_seq * c->n_kv_head * pl.qgroups;
+        const int64_t slots = (int64_t)sm_count * ki.blocks_per_sm * (n_seq > 1 ? 8 : 1);
+        int64_t chunk = units > slots ? rows : (rows * units + slots - 1) / slots;
+        chunk = (chunk + ki.tile_rows - 1) / ki.tile_rows * ki.tile_rows;
+        const int64_t P = (rows + chunk - 1) / chunk;
+        pl.n_splits = (int)(P < 1 ? 1 : P > kMaxPagedSplits ? kMaxPagedSplits : P);
+    }
+    pl.workspace = pl.n_splits > 1 ? attn_workspace_size(n_seq, n_q * n_head, c->head_dim, pl.n_splits) : 0;
+}
+
+} // namespace
+
+extern "C" {
+
+attn_status attn_rope_steps(int rot_dim, double base, int scaling, double factor, double low_turns,
+                            double high_turns, int64_t trained_len, uint64_t *steps)
+{
+    if (!steps || rot_dim < 16 || rot_dim > 256 || rot_dim % 16 != 0) return ATTN_ERR_INVALID_ARG;
+    if (!std::isfinite(base) || base < 1.0) return ATTN_ERR_INVALID_ARG;
+    if (scaling < ATTN_ROPE_PLAIN || scaling > ATTN_ROPE_BANDS) return ATTN_ERR_INVALID_ARG;
+    if (scaling != ATTN_ROPE_PLAIN && (!std::isfinite(factor) || factor <= 0.0)) return ATTN_ERR_INVALID_ARG;
+    if (scaling == ATTN_ROPE_BANDS && (!std::isfinite(low_turns) || !std::isfinite(high_turns) ||
+                                       !(low_turns < high_turns) || trained_len < 1))
+        return ATTN_ERR_INVALID_ARG;
+    const double two_pi = 6.283185307179586476925;
+    if (scaling == ATTN_ROPE_BASE) base *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
+    uint64_t out[128];
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        double f = std::pow(base, -2.0 * i / rot_dim);
+        if (scaling == ATTN_ROPE_LINEAR) f /= factor;
+        if (scaling == ATTN_ROPE_BANDS) {
+            const double n = (double)trained_len * f / two_pi;
+            const double keep = n >= high_turns ? 1.0 : n <= low_turns ? 0.0 : (n - low_turns) / (high_turns - low_turns);
+            f = keep * f + (1.0 - keep) * f / factor;
+        }
+        const double turns = f / two_pi;
+        if (!(turns < 1.0)) return ATTN_ERR_INVALID_ARG;       // infinite and NaN too
+        const double x = std::floor(turns * 18446744073709551616.0 + 0.5);
+        out[i] = x >= 18446744073709551616.0 ? ~(uint64_t)0 : (uint64_t)x;
+    }
+    for (int i = 0; i < rot_dim / 2; ++i) steps[i] = out[i];
+    return ATTN_OK;
+}
+
+attn_status attn_rope_append(const attn_paged_cache *cache, const int32_t *block_table, int max_pages,
+                             const int32_t *positions, const int32_t *cu_tokens, int n_seq, int64_t n_tokens,
+                             const void *q, const void *k_new, const void *v_new, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, int in_type, float *q_out, int n_head,
+                             const attn_rope *rope, attn_stream_t stream)
+{
+    attn_status st = check_cache_pointers(cache);
+    if (st != ATTN_OK) return st;
+    if (in_type != ATTN_TYPE_F32 && in_type != ATTN_TYPE_F16 && in_type != ATTN_TYPE_BF16) return ATTN_ERR_INVALID_ARG;
+    if (n_seq < 0 || n_seq > 65535 || n_tokens < 0 || n_tokens > kMaxRows) return ATTN_ERR_INVALID_ARG;
+    if (n_seq == 0 && n_tokens != 0) return ATTN_ERR_INVALID_ARG;
+    if (!cu_tokens && n_seq > 0 && n_tokens % n_seq != 0) return ATTN_ERR_INVALID_ARG;
+    if (n_tokens > 0 && (!block_table || !positions || !k_new || !v_new)) return ATTN_ERR_INVALID_ARG;
+    if ((q != nullptr) != (q_out != nullptr) || (q && (n_head < 1 || n_head > 65535))) return ATTN_ERR_INVALID_ARG;
+    for (const void *p : {q, k_new, v_new, static_cast<const void *>(q_out)})
+        if (!aligned(p, 16)) return ATTN_ERR_INVALID_ARG;
+    for (const int32_t *p : {block_table, positions, cu_tokens})
+        if (!aligned(p, 4)) return ATTN_ERR_INVALID_ARG;
+    if (rope && (!rope->steps || !aligned(rope->steps, 16) || rope->rot_dim < 16 || rope->rot_dim % 16 != 0 ||
+                 rope->rot_dim > cache->head_dim || (rope->interleaved != 0 && rope->interleaved != 1) ||
+                 !std::isfinite(rope->mscale) || rope->reserved != 0))
+        return ATTN_ERR_INVALID_ARG;
+    Strides cs;
+    st = check_cache_shape(cache, max_pages, cs);
+    if (st != ATTN_OK) return st;
+    const int64_t hd = cache->head_dim, es = type_bytes(in_type);
+    const int64_t q_dense = (int64_t)n_head * hd, kv_dense = (int64_t)cache->n_kv_head * hd;
+    if (q_stride == 0 || !q) q_stride = q_dense;
+    if (k_stride == 0) k_stride = kv_dense;
+    if (v_stride == 0) v_stride = kv_dense;
+    if ((q && q_stride < q_dense) || k_stride < kv_dense || v_stride < kv_dense) return ATTN_ERR_INVALID_ARG;
+    for (int64_t x : {q ? q_stride : kv_dense, k_stride, v_stride})
+        if (x >= kMaxStrideBytes / es || x * es % 16 != 0) return ATTN_ERR_INVALID_ARG;
+    if (q && static_cast<const void *>(q_out) == q && (in_type != ATTN_TYPE_F32 || q_stride != q_dense))
+        return ATTN_ERR_INVALID_ARG;
+    if (n_tokens == 0) return ATTN_OK;
+
+    attn::AppendRequest r{};
+    attn::AppendArgs &a = r.a;
+    a.q = q;
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.q_out = q_out;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.k = cache->k;
+    a.v = cache->v;
+    a.k_scale = cache->k_scale;
+    a.v_scale = cache->v_scale;
+    a.page_stride = cs.page;
+    a.row_stride = cs.row;
+    a.head_stride = cs.head;
+    a.table = block_table;
+    a.positions = positions;
+    a.cu = cu_tokens;
+    a.steps = rope ? rope->steps : nullptr;
+    a.mscale = rope ? rope->mscale : 1.f;
+    a.rot_dim = rope ? rope->rot_dim : 0;
+    a.interleaved = rope ? rope->interleaved : 0;
+    a.n_seq = n_seq;
+    a.n_head = n_head;
+    a.n_kv_head = cache->n_kv_head;
+    a.n_tokens = n_tokens;
+    a.n_each = cu_tokens ? 0 : n_tokens / n_seq;
+    a.max_pages = max_pages;
+    a.n_pages = cache->n_pages;
+    a.page_size = cache->page_size;
+    // (sequence, page) pairs that may be touched: the page jobs' numbering on the device
+    a.page_items = cu_tokens ? n_tokens / cache->page_size + 2 * (int64_t)n_seq
+                             : (int64_t)n_seq * ((a.n_each + cache->page_size - 2) / cache->page_size + 1);
+    r.head_dim = cache->head_dim;
+    r.in_type = in_type;
+    r.kv_type = cache->kv_type;
+    r.stream = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = attn::launch_append(r);
+    return e == cudaSuccess ? ATTN_OK : fail(e);
+}
+
+attn_status attn_paged_plan(const attn_paged_cache *cache, int max_pages, int n_seq, int n_q, int n_head,
+                            int window, int n_splits, int sm_count, int *n_splits_out,
+                            size_t *workspace_bytes_out)
+{
+    Strides cs;
+    attn_status st = check_cache_shape(cache, max_pages, cs);
+    if (!cache) return st;
+    const attn_status sh = st == ATTN_OK || st == ATTN_ERR_UNSUPPORTED
+                               ? check_heads(cache, n_seq, n_q, n_head, window, n_splits) : st;
+    if (sh != ATTN_OK) return sh;
+    if (st != ATTN_OK) return st;
+    if (n_seq == 0) return ATTN_ERR_INVALID_ARG;          // nothing to plan
+    if (sm_count <= 0) {
+        unsigned *err = nullptr;
+        const cudaError_t e = attn::device_facts(&sm_count, &err);
+        if (e != cudaSuccess) return fail(e);
+    }
+    PagedPlan pl;
+    make_plan(cache, max_pages, n_seq, n_q, n_head, window, n_splits, sm_count, pl);
+    if (n_splits_out) *n_splits_out = pl.n_splits;
+    if (workspace_bytes_out) *workspace_bytes_out = pl.workspace;
+    return ATTN_OK;
+}
+
+attn_status attn_decode_paged(const attn_paged_cache *cache, const int32_t *block_table, int max_pages,
+                              const int32_t *positions, const float *q, float *out, int n_seq, int n_q,
+                              int n_head, float scale, const attn_score_rules *rules, int n_splits,
+                              void *workspace, size_t workspace_bytes, attn_stream_t stream)
+{
+    attn_status st = check_cache_pointers(cache);
+    if (st != ATTN_OK) return st;
+    if (!std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+    if (n_seq > 0 && (!block_table || !positions || !q || !out)) return ATTN_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(positions, 4))
+        return ATTN_ERR_INVALID_ARG;
+    const float softcap = rules ? rules->softcap : 0.f;
+    const int window = rules ? rules->window : 0;
+    if (!std::isfinite(softcap) || softcap < 0.f) return ATTN_ERR_INVALID_ARG;
+    if (rules && (!aligned(rules->slopes, 4) || !aligned(rules->starts, 4))) return ATTN_ERR_INVALID_ARG;
+    if (!aligned(workspace, 256)) return ATTN_ERR_INVALID_ARG;
+    Strides cs;
+    st = check_cache_shape(cache, max_pages, cs);
+    if (st == ATTN_ERR_INVALID_ARG) return st;
+    const attn_status sh = check_heads(cache, n_seq, n_q, n_head, window, n_splits);
+    if (sh != ATTN_OK) return sh;
+    if (st != ATTN_OK) return st;
+    if (n_seq == 0) return ATTN_OK;
+
+    int sm_count = 0;
+    unsigned *err = nullptr;
+    cudaError_t e = attn::device_facts(&sm_count, &err);
+    if (e != cudaSuccess) return fail(e);
+    PagedPlan pl;
+    make_plan(cache, max_pages, n_seq, n_q, n_head, window, n_splits, sm_count, pl);
+    if ((int64_t)cache->n_kv_head * pl.qgroups > 0x7fffffff) return ATTN_ERR_INVALID_ARG;
+    if (pl.workspace > 0) {
+        if (!workspace) {
+            bool ok = false;
+            e = attn::owned_workspace(pl.workspace, reinterpret_cast<cudaStream_t>(stream), &workspace, &ok);
+            if (e != cudaSuccess) return fail(e);
+            if (!ok) return ATTN_ERR_WORKSPACE;
+        } else if (workspace_bytes < pl.workspace) {
+            return ATTN_ERR_WORKSPACE;
+        }
+    }
+
+    attn::PagedRequest r{};
+    attn::PagedArgs &a = r.pa;
+    const int P = pl.n_splits;
+    a.q = q;
+    a.out = out;
+    a.positions = positions;
+    a.table = block_table;
+    a.k_scale = cache->k_scale;
+    a.v_scale = cache->v_scale;
+    a.slopes = rules ? rules->slopes : nullptr;
+    a.starts = rules ? rules->starts : nullptr;
+    const size_t slots = (size_t)n_seq * n_q * n_head * P;
+    a.ws_o = static_cast<float *>(workspace);
+    a.ws_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) +
+                                         ((slots * cache->head_dim * sizeof(float) + 255) & ~size_t(255)));
+    a.err = err;
+    a.n_head = n_head;
+    a.n_kv_head = cache->n_kv_head;
+    a.group = n_head / cache->n_kv_head;
+    a.n_q = n_q;
+    a.qgroups = pl.qgroups;
+    a.n_splits = P;
+    a.max_pages = max_pages;
+    a.n_pages = cache->n_pages;
+    a.page_size = cache->page_size;
+    a.cap = max_pages * cache->page_size;
+    a.window = window > a.cap ? 0 : window;        // past the capacity it masks nothing
+    a.box_rows = cache->page_size % 64 == 0 ? 64 : cache->page_size % 32 == 0 ? 32 : 16;
+    a.qscale = softcap > 0.f ? (float)((double)scale / softcap) : (float)((double)scale * 1.4426950408889634);
+    a.cap_log2 = (float)((double)softcap * 1.4426950408889634);
+    r.k = cache->k;
+    r.v = cache->v;
+    r.page_stride = cs.page;
+    r.row_stride = cs.row;
+    r.head_stride = cs.head;
+    r.n_seq = n_seq;
+    r.head_dim = cache->head_dim;
+    r.kv_type = cache->kv_type;
+    r.rules = softcap > 0.f || a.slopes;
+    r.stream = reinterpret_cast<cudaStream_t>(stream);
+    const int ti = cache->kv_type - ATTN_TYPE_F16;
+    using Launch = cudaError_t (*)(const attn::PagedRequest &);
+    static const Launch table[3][3] = {
+        {attn::launch_paged_hd64_f16, attn::launch_paged_hd64_bf16, attn::launch_paged_hd64_e4m3},
+        {attn::launch_paged_hd128_f16, attn::launch_paged_hd128_bf16, attn::launch_paged_hd128_e4m3},
+        {attn::launch_paged_hd256_f16, attn::launch_paged_hd256_bf16, attn::launch_paged_hd256_e4m3}};
+    const int hi = cache->head_dim == 64 ? 0 : cache->head_dim == 128 ? 1 : 2;
+    e = table[hi][ti](r);
+    if (e != cudaSuccess) return fail(e);
+    if (P > 1) {
+        attn::LaunchRequest c{};
+        c.pa.ws_o = a.ws_o;
+        c.pa.ws_ml = a.ws_ml;
+        c.pa.n_head = n_head;
+        c.pa.n_q = 1;
+        c.pa.n_splits = P;
+        c.out = out;
+        c.n_seq = n_seq;
+        c.head_dim = cache->head_dim;
+        c.group = 1;
+        c.variant = attn::kVariantSimt;
+        c.stages = attn::kStageCombine;
+        c.stream = r.stream;
+        c.pa.n_head = n_head * n_q;                // partial heads per sequence
+        e = attn::launch_any(c);
+        if (e != cudaSuccess) return fail(e);
+    }
+    return ATTN_OK;
+}
+
+} // extern "C"

@@ -1,0 +1,6 @@
+// Paged decode kernels for head_dim 128 over a bf16 cache.
+#include "attn_paged_impl.cuh"
+
+namespace attn {
+cudaError_t launch_paged_hd128_bf16(const PagedRequest &r) { return launch_paged_for<128, __nv_bfloat16>(r); }
+} // namespace attn

@@ -1,0 +1,6 @@
+// Paged decode kernels for head_dim 64 over a f16 cache.
+#include "attn_paged_impl.cuh"
+
+namespace attn {
+cudaError_t launch_paged_hd64_f16(const PagedRequest &r) { return launch_paged_for<64, __half>(r); }
+} // namespace attn

@@ -1,0 +1,111 @@
+// attn_paged_launch.h -- internal host interface of the paged-cache operators:
+// between their C-ABI layer (attn_paged_api.cu), the kernel translation units
+// (attn_paged_hd*.cu, attn_rope_append.cu) and the device state that
+// attn_api.cu owns. Not installed; not part of the public ABI.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace attn {
+
+constexpr int kTypeF32 = 0, kTypeF16 = 1, kTypeBf16 = 2, kTypeE4m3 = 3;   // ATTN_TYPE_*
+
+struct PagedArgs {
+    const float *q;           // [n_seq][n_q][n_head][HD]
+    float *out;               // the same; written by the partial kernel when n_splits == 1
+    const int32_t *positions; // [n_seq]
+    const int32_t *table;     // [n_seq][max_pages]
+    const float *k_scale;     // [n_pages][n_kv_head], e4m3 only
+    const float *v_scale;
+    const float *slopes;      // [n_head] or null
+    const int32_t *starts;    // [n_seq] or null
+    float *ws_o;              // [n_seq][n_q * n_head][P][HD]
+    float2 *ws_ml;            // [n_seq][n_q * n_head][P]
+    unsigned *err;
+    int n_head, n_kv_head, group, n_q;
+    int qgroups;              // blocks per (split, KV head) along the (query row, head) slots
+    int n_splits;             // P
+    int max_pages, n_pages, page_size;
+    int cap;                  // max_pages * page_size
+    int window;               // 0: none
+    int box_rows;             // rows of one TMA box: it divides the page and the tile
+    float qscale;             // scale * log2 e, or scale / softcap
+    float cap_log2;           // softcap * log2 e, or 0
+};
+
+struct PagedRequest {
+    PagedArgs pa;
+    const void *k, *v;
+    int64_t page_stride, row_stride, head_stride;   // elements
+    int n_seq, head_dim, kv_type;
+    bool rules;               // softcap or slopes
+    cudaStream_t stream;
+};
+
+// Shape of the paged partial kernel for (head_dim, element size, slots).
+struct PagedInfo {
+    int tile_rows;
+    int blocks_per_sm;
+};
+
+// (query row, head) slots of a block: 8 where a KV head's slots fit in 8, else 16.
+inline int paged_slots(int n_q, int group) { return n_q * group <= 8 ? 8 : 16; }
+
+PagedInfo paged_info(int head_dim, int kv_type, int slots);
+cudaError_t launch_paged_hd64_f16(const PagedRequest &r);
+cudaError_t launch_paged_hd64_bf16(const PagedRequest &r);
+cudaError_t launch_paged_hd64_e4m3(const PagedRequest &r);
+cudaError_t launch_paged_hd128_f16(const PagedRequest &r);
+cudaError_t launch_paged_hd128_bf16(const PagedRequest &r);
+cudaError_t launch_paged_hd128_e4m3(const PagedRequest &r);
+cudaError_t launch_paged_hd256_f16(const PagedRequest &r);
+cudaError_t launch_paged_hd256_bf16(const PagedRequest &r);
+cudaError_t launch_paged_hd256_e4m3(const PagedRequest &r);
+
+struct AppendArgs {
+    const void *q, *k_new, *v_new;
+    float *q_out;
+    int64_t q_stride, k_stride, v_stride;           // elements between tokens
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int64_t page_stride, row_stride, head_stride;   // elements
+    const int32_t *table, *positions, *cu;
+    const uint64_t *steps;                          // null: no rotation
+    unsigned *err;
+    float mscale;
+    int rot_dim, interleaved;
+    int n_seq, n_head, n_kv_head;
+    int64_t n_tokens;
+    int64_t n_each;                                 // tokens per sequence when cu is null
+    int max_pages, n_pages, page_size;
+    int64_t page_items;                             // (sequence, page) candidates, e4m3 only
+    int64_t page_blocks;                            // blocks of page jobs
+    int iters;                                      // head groups one warp takes for its token
+    int chunks;                                     // warps per token
+};
+
+struct AppendRequest {
+    AppendArgs a;
+    int head_dim, in_type, kv_type;
+    cudaStream_t stream;
+};
+
+cudaError_t launch_append(const AppendRequest &r);
+
+// Implemented in attn_api.cu.
+// The current device's SM count and error word.
+cudaError_t device_facts(int *sm_count, unsigned **err_word);
+// The library-owned workspace of the current device, grown to `need` bytes
+// outside capture. *ok false: it would have to grow while `stream` captures.
+cudaError_t owned_workspace(size_t need, cudaStream_t stream, void **ws, bool *ok);
+// A paged pool as a 4-D tensor (x = element, y = KV head, z = row, w = page) with
+// a box of (box_x, 1, box_rows, 1); strides in bytes; swizzled as wide as the box's rows.
+cudaError_t encode_paged_map(CUtensorMap *map, const void *base, int elem_bytes, bool bf16, int head_dim,
+                             int n_kv_head, int page_size, int n_pages, int64_t head_bytes,
+                             int64_t row_bytes, int64_t page_bytes, int box_x, int box_rows);
+// Remembers the error for attn_last_cuda_error.
+void note_cuda_error(cudaError_t e);
+
+} // namespace attn

@@ -1,0 +1,235 @@
+"""The paged-cache operators without a GPU: refusals of the C entry points (all before any CUDA
+call), of the torch forms, the split plan for a given SM count, and the rotary steps."""
+import ctypes
+import math
+from decimal import Decimal, getcontext
+
+import numpy as np
+import pytest
+
+import decode_attention_gqa_gb300 as pkg
+import paged_reference as ref
+from decode_attention_gqa_gb300 import build as cuda_build
+
+INVALID, UNSUPPORTED, OK = pkg.ATTN_ERR_INVALID_ARG, pkg.ATTN_ERR_UNSUPPORTED, pkg.ATTN_OK
+
+
+@pytest.fixture(scope="module")
+def lib():
+    cuda_build.build()
+    return pkg.load()
+
+
+def _cache(**kw):
+    a = dict(k=256, v=256, k_scale=0, v_scale=0, page_stride=0, row_stride=0, head_stride=0, n_pages=4,
+             page_size=64, n_kv_head=2, head_dim=128, kv_type=pkg.ATTN_TYPE_F16, reserved=0)
+    a.update(kw)
+    return pkg._CacheStruct(*[a[n] for n, _ in pkg._CacheStruct._fields_])
+
+
+def _addr(s):
+    return ctypes.addressof(s) if s is not None else None
+
+
+CACHE_FAULTS = [
+    (dict(k=0), INVALID), (dict(v=8), INVALID), (dict(k_scale=256, v_scale=256), INVALID),
+    (dict(kv_type=pkg.ATTN_TYPE_E4M3), INVALID),                       # no scales
+    (dict(kv_type=pkg.ATTN_TYPE_E4M3, k_scale=256), INVALID),
+    (dict(kv_type=pkg.ATTN_TYPE_E4M3, k_scale=256, v_scale=258), INVALID),
+    (dict(kv_type=pkg.ATTN_TYPE_F32), INVALID), (dict(kv_type=4), INVALID), (dict(reserved=1), INVALID),
+    (dict(n_pages=0), INVALID), (dict(n_kv_head=0), INVALID), (dict(n_kv_head=70000), INVALID),
+    (dict(page_size=0), INVALID), (dict(page_size=8), INVALID), (dict(page_size=24), INVALID),
+    (dict(page_size=1040), INVALID), (dict(head_dim=96), UNSUPPORTED), (dict(head_dim=8), UNSUPPORTED),
+    (dict(head_dim=0), INVALID),
+    (dict(page_stride=64 * 256, row_stride=256), INVALID),             # head stride missing
+    (dict(page_stride=64 * 256, row_stride=256, head_stride=132), INVALID),      # 264 bytes
+    (dict(page_stride=64 * 256, row_stride=-256, head_stride=128), INVALID),
+    (dict(page_stride=1 << 40, row_stride=256, head_stride=128), INVALID),
+]
+
+
+def _attend(lib, cache=None, rules=None, **kw):
+    a = dict(table=16, max_pages=8, pos=16, q=16, out=16, n_seq=1, n_q=1, n_head=8, scale=0.1, P=0, ws=None,
+             ws_bytes=0)
+    a.update(kw)
+    c = cache if cache is not None else _cache()
+    return lib.attn_decode_paged(_addr(c), a["table"], a["max_pages"], a["pos"], a["q"], a["out"], a["n_seq"],
+                                 a["n_q"], a["n_head"], a["scale"], _addr(rules), a["P"], a["ws"], a["ws_bytes"],
+                                 None)
+
+
+def _append(lib, cache=None, rope=None, **kw):
+    a = dict(table=16, max_pages=8, pos=16, cu=None, n_seq=1, n_tokens=1, q=16, k=16, v=16, qs=0, ks=0, vs=0,
+             t=pkg.ATTN_TYPE_F16, q_out=32, n_head=8)
+    a.update(kw)
+    c = cache if cache is not None else _cache()
+    return lib.attn_rope_append(_addr(c), a["table"], a["max_pages"], a["pos"], a["cu"], a["n_seq"], a["n_tokens"],
+                                a["q"], a["k"], a["v"], a["qs"], a["ks"], a["vs"], a["t"], a["q_out"], a["n_head"],
+                                _addr(rope), None)
+
+
+@pytest.mark.parametrize("fault,want", CACHE_FAULTS)
+def test_a_wrong_pool_is_refused(lib, fault, want):
+    assert _attend(lib, _cache(**fault)) == want
+    assert _append(lib, _cache(**fault)) == want
+
+
+def test_attention_refuses_wrong_arguments(lib):
+    assert lib.attn_decode_paged(None, 16, 8, 16, 16, 16, 1, 1, 8, 0.1, None, 0, None, 0, None) == INVALID
+    for kw in (dict(table=None), dict(pos=None), dict(q=None), dict(out=None), dict(q=8), dict(out=20),
+               dict(table=18), dict(pos=17), dict(max_pages=0), dict(max_pages=1 << 26), dict(n_seq=-1),
+               dict(n_seq=70000), dict(n_q=0), dict(n_q=1025), dict(n_head=0), dict(n_head=7),
+               dict(scale=math.nan), dict(scale=math.inf), dict(P=-1), dict(P=5000), dict(ws=128)):
+        assert _attend(lib, **kw) == INVALID, kw
+    assert _attend(lib, n_head=130) == UNSUPPORTED                      # 65 query heads a KV head
+    for r in ((-1.0, 0, 0, 0), (math.nan, 0, 0, 0), (math.inf, 0, 0, 0), (0.0, -1, 0, 0), (0.0, 0, 2, 0),
+              (0.0, 0, 0, 3)):
+        assert _attend(lib, rules=pkg._RulesStruct(*r)) == INVALID, r
+    assert _attend(lib, n_seq=0, table=None, pos=None, q=None, out=None) == OK
+
+
+def test_append_refuses_wrong_arguments(lib):
+    assert lib.attn_rope_append(None, 16, 8, 16, None, 1, 1, 16, 16, 16, 0, 0, 0, 1, 32, 8, None, None) == INVALID
+    for kw in (dict(table=None), dict(pos=None), dict(k=None), dict(v=None), dict(q=None), dict(q_out=None),
+               dict(k=8), dict(v=4), dict(q=24), dict(q_out=8), dict(cu=2), dict(t=pkg.ATTN_TYPE_E4M3),
+               dict(t=9), dict(n_seq=-1), dict(n_seq=70000), dict(n_tokens=-1), dict(n_seq=2, n_tokens=3),
+               dict(n_seq=0, n_tokens=1), dict(n_head=0), dict(max_pages=0), dict(qs=100), dict(qs=1028),
+               dict(ks=128), dict(vs=260), dict(q=32, q_out=32)):
+        assert _append(lib, **kw) == INVALID, kw
+    for r in ((0, 128, 0, 1.0, 0), (24, 128, 0, 1.0, 0), (16, 0, 0, 1.0, 0), (16, 24, 0, 1.0, 0),
+              (16, 144, 0, 1.0, 0), (16, 128, 2, 1.0, 0), (16, 128, 0, math.nan, 0), (16, 128, 0, 1.0, 1)):
+        assert _append(lib, rope=pkg._RopeStruct(*r)) == INVALID, r
+    assert _append(lib, n_tokens=0, n_seq=0, table=None, pos=None, k=None, v=None) == OK
+    assert _append(lib, n_tokens=0, cu=16) == OK
+
+
+def test_plan_for_a_given_sm_count(lib):
+    def plan(cache=None, max_pages=128, n_seq=1, n_q=1, n_head=8, window=0, P=0, sms=152):
+        c = cache or _cache()
+        return pkg.attn_paged_plan(ctypes.addressof(c), max_pages, n_seq, n_q, n_head, window, P, sms)
+    # one sequence, 2 KV heads, 8192 rows: one wave of 2 x 152 blocks in whole 64-row tiles
+    P, ws = plan()
+    assert P == 128 and ws == pkg.attn_workspace_size(1, 8, 128, 128)
+    # a window bounds the rows that a sequence can need, and so the splits
+    assert plan(window=100)[0] < 8
+    # enough units to fill the waves: one split, and no workspace
+    assert plan(n_seq=4096) == (1, 0)
+    assert plan(P=7) == (7, pkg.attn_workspace_size(1, 8, 128, 7))
+    assert plan(n_q=4)[1] == pkg.attn_workspace_size(1, 32, 128, plan(n_q=4)[0])
+    for kw, st in ((dict(n_seq=0), INVALID), (dict(n_head=3), INVALID), (dict(window=-1), INVALID),
+                   (dict(P=-2), INVALID), (dict(n_head=130), UNSUPPORTED),
+                   (dict(cache=_cache(head_dim=32)), UNSUPPORTED), (dict(max_pages=0), INVALID)):
+        with pytest.raises(pkg.AttnError) as e:
+            plan(**kw)
+        assert e.value.status == st, kw
+    # only the pool's shape is looked at
+    assert plan(cache=_cache(k=0, v=0)) == plan()
+
+
+def test_torch_forms_refuse_wrong_tensors(lib, monkeypatch):
+    torch = pytest.importorskip("torch")
+    k = torch.zeros(3, 16, 2, 64, dtype=torch.float16)
+    with pytest.raises(TypeError):
+        pkg.PagedCache(k.float(), k.float())
+    with pytest.raises(TypeError):
+        pkg.PagedCache(k, k.bfloat16())
+    with pytest.raises(ValueError):
+        pkg.PagedCache(k, torch.zeros(3, 16, 2, 128, dtype=torch.float16))
+    with pytest.raises(ValueError):
+        pkg.PagedCache(k, torch.zeros(3, 2, 16, 64, dtype=torch.float16).transpose(1, 2))   # other strides
+    with pytest.raises(ValueError):
+        pkg.PagedCache(k, k.clone(), torch.ones(3, 2), torch.ones(3, 2))                    # scales of a 16-bit cache
+    k8 = torch.zeros(3, 16, 2, 64, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    with pytest.raises(ValueError):
+        pkg.PagedCache(k8, k8)
+    with pytest.raises(ValueError):
+        pkg.PagedCache(k8, k8, torch.ones(3, 1), torch.ones(3, 2))
+    with pytest.raises(TypeError):
+        pkg.PagedCache(k8, k8, torch.ones(3, 2).double(), torch.ones(3, 2))
+    c = pkg.PagedCache(k, k.clone())
+    table, pos = torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    q = torch.zeros(1, 4, 64)
+    with pytest.raises(ValueError):                                    # host tensors
+        pkg.paged_decode_attention(c, table, pos, q)
+    with pytest.raises(ValueError):
+        pkg.rope_append(c, table, pos, k[0, :1], k[0, :1])
+    # the checks behind the device's
+    monkeypatch.setattr(pkg, "_same_device", lambda d: None)
+    for bad in (dict(q=q.double()), dict(q=q[0]), dict(q=torch.zeros(2, 4, 64)), dict(q=torch.zeros(1, 4, 32)),
+                dict(q=torch.zeros(1, 64, 4).transpose(1, 2)), dict(table=table.long()), dict(table=table[0]),
+                dict(pos=pos.long()), dict(pos=torch.zeros(2, dtype=torch.int32)), dict(out=torch.zeros(1, 4, 32)),
+                dict(out=torch.zeros(1, 4, 64).half()), dict(slopes=torch.zeros(3)), dict(slopes=torch.zeros(4).half()),
+                dict(starts=torch.zeros(1)), dict(starts=torch.zeros(2, dtype=torch.int32))):
+        a = dict(table=table, pos=pos, q=q)
+        a.update(bad)
+        with pytest.raises((TypeError, ValueError)):
+            pkg.paged_decode_attention(c, a.pop("table"), a.pop("pos"), a.pop("q"), **a)
+    x = torch.zeros(1, 2, 64)
+    for bad in (dict(k=x.double()), dict(k=x.long()), dict(v=x.half()), dict(v=torch.zeros(2, 2, 64)),
+                dict(k=torch.zeros(1, 3, 64)), dict(k=torch.zeros(1, 64, 2).transpose(1, 2)), dict(q=x[0]),
+                dict(q=torch.zeros(1, 4, 64), q_out=torch.zeros(1, 4, 64).half()), dict(q_out=x),
+                dict(q=torch.zeros(1, 4, 64), q_out=torch.zeros(1, 2, 64)), dict(cu_tokens=pos),
+                dict(cu_tokens=torch.zeros(2))):
+        a = dict(k=x, v=x)
+        a.update(bad)
+        with pytest.raises((TypeError, ValueError)):
+            pkg.rope_append(c, table, pos, a.pop("k"), a.pop("v"), **a)
+
+
+PI = Decimal("3.14159265358979323846264338327950288419716939937510")
+
+
+@pytest.mark.parametrize("rot,base,scaling,kw", [
+    (128, 10000.0, 0, {}), (64, 500000.0, 0, {}), (16, 1.0, 0, {}), (256, 1e6, 1, dict(factor=8.0)),
+    (128, 10000.0, 2, dict(factor=4.0)),
+    (128, 500000.0, 3, dict(factor=8.0, low_turns=1.0, high_turns=4.0, trained_len=8192))])
+def test_rope_steps(lib, rot, base, scaling, kw):
+    """Against 50-digit arithmetic: the angle at a far position is within pos * f * 2^-50 radians."""
+    getcontext().prec = 50
+    got = pkg.attn_rope_steps(rot, base, scaling, **kw)
+    assert len(got) == rot // 2
+    factor = Decimal(kw.get("factor", 1.0))
+    b = Decimal(base) * (factor ** (Decimal(rot) / Decimal(rot - 2)) if scaling == 2 else 1)
+    for i, step in enumerate(got):
+        f = b ** (Decimal(-2 * i) / Decimal(rot))
+        if scaling == 1:
+            f = f / factor
+        if scaling == 3:
+            n = Decimal(kw["trained_len"]) * f / (2 * PI)
+            lo, hi = Decimal(kw["low_turns"]), Decimal(kw["high_turns"])
+            keep = min(max((n - lo) / (hi - lo), Decimal(0)), Decimal(1))
+            f = keep * f + (1 - keep) * f / factor
+        want = f / (2 * PI) * Decimal(2) ** 64
+        assert abs(Decimal(step) - want) <= want * Decimal(2) ** -50 + Decimal("0.5"), i
+
+
+def test_rope_steps_refusals(lib):
+    buf = (ctypes.c_uint64 * 128)()
+    a = ctypes.addressof(buf)
+    inf, nan = math.inf, math.nan
+    for args in ((0, 1e4, 0, 1, 0, 0, 0), (24, 1e4, 0, 1, 0, 0, 0), (272, 1e4, 0, 1, 0, 0, 0),
+                 (64, 0.5, 0, 1, 0, 0, 0), (64, nan, 0, 1, 0, 0, 0), (64, inf, 0, 1, 0, 0, 0),
+                 (64, 1e4, 4, 1, 0, 0, 0), (64, 1e4, -1, 1, 0, 0, 0), (64, 1e4, 1, 0.0, 0, 0, 0),
+                 (64, 1e4, 1, nan, 0, 0, 0), (64, 1e4, 1, 0.01, 0, 0, 0),      # more than a turn per position
+                 (64, 1e4, 3, 8, 4, 4, 10), (64, 1e4, 3, 8, 1, 4, 0), (64, 1e4, 3, 8, nan, 4, 10)):
+        assert lib.attn_rope_steps(*args, a) == INVALID, args
+    assert lib.attn_rope_steps(64, 1e4, 0, 1.0, 0.0, 0.0, 0, None) == INVALID
+    assert all(x == 0 for x in buf)                                    # nothing written on a refusal
+
+
+def test_reference_codes():
+    """The tests' own e4m3: exact on every code, ties to even, against torch's cast."""
+    torch = pytest.importorskip("torch")
+    codes = np.arange(256, dtype=np.uint8)
+    want = torch.from_numpy(codes).view(torch.float8_e4m3fn).double().numpy()
+    np.testing.assert_array_equal(ref.VALUES, want)
+    fin = codes[np.isfinite(ref.VALUES)]
+    np.testing.assert_array_equal(ref.to_e4m3(ref.VALUES[fin]), fin)
+    x = np.random.default_rng(0).standard_normal(20000) * np.exp(np.random.default_rng(1).uniform(-8, 5, 20000))
+    mid = (ref.VALUES[:126] + ref.VALUES[1:127]) / 2                   # ties
+    x = np.concatenate([x, mid, -mid]).clip(-448, 448)
+    got = torch.from_numpy(x).float().to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    np.testing.assert_array_equal(ref.to_e4m3(x.astype(np.float32)), got)
+    for a in (1.0, 447.9, 448.0, 448.1, 3e-5, 1e30, 0.0):
+        s = ref.scale_for(a)
+        assert (a <= 448 * s or s == 2.0 ** 60) and (a > 224 * s or s == 2.0 ** -60)
