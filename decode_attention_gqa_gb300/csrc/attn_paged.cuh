@@ -17,10 +17,12 @@
 // gcd(page_size, 64) rows, swizzled) and leaves the page's scales with the
 // stage. Rows a block does not attend are neither waited for nor used.
 //
-// Tensor cores. 16x8x16 MMAs, f32 accumulation; q and p as hi + lo pairs of the
-// cache's type (f16 for e4m3, whose codes f16 holds exactly). With 8 slots the
-// 16 MMA rows are the hi and the lo parts, with 16 slots each part has its own
-// MMA. The order of a dot product's terms is free, so a lane's share of a K row
+// Tensor cores. 16x8x16 MMAs, f32 accumulation; q and p as two f16 parts (an f16
+// or e4m3 cache; f16 holds the codes exactly) or three bf16 parts, so that
+// neither loses what 32 bits hold. S = Q Kᵀ: with 8 slots two parts lie over each
+// other in the 16 MMA rows, with 16 slots each part has its own MMA. Oᵀ = Vᵀ Pᵀ: the
+// parts of p add up in one accumulator, 4 registers for 16 dimensions x 8 slots,
+// and P is used in the registers where S was accumulated. The order of a dot product's terms is free, so a lane's share of a K row
 // is contiguous: 16-byte shared loads give it whole k-steps, with no
 // ldmatrix and, for 8 bits, no shuffling before the conversion. 8-bit V
 // needs pairs of rows in a register: a lane reads its four rows' 16
@@ -43,6 +45,11 @@ template <typename KV> struct PagedMma { using T = KV; };
 template <> struct PagedMma<E4m3> { using T = __half; };
 
 constexpr unsigned kErrBadPage = 0x4u;    // ATTN_DEVERR_BAD_PAGE
+
+__device__ __forceinline__ int div(const FastDiv &d, int n)
+{
+    return (int)((__umulhi((unsigned)n, d.mul) + (unsigned)n) >> d.shift);
+}
 
 // Two e4m3 codes (in 16 bits) to two f16 values, exact.
 __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint16_t w)
@@ -79,37 +86,52 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], uint32_t p)
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(p));
 }
 
-template <int HD_, int SLOTS_, typename KV_, int S_, int MINB_>
+template <int HD_, int SLOTS_, typename KV_>
 struct PagedCfg {
-    static constexpr int HD = HD_, SLOTS = SLOTS_, S = S_, MIN_BLOCKS = MINB_;
+    static constexpr int HD = HD_, SLOTS = SLOTS_;
     using KV = KV_;
     using MT = typename PagedMma<KV>::T;
     static constexpr bool E8 = std::is_same<KV, E4m3>::value;
     static constexpr int ES = E8 ? 1 : 2;
-    static constexpr int NWC = 4, WR = 16, TILE = NWC * WR, NSL = TILE / WR;
+    static constexpr PagedShape SHAPE = paged_shape(HD, ES, SLOTS);
+    static constexpr int S = SHAPE.stages, MIN_BLOCKS = SHAPE.blocks;
+    static constexpr int NWC = SHAPE.warps, WR = 16, NSL = SHAPE.nsl, TILE = NSL * WR;
+    static constexpr int WPT = NWC / NSL;                         // stages the warps work on at a time
     static constexpr int THREADS = (NWC + 1) * 32;
+    static constexpr int TPG = 32 / NSL;                          // tiles of a descriptor group
     static constexpr int ROWB = HD * ES;                          // bytes of a row of one head
     static constexpr int CHB = ROWB < 128 ? ROWB : 128;           // bytes of a swizzled chunk's row
     static constexpr int NCH = ROWB / CHB;
     static constexpr int CW = CHB / ES;                           // dimensions of a chunk
     static constexpr uint32_t TILE_BYTES = (uint32_t)TILE * ROWB;
     static constexpr uint32_t STAGE_BYTES = 2 * TILE_BYTES;
-    static constexpr int KSTEPS = HD / 16, NTD = HD / 8;
+    static constexpr int KSTEPS = HD / 16;
     static constexpr int KPC = CW / 16;                           // k-steps of a chunk
-    static constexpr int PARTS = SLOTS / 8;                       // Q operands: 1 (hi over lo) or 2 (hi, lo)
     static constexpr int SPL = SLOTS / 8;                         // slots a lane owns
-    static constexpr bool Q_REGS = E8 && HD <= 128 && SLOTS == 8;   // else they are read per k-step (no spills)
-    static constexpr uint32_t Q_BYTES = (uint32_t)PARTS * KSTEPS * 512;   // fragments, 16 bytes a lane
-    static constexpr uint32_t OFF_Q = S * STAGE_BYTES;
-    static constexpr uint32_t OFF_SLOT = OFF_Q + Q_BYTES;         // SlotInfo[SLOTS]
-    static constexpr uint32_t OFF_INFO = OFF_SLOT + SLOTS * 16;   // SliceInfo[S][NSL]
-    static constexpr uint32_t OFF_BAR = OFF_INFO + S * NSL * 16;
-    static constexpr uint32_t SMEM_BYTES = OFF_BAR + 2 * S * 8 + 16 + 1024;
+    // 16-bit parts that carry q and p: two f16 (22 bits), three bf16 (24; two would keep 16)
+    static constexpr int NP = std::is_same<MT, __nv_bfloat16>::value ? 3 : 2;
+    // Q operands: 8 slots: parts in pairs, one over the other in the 16 rows (a third part alone: half
+    // an operand); 16 slots: a part each
+    static constexpr int PARTS = SLOTS == 8 ? (NP + 1) / 2 : NP;
+    static constexpr bool Q_REGS = E8 && HD == 64 && SLOTS == 8;   // else they are read per k-step (no spills)
+    static constexpr uint32_t Q_BYTES = (uint32_t)(SLOTS == 8 ? NP : 2 * NP) * KSTEPS * 256;
     static constexpr int MS = merge_stride<HD>();
-    static constexpr uint32_t OFF_MO = (uint32_t)2 * NWC * SLOTS;   // floats, a multiple of 4
-    static_assert((OFF_MO + (uint32_t)NWC * SLOTS * MS) * 4 <= S * STAGE_BYTES, "merge area must fit in the ring");
+    static constexpr uint32_t OFF_MO = 2 * NWC * SLOTS;           // floats, a multiple of 4
+    static constexpr uint32_t MERGE_BYTES = (OFF_MO + SLOTS * MS) * 4;
+    static constexpr uint32_t OFF_Q = S * STAGE_BYTES;            // Q fragments; then the merge area
+    static constexpr uint32_t OFF_SLOT = OFF_Q + (Q_BYTES > MERGE_BYTES ? Q_BYTES : MERGE_BYTES);
+    static constexpr uint32_t OFF_SEG = OFF_SLOT + SLOTS * 16;    // SegInfo
+    static constexpr uint32_t OFF_DESC = OFF_SEG + 32;            // SliceInfo[4][32]
+    static constexpr uint32_t OFF_BAR = OFF_DESC + 4 * 32 * 16;
+    static constexpr uint32_t OFF_SEQ = OFF_BAR + 2 * S * 8 + 16;
+    static constexpr uint32_t SMEM_BYTES = OFF_SEQ + (3 * kPagedSeqs + 1) * 4;
+    static_assert(NWC % NSL == 0 && S <= TPG, "descriptor buffers outlive the stages in flight");
+    // a warp waits for the phases of its own stages only: if a stage changed hands, a warp could take the
+    // parity of an older phase for its own
+    static_assert(S % WPT == 0, "a stage belongs to the same warps throughout");
+    static_assert((size_t)NWC * SLOTS * MS * 4 <= S * STAGE_BYTES, "the last merge lies over the ring");
     static_assert(SMEM_BYTES <= 227 * 1024 && MIN_BLOCKS * (SMEM_BYTES + 1024u) <= 233472u, "shared memory");
-    static_assert((TILE_BYTES / NCH) % 1024 == 0, "swizzled chunks stay 1024-aligned");
+    static_assert((TILE_BYTES / NCH) % 1024 == 0 && OFF_MO % 4 == 0, "alignment");
 
     // Rows are stored as chunks of CHB bytes, swizzled as TMA writes them. `row` is the offset of a row
     // with its swizzle bits set; `unit` adds 16-byte unit U: one exclusive or with a constant
@@ -125,17 +147,23 @@ struct PagedCfg {
     }
 };
 
-struct __align__(16) SliceInfo {  // of one 16-row slice of a stage
-    int page;             // -1: not there
+struct __align__(16) SliceInfo {  // of one 16-row slice
+    int page;             // -1: not there, or nothing the stage needs
+    int z;                // its first row in the page
     float ks, vs;
-    int pad;
 };
 
-struct __align__(16) SlotInfo {   // of one (query row, head) slot of the block
+struct __align__(16) SlotInfo {   // of one (query row, head) slot of the block, for the sequence at hand
     float inv;            // undoes the power of two q was scaled by
     float slope;          // times log2 e
-    int t;                // query row, -1: no such slot
-    int pad;
+    int last, low;        // the rows it sees; no such slot: -1, 0
+};
+
+struct __align__(16) SegInfo {    // the sequence at hand
+    int seen_lo, seen_hi; // rows every slot of the block sees
+    int any_lo, any_hi;   // rows some slot sees
+    int row0;             // first row of the block's tile 0, were it this sequence's
+    int seq, from, to;    // the sequence, and its tiles of this block
 };
 
 // The rows the slots of query rows [t0, t1] see, as [first row of t0, last row of t1]
@@ -155,13 +183,18 @@ struct PagedWarp {
     static constexpr float TAU = 8.f, OFF = 7.f;      // lazy rescale threshold, headroom of p (log2)
     using MT = typename C::MT;
     uint32_t qa[C::Q_REGS ? C::KSTEPS : 1][4];
-    float o[C::NTD][4];
+    float o[C::SPL][C::HD / 16][4];    // Oᵀ: 16 dimensions x 8 slots a tile
     float m[C::SPL], l[C::SPL];
 
-    static __device__ __forceinline__ SlotInfo slot(uint32_t smem, int k, int lane)
+    static __device__ __forceinline__ SlotInfo slot_at(uint32_t smem, int i)
     {
-        const uint4 u = lds128(smem + C::OFF_SLOT + ((lane >> 2) + 8 * k) * 16);
-        return SlotInfo{__uint_as_float(u.x), __uint_as_float(u.y), (int)u.z, 0};
+        const uint4 u = lds128(smem + C::OFF_SLOT + i * 16);
+        return SlotInfo{__uint_as_float(u.x), __uint_as_float(u.y), (int)u.z, (int)u.w};
+    }
+    static __device__ __forceinline__ int4 seg_rows(uint32_t smem)        // seen_lo, seen_hi, any_lo, any_hi
+    {
+        const uint4 u = lds128(smem + C::OFF_SEG);
+        return make_int4((int)u.x, (int)u.y, (int)u.z, (int)u.w);
     }
 
     __device__ __forceinline__ void init(uint32_t smem, int lane)
@@ -171,11 +204,11 @@ struct PagedWarp {
             for (int kk = 0; kk < C::KSTEPS; ++kk) load_q(qa[kk], smem, 0, kk, lane);
         }
 #pragma unroll
-        for (int n = 0; n < C::NTD; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
-#pragma unroll
         for (int k = 0; k < C::SPL; ++k) {
+#pragma unroll
+            for (int n = 0; n < C::HD / 16; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[k][n][i] = 0.f;
             m[k] = -INFINITY;
             l[k] = 0.f;
         }
@@ -183,8 +216,14 @@ struct PagedWarp {
 
     static __device__ __forceinline__ void load_q(uint32_t (&f)[4], uint32_t smem, int part, int kk, int lane)
     {
-        const uint4 u = lds128(smem + C::OFF_Q + ((uint32_t)(part * C::KSTEPS + kk) * 32 + lane) * 16);
-        f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w;
+        if (C::SLOTS == 8 && C::NP == 3 && part == 1) {        // rows 8-15 have no part
+            const uint2 u = lds64(smem + C::OFF_Q + C::KSTEPS * 512 + (uint32_t)(kk * 32 + lane) * 8);
+            f[0] = u.x; f[2] = u.y;
+            f[1] = f[3] = 0u;
+        } else {
+            const uint4 u = lds128(smem + C::OFF_Q + ((uint32_t)(part * C::KSTEPS + kk) * 32 + lane) * 16);
+            f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w;
+        }
     }
 
     // Scores of the slice at stage row r0: c[k][j], slot k of the lane, row j of
@@ -192,7 +231,7 @@ struct PagedWarp {
     __device__ __forceinline__ void scores(float (&sc)[C::SPL][4], uint32_t smem, uint32_t ks, int r0, int lane)
     {
         const int g = lane >> 2, u = lane & 3;
-        float acc[2][2][4];      // [even and odd k-steps, or hi and lo][rows 0-7, 8-15]
+        float acc[2][2][4];      // [two chains][rows 0-7, 8-15]
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -227,24 +266,18 @@ struct PagedWarp {
                             b[n][1] = w[n][2 * i + 1];
                         }
                     }
-                    if constexpr (C::SLOTS == 8) {
+#pragma unroll
+                    for (int part = 0; part < C::PARTS; ++part) {
                         uint32_t f[4];
                         if constexpr (C::Q_REGS) {
 #pragma unroll
                             for (int x = 0; x < 4; ++x) f[x] = qa[kk][x];
                         } else {
-                            load_q(f, smem, 0, kk, lane);
+                            load_q(f, smem, part, kk, lane);
                         }
-                        mma_16816<MT>(acc[kk & 1][0], f, b[0][0], b[0][1]);
-                        mma_16816<MT>(acc[kk & 1][1], f, b[1][0], b[1][1]);
-                    } else {
-                        uint32_t fh[4], fl[4];
-                        load_q(fh, smem, 0, kk, lane);
-                        load_q(fl, smem, 1, kk, lane);
-                        mma_16816<MT>(acc[0][0], fh, b[0][0], b[0][1]);
-                        mma_16816<MT>(acc[1][0], fl, b[0][0], b[0][1]);
-                        mma_16816<MT>(acc[0][1], fh, b[1][0], b[1][1]);
-                        mma_16816<MT>(acc[1][1], fl, b[1][0], b[1][1]);
+                        const int e = C::PARTS == 1 ? kk & 1 : part & 1;
+                        mma_16816<MT>(acc[e][0], f, b[0][0], b[0][1]);
+                        mma_16816<MT>(acc[e][1], f, b[1][0], b[1][1]);
                     }
                 }
             }
@@ -260,36 +293,36 @@ struct PagedWarp {
         }
     }
 
-    // One pair of n-tiles' worth of P.V; `ph`, `pl` are the A operands (8 slots: ph holds both parts).
-    __device__ __forceinline__ void mma_pv(float (&acc)[4], const uint32_t (&ph)[4], const uint32_t (&pl)[4],
-                                           uint32_t b0, uint32_t b1)
-    {
-        mma_16816<MT>(acc, ph, b0, b1);
-        if constexpr (C::SLOTS == 16) mma_16816<MT>(acc, pl, b0, b1);
-    }
-
-    // O += P.V over the slice. EDGE: V rows whose bits in m0 (rows 2u, 2u+1) and m1 (rows 8+2u,
+    // Oᵀ += Vᵀ Pᵀ over the slice, V's 16 dimensions x 16 rows as the A operand, so that all parts of p add
+    // up in the same accumulators. P's B fragments (slot g, rows 2u, 2u+1 and 8+2u, 9+2u) are where the
+    // scores' accumulators left them. EDGE: V rows whose bits in m0 (rows 2u, 2u+1) and m1 (rows 8+2u,
     // 9+2u) are clear are taken as 0.
     template <bool EDGE>
-    __device__ __forceinline__ void values(uint32_t vs, int r0, const uint32_t (&ph)[4], const uint32_t (&pl)[4],
-                                           uint32_t m0, uint32_t m1, int lane)
+    __device__ __forceinline__ void values(uint32_t vs, int r0, const uint32_t (&pb)[C::SPL][C::NP][2], uint32_t m0,
+                                           uint32_t m1, int lane)
     {
-        auto step = [&](int n, uint32_t b0, uint32_t b1) {
-            if constexpr (EDGE) mma_pv(o[n], ph, pl, b0 & m0, b1 & m1);
-            else mma_pv(o[n], ph, pl, b0, b1);
+        auto step = [&](int n, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+            uint32_t f[4] = {a0, a1, a2, a3};
+            if constexpr (EDGE) {
+                f[0] &= m0; f[1] &= m0; f[2] &= m1; f[3] &= m1;
+            }
+#pragma unroll
+            for (int x = 0; x < C::NP; ++x)
+#pragma unroll
+                for (int k = 0; k < C::SPL; ++k) mma_16816<MT>(o[k][n], f, pb[k][x][0], pb[k][x][1]);
         };
         if constexpr (C::E8) {
-            // n-tile n = c * TPC + j holds dimension c * CW + g * TPC + j in column g
+            // tile n = c * TPC + j holds dimensions c * CW + g * 2 TPC + 2 j and the next in rows g and g + 8
             const int g = lane >> 2, u = lane & 3;
-            constexpr int TPC = C::CW / 8;            // n-tiles of a chunk: 16, or 8 at head_dim 64
-            const uint32_t in = TPC == 16 ? (uint32_t)(g << 4) : (uint32_t)((g >> 1) << 4);
+            constexpr int TPC = C::CW / 16;           // tiles of a chunk: 8, or 4 at head_dim 64
+            const uint32_t in = TPC == 8 ? (uint32_t)(g << 4) : (uint32_t)((g >> 1) << 4);
             const uint32_t vr[2] = {vs + (C::row(r0 + 2 * u) ^ in), vs + (C::row(r0 + 2 * u + 1) ^ in)};
             // words of a row a lane holds at once: all of a chunk's, or half (registers)
-            constexpr int NW = TPC == 16 && !(C::HD == 256 && C::SLOTS == 16) ? 4 : 2;
+            constexpr int NW = TPC == 8 && C::SLOTS == 8 ? 4 : 2;
 #pragma unroll
             for (int c = 0; c < C::NCH; ++c)
 #pragma unroll
-                for (int h = 0; h < TPC / 4; h += NW) {
+                for (int h = 0; h < TPC / 2; h += NW) {
                     uint32_t w[4][NW];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
@@ -298,7 +331,7 @@ struct PagedWarp {
                             const uint4 x = lds128(at);
                             w[r][0] = x.x; w[r][1] = x.y; w[r][2] = x.z; w[r][3] = x.w;
                         } else {
-                            const uint2 x = lds64(at + (TPC == 16 ? h * 4 : (g & 1) * 8));
+                            const uint2 x = lds64(at + (TPC == 8 ? h * 4 : (g & 1) * 8));
                             w[r][0] = x.x; w[r][1] = x.y;
                         }
                     }
@@ -309,67 +342,73 @@ struct PagedWarp {
                         e4m3x4_to_half4(__byte_perm(w[0][i], w[1][i], 0x7362), a[2], a[3]);
                         e4m3x4_to_half4(__byte_perm(w[2][i], w[3][i], 0x5140), b[0], b[1]);
                         e4m3x4_to_half4(__byte_perm(w[2][i], w[3][i], 0x7362), b[2], b[3]);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) step(c * TPC + (h + i) * 4 + j, a[j], b[j]);
+                        step(c * TPC + (h + i) * 2, a[0], a[1], b[0], b[1]);
+                        step(c * TPC + (h + i) * 2 + 1, a[2], a[3], b[2], b[3]);
                     }
                 }
         } else {
+            // tile n holds dimensions 16 n + g and 16 n + 8 + g in rows g and g + 8
             const int i8 = lane >> 3;
             const uint32_t vr = vs + (C::row(r0 + (i8 & 1) * 8 + (lane & 7)) ^ (uint32_t)((i8 >> 1) << 4));
 #pragma unroll
-            for (int n = 0; n < C::NTD; n += 2) {
+            for (int n = 0; n < C::HD / 16; ++n) {
                 uint32_t b[4];
-                ldsm_x4_trans(b, C::unit(vr, n));
-                step(n, b[0], b[1]);
-                step(n + 1, b[2], b[3]);
+                ldsm_x4_trans(b, C::unit(vr, 2 * n));
+                step(n, b[0], b[2], b[1], b[3]);
             }
         }
     }
 
-    // o += p v for slice row r alone, v that row of V, by the lanes that have `sees` set (their slot k sees it).
-    __device__ __forceinline__ void add_row(uint32_t vs, int r, int k, float p, bool sees, int lane)
+    // o += p v for stage row r alone: p0, p1 of the lane's accumulators' slots 2u and 2u+1 (+ 8 k), each
+    // only where that slot sees the row.
+    __device__ __forceinline__ void add_row(uint32_t vs, int r, int k, float p0, float p1, bool s0, bool s1, int lane)
     {
-        if (!sees) return;
-        const int u = lane & 3, at = C::SLOTS == 8 ? 0 : 2 * k;
+        const int g = lane >> 2;
+        auto add = [&](int n, float v0, float v1) {
+            if (s0) {
+                o[k][n][0] = fmaf(p0, v0, o[k][n][0]);
+                o[k][n][2] = fmaf(p0, v1, o[k][n][2]);
+            }
+            if (s1) {
+                o[k][n][1] = fmaf(p1, v0, o[k][n][1]);
+                o[k][n][3] = fmaf(p1, v1, o[k][n][3]);
+            }
+        };
         if constexpr (C::E8) {
-            constexpr int TPC = C::CW / 8;
+            constexpr int TPC = C::CW / 16;
 #pragma unroll
             for (int c = 0; c < C::NCH; ++c)
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
+                for (int h = 0; h < TPC; h += 4) {
+                    const int d = g * 2 * TPC + 2 * h;                 // 8 dimensions from d of the chunk
+                    const uint2 x = lds64(vs + (C::row(r) ^ (uint32_t)(d >> 4 << 4)) + c * (C::TILE * 128) + (d & 15));
 #pragma unroll
-                    for (int h = 0; h < TPC; h += 8) {
-                        const int d = (2 * u + e) * TPC + h;       // 8 dimensions from d of the chunk
-                        const uint2 x = lds64(vs + (C::row(r) ^ (uint32_t)(d >> 4 << 4)) + c * (C::TILE * 128) + (d & 15));
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            uint32_t w0, w1;
-                            e4m3x4_to_half4(i ? x.y : x.x, w0, w1);
-                            const float2 f0 = kv2_to_float2<__half>(w0), f1 = kv2_to_float2<__half>(w1);
-                            const int n = c * TPC + h + 4 * i;
-                            o[n][at + e] = fmaf(p, f0.x, o[n][at + e]);
-                            o[n + 1][at + e] = fmaf(p, f0.y, o[n + 1][at + e]);
-                            o[n + 2][at + e] = fmaf(p, f1.x, o[n + 2][at + e]);
-                            o[n + 3][at + e] = fmaf(p, f1.y, o[n + 3][at + e]);
-                        }
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t w0, w1;
+                        e4m3x4_to_half4(i ? x.y : x.x, w0, w1);
+                        const float2 f0 = kv2_to_float2<__half>(w0), f1 = kv2_to_float2<__half>(w1);
+                        add(c * TPC + h + 2 * i, f0.x, f0.y);
+                        add(c * TPC + h + 2 * i + 1, f1.x, f1.y);
                     }
+                }
         } else {
 #pragma unroll
-            for (int n = 0; n < C::NTD; ++n) {
-                uint32_t x;
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(C::unit(vs + C::row(r), n) + 4 * u));
-                const float2 f = kv2_to_float2<MT>(x);
-                o[n][at] = fmaf(p, f.x, o[n][at]);
-                o[n][at + 1] = fmaf(p, f.y, o[n][at + 1]);
+            for (int n = 0; n < C::HD / 16; ++n) {
+                uint16_t x0, x1;
+                const uint32_t at = vs + C::row(r);
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x0) : "r"(C::unit(at, 2 * n) + 2 * g));
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x1) : "r"(C::unit(at, 2 * n + 1) + 2 * g));
+                const float2 f = kv2_to_float2<MT>((uint32_t)x0 | (uint32_t)x1 << 16);
+                add(n, f.x, f.y);
             }
         }
     }
 
     // The slice at stage row r0, cache rows [row0, row0 + 16). edge: some slot of the block does not see all of them.
-    __device__ __forceinline__ void process(uint32_t smem, uint32_t ks, uint32_t vs, int r0, int row0,
-                                            const SliceInfo &info, bool edge, const SlotRows &sr, int t0, int t1,
-                                            const PagedArgs &a, int lane)
+    __device__ __forceinline__ void process(uint32_t smem, uint32_t ks, int r0, int row0, float kscale, float vscale,
+                                            bool edge, float cap_log2, int lane)
     {
+        const uint32_t vs = ks + C::TILE_BYTES;
         const int u = lane & 3;
         const int col[4] = {2 * u, 2 * u + 1, 8 + 2 * u, 9 + 2 * u};
         float sc[C::SPL][4];
@@ -377,28 +416,27 @@ struct PagedWarp {
         // log2 of the V scale, rounded up: its exponent field
         float lv = 0.f;
         if constexpr (C::E8) {
-            const int e = (int)((__float_as_uint(info.vs) >> 23) & 0xFFu) - 126;
+            const int e = (int)((__float_as_uint(vscale) >> 23) & 0xFFu) - 126;
             lv = (float)min(max(e, -60), 61);
         }
 #pragma unroll
         for (int k = 0; k < C::SPL; ++k) {
-            const SlotInfo si = slot(smem, k, lane);
-            const float f = C::E8 ? si.inv * info.ks : si.inv;
+            const SlotInfo si = slot_at(smem, (lane >> 2) + 8 * k);
+            const float f = C::E8 ? si.inv * kscale : si.inv;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float x = sc[k][j] * f;
                 if constexpr (RULES) {
-                    if (a.cap_log2 > 0.f) x = a.cap_log2 * tanhf(x);
-                    x = fmaf(si.slope, (float)(row0 + col[j] - sr.last(si.t)), x);
+                    if (cap_log2 > 0.f) x = cap_log2 * tanhf(x);
+                    x = fmaf(si.slope, (float)(row0 + col[j] - si.last), x);
                 }
                 sc[k][j] = x;
             }
             if (edge) {
-                const int last = si.t < 0 ? -1 : sr.last(si.t), low = si.t < 0 ? 0 : sr.low(si.t);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int row = row0 + col[j];
-                    if (row > last || row < low) sc[k][j] = -INFINITY;
+                    if (row > si.last || row < si.low) sc[k][j] = -INFINITY;
                 }
             }
         }
@@ -415,126 +453,161 @@ struct PagedWarp {
             any |= need[k];
         }
         if (__any_sync(0xffffffffu, any)) {
-            float corr[2] = {1.f, 1.f};
 #pragma unroll
             for (int k = 0; k < C::SPL; ++k) {
+                float corr = 1.f;
                 if (need[k]) {
-                    corr[k] = ex2(m[k] - mt[k]);       // 0 while m is -inf
+                    corr = ex2(m[k] - mt[k]);          // 0 while m is -inf
                     m[k] = mt[k];
                 }
-                l[k] *= corr[k];
+                l[k] *= corr;
+                // the accumulators' slots are 2u and 2u + 1
+                const float c0 = __shfl_sync(0xffffffffu, corr, 8 * u), c1 = __shfl_sync(0xffffffffu, corr, 8 * u + 4);
+#pragma unroll
+                for (int n = 0; n < C::HD / 16; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[k][n][i] *= i & 1 ? c1 : c0;
             }
-            if constexpr (C::SLOTS == 8) corr[1] = corr[0];
-#pragma unroll
-            for (int n = 0; n < C::NTD; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[n][i] *= corr[i >> 1];
         }
-        uint32_t ph[4], pl[4];
+        // the scores become the weights
+#pragma unroll
+        for (int k = 0; k < C::SPL; ++k) {
+            const float base = m[k] == -INFINITY ? 0.f : m[k] - OFF;     // no row seen yet: every p is 0
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sc[k][j] = ex2(sc[k][j] - base);
+            l[k] += (sc[k][0] + sc[k][1]) + (sc[k][2] + sc[k][3]);
+            if constexpr (C::E8) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sc[k][j] *= vscale;
+            }
+        }
         // A row that a slot does not see must not reach it: its weight 0 times what an unwritten or
         // unseen row holds (NaN, infinity) would. Rows that every slot of the block sees go
         // through the MMAs, with the others' V taken as 0; rows that only some query rows see (the last n_q - 1,
         // and as many at a window's start) are added one by one to the slots that see them.
-        const bool some = edge && t0 != t1;
+        if (edge) {
+            const int4 sg = seg_rows(smem);
+            if (sg.x != sg.z || sg.y != sg.w) {
 #pragma unroll
-        for (int k = 0; k < C::SPL; ++k) {
-            const float base = m[k] == -INFINITY ? 0.f : m[k] - OFF;     // no row seen yet: every p is 0
-            float p[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) p[j] = ex2(sc[k][j] - base);
-            l[k] += (p[0] + p[1]) + (p[2] + p[3]);
-            if constexpr (C::E8) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) p[j] *= info.vs;
-            }
-            if (some) {
-                const int st = slot(smem, k, lane).t;
+                for (int k = 0; k < C::SPL; ++k) {
+                    const SlotInfo sa = slot_at(smem, 2 * u + 8 * k), sb = slot_at(smem, 2 * u + 1 + 8 * k);
 #pragma unroll 1
-                for (int r = 0; r < C::WR; ++r) {
-                    const int row = row0 + r;
-                    if (row > sr.last(t1) || row < sr.low(t0) || (row <= sr.last(t0) && row >= sr.low(t1))) continue;
-                    const float x = r & 8 ? (r & 1 ? p[3] : p[2]) : (r & 1 ? p[1] : p[0]);
-                    const float pr = __shfl_sync(0xffffffffu, x, (lane & ~3) | ((r & 7) >> 1));
-                    add_row(vs, r0 + r, k, pr, st >= 0 && row <= sr.last(st) && row >= sr.low(st), lane);
+                    for (int r = 0; r < C::WR; ++r) {
+                        const int row = row0 + r;
+                        if (row < sg.z || row > sg.w || (row >= sg.x && row <= sg.y)) continue;
+                        const float x = r & 8 ? (r & 1 ? sc[k][3] : sc[k][2]) : (r & 1 ? sc[k][1] : sc[k][0]);
+                        const float p0 = __shfl_sync(0xffffffffu, x, 8 * u + ((r & 7) >> 1));
+                        const float p1 = __shfl_sync(0xffffffffu, x, 8 * u + 4 + ((r & 7) >> 1));
+                        add_row(vs, r0 + r, k, p0, p1, row <= sa.last && row >= sa.low, row <= sb.last && row >= sb.low,
+                                lane);
+                    }
                 }
             }
-            const uint32_t h01 = float2_to_kv2<MT>(p[0], p[1]), h23 = float2_to_kv2<MT>(p[2], p[3]);
-            const float2 f01 = kv2_to_float2<MT>(h01), f23 = kv2_to_float2<MT>(h23);
-            const uint32_t l01 = float2_to_kv2<MT>(p[0] - f01.x, p[1] - f01.y);
-            const uint32_t l23 = float2_to_kv2<MT>(p[2] - f23.x, p[3] - f23.y);
-            if constexpr (C::SLOTS == 8) {
-                ph[0] = h01; ph[1] = l01; ph[2] = h23; ph[3] = l23;
-                pl[0] = pl[1] = pl[2] = pl[3] = 0u;
-            } else {
-                ph[k] = h01; ph[2 + k] = h23;
-                pl[k] = l01; pl[2 + k] = l23;
-            }
         }
-        if (!edge) {
-            values<false>(vs, r0, ph, pl, 0u, 0u, lane);
-        } else {
-            uint32_t mask[2] = {0u, 0u};
+        // p in NP parts: each the rounding of what the ones before leave
+        uint32_t pb[C::SPL][C::NP][2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int row = row0 + col[j];
-                if (row <= sr.last(t0) && row >= sr.low(t1)) mask[j >> 1] |= 0xFFFFu << (16 * (j & 1));
+        for (int k = 0; k < C::SPL; ++k)
+#pragma unroll
+            for (int x = 0; x < C::NP; ++x)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    pb[k][x][h] = float2_to_kv2<MT>(sc[k][2 * h], sc[k][2 * h + 1]);
+                    const float2 f = kv2_to_float2<MT>(pb[k][x][h]);
+                    sc[k][2 * h] -= f.x;
+                    sc[k][2 * h + 1] -= f.y;
+                }
+        // three parts of p (bf16): one copy of the sweep, masked throughout (the second would not fit the registers)
+        if (C::NP == 2 && !edge) {
+            values<false>(vs, r0, pb, 0u, 0u, lane);
+        } else {
+            uint32_t mask[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+            if (edge) {
+                const int4 sg = seg_rows(smem);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int row = row0 + col[j];
+                    if (row < sg.x || row > sg.y) mask[j >> 1] &= 0xFFFFu << (16 * (1 - (j & 1)));
+                }
             }
-            values<true>(vs, r0, ph, pl, mask[0], mask[1], lane);
+            values<true>(vs, r0, pb, mask[0], mask[1], lane);
         }
     }
 
-    // mm[slot] = (reference, sum), mo[slot * MS + d] = accumulator.
-    __device__ __forceinline__ void publish(float2 *mm, float *mo, int lane)
+    // (reference, sum) of the warp's slots. A slot that has seen no row has -inf; one whose every score is NaN
+    // keeps its NaN sum.
+    __device__ __forceinline__ void publish(float2 *mm, int lane)
     {
-        const int g = lane >> 2, u = lane & 3;
 #pragma unroll
         for (int k = 0; k < C::SPL; ++k) {
             float lt = l[k];
             lt += __shfl_xor_sync(0xffffffffu, lt, 1);
             lt += __shfl_xor_sync(0xffffffffu, lt, 2);
-            const int i = g + 8 * k;
-            if (u == 0) mm[i] = make_float2(m[k] - OFF, lt);
-            auto val = [&](int n, int e) {
-                return C::SLOTS == 8 ? o[n][e] + o[n][2 + e] : o[n][2 * k + e];
-            };
-            if constexpr (C::E8) {
-                constexpr int TPC = C::CW / 8;
-#pragma unroll
-                for (int c = 0; c < C::NCH; ++c)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int j = 0; j < TPC; j += 4) {
-                            const int n = c * TPC + j;
-                            *reinterpret_cast<float4 *>(mo + i * C::MS + c * C::CW + (2 * u + e) * TPC + j) =
-                                make_float4(val(n, e), val(n + 1, e), val(n + 2, e), val(n + 3, e));
-                        }
-            } else {
-#pragma unroll
-                for (int n = 0; n < C::NTD; ++n)
-                    *reinterpret_cast<float2 *>(mo + i * C::MS + n * 8 + 2 * u) = make_float2(val(n, 0), val(n, 1));
-            }
+            if ((lane & 3) == 0)
+                mm[(lane >> 2) + 8 * k] = make_float2(m[k] == -INFINITY && lt != 0.f ? 0.f : m[k] - OFF, lt);
         }
+    }
+
+    // The accumulators, scaled to the largest reference among the warps, into (add: onto) mo[slot * MS + d].
+    __device__ __forceinline__ void deposit(const float2 *mm, float *mo, int warp, bool add, int lane)
+    {
+        const int g = lane >> 2, u = lane & 3;
+#pragma unroll
+        for (int k = 0; k < C::SPL; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 2 * u + e + 8 * k;
+                float M = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < C::NWC; ++w) M = fmaxf(M, mm[w * C::SLOTS + i].x);
+                const float x = mm[warp * C::SLOTS + i].x;
+                const float wt = x == -INFINITY ? 0.f : ex2(x - M);
+                float *row = mo + i * C::MS;
+                if constexpr (C::E8) {
+                    constexpr int TPC = C::CW / 16;
+#pragma unroll
+                    for (int c = 0; c < C::NCH; ++c)
+#pragma unroll
+                        for (int j = 0; j < TPC; j += 2) {
+                            const int n = c * TPC + j;
+                            float4 *p = reinterpret_cast<float4 *>(row + c * C::CW + g * 2 * TPC + 2 * j);
+                            float4 v = add ? *p : make_float4(0.f, 0.f, 0.f, 0.f);
+                            v.x = fmaf(o[k][n][e], wt, v.x);
+                            v.y = fmaf(o[k][n][2 + e], wt, v.y);
+                            v.z = fmaf(o[k][n + 1][e], wt, v.z);
+                            v.w = fmaf(o[k][n + 1][2 + e], wt, v.w);
+                            *p = v;
+                        }
+                } else {
+#pragma unroll
+                    for (int n = 0; n < C::HD / 16; ++n) {
+                        float *p = row + 16 * n + g;
+                        p[0] = fmaf(o[k][n][e], wt, add ? p[0] : 0.f);
+                        p[8] = fmaf(o[k][n][2 + e], wt, add ? p[8] : 0.f);
+                    }
+                }
+            }
     }
 };
 
-// Q of the block's slots as MMA A fragments in shared memory: hi = T(q sc), lo = T(q sc - hi) with a
-// power of two sc per slot (exact). Slots past the last are zero.
+// Q of the block's slots as MMA A fragments in shared memory: NP parts, each the rounding of what the
+// ones before leave of q sc, with a power of two sc per slot (exact). Slots past the last are zero.
 template <class C>
-__device__ __forceinline__ void paged_prepare_q(uint8_t *smem, const PagedArgs &a, int s, int hk, int qg, int tid)
+__device__ __forceinline__ void paged_prepare_q(uint8_t *smem, const PagedArgs &a, const SlotRows &sr, int s, int hk, int qg,
+                                                int tid)
 {
     using MT = typename C::MT;
     const int warp = tid >> 5, lane = tid & 31;
     constexpr int NW = C::NWC;                                   // the compute warps
     constexpr int V4 = C::HD <= 128 ? 1 : 2;                     // float4 of a row a lane owns
-    constexpr int ITER = C::SLOTS / NW;
+    constexpr int ITER = (C::SLOTS + NW - 1) / NW;
     const bool active = lane * 4 < C::HD;
     float4 x[ITER][V4];
 #pragma unroll
     for (int it = 0; it < ITER; ++it) {
         const int i = warp + it * NW, qh = qg * C::SLOTS + i;
-        const bool have = qh < a.n_q * a.group;
-        const int t = have ? qh / a.group : 0, g = have ? qh - t * a.group : 0;
+        const bool have = i < C::SLOTS && qh < a.n_q * a.group;
+        const int t = have ? div(a.by_group, qh) : 0, g = have ? qh - t * a.group : 0;
         const float *row = a.q + (((size_t)s * a.n_q + t) * a.n_head + (size_t)hk * a.group + g) * C::HD;
 #pragma unroll
         for (int v = 0; v < V4; ++v) {
@@ -545,6 +618,7 @@ __device__ __forceinline__ void paged_prepare_q(uint8_t *smem, const PagedArgs &
 #pragma unroll
     for (int it = 0; it < ITER; ++it) {
         const int i = warp + it * NW;
+        if (i >= C::SLOTS) break;
         float amax = 0.f;
 #pragma unroll
         for (int v = 0; v < V4; ++v) {
@@ -559,292 +633,466 @@ __device__ __forceinline__ void paged_prepare_q(uint8_t *smem, const PagedArgs &
             const int qh = qg * C::SLOTS + i;
             SlotInfo si;
             si.inv = inv;
-            si.t = qh < a.n_q * a.group ? qh / a.group : -1;
-            si.slope = a.slopes && si.t >= 0 ? ld_dep(a.slopes + hk * a.group + qh % a.group) * kLog2e : 0.f;
-            si.pad = 0;
+            const bool have = qh < a.n_q * a.group;
+            const int t = div(a.by_group, qh);
+            si.last = have ? sr.last(t) : -1;
+            si.low = have ? sr.low(t) : 0;
+            si.slope = a.slopes && have ? ld_dep(a.slopes + hk * a.group + qh - t * a.group) * kLog2e : 0.f;
             reinterpret_cast<SlotInfo *>(smem + C::OFF_SLOT)[i] = si;
         }
         if (!active) continue;
 #pragma unroll
         for (int v = 0; v < V4; ++v) {
             const int d = v * 128 + lane * 4;
-            const float f[4] = {x[it][v].x * sc, x[it][v].y * sc, x[it][v].z * sc, x[it][v].w * sc};
-            uint32_t hw[2], lw[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                hw[j] = float2_to_kv2<MT>(f[2 * j], f[2 * j + 1]);
-                const float2 b = kv2_to_float2<MT>(hw[j]);
-                lw[j] = float2_to_kv2<MT>(f[2 * j] - b.x, f[2 * j + 1] - b.y);
-            }
+            float f[4] = {x[it][v].x * sc, x[it][v].y * sc, x[it][v].z * sc, x[it][v].w * sc};
             // dimension d is element 0 of a lane's four in k-step kk (the K loads' order)
             const int c = d / C::CW, in = d % C::CW, u = in / (C::CW / 4), w = in % (C::CW / 4) / 4;
             const int kk = c * C::KPC + w, fl = (i & 7) * 4 + u;
-            uint32_t *hi, *lo;
-            if constexpr (C::SLOTS == 8) {
-                uint32_t *p = reinterpret_cast<uint32_t *>(smem + C::OFF_Q) + (kk * 32 + fl) * 4;
-                hi = p;
-                lo = p + 1;
-            } else {
-                hi = reinterpret_cast<uint32_t *>(smem + C::OFF_Q) + (kk * 32 + fl) * 4 + (i >> 3);
-                lo = hi + C::KSTEPS * 128;
+            uint32_t *q0 = reinterpret_cast<uint32_t *>(smem + C::OFF_Q);
+#pragma unroll
+            for (int part = 0; part < C::NP; ++part) {
+                uint32_t *to;
+                int next = 2;                                    // words to the pair's second half
+                if (C::SLOTS == 16) {
+                    to = q0 + ((part * C::KSTEPS + kk) * 32 + fl) * 4 + (i >> 3);
+                } else if (part < 2) {
+                    to = q0 + (kk * 32 + fl) * 4 + part;
+                } else {
+                    to = q0 + C::KSTEPS * 128 + (kk * 32 + fl) * 2;
+                    next = 1;
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t b = float2_to_kv2<MT>(f[2 * j], f[2 * j + 1]);
+                    to[next * j] = b;
+                    const float2 r = kv2_to_float2<MT>(b);
+                    f[2 * j] -= r.x;
+                    f[2 * j + 1] -= r.y;
+                }
             }
-            hi[0] = hw[0]; hi[2] = hw[1];
-            lo[0] = lw[0]; lo[2] = lw[1];
         }
     }
 }
 
+// The tiles of all sequences, laid end to end, over the ranks: rank r takes [r share, (r + 1) share), with the
+// share that lets all ranks but the last few have the same. No rank below the last one with tiles has none,
+// so every rank between a sequence's first and last has some of it.
+__device__ __forceinline__ int rank_share(int total, int ranks)
+{
+    return max((int)(((unsigned)total + (unsigned)ranks - 1u) / (unsigned)ranks), 1);
+}
+
+__device__ __forceinline__ int rank_tile(int r, int total, int share)
+{
+    return (int)min((int64_t)r * share, (int64_t)total);
+}
+
+__device__ __forceinline__ SlotRows seq_rows(const PagedArgs &a, int nkv, int start)
+{
+    return SlotRows{nkv, nkv - a.n_q, start, a.window};
+}
+
+// The sequence that tile t belongs to: the first one whose end lies past it.
+__device__ __forceinline__ int find_seq(const int *cs, int n, int t)
+{
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (cs[mid + 1] > t) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+
+// First row of the first tile of a sequence, and one past its last row
+template <int TILE>
+__device__ __forceinline__ int2 seq_extent(const PagedArgs &a, const SlotRows &sr)
+{
+    const int R = max(sr.last(a.n_q - 1) + 1, 0), L = min(sr.low(0), R);
+    return make_int2(L / TILE * TILE, R);
+}
+
 template <class C, bool RULES>
 __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
-attn_paged_partial(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                   const PagedArgs a)
+attn_paged_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                  const PagedArgs a)
 {
-    constexpr int NWC = C::NWC, S = C::S, TILE = C::TILE, WR = C::WR, NSL = C::NSL;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    SliceInfo *info = reinterpret_cast<SliceInfo *>(smem + C::OFF_INFO);
+    constexpr int NWC = C::NWC, S = C::S, TILE = C::TILE, WR = C::WR, NSL = C::NSL, TPG = C::TPG;
+    extern __shared__ __align__(1024) uint8_t smem[];      // the swizzle needs the alignment (launch: no static shared memory)
+    SliceInfo *desc = reinterpret_cast<SliceInfo *>(smem + C::OFF_DESC);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *empty = full + S;
     volatile int *flags = reinterpret_cast<volatile int *>(empty + S);   // [0] abort, [1] tiles issued
+    int *cs = reinterpret_cast<int *>(smem + C::OFF_SEQ);    // tiles before each sequence
+    int *snkv = cs + kPagedSeqs + 1, *sstart = snkv + kPagedSeqs;
 
-    const int sp = blockIdx.y, s = blockIdx.z;
-    const int hk = blockIdx.x / a.qgroups, qg = blockIdx.x % a.qgroups;
+    const int hk = blockIdx.y, qg = blockIdx.x, unit = hk * a.qgroups + qg, rank = blockIdx.z;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int P = a.n_splits;
-    const size_t heads = (size_t)a.n_q * a.n_head;
-
-    if (tid == NWC * 32) {
-        for (int i = 0; i < S; ++i) {
-            mbar_init(full + i, 2);          // the copies' issue, and the slices' info
-            mbar_init(empty + i, NWC);
-        }
-        flags[0] = 0;
-        flags[1] = 0;
-        fence_barrier_init();
-        prefetch_tensormap(&kmap);
-        prefetch_tensormap(&vmap);
-    }
-    pdl_wait();
-    pdl_launch_dependents();
-
-    // The rows of this block's query rows [t0, t1], and its split of them
-    SlotRows sr;
-    {
-        const int64_t n = (int64_t)ld_dep(a.positions + s) + 1;
-        const bool ok = n >= 0 && n <= a.cap;
-        if (!ok && sp == 0 && blockIdx.x == 0 && tid == 0) atomicOr(a.err, kErrPositionClamped);
-        sr.nkv = ok ? (int)n : n < 0 ? 0 : a.cap;
-        sr.base = sr.nkv - a.n_q;
-        sr.start = a.starts ? ld_dep(a.starts + s) : 0;
-        sr.window = a.window;
-    }
-    const int x1 = min((qg + 1) * C::SLOTS, a.n_q * a.group) - 1;
-    const int t0 = qg * C::SLOTS / a.group, t1 = x1 / a.group;
-    const int R = max(sr.last(t1) + 1, 0), L = min(sr.low(t0), R);       // rows [L, R): seen by some slot
-    const int L0 = L / TILE * TILE;
-    int chunk = (R - L0 + P - 1) / P;
-    chunk = (chunk + TILE - 1) / TILE * TILE;
-    const int64_t lo64 = (int64_t)L0 + (int64_t)sp * chunk;
-    const int lo = lo64 < R ? (int)lo64 : R;
-    const int hi = chunk < R - lo ? lo + chunk : R;
-    if (lo >= hi || L >= R) {                                            // nothing in this split
-        for (int i = tid; i < C::SLOTS; i += C::THREADS) {
-            const int x = qg * C::SLOTS + i;
-            if (x >= a.n_q * a.group) break;
-            const int t = x / a.group;
-            const size_t row = (size_t)s * heads + (size_t)t * a.n_head + hk * a.group + (x - t * a.group);
-            if (P > 1) a.ws_ml[row * P + sp] = make_float2(-INFINITY, 0.f);
-            else
-                for (int d = 0; d < C::HD; d += 4)
-                    *reinterpret_cast<float4 *>(a.out + row * C::HD + d) = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        return;
-    }
-    const int ntiles = (hi - lo + TILE - 1) / TILE;
-
-    if (warp != NWC) paged_prepare_q<C>(smem, a, s, hk, qg, tid);
 
     if (warp == NWC) {
         // ---------------- producer warp ----------------
-        // Lane i keeps the page and the scales of slice i of a group of 8 tiles (32 slices); the next
-        // group's entries are loaded while this one's tiles go out.
-        const int32_t *table = a.table + (size_t)s * a.max_pages;
-        auto load_page = [&](int grp) {
-            const int64_t row = (int64_t)lo + ((int64_t)grp * 32 + lane) * WR;
-            int p = -1;
-            if (row < hi && row + WR > L) {
-                p = ld_dep(table + (int)row / a.page_size);
-                if (p < 0 || p >= a.n_pages) {
-                    atomicOr(a.err, kErrBadPage);
-                    p = -1;
-                }
+        if (lane == 0) {
+            for (int i = 0; i < S; ++i) {
+                mbar_init(full + i, 1);
+                mbar_init(empty + i, NSL);
             }
-            return p;
+            flags[0] = 0;
+            flags[1] = 0;
+            fence_barrier_init();
+            prefetch_tensormap(&kmap);
+            prefetch_tensormap(&vmap);
+        }
+        pdl_wait();
+        pdl_launch_dependents();
+        // rows and tiles of every sequence, and the tiles before it: lane i takes `per` of them
+        const int per = (a.n_seq + 31) / 32;
+        int sum = 0;
+        for (int i = 0; i < per; ++i) {
+            const int s = lane * per + i;
+            if (s >= a.n_seq) break;
+            const int64_t n = (int64_t)ld_dep(a.positions + s) + 1;
+            const bool ok = n >= 0 && n <= a.cap;
+            if (!ok && unit == 0 && rank == 0) atomicOr(a.err, kErrPositionClamped);
+            const int nkv = ok ? (int)n : n < 0 ? 0 : a.cap, start = a.starts ? ld_dep(a.starts + s) : 0;
+            snkv[s] = nkv;
+            sstart[s] = start;
+            const int2 x = seq_extent<TILE>(a, seq_rows(a, nkv, start));
+            cs[s] = sum;
+            sum += x.x < x.y && seq_rows(a, nkv, start).low(0) < x.y ? (x.y - x.x + TILE - 1) / TILE : 0;
+        }
+        int before = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, before, off);
+            if (lane >= off) before += y;
+        }
+        const int total = __shfl_sync(0xffffffffu, before, 31);
+        before -= sum;
+        for (int i = 0; i < per && lane * per + i < a.n_seq; ++i) cs[lane * per + i] += before;
+        if (lane == 0) cs[a.n_seq] = total;
+        __syncthreads();                                       // the compute warps go on to their first q
+        const int share = rank_share(total, a.ranks);
+        const int first = rank_tile(rank, total, share), end = rank_tile(rank + 1, total, share);
+        const int ntiles = end - first;
+
+        // Descriptors: lane i has slice i of a group of TPG tiles. A group's pages are loaded two groups
+        // ahead and its scales one ahead, so that nothing waits for them; its descriptors go to one of four
+        // buffers (a buffer's tiles are consumed before it comes round again).
+        int seq = find_seq(cs, a.n_seq, first + lane / NSL);   // the lane's sequence; it only moves on
+        int row = 0;
+        bool need = false;                                     // some row of the slice's box is attended
+        auto locate = [&](int grp) {
+            const int t = first + grp * TPG + lane / NSL;
+            need = t < end;
+            if (!need) return;
+            while (cs[seq + 1] <= t) ++seq;
+            const SlotRows sr = seq_rows(a, snkv[seq], sstart[seq]);
+            const int2 x = seq_extent<TILE>(a, sr);
+            row = x.x + (t - cs[seq]) * TILE + lane % NSL * WR;
+            const int box = row & -a.box_rows;
+            need = box < x.y && box + a.box_rows > sr.low(0);
+        };
+        auto load_page = [&](int &z) {                         // and the row in the page
+            const int pg = div(a.by_page, row);
+            z = row - pg * a.page_size;
+            return need ? ld_dep(a.table + (size_t)seq * a.max_pages + pg) : -1;
         };
         auto load_scales = [&](int p) {
             float2 f = make_float2(1.f, 1.f);
-            if constexpr (C::E8) {
-                if (p >= 0) {
-                    f.x = ld_dep(a.k_scale + (size_t)p * a.n_kv_head + hk);
-                    f.y = ld_dep(a.v_scale + (size_t)p * a.n_kv_head + hk);
-                }
+            if (C::E8 && (unsigned)p < (unsigned)a.n_pages) {
+                f.x = ld_dep(a.k_scale + (size_t)p * a.n_kv_head + hk);
+                f.y = ld_dep(a.v_scale + (size_t)p * a.n_kv_head + hk);
             }
             return f;
         };
+        auto write = [&](int grp, int p, int z, bool wanted, float2 f) {
+            const bool there = (unsigned)p < (unsigned)a.n_pages;
+            if (wanted && !there) atomicOr(a.err, kErrBadPage);
+            desc[(grp & 3) * 32 + lane] = SliceInfo{there ? p : -1, z, f.x, f.y};
+        };
         const int BR = a.box_rows, nbox = TILE / BR, bsl = BR / WR;
-        auto issue = [&](int t, int st, int page) {        // `page`: lane i's of the tile's group
-            const int row0 = lo + t * TILE;
-            unsigned bytes = 0;
-            for (int b = 0; b < nbox; ++b) {
-                const int first = row0 + b * BR;
-                // the box's page is that of any of its slices that holds a row in range
-                int p = -1;
-                for (int i = 0; i < bsl; ++i) p = max(p, __shfl_sync(0xffffffffu, page, (t & 7) * NSL + b * bsl + i));
-                if (p >= 0 && first < hi) bytes += 2u * (unsigned)BR * C::ROWB;
-            }
-            if (lane == 0) mbar_arrive_expect_tx(full + st, bytes);
-            __syncwarp();
-            uint8_t *kst = smem + st * C::STAGE_BYTES;
-            uint8_t *vst = kst + C::TILE_BYTES;
-            for (int b = 0; b < nbox; ++b) {
-                const int first = row0 + b * BR;
-                int p = -1;
-                for (int i = 0; i < bsl; ++i) p = max(p, __shfl_sync(0xffffffffu, page, (t & 7) * NSL + b * bsl + i));
-                if (p >= 0 && first < hi && lane == 0) {
-                    const int z = first % a.page_size;
-#pragma unroll
-                    for (int c = 0; c < C::NCH; ++c) {
-                        const uint32_t off = c * (C::TILE_BYTES / C::NCH) + b * BR * C::CHB;
-                        tma_load_4d(kst + off, &kmap, full + st, c * C::CW, hk, z, p);
-                        tma_load_4d(vst + off, &vmap, full + st, c * C::CW, hk, z, p);
-                    }
-                }
-            }
-            if (lane == 0) flags[1] = t + 1;
-        };
-        auto inform = [&](int t, int st, int page, float2 sc) {
-            const int i = lane - (t & 7) * NSL;
-            if (i >= 0 && i < NSL) {
-                SliceInfo f;
-                f.page = page;
-                f.ks = sc.x;
-                f.vs = sc.y;
-                f.pad = 0;
-                info[st * NSL + i] = f;
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(full + st);
-        };
-        int page = load_page(0), next = -1;
-        const int early = min(min(S, 8), ntiles);
-        for (int t = 0; t < early; ++t) issue(t, t, page);
-        float2 sc = load_scales(page), nsc = make_float2(1.f, 1.f);
-        for (int t = 0; t < early; ++t) inform(t, t, page, sc);
-        next = load_page(1);
-        nsc = load_scales(next);
-        __syncthreads();
-        for (int t = early; t < ntiles; ++t) {
+        auto issue = [&](int t) {                              // by lane 0
             const int st = t % S;
-            int ok = 1;
-            if (lane == 0) {
-                if (t >= S && !mbar_wait_bounded(empty + st, ((t / S) - 1) & 1)) {
-                    flags[0] = 1;
-                    atomicOr(a.err, kErrPipelineTimeout);
+            const SliceInfo *d = desc + (t / TPG & 3) * 32 + t % TPG * NSL;
+            unsigned bytes = 0;
+            for (int b = 0; b < nbox; ++b) bytes += d[b * bsl].page >= 0 ? 2u * (unsigned)BR * C::ROWB : 0u;
+            mbar_arrive_expect_tx(full + st, bytes);
+            uint8_t *kst = smem + st * C::STAGE_BYTES;
+            for (int b = 0; b < nbox; ++b) {
+                const SliceInfo x = d[b * bsl];
+                if (x.page < 0) continue;
+#pragma unroll
+                for (int c = 0; c < C::NCH; ++c) {
+                    uint8_t *to = kst + c * (C::TILE_BYTES / C::NCH) + b * BR * C::CHB;
+                    tma_load_4d(to, &kmap, full + st, c * C::CW, hk, x.z, x.page);
+                    tma_load_4d(to + C::TILE_BYTES, &vmap, full + st, c * C::CW, hk, x.z, x.page);
                 }
-                ok = !flags[0];
             }
-            if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-            if ((t & 7) == 0) {
-                page = next;
-                sc = nsc;
+            flags[1] = t + 1;
+        };
+        // the first copies go out before the scales are there
+        locate(0);
+        int z0, z1;
+        const int p0 = load_page(z0);
+        const bool n0 = need;
+        desc[lane] = SliceInfo{(unsigned)p0 < (unsigned)a.n_pages ? p0 : -1, z0, 1.f, 1.f};
+        const float2 f0 = load_scales(p0);
+        __syncwarp();
+        const int early = min(S, ntiles);
+        if (lane == 0)
+            for (int t = 0; t < early; ++t) issue(t);
+        locate(1);
+        int p1 = load_page(z1);
+        bool n1 = need;
+        __syncwarp();
+        write(0, p0, z0, n0, f0);
+        // group 0's descriptors are complete (without tiles nobody waits)
+        if (ntiles > 0) asm volatile("bar.arrive 2, %0;" :: "r"(C::THREADS) : "memory");
+        float2 f1 = load_scales(p1);
+        bool dead = false;
+        for (int grp = 0; grp * TPG < ntiles; ++grp) {
+            locate(grp + 2);
+            int z2;
+            const int p2 = load_page(z2);
+            const bool n2 = need;
+            if (lane == 0) {
+                const int stop = min((grp + 1) * TPG, ntiles);
+                for (int t = grp ? grp * TPG : early; t < stop; ++t) {
+                    if (t >= S && !mbar_wait_bounded(empty + t % S, ((t / S) - 1) & 1)) {
+                        flags[0] = 1;
+                        atomicOr(a.err, kErrPipelineTimeout);
+                        dead = true;
+                        break;
+                    }
+                    issue(t);
+                }
             }
-            issue(t, st, page);
-            inform(t, st, page, sc);
-            if ((t & 7) == 1) next = load_page((t >> 3) + 1);
-            if ((t & 7) == 5) nsc = load_scales(next);
+            __syncwarp();
+            if (__shfl_sync(0xffffffffu, (int)dead, 0)) break;
+            write(grp + 1, p1, z1, n1, f1);
+            p1 = p2;
+            z1 = z2;
+            n1 = n2;
+            f1 = load_scales(p1);
+            __syncwarp();
         }
     } else {
         // ---------------- compute warps ----------------
+        pdl_wait();
+        pdl_launch_dependents();
         __syncthreads();
-        PagedWarp<C, RULES> w;
-        const uint32_t smem_u = smem_u32(smem);
-        w.init(smem_u, lane);
-        const int seen_lo = sr.low(t1), seen_hi = sr.last(t0);           // rows every slot sees
-#pragma unroll 1
-        for (int t = 0; t < ntiles; ++t) {
-            const int st = t % S;
-            const bool landed = mbar_wait_bounded(full + st, (t / S) & 1);
-            if (!__all_sync(0xffffffffu, landed)) {
-                if (lane == 0) { flags[0] = 1; atomicOr(a.err, kErrPipelineTimeout); }
-                break;
+        // Values that only the ends of a sequence need are read again from shared memory there, so that the tile
+        // loop's registers hold the accumulators.
+        volatile SegInfo *seg = reinterpret_cast<volatile SegInfo *>(smem + C::OFF_SEG);
+        const size_t heads = (size_t)a.n_q * a.n_head;
+        auto nslots = [&] { return min(C::SLOTS, a.n_q * a.group - qg * C::SLOTS); };
+        auto head_row = [&](int s, int i) {                    // of slot i of the block
+            const int x = qg * C::SLOTS + i, t = div(a.by_group, x);
+            return (size_t)s * heads + (size_t)t * a.n_head + hk * a.group + (x - t * a.group);
+        };
+        // sequences that start here: which ranks have their rows; no rows at all: 0
+        const int total = cs[a.n_seq], share = rank_share(total, a.ranks);
+        const int first = rank_tile(rank, total, share), end = rank_tile(rank + 1, total, share);
+        {
+            for (int s = tid; s < a.n_seq; s += NWC * 32) {
+                const int c = cs[s], n = cs[s + 1] - c;
+                if (!((c >= first && c < end) || (c == total && rank == 0))) continue;
+                if (a.ranks > 1 && unit == 0)
+                    a.ws_span[s] = make_int2(rank, n > 0 ? (c + n - 1) / share : rank);
+                if (n == 0)
+                    for (int i = 0; i < nslots(); ++i)
+                        for (int d = 0; d < C::HD; d += 4)
+                            *reinterpret_cast<float4 *>(a.out + head_row(s, i) * C::HD + d) = make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            if (__shfl_sync(0xffffffffu, flags[0], 0)) break;
-            const int row0 = lo + t * TILE + warp * WR;
-            const SliceInfo f = info[st * NSL + warp];
-            if (f.page >= 0 && row0 < hi) {
-                const uint32_t kst = smem_u + st * C::STAGE_BYTES;
-                const bool edge = row0 < seen_lo || row0 + WR - 1 > seen_hi;
-                w.process(smem_u, kst, kst + C::TILE_BYTES, warp * WR, row0, f, edge, sr, t0, t1, a, lane);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(empty + st);
         }
-        // the merge area lies over the ring: every compute warp is done with it first
-        asm volatile("bar.sync 1, %0;" :: "r"(NWC * 32) : "memory");
-        if (!__shfl_sync(0xffffffffu, flags[0], 0))
-            w.publish(reinterpret_cast<float2 *>(smem) + warp * C::SLOTS,
-                      reinterpret_cast<float *>(smem) + C::OFF_MO + warp * C::SLOTS * C::MS, lane);
+        const uint32_t smem_u = smem_u32(smem);
+        float2 *mm = reinterpret_cast<float2 *>(smem + C::OFF_Q);
+        float *mo = reinterpret_cast<float *>(smem + C::OFF_Q) + C::OFF_MO;
+        bool begun = false;
+        for (int at = first; at < end;) {
+            {
+                const int s = find_seq(cs, a.n_seq, at);
+                const SlotRows sr = seq_rows(a, snkv[s], sstart[s]);
+                const int t0 = div(a.by_group, qg * C::SLOTS), t1 = div(a.by_group, qg * C::SLOTS + nslots() - 1);
+                paged_prepare_q<C>(smem, a, sr, s, hk, qg, tid);
+                if (tid == 0) {
+                    seg->seen_lo = sr.low(t1);
+                    seg->seen_hi = sr.last(t0);
+                    seg->any_lo = sr.low(t0);
+                    seg->any_hi = sr.last(t1);
+                    seg->row0 = seq_extent<TILE>(a, sr).x + (first - cs[s]) * TILE;
+                    seg->seq = s;
+                    seg->from = at - first;
+                    seg->to = min(end, cs[s + 1]) - first;
+                }
+            }
+            if (!begun) asm volatile("bar.sync 2, %0;" :: "r"(C::THREADS) : "memory");
+            else asm volatile("bar.sync 1, %0;" :: "r"(NWC * 32) : "memory");
+            begun = true;
+            PagedWarp<C, RULES> w;
+            w.init(smem_u, lane);
+            // warp w has slice w % NSL of every WPT-th stage
+            int t = seg->from;
+            t += (warp / NSL + C::WPT - t % C::WPT) % C::WPT;
+            const int to = flags[0] ? 0 : seg->to;       // after a timeout nothing is waited for any more
+#pragma unroll 1
+            for (; t < to; t += C::WPT) {
+                const int st = t % S;
+                const bool landed = mbar_wait_bounded(full + st, (t / S) & 1);
+                if (!__all_sync(0xffffffffu, landed)) {
+                    if (lane == 0) { flags[0] = 1; atomicOr(a.err, kErrPipelineTimeout); }
+                    break;
+                }
+                const int row0 = seg->row0 + t * TILE + warp % NSL * WR;
+                const int4 sg = PagedWarp<C, RULES>::seg_rows(smem_u);
+                const uint4 f = lds128(smem_u + C::OFF_DESC + ((t / TPG & 3) * 32 + t % TPG * NSL + warp % NSL) * 16);
+                if ((int)f.x >= 0 && row0 <= sg.w && row0 + WR > sg.z)
+                    w.process(smem_u, smem_u + st * C::STAGE_BYTES, warp % NSL * WR, row0, __uint_as_float(f.z),
+                              __uint_as_float(f.w), row0 < sg.x || row0 + WR - 1 > sg.y, a.cap_log2, lane);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty + st);
+            }
+            // merge the warps' states: over the Q fragments, which are no longer read
+            asm volatile("bar.sync 1, %0;" :: "r"(NWC * 32) : "memory");
+            w.publish(mm + warp * C::SLOTS, lane);
+            asm volatile("bar.sync 1, %0;" :: "r"(NWC * 32) : "memory");
+            // the block's last sequence: every tile has been consumed and none is on its way, so that each warp
+            // has a part of the ring to itself; before that, one after the other onto one area
+            const bool over = seg->to == end - first;
+            float *area = over ? reinterpret_cast<float *>(smem) : mo;
+#pragma unroll 1
+            for (int i = 0; i < NWC; ++i) {
+                if (warp == i) w.deposit(mm, area + (over ? i * C::SLOTS * C::MS : 0), warp, !over && i > 0, lane);
+                if (!over) asm volatile("bar.sync 1, %0;" :: "r"(NWC * 32) : "memory");
+            }
+            if (over) asm volatile("bar.sync 1, %0;" :: "r"(NWC * 32) : "memory");
+            const int q = seg->seq, from = seg->from + first, stop = seg->to + first;
+            const bool begins = from == cs[q], whole = begins && stop == cs[q + 1];
+            const size_t part = ((size_t)(rank * 2 + (begins ? 1 : 0)) * a.units + unit) * C::SLOTS;
+            const bool bad = flags[0] != 0;              // left unwritten; the error word says why
+            constexpr int D4 = C::HD / 4;
+            for (int i = tid; i < nslots() * D4 && !bad; i += NWC * 32) {
+                const int g = i / D4, d = (i % D4) * 4;
+                float M = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int x = 0; x < NWC; ++x) M = fmaxf(M, mm[x * C::SLOTS + g].x);
+#pragma unroll
+                for (int x = 0; x < NWC; ++x) {
+                    const float2 ml = mm[x * C::SLOTS + g];
+                    if (ml.x != -INFINITY) sum = fmaf(ex2(ml.x - M), ml.y, sum);
+                }
+                float4 O = *reinterpret_cast<const float4 *>(area + g * C::MS + d);
+                if (over) {
+#pragma unroll
+                    for (int x = 1; x < NWC; ++x) {
+                        const float4 v = *reinterpret_cast<const float4 *>(area + (x * C::SLOTS + g) * C::MS + d);
+                        O.x += v.x; O.y += v.y; O.z += v.z; O.w += v.w;
+                    }
+                }
+                if (whole) {
+                    if (sum == 0.f) O = make_float4(0.f, 0.f, 0.f, 0.f);
+                    else { O.x /= sum; O.y /= sum; O.z /= sum; O.w /= sum; }
+                    *reinterpret_cast<float4 *>(a.out + head_row(q, g) * C::HD + d) = O;
+                } else {
+                    *reinterpret_cast<float4 *>(a.ws_o + (part + g) * C::HD + d) = O;
+                    if (d == 0) a.ws_ml[part + g] = make_float2(M, sum);
+                }
+            }
+            at = stop;
+            asm volatile("bar.sync 1, %0;" :: "r"(NWC * 32) : "memory");
+        }
     }
     __syncthreads();
 
-    // No copy may still be writing shared memory when the block exits; without an
-    // abort every issued tile has been waited for.
-    if (flags[0]) {
-        if (tid == NWC * 32) {
-            const int issued = flags[1];
-            for (int t = issued - S > 0 ? issued - S : 0; t < issued; ++t)
-                (void)mbar_wait_bounded(full + (t % S), (t / S) & 1);
-        }
-        return;
+    // No copy may still be writing shared memory when the block exits; without an abort every issued
+    // tile has been waited for.
+    if (flags[0] && tid == NWC * 32) {
+        const int issued = flags[1];
+        for (int t = issued - S > 0 ? issued - S : 0; t < issued; ++t)
+            (void)mbar_wait_bounded(full + (t % S), (t / S) & 1);
     }
+}
 
-    // Merge the warps' states; one split: the result itself
-    const float2 *mm = reinterpret_cast<const float2 *>(smem);
-    const float *mo = reinterpret_cast<const float *>(smem) + C::OFF_MO;
-    constexpr int D4 = C::HD / 4;
-    for (int i = tid; i < C::SLOTS * D4; i += C::THREADS) {
-        const int g = i / D4, d = (i % D4) * 4;
-        const int x = qg * C::SLOTS + g;
-        if (x >= a.n_q * a.group) break;
-        float2 ml[NWC];
+// The sequences whose rows several ranks share: o = sum w oc / sum w S over their parts, w = 2^(mx - max mx).
+// One block per (row, sequence, chunk of DC dimensions); a group of DC / 4 lanes folds every NG-th part,
+// BATCH of them in flight, and the groups are folded through shared memory.
+template <int HD, int DC>
+__global__ void __launch_bounds__(128) attn_paged_combine(const PagedArgs a, int slots)
+{
+    constexpr int LPS = DC / 4, NG = 128 / LPS, BATCH = 8;
+    __shared__ float2 sm_ml[NG];
+    __shared__ float sm_acc[NG][DC];
+    // no early start for the kernel after this one: a streaming block that becomes resident beside these finds
+    // the SM's shared memory and registers in pieces, and one of the blocks that should be there then waits
+    // for a whole block's time (131072 rows: 54 us with one block fewer than fit, 73 with all)
+    pdl_wait();
+    const int s = blockIdx.y, r = blockIdx.x;
+    const uint2 sp = [&] {
+        uint2 v;
+        asm volatile("ld.global.cg.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(a.ws_span + s) : "memory");
+        return v;
+    }();
+    if (sp.x == sp.y) return;
+    const int t = r / a.n_head, h = r - t * a.n_head, hk = h / a.group;
+    const int x = t * a.group + (h - hk * a.group);
+    const size_t in_rank = (size_t)(hk * a.qgroups + x / slots) * slots + x % slots;
+    const size_t rank_rows = (size_t)a.units * slots;
+    const int P = (int)(sp.y - sp.x) + 1;
+    const int group = threadIdx.x / LPS, dl = threadIdx.x % LPS;
+    auto at = [&](int j) { return ((size_t)(sp.x + j) * 2 + (j == 0 ? 1 : 0)) * rank_rows + in_rank; };
+
+    float m = -INFINITY, S = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int base = group; base < P; base += NG * BATCH) {
+        float2 ml[BATCH];
+        float4 v[BATCH];
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            const int j = base + b * NG;
+            ml[b] = make_float2(-INFINITY, 0.f);
+            v[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (j < P) {
+                const size_t row = at(j);
+                ml[b] = ld_dep(a.ws_ml + row);
+                v[b] = ld_dep(reinterpret_cast<const float4 *>(a.ws_o + row * HD + blockIdx.z * DC) + dl);
+            }
+        }
+        float mb = m;
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) mb = fmaxf(mb, ml[b].x);
+        if (mb == -INFINITY) continue;
+        const float c = m == -INFINITY ? 0.f : ex2(m - mb);
+        S *= c;
+        acc.x *= c; acc.y *= c; acc.z *= c; acc.w *= c;
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            if (ml[b].x == -INFINITY) continue;
+            const float w = ex2(ml[b].x - mb);
+            S = fmaf(w, ml[b].y, S);
+            acc.x = fmaf(w, v[b].x, acc.x);
+            acc.y = fmaf(w, v[b].y, acc.y);
+            acc.z = fmaf(w, v[b].z, acc.z);
+            acc.w = fmaf(w, v[b].w, acc.w);
+        }
+        m = mb;
+    }
+    if (dl == 0) sm_ml[group] = make_float2(m, S);
+    *reinterpret_cast<float4 *>(&sm_acc[group][dl * 4]) = acc;
+    __syncthreads();
+    for (int d = threadIdx.x; d < DC; d += 128) {
         float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < NWC; ++w) {
-            ml[w] = mm[w * C::SLOTS + g];
-            M = fmaxf(M, ml[w].x);
-        }
-        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
+        for (int g = 0; g < NG; ++g) M = fmaxf(M, sm_ml[g].x);
+        float sum = 0.f, o = 0.f;
 #pragma unroll
-        for (int w = 0; w < NWC; ++w) {
-            const float wt = ml[w].x == -INFINITY ? 0.f : ex2(ml[w].x - M);
-            const float4 v = *reinterpret_cast<const float4 *>(mo + (w * C::SLOTS + g) * C::MS + d);
-            O.x = fmaf(wt, v.x, O.x);
-            O.y = fmaf(wt, v.y, O.y);
-            O.z = fmaf(wt, v.z, O.z);
-            O.w = fmaf(wt, v.w, O.w);
-            sum = fmaf(wt, ml[w].y, sum);
+        for (int g = 0; g < NG; ++g) {
+            const float2 y = sm_ml[g];
+            const float w = y.x == -INFINITY ? 0.f : ex2(y.x - M);
+            sum = fmaf(w, y.y, sum);
+            o = fmaf(w, sm_acc[g][d], o);
         }
-        const int t = x / a.group;
-        const size_t row = (size_t)s * heads + (size_t)t * a.n_head + hk * a.group + (x - t * a.group);
-        if (P > 1) {
-            *reinterpret_cast<float4 *>(a.ws_o + (row * P + sp) * C::HD + d) = O;
-            if (d == 0) a.ws_ml[row * P + sp] = make_float2(M, sum);
-        } else {
-            if (sum == 0.f) O = make_float4(0.f, 0.f, 0.f, 0.f);
-            else { O.x /= sum; O.y /= sum; O.z /= sum; O.w /= sum; }
-            *reinterpret_cast<float4 *>(a.out + row * C::HD + d) = O;
-        }
+        const size_t row = (size_t)s * a.n_q * a.n_head + r;
+        a.out[row * HD + blockIdx.z * DC + d] = sum == 0.f ? 0.f : o / sum;
     }
 }
 

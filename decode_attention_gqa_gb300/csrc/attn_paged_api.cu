@@ -10,20 +10,9 @@
 #include "attn_paged.h"
 #include "attn_paged_launch.h"
 
-namespace attn {
-
-PagedInfo paged_info(int head_dim, int kv_type, int)
-{
-    // the resident blocks of PagedShape (attn_paged_impl.cuh)
-    (void)kv_type;
-    return PagedInfo{64, head_dim == 256 ? 1 : 2};
-}
-
-} // namespace attn
-
 namespace {
 
-constexpr int kMaxPagedSplits = 4096;              // the combine's limit
+constexpr int kMaxPagedSplits = 4096;
 constexpr int64_t kMaxRows = (int64_t)0x7fffffff - 16384;
 constexpr int64_t kMaxStrideBytes = (int64_t)1 << 40;
 
@@ -73,8 +62,9 @@ attn_status check_cache_pointers(const attn_paged_cache *c)
 }
 
 struct PagedPlan {
+    attn::PagedShape shape{};
     int slots = 8, qgroups = 1, n_splits = 1;
-    size_t workspace = 0;
+    size_t o_bytes = 0, ml_bytes = 0, workspace = 0;
 };
 
 attn_status check_heads(const attn_paged_cache *c, int n_seq, int n_q, int n_head, int window, int n_splits)
@@ -86,29 +76,41 @@ attn_status check_heads(const attn_paged_cache *c, int n_seq, int n_q, int n_hea
     return ATTN_OK;
 }
 
-// Split count from the shape and the capacity (the host never sees the lengths): the chunk that
-// fills one wave of resident blocks at full capacity for a single sequence, eight waves for a batch whose
-// ragged lengths then balance, in whole 64-row tiles; the device divides the rows that are there.
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// How many blocks share the call's rows, per KV head and group of slots: as many as fill the SMs with
+// resident blocks once, since each takes an equal part of the rows that are there (the device divides them,
+// across sequences). Where that leaves much of the GPU without a block (units just over half of its
+// slots), enough for four rounds of blocks, whose last is nearly full; no more than there are tiles of rows at
+// full capacity.
 void make_plan(const attn_paged_cache *c, int max_pages, int n_seq, int n_q, int n_head, int window, int n_splits,
                int sm_count, PagedPlan &pl)
 {
     const int group = n_head / c->n_kv_head;
     pl.slots = attn::paged_slots(n_q, group);
     pl.qgroups = (n_q * group + pl.slots - 1) / pl.slots;
+    pl.shape = attn::paged_shape(c->head_dim, type_bytes(c->kv_type), pl.slots);
+    const int64_t units = (int64_t)c->n_kv_head * pl.qgroups;
     if (n_splits > 0) {
         pl.n_splits = n_splits;
     } else {
-        const attn::PagedInfo ki = attn::paged_info(c->head_dim, c->kv_type, pl.slots);
+        const int64_t tile = pl.shape.nsl * 16;
         int64_t rows = (int64_t)max_pages * c->page_size;
-        if (window > 0 && (int64_t)window + n_q + ki.tile_rows < rows) rows = (int64_t)window + n_q + ki.tile_rows;
-        const int64_t units = (int64_t)n_seq * c->n_kv_head * pl.qgroups;
-        const int64_t slots = (int64_t)sm_count * ki.blocks_per_sm * (n_seq > 1 ? 8 : 1);
-        int64_t chunk = units > slots ? rows : (rows * units + slots - 1) / slots;
-        chunk = (chunk + ki.tile_rows - 1) / ki.tile_rows * ki.tile_rows;
-        const int64_t P = (rows + chunk - 1) / chunk;
+        if (window > 0 && (int64_t)window + n_q + tile < rows) rows = (int64_t)window + n_q + tile;
+        const int64_t tiles = (rows + tile - 1) / tile * (n_seq < attn::kPagedSeqs ? n_seq : attn::kPagedSeqs);
+        const int64_t slots = (int64_t)sm_count * pl.shape.blocks;
+        int64_t P = slots / units;
+        if (P * units * 20 < slots * 17) P = 4 * slots / units;
+        if (P > tiles) P = tiles;
         pl.n_splits = (int)(P < 1 ? 1 : P > kMaxPagedSplits ? kMaxPagedSplits : P);
     }
-    pl.workspace = pl.n_splits > 1 ? attn_workspace_size(n_seq, n_q * n_head, c->head_dim, pl.n_splits) : 0;
+    if (pl.n_splits > 1) {
+        const size_t parts = (size_t)pl.n_splits * 2 * units * pl.slots;
+        const size_t seqs = n_seq < attn::kPagedSeqs ? n_seq : attn::kPagedSeqs;
+        pl.o_bytes = align256(parts * c->head_dim * sizeof(float));
+        pl.ml_bytes = align256(parts * 2 * sizeof(float));
+        pl.workspace = pl.o_bytes + pl.ml_bytes + align256(seqs * 8);
+    }
 }
 
 } // namespace
@@ -290,34 +292,35 @@ attn_status attn_decode_paged(const attn_paged_cache *cache, const int32_t *bloc
         }
     }
 
+    const int64_t units = (int64_t)cache->n_kv_head * pl.qgroups;
     attn::PagedRequest r{};
     attn::PagedArgs &a = r.pa;
-    const int P = pl.n_splits;
-    a.q = q;
-    a.out = out;
-    a.positions = positions;
-    a.table = block_table;
     a.k_scale = cache->k_scale;
     a.v_scale = cache->v_scale;
     a.slopes = rules ? rules->slopes : nullptr;
-    a.starts = rules ? rules->starts : nullptr;
-    const size_t slots = (size_t)n_seq * n_q * n_head * P;
-    a.ws_o = static_cast<float *>(workspace);
-    a.ws_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) +
-                                         ((slots * cache->head_dim * sizeof(float) + 255) & ~size_t(255)));
+    if (pl.workspace > 0) {
+        uint8_t *ws = static_cast<uint8_t *>(workspace);
+        a.ws_o = reinterpret_cast<float *>(ws);
+        a.ws_ml = reinterpret_cast<float2 *>(ws + pl.o_bytes);
+        a.ws_span = reinterpret_cast<int2 *>(ws + pl.o_bytes + pl.ml_bytes);
+    }
     a.err = err;
     a.n_head = n_head;
     a.n_kv_head = cache->n_kv_head;
     a.group = n_head / cache->n_kv_head;
     a.n_q = n_q;
     a.qgroups = pl.qgroups;
-    a.n_splits = P;
+    a.units = (int)units;
+    a.ranks = pl.n_splits;
     a.max_pages = max_pages;
     a.n_pages = cache->n_pages;
     a.page_size = cache->page_size;
     a.cap = max_pages * cache->page_size;
     a.window = window > a.cap ? 0 : window;        // past the capacity it masks nothing
-    a.box_rows = cache->page_size % 64 == 0 ? 64 : cache->page_size % 32 == 0 ? 32 : 16;
+    const int tile = pl.shape.nsl * 16;
+    a.box_rows = cache->page_size % 64 == 0 && tile >= 64 ? 64 : cache->page_size % 32 == 0 && tile >= 32 ? 32 : 16;
+    a.by_page = attn::fast_div((unsigned)cache->page_size);
+    a.by_group = attn::fast_div((unsigned)a.group);
     a.qscale = softcap > 0.f ? (float)((double)scale / softcap) : (float)((double)scale * 1.4426950408889634);
     a.cap_log2 = (float)((double)softcap * 1.4426950408889634);
     r.k = cache->k;
@@ -325,7 +328,6 @@ attn_status attn_decode_paged(const attn_paged_cache *cache, const int32_t *bloc
     r.page_stride = cs.page;
     r.row_stride = cs.row;
     r.head_stride = cs.head;
-    r.n_seq = n_seq;
     r.head_dim = cache->head_dim;
     r.kv_type = cache->kv_type;
     r.rules = softcap > 0.f || a.slopes;
@@ -337,24 +339,18 @@ attn_status attn_decode_paged(const attn_paged_cache *cache, const int32_t *bloc
         {attn::launch_paged_hd128_f16, attn::launch_paged_hd128_bf16, attn::launch_paged_hd128_e4m3},
         {attn::launch_paged_hd256_f16, attn::launch_paged_hd256_bf16, attn::launch_paged_hd256_e4m3}};
     const int hi = cache->head_dim == 64 ? 0 : cache->head_dim == 128 ? 1 : 2;
-    e = table[hi][ti](r);
-    if (e != cudaSuccess) return fail(e);
-    if (P > 1) {
-        attn::LaunchRequest c{};
-        c.pa.ws_o = a.ws_o;
-        c.pa.ws_ml = a.ws_ml;
-        c.pa.n_head = n_head;
-        c.pa.n_q = 1;
-        c.pa.n_splits = P;
-        c.out = out;
-        c.n_seq = n_seq;
-        c.head_dim = cache->head_dim;
-        c.group = 1;
-        c.variant = attn::kVariantSimt;
-        c.stages = attn::kStageCombine;
-        c.stream = r.stream;
-        c.pa.n_head = n_head * n_q;                // partial heads per sequence
-        e = attn::launch_any(c);
+    // tiles are counted in 32 bits: fewer sequences a launch where the capacity is huge
+    const int64_t per_seq = (a.cap + (int64_t)tile - 1) / tile + 1;
+    const int batch = (int)(0x7fffffff / per_seq < attn::kPagedSeqs ? 0x7fffffff / per_seq : attn::kPagedSeqs);
+    for (int s0 = 0; s0 < n_seq; s0 += batch) {
+        const size_t rows = (size_t)s0 * n_q * n_head * cache->head_dim;
+        a.n_seq = n_seq - s0 < batch ? n_seq - s0 : batch;
+        a.q = q + rows;
+        a.out = out + rows;
+        a.positions = positions + s0;
+        a.table = block_table + (size_t)s0 * max_pages;
+        a.starts = rules && rules->starts ? rules->starts + s0 : nullptr;
+        e = table[hi][ti](r);
         if (e != cudaSuccess) return fail(e);
     }
     return ATTN_OK;

@@ -8,21 +8,6 @@
 
 namespace attn {
 
-// Stages and resident blocks per SM: about 190 KB of stages on an SM whatever
-// the row size, so that enough copies are in flight for HBM, in as many blocks as
-// the accumulators (head_dim / 2 registers a thread) leave room for.
-template <int HD, int ES> struct PagedShape;
-template <> struct PagedShape<64, 1>  { static constexpr int S = 8, MINB = 2; };
-template <> struct PagedShape<128, 1> { static constexpr int S = 6, MINB = 2; };
-template <> struct PagedShape<256, 1> { static constexpr int S = 6, MINB = 1; };
-template <> struct PagedShape<64, 2>  { static constexpr int S = 6, MINB = 2; };
-template <> struct PagedShape<128, 2> { static constexpr int S = 3, MINB = 2; };
-template <> struct PagedShape<256, 2> { static constexpr int S = 3, MINB = 1; };
-
-template <int HD, typename KV, int SLOTS>
-using PagedCfgFor = PagedCfg<HD, SLOTS, KV, PagedShape<HD, std::is_same<KV, E4m3>::value ? 1 : 2>::S,
-                             PagedShape<HD, std::is_same<KV, E4m3>::value ? 1 : 2>::MINB>;
-
 template <class C, bool RULES>
 cudaError_t launch_paged_kernel(const PagedRequest &r)
 {
@@ -35,23 +20,33 @@ cudaError_t launch_paged_kernel(const PagedRequest &r)
     e = encode_paged_map(&vmap, r.v, C::ES, bf, C::HD, r.pa.n_kv_head, r.pa.page_size, r.pa.n_pages,
                          r.head_stride * es, r.row_stride * es, r.page_stride * es, C::CW, r.pa.box_rows);
     if (e != cudaSuccess) return e;
-    const void *fn = reinterpret_cast<const void *>(&attn_paged_partial<C, RULES>);
+    const void *fn = reinterpret_cast<const void *>(&attn_paged_stream<C, RULES>);
     e = ensure_smem_attr(fn, (int)C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     PagedArgs pa = r.pa;
     void *args[] = {&kmap, &vmap, &pa};
-    return launch_pdl(fn, dim3(pa.n_kv_head * pa.qgroups, pa.n_splits, r.n_seq), dim3(C::THREADS), C::SMEM_BYTES,
-                      r.stream, args);
+    e = launch_pdl(fn, dim3((unsigned)pa.qgroups, (unsigned)pa.n_kv_head, (unsigned)pa.ranks), dim3(C::THREADS), C::SMEM_BYTES, r.stream, args);
+    if (e != cudaSuccess || pa.ranks == 1) return e;
+    // chunks of 32 dimensions while there are few rows (more blocks share the parts' loads), else whole rows
+    const int64_t rows = (int64_t)pa.n_q * pa.n_head;
+    const bool chunks = rows * pa.n_seq <= 512;
+    int slots = C::SLOTS;
+    const void *cf = chunks ? reinterpret_cast<const void *>(&attn_paged_combine<C::HD, 32>)
+                            : reinterpret_cast<const void *>(&attn_paged_combine<C::HD, C::HD>);
+    e = ensure_smem_attr(cf, 0);
+    if (e != cudaSuccess) return e;
+    void *cargs[] = {&pa, &slots};
+    return launch_pdl(cf, dim3((unsigned)rows, (unsigned)pa.n_seq, chunks ? C::HD / 32 : 1), dim3(128), 0, r.stream, cargs);
 }
 
 template <int HD, typename KV>
 cudaError_t launch_paged_for(const PagedRequest &r)
 {
     if (paged_slots(r.pa.n_q, r.pa.group) == 8) {
-        using C = PagedCfgFor<HD, KV, 8>;
+        using C = PagedCfg<HD, 8, KV>;
         return r.rules ? launch_paged_kernel<C, true>(r) : launch_paged_kernel<C, false>(r);
     }
-    using C = PagedCfgFor<HD, KV, 16>;
+    using C = PagedCfg<HD, 16, KV>;
     return r.rules ? launch_paged_kernel<C, true>(r) : launch_paged_kernel<C, false>(r);
 }
 

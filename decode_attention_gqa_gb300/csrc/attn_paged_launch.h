@@ -12,25 +12,65 @@ namespace attn {
 
 constexpr int kTypeF32 = 0, kTypeF16 = 1, kTypeBf16 = 2, kTypeE4m3 = 3;   // ATTN_TYPE_*
 
+// Shape of the paged kernel for (head_dim, bytes of an element, slots).
+struct PagedShape {
+    int nsl;                  // 16-row slices of a stage
+    int warps;                // compute warps: a multiple of nsl
+    int stages;               // a multiple of warps / nsl, so that a stage is always the same warps'
+    int blocks;               // resident blocks per SM
+};
+
+// About 190 KB of stages on an SM whatever the row size, in as many blocks as the accumulators
+// (head_dim / 4 registers a thread for 8 slots, head_dim / 2 for 16) leave room for.
+constexpr PagedShape paged_shape(int head_dim, int es, int slots)
+{
+    return es == 1 ? (head_dim == 64    ? PagedShape{4, 4, 6, 3}
+                      : head_dim == 128 ? (slots == 8 ? PagedShape{4, 4, 4, 3} : PagedShape{4, 4, 6, 2})
+                                        : (slots == 8 ? PagedShape{4, 4, 3, 2} : PagedShape{2, 6, 12, 1}))
+                   : (head_dim == 64    ? (slots == 8 ? PagedShape{4, 4, 4, 3} : PagedShape{4, 4, 6, 2})
+                      : head_dim == 128 ? PagedShape{4, 4, 3, 2}
+                                        : PagedShape{2, 6, 6, 1});
+}
+
+constexpr int kPagedSeqs = 128;   // sequences one launch takes
+
+// Division of 0 <= n < 2^31 by a divisor known on the host: (mulhi(n, mul) + n) >> shift.
+struct FastDiv {
+    unsigned mul, shift;
+};
+
+inline FastDiv fast_div(unsigned d)
+{
+    unsigned s = 0;
+    while (s < 31 && (1u << s) < d) ++s;
+    return FastDiv{(unsigned)((((uint64_t)1 << 32) * (((uint64_t)1 << s) - d)) / d + 1), s};
+}
+
 struct PagedArgs {
     const float *q;           // [n_seq][n_q][n_head][HD]
-    float *out;               // the same; written by the partial kernel when n_splits == 1
+    float *out;
     const int32_t *positions; // [n_seq]
     const int32_t *table;     // [n_seq][max_pages]
     const float *k_scale;     // [n_pages][n_kv_head], e4m3 only
     const float *v_scale;
     const float *slopes;      // [n_head] or null
     const int32_t *starts;    // [n_seq] or null
-    float *ws_o;              // [n_seq][n_q * n_head][P][HD]
-    float2 *ws_ml;            // [n_seq][n_q * n_head][P]
+    // Partial results: row ((rank * 2 + which) * units + unit) * slots + slot, `which` 1 where the
+    // sequence began in this rank's rows, 0 where it began before them
+    float *ws_o;              // [rows][HD]
+    float2 *ws_ml;            // [rows]
+    int2 *ws_span;            // [n_seq]: first and last rank that has rows of the sequence
     unsigned *err;
+    int n_seq;                // at most kPagedSeqs
     int n_head, n_kv_head, group, n_q;
-    int qgroups;              // blocks per (split, KV head) along the (query row, head) slots
-    int n_splits;             // P
+    int qgroups;              // blocks per (rank, KV head) along the (query row, head) slots
+    int units;                // n_kv_head * qgroups
+    int ranks;                // blocks that share the rows, per unit
     int max_pages, n_pages, page_size;
     int cap;                  // max_pages * page_size
     int window;               // 0: none
-    int box_rows;             // rows of one TMA box: it divides the page and the tile
+    int box_rows;             // rows of one TMA box: a power of two that divides the page and the stage
+    FastDiv by_page, by_group;
     float qscale;             // scale * log2 e, or scale / softcap
     float cap_log2;           // softcap * log2 e, or 0
 };
@@ -39,21 +79,14 @@ struct PagedRequest {
     PagedArgs pa;
     const void *k, *v;
     int64_t page_stride, row_stride, head_stride;   // elements
-    int n_seq, head_dim, kv_type;
+    int head_dim, kv_type;
     bool rules;               // softcap or slopes
     cudaStream_t stream;
-};
-
-// Shape of the paged partial kernel for (head_dim, element size, slots).
-struct PagedInfo {
-    int tile_rows;
-    int blocks_per_sm;
 };
 
 // (query row, head) slots of a block: 8 where a KV head's slots fit in 8, else 16.
 inline int paged_slots(int n_q, int group) { return n_q * group <= 8 ? 8 : 16; }
 
-PagedInfo paged_info(int head_dim, int kv_type, int slots);
 cudaError_t launch_paged_hd64_f16(const PagedRequest &r);
 cudaError_t launch_paged_hd64_bf16(const PagedRequest &r);
 cudaError_t launch_paged_hd64_e4m3(const PagedRequest &r);

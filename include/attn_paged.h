@@ -181,7 +181,10 @@ typedef struct {
  *   n_q          1 .. 1024
  *   scale        multiplies q.k
  *   rules        NULL: plain scores
- *   n_splits     splits of each sequence's rows; 0: attn_paged_plan's count
+ *   n_splits     blocks that share the call's rows, per KV head (and group of
+ *                16 (query row, head) pairs of it): each takes an equal part of
+ *                the rows of all sequences laid end to end; 0: attn_paged_plan's
+ *                count, which fills the GPU once
  *   workspace    device buffer of the bytes attn_paged_plan reports, 256-byte
  *                aligned; NULL: the library-owned buffer (see attn_decode: one
  *                stream at a time, no growth while capturing, and graphs that
@@ -196,7 +199,7 @@ attn_status attn_decode_paged(const attn_paged_cache *cache, const int32_t *bloc
                               void *workspace, size_t workspace_bytes, attn_stream_t stream);
 
 /*
- * attn_paged_plan -- host-only: the split count and the workspace bytes (0 for one split)
+ * attn_paged_plan -- host-only: the split count and the workspace bytes (0 for one block)
  * of an attn_decode_paged call with these arguments; only the shape fields of
  * the cache are looked at. n_splits as in the call, window as in its rules (0:
  * none). sm_count <= 0 asks the current device. Either output may be NULL.

@@ -170,6 +170,26 @@ def test_several_query_rows_and_large_groups(pkg, kv, hd, n_q, group, page):
     assert pkg.attn_read_device_error() == 0
 
 
+@pytest.mark.parametrize("kv", ["e4m3", "f16", "bf16"])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("n_q,group", [(1, 2), (4, 4)])
+def test_many_tiles_a_block(pkg, kv, hd, n_q, group):
+    """Blocks that go round their stages and descriptor buffers many times, across sequences, also with a
+    window that begins late."""
+    pool = Pool(hd + n_q, kv, 1, hd, 32, (2900, 0, 1411, 33, 800))
+    attend_check(pkg, pool, n_q, group, splits=(1, 2, 5, 0))
+    attend_check(pkg, pool, n_q, group, splits=(1, 3), window=1300)
+    assert pkg.attn_read_device_error() == 0
+
+
+def test_more_sequences_than_a_launch_takes(pkg):
+    rng = np.random.default_rng(0)
+    pool = Pool(1, "e4m3", 1, 64, 16, [int(x) for x in rng.integers(0, 70, 300)])
+    attend_check(pkg, pool, 1, 2, splits=(0, 1, 5))
+    attend_check(pkg, pool, 2, 2, splits=(0,), starts=[int(x) for x in rng.integers(0, 40, 300)], window=30)
+    assert pkg.attn_read_device_error() == 0
+
+
 RULES = [
     dict(softcap=20.0), dict(window=1), dict(window=40), dict(window=100000), dict(slopes=True),
     dict(starts=True), dict(softcap=5.0, window=33, slopes=True, starts=True), dict(window=70, starts=True),

@@ -107,15 +107,21 @@ def test_plan_for_a_given_sm_count(lib):
     def plan(cache=None, max_pages=128, n_seq=1, n_q=1, n_head=8, window=0, P=0, sms=152):
         c = cache or _cache()
         return pkg.attn_paged_plan(ctypes.addressof(c), max_pages, n_seq, n_q, n_head, window, P, sms)
-    # one sequence, 2 KV heads, 8192 rows: one wave of 2 x 152 blocks in whole 64-row tiles
-    P, ws = plan()
-    assert P == 128 and ws == pkg.attn_workspace_size(1, 8, 128, 128)
-    # a window bounds the rows that a sequence can need, and so the splits
+    def ws(P, units, slots=8, n_seq=1, hd=128):
+        parts = P * 2 * units * slots
+        return -(-parts * hd * 4 // 256) * 256 + -(-parts * 8 // 256) * 256 + -(-min(n_seq, 128) * 8 // 256) * 256
+    # one sequence, 2 KV heads, 8192 rows: 2 x 152 resident blocks, but no more than there are 64-row tiles
+    assert plan() == (128, ws(128, 2))
+    assert plan(n_seq=2) == (152, ws(152, 2, n_seq=2))
+    assert plan(n_seq=1000) == (152, ws(152, 2, n_seq=1000))
+    # a window bounds the rows that a sequence can need, and so the blocks
     assert plan(window=100)[0] < 8
-    # enough units to fill the waves: one split, and no workspace
-    assert plan(n_seq=4096) == (1, 0)
-    assert plan(P=7) == (7, pkg.attn_workspace_size(1, 8, 128, 7))
-    assert plan(n_q=4)[1] == pkg.attn_workspace_size(1, 32, 128, plan(n_q=4)[0])
+    # 16 (query row, head) slots a block, several blocks a KV head
+    assert plan(n_q=4, n_seq=9) == (152, ws(152, 2, 16, 9)) and plan(n_q=12, n_seq=9)[0] == 50
+    # units just over half of the resident blocks: four rounds; far more units than blocks: one block each
+    assert plan(cache=_cache(n_kv_head=160), n_head=160, n_seq=2)[0] == 7
+    assert plan(cache=_cache(n_kv_head=2000), n_head=2000) == (1, 0)
+    assert plan(P=7) == (7, ws(7, 2)) and plan(P=1) == (1, 0)
     for kw, st in ((dict(n_seq=0), INVALID), (dict(n_head=3), INVALID), (dict(window=-1), INVALID),
                    (dict(P=-2), INVALID), (dict(n_head=130), UNSUPPORTED),
                    (dict(cache=_cache(head_dim=32)), UNSUPPORTED), (dict(max_pages=0), INVALID)):
