@@ -423,6 +423,19 @@ def _struct(x):
     return x._address
 
 
+# The torch forms below check their tensors in one expression, since a decode step's call costs the host
+# more than the GPU; `_refuse` finds out what was wrong with them.
+_torch = None
+
+
+def _torch_module():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _on_device(name, t, dtype, device):
     if t.dtype != dtype:
         raise TypeError("%s must be %s" % (name, str(dtype).replace("torch.", "")))
@@ -433,6 +446,21 @@ def _on_device(name, t, dtype, device):
 def _dense(name, t):
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
+
+
+def _refuse(checks, device, shapes):
+    """Raise for the first of `checks` (name, tensor, dtype, dense) or of `shapes` (holds, message)
+    that fails."""
+    _same_device(device)
+    for name, t, dtype, dense in checks:
+        if t is not None:
+            _on_device(name, t, dtype, device)
+            if dense:
+                _dense(name, t)
+    for holds, message in shapes:
+        if not holds:
+            raise ValueError(message)
+    raise ValueError("the tensors do not fit together")
 
 
 class PagedCache:
@@ -470,18 +498,8 @@ class PagedCache:
                                k.stride(0), k.stride(1), k.stride(2), n_pages, page_size, n_kv_head,
                                head_dim, types[k.dtype], 0)
         self._address = ctypes.addressof(self._c)
+        self._index = k.get_device()
         self._plans = {}
-
-    def _plan(self, max_pages, n_seq, n_q, n_head, window, n_splits):
-        # the plan is a function of these numbers, the pool's shape and the device
-        key = (max_pages, n_seq, n_q, n_head, window, n_splits)
-        got = self._plans.get(key)
-        if got is None:
-            if len(self._plans) >= 4096:
-                self._plans.clear()
-            got = self._plans[key] = attn_paged_plan(self, max_pages, n_seq, n_q, n_head, window,
-                                                     n_splits)
-        return got
 
 
 class Rope:
@@ -495,36 +513,32 @@ class Rope:
         self.steps = torch.tensor([s - (1 << 64) if s >> 63 else s for s in steps],
                                   dtype=torch.int64, device=device)
         self.rot_dim = rot_dim
+        self._index = self.steps.get_device()
         self._c = _RopeStruct(self.steps.data_ptr(), rot_dim, 1 if interleaved else 0, mscale, 0)
         self._address = ctypes.addressof(self._c)
 
 
 def _same_device(device):
-    import torch
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
+    if device.type != "cuda" or device.index != _torch_module().cuda.current_device():
         raise ValueError("the cache must be on the current CUDA device")
 
 
-def _batch(cache, block_table, positions):
-    import torch
-    _on_device("block_table", block_table, torch.int32, cache.device)
-    _on_device("positions", positions, torch.int32, cache.device)
-    if block_table.dim() != 2 or positions.dim() != 1 or positions.shape[0] != block_table.shape[0]:
-        raise ValueError("block_table must be [n_seq, max_pages] and positions [n_seq]")
-    _dense("block_table", block_table)
-    _dense("positions", positions)
-    return block_table.shape
+def _current_stream(index):
+    """The handle of torch's current stream on device `index`."""
+    cuda = _torch_module().cuda
+    get = getattr(_torch._C, "_cuda_getCurrentRawStream", None)    # the handle without a Stream object
+    return get(index) if get is not None else cuda.current_stream(index).cuda_stream
 
 
-def _tokens(name, t, n_tokens, heads, head_dim, dtype, device):
-    _on_device(name, t, dtype, device)
-    if t.dim() != 3 or t.shape[0] != n_tokens or t.shape[2] != head_dim or \
-            (heads is not None and t.shape[1] != heads):
-        raise ValueError("%s must be [n_tokens, heads, head_dim]" % name)
-    s = t.stride()
-    if s[2] != 1 or (s[1] != head_dim and t.shape[1] > 1):
-        raise ValueError("%s must be dense within a token" % name)
-    return s[0] if n_tokens > 1 else 0
+def _in_type(dtype):
+    torch = _torch_module()
+    if dtype is torch.bfloat16:
+        return ATTN_TYPE_BF16
+    if dtype is torch.float16:
+        return ATTN_TYPE_F16
+    if dtype is torch.float32:
+        return ATTN_TYPE_F32
+    raise TypeError("k_new must be float32, float16 or bfloat16")
 
 
 def rope_append(cache, block_table, positions, k_new, v_new, q=None, q_out=None, rope=None,
@@ -535,39 +549,64 @@ def rope_append(cache, block_table, positions, k_new, v_new, q=None, q_out=None,
     block_table int32 [n_seq, max_pages]; positions int32 [n_seq]; cu_tokens int32 [n_seq + 1], or
     None for the same number of tokens in every sequence. `q_out` (float32) is allocated when not
     given. Returns q_out (None without q)."""
-    import torch
-    _same_device(cache.device)
-    n_seq, max_pages = _batch(cache, block_table, positions)
-    types = {torch.float32: ATTN_TYPE_F32, torch.float16: ATTN_TYPE_F16,
-             torch.bfloat16: ATTN_TYPE_BF16}
-    dt = k_new.dtype
-    if dt not in types:
-        raise TypeError("k_new must be float32, float16 or bfloat16")
-    n_tokens, hd = k_new.shape[0], cache.head_dim
-    ks = _tokens("k_new", k_new, n_tokens, cache.n_kv_head, hd, dt, cache.device)
-    vs = _tokens("v_new", v_new, n_tokens, cache.n_kv_head, hd, dt, cache.device)
-    qs, n_head = 0, 0
+    torch = _torch or _torch_module()
+    i32, index, dt, hd = torch.int32, cache._index, k_new.dtype, cache.head_dim
+    in_type = _in_type(dt)
+    shape, ks, vs = k_new.shape, k_new.stride(), v_new.stride()
+    n_tokens, n_kv = shape[0], cache.n_kv_head
+    n_seq, max_pages = block_table.shape if block_table.dim() == 2 else (-1, 0)
+    row = (n_kv, hd)
+    if not (index >= 0 and index == torch.cuda.current_device() and shape[1:] == row and v_new.shape == shape and
+            v_new.dtype is dt and k_new.get_device() == index and v_new.get_device() == index and
+            ks[2] == 1 and vs[2] == 1 and (n_kv == 1 or (ks[1] == hd and vs[1] == hd)) and
+            block_table.dtype is i32 and block_table.get_device() == index and block_table.is_contiguous() and
+            positions.dtype is i32 and positions.get_device() == index and positions.is_contiguous() and
+            positions.shape == (n_seq,)):
+        _refuse((("k_new", k_new, dt, False), ("v_new", v_new, dt, False),
+                 ("block_table", block_table, i32, True), ("positions", positions, i32, True)), cache.device,
+                ((shape[1:] == row and v_new.shape == shape, "k_new and v_new must be [n_tokens, n_kv_head, head_dim]"),
+                 (n_seq >= 0 and positions.shape == (n_seq,),
+                  "block_table must be [n_seq, max_pages] and positions [n_seq]"),
+                 (False, "k_new and v_new must be dense within a token")))
+    qs = n_head = 0
+    qp = op = cp = None
     if q is not None:
-        qs = _tokens("q", q, n_tokens, None, hd, dt, cache.device)
-        n_head = q.shape[1]
+        qshape, qst = q.shape, q.stride()
+        if not (len(qshape) == 3 and qshape[0] == n_tokens and qshape[2] == hd and q.dtype is dt and
+                q.get_device() == index and qst[2] == 1 and (qshape[1] == 1 or qst[1] == hd)):
+            _refuse((("q", q, dt, False),), cache.device,
+                    ((False, "q must be [n_tokens, n_head, head_dim], dense within a token"),))
+        n_head, qs = qshape[1], qst[0]
         if q_out is None:
-            q_out = torch.empty(n_tokens, n_head, hd, dtype=torch.float32, device=cache.device)
-        else:
-            _on_device("q_out", q_out, torch.float32, cache.device)
-            if q_out.shape != q.shape:
-                raise ValueError("q_out must have the shape of q")
-            _dense("q_out", q_out)
+            q_out = torch.empty(qshape, dtype=torch.float32, device=cache.device)
+        elif not (q_out.shape == qshape and q_out.dtype is torch.float32 and q_out.get_device() == index and
+                  q_out.is_contiguous()):
+            _refuse((("q_out", q_out, torch.float32, True),), cache.device,
+                    ((False, "q_out must have the shape of q"),))
+        qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
     if cu_tokens is not None:
-        _on_device("cu_tokens", cu_tokens, torch.int32, cache.device)
-        if cu_tokens.shape != (n_seq + 1,):
-            raise ValueError("cu_tokens must be [n_seq + 1]")
-        _dense("cu_tokens", cu_tokens)
-    if rope is not None and rope.steps.device != cache.device:
-        raise ValueError("rope must be on the cache's device")
-    attn_rope_append(cache, block_table, max_pages, positions, cu_tokens, n_seq, n_tokens, q, k_new,
-                     v_new, qs, ks, vs, types[dt], q_out, n_head, rope, stream)
+        if not (cu_tokens.dtype is i32 and cu_tokens.get_device() == index and cu_tokens.shape == (n_seq + 1,) and
+                cu_tokens.is_contiguous()):
+            _refuse((("cu_tokens", cu_tokens, i32, True),), cache.device,
+                    ((False, "cu_tokens must be [n_seq + 1]"),))
+        cp = cu_tokens.data_ptr()
+    rp = None
+    if rope is not None:
+        if rope._index != index:
+            raise ValueError("rope must be on the cache's device")
+        rp = rope._address
+    if n_tokens <= 1:
+        qs, kst, vst = 0, 0, 0                       # one token has no stride
+    else:
+        kst, vst = ks[0], vs[0]
+    status = (_lib or load()).attn_rope_append(
+        cache._address, block_table.data_ptr(), max_pages, positions.data_ptr(), cp, n_seq, n_tokens, qp,
+        k_new.data_ptr(), v_new.data_ptr(), qs, kst, vst, in_type, op, n_head, rp,
+        _current_stream(index) if stream is None else _stream(stream))
+    if status:
+        raise AttnError(status, "attn_rope_append")
     return q_out
 
 
@@ -580,49 +619,59 @@ def paged_decode_attention(cache, block_table, positions, q, scale=None, out=Non
     from torch's allocator on the current stream (pass that stream, or None: another one would
     not be ordered with the workspace's reuse), so captured graphs hold workspaces of their own.
     Returns out."""
-    import torch
-    _same_device(cache.device)
-    n_seq, max_pages = _batch(cache, block_table, positions)
-    _on_device("q", q, torch.float32, cache.device)
+    torch = _torch or _torch_module()
+    i32, f32, index, hd = torch.int32, torch.float32, cache._index, cache.head_dim
     shape = q.shape
     if len(shape) == 3:
-        n_q, (qs, n_head, hd) = 1, shape
+        n_q, (qs, n_head, qd) = 1, shape
     elif len(shape) == 4:
-        qs, n_q, n_head, hd = shape
+        qs, n_q, n_head, qd = shape
     else:
         raise ValueError("q must be [n_seq, n_head, head_dim] or [n_seq, n_q, n_head, head_dim]")
-    if qs != n_seq or hd != cache.head_dim:
-        raise ValueError("q, the cache and positions disagree on n_seq or head_dim")
-    _dense("q", q)
+    n_seq, max_pages = block_table.shape if block_table.dim() == 2 else (-1, 0)
+    if not (index >= 0 and index == torch.cuda.current_device() and qs == n_seq and qd == hd and q.dtype is f32 and
+            q.get_device() == index and q.is_contiguous() and
+            block_table.dtype is i32 and block_table.get_device() == index and block_table.is_contiguous() and
+            positions.dtype is i32 and positions.get_device() == index and positions.is_contiguous() and
+            positions.shape == (n_seq,)):
+        _refuse((("block_table", block_table, i32, True), ("positions", positions, i32, True), ("q", q, f32, True)),
+                cache.device,
+                ((n_seq >= 0 and positions.shape == (n_seq,),
+                  "block_table must be [n_seq, max_pages] and positions [n_seq]"),
+                 (False, "q, the cache and positions disagree on n_seq or head_dim")))
     if out is None:
         out = torch.empty_like(q)
-    else:
-        _on_device("out", out, torch.float32, cache.device)
-        if out.shape != shape:
-            raise ValueError("out must have the shape of q")
-        _dense("out", out)
+    elif not (out.shape == shape and out.dtype is f32 and out.get_device() == index and out.is_contiguous()):
+        _refuse((("out", out, f32, True),), cache.device, ((False, "out must have the shape of q"),))
     rules = None
     if softcap or window or slopes is not None or starts is not None:
-        if slopes is not None:
-            _on_device("slopes", slopes, torch.float32, cache.device)
-            if slopes.shape != (n_head,):
-                raise ValueError("slopes must be [n_head]")
-            _dense("slopes", slopes)
-        if starts is not None:
-            _on_device("starts", starts, torch.int32, cache.device)
-            if starts.shape != (n_seq,):
-                raise ValueError("starts must be [n_seq]")
-            _dense("starts", starts)
-        rules = (softcap, window, slopes, starts)
-    if scale is None:
-        scale = hd ** -0.5
+        if slopes is not None and not (slopes.dtype is f32 and slopes.get_device() == index and
+                                       slopes.shape == (n_head,) and slopes.is_contiguous()):
+            _refuse((("slopes", slopes, f32, True),), cache.device, ((False, "slopes must be [n_head]"),))
+        if starts is not None and not (starts.dtype is i32 and starts.get_device() == index and
+                                       starts.shape == (n_seq,) and starts.is_contiguous()):
+            _refuse((("starts", starts, i32, True),), cache.device, ((False, "starts must be [n_seq]"),))
+        kept = _RulesStruct(softcap, window, slopes.data_ptr() if slopes is not None else None,
+                            starts.data_ptr() if starts is not None else None)
+        rules = ctypes.addressof(kept)
     if n_seq == 0:
         return out
-    handle = torch.cuda.current_stream().cuda_stream
+    handle = _current_stream(index)
     if stream is not None and _stream(stream) != handle:
         raise ValueError("stream must be the current stream (torch.cuda.stream selects one)")
-    n_splits, need = cache._plan(max_pages, n_seq, n_q, n_head, window, n_splits)
+    # the plan is a function of these numbers, the pool's shape and the device
+    key = (max_pages, n_seq, n_q, n_head, window, n_splits)
+    plan = cache._plans.get(key)
+    if plan is None:
+        if len(cache._plans) >= 4096:
+            cache._plans.clear()
+        plan = cache._plans[key] = attn_paged_plan(cache, max_pages, n_seq, n_q, n_head, window, n_splits)
+    n_splits, need = plan
     ws = torch.empty(need, dtype=torch.uint8, device=cache.device) if need else None
-    attn_decode_paged(cache, block_table, max_pages, positions, q, out, n_seq, n_q, n_head, scale,
-                      rules, n_splits, ws, need, handle)
+    status = (_lib or load()).attn_decode_paged(
+        cache._address, block_table.data_ptr(), max_pages, positions.data_ptr(), q.data_ptr(), out.data_ptr(),
+        n_seq, n_q, n_head, hd ** -0.5 if scale is None else scale, rules, n_splits,
+        ws.data_ptr() if need else None, need, handle)
+    if status:
+        raise AttnError(status, "attn_decode_paged")
     return out
