@@ -115,7 +115,9 @@ struct PagedCfg {
     static constexpr int PARTS = SLOTS == 8 ? (NP + 1) / 2 : NP;
     static constexpr bool Q_REGS = E8 && HD == 64 && SLOTS == 8;   // else they are read per k-step (no spills)
     static constexpr uint32_t Q_BYTES = (uint32_t)(SLOTS == 8 ? NP : 2 * NP) * KSTEPS * 256;
-    static constexpr int MS = merge_stride<HD>();
+    // Row stride of the merge area: 4 floats past a multiple of 32, so that the rows of a warp's slots (2u) lie 8
+    // banks apart
+    static constexpr int MS = HD + 4;
     static constexpr uint32_t OFF_MO = 2 * NWC * SLOTS;           // floats, a multiple of 4
     static constexpr uint32_t MERGE_BYTES = (OFF_MO + SLOTS * MS) * 4;
     static constexpr uint32_t OFF_Q = S * STAGE_BYTES;            // Q fragments; then the merge area
@@ -139,6 +141,14 @@ struct PagedCfg {
     static __device__ __forceinline__ uint32_t row(int r)
     {
         return CHB == 128 ? (uint32_t)(r * 128 + ((r & 7) << 4)) : (uint32_t)(r * 64 + (((r >> 1) & 3) << 4));
+    }
+    // Where four dimensions from d stand in a row of the merge area: as they are, or (8 bits, where a lane
+    // holds neighbouring fours) the fours of the eight lanes next to each other.
+    static __device__ __forceinline__ int merge_at(int d)
+    {
+        if constexpr (!E8) return d;
+        constexpr int LD = CW / 8;                                // dimensions of a lane in a chunk
+        return d / CW * CW + (d % LD / 4 * 8 + d % CW / LD) * 4;
     }
     static __device__ __forceinline__ uint32_t unit(uint32_t base_row, int U)
     {
@@ -491,10 +501,15 @@ struct PagedWarp {
 #pragma unroll
                 for (int k = 0; k < C::SPL; ++k) {
                     const SlotInfo sa = slot_at(smem, 2 * u + 8 * k), sb = slot_at(smem, 2 * u + 1 + 8 * k);
+                    int r = max(sg.z - row0, 0);
+                    const int stop = min(sg.w - row0, C::WR - 1);
 #pragma unroll 1
-                    for (int r = 0; r < C::WR; ++r) {
+                    for (; r <= stop; ++r) {
                         const int row = row0 + r;
-                        if (row < sg.z || row > sg.w || (row >= sg.x && row <= sg.y)) continue;
+                        if (row >= sg.x && row <= sg.y) {             // skip the rows every slot sees
+                            r = min(sg.y - row0, stop);
+                            continue;
+                        }
                         const float x = r & 8 ? (r & 1 ? sc[k][3] : sc[k][2]) : (r & 1 ? sc[k][1] : sc[k][0]);
                         const float p0 = __shfl_sync(0xffffffffu, x, 8 * u + ((r & 7) >> 1));
                         const float p1 = __shfl_sync(0xffffffffu, x, 8 * u + 4 + ((r & 7) >> 1));
@@ -570,7 +585,7 @@ struct PagedWarp {
 #pragma unroll
                         for (int j = 0; j < TPC; j += 2) {
                             const int n = c * TPC + j;
-                            float4 *p = reinterpret_cast<float4 *>(row + c * C::CW + g * 2 * TPC + 2 * j);
+                            float4 *p = reinterpret_cast<float4 *>(row + C::merge_at(c * C::CW + g * 2 * TPC + 2 * j));
                             float4 v = add ? *p : make_float4(0.f, 0.f, 0.f, 0.f);
                             v.x = fmaf(o[k][n][e], wt, v.x);
                             v.y = fmaf(o[k][n][2 + e], wt, v.y);
@@ -781,11 +796,20 @@ attn_paged_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         int seq = find_seq(cs, a.n_seq, first + lane / NSL);   // the lane's sequence; it only moves on
         int row = 0;
         bool need = false;                                     // some row of the slice's box is attended
+        // q of a sequence that is about to begin, into L2: the rows of the block's slots
+        auto prefetch_q = [&](int s) {
+            const int x0 = qg * C::SLOTS, x1 = min(x0 + C::SLOTS, a.n_q * a.group) - 1;
+            for (int t = div(a.by_group, x0); t <= div(a.by_group, x1); ++t)
+                prefetch_l2(a.q + (((size_t)s * a.n_q + t) * a.n_head + (size_t)hk * a.group) * C::HD,
+                            (uint32_t)(a.group * C::HD * sizeof(float)));
+        };
         auto locate = [&](int grp) {
             const int t = first + grp * TPG + lane / NSL;
             need = t < end;
             if (!need) return;
+            const int was = seq;
             while (cs[seq + 1] <= t) ++seq;
+            if (seq != was && lane % NSL == 0) prefetch_q(seq);
             const SlotRows sr = seq_rows(a, snkv[seq], sstart[seq]);
             const int2 x = seq_extent<TILE>(a, sr);
             row = x.x + (t - cs[seq]) * TILE + lane % NSL * WR;
@@ -838,7 +862,7 @@ attn_paged_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         desc[lane] = SliceInfo{(unsigned)p0 < (unsigned)a.n_pages ? p0 : -1, z0, 1.f, 1.f};
         const float2 f0 = load_scales(p0);
         __syncwarp();
-        const int early = min(S, ntiles);
+        const int early = min(C::WPT, ntiles);                  // what the compute warps start with; the rest below
         if (lane == 0)
             for (int t = 0; t < early; ++t) issue(t);
         locate(1);
@@ -981,11 +1005,11 @@ attn_paged_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     const float2 ml = mm[x * C::SLOTS + g];
                     if (ml.x != -INFINITY) sum = fmaf(ex2(ml.x - M), ml.y, sum);
                 }
-                float4 O = *reinterpret_cast<const float4 *>(area + g * C::MS + d);
+                float4 O = *reinterpret_cast<const float4 *>(area + g * C::MS + C::merge_at(d));
                 if (over) {
 #pragma unroll
                     for (int x = 1; x < NWC; ++x) {
-                        const float4 v = *reinterpret_cast<const float4 *>(area + (x * C::SLOTS + g) * C::MS + d);
+                        const float4 v = *reinterpret_cast<const float4 *>(area + (x * C::SLOTS + g) * C::MS + C::merge_at(d));
                         O.x += v.x; O.y += v.y; O.z += v.z; O.w += v.w;
                     }
                 }
