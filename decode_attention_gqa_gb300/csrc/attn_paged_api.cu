@@ -218,6 +218,10 @@ attn_status attn_rope_append(const attn_paged_cache *cache, const int32_t *block
     // (sequence, page) pairs that may be touched: the page jobs' numbering on the device
     a.page_items = cu_tokens ? n_tokens / cache->page_size + 2 * (int64_t)n_seq
                              : (int64_t)n_seq * ((a.n_each + cache->page_size - 2) / cache->page_size + 1);
+    a.wide = aligned(q, 32) && aligned(k_new, 32) && aligned(v_new, 32) && aligned(q_out, 32) &&
+             (q ? q_stride : 0) * es % 32 == 0 && k_stride * es % 32 == 0 && v_stride * es % 32 == 0 &&
+             aligned(cache->k, 32) && aligned(cache->v, 32);
+    for (int64_t x : {cs.page, cs.row, cs.head}) a.wide = a.wide && x * type_bytes(cache->kv_type) % 32 == 0;
     r.head_dim = cache->head_dim;
     r.in_type = in_type;
     r.kv_type = cache->kv_type;

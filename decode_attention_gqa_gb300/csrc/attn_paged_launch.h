@@ -114,7 +114,9 @@ struct AppendArgs {
     int64_t n_each;                                 // tokens per sequence when cu is null
     int max_pages, n_pages, page_size;
     int64_t page_items;                             // (sequence, page) candidates, e4m3 only
-    int64_t page_blocks;                            // blocks of page jobs
+    int64_t page_blocks;                            // blocks of page jobs, before those of token jobs
+    bool kv_apart;                                  // page jobs take K or V, not both
+    bool wide;                                      // every row and head starts at a multiple of 32 bytes
     int iters;                                      // head groups one warp takes for its token
     int chunks;                                     // warps per token
 };
