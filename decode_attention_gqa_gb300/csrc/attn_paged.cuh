@@ -46,6 +46,20 @@ template <> struct PagedMma<E4m3> { using T = __half; };
 
 constexpr unsigned kErrBadPage = 0x4u;    // ATTN_DEVERR_BAD_PAGE
 
+// A TMA box whose lines L2 gives up first: a cache is read once a step, and what else the step works on (block
+// table, scales, q, the next layers' weights) should not make room for it (a batch of 339 MB 62.3 -> 59.7
+// us a call, since its small reads then hit L2).
+__device__ __forceinline__ void tma_load_4d_once(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z,
+                                                 int w, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;"
+        :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w),
+           "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
 __device__ __forceinline__ int div(const FastDiv &d, int n)
 {
     return (int)((__umulhi((unsigned)n, d.mul) + (unsigned)n) >> d.shift);
@@ -142,13 +156,21 @@ struct PagedCfg {
     {
         return CHB == 128 ? (uint32_t)(r * 128 + ((r & 7) << 4)) : (uint32_t)(r * 64 + (((r >> 1) & 3) << 4));
     }
-    // Where four dimensions from d stand in a row of the merge area: as they are, or (8 bits, where a lane
-    // holds neighbouring fours) the fours of the eight lanes next to each other.
+    // Where four dimensions from d stand in a row of the merge area (8 bits: a lane holds neighbouring fours): the
+    // fours of eight lanes next to each other, so that they are written without bank conflicts.
     static __device__ __forceinline__ int merge_at(int d)
     {
-        if constexpr (!E8) return d;
         constexpr int LD = CW / 8;                                // dimensions of a lane in a chunk
         return d / CW * CW + (d % LD / 4 * 8 + d % CW / LD) * 4;
+    }
+    // The same for one dimension and 16 bits, where a lane holds every eighth: its fours are dimensions
+    // 32 i + g + {0, 8, 16, 24}.
+    static __device__ __forceinline__ int merge_at16(int d) { return d / 32 * 32 + d % 8 * 4 + d % 32 / 8; }
+    static __device__ __forceinline__ float4 merge_read(const float *row, int d)   // dimensions d .. d + 3
+    {
+        if constexpr (E8) return *reinterpret_cast<const float4 *>(row + merge_at(d));
+        const float *p = row + merge_at16(d);
+        return make_float4(p[0], p[4], p[8], p[12]);
     }
     static __device__ __forceinline__ uint32_t unit(uint32_t base_row, int U)
     {
@@ -563,9 +585,13 @@ struct PagedWarp {
         }
     }
 
-    // The accumulators, scaled to the largest reference among the warps, into (add: onto) mo[slot * MS + d].
-    __device__ __forceinline__ void deposit(const float2 *mm, float *mo, int warp, bool add, int lane)
+    // The accumulators, scaled to the largest reference among the warps, into mo[slot * MS + d]; round -1: all of
+    // them; else the 32-dimension parts whose turn it is, so that each part is one warp's in a round, set in
+    // round 0 and added to in the others.
+    __device__ __forceinline__ void deposit(const float2 *mm, float *mo, int warp, int round, int lane)
     {
+        const bool add = round > 0;
+        auto mine = [&](int part) { return round < 0 || (part + warp) % C::NWC == round; };
         const int g = lane >> 2, u = lane & 3;
 #pragma unroll
         for (int k = 0; k < C::SPL; ++k)
@@ -585,6 +611,7 @@ struct PagedWarp {
 #pragma unroll
                         for (int j = 0; j < TPC; j += 2) {
                             const int n = c * TPC + j;
+                            if (!mine(n / 2)) continue;
                             float4 *p = reinterpret_cast<float4 *>(row + C::merge_at(c * C::CW + g * 2 * TPC + 2 * j));
                             float4 v = add ? *p : make_float4(0.f, 0.f, 0.f, 0.f);
                             v.x = fmaf(o[k][n][e], wt, v.x);
@@ -595,10 +622,15 @@ struct PagedWarp {
                         }
                 } else {
 #pragma unroll
-                    for (int n = 0; n < C::HD / 16; ++n) {
-                        float *p = row + 16 * n + g;
-                        p[0] = fmaf(o[k][n][e], wt, add ? p[0] : 0.f);
-                        p[8] = fmaf(o[k][n][2 + e], wt, add ? p[8] : 0.f);
+                    for (int n = 0; n < C::HD / 16; n += 2) {
+                        if (!mine(n / 2)) continue;
+                        float4 *p = reinterpret_cast<float4 *>(row + 16 * n + 4 * g);
+                        float4 v = add ? *p : make_float4(0.f, 0.f, 0.f, 0.f);
+                        v.x = fmaf(o[k][n][e], wt, v.x);
+                        v.y = fmaf(o[k][n][2 + e], wt, v.y);
+                        v.z = fmaf(o[k][n + 1][e], wt, v.z);
+                        v.w = fmaf(o[k][n + 1][2 + e], wt, v.w);
+                        *p = v;
                     }
                 }
             }
@@ -759,21 +791,32 @@ attn_paged_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         }
         pdl_wait();
         pdl_launch_dependents();
-        // rows and tiles of every sequence, and the tiles before it: lane i takes `per` of them
+        // rows and tiles of every sequence, and the tiles before it: lane i takes `per` of them, their positions
+        // and starts loaded together
         const int per = (a.n_seq + 31) / 32;
-        int sum = 0;
-        for (int i = 0; i < per; ++i) {
+        constexpr int MOST = kPagedSeqs / 32;
+        int pos[MOST], st[MOST];
+#pragma unroll
+        for (int i = 0; i < MOST; ++i) {
             const int s = lane * per + i;
-            if (s >= a.n_seq) break;
-            const int64_t n = (int64_t)ld_dep(a.positions + s) + 1;
+            const bool have = i < per && s < a.n_seq;
+            pos[i] = have ? ld_dep(a.positions + s) : -1;
+            st[i] = have && a.starts ? ld_dep(a.starts + s) : 0;
+        }
+        int sum = 0;
+#pragma unroll
+        for (int i = 0; i < MOST; ++i) {
+            const int s = lane * per + i;
+            if (i >= per || s >= a.n_seq) break;
+            const int64_t n = (int64_t)pos[i] + 1;
             const bool ok = n >= 0 && n <= a.cap;
             if (!ok && unit == 0 && rank == 0) atomicOr(a.err, kErrPositionClamped);
-            const int nkv = ok ? (int)n : n < 0 ? 0 : a.cap, start = a.starts ? ld_dep(a.starts + s) : 0;
+            const int nkv = ok ? (int)n : n < 0 ? 0 : a.cap;
             snkv[s] = nkv;
-            sstart[s] = start;
-            const int2 x = seq_extent<TILE>(a, seq_rows(a, nkv, start));
+            sstart[s] = st[i];
+            const int2 x = seq_extent<TILE>(a, seq_rows(a, nkv, st[i]));
             cs[s] = sum;
-            sum += x.x < x.y && seq_rows(a, nkv, start).low(0) < x.y ? (x.y - x.x + TILE - 1) / TILE : 0;
+            sum += x.x < x.y && seq_rows(a, nkv, st[i]).low(0) < x.y ? (x.y - x.x + TILE - 1) / TILE : 0;
         }
         int before = sum;
 #pragma unroll
@@ -834,6 +877,8 @@ attn_paged_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             if (wanted && !there) atomicOr(a.err, kErrBadPage);
             desc[(grp & 3) * 32 + lane] = SliceInfo{there ? p : -1, z, f.x, f.y};
         };
+        uint64_t once;
+        asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
         const int BR = a.box_rows, nbox = TILE / BR, bsl = BR / WR;
         auto issue = [&](int t) {                              // by lane 0
             const int st = t % S;
@@ -848,8 +893,8 @@ attn_paged_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
                 for (int c = 0; c < C::NCH; ++c) {
                     uint8_t *to = kst + c * (C::TILE_BYTES / C::NCH) + b * BR * C::CHB;
-                    tma_load_4d(to, &kmap, full + st, c * C::CW, hk, x.z, x.page);
-                    tma_load_4d(to + C::TILE_BYTES, &vmap, full + st, c * C::CW, hk, x.z, x.page);
+                    tma_load_4d_once(to, &kmap, full + st, c * C::CW, hk, x.z, x.page, once);
+                    tma_load_4d_once(to + C::TILE_BYTES, &vmap, full + st, c * C::CW, hk, x.z, x.page, once);
                 }
             }
             flags[1] = t + 1;
@@ -981,15 +1026,19 @@ attn_paged_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             w.publish(mm + warp * C::SLOTS, lane);
             asm volatile("bar.sync 1, %0;" :: "r"(NWC * 32) : "memory");
             // the block's last sequence: every tile has been consumed and none is on its way, so that each warp
-            // has a part of the ring to itself; before that, one after the other onto one area
+            // has a part of the ring to itself; before that, onto one area in rounds
             const bool over = seg->to == end - first;
             float *area = over ? reinterpret_cast<float *>(smem) : mo;
+            if (over) {
+                w.deposit(mm, area + warp * C::SLOTS * C::MS, warp, -1, lane);
+                asm volatile("bar.sync 1, %0;" :: "r"(NWC * 32) : "memory");
+            } else {
 #pragma unroll 1
-            for (int i = 0; i < NWC; ++i) {
-                if (warp == i) w.deposit(mm, area + (over ? i * C::SLOTS * C::MS : 0), warp, !over && i > 0, lane);
-                if (!over) asm volatile("bar.sync 1, %0;" :: "r"(NWC * 32) : "memory");
+                for (int i = 0; i < NWC; ++i) {
+                    w.deposit(mm, area, warp, i, lane);
+                    asm volatile("bar.sync 1, %0;" :: "r"(NWC * 32) : "memory");
+                }
             }
-            if (over) asm volatile("bar.sync 1, %0;" :: "r"(NWC * 32) : "memory");
             const int q = seg->seq, from = seg->from + first, stop = seg->to + first;
             const bool begins = from == cs[q], whole = begins && stop == cs[q + 1];
             const size_t part = ((size_t)(rank * 2 + (begins ? 1 : 0)) * a.units + unit) * C::SLOTS;
@@ -1005,11 +1054,11 @@ attn_paged_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     const float2 ml = mm[x * C::SLOTS + g];
                     if (ml.x != -INFINITY) sum = fmaf(ex2(ml.x - M), ml.y, sum);
                 }
-                float4 O = *reinterpret_cast<const float4 *>(area + g * C::MS + C::merge_at(d));
+                float4 O = C::merge_read(area + g * C::MS, d);
                 if (over) {
 #pragma unroll
                     for (int x = 1; x < NWC; ++x) {
-                        const float4 v = *reinterpret_cast<const float4 *>(area + (x * C::SLOTS + g) * C::MS + C::merge_at(d));
+                        const float4 v = C::merge_read(area + (x * C::SLOTS + g) * C::MS, d);
                         O.x += v.x; O.y += v.y; O.z += v.z; O.w += v.w;
                     }
                 }

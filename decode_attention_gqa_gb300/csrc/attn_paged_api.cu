@@ -102,6 +102,9 @@ void make_plan(const attn_paged_cache *c, int max_pages, int n_seq, int n_q, int
         int64_t P = slots / units;
         if (P * units * 20 < slots * 17) P = 4 * slots / units;
         if (P > tiles) P = tiles;
+        // a few tiles: one block a unit takes them in about the time that the second launch adds (a tile of 64
+        // rows 0.9 us, the launch 2.5), with less work for the host
+        if (tiles * tile <= 256) P = 1;
         pl.n_splits = (int)(P < 1 ? 1 : P > kMaxPagedSplits ? kMaxPagedSplits : P);
     }
     if (pl.n_splits > 1) {
