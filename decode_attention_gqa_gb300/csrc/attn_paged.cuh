@@ -132,7 +132,10 @@ struct PagedCfg {
     // Row stride of the merge area: 4 floats past a multiple of 32, so that the rows of a warp's slots (2u) lie 8
     // banks apart
     static constexpr int MS = HD + 4;
-    static constexpr uint32_t OFF_MO = 2 * NWC * SLOTS;           // floats, a multiple of 4
+    // Merge area (floats): the warps' (reference, sum) per slot, their merge, the accumulator rows
+    static constexpr uint32_t OFF_RES = 2 * NWC * SLOTS, OFF_MO = OFF_RES + 2 * SLOTS;
+    static constexpr int NPART = HD / 32;                         // 32-dimension parts of a row
+    static constexpr bool Q_EARLY = !(HD == 256 && SLOTS == 16);  // q of the next sequence is loaded before the merge (registers)
     static constexpr uint32_t MERGE_BYTES = (OFF_MO + SLOTS * MS) * 4;
     static constexpr uint32_t OFF_Q = S * STAGE_BYTES;            // Q fragments; then the merge area
     static constexpr uint32_t OFF_SLOT = OFF_Q + (Q_BYTES > MERGE_BYTES ? Q_BYTES : MERGE_BYTES);
@@ -156,21 +159,19 @@ struct PagedCfg {
     {
         return CHB == 128 ? (uint32_t)(r * 128 + ((r & 7) << 4)) : (uint32_t)(r * 64 + (((r >> 1) & 3) << 4));
     }
-    // Where four dimensions from d stand in a row of the merge area (8 bits: a lane holds neighbouring fours): the
-    // fours of eight lanes next to each other, so that they are written without bank conflicts.
-    static __device__ __forceinline__ int merge_at(int d)
+    // A row of the merge area holds 32-dimension parts; in a part, the fours of lanes g = 0..7 (two tiles of
+    // accumulators) stand next to each other, so that they are written without bank conflicts. Reads
+    // dimensions d .. d + 3: 8 bits, where a lane holds neighbours, one of the fours; 16 bits, where it holds
+    // every eighth, an element of four of them.
+    static __device__ __forceinline__ float4 merge_read(const float *row, int d)
     {
-        constexpr int LD = CW / 8;                                // dimensions of a lane in a chunk
-        return d / CW * CW + (d % LD / 4 * 8 + d % CW / LD) * 4;
-    }
-    // The same for one dimension and 16 bits, where a lane holds every eighth: its fours are dimensions
-    // 32 i + g + {0, 8, 16, 24}.
-    static __device__ __forceinline__ int merge_at16(int d) { return d / 32 * 32 + d % 8 * 4 + d % 32 / 8; }
-    static __device__ __forceinline__ float4 merge_read(const float *row, int d)   // dimensions d .. d + 3
-    {
-        if constexpr (E8) return *reinterpret_cast<const float4 *>(row + merge_at(d));
-        const float *p = row + merge_at16(d);
-        return make_float4(p[0], p[4], p[8], p[12]);
+        if constexpr (E8) {
+            constexpr int LD = CW / 8;                            // dimensions of a lane in a chunk
+            return *reinterpret_cast<const float4 *>(row + d / CW * CW + (d % LD / 4 * 8 + d % CW / LD) * 4);
+        } else {
+            const float *p = row + d / 32 * 32 + d % 8 * 4 + d % 32 / 8;
+            return make_float4(p[0], p[4], p[8], p[12]);
+        }
     }
     static __device__ __forceinline__ uint32_t unit(uint32_t base_row, int U)
     {
@@ -585,54 +586,84 @@ struct PagedWarp {
         }
     }
 
-    // The accumulators, scaled to the largest reference among the warps, into mo[slot * MS + d]; round -1: all of
-    // them; else the 32-dimension parts whose turn it is, so that each part is one warp's in a round, set in
-    // round 0 and added to in the others.
-    __device__ __forceinline__ void deposit(const float2 *mm, float *mo, int warp, int round, int lane)
+    // The accumulators times 2^(own reference - the largest among the warps).
+    __device__ __forceinline__ void weigh(const float2 *mm, int warp, int lane)
     {
-        const bool add = round > 0;
-        auto mine = [&](int part) { return round < 0 || (part + warp) % C::NWC == round; };
-        const int g = lane >> 2, u = lane & 3;
 #pragma unroll
         for (int k = 0; k < C::SPL; ++k)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int i = 2 * u + e + 8 * k;
+                const int i = 2 * (lane & 3) + e + 8 * k;
                 float M = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < C::NWC; ++w) M = fmaxf(M, mm[w * C::SLOTS + i].x);
                 const float x = mm[warp * C::SLOTS + i].x;
                 const float wt = x == -INFINITY ? 0.f : ex2(x - M);
-                float *row = mo + i * C::MS;
-                if constexpr (C::E8) {
-                    constexpr int TPC = C::CW / 16;
 #pragma unroll
-                    for (int c = 0; c < C::NCH; ++c)
+                for (int n = 0; n < C::HD / 16; ++n) {
+                    o[k][n][e] *= wt;
+                    o[k][n][2 + e] *= wt;
+                }
+            }
+    }
+
+    __device__ __forceinline__ float4 four(int k, int part, int e) const
+    {
+        return make_float4(o[k][2 * part][e], o[k][2 * part][2 + e], o[k][2 * part + 1][e], o[k][2 * part + 1][2 + e]);
+    }
+
+    // All of them into the warp's own area
+    __device__ __forceinline__ void spread(float *area, int lane) const
+    {
+        float *at = area + 2 * (lane & 3) * C::MS + 4 * (lane >> 2);
 #pragma unroll
-                        for (int j = 0; j < TPC; j += 2) {
-                            const int n = c * TPC + j;
-                            if (!mine(n / 2)) continue;
-                            float4 *p = reinterpret_cast<float4 *>(row + C::merge_at(c * C::CW + g * 2 * TPC + 2 * j));
-                            float4 v = add ? *p : make_float4(0.f, 0.f, 0.f, 0.f);
-                            v.x = fmaf(o[k][n][e], wt, v.x);
-                            v.y = fmaf(o[k][n][2 + e], wt, v.y);
-                            v.z = fmaf(o[k][n + 1][e], wt, v.z);
-                            v.w = fmaf(o[k][n + 1][2 + e], wt, v.w);
-                            *p = v;
-                        }
-                } else {
+        for (int k = 0; k < C::SPL; ++k)
 #pragma unroll
-                    for (int n = 0; n < C::HD / 16; n += 2) {
-                        if (!mine(n / 2)) continue;
-                        float4 *p = reinterpret_cast<float4 *>(row + 16 * n + 4 * g);
-                        float4 v = add ? *p : make_float4(0.f, 0.f, 0.f, 0.f);
-                        v.x = fmaf(o[k][n][e], wt, v.x);
-                        v.y = fmaf(o[k][n][2 + e], wt, v.y);
-                        v.z = fmaf(o[k][n + 1][e], wt, v.z);
-                        v.w = fmaf(o[k][n + 1][2 + e], wt, v.w);
-                        *p = v;
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int p = 0; p < C::NPART; ++p)
+                    *reinterpret_cast<float4 *>(at + (e + 8 * k) * C::MS + 32 * p) = four(k, p, e);
+    }
+
+    // All warps onto one area (zeroed): in round r warp w adds part (w + r) % NPART, so that no two meet. The
+    // registers are first turned by w parts, for their index to be r in every warp.
+    __device__ __forceinline__ void gather(float *area, int warp, int lane)
+    {
+#pragma unroll
+        for (int b = 1; b < C::NPART; b <<= 1) {
+            const bool on = (warp & b) != 0;
+#pragma unroll
+            for (int k = 0; k < C::SPL; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float x[C::NPART];
+#pragma unroll
+                        for (int p = 0; p < C::NPART; ++p) x[p] = o[k][2 * p + h][i];
+#pragma unroll
+                        for (int p = 0; p < C::NPART; ++p) o[k][2 * p + h][i] = on ? x[(p + b) % C::NPART] : x[p];
+                    }
+        }
+        float *at = area + 2 * (lane & 3) * C::MS + 4 * (lane >> 2);
+#pragma unroll 1
+        for (int grp = 0; grp * C::NPART < C::NWC; ++grp)          // more warps than parts: in groups
+#pragma unroll
+            for (int r = 0; r < C::NPART; ++r) {
+                if (warp / C::NPART == grp) {
+                    float *p = at + 32 * ((warp + r) & (C::NPART - 1));
+                    float4 v[2 * C::SPL];
+#pragma unroll
+                    for (int x = 0; x < 2 * C::SPL; ++x)
+                        v[x] = *reinterpret_cast<const float4 *>(p + ((x & 1) + 8 * (x >> 1)) * C::MS);
+#pragma unroll
+                    for (int x = 0; x < 2 * C::SPL; ++x) {
+                        const float4 y = four(x >> 1, r, x & 1);
+                        v[x].x += y.x; v[x].y += y.y; v[x].z += y.z; v[x].w += y.w;
+                        *reinterpret_cast<float4 *>(p + ((x & 1) + 8 * (x >> 1)) * C::MS) = v[x];
                     }
                 }
+                asm volatile("bar.sync 1, %0;" :: "r"(C::NWC * 32) : "memory");
             }
     }
 };
@@ -640,28 +671,38 @@ struct PagedWarp {
 // Q of the block's slots as MMA A fragments in shared memory: NP parts, each the rounding of what the
 // ones before leave of q sc, with a power of two sc per slot (exact). Slots past the last are zero.
 template <class C>
-__device__ __forceinline__ void paged_prepare_q(uint8_t *smem, const PagedArgs &a, const SlotRows &sr, int s, int hk, int qg,
-                                                int tid)
+struct PagedQ {
+    static constexpr int NW = C::NWC;                            // the compute warps
+    static constexpr int V4 = C::HD <= 128 ? 1 : 2;              // float4 of a row a lane owns
+    static constexpr int ITER = (C::SLOTS + NW - 1) / NW;
+    float4 x[ITER][V4];
+
+    __device__ __forceinline__ void load(const PagedArgs &a, int s, int hk, int qg, int tid)
+    {
+        const int warp = tid >> 5, lane = tid & 31;
+#pragma unroll
+        for (int it = 0; it < ITER; ++it) {
+            const int i = warp + it * NW, qh = qg * C::SLOTS + i;
+            const bool have = i < C::SLOTS && qh < a.n_q * a.group;
+            const int t = have ? div(a.by_group, qh) : 0, g = have ? qh - t * a.group : 0;
+            const float *row = a.q + (((size_t)s * a.n_q + t) * a.n_head + (size_t)hk * a.group + g) * C::HD;
+#pragma unroll
+            for (int v = 0; v < V4; ++v) {
+                x[it][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (have && lane * 4 < C::HD) x[it][v] = ld_dep(reinterpret_cast<const float4 *>(row + v * 128) + lane);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(uint8_t *smem, const PagedArgs &a, const SlotRows &sr, int hk, int qg, int tid);
+};
+
+template <class C>
+__device__ __forceinline__ void PagedQ<C>::store(uint8_t *smem, const PagedArgs &a, const SlotRows &sr, int hk, int qg,
+                                                 int tid)
 {
     using MT = typename C::MT;
     const int warp = tid >> 5, lane = tid & 31;
-    constexpr int NW = C::NWC;                                   // the compute warps
-    constexpr int V4 = C::HD <= 128 ? 1 : 2;                     // float4 of a row a lane owns
-    constexpr int ITER = (C::SLOTS + NW - 1) / NW;
     const bool active = lane * 4 < C::HD;
-    float4 x[ITER][V4];
-#pragma unroll
-    for (int it = 0; it < ITER; ++it) {
-        const int i = warp + it * NW, qh = qg * C::SLOTS + i;
-        const bool have = i < C::SLOTS && qh < a.n_q * a.group;
-        const int t = have ? div(a.by_group, qh) : 0, g = have ? qh - t * a.group : 0;
-        const float *row = a.q + (((size_t)s * a.n_q + t) * a.n_head + (size_t)hk * a.group + g) * C::HD;
-#pragma unroll
-        for (int v = 0; v < V4; ++v) {
-            x[it][v] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (have && active) x[it][v] = ld_dep(reinterpret_cast<const float4 *>(row + v * 128) + lane);
-        }
-    }
 #pragma unroll
     for (int it = 0; it < ITER; ++it) {
         const int i = warp + it * NW;
@@ -907,7 +948,7 @@ attn_paged_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         desc[lane] = SliceInfo{(unsigned)p0 < (unsigned)a.n_pages ? p0 : -1, z0, 1.f, 1.f};
         const float2 f0 = load_scales(p0);
         __syncwarp();
-        const int early = min(C::WPT, ntiles);                  // what the compute warps start with; the rest below
+        const int early = min(1, ntiles);                      // the rest when the descriptors are complete
         if (lane == 0)
             for (int t = 0; t < early; ++t) issue(t);
         locate(1);
@@ -976,14 +1017,18 @@ attn_paged_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         }
         const uint32_t smem_u = smem_u32(smem);
         float2 *mm = reinterpret_cast<float2 *>(smem + C::OFF_Q);
+        float2 *res = reinterpret_cast<float2 *>(reinterpret_cast<float *>(smem + C::OFF_Q) + C::OFF_RES);
         float *mo = reinterpret_cast<float *>(smem + C::OFF_Q) + C::OFF_MO;
         bool begun = false;
+        PagedQ<C> q;
+        if (first < end && C::Q_EARLY) q.load(a, find_seq(cs, a.n_seq, first), hk, qg, tid);
         for (int at = first; at < end;) {
             {
                 const int s = find_seq(cs, a.n_seq, at);
                 const SlotRows sr = seq_rows(a, snkv[s], sstart[s]);
                 const int t0 = div(a.by_group, qg * C::SLOTS), t1 = div(a.by_group, qg * C::SLOTS + nslots() - 1);
-                paged_prepare_q<C>(smem, a, sr, s, hk, qg, tid);
+                if (!C::Q_EARLY) q.load(a, s, hk, qg, tid);
+                q.store(smem, a, sr, hk, qg, tid);
                 if (tid == 0) {
                     seg->seen_lo = sr.low(t1);
                     seg->seen_hi = sr.last(t0);
@@ -1021,39 +1066,45 @@ attn_paged_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty + st);
             }
-            // merge the warps' states: over the Q fragments, which are no longer read
+            // The next sequence's q is on its way while the warps' states are merged, over the Q fragments, which
+            // are no longer read. At the block's last sequence every tile has been consumed and none is on its
+            // way, so that each warp has a part of the ring to itself; before that, onto one area in rounds.
+            const int from = seg->from + first, stop = seg->to + first;
+            if (C::Q_EARLY && stop < end) q.load(a, find_seq(cs, a.n_seq, stop), hk, qg, tid);
+            const bool over = stop == end;
+            float *area = over ? reinterpret_cast<float *>(smem) : mo;
             asm volatile("bar.sync 1, %0;" :: "r"(NWC * 32) : "memory");
             w.publish(mm + warp * C::SLOTS, lane);
+            if (!over)
+                for (int i = tid; i < C::SLOTS * C::MS / 4; i += NWC * 32)
+                    reinterpret_cast<float4 *>(mo)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             asm volatile("bar.sync 1, %0;" :: "r"(NWC * 32) : "memory");
-            // the block's last sequence: every tile has been consumed and none is on its way, so that each warp
-            // has a part of the ring to itself; before that, onto one area in rounds
-            const bool over = seg->to == end - first;
-            float *area = over ? reinterpret_cast<float *>(smem) : mo;
+            if (tid < C::SLOTS) {                        // (reference, sum) of the block
+                float M = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int x = 0; x < NWC; ++x) M = fmaxf(M, mm[x * C::SLOTS + tid].x);
+#pragma unroll
+                for (int x = 0; x < NWC; ++x) {
+                    const float2 ml = mm[x * C::SLOTS + tid];
+                    if (ml.x != -INFINITY) sum = fmaf(ex2(ml.x - M), ml.y, sum);
+                }
+                res[tid] = make_float2(M, sum);
+            }
+            w.weigh(mm, warp, lane);
             if (over) {
-                w.deposit(mm, area + warp * C::SLOTS * C::MS, warp, -1, lane);
+                w.spread(area + warp * C::SLOTS * C::MS, lane);
                 asm volatile("bar.sync 1, %0;" :: "r"(NWC * 32) : "memory");
             } else {
-#pragma unroll 1
-                for (int i = 0; i < NWC; ++i) {
-                    w.deposit(mm, area, warp, i, lane);
-                    asm volatile("bar.sync 1, %0;" :: "r"(NWC * 32) : "memory");
-                }
+                w.gather(area, warp, lane);
             }
-            const int q = seg->seq, from = seg->from + first, stop = seg->to + first;
-            const bool begins = from == cs[q], whole = begins && stop == cs[q + 1];
+            const int sq = seg->seq;
+            const bool begins = from == cs[sq], whole = begins && stop == cs[sq + 1];
             const size_t part = ((size_t)(rank * 2 + (begins ? 1 : 0)) * a.units + unit) * C::SLOTS;
             const bool bad = flags[0] != 0;              // left unwritten; the error word says why
             constexpr int D4 = C::HD / 4;
             for (int i = tid; i < nslots() * D4 && !bad; i += NWC * 32) {
                 const int g = i / D4, d = (i % D4) * 4;
-                float M = -INFINITY, sum = 0.f;
-#pragma unroll
-                for (int x = 0; x < NWC; ++x) M = fmaxf(M, mm[x * C::SLOTS + g].x);
-#pragma unroll
-                for (int x = 0; x < NWC; ++x) {
-                    const float2 ml = mm[x * C::SLOTS + g];
-                    if (ml.x != -INFINITY) sum = fmaf(ex2(ml.x - M), ml.y, sum);
-                }
+                const float2 ml = res[g];
                 float4 O = C::merge_read(area + g * C::MS, d);
                 if (over) {
 #pragma unroll
@@ -1063,12 +1114,12 @@ attn_paged_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     }
                 }
                 if (whole) {
-                    if (sum == 0.f) O = make_float4(0.f, 0.f, 0.f, 0.f);
-                    else { O.x /= sum; O.y /= sum; O.z /= sum; O.w /= sum; }
-                    *reinterpret_cast<float4 *>(a.out + head_row(q, g) * C::HD + d) = O;
+                    const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
+                    *reinterpret_cast<float4 *>(a.out + head_row(sq, g) * C::HD + d) =
+                        make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
                 } else {
                     *reinterpret_cast<float4 *>(a.ws_o + (part + g) * C::HD + d) = O;
-                    if (d == 0) a.ws_ml[part + g] = make_float2(M, sum);
+                    if (d == 0) a.ws_ml[part + g] = ml;
                 }
             }
             at = stop;
