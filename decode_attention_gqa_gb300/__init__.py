@@ -477,7 +477,9 @@ class PagedCache:
             raise TypeError("k and v must both be float16, bfloat16 or float8_e4m3fn")
         if k.dim() != 4 or k.shape != v.shape:
             raise ValueError("k and v must be [n_pages, page_size, n_kv_head, head_dim]")
-        if k.stride() != v.stride() or k.stride(3) != 1:
+        # a dimension of one element has no stride
+        strides, vstrides = ([t.stride(i) if t.shape[i] > 1 else t.shape[3] for i in range(3)] for t in (k, v))
+        if strides != vstrides or k.stride(3) != 1 or v.stride(3) != 1:
             raise ValueError("k and v must have the same strides, and dense rows")
         if v.device != k.device:
             raise ValueError("k and v must be on the same device")
@@ -495,7 +497,7 @@ class PagedCache:
         self.n_kv_head, self.head_dim, self.page_size = n_kv_head, head_dim, page_size
         self.device = k.device
         self._c = _CacheStruct(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale),
-                               k.stride(0), k.stride(1), k.stride(2), n_pages, page_size, n_kv_head,
+                               *strides, n_pages, page_size, n_kv_head,
                                head_dim, types[k.dtype], 0)
         self._address = ctypes.addressof(self._c)
         self._index = k.get_device()
@@ -548,7 +550,8 @@ def rope_append(cache, block_table, positions, k_new, v_new, q=None, q_out=None,
     type (float32, float16 or bfloat16), dense within a token and of any stride between tokens;
     block_table int32 [n_seq, max_pages]; positions int32 [n_seq]; cu_tokens int32 [n_seq + 1], or
     None for the same number of tokens in every sequence. `q_out` (float32) is allocated when not
-    given. Returns q_out (None without q)."""
+    given (on the current stream, so another `stream` needs it given). Returns q_out (None without
+    q)."""
     torch = _torch or _torch_module()
     i32, index, dt, hd = torch.int32, cache._index, k_new.dtype, cache.head_dim
     in_type = _in_type(dt)
@@ -578,6 +581,8 @@ def rope_append(cache, block_table, positions, k_new, v_new, q=None, q_out=None,
                     ((False, "q must be [n_tokens, n_head, head_dim], dense within a token"),))
         n_head, qs = qshape[1], qst[0]
         if q_out is None:
+            if stream is not None and _stream(stream) != _current_stream(index):
+                raise ValueError("q_out must be given with a stream that is not the current one")
             q_out = torch.empty(qshape, dtype=torch.float32, device=cache.device)
         elif not (q_out.shape == qshape and q_out.dtype is torch.float32 and q_out.get_device() == index and
                   q_out.is_contiguous()):
@@ -663,6 +668,8 @@ def paged_decode_attention(cache, block_table, positions, q, scale=None, out=Non
     key = (max_pages, n_seq, n_q, n_head, window, n_splits)
     plan = cache._plans.get(key)
     if plan is None:
+        if not (0 <= window < 1 << 31 and 0 <= n_splits < 1 << 31):
+            raise ValueError("window and n_splits must be non-negative 32-bit integers")
         if len(cache._plans) >= 4096:
             cache._plans.clear()
         plan = cache._plans[key] = attn_paged_plan(cache, max_pages, n_seq, n_q, n_head, window, n_splits)

@@ -140,7 +140,7 @@ struct PagedCfg {
     static constexpr uint32_t OFF_Q = S * STAGE_BYTES;            // Q fragments; then the merge area
     static constexpr uint32_t OFF_SLOT = OFF_Q + (Q_BYTES > MERGE_BYTES ? Q_BYTES : MERGE_BYTES);
     static constexpr uint32_t OFF_SEG = OFF_SLOT + SLOTS * 16;    // SegInfo
-    static constexpr uint32_t OFF_DESC = OFF_SEG + 32;            // SliceInfo[4][32]
+    static constexpr uint32_t OFF_DESC = OFF_SEG + 48;            // SliceInfo[4][32]
     static constexpr uint32_t OFF_BAR = OFF_DESC + 4 * 32 * 16;
     static constexpr uint32_t OFF_SEQ = OFF_BAR + 2 * S * 8 + 16;
     static constexpr uint32_t SMEM_BYTES = OFF_SEQ + (3 * kPagedSeqs + 1) * 4;
@@ -195,9 +195,10 @@ struct __align__(16) SlotInfo {   // of one (query row, head) slot of the block,
 struct __align__(16) SegInfo {    // the sequence at hand
     int seen_lo, seen_hi; // rows every slot of the block sees
     int any_lo, any_hi;   // rows some slot sees
-    int row0;             // first row of the block's tile 0, were it this sequence's
+    int row0, tile0;      // first row of its first tile; that tile, counted from the block's first
     int seq, from, to;    // the sequence, and its tiles of this block
 };
+static_assert(sizeof(SegInfo) <= 48, "its place in shared memory");
 
 // The rows the slots of query rows [t0, t1] see, as [first row of t0, last row of t1]
 struct SlotRows {
@@ -1034,7 +1035,8 @@ attn_paged_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     seg->seen_hi = sr.last(t0);
                     seg->any_lo = sr.low(t0);
                     seg->any_hi = sr.last(t1);
-                    seg->row0 = seq_extent<TILE>(a, sr).x + (first - cs[s]) * TILE;
+                    seg->row0 = seq_extent<TILE>(a, sr).x;
+                    seg->tile0 = cs[s] - first;
                     seg->seq = s;
                     seg->from = at - first;
                     seg->to = min(end, cs[s + 1]) - first;
@@ -1057,7 +1059,7 @@ attn_paged_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     if (lane == 0) { flags[0] = 1; atomicOr(a.err, kErrPipelineTimeout); }
                     break;
                 }
-                const int row0 = seg->row0 + t * TILE + warp % NSL * WR;
+                const int row0 = seg->row0 + (t - seg->tile0) * TILE + warp % NSL * WR;
                 const int4 sg = PagedWarp<C, RULES>::seg_rows(smem_u);
                 const uint4 f = lds128(smem_u + C::OFF_DESC + ((t / TPG & 3) * 32 + t % TPG * NSL + warp % NSL) * 16);
                 if ((int)f.x >= 0 && row0 <= sg.w && row0 + WR > sg.z)

@@ -270,7 +270,9 @@ attn_status attn_decode_paged(const attn_paged_cache *cache, const int32_t *bloc
         return ATTN_ERR_INVALID_ARG;
     const float softcap = rules ? rules->softcap : 0.f;
     const int window = rules ? rules->window : 0;
-    if (!std::isfinite(softcap) || softcap < 0.f) return ATTN_ERR_INVALID_ARG;
+    if (!(softcap == 0.f || (softcap >= 0x1p-40f && softcap <= 0x1p40f))) return ATTN_ERR_INVALID_ARG;
+    const float qscale = softcap > 0.f ? (float)((double)scale / softcap) : (float)((double)scale * 1.4426950408889634);
+    if (!std::isfinite(qscale)) return ATTN_ERR_INVALID_ARG;
     if (rules && (!aligned(rules->slopes, 4) || !aligned(rules->starts, 4))) return ATTN_ERR_INVALID_ARG;
     if (!aligned(workspace, 256)) return ATTN_ERR_INVALID_ARG;
     Strides cs;
@@ -328,7 +330,7 @@ attn_status attn_decode_paged(const attn_paged_cache *cache, const int32_t *bloc
     a.box_rows = cache->page_size % 64 == 0 && tile >= 64 ? 64 : cache->page_size % 32 == 0 && tile >= 32 ? 32 : 16;
     a.by_page = attn::fast_div((unsigned)cache->page_size);
     a.by_group = attn::fast_div((unsigned)a.group);
-    a.qscale = softcap > 0.f ? (float)((double)scale / softcap) : (float)((double)scale * 1.4426950408889634);
+    a.qscale = qscale;
     a.cap_log2 = (float)((double)softcap * 1.4426950408889634);
     r.k = cache->k;
     r.v = cache->v;
@@ -346,9 +348,9 @@ attn_status attn_decode_paged(const attn_paged_cache *cache, const int32_t *bloc
         {attn::launch_paged_hd128_f16, attn::launch_paged_hd128_bf16, attn::launch_paged_hd128_e4m3},
         {attn::launch_paged_hd256_f16, attn::launch_paged_hd256_bf16, attn::launch_paged_hd256_e4m3}};
     const int hi = cache->head_dim == 64 ? 0 : cache->head_dim == 128 ? 1 : 2;
-    // tiles are counted in 32 bits: fewer sequences a launch where the capacity is huge
+    // tiles are counted in 32 bits, some groups past the last: fewer sequences a launch where the capacity is huge
     const int64_t per_seq = (a.cap + (int64_t)tile - 1) / tile + 1;
-    const int batch = (int)(0x7fffffff / per_seq < attn::kPagedSeqs ? 0x7fffffff / per_seq : attn::kPagedSeqs);
+    const int batch = (int)(0x7fff0000 / per_seq < attn::kPagedSeqs ? 0x7fff0000 / per_seq : attn::kPagedSeqs);
     for (int s0 = 0; s0 < n_seq; s0 += batch) {
         const size_t rows = (size_t)s0 * n_q * n_head * cache->head_dim;
         a.n_seq = n_seq - s0 < batch ? n_seq - s0 : batch;

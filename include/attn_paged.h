@@ -6,11 +6,12 @@
  * and windowed.
  *
  * The conventions of attn_decode.h hold: device pointers are caller-owned and
- * 16-byte aligned (int32 arrays, scales and slopes 4-byte aligned), argument errors come back synchronously before anything is
- * launched, nothing synchronises the stream, data-dependent errors set a bit
- * of the sticky device error word (attn_read_device_error), and every launch
- * can be captured in a CUDA graph and replayed while positions, tables and
- * contents change. Calls run on the current device.
+ * 16-byte aligned (int32 arrays, scales and slopes 4-byte aligned), argument
+ * errors come back synchronously before anything is launched, nothing
+ * synchronises the stream, data-dependent errors set a bit of the sticky
+ * device error word (attn_read_device_error), and every launch can be captured
+ * in a CUDA graph and replayed while positions, tables and contents change.
+ * Calls run on the current device.
  *
  * Paged cache. The rows of a sequence live in pages of page_size rows taken
  * from a pool of n_pages pages. Row j of sequence s is row j % page_size of
@@ -22,7 +23,8 @@
  *
  * Rows at or past positions[s] + 1 are never used and never change a result,
  * whatever they hold; the page that holds row positions[s] may be read to its
- * end.
+ * end. Rows that are seen are taken to hold finite values: NaN gives NaN, an
+ * infinity among them infinity or NaN.
  */
 #ifndef ATTN_PAGED_H
 #define ATTN_PAGED_H
@@ -140,7 +142,8 @@ attn_status attn_rope_steps(int rot_dim, double base, int scaling, double factor
  * it grows (exact but for values that fall below 2^-6 s). The first row of a page starts its
  * scale afresh. Infinite elements take the largest code, NaN stays NaN, and
  * neither counts for the scale.
- * Each page may be written by one sequence of the call only. A token whose
+ * Each page may be written by one sequence of the call only, and stand at one
+ * place of its table (what a page written twice holds is not defined). A token whose
  * position lies outside [0, max_pages * page_size) is not written and sets
  * ATTN_DEVERR_POSITION_CLAMPED, except that positions[s] == -1 marks an idle
  * sequence; its q is rotated all the same.
@@ -153,7 +156,7 @@ attn_status attn_rope_append(const attn_paged_cache *cache, const int32_t *block
 
 /*
  * What happens to a score between the product and the softmax, in this order:
- *   softcap  > 0: score = softcap * tanh(score / softcap); 0: none
+ *   softcap  2^-40 .. 2^40: score = softcap * tanh(score / softcap); 0: none
  *   slopes   device, float [n_head], or NULL: score -= slopes[h] * (position of the
  *            query - j) for cache row j
  *   window   > 0: rows j <= position of the query - window are masked; 0: none
@@ -189,9 +192,9 @@ typedef struct {
  *                aligned; NULL: the library-owned buffer (see attn_decode: one
  *                stream at a time, no growth while capturing, and graphs that
  *                may run at once need workspaces of their own).
- * q and the softmax weights are carried in two 16-bit parts each, sums in 32
- * bits, so that the result has the accuracy of 32-bit arithmetic on the values
- * the cache stands for.
+ * q and the softmax weights are carried in 16-bit parts (two of binary16, 22
+ * bits, or three of bfloat16, 24), sums in 32 bits, so that the result has about
+ * the accuracy of 32-bit arithmetic on the values the cache stands for.
  */
 attn_status attn_decode_paged(const attn_paged_cache *cache, const int32_t *block_table, int max_pages,
                               const int32_t *positions, const float *q, float *out, int n_seq, int n_q,
@@ -199,9 +202,9 @@ attn_status attn_decode_paged(const attn_paged_cache *cache, const int32_t *bloc
                               void *workspace, size_t workspace_bytes, attn_stream_t stream);
 
 /*
- * attn_paged_plan -- host-only: the split count and the workspace bytes (0 for one block)
- * of an attn_decode_paged call with these arguments; only the shape fields of
- * the cache are looked at. n_splits as in the call, window as in its rules (0:
+ * attn_paged_plan -- host-only: n_splits and the workspace bytes (0 for one
+ * split) of an attn_decode_paged call with these arguments; only the shape
+ * fields of the cache are looked at. n_splits as in the call, window as in its rules (0:
  * none). sm_count <= 0 asks the current device. Either output may be NULL.
  */
 attn_status attn_paged_plan(const attn_paged_cache *cache, int max_pages, int n_seq, int n_q, int n_head,

@@ -15,7 +15,7 @@ from harness import ABS_TOL, REL_TOL
 
 pytestmark = pytest.mark.gpu
 
-EPS_PAIR = {"f16": 2.0 ** -22, "bf16": 2.0 ** -16, "e4m3": 2.0 ** -22}
+EPS_PAIR = {"f16": 2.0 ** -22, "bf16": 2.0 ** -24, "e4m3": 2.0 ** -22}    # two or three parts of q and p
 
 
 @pytest.fixture(scope="module")
@@ -367,6 +367,80 @@ def test_same_bits_again_and_from_any_workspace(pkg):
     assert e.value.status == pkg.ATTN_ERR_WORKSPACE
 
 
+def test_pages_that_sequences_share(pkg):
+    """A prefix that several sequences have in common, held once; one page twice in a sequence."""
+    for kv in ("e4m3", "bf16"):
+        pool = Pool(13, kv, 2, 128, 16, (200, 150, 90, 64))
+        pool.table[1, :4] = pool.table[0, :4]
+        pool.table[2, :5] = pool.table[0, :5]
+        pool.table[3, :4] = pool.table[3, 0]
+        attend_check(pkg, pool, 1, 8, splits=(0, 1, 4))
+        attend_check(pkg, pool, 4, 4, splits=(0,))
+    assert pkg.attn_read_device_error() == 0
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "f16"])
+def test_many_query_rows_and_the_largest_pages(pkg, kv):
+    pool = Pool(14, kv, 1, 64, 1024, (1500, 1030, 700))
+    attend_check(pkg, pool, 1024, 2, splits=(0,), window=300)
+    attend_check(pkg, pool, 1024, 1, splits=(0, 3))
+    assert pkg.attn_read_device_error() == 0
+
+
+def test_a_query_row_of_nan_stays_alone(pkg):
+    import torch
+    pool = Pool(15, "e4m3", 2, 128, 32, (300, 40))
+    cache, table, pos = pool.cache(pkg), tt(pool.table), tt(np.int32([299, 39]))
+    for n_q, n_head in ((1, 8), (3, 12)):
+        q = tt(np.random.default_rng(3).standard_normal((2, n_q, n_head, 128)).astype(np.float32))
+        want = pkg.paged_decode_attention(cache, table, pos, q)
+        q[0, 0, 1] = math.nan
+        q[1, n_q - 1, n_head - 1, 5] = math.nan
+        got = pkg.paged_decode_attention(cache, table, pos, q)
+        bad = torch.zeros(2, n_q, n_head, dtype=torch.bool, device="cuda")
+        bad[0, 0, 1] = bad[1, n_q - 1, n_head - 1] = True
+        assert bool(got[bad].isnan().all())
+        assert torch.equal(got[~bad], want[~bad])
+
+
+def test_one_kv_head_and_one_page_with_strides_of_no_meaning(pkg):
+    import torch
+    pool = Pool(16, "f16", 1, 64, 48, (40,), spare=0)
+    for i in range(2):
+        pool.dev[i] = torch.as_strided(pool.dev[i], (1, 48, 1, 64), (1, 64, 7, 1))
+    attend_check(pkg, pool, 1, 4)
+    k = torch.ones(1, 1, 64, device="cuda")
+    pkg.rope_append(pool.cache(pkg), tt(pool.table), tt(np.int32([39])), k, k)
+    assert bool((pool.dev[1][0, 39] == 1).all()) and pkg.attn_read_device_error() == 0
+
+
+def test_numbers_past_32_bits_are_refused(pkg):
+    pool = Pool(18, "f16", 1, 64, 16, (40,))
+    for bad in (dict(window=1 << 31), dict(window=(1 << 32) + 5), dict(n_splits=1 << 32), dict(n_splits=-1)):
+        with pytest.raises(ValueError):
+            pkg.paged_decode_attention(pool.cache(pkg), tt(pool.table), tt(np.int32([39])),
+                                       tt(np.zeros((1, 2, 64), np.float32)), **bad)
+
+
+def test_calls_on_several_streams_at_once(pkg):
+    """Eager calls of different shapes, interleaved on streams, each with the workspace torch gives it."""
+    import torch
+    jobs = []
+    for i, (kv, ctx) in enumerate((("e4m3", (3000, 5)), ("f16", (900, 900)), ("bf16", (2048,)))):
+        pool = Pool(40 + i, kv, 2, 128, 64, ctx)
+        cache, table, pos = pool.cache(pkg), tt(pool.table), tt(np.int32([c - 1 for c in ctx]))
+        q = tt(np.random.default_rng(i).standard_normal((len(ctx), 8, 128)).astype(np.float32))
+        jobs.append((cache, table, pos, q, pkg.paged_decode_attention(cache, table, pos, q), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(20):
+        for cache, table, pos, q, want, stream in jobs:
+            with torch.cuda.stream(stream):
+                outs.append((pkg.paged_decode_attention(cache, table, pos, q), want))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in outs)
+
+
 # ---------------------------------------------------------------------------
 # Append.
 # ---------------------------------------------------------------------------
@@ -567,6 +641,62 @@ def test_append_infinities_and_nan(pkg):
     rest = np.ones((2, 64), bool)
     rest[0, 3] = rest[0, 4] = rest[1, 5] = False
     assert (got[rest] == 1.0).all()
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "f16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_at_addresses_of_16_bytes(pkg, kv, interleaved):
+    """Tensors and a pool that start 16 bytes past a multiple of 32 give what aligned ones give."""
+    import torch
+    rng = np.random.default_rng(8)
+    dt, es = (torch.uint8, 1) if kv == "e4m3" else (torch.float16, 2)
+
+    def shifted(x):
+        n, by = x.numel(), 16 // x.element_size()
+        base = torch.zeros(n + 2 * by, dtype=x.dtype, device="cuda")
+        out = base[by:by + n].view(x.shape)
+        out.copy_(x)
+        assert out.data_ptr() % 32 == 16
+        return out
+
+    x = [tt(rng.standard_normal((5, h, 128)).astype(np.float32)) for h in (4, 2, 2)]
+    table, pos, cu = tt(np.int32([[1, 0], [2, 3]])), tt(np.int32([17, 1])), tt(np.int32([0, 3, 5]))
+    rope, got = pkg.Rope(96, interleaved=interleaved), []
+    for place in (lambda t: t, shifted):
+        pools = [place(torch.zeros(4, 16, 2, 128, dtype=dt, device="cuda")) for _ in range(2)]
+        scales = [torch.zeros(4, 2, device="cuda") if es == 1 else None for _ in range(2)]
+        view = [p.view(torch.float8_e4m3fn) if es == 1 else p for p in pools]
+        q_out = place(torch.zeros(5, 4, 128, device="cuda"))
+        cache = pkg.PagedCache(view[0], view[1], scales[0], scales[1])
+        pkg.rope_append(cache, table, pos, place(x[1]), place(x[2]), q=place(x[0]), q_out=q_out, rope=rope, cu_tokens=cu)
+        got.append([q_out] + pools + [s for s in scales if s is not None] +
+                   [pkg.paged_decode_attention(cache, table, pos, place(torch.ones(2, 4, 128, device="cuda")))])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert pkg.attn_read_device_error() == 0
+
+
+def test_append_nothing_and_in_place(pkg):
+    import torch
+    pool = Pool(17, "e4m3", 2, 64, 16, (20, 3))
+    cache, table, pos = pool.cache(pkg), tt(pool.table), tt(np.int32([19, 2]))
+    before = [d.view(torch.uint8).clone() for d in pool.dev]
+    none = torch.zeros(0, 2, 64, device="cuda")
+    out = pkg.rope_append(cache, table, pos, none, none, q=torch.zeros(0, 4, 64, device="cuda"), rope=pkg.Rope(64),
+                          cu_tokens=torch.zeros(3, dtype=torch.int32, device="cuda"))
+    assert out.shape == (0, 4, 64)
+    # a padded batch without a token: everything lies behind the last sequence
+    pad = torch.ones(4, 2, 64, device="cuda")
+    pkg.rope_append(cache, table, pos, pad, pad, cu_tokens=torch.zeros(3, dtype=torch.int32, device="cuda"))
+    assert all(torch.equal(d.view(torch.uint8), b) for d, b in zip(pool.dev, before))
+    # q turned where it is
+    q = tt(np.random.default_rng(1).standard_normal((2, 4, 64)).astype(np.float32))
+    k = torch.ones(2, 2, 64, device="cuda")
+    want = pkg.rope_append(cache, table, pos, k, k, q=q, rope=pkg.Rope(64))
+    same = pkg.rope_append(cache, table, pos, k, k, q=q, q_out=q, rope=pkg.Rope(64))
+    assert same is q and torch.equal(q, want)
+    with pytest.raises(ValueError):                          # q_out would be allocated on another stream
+        pkg.rope_append(cache, table, pos, k, k, q=q, stream=torch.cuda.Stream())
+    assert pkg.attn_read_device_error() == 0
 
 
 # ---------------------------------------------------------------------------

@@ -82,8 +82,10 @@ def test_attention_refuses_wrong_arguments(lib):
                dict(scale=math.nan), dict(scale=math.inf), dict(P=-1), dict(P=5000), dict(ws=128)):
         assert _attend(lib, **kw) == INVALID, kw
     assert _attend(lib, n_head=130) == UNSUPPORTED                      # 65 query heads a KV head
+    assert _attend(lib, scale=3e38) == INVALID                          # past 32 bits with log2 e
+    assert _attend(lib, scale=1e30, rules=pkg._RulesStruct(1e-10, 0, 0, 0)) == INVALID
     for r in ((-1.0, 0, 0, 0), (math.nan, 0, 0, 0), (math.inf, 0, 0, 0), (0.0, -1, 0, 0), (0.0, 0, 2, 0),
-              (0.0, 0, 0, 3)):
+              (0.0, 0, 0, 3), (1e-20, 0, 0, 0), (1e30, 0, 0, 0)):
         assert _attend(lib, rules=pkg._RulesStruct(*r)) == INVALID, r
     assert _attend(lib, n_seq=0, table=None, pos=None, q=None, out=None) == OK
 
@@ -239,3 +241,32 @@ def test_reference_codes():
     for a in (1.0, 447.9, 448.0, 448.1, 3e-5, 1e30, 0.0):
         s = ref.scale_for(a)
         assert (a <= 448 * s or s == 2.0 ** 60) and (a > 224 * s or s == 2.0 ** -60)
+
+
+def test_the_header_is_plain_c(tmp_path):
+    import os
+    import subprocess
+    src = tmp_path / "t.c"
+    src.write_text("#include \"attn_paged.h\"\nint main(void) { attn_paged_cache c = {0}; attn_rope r = {0};\n"
+                   "attn_score_rules s = {0}; return (int)(sizeof c + sizeof r + sizeof s) == 0; }\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-I", os.path.join(root, "include"), "-c", str(src),
+                    "-o", str(tmp_path / "t.o")], check=True)
+    # the binding's structures have the header's sizes
+    probe = tmp_path / "p.c"
+    probe.write_text("#include <stdio.h>\n#include \"attn_paged.h\"\nint main(void) { printf(\"%zu %zu %zu\\n\", "
+                     "sizeof(attn_paged_cache), sizeof(attn_rope), sizeof(attn_score_rules)); return 0; }\n")
+    subprocess.run(["gcc", "-I", os.path.join(root, "include"), str(probe), "-o", str(tmp_path / "p")], check=True)
+    sizes = [int(x) for x in subprocess.run([str(tmp_path / "p")], capture_output=True, text=True).stdout.split()]
+    assert sizes == [ctypes.sizeof(x) for x in (pkg._CacheStruct, pkg._RopeStruct, pkg._RulesStruct)]
+
+
+def test_paged_constants_match_the_header():
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "include", "attn_paged.h")).read()
+    found = re.findall(r"^#define (ATTN_(?:TYPE|ROPE|DEVERR)_\w+)\s+(0x[0-9a-fA-F]+|\d+)u?\b", text, flags=re.M)
+    assert len(found) == 9
+    for name, val in found:
+        assert getattr(pkg, name) == int(val, 0), name
