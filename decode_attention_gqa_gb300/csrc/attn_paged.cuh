@@ -1,35 +1,48 @@
-// attn_paged.cuh -- the split partial kernel over a paged cache.
+// attn_paged.cuh -- decode attention over a paged cache: the streaming kernel and
+// the merge of the parts it leaves.
 //
 // Mathematics. For a (query row, head) slot at position x over the cache rows j it sees,
 //     s_j = rules(scale q.k_j),  o = sum_j p_j v_j / sum_j p_j,  p_j = 2^(s_j log2 e - m),
-// one pass with a running reference m; a split stores (m, sum p, sum p v) and
-// attn_combine merges the splits (with one split the block writes o itself).
-// An e4m3 cache holds codes with one scale per page and KV head: q.k_j is the
-// product with the codes times the page's K scale, one multiplication per
-// score, and the V scale multiplies p before P.V. The running reference follows
-// s + log2 of the V scale (rounded up), so that p times the scale stays in
-// the 16-bit range whatever the scales are; sum p stays in f32.
+// one pass with a running reference m that moves when a score passes it by 8. An e4m3
+// cache holds codes with one scale per page and KV head: q.k_j is the product with the
+// codes times the page's K scale, one multiplication a score, and the V scale multiplies
+// p before P.V. The reference follows s + log2 of the V scale (rounded up), so that p
+// times the scale stays in the 16-bit range whatever the scales are; sum p is f32.
 //
-// Layout. One block per (split, KV head and group of 8 or 16 slots, sequence):
-// 4 compute warps and a producer warp over a ring of 64-row stages. A 16-row
-// slice of a stage belongs to one compute warp and lies in one page; the
-// producer looks the pages up, loads each page's piece by TMA (boxes of
-// gcd(page_size, 64) rows, swizzled) and leaves the page's scales with the
-// stage. Rows a block does not attend are neither waited for nor used.
+// Work. The tiles (TILE rows) of all sequences that any query row sees are laid end to
+// end on the device, and as many blocks as fill the GPU once ("ranks", per KV head and
+// group of 8 or 16 slots) take equal runs of them. A block goes through its run without a
+// pause for the copies: at the end of a sequence its warps' states are merged, and
+// written as the output where the whole sequence was the block's, else as a part
+// (reference, sum, sum p v) that attn_paged_combine joins with the others'. A grid of
+// (split, sequence) blocks left the tail of a ragged batch to a few of them: 32 sequences
+// of 1 .. 32768 rows took 270 us that way and take 160 this way, 1.00 of the copy
+// bandwidth.
+//
+// Layout. NWC compute warps and a producer warp over a ring of S stages of one tile. A
+// 16-row slice of a tile belongs to one warp and lies in one page; the producer looks the
+// pages up two groups of 32 slices ahead, loads each page's piece by TMA (boxes of up to
+// 64 rows of the page, swizzled, first to leave L2) and leaves page and scales beside the
+// stage. Slices that nothing sees are neither loaded nor waited for.
 //
 // Tensor cores. 16x8x16 MMAs, f32 accumulation; q and p as two f16 parts (an f16
 // or e4m3 cache; f16 holds the codes exactly) or three bf16 parts, so that
-// neither loses what 32 bits hold. S = Q Kᵀ: with 8 slots two parts lie over each
-// other in the 16 MMA rows, with 16 slots each part has its own MMA. Oᵀ = Vᵀ Pᵀ: the
+// neither loses what 32 bits hold. S = Q K^T: with 8 slots two parts lie over each
+// other in the 16 MMA rows, with 16 slots each part has its own MMA. O^T = V^T P^T: the
 // parts of p add up in one accumulator, 4 registers for 16 dimensions x 8 slots,
-// and P is used in the registers where S was accumulated. The order of a dot product's terms is free, so a lane's share of a K row
-// is contiguous: 16-byte shared loads give it whole k-steps, with no
-// ldmatrix and, for 8 bits, no shuffling before the conversion. 8-bit V
-// needs pairs of rows in a register: a lane reads its four rows' 16
+// and P is used in the registers where S was accumulated. The order of a dot
+// product's terms is free, so a lane's share of a K row is contiguous: 16-byte shared
+// loads give it whole k-steps, with no ldmatrix and, for 8 bits, no shuffling before the
+// conversion. 8-bit V needs pairs of rows in a register: a lane reads its four rows' 16
 // contiguous dimensions and pairs bytes of two rows before converting.
 //
-// What bounds it: HBM for long caches. The measured rates stand with the
-// launch rules in attn_paged_impl.cuh.
+// What bounds it. HBM where there are many rows (ragged batch above; 48 sequences of
+// 129 .. 4097 rows with a distance bias 58 us, 0.87 of the copy bandwidth; 131072 rows of
+// 8 KV heads 47 us, 0.84: about 8 us of the last two are the chain before the first tile
+// -- positions, table, page -- the merges, the second launch and the blocks' uneven ends).
+// Latency where there are few: one sequence of 512 rows 6.2 us, 8192 rows of 4 KV heads
+// 8.9; with 16 slots of 256 dimensions (4 sequences of up to 8400 rows, 32 slots a KV head: 26 us)
+// the six warps that the accumulators leave room for, and a merge of 3.5 us a sequence.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -65,14 +78,7 @@ __device__ __forceinline__ int div(const FastDiv &d, int n)
     return (int)((__umulhi((unsigned)n, d.mul) + (unsigned)n) >> d.shift);
 }
 
-// Two e4m3 codes (in 16 bits) to two f16 values, exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint16_t w)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(w));
-    return r;
-}
-
+// Four e4m3 codes to four f16 values, exact.
 __device__ __forceinline__ void e4m3x4_to_half4(uint32_t w, uint32_t &lo, uint32_t &hi)
 {
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
@@ -202,7 +208,7 @@ static_assert(sizeof(SegInfo) <= 48, "its place in shared memory");
 
 // The rows the slots of query rows [t0, t1] see, as [first row of t0, last row of t1]
 struct SlotRows {
-    int nkv, base;        // row t's position is base + t
+    int base;             // row t's position is base + t
     int start, window;
     __device__ __forceinline__ int last(int t) const { return base + t; }
     __device__ __forceinline__ int low(int t) const
@@ -778,7 +784,7 @@ __device__ __forceinline__ int rank_tile(int r, int total, int share)
 
 __device__ __forceinline__ SlotRows seq_rows(const PagedArgs &a, int nkv, int start)
 {
-    return SlotRows{nkv, nkv - a.n_q, start, a.window};
+    return SlotRows{nkv - a.n_q, start, a.window};
 }
 
 // The sequence that tile t belongs to: the first one whose end lies past it.

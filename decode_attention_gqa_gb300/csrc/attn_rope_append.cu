@@ -9,12 +9,16 @@
 //
 // Two kinds of blocks in one launch. Token jobs: a warp takes one token and some
 // of its heads -- q, and with a 16-bit cache k and v. Page jobs (e4m3): a block
-// takes the new rows of one page of one KV head of K or V, since the scale
-// they share needs their largest magnitude before the first code: one sweep for
-// the rotation and the maximum, rows kept in the page rescaled where the scale
-// grows, one sweep for the codes.
+// takes the new rows of one page of one KV head, since the scale they share needs
+// their largest magnitude before the first code: the rows are staged in shared memory,
+// one sweep for the rotation and the maximum, rows kept in the page rescaled where the
+// scale grows, one sweep for the codes.
 //
-// What bounds it: launch latency for a decode step, HBM for prompts.
+// What bounds it. HBM for prompts: 7370 bfloat16 tokens of 28 + 4 heads of 128 into e4m3
+// pages 33 us, 0.81 of the copy bandwidth (two thirds of the bytes are writes); 8399
+// float32 tokens of 16 + 2 heads of 256 into bfloat16 pages 52 us, 0.93. Launch latency for
+// a decode step: one token 4.2 us, 64 sequences of one 3.4 (a chain of position, table,
+// old scale and store).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
