@@ -83,36 +83,48 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // across sequences). Where that leaves much of the GPU without a block (units just over half of its
 // slots), enough for four rounds of blocks, whose last is nearly full; no more than there are tiles of rows at
 // full capacity.
+int64_t fill_gpu(const attn::PagedShape &sh, int64_t units, int64_t rows, int64_t seqs, int sm_count)
+{
+    const int64_t tile = sh.nsl * 16, tiles = (rows + tile - 1) / tile * seqs;
+    const int64_t blocks = (int64_t)sm_count * sh.blocks;
+    int64_t P = blocks / units;
+    if (P * units * 20 < blocks * 17) P = 4 * blocks / units;
+    if (P > tiles) P = tiles;
+    // a few tiles: one block a unit takes them in about the time that the second launch adds (a tile of 64
+    // rows 0.9 us, the launch 2.5), with less work for the host
+    if (tiles * tile <= 256) P = 1;
+    return P < 1 ? 1 : P > kMaxPagedSplits ? kMaxPagedSplits : P;
+}
+
 void make_plan(const attn_paged_cache *c, int max_pages, int n_seq, int n_q, int n_head, int window, int n_splits,
                int sm_count, PagedPlan &pl)
 {
-    const int group = n_head / c->n_kv_head;
-    pl.slots = attn::paged_slots(n_q, group);
-    pl.qgroups = (n_q * group + pl.slots - 1) / pl.slots;
-    pl.shape = attn::paged_shape(c->head_dim, type_bytes(c->kv_type), pl.slots);
-    const int64_t units = (int64_t)c->n_kv_head * pl.qgroups;
-    if (n_splits > 0) {
-        pl.n_splits = n_splits;
-    } else {
-        const int64_t tile = pl.shape.nsl * 16;
-        int64_t rows = (int64_t)max_pages * c->page_size;
-        if (window > 0 && (int64_t)window + n_q + tile < rows) rows = (int64_t)window + n_q + tile;
-        const int64_t tiles = (rows + tile - 1) / tile * (n_seq < attn::kPagedSeqs ? n_seq : attn::kPagedSeqs);
-        const int64_t slots = (int64_t)sm_count * pl.shape.blocks;
-        int64_t P = slots / units;
-        if (P * units * 20 < slots * 17) P = 4 * slots / units;
-        if (P > tiles) P = tiles;
-        // a few tiles: one block a unit takes them in about the time that the second launch adds (a tile of 64
-        // rows 0.9 us, the launch 2.5), with less work for the host
-        if (tiles * tile <= 256) P = 1;
-        pl.n_splits = (int)(P < 1 ? 1 : P > kMaxPagedSplits ? kMaxPagedSplits : P);
-    }
+    const int group = n_head / c->n_kv_head, es = type_bytes(c->kv_type), need = n_q * group;
+    const int64_t seqs = n_seq < attn::kPagedSeqs ? n_seq : attn::kPagedSeqs;
+    int64_t rows = (int64_t)max_pages * c->page_size;
+    if (window > 0 && (int64_t)window + n_q + 64 < rows) rows = (int64_t)window + n_q + 64;
+    auto shape = [&](int slots) { return attn::paged_shape(c->head_dim, es, slots); };
+    auto units = [&](int slots) { return (int64_t)c->n_kv_head * ((need + slots - 1) / slots); };
+    // 8 slots a block where a KV head has no more. Else 16 read and convert each row half as often, and 8 have
+    // more blocks at work at a time and a merge half as long. With 8 bits, 8 slots
+    // - while a block has few rows at full capacity (4 sequences of 8000 rows, 16 slots a KV head: head_dim 64 13.5 us
+    //   with 16, 10.7 with 8; 128 15.7 and 13.4; 256 22.9 and 19.9; of 32000 rows 19.6 and 21.6, 26.2 and 28.0,
+    //   44.2 and 43.5; 16-bit rows of 256 dimensions 28.4 and 33.5);
+    // - where the second 16 would be half empty (24 slots, 65000 rows: head_dim 256 127.8 and 107.5 us, 128 64.3 and
+    //   61.0, but 64 43.1 and 47.5).
+    pl.slots = need <= 8 ? 8 : 16;
+    if (need > 8 && es == 1 &&
+        (rows * seqs <= (c->head_dim == 256 ? 1664 : 384) * fill_gpu(shape(8), units(8), rows, seqs, sm_count) ||
+         (need > 16 && need <= 24 && c->head_dim >= 128)))
+        pl.slots = 8;
+    pl.qgroups = (need + pl.slots - 1) / pl.slots;
+    pl.shape = shape(pl.slots);
+    pl.n_splits = n_splits > 0 ? n_splits : (int)fill_gpu(pl.shape, units(pl.slots), rows, seqs, sm_count);
     if (pl.n_splits > 1) {
-        const size_t parts = (size_t)pl.n_splits * 2 * units * pl.slots;
-        const size_t seqs = n_seq < attn::kPagedSeqs ? n_seq : attn::kPagedSeqs;
+        const size_t parts = (size_t)pl.n_splits * 2 * units(pl.slots) * pl.slots;
         pl.o_bytes = align256(parts * c->head_dim * sizeof(float));
         pl.ml_bytes = align256(parts * 2 * sizeof(float));
-        pl.workspace = pl.o_bytes + pl.ml_bytes + align256(seqs * 8);
+        pl.workspace = pl.o_bytes + pl.ml_bytes + align256((size_t)seqs * 8);
     }
 }
 
@@ -340,6 +352,7 @@ attn_status attn_decode_paged(const attn_paged_cache *cache, const int32_t *bloc
     r.head_dim = cache->head_dim;
     r.kv_type = cache->kv_type;
     r.rules = softcap > 0.f || a.slopes;
+    r.slots = pl.slots;
     r.stream = reinterpret_cast<cudaStream_t>(stream);
     const int ti = cache->kv_type - ATTN_TYPE_F16;
     using Launch = cudaError_t (*)(const attn::PagedRequest &);

@@ -42,7 +42,7 @@ cudaError_t launch_paged_kernel(const PagedRequest &r)
 template <int HD, typename KV>
 cudaError_t launch_paged_for(const PagedRequest &r)
 {
-    if (paged_slots(r.pa.n_q, r.pa.group) == 8) {
+    if (r.slots == 8) {
         using C = PagedCfg<HD, 8, KV>;
         return r.rules ? launch_paged_kernel<C, true>(r) : launch_paged_kernel<C, false>(r);
     }

@@ -81,11 +81,9 @@ struct PagedRequest {
     int64_t page_stride, row_stride, head_stride;   // elements
     int head_dim, kv_type;
     bool rules;               // softcap or slopes
+    int slots;                // (query row, head) slots of a block: 8 or 16
     cudaStream_t stream;
 };
-
-// (query row, head) slots of a block: 8 where a KV head's slots fit in 8, else 16.
-inline int paged_slots(int n_q, int group) { return n_q * group <= 8 ? 8 : 16; }
 
 cudaError_t launch_paged_hd64_f16(const PagedRequest &r);
 cudaError_t launch_paged_hd64_bf16(const PagedRequest &r);

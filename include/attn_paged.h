@@ -185,7 +185,7 @@ typedef struct {
  *   scale        multiplies q.k
  *   rules        NULL: plain scores
  *   n_splits     blocks that share the call's rows, per KV head (and group of
- *                16 (query row, head) pairs of it): each takes an equal part of
+ *                8 or 16 (query row, head) pairs): each takes an equal part of
  *                the rows of all sequences laid end to end; 0: attn_paged_plan's
  *                count, which fills the GPU once
  *   workspace    device buffer of the bytes attn_paged_plan reports, 256-byte

@@ -170,6 +170,15 @@ def test_several_query_rows_and_large_groups(pkg, kv, hd, n_q, group, page):
     assert pkg.attn_read_device_error() == 0
 
 
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("n_q,group,rules", [(2, 5, {}), (5, 7, {}), (1, 13, {}), (4, 8, dict(window=60, softcap=20.0)), (17, 3, {})])
+def test_large_groups_in_a_large_capacity(pkg, hd, n_q, group, rules):
+    """8 bits: 16 slots a block where the capacity is large, whatever rows there are."""
+    pool = Pool(hd + n_q, "e4m3", 2, hd, 64, (0, 1, 70, 333, 1000), extra_pages=4000)
+    attend_check(pkg, pool, n_q, group * 2, splits=(0, 1, 3), **rules)
+    assert pkg.attn_read_device_error() == 0
+
+
 @pytest.mark.parametrize("kv", ["e4m3", "f16", "bf16"])
 @pytest.mark.parametrize("hd", [64, 128, 256])
 @pytest.mark.parametrize("n_q,group", [(1, 2), (4, 4)])

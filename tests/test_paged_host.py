@@ -120,6 +120,11 @@ def test_plan_for_a_given_sm_count(lib):
     assert plan(window=300)[0] < 8 and plan(window=100)[0] == 1
     # 16 (query row, head) slots a block, several blocks a KV head
     assert plan(n_q=4, n_seq=9) == (152, ws(152, 2, 16, 9)) and plan(n_q=12, n_seq=9)[0] == 50
+    # 8 bits: 8 slots a block while the blocks have few rows, or 16
+    e8 = dict(kv_type=pkg.ATTN_TYPE_E4M3, k_scale=256, v_scale=256)
+    assert plan(cache=_cache(**e8), n_q=4, n_seq=3) == (114, ws(114, 4, 8, 3))
+    assert plan(cache=_cache(**e8), n_q=4, n_seq=9) == (152, ws(152, 2, 16, 9))
+    assert plan(cache=_cache(**e8), n_q=5, n_seq=99) == (76, ws(76, 6, 8, 99))      # 20 slots: the second 16 half empty
     # units just over half of the resident blocks: four rounds; far more units than blocks: one block each
     assert plan(cache=_cache(n_kv_head=160), n_head=160, n_seq=2)[0] == 7
     assert plan(cache=_cache(n_kv_head=2000), n_head=2000) == (1, 0)
