@@ -149,7 +149,7 @@ struct PagedCfg {
     static constexpr uint32_t OFF_DESC = OFF_SEG + 48;            // SliceInfo[4][32]
     static constexpr uint32_t OFF_BAR = OFF_DESC + 4 * 32 * 16;
     static constexpr uint32_t OFF_SEQ = OFF_BAR + 2 * S * 8 + 16;
-    static constexpr uint32_t SMEM_BYTES = OFF_SEQ + (3 * kPagedSeqs + 1) * 4;
+    static constexpr uint32_t SMEM_BYTES = OFF_SEQ + 16 + (3 * kPagedSeqs + 1) * 4 + kPagedSeqs;
     static_assert(NWC % NSL == 0 && S <= TPG, "descriptor buffers outlive the stages in flight");
     // a warp waits for the phases of its own stages only: if a stage changed hands, a warp could take the
     // parity of an older phase for its own
@@ -769,19 +769,6 @@ __device__ __forceinline__ void PagedQ<C>::store(uint8_t *smem, const PagedArgs 
     }
 }
 
-// The tiles of all sequences, laid end to end, over the ranks: rank r takes [r share, (r + 1) share), with the
-// share that lets all ranks but the last few have the same. No rank below the last one with tiles has none,
-// so every rank between a sequence's first and last has some of it.
-__device__ __forceinline__ int rank_share(int total, int ranks)
-{
-    return max((int)(((unsigned)total + (unsigned)ranks - 1u) / (unsigned)ranks), 1);
-}
-
-__device__ __forceinline__ int rank_tile(int r, int total, int share)
-{
-    return (int)min((int64_t)r * share, (int64_t)total);
-}
-
 __device__ __forceinline__ SlotRows seq_rows(const PagedArgs &a, int nkv, int start)
 {
     return SlotRows{nkv - a.n_q, start, a.window};
@@ -799,12 +786,12 @@ __device__ __forceinline__ int find_seq(const int *cs, int n, int t)
     return lo;
 }
 
-// First row of the first tile of a sequence, and one past its last row
+// First row of the first tile of a sequence, and one past its last row (TILE is a power of two)
 template <int TILE>
 __device__ __forceinline__ int2 seq_extent(const PagedArgs &a, const SlotRows &sr)
 {
     const int R = max(sr.last(a.n_q - 1) + 1, 0), L = min(sr.low(0), R);
-    return make_int2(L / TILE * TILE, R);
+    return make_int2(L & -TILE, R);
 }
 
 template <class C, bool RULES>
@@ -818,10 +805,12 @@ attn_paged_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *empty = full + S;
     volatile int *flags = reinterpret_cast<volatile int *>(empty + S);   // [0] abort, [1] tiles issued
-    int *cs = reinterpret_cast<int *>(smem + C::OFF_SEQ);    // tiles before each sequence
+    int4 *srank = reinterpret_cast<int4 *>(smem + C::OFF_SEQ);   // the rank's first tile, one past its last; share, gap
+    int *cs = reinterpret_cast<int *>(srank + 1);            // tiles before each sequence
     int *snkv = cs + kPagedSeqs + 1, *sstart = snkv + kPagedSeqs;
+    uint8_t *behind = reinterpret_cast<uint8_t *>(sstart + kPagedSeqs);   // sequences with tiles before each
 
-    const int hk = blockIdx.y, qg = blockIdx.x, unit = hk * a.qgroups + qg, rank = blockIdx.z;
+    const int hk = blockIdx.y, qg = blockIdx.x, rank = blockIdx.z;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (warp == NWC) {
@@ -851,34 +840,68 @@ attn_paged_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             pos[i] = have ? ld_dep(a.positions + s) : -1;
             st[i] = have && a.starts ? ld_dep(a.starts + s) : 0;
         }
-        int sum = 0;
+        int n[MOST], sum = 0, some = 0;
 #pragma unroll
         for (int i = 0; i < MOST; ++i) {
             const int s = lane * per + i;
-            if (i >= per || s >= a.n_seq) break;
-            const int64_t n = (int64_t)pos[i] + 1;
-            const bool ok = n >= 0 && n <= a.cap;
-            if (!ok && unit == 0 && rank == 0) atomicOr(a.err, kErrPositionClamped);
-            const int nkv = ok ? (int)n : n < 0 ? 0 : a.cap;
+            n[i] = 0;
+            if (i >= per || s >= a.n_seq) continue;
+            const int nkv = min(max(pos[i], -1), a.cap - 1) + 1;
+            if ((pos[i] < -1 || pos[i] >= a.cap) && (hk | qg) == 0 && rank == 0) atomicOr(a.err, kErrPositionClamped);
             snkv[s] = nkv;
             sstart[s] = st[i];
-            const int2 x = seq_extent<TILE>(a, seq_rows(a, nkv, st[i]));
-            cs[s] = sum;
-            sum += x.x < x.y && seq_rows(a, nkv, st[i]).low(0) < x.y ? (x.y - x.x + TILE - 1) / TILE : 0;
+            const SlotRows sr = seq_rows(a, nkv, st[i]);
+            const int2 x = seq_extent<TILE>(a, sr);
+            if (sr.low(0) < x.y) n[i] = (int)((unsigned)(x.y - x.x + TILE - 1) / TILE);
+            sum += n[i];
+            some += n[i] > 0;
         }
-        int before = sum;
+        int before = sum, upto = some;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, before, off);
-            if (lane >= off) before += y;
+            const int y = __shfl_up_sync(0xffffffffu, before, off), z = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) {
+                before += y;
+                upto += z;
+            }
         }
         const int total = __shfl_sync(0xffffffffu, before, 31);
+        // Going from one sequence to the next costs a block the time of `turn` tiles (the merge, the next q). So the
+        // ranks take equal parts not of the tiles but of places: a tile each, and `gap` between two
+        // sequences with tiles (`turn`, or half of a rank's part where that is less). A sequence's own tiles
+        // have no gap, so that every rank between its first and its last has some of them.
+        const int turns = max(__shfl_sync(0xffffffffu, upto, 31) - 1, 0);
+        const int gap = min(a.turn, div(a.by_ranks, total + a.ranks - 1) / 2);
+        const int share = max(div(a.by_ranks, total + gap * turns + a.ranks - 1), 1);
+        // the first tiles at or past the rank's first place and the next rank's
+        const int from = rank * share;
+        int first = -1, end = -1;
         before -= sum;
-        for (int i = 0; i < per && lane * per + i < a.n_seq; ++i) cs[lane * per + i] += before;
-        if (lane == 0) cs[a.n_seq] = total;
+        upto -= some;
+#pragma unroll
+        for (int i = 0; i < MOST; ++i) {
+            const int s = lane * per + i;
+            if (i >= per || s >= a.n_seq) continue;
+            cs[s] = before;
+            behind[s] = (uint8_t)upto;
+            const int shift = gap * upto;                      // a tile's place is its number and this
+            if (n[i] > 0) {
+                if (first < 0 && before + n[i] + shift > from) first = max(from - shift, before);
+                if (end < 0 && before + n[i] + shift > from + share) end = max(from + share - shift, before);
+                before += n[i];
+                ++upto;
+            }
+        }
+        const unsigned hf = __ballot_sync(0xffffffffu, first >= 0), he = __ballot_sync(0xffffffffu, end >= 0);
+        first = __shfl_sync(0xffffffffu, first, __ffs(hf) - 1);
+        end = __shfl_sync(0xffffffffu, end, __ffs(he) - 1);
+        if (hf == 0) first = total;
+        if (he == 0) end = total;
+        if (lane == 0) {
+            cs[a.n_seq] = total;
+            *srank = make_int4(first, end, share, gap);
+        }
         __syncthreads();                                       // the compute warps go on to their first q
-        const int share = rank_share(total, a.ranks);
-        const int first = rank_tile(rank, total, share), end = rank_tile(rank + 1, total, share);
         const int ntiles = end - first;
 
         // Descriptors: lane i has slice i of a group of TPG tiles. A group's pages are loaded two groups
@@ -1001,26 +1024,22 @@ attn_paged_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         // Values that only the ends of a sequence need are read again from shared memory there, so that the tile
         // loop's registers hold the accumulators.
         volatile SegInfo *seg = reinterpret_cast<volatile SegInfo *>(smem + C::OFF_SEG);
-        const size_t heads = (size_t)a.n_q * a.n_head;
         auto nslots = [&] { return min(C::SLOTS, a.n_q * a.group - qg * C::SLOTS); };
         auto head_row = [&](int s, int i) {                    // of slot i of the block
             const int x = qg * C::SLOTS + i, t = div(a.by_group, x);
-            return (size_t)s * heads + (size_t)t * a.n_head + hk * a.group + (x - t * a.group);
+            return ((size_t)s * a.n_q + t) * a.n_head + hk * a.group + (x - t * a.group);
         };
         // sequences that start here: which ranks have their rows; no rows at all: 0
-        const int total = cs[a.n_seq], share = rank_share(total, a.ranks);
-        const int first = rank_tile(rank, total, share), end = rank_tile(rank + 1, total, share);
-        {
-            for (int s = tid; s < a.n_seq; s += NWC * 32) {
-                const int c = cs[s], n = cs[s + 1] - c;
-                if (!((c >= first && c < end) || (c == total && rank == 0))) continue;
-                if (a.ranks > 1 && unit == 0)
-                    a.ws_span[s] = make_int2(rank, n > 0 ? (c + n - 1) / share : rank);
-                if (n == 0)
-                    for (int i = 0; i < nslots(); ++i)
-                        for (int d = 0; d < C::HD; d += 4)
-                            *reinterpret_cast<float4 *>(a.out + head_row(s, i) * C::HD + d) = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
+        const int first = srank->x, end = srank->y;
+        for (int s = tid; s < a.n_seq; s += NWC * 32) {
+            const int c = cs[s], n = cs[s + 1] - c;
+            if (!((c >= first && c < end) || (n == 0 && c == cs[a.n_seq] && rank == 0))) continue;
+            if (a.ranks > 1 && (hk | qg) == 0)
+                a.ws_span[s] = make_int2(rank, n > 0 ? (c + srank->w * behind[s] + n - 1) / srank->z : rank);
+            if (n == 0)
+                for (int i = 0; i < nslots(); ++i)
+                    for (int d = 0; d < C::HD; d += 4)
+                        *reinterpret_cast<float4 *>(a.out + head_row(s, i) * C::HD + d) = make_float4(0.f, 0.f, 0.f, 0.f);
         }
         const uint32_t smem_u = smem_u32(smem);
         float2 *mm = reinterpret_cast<float2 *>(smem + C::OFF_Q);
@@ -1107,7 +1126,7 @@ attn_paged_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             }
             const int sq = seg->seq;
             const bool begins = from == cs[sq], whole = begins && stop == cs[sq + 1];
-            const size_t part = ((size_t)(rank * 2 + (begins ? 1 : 0)) * a.units + unit) * C::SLOTS;
+            const size_t part = ((size_t)(rank * 2 + (begins ? 1 : 0)) * a.units + (hk * a.qgroups + qg)) * C::SLOTS;
             const bool bad = flags[0] != 0;              // left unwritten; the error word says why
             constexpr int D4 = C::HD / 4;
             for (int i = tid; i < nslots() * D4 && !bad; i += NWC * 32) {

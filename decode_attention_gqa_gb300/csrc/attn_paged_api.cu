@@ -333,6 +333,10 @@ attn_status attn_decode_paged(const attn_paged_cache *cache, const int32_t *bloc
     a.qgroups = pl.qgroups;
     a.units = (int)units;
     a.ranks = pl.n_splits;
+    // the merge grows with the slots and the dimensions faster than the time of a tile (places between two
+    // sequences 0, 2, 3, 4: head_dim 128, 8 slots 57.8, 56.9, 57.7, 59.0 us; 256, 8 slots 38.7, 38.5, 37.5, 37.6;
+    // 128, 16 slots 34.5, 32.2, 30.9, 29.8; 256, 16 slots, 16 bits 28.7, 26.8, 26.4, 25.8)
+    a.turn = 2 + (pl.slots == 16 ? 2 : 0) + (cache->head_dim == 256 ? 1 : 0);
     a.max_pages = max_pages;
     a.n_pages = cache->n_pages;
     a.page_size = cache->page_size;
@@ -342,6 +346,7 @@ attn_status attn_decode_paged(const attn_paged_cache *cache, const int32_t *bloc
     a.box_rows = cache->page_size % 64 == 0 && tile >= 64 ? 64 : cache->page_size % 32 == 0 && tile >= 32 ? 32 : 16;
     a.by_page = attn::fast_div((unsigned)cache->page_size);
     a.by_group = attn::fast_div((unsigned)a.group);
+    a.by_ranks = attn::fast_div((unsigned)a.ranks);
     a.qscale = qscale;
     a.cap_log2 = (float)((double)softcap * 1.4426950408889634);
     r.k = cache->k;
@@ -361,8 +366,8 @@ attn_status attn_decode_paged(const attn_paged_cache *cache, const int32_t *bloc
         {attn::launch_paged_hd128_f16, attn::launch_paged_hd128_bf16, attn::launch_paged_hd128_e4m3},
         {attn::launch_paged_hd256_f16, attn::launch_paged_hd256_bf16, attn::launch_paged_hd256_e4m3}};
     const int hi = cache->head_dim == 64 ? 0 : cache->head_dim == 128 ? 1 : 2;
-    // tiles are counted in 32 bits, some groups past the last: fewer sequences a launch where the capacity is huge
-    const int64_t per_seq = (a.cap + (int64_t)tile - 1) / tile + 1;
+    // tiles and places are counted in 32 bits, some groups past the last: fewer sequences a launch where the capacity is huge
+    const int64_t per_seq = (a.cap + (int64_t)tile - 1) / tile + 1 + a.turn;
     const int batch = (int)(0x7fff0000 / per_seq < attn::kPagedSeqs ? 0x7fff0000 / per_seq : attn::kPagedSeqs);
     for (int s0 = 0; s0 < n_seq; s0 += batch) {
         const size_t rows = (size_t)s0 * n_q * n_head * cache->head_dim;

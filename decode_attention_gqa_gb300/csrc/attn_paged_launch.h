@@ -66,11 +66,12 @@ struct PagedArgs {
     int qgroups;              // blocks per (rank, KV head) along the (query row, head) slots
     int units;                // n_kv_head * qgroups
     int ranks;                // blocks that share the rows, per unit
+    int turn;                 // what going to the next sequence costs a block, in tiles
     int max_pages, n_pages, page_size;
     int cap;                  // max_pages * page_size
     int window;               // 0: none
     int box_rows;             // rows of one TMA box: a power of two that divides the page and the stage
-    FastDiv by_page, by_group;
+    FastDiv by_page, by_group, by_ranks;
     float qscale;             // scale * log2 e, or scale / softcap
     float cap_log2;           // softcap * log2 e, or 0
 };

@@ -199,6 +199,17 @@ def test_more_sequences_than_a_launch_takes(pkg):
     assert pkg.attn_read_device_error() == 0
 
 
+@pytest.mark.parametrize("kv,hd,n_q,group", [("f16", 64, 1, 2), ("bf16", 128, 3, 4), ("e4m3", 256, 1, 1)])
+def test_blocks_that_cross_many_sequences(pkg, kv, hd, n_q, group):
+    """Long, short and empty sequences in turn, over few and many blocks: every place a boundary can fall."""
+    rng = np.random.default_rng(hd)
+    ctx = [int(x) for x in rng.choice([0, 1, 40, 64, 200, 700, 1500], 40)]
+    pool = Pool(hd, kv, 1, hd, 64, ctx)
+    attend_check(pkg, pool, n_q, group, splits=(0, 1, 2, 3, 7, 31, 100, 300))
+    attend_check(pkg, pool, n_q, group, splits=(0, 5, 40), window=150, starts=[int(x) for x in rng.choice([0, 30, 650], 40)])
+    assert pkg.attn_read_device_error() == 0
+
+
 RULES = [
     dict(softcap=20.0), dict(window=1), dict(window=40), dict(window=100000), dict(slopes=True),
     dict(starts=True), dict(softcap=5.0, window=33, slopes=True, starts=True), dict(window=70, starts=True),
