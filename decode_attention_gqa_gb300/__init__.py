@@ -429,9 +429,16 @@ _torch = None
 
 
 def _torch_module():
-    global _torch
+    global _torch, _alloc, _free
     if _torch is None:
         import torch
+        # torch's allocator without a tensor around the memory, or by its public names where these are missing
+        _alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+        _free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
+        if _alloc is None or _free is None:
+            def _alloc(size, stream):
+                return torch.cuda.caching_allocator_alloc(size, stream=stream)
+            _free = torch.cuda.caching_allocator_delete
         _torch = torch
     return _torch
 
@@ -674,11 +681,14 @@ def paged_decode_attention(cache, block_table, positions, q, scale=None, out=Non
             cache._plans.clear()
         plan = cache._plans[key] = attn_paged_plan(cache, max_pages, n_seq, n_q, n_head, window, n_splits)
     n_splits, need = plan
-    ws = torch.empty(need, dtype=torch.uint8, device=cache.device) if need else None
-    status = (_lib or load()).attn_decode_paged(
-        cache._address, block_table.data_ptr(), max_pages, positions.data_ptr(), q.data_ptr(), out.data_ptr(),
-        n_seq, n_q, n_head, hd ** -0.5 if scale is None else scale, rules, n_splits,
-        ws.data_ptr() if need else None, need, handle)
+    ws = _alloc(need, handle) if need else None
+    try:
+        status = (_lib or load()).attn_decode_paged(
+            cache._address, block_table.data_ptr(), max_pages, positions.data_ptr(), q.data_ptr(), out.data_ptr(),
+            n_seq, n_q, n_head, hd ** -0.5 if scale is None else scale, rules, n_splits, ws, need, handle)
+    finally:
+        if need:
+            _free(ws)                   # for what follows on this stream
     if status:
         raise AttnError(status, "attn_decode_paged")
     return out
