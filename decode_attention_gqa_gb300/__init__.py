@@ -429,16 +429,23 @@ _torch = None
 
 
 def _torch_module():
-    global _torch, _alloc, _free
+    global _torch, _alloc, _free, _device, _raw_stream
     if _torch is None:
         import torch
-        # torch's allocator without a tensor around the memory, or by its public names where these are missing
-        _alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
-        _free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
+        # torch's allocator without a tensor around the memory, the current device, and a stream's handle without an
+        # object; by their public names where these are missing
+        c = torch._C
+        _alloc = getattr(c, "_cuda_cudaCachingAllocator_raw_alloc", None)
+        _free = getattr(c, "_cuda_cudaCachingAllocator_raw_delete", None)
         if _alloc is None or _free is None:
             def _alloc(size, stream):
                 return torch.cuda.caching_allocator_alloc(size, stream=stream)
             _free = torch.cuda.caching_allocator_delete
+        _device = getattr(c, "_cuda_getDevice", torch.cuda.current_device)
+        _raw_stream = getattr(c, "_cuda_getCurrentRawStream", None)
+        if _raw_stream is None:
+            def _raw_stream(index):
+                return torch.cuda.current_stream(index).cuda_stream
         _torch = torch
     return _torch
 
@@ -532,13 +539,6 @@ def _same_device(device):
         raise ValueError("the cache must be on the current CUDA device")
 
 
-def _current_stream(index):
-    """The handle of torch's current stream on device `index`."""
-    cuda = _torch_module().cuda
-    get = getattr(_torch._C, "_cuda_getCurrentRawStream", None)    # the handle without a Stream object
-    return get(index) if get is not None else cuda.current_stream(index).cuda_stream
-
-
 def _in_type(dtype):
     torch = _torch_module()
     if dtype is torch.bfloat16:
@@ -566,7 +566,7 @@ def rope_append(cache, block_table, positions, k_new, v_new, q=None, q_out=None,
     n_tokens, n_kv = shape[0], cache.n_kv_head
     n_seq, max_pages = block_table.shape if block_table.dim() == 2 else (-1, 0)
     row = (n_kv, hd)
-    if not (index >= 0 and index == torch.cuda.current_device() and shape[1:] == row and v_new.shape == shape and
+    if not (index >= 0 and index == _device() and shape[1:] == row and v_new.shape == shape and
             v_new.dtype is dt and k_new.get_device() == index and v_new.get_device() == index and
             ks[2] == 1 and vs[2] == 1 and (n_kv == 1 or (ks[1] == hd and vs[1] == hd)) and
             block_table.dtype is i32 and block_table.get_device() == index and block_table.is_contiguous() and
@@ -588,7 +588,7 @@ def rope_append(cache, block_table, positions, k_new, v_new, q=None, q_out=None,
                     ((False, "q must be [n_tokens, n_head, head_dim], dense within a token"),))
         n_head, qs = qshape[1], qst[0]
         if q_out is None:
-            if stream is not None and _stream(stream) != _current_stream(index):
+            if stream is not None and _stream(stream) != _raw_stream(index):
                 raise ValueError("q_out must be given with a stream that is not the current one")
             q_out = torch.empty(qshape, dtype=torch.float32, device=cache.device)
         elif not (q_out.shape == qshape and q_out.dtype is torch.float32 and q_out.get_device() == index and
@@ -616,7 +616,7 @@ def rope_append(cache, block_table, positions, k_new, v_new, q=None, q_out=None,
     status = (_lib or load()).attn_rope_append(
         cache._address, block_table.data_ptr(), max_pages, positions.data_ptr(), cp, n_seq, n_tokens, qp,
         k_new.data_ptr(), v_new.data_ptr(), qs, kst, vst, in_type, op, n_head, rp,
-        _current_stream(index) if stream is None else _stream(stream))
+        _raw_stream(index) if stream is None else _stream(stream))
     if status:
         raise AttnError(status, "attn_rope_append")
     return q_out
@@ -641,7 +641,7 @@ def paged_decode_attention(cache, block_table, positions, q, scale=None, out=Non
     else:
         raise ValueError("q must be [n_seq, n_head, head_dim] or [n_seq, n_q, n_head, head_dim]")
     n_seq, max_pages = block_table.shape if block_table.dim() == 2 else (-1, 0)
-    if not (index >= 0 and index == torch.cuda.current_device() and qs == n_seq and qd == hd and q.dtype is f32 and
+    if not (index >= 0 and index == _device() and qs == n_seq and qd == hd and q.dtype is f32 and
             q.get_device() == index and q.is_contiguous() and
             block_table.dtype is i32 and block_table.get_device() == index and block_table.is_contiguous() and
             positions.dtype is i32 and positions.get_device() == index and positions.is_contiguous() and
@@ -668,7 +668,7 @@ def paged_decode_attention(cache, block_table, positions, q, scale=None, out=Non
         rules = ctypes.addressof(kept)
     if n_seq == 0:
         return out
-    handle = _current_stream(index)
+    handle = _raw_stream(index)
     if stream is not None and _stream(stream) != handle:
         raise ValueError("stream must be the current stream (torch.cuda.stream selects one)")
     # the plan is a function of these numbers, the pool's shape and the device
