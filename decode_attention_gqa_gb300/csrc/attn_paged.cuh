@@ -835,17 +835,21 @@ attn_paged_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         int pos[MOST], st[MOST];
 #pragma unroll
         for (int i = 0; i < MOST; ++i) {
-            const int s = lane * per + i;
-            const bool have = i < per && s < a.n_seq;
-            pos[i] = have ? ld_dep(a.positions + s) : -1;
-            st[i] = have && a.starts ? ld_dep(a.starts + s) : 0;
+            pos[i] = -1;
+            st[i] = 0;
+            if (i < per) {
+                const int s = lane * per + i;
+                if (s < a.n_seq) pos[i] = ld_dep(a.positions + s);
+                if (a.starts && s < a.n_seq) st[i] = ld_dep(a.starts + s);
+            }
         }
         int n[MOST], sum = 0, some = 0;
 #pragma unroll
         for (int i = 0; i < MOST; ++i) {
-            const int s = lane * per + i;
             n[i] = 0;
-            if (i >= per || s >= a.n_seq) continue;
+            if (i >= per) break;
+            const int s = lane * per + i;
+            if (s >= a.n_seq) continue;
             const int nkv = min(max(pos[i], -1), a.cap - 1) + 1;
             if ((pos[i] < -1 || pos[i] >= a.cap) && (hk | qg) == 0 && rank == 0) atomicOr(a.err, kErrPositionClamped);
             snkv[s] = nkv;
@@ -880,8 +884,9 @@ attn_paged_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         upto -= some;
 #pragma unroll
         for (int i = 0; i < MOST; ++i) {
+            if (i >= per) break;
             const int s = lane * per + i;
-            if (i >= per || s >= a.n_seq) continue;
+            if (s >= a.n_seq) continue;
             cs[s] = before;
             behind[s] = (uint8_t)upto;
             const int shift = gap * upto;                      // a tile's place is its number and this
