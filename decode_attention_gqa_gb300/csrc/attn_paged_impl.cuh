@@ -27,16 +27,20 @@ cudaError_t launch_paged_kernel(const PagedRequest &r)
     void *args[] = {&kmap, &vmap, &pa};
     e = launch_pdl(fn, dim3((unsigned)pa.qgroups, (unsigned)pa.n_kv_head, (unsigned)pa.ranks), dim3(C::THREADS), C::SMEM_BYTES, r.stream, args);
     if (e != cudaSuccess || pa.ranks == 1) return e;
-    // chunks of 32 dimensions while there are few rows (more blocks share the parts' loads), else whole rows
-    const int64_t rows = (int64_t)pa.n_q * pa.n_head;
-    const bool chunks = rows * pa.n_seq <= 512;
+    // The widest piece of a row a block that leaves enough of them: a piece brings its row's sums and span along, and
+    // few blocks hide no latency (pieces of 32, 64, all dimensions: 64 rows of 128 47.5, 46.9, 47.5 us the
+    // whole call; 256 rows of 256 21.3, 19.8, 19.9; 360 rows of 256 17.2, 15.8, 15.4; 28 rows of 128 9.0, 9.0, 9.8;
+    // 16 rows of 256 14.1, 14.7, 19.0).
+    const int64_t rows = (int64_t)pa.n_q * pa.n_head, pieces64 = rows * pa.n_seq * C::HD / 64;
+    const int piece = rows * pa.n_seq > 256 ? C::HD : pieces64 >= 128 ? 64 : 32;
     int slots = C::SLOTS;
-    const void *cf = chunks ? reinterpret_cast<const void *>(&attn_paged_combine<C::HD, 32>)
-                            : reinterpret_cast<const void *>(&attn_paged_combine<C::HD, C::HD>);
+    const void *cf = piece == C::HD ? reinterpret_cast<const void *>(&attn_paged_combine<C::HD, C::HD>)
+                     : piece == 64 ? reinterpret_cast<const void *>(&attn_paged_combine<C::HD, 64>)
+                                   : reinterpret_cast<const void *>(&attn_paged_combine<C::HD, 32>);
     e = ensure_smem_attr(cf, 0);
     if (e != cudaSuccess) return e;
     void *cargs[] = {&pa, &slots};
-    return launch_pdl(cf, dim3((unsigned)rows, (unsigned)pa.n_seq, chunks ? C::HD / 32 : 1), dim3(128), 0, r.stream, cargs);
+    return launch_pdl(cf, dim3((unsigned)rows, (unsigned)pa.n_seq, (unsigned)(C::HD / piece)), dim3(128), 0, r.stream, cargs);
 }
 
 template <int HD, typename KV>
