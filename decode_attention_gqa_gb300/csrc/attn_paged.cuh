@@ -11,13 +11,14 @@
 //
 // Work. The tiles (TILE rows) of all sequences that any query row sees are laid end to
 // end on the device, and as many blocks as fill the GPU once ("ranks", per KV head and
-// group of 8 or 16 slots) take equal runs of them. A block goes through its run without a
-// pause for the copies: at the end of a sequence its warps' states are merged, and
-// written as the output where the whole sequence was the block's, else as a part
-// (reference, sum, sum p v) that attn_paged_combine joins with the others'. A grid of
-// (split, sequence) blocks left the tail of a ragged batch to a few of them: 32 sequences
-// of 1 .. 32768 rows took 270 us that way and take 160 this way, 1.00 of the copy
-// bandwidth.
+// group of 8 or 16 slots) take equal runs of them, the turn to the next sequence counted
+// as the few tiles whose time it takes (21.4 us against 22.9 for the draft rows below). A
+// block goes through its run without a pause for the copies: at the end of a sequence its
+// warps' states are merged, and written as the output where the whole sequence was the
+// block's, else as a part (reference, sum, sum p v) that attn_paged_combine joins with
+// the others'. A grid of (split, sequence) blocks left the tail of a ragged batch to a few
+// of them: 32 sequences of 1 .. 32768 rows took 270 us that way and take 159 this way, 1.00
+// of the copy bandwidth.
 //
 // Layout. NWC compute warps and a producer warp over a ring of S stages of one tile. A
 // 16-row slice of a tile belongs to one warp and lies in one page; the producer looks the
@@ -37,12 +38,13 @@
 // contiguous dimensions and pairs bytes of two rows before converting.
 //
 // What bounds it. HBM where there are many rows (ragged batch above; 48 sequences of
-// 129 .. 4097 rows with a distance bias 58 us, 0.87 of the copy bandwidth; 131072 rows of
-// 8 KV heads 47 us, 0.84: about 8 us of the last two are the chain before the first tile
-// -- positions, table, page -- the merges, the second launch and the blocks' uneven ends).
-// Latency where there are few: one sequence of 512 rows 6.2 us, 8192 rows of 4 KV heads
-// 8.9; with 16 slots of 256 dimensions (4 sequences of up to 8400 rows, 32 slots a KV head: 26 us)
-// the six warps that the accumulators leave room for, and a merge of 3.5 us a sequence.
+// 129 .. 4097 rows with a distance bias 57 us, 0.88 of the copy bandwidth; 131072 rows of
+// 8 KV heads 46.5 us, 0.85: 5 to 7 us of the last two are the chain before the first tile
+// -- positions, table, page --, the merges, the joining kernel and uneven ends). Latency
+// where there are few: one sequence of 512 rows 6.2 us, 8192 rows of 4 KV heads 8.9; 4
+// draft rows of 4 sequences of up to 8400 rows, 32 slots of 256 dimensions a KV head, 19.5
+// us: the accumulators leave room for eight warps an SM, which keep the tensor pipe
+// half busy.
 #pragma once
 
 #include <cuda_fp8.h>

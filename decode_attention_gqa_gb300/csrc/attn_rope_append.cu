@@ -15,7 +15,7 @@
 // scale grows, one sweep for the codes.
 //
 // What bounds it. HBM for prompts: 7370 bfloat16 tokens of 28 + 4 heads of 128 into e4m3
-// pages 33 us, 0.81 of the copy bandwidth (two thirds of the bytes are writes); 8399
+// pages 33 us, 0.81 of the copy bandwidth (three fifths of the bytes are writes); 8399
 // float32 tokens of 16 + 2 heads of 256 into bfloat16 pages 52 us, 0.93. Launch latency for
 // a decode step: one token 4.2 us, 64 sequences of one 3.4 (a chain of position, table,
 // old scale and store).
