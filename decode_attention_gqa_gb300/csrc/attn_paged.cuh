@@ -143,7 +143,8 @@ struct PagedCfg {
     // Merge area (floats): the warps' (reference, sum) per slot, their merge, the accumulator rows
     static constexpr uint32_t OFF_RES = 2 * NWC * SLOTS, OFF_MO = OFF_RES + 2 * SLOTS;
     static constexpr int NPART = HD / 32;                         // 32-dimension parts of a row
-    static constexpr bool Q_EARLY = !(HD == 256 && SLOTS == 16);  // q of the next sequence is loaded before the merge (registers)
+    // q of the next sequence is loaded before the merge, where the registers are enough
+    static constexpr bool Q_EARLY = !(SLOTS == 16 && (HD == 256 || (HD == 64 && !E8)));
     static constexpr uint32_t MERGE_BYTES = (OFF_MO + SLOTS * MS) * 4;
     static constexpr uint32_t OFF_Q = S * STAGE_BYTES;            // Q fragments; then the merge area
     static constexpr uint32_t OFF_SLOT = OFF_Q + (Q_BYTES > MERGE_BYTES ? Q_BYTES : MERGE_BYTES);

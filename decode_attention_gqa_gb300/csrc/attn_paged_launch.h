@@ -20,14 +20,17 @@ struct PagedShape {
     int blocks;               // resident blocks per SM
 };
 
-// About 190 KB of stages on an SM whatever the row size, in as many blocks as the accumulators
-// (head_dim / 4 registers a thread for 8 slots, head_dim / 2 for 16) leave room for.
+// 130 to 190 KB of stages on an SM, in as many blocks as the accumulators (head_dim / 4 registers a thread for 8
+// slots, head_dim / 2 for 16) leave room for: the more warps, the better they hide each other's latency
+// (head_dim 64, 8 bits, 8 slots: a ragged batch 106 us with three blocks an SM, 97 with four; 16 bits, 16 slots, 65000 rows:
+// 49.6 with two, 42.1 with three). Where the registers would have to be squeezed further, it does not pay
+// (head_dim 256, 8 bits, 8 slots: draft rows 22.9 with two blocks, 23.3 with three and spills).
 constexpr PagedShape paged_shape(int head_dim, int es, int slots)
 {
-    return es == 1 ? (head_dim == 64    ? PagedShape{4, 4, 6, 3}
+    return es == 1 ? (head_dim == 64    ? (slots == 8 ? PagedShape{4, 4, 5, 4} : PagedShape{4, 4, 6, 3})
                       : head_dim == 128 ? (slots == 8 ? PagedShape{4, 4, 4, 3} : PagedShape{4, 4, 6, 2})
                                         : (slots == 8 ? PagedShape{4, 4, 3, 2} : PagedShape{2, 6, 12, 1}))
-                   : (head_dim == 64    ? (slots == 8 ? PagedShape{4, 4, 4, 3} : PagedShape{4, 4, 6, 2})
+                   : (head_dim == 64    ? (slots == 8 ? PagedShape{4, 4, 3, 4} : PagedShape{4, 4, 4, 3})
                       : head_dim == 128 ? PagedShape{4, 4, 3, 2}
                                         : PagedShape{2, 6, 6, 1});
 }
