@@ -75,11 +75,6 @@ __device__ __forceinline__ void tma_load_4d_once(void *dst, const CUtensorMap *m
         : "memory");
 }
 
-__device__ __forceinline__ int div(const FastDiv &d, int n)
-{
-    return (int)((__umulhi((unsigned)n, d.mul) + (unsigned)n) >> d.shift);
-}
-
 // Four e4m3 codes to four f16 values, exact.
 __device__ __forceinline__ void e4m3x4_to_half4(uint32_t w, uint32_t &lo, uint32_t &hi)
 {

@@ -49,6 +49,13 @@ inline FastDiv fast_div(unsigned d)
     return FastDiv{(unsigned)((((uint64_t)1 << 32) * (((uint64_t)1 << s) - d)) / d + 1), s};
 }
 
+#ifdef __CUDACC__
+__device__ __forceinline__ int div(const FastDiv &d, int n)
+{
+    return (int)((__umulhi((unsigned)n, d.mul) + (unsigned)n) >> d.shift);
+}
+#endif
+
 struct PagedArgs {
     const float *q;           // [n_seq][n_q][n_head][HD]
     float *out;
@@ -121,6 +128,9 @@ struct AppendArgs {
     bool wide;                                      // every row and head starts at a multiple of 32 bytes
     int iters;                                      // head groups one warp takes for its token
     int chunks;                                     // warps per token
+    // Every number of tokens, pages and jobs is below 2^31; a 64-bit division took a warp some 500 cycles, and a job's
+    // place half a dozen of them (one token 4.2 -> 3.8 us)
+    FastDiv by_page, by_chunks, by_each, by_item, by_seq;   // page_size, chunks, n_each; jobs of a page, pages of a sequence
 };
 
 struct AppendRequest {

@@ -15,9 +15,9 @@
 // scale grows, one sweep for the codes.
 //
 // What bounds it. HBM for prompts: 7370 bfloat16 tokens of 28 + 4 heads of 128 into e4m3
-// pages 33 us, 0.81 of the copy bandwidth (three fifths of the bytes are writes); 8399
+// pages 31 us, 0.87 of the copy bandwidth (three fifths of the bytes are writes); 8399
 // float32 tokens of 16 + 2 heads of 256 into bfloat16 pages 52 us, 0.93. Launch latency for
-// a decode step: one token 4.2 us, 64 sequences of one 3.4 (a chain of position, table,
+// a decode step: one token 3.8 us, 64 sequences of one 3.1 (a chain of position, table,
 // old scale and store).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -250,11 +250,11 @@ __device__ __forceinline__ uint2 e4m3x8(const float (&x)[8], const Divisor &d)
 
 // The last s in [0, n) with value(s) <= x (value non-decreasing, value(0) <= x), by a warp.
 template <class F>
-__device__ __forceinline__ int warp_search(int n, int64_t x, int lane, F value)
+__device__ __forceinline__ int warp_search(int n, int x, int lane, F value)
 {
     int lo = 0;
     while (n > 1) {
-        const int step = (n + 31) / 32;
+        const int step = (n + 31) >> 5;
         const int i = lane * step;
         const bool le = i < n && value(lo + i) <= x;
         const int last = max(__popc(__ballot_sync(0xffffffffu, le)) - 1, 0);
@@ -264,21 +264,31 @@ __device__ __forceinline__ int warp_search(int n, int64_t x, int lane, F value)
     return lo;
 }
 
-__device__ __forceinline__ int64_t cu_at(const AppendArgs &g, int s)
+// Numbers that every warp of the call looks up, through L1 (kept behind the wait for the grid before, which makes
+// what it wrote visible). Through L2 thousands of warps asked for the same few sectors at once, which was half of
+// the time of short prompts (52 sequences of 9 to 38 tokens 13.1 -> 7.9 us, six prompts of 7370 34 -> 31).
+__device__ __forceinline__ int ld_shared_by_all(const int *p)
 {
-    return g.cu ? min(max((int64_t)ld_dep(g.cu + s), (int64_t)0), g.n_tokens) : (int64_t)s * g.n_each;
+    int v;
+    asm volatile("ld.global.ca.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ int cu_at(const AppendArgs &g, int s)
+{
+    return g.cu ? min(max(ld_shared_by_all(g.cu + s), 0), (int)g.n_tokens) : s * (int)g.n_each;
 }
 
 // One token, `iters` groups of HPW of its heads: of q, then (16-bit cache) of k and v. The loads of the next D
 // groups are always on their way. Warps in order take tokens in order: a sweep over memory (with each warp at a
 // place of its own, over its share of the tokens, prompts took a third longer).
 template <int HD, typename IN, class CT>
-__device__ __forceinline__ void token_job(const AppendArgs &g, const Stage<HD, IN> &stage, int64_t job, int lane)
+__device__ __forceinline__ void token_job(const AppendArgs &g, const Stage<HD, IN> &stage, int job, int lane)
 {
     constexpr int LPH = HD / 16, HPW = 32 / LPH, D = Stage<HD, IN>::kSlots;
     constexpr bool E8 = std::is_same<CT, CacheE4m3>::value;
-    const int64_t tok = job / g.chunks;
-    const int chunk = (int)(job - tok * g.chunks);
+    const int at_tok = div(g.by_chunks, job), chunk = job - at_tok * g.chunks;
+    const int64_t tok = at_tok;
     if (tok >= g.n_tokens) return;
     const int nq = g.q ? g.n_head : 0;
     const int heads = nq + (E8 ? 0 : 2 * g.n_kv_head);
@@ -298,15 +308,15 @@ __device__ __forceinline__ void token_job(const AppendArgs &g, const Stage<HD, I
     };
 #pragma unroll 1
     for (int i = 0; i < D; ++i) fetch(i);                         // ... while the token's position is found
-    const int s = g.cu ? warp_search(g.n_seq, tok, lane, [&](int i) { return cu_at(g, i); }) : (int)(tok / g.n_each);
+    const int s = g.cu ? warp_search(g.n_seq, at_tok, lane, [&](int i) { return cu_at(g, i); }) : div(g.by_each, at_tok);
     const int64_t end = cu_at(g, s + 1);
-    const int64_t last = ld_dep(g.positions + s);
+    const int64_t last = ld_shared_by_all(g.positions + s);
     const int64_t pos = last + 1 - (end - tok);
     int page = -1;
     int64_t off = -1;                                             // of the token's row in its page; -1: no row
     if (!E8 && tok < end) {
         if (pos >= 0 && pos < (int64_t)g.max_pages * g.page_size) {
-            const int pg = (int)((unsigned)pos / (unsigned)g.page_size);
+            const int pg = div(g.by_page, (int)pos);
             off = (pos - (int64_t)pg * g.page_size) * g.row_stride;
             page = ld_dep(g.table + (size_t)s * g.max_pages + pg);
         } else if (last != -1 && lane == 0 && chunk == 0) {
@@ -367,35 +377,34 @@ __device__ __forceinline__ float scale_for(float amax)
 // of its rows as the stage holds are read once, later ones (large pages) once for the maximum and once for
 // the codes. K's angles are computed both times, which costs less than keeping the values.
 template <int HD, typename IN>
-__device__ __forceinline__ void page_job(const AppendArgs &g, const Stage<HD, IN> &stage, int64_t job)
+__device__ __forceinline__ void page_job(const AppendArgs &g, const Stage<HD, IN> &stage, int job)
 {
     constexpr int LPH = HD / 16;
     __shared__ float sm_max[2][kAppendMost / 32];
     const int tid = threadIdx.x, lane = tid & 31, TPB = blockDim.x / LPH;
     const int per_item = g.kv_apart ? 2 * g.n_kv_head : g.n_kv_head;
-    const int which = (int)(job % per_item), kh = which % g.n_kv_head;
+    const int item = div(g.by_item, job), which = job - item * per_item;
     const int w0 = which < g.n_kv_head ? 0 : 1, w1 = g.kv_apart ? w0 + 1 : 2;   // K: 0, V: 1
-    const int64_t item = job / per_item;
+    const int kh = which - w0 * g.n_kv_head;
 
-    int s;
-    int64_t idx;                                                  // the item's page, counted from the first touched
+    int s, idx;                                                   // idx: the item's page, counted from the first touched
     if (g.cu) {
         // sequence s may touch floor(cu[s+1] / page) - floor(cu[s] / page) + 2 pages at most
-        auto first_item = [&](int i) { return cu_at(g, i) / g.page_size + 2 * (int64_t)i; };
+        auto first_item = [&](int i) { return div(g.by_page, cu_at(g, i)) + 2 * i; };
         s = warp_search(g.n_seq, item, lane, first_item);
         idx = item - first_item(s);
     } else {
-        const int64_t per = (g.n_each + g.page_size - 2) / g.page_size + 1;
-        s = (int)(item / per);
+        const int per = div(g.by_page, (int)g.n_each + g.page_size - 2) + 1;
+        s = div(g.by_seq, item);
         idx = item - s * per;
     }
     const int64_t tok0 = cu_at(g, s), tok1 = cu_at(g, s + 1);
     if (tok1 <= tok0) return;
     const int64_t cap = (int64_t)g.max_pages * g.page_size;
-    const int64_t last = ld_dep(g.positions + s), first = last + 1 - (tok1 - tok0);
+    const int64_t last = ld_shared_by_all(g.positions + s), first = last + 1 - (tok1 - tok0);
     if (idx == 0 && which == 0 && tid == 0 && last != -1 && (first < 0 || last >= cap))
         atomicOr(g.err, kErrPositionClamped);
-    const int64_t pg = max(first, (int64_t)0) / g.page_size + idx;
+    const int64_t pg = div(g.by_page, (int)min(max(first, (int64_t)0), cap)) + (int64_t)idx;
     const int64_t r0 = max(max(first, (int64_t)0), pg * g.page_size);
     const int64_t r1 = min(min(last + 1, cap), (pg + 1) * g.page_size);
     if (r0 >= r1) return;
@@ -543,15 +552,15 @@ __global__ void __launch_bounds__(kAppendMost, 3) attn_append(const AppendArgs g
     // no early start for the kernel after this one: it is the attention over this cache, whose blocks fill an SM and
     // would find it in pieces beside these (32 sequences, both calls: 171.7 us with an early start, 165.2 without)
     pdl_wait();
-    int64_t block = blockIdx.x;
+    int block = (int)blockIdx.x;
     if constexpr (std::is_same<CT, CacheE4m3>::value) {
         if (block < g.page_blocks) {
             page_job<HD, IN>(g, stage, block);
             return;
         }
-        block -= g.page_blocks;
+        block -= (int)g.page_blocks;
     }
-    token_job<HD, IN, CT>(g, stage, block * (blockDim.x / 32) + (threadIdx.x >> 5), threadIdx.x & 31);
+    token_job<HD, IN, CT>(g, stage, block * (int)(blockDim.x / 32) + (int)(threadIdx.x >> 5), threadIdx.x & 31);
 }
 
 template <int HD, typename IN, class CT>
@@ -589,6 +598,11 @@ cudaError_t launch_it(AppendArgs g, cudaStream_t stream)
     const int64_t warps = g.n_tokens * g.chunks;
     const int64_t blocks = g.page_blocks + (warps + threads / 32 - 1) / (threads / 32);
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    g.by_page = fast_div((unsigned)g.page_size);
+    g.by_chunks = fast_div((unsigned)(g.chunks > 0 ? g.chunks : 1));
+    g.by_each = fast_div((unsigned)(g.n_each > 0 ? g.n_each : 1));
+    g.by_item = fast_div((unsigned)(g.n_kv_head * (g.kv_apart ? 2 : 1)));
+    g.by_seq = fast_div((unsigned)((g.n_each + g.page_size - 2) / g.page_size + 1));
     const void *fn = reinterpret_cast<const void *>(&attn_append<HD, IN, CT>);
     e = ensure_smem_attr(fn, (int)Stage<HD, IN>::bytes(kAppendMost));
     if (e != cudaSuccess) return e;
