@@ -17,7 +17,7 @@
 // What bounds it. HBM for prompts: 7370 bfloat16 tokens of 28 + 4 heads of 128 into e4m3
 // pages 31 us, 0.87 of the copy bandwidth (three fifths of the bytes are writes); 8399
 // float32 tokens of 16 + 2 heads of 256 into bfloat16 pages 52 us, 0.93. Launch latency for
-// a decode step: one token 3.8 us, 64 sequences of one 3.1 (a chain of position, table,
+// a decode step: one token 3.5 us, 64 sequences of one 3.1 (a chain of position, table,
 // old scale and store).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -166,14 +166,22 @@ __device__ __forceinline__ void angle(int64_t pos, uint64_t step, float &c, floa
     c = (quarter + 1) & 2 ? -b : b;
 }
 
-__device__ __forceinline__ void make_turn(const AppendArgs &g, const LaneUnits &u, int64_t pos, Turn &t)
-{
-    if (!u.rot) return;
+// The steps of a lane's eight pairs, loaded before the position is known (one token 3.8 -> 3.5 us)
+struct Steps {
+    ulonglong2 st[4];
+    __device__ __forceinline__ void load(const uint64_t *steps, const LaneUnits &u)
+    {
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-        const ulonglong2 st = *reinterpret_cast<const ulonglong2 *>(g.steps + u.pair0 + j);
-        angle(pos, st.x, t.c[j], t.s[j]);
-        angle(pos, st.y, t.c[j + 1], t.s[j + 1]);
+        for (int j = 0; j < 4; ++j) st[j] = u.rot ? reinterpret_cast<const ulonglong2 *>(steps + u.pair0)[j] : make_ulonglong2(0, 0);
+    }
+};
+
+__device__ __forceinline__ void make_turn(const AppendArgs &g, const Steps &p, int64_t pos, Turn &t)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        angle(pos, p.st[j].x, t.c[2 * j], t.s[2 * j]);
+        angle(pos, p.st[j].y, t.c[2 * j + 1], t.s[2 * j + 1]);
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -308,6 +316,8 @@ __device__ __forceinline__ void token_job(const AppendArgs &g, const Stage<HD, I
     };
 #pragma unroll 1
     for (int i = 0; i < D; ++i) fetch(i);                         // ... while the token's position is found
+    Steps steps;
+    steps.load(g.steps, u);
     const int s = g.cu ? warp_search(g.n_seq, at_tok, lane, [&](int i) { return cu_at(g, i); }) : div(g.by_each, at_tok);
     const int64_t end = cu_at(g, s + 1);
     const int64_t last = ld_shared_by_all(g.positions + s);
@@ -324,7 +334,7 @@ __device__ __forceinline__ void token_job(const AppendArgs &g, const Stage<HD, I
         }
     }
     Turn tr;
-    make_turn(g, u, pos, tr);
+    if (u.rot) make_turn(g, steps, pos, tr);
     const int n = tok < end ? g.iters : 0;                        // behind the last sequence: nothing
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
@@ -423,6 +433,9 @@ __device__ __forceinline__ void page_job(const AppendArgs &g, const Stage<HD, IN
     for (int w = w0; w < w1; ++w)
 #pragma unroll 1
         for (int k = 0; k < kept && r + k * TPB < rows; ++k) stage.fetch((w - w0) * places + k, source(w, tok + r + k * TPB));
+    __shared__ __align__(16) uint64_t sm_steps[HD / 2];
+    if (w0 == 0 && tid < g.rot_dim / 4)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(sm_steps + 2 * tid)), "l"(g.steps + 2 * tid) : "memory");
     stage.commit();
     const int page = ld_dep(g.table + (size_t)s * g.max_pages + pg);
     const bool there = page >= 0 && page < g.n_pages;
@@ -471,7 +484,9 @@ __device__ __forceinline__ void page_job(const AppendArgs &g, const Stage<HD, IN
                     // one row in four from its position, the others from the one before (three products of 32-bit
                     // rounding at most)
                     if (k % 4 == 0) {
-                        make_turn(g, u, vr0 + i, tr);
+                        Steps steps;
+                        steps.load(sm_steps, u);
+                        make_turn(g, steps, vr0 + i, tr);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) turn_pair(tr.c[j], tr.s[j], by[u.pair0 + j].x, by[u.pair0 + j].y);
