@@ -110,12 +110,17 @@ void make_plan(const attn_paged_cache *c, int max_pages, int n_seq, int n_q, int
     // - while a block has few rows at full capacity (4 sequences of 8000 rows, 16 slots a KV head: head_dim 64 13.5 us
     //   with 16, 10.7 with 8; 128 15.7 and 13.4; 256 22.9 and 19.9; of 32000 rows 19.6 and 21.6, 26.2 and 28.0,
     //   44.2 and 43.5; 16-bit rows of 256 dimensions 28.4 and 33.5);
-    // - where the second 16 would be half empty (24 slots, 65000 rows: head_dim 256 127.8 and 107.5 us, 128 64.3 and
-    //   61.0, but 64 43.1 and 47.5).
+    // - where the last 16 would be half empty and 16 cost almost twice as much as 8: head_dim 256 (24, 40, 56 slots, 65000
+    //   rows: 127.8 us with 16, 107.5 with 8; 183.9 and 163.7; 237.8 and 229.5), 128 up to 24 slots (64.3 and 61.0; 40
+    //   slots 91.2 and 92.4), not 64 (43.1 and 47.5);
+    // - at head_dim 256 for short sequences, whose merges count most (28 sequences up to 1638 rows, 32 slots: 43.4 and
+    //   40.0; 60 of up to 4000, 16 slots: 138.0 and 142.2).
+    const int64_t few = c->head_dim == 256 ? 1664 : 384;
+    const bool half_empty = (need - 1) / 8 % 2 == 0;
     pl.slots = need <= 8 ? 8 : 16;
     if (need > 8 && es == 1 &&
-        (rows * seqs <= (c->head_dim == 256 ? 1664 : 384) * fill_gpu(shape(8), units(8), rows, seqs, sm_count) ||
-         (need > 16 && need <= 24 && c->head_dim >= 128)))
+        (rows * seqs <= few * fill_gpu(shape(8), units(8), rows, seqs, sm_count) ||
+         (c->head_dim == 256 && (rows <= few || half_empty)) || (c->head_dim == 128 && need <= 24 && half_empty)))
         pl.slots = 8;
     pl.qgroups = (need + pl.slots - 1) / pl.slots;
     pl.shape = shape(pl.slots);

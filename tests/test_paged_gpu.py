@@ -171,11 +171,15 @@ def test_several_query_rows_and_large_groups(pkg, kv, hd, n_q, group, page):
 
 
 @pytest.mark.parametrize("hd", [64, 128, 256])
-@pytest.mark.parametrize("n_q,group,rules", [(2, 5, {}), (5, 7, {}), (1, 13, {}), (4, 8, dict(window=60, softcap=20.0)), (17, 3, {})])
+@pytest.mark.parametrize("n_q,group,rules", [(2, 5, {}), (5, 7, {}), (1, 13, {}), (4, 8, dict(window=60, softcap=20.0)), (17, 3, {}),
+                                             (4, 8, dict(softcap=20.0, slopes=True)), (2, 7, dict(starts=[0, 0, 69, 5, 900]))])
 def test_large_groups_in_a_large_capacity(pkg, hd, n_q, group, rules):
     """8 bits: 16 slots a block where the capacity is large, whatever rows there are."""
     pool = Pool(hd + n_q, "e4m3", 2, hd, 64, (0, 1, 70, 333, 1000), extra_pages=4000)
-    attend_check(pkg, pool, n_q, group * 2, splits=(0, 1, 3), **rules)
+    r = dict(rules)
+    if r.get("slopes"):
+        r["slopes"] = [2.0 ** -(h + 1) for h in range(group * 2)]
+    attend_check(pkg, pool, n_q, group * 2, splits=(0, 1, 3), **r)
     assert pkg.attn_read_device_error() == 0
 
 
