@@ -125,6 +125,8 @@ def test_plan_for_a_given_sm_count(lib):
     assert plan(cache=_cache(**e8), n_q=4, n_seq=3) == (114, ws(114, 4, 8, 3))
     assert plan(cache=_cache(**e8), n_q=4, n_seq=9) == (152, ws(152, 2, 16, 9))
     assert plan(cache=_cache(**e8), n_q=5, n_seq=99) == (76, ws(76, 6, 8, 99))      # 20 slots: the second 16 half empty
+    # a third block an SM only where it has more than two tiles
+    assert plan(cache=_cache(n_kv_head=4, **e8), n_head=28) == (64, ws(64, 4))
     # units just over half of the resident blocks: four rounds; far more units than blocks: one block each
     assert plan(cache=_cache(n_kv_head=160), n_head=160, n_seq=2)[0] == 7
     assert plan(cache=_cache(n_kv_head=2000), n_head=2000) == (1, 0)
