@@ -554,7 +554,8 @@ def rope_append(cache, block_table, positions, k_new, v_new, q=None, q_out=None,
                 cu_tokens=None, stream=None):
     """Convenience form of attn_rope_append for torch tensors: the sizes come from the shapes --
     k_new, v_new [n_tokens, n_kv_head, head_dim] and q [n_tokens, n_head, head_dim] (or None) of one
-    type (float32, float16 or bfloat16), dense within a token and of any stride between tokens;
+    type (float32, float16 or bfloat16), dense within a token and of any stride between tokens that
+    do not overlap (a row repeated by expand is refused; pass its contiguous() copy);
     block_table int32 [n_seq, max_pages]; positions int32 [n_seq]; cu_tokens int32 [n_seq + 1], or
     None for the same number of tokens in every sequence. `q_out` (float32) is allocated when not
     given (on the current stream, so another `stream` needs it given). Returns q_out (None without
@@ -612,7 +613,11 @@ def rope_append(cache, block_table, positions, k_new, v_new, q=None, q_out=None,
     if n_tokens <= 1:
         qs, kst, vst = 0, 0, 0                       # one token has no stride
     else:
+        # the C call takes a stride of 0 for dense, and would read past the end of a row repeated by expand
         kst, vst = ks[0], vs[0]
+        if kst < n_kv * hd or vst < n_kv * hd or qs < n_head * hd:
+            _refuse((), cache.device, [(st >= h * hd, "%s must not have tokens that overlap" % name) for name, st, h in
+                                       (("k_new", kst, n_kv), ("v_new", vst, n_kv), ("q", qs, n_head))])
     status = (_lib or load()).attn_rope_append(
         cache._address, block_table.data_ptr(), max_pages, positions.data_ptr(), cp, n_seq, n_tokens, qp,
         k_new.data_ptr(), v_new.data_ptr(), qs, kst, vst, in_type, op, n_head, rp,

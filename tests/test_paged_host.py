@@ -277,3 +277,62 @@ def test_paged_constants_match_the_header():
     assert len(found) == 9
     for name, val in found:
         assert getattr(pkg, name) == int(val, 0), name
+
+
+# ---------------------------------------------------------------------------
+# The torch forms up to the library's door: host tensors that say they are on device 0, and a
+# recorder in place of the library, so that valid arguments get through and each refusal is the
+# check's own.
+# ---------------------------------------------------------------------------
+class Recorder:
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return pkg.ATTN_OK
+        return call
+
+
+@pytest.fixture
+def door(lib, monkeypatch):
+    torch = pytest.importorskip("torch")
+    rec = Recorder()
+    pkg._torch_module()
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
+    monkeypatch.setattr(pkg, "_same_device", lambda d: None)
+    monkeypatch.setattr(pkg, "_device", lambda: 0)
+    monkeypatch.setattr(pkg, "_raw_stream", lambda i: 0)
+    monkeypatch.setattr(pkg, "_alloc", lambda size, stream: 1 << 20)
+    monkeypatch.setattr(pkg, "_free", lambda p: None)
+    monkeypatch.setattr(pkg, "attn_paged_plan", lambda *a: (4, 4096))
+    monkeypatch.setattr(pkg, "_lib", rec)
+    return rec
+
+
+def _pool_and_ids():
+    import torch
+    k = torch.zeros(3, 16, 2, 64, dtype=torch.float16)
+    return (pkg.PagedCache(k, k.clone()), torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+
+
+def test_tokens_that_overlap_are_refused(door):
+    """A row repeated by expand has a stride of 0, which the C call takes for dense: it would be read
+    past its end. Strides below a token's elements are refused with it."""
+    import torch
+    cache, table, pos = _pool_and_ids()
+    good = {"k_new": torch.zeros(4, 2, 64), "v_new": torch.zeros(4, 2, 64), "q": torch.zeros(4, 4, 64)}
+    pkg.rope_append(cache, table, pos, **good)
+    wide = torch.zeros(4, 8, 64)
+    pkg.rope_append(cache, table, pos, k_new=wide[:, 4:6], v_new=wide[:, 6:], q=wide[:, :4])
+    assert [c[1][10:13] for c in door.calls] == [(256, 128, 128), (512, 512, 512)]
+    for name, x in good.items():
+        for bad in (x[:1].expand(4, -1, -1), torch.zeros(4 * 64 * 4).as_strided(x.shape, (64, 64, 1))):
+            with pytest.raises(ValueError, match="%s must not have tokens that overlap" % name):
+                pkg.rope_append(cache, table, pos, **dict(good, **{name: bad}))
+    assert len(door.calls) == 2
+    # one token has no stride
+    one = {n: x[:1].as_strided(x[:1].shape, (0, 64, 1)) for n, x in good.items()}
+    pkg.rope_append(cache, table, pos, **one)
+    assert door.calls[-1][1][10:13] == (0, 0, 0)
