@@ -480,7 +480,7 @@ def _refuse(checks, device, shapes):
 class PagedCache:
     """The pool of a paged cache: k, v [n_pages, page_size, n_kv_head, head_dim] float16, bfloat16
     or float8_e4m3fn, as torch tensors of any strides over the first three dimensions (the same for
-    both; the last one dense); k_scale, v_scale float32 [n_pages, n_kv_head] for float8_e4m3fn.
+    both, at least head_dim; the last one dense); k_scale, v_scale float32 [n_pages, n_kv_head] for float8_e4m3fn.
     Holds the tensors and the C structure that describes them."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
@@ -495,6 +495,8 @@ class PagedCache:
         strides, vstrides = ([t.stride(i) if t.shape[i] > 1 else t.shape[3] for i in range(3)] for t in (k, v))
         if strides != vstrides or k.stride(3) != 1 or v.stride(3) != 1:
             raise ValueError("k and v must have the same strides, and dense rows")
+        if min(strides) < k.shape[3]:        # three strides of 0 would stand for a dense pool
+            raise ValueError("rows of k and v must not overlap (strides below head_dim)")
         if v.device != k.device:
             raise ValueError("k and v must be on the same device")
         e4m3 = k.dtype == torch.float8_e4m3fn

@@ -336,3 +336,23 @@ def test_tokens_that_overlap_are_refused(door):
     one = {n: x[:1].as_strided(x[:1].shape, (0, 64, 1)) for n, x in good.items()}
     pkg.rope_append(cache, table, pos, **one)
     assert door.calls[-1][1][10:13] == (0, 0, 0)
+
+
+def test_pools_whose_rows_overlap_are_refused(lib):
+    """A pool expanded from one row has three strides of 0, which the C call takes for a dense pool: an
+    append would write past its allocation. Pages, rows or heads that lie on each other are refused alike."""
+    torch = pytest.importorskip("torch")
+    shape = (3, 16, 2, 64)
+    row = torch.zeros(64, dtype=torch.float16)
+    for bad in (row.expand(shape), torch.zeros(1, 16, 2, 64, dtype=torch.float16).expand(shape),
+                torch.zeros(3, 1, 2, 64, dtype=torch.float16).expand(shape),
+                torch.zeros(3, 16, 1, 64, dtype=torch.float16).expand(shape),
+                torch.zeros(9999, dtype=torch.float16).as_strided(shape, (2048, 128, 32, 1)),
+                row.view(torch.uint8)[:64].expand(shape).view(torch.float8_e4m3fn)):
+        scales = (torch.ones(3, 2), torch.ones(3, 2)) if bad.dtype == torch.float8_e4m3fn else ()
+        with pytest.raises(ValueError, match="must not overlap"):
+            pkg.PagedCache(bad, bad, *scales)
+    # a dimension of one element has no stride, and any other order of the three is fine
+    pkg.PagedCache(row.expand(1, 1, 1, 64), row.expand(1, 1, 1, 64))
+    k = torch.zeros(3, 2, 16, 64, dtype=torch.float16).transpose(1, 2)
+    pkg.PagedCache(k, k)
