@@ -407,7 +407,7 @@ def attn_decode_paged(cache, block_table, max_pages, positions, q, out, n_seq, n
         workspace_bytes = workspace.nbytes
     if rules is not None:
         softcap, window, slopes, starts = rules
-        rules = _RulesStruct(softcap, window, _ptr(slopes), _ptr(starts))
+        rules = _rules(softcap, window, _ptr(slopes), _ptr(starts))
         rules_p = ctypes.addressof(rules)
     else:
         rules_p = None
@@ -415,6 +415,13 @@ def attn_decode_paged(cache, block_table, max_pages, positions, q, out, n_seq, n
                                     _ptr(q), _ptr(out), n_seq, n_q, n_head, scale, rules_p,
                                     n_splits, _ptr(workspace), workspace_bytes, _stream(stream)),
            "attn_decode_paged")
+
+
+def _rules(softcap, window, slopes, starts):
+    r = _RulesStruct(softcap, window, slopes, starts)
+    if softcap and not r.softcap:
+        raise ValueError("softcap is 0 in 32 bits, which stands for none")
+    return r
 
 
 def _struct(x):
@@ -670,8 +677,8 @@ def paged_decode_attention(cache, block_table, positions, q, scale=None, out=Non
         if starts is not None and not (starts.dtype is i32 and starts.get_device() == index and
                                        starts.shape == (n_seq,) and starts.is_contiguous()):
             _refuse((("starts", starts, i32, True),), cache.device, ((False, "starts must be [n_seq]"),))
-        kept = _RulesStruct(softcap, window, slopes.data_ptr() if slopes is not None else None,
-                            starts.data_ptr() if starts is not None else None)
+        kept = _rules(softcap, window, slopes.data_ptr() if slopes is not None else None,
+                      starts.data_ptr() if starts is not None else None)
         rules = ctypes.addressof(kept)
     if n_seq == 0:
         return out

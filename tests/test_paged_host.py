@@ -356,3 +356,20 @@ def test_pools_whose_rows_overlap_are_refused(lib):
     pkg.PagedCache(row.expand(1, 1, 1, 64), row.expand(1, 1, 1, 64))
     k = torch.zeros(3, 2, 16, 64, dtype=torch.float16).transpose(1, 2)
     pkg.PagedCache(k, k)
+
+
+def test_a_softcap_that_32_bits_take_for_none_is_refused(door):
+    """Below the smallest 32-bit number a cap would arrive as 0, which stands for no cap."""
+    import torch
+    cache, table, pos = _pool_and_ids()
+    q = torch.zeros(1, 4, 64)
+    for softcap in (0.0, 2.0 ** -40, 30.0):
+        pkg.paged_decode_attention(cache, table, pos, q, softcap=softcap)
+        pkg.attn_decode_paged(cache, table, 1, pos, q, q, 1, 1, 4, 0.1, (softcap, 0, None, None), stream=0)
+    n = len(door.calls)
+    for softcap in (1e-50, -1e-50, 5e-324):
+        with pytest.raises(ValueError, match="softcap"):
+            pkg.paged_decode_attention(cache, table, pos, q, softcap=softcap)
+        with pytest.raises(ValueError, match="softcap"):
+            pkg.attn_decode_paged(cache, table, 1, pos, q, q, 1, 1, 4, 0.1, (softcap, 0, None, None), stream=0)
+    assert len(door.calls) == n
