@@ -152,6 +152,7 @@ attn_status attn_rope_steps(int rot_dim, double base, int scaling, double factor
         return ATTN_ERR_INVALID_ARG;
     const double two_pi = 6.283185307179586476925;
     if (scaling == ATTN_ROPE_BASE) base *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
+    if (!std::isfinite(base)) return ATTN_ERR_INVALID_ARG;     // every pair but the first would stand still
     uint64_t out[128];
     for (int i = 0; i < rot_dim / 2; ++i) {
         double f = std::pow(base, -2.0 * i / rot_dim);

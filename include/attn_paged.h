@@ -108,7 +108,8 @@ typedef struct {
  * modulo 2^64 is the angle of that position without a loss that grows with
  * it: the angle is off by at most position * f_i * 2^-50 radians.
  *   rot_dim  as in attn_rope; base finite and >= 1; scaling ATTN_ROPE_*
- *   factor   > 0 and finite (not ATTN_ROPE_PLAIN); low_turns < high_turns and
+ *   factor   > 0 and finite (not ATTN_ROPE_PLAIN), the enlarged base of
+ *            ATTN_ROPE_BASE finite too; low_turns < high_turns and
  *            trained_len >= 1 for ATTN_ROPE_BANDS. f_i must stay below 2 pi.
  */
 attn_status attn_rope_steps(int rot_dim, double base, int scaling, double factor, double low_turns,

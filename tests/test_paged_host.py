@@ -373,3 +373,14 @@ def test_a_softcap_that_32_bits_take_for_none_is_refused(door):
         with pytest.raises(ValueError, match="softcap"):
             pkg.attn_decode_paged(cache, table, 1, pos, q, q, 1, 1, 4, 0.1, (softcap, 0, None, None), stream=0)
     assert len(door.calls) == n
+
+
+def test_rope_steps_of_an_enlarged_base_past_64_bits(lib):
+    """base * factor^(rot_dim / (rot_dim - 2)) that overflows would leave every pair but the first unturned."""
+    buf = (ctypes.c_uint64 * 128)()
+    a = ctypes.addressof(buf)
+    assert lib.attn_rope_steps(128, 1e300, pkg.ATTN_ROPE_BASE, 1e10, 0.0, 0.0, 0, a) == INVALID
+    assert lib.attn_rope_steps(16, 1e4, pkg.ATTN_ROPE_BASE, 1e300, 0.0, 0.0, 0, a) == INVALID
+    assert all(x == 0 for x in buf)
+    assert lib.attn_rope_steps(128, 1e300, pkg.ATTN_ROPE_BASE, 1e6, 0.0, 0.0, 0, a) == OK
+    assert buf[1] > 0
