@@ -384,3 +384,102 @@ def test_rope_steps_of_an_enlarged_base_past_64_bits(lib):
     assert all(x == 0 for x in buf)
     assert lib.attn_rope_steps(128, 1e300, pkg.ATTN_ROPE_BASE, 1e6, 0.0, 0.0, 0, a) == OK
     assert buf[1] > 0
+
+
+def _each_refused(call, good, cases, door):
+    """`call` with `good` reaches the library; with each of `cases` it raises that error first."""
+    call(**good)
+    n = len(door.calls)
+    for bad, error, message in cases:
+        with pytest.raises(error, match=message):
+            call(**dict(good, **bad))
+        assert len(door.calls) == n, bad
+    call(**good)
+    assert len(door.calls) == n + 1
+
+
+def test_each_refusal_of_the_attention_call(door):
+    import torch
+    cache, table, pos = _pool_and_ids()
+    i32, f16 = torch.int32, torch.float16
+    good = dict(block_table=table, positions=pos, q=torch.zeros(1, 4, 64), out=torch.zeros(1, 4, 64),
+                slopes=torch.zeros(4), starts=torch.zeros(1, dtype=i32), window=5, n_splits=3)
+    disagree = "disagree on n_seq or head_dim"
+    _each_refused(lambda **a: pkg.paged_decode_attention(cache, **a), good, [
+        (dict(q=torch.zeros(4, 64)), ValueError, "q must be .n_seq"),
+        (dict(q=torch.zeros(1, 1, 1, 4, 64)), ValueError, "q must be .n_seq"),
+        (dict(q=good["q"].double()), TypeError, "q must be float32"),
+        (dict(q=good["q"].half()), TypeError, "q must be float32"),
+        (dict(q=torch.zeros(2, 4, 64)), ValueError, disagree),
+        (dict(q=torch.zeros(1, 4, 32)), ValueError, disagree),
+        (dict(q=torch.zeros(1, 64, 4).transpose(1, 2)), ValueError, "q must be contiguous"),
+        (dict(block_table=table.long()), TypeError, "block_table must be int32"),
+        (dict(block_table=table[0]), ValueError, "block_table must be .n_seq, max_pages"),
+        (dict(block_table=torch.zeros(1, 4, dtype=i32)[:, ::2]), ValueError, "block_table must be contiguous"),
+        (dict(positions=pos.long()), TypeError, "positions must be int32"),
+        (dict(positions=torch.zeros(2, dtype=i32)), ValueError, "positions .n_seq"),
+        (dict(positions=torch.zeros(1, 1, dtype=i32)), ValueError, "positions .n_seq"),
+        (dict(out=torch.zeros(1, 4, 32)), ValueError, "out must have the shape of q"),
+        (dict(out=torch.zeros(1, 4, 64, dtype=f16)), TypeError, "out must be float32"),
+        (dict(out=torch.zeros(1, 64, 4).transpose(1, 2)), ValueError, "out must be contiguous"),
+        (dict(slopes=torch.zeros(3)), ValueError, "slopes must be .n_head"),
+        (dict(slopes=torch.zeros(4, dtype=f16)), TypeError, "slopes must be float32"),
+        (dict(slopes=torch.zeros(8)[::2]), ValueError, "slopes must be contiguous"),
+        (dict(starts=torch.zeros(1)), TypeError, "starts must be int32"),
+        (dict(starts=torch.zeros(2, dtype=i32)), ValueError, "starts must be .n_seq"),
+        (dict(window=-1), ValueError, "window and n_splits"),
+        (dict(window=1 << 31), ValueError, "window and n_splits"),
+        (dict(n_splits=-1), ValueError, "window and n_splits"),
+        (dict(n_splits=1 << 32), ValueError, "window and n_splits"),
+        (dict(stream=7), ValueError, "stream must be the current stream"),
+    ], door)
+
+
+def test_each_refusal_of_the_append_call(door, monkeypatch):
+    import torch
+    cache, _, _ = _pool_and_ids()
+    i32, f16 = torch.int32, torch.float16
+    table, pos = torch.zeros(2, 1, dtype=i32), torch.zeros(2, dtype=i32)
+    x = torch.zeros(2, 2, 64)
+    q = torch.zeros(2, 4, 64)
+    rope = pkg.Rope(64, device="cpu")
+    assert rope._index == 0
+    far = pkg.Rope(64, device="cpu")
+    far._index = 1
+    good = dict(block_table=table, positions=pos, k_new=x, v_new=x, q=q, q_out=torch.zeros(2, 4, 64), rope=rope,
+                cu_tokens=torch.tensor([0, 1, 2], dtype=i32))
+    shape = "k_new and v_new must be .n_tokens"
+    _each_refused(lambda **a: pkg.rope_append(cache, **a), good, [
+        (dict(k_new=x.double()), TypeError, "k_new must be float32, float16 or bfloat16"),
+        (dict(k_new=x.long()), TypeError, "k_new must be float32, float16 or bfloat16"),
+        (dict(v_new=x.half()), TypeError, "v_new must be float32"),
+        (dict(v_new=torch.zeros(3, 2, 64)), ValueError, shape),
+        (dict(k_new=torch.zeros(2, 3, 64), v_new=torch.zeros(2, 3, 64)), ValueError, shape),
+        (dict(k_new=torch.zeros(2, 2, 32), v_new=torch.zeros(2, 2, 32)), ValueError, shape),
+        (dict(k_new=torch.zeros(2, 64, 2).transpose(1, 2)), ValueError, "dense within a token"),
+        (dict(v_new=torch.zeros(2, 4, 64)[:, ::2]), ValueError, "dense within a token"),
+        (dict(block_table=table.long()), TypeError, "block_table must be int32"),
+        (dict(block_table=table[0]), ValueError, "block_table must be .n_seq, max_pages"),
+        (dict(positions=pos.long()), TypeError, "positions must be int32"),
+        (dict(positions=torch.zeros(3, dtype=i32)), ValueError, "positions .n_seq"),
+        (dict(q=q[0]), ValueError, "q must be .n_tokens"),
+        (dict(q=torch.zeros(3, 4, 64)), ValueError, "q must be .n_tokens"),
+        (dict(q=q.half()), TypeError, "q must be float32"),
+        (dict(q=torch.zeros(2, 64, 4).transpose(1, 2)), ValueError, "q must be .n_tokens"),
+        (dict(q_out=torch.zeros(2, 4, 64, dtype=f16)), TypeError, "q_out must be float32"),
+        (dict(q_out=torch.zeros(2, 2, 64)), ValueError, "q_out must have the shape of q"),
+        (dict(q_out=torch.zeros(2, 64, 4).transpose(1, 2)), ValueError, "q_out must be contiguous"),
+        (dict(q=None), ValueError, "q_out without q"),
+        (dict(q_out=None, stream=7), ValueError, "q_out must be given"),
+        (dict(cu_tokens=torch.zeros(3)), TypeError, "cu_tokens must be int32"),
+        (dict(cu_tokens=torch.zeros(2, dtype=i32)), ValueError, "cu_tokens must be .n_seq"),
+        (dict(cu_tokens=torch.zeros(6, dtype=i32)[::2]), ValueError, "cu_tokens must be contiguous"),
+        (dict(rope=far), ValueError, "rope must be on the cache's device"),
+    ], door)
+    # another device than the current one
+    monkeypatch.setattr(pkg, "_device", lambda: 1)
+    for call in (lambda: pkg.rope_append(cache, **good), lambda: pkg.paged_decode_attention(cache, table, pos, q)):
+        n = len(door.calls)
+        with pytest.raises(ValueError):
+            call()
+        assert len(door.calls) == n
