@@ -530,14 +530,14 @@ __device__ __forceinline__ void page_job(const AppendArgs &g, const Stage<HD, IN
             const float o = sm_old[w];
             float m = 0.f;
             for (int i = 0; i < (int)blockDim.x / 32; ++i) m = fmaxf(m, sm_max[w][i]);
-            const bool had = o > 0.f && o < INFINITY;
-            const float n = had ? fmaxf(o, scale_for(m)) : scale_for(m);
+            const float n = fabsf(o) < INFINITY ? fmaxf(fabsf(o), scale_for(m)) : scale_for(m);
             if (tid == 0) {
                 sm_now[w] = n;
                 (w ? g.v_scale : g.k_scale)[sc] = n;
             }
-            if (!had || !(n > o)) continue;
-            const Divisor d(n);                                  // rows [0, at) at the new scale
+            if (at == 0 || n == o || !(fabsf(o) < INFINITY)) continue;
+            // rows [0, at) at the new scale: exact but for the codes' rounding where n is a power of two or -o
+            const float ratio = o / n;
 #pragma unroll 1
             for (int i = r; i < at; i += TPB) {
                 uint8_t *p = static_cast<uint8_t *>(w ? g.v : g.k) + vbase + i * g.row_stride + 16 * l;
@@ -550,7 +550,7 @@ __device__ __forceinline__ void page_job(const AppendArgs &g, const Stage<HD, IN
                         "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
                         : "=r"(f0), "=r"(f1) : "r"(cw[k]));
                     const float2 v0 = kv2_to_float2<__half>(f0), v1 = kv2_to_float2<__half>(f1);
-                    cw[k] = to_e4m3x2(d(v0.x * o), d(v0.y * o)) | to_e4m3x2(d(v1.x * o), d(v1.y * o)) << 16;
+                    cw[k] = to_e4m3x2(v0.x * ratio, v0.y * ratio) | to_e4m3x2(v1.x * ratio, v1.y * ratio) << 16;
                 }
                 *reinterpret_cast<uint4 *>(p) = c;
             }

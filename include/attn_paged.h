@@ -56,7 +56,8 @@ extern "C" {
  *   page_size   a multiple of 16, at most 1024
  *   k_scale, v_scale  E4M3 only: float [n_pages][n_kv_head], dense; the value of
  *               an element is its code times the scale of its page and head.
- *               attn_rope_append writes powers of two between 2^-60 and 2^60;
+ *               attn_rope_append writes powers of two between 2^-60 and 2^60, or
+ *               the magnitude of what it finds on a page filled elsewhere;
  *               attention takes any finite scale of magnitude up to 2^60.
  */
 typedef struct {
@@ -137,12 +138,16 @@ attn_status attn_rope_steps(int rot_dim, double base, int scaling, double factor
  *   rope         NULL: nothing is rotated (q is converted)
  * Angles and products are taken in 32 bits from the exact fixed-point angle;
  * each result is rounded once to the type it is stored in.
- * E4M3: the new rows of a page and head, with the scale the page has where it
- * holds rows before them, set the scale to the smallest power of two s with
- * |x| <= 448 s that is not below the page's; rows before them are rescaled where
- * it grows (exact but for values that fall below 2^-6 s). The first row of a page starts its
- * scale afresh. Infinite elements take the largest code, NaN stays NaN, and
- * neither counts for the scale.
+ * E4M3: the new rows of a page and head set its scale to the smallest power of
+ * two s (2^-60 .. 2^60) with |x| <= 448 s, or, where the page holds rows before
+ * them, to the magnitude of the scale it has if that is larger. The rows
+ * before them keep their values: where the scale changes, each code becomes the
+ * one nearest to its value at the new scale (with powers of two exact but for
+ * values that fall below 2^-6 s; a scale of 0, negative or no power of two, of a
+ * page filled elsewhere, is taken for what it is; one that is not finite counts
+ * as none, and the codes stay). The first row of a page starts its scale
+ * afresh. Infinite elements take the largest code, as those past 448 * 2^60
+ * do, NaN stays NaN, and neither infinities nor NaN count for the scale.
  * Each page may be written by one sequence of the call only, and stand at one
  * place of its table (what a page written twice holds is not defined). A token whose
  * position lies outside [0, max_pages * page_size) is not written and sets

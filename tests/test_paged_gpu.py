@@ -861,3 +861,53 @@ def test_a_stream_of_the_callers(pkg):
     assert bool((pool.dev[0][pool.table[0, 6], 99 % 16] == 1).all())
     with pytest.raises(ValueError):
         pkg.paged_decode_attention(cache, table, pos, q, stream=s)
+
+
+# ---------------------------------------------------------------------------
+# What an append finds in a page, angles at their borders, weights of small scales.
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("n_kv", [1, 40])             # K and V in jobs of their own, or together
+def test_append_onto_pages_of_any_scale(pkg, n_kv, interleaved):
+    """Pages filled elsewhere, with scales of 0, negative or no power of two, get a row: the rows that they
+    hold keep their values, as near as a code at the new scale comes. With old scale o and the rows' own
+    smallest power of two n, the new scale is max(|o|, n) and each kept code the rounding of value * (o / new),
+    a product rounded to 32 bits."""
+    import torch
+    rng = np.random.default_rng(n_kv)
+    old = np.float32([0.0, -0.0, -0.5, -0.3, 0.3, 7.0, -7.0, 2.0 ** -60, -2.0 ** -60, 2.0 ** 60, -2.0 ** 60, 0.25, 1e-3])
+    n, hd, page, at = len(old), 64, 16, 5
+    for size in (1e-4, 100.0, 1e5):
+        x = np.clip(rng.standard_normal((n, n_kv, hd)), -3, 3).astype(np.float32) * np.float32(size)
+        codes = [rng.integers(0, 256, (n, page, n_kv, hd)).astype(np.uint8) for _ in range(2)]
+        scales = [np.repeat(old[:, None], n_kv, 1), np.repeat(np.roll(old, 3)[:, None], n_kv, 1)]
+        dev, dsc = [tt(c) for c in codes], [tt(s) for s in scales]
+        cache = pkg.PagedCache(dev[0].view(torch.float8_e4m3fn), dev[1].view(torch.float8_e4m3fn), *dsc)
+        table = tt(np.arange(n, dtype=np.int32)[:, None])
+        # position 0 turns nothing but goes through the rotation: the angle of the row's own position is 0
+        rope = pkg.Rope(hd, interleaved=interleaved)
+        rope.steps.zero_()
+        pkg.rope_append(cache, table, tt(np.full(n, at, np.int32)), tt(x), tt(-x), rope=rope)
+        for i, rows in ((0, x), (1, -x)):
+            want, now = codes[i].copy(), np.zeros((n, n_kv), np.float32)
+            for p in range(n):
+                for h in range(n_kv):
+                    o = scales[i][p, h]
+                    now[p, h] = max(abs(o), np.float32(ref.scale_for(float(np.abs(rows[p, h]).max()))))
+                    kept = np.float32(ref.VALUES[codes[i][p, :at, h]]) * np.float32(o / now[p, h])
+                    new = ref.to_e4m3(kept)
+                    # a NaN code stays one, whatever its sign
+                    nan = np.isnan(ref.VALUES[codes[i][p, :at, h]])
+                    want[p, :at, h] = np.where(nan, 0x7F, new)
+                    want[p, at, h] = ref.to_e4m3(rows[p, h] / now[p, h])
+            got = dev[i].cpu().numpy()
+            was_nan = (codes[i] & 0x7F) == 0x7F
+            was_nan[:, at:] = False
+            got = np.where(was_nan & ((got & 0x7F) == 0x7F), 0x7F, got)
+            # nothing to rescale: the codes are left as they are
+            same = (now == scales[i])[:, None, :, None] & (np.arange(page) < at)[None, :, None, None]
+            want = np.where(same & ~was_nan, codes[i], want)
+            np.testing.assert_array_equal(dsc[i].cpu().numpy(), now)
+            zero = lambda c: np.where((c & 0x7F) == 0, 0, c)                # the sign of a 0 is not looked at
+            np.testing.assert_array_equal(zero(got), zero(want), err_msg="size %g, tensor %d" % (size, i))
+    assert pkg.attn_read_device_error() == 0
