@@ -140,15 +140,16 @@ struct Turn {
     float c[8], s[8];
 };
 
-// Sine and cosine of `pos` steps, to about an ulp. The wrapping product is the angle in 2^-64 turns; its upper
-// half, rounded to a quarter turn, leaves r in [-1/8, 1/8] turns, exactly. There the Taylor series of sine
+// Sine and cosine of `pos` steps, to 4.4 2^-24 + 2 pi 2^-32. The wrapping product is the angle in 2^-64 turns; the
+// quarter turn nearest to its upper half leaves r in [-1/8, 1/8] turns, an integer in 2^-32 turns without a loss
+// (wrapping too, so unsigned), then rounded to 24 bits. There the Taylor series of sine
 // (to x^9, remainder 2e-9) and cosine (to x^10, 1e-10) hold, and the quarter turns swap them and set signs.
 // (sincospif made the rotation of a token the larger part of a warp's time.)
 __device__ __forceinline__ void angle(int64_t pos, uint64_t step, float &c, float &s)
 {
-    const int hi = (int)(((uint64_t)pos * step) >> 32);
-    const int quarter = (int)(((unsigned)hi + 0x20000000u) >> 30);
-    const float x = (float)(hi - (int)((unsigned)quarter << 30)) * 1.4629180792671596e-9f;   // 2 pi 2^-32
+    const unsigned hi = (unsigned)(((uint64_t)pos * step) >> 32);
+    const unsigned quarter = (hi + 0x20000000u) >> 30;
+    const float x = (float)(int)(hi - (quarter << 30)) * 1.4629180792671596e-9f;   // 2 pi 2^-32
     const float z = x * x;
     float ps = 2.7557319e-6f;                        // 1 / 9!
     ps = fmaf(ps, z, -1.9841270e-4f);                // 1 / 7!

@@ -911,3 +911,27 @@ def test_append_onto_pages_of_any_scale(pkg, n_kv, interleaved):
             zero = lambda c: np.where((c & 0x7F) == 0, 0, c)                # the sign of a 0 is not looked at
             np.testing.assert_array_equal(zero(got), zero(want), err_msg="size %g, tensor %d" % (size, i))
     assert pkg.attn_read_device_error() == 0
+
+
+def test_angles_at_every_border(pkg):
+    """A step of any 64-bit number at position 1: the angle is that number of 2^-64 turns, also beside the
+    eighths of a turn where the kernel goes from one quarter to the next."""
+    import torch
+    edges = [(e << 61) + d for e in range(8) for d in (-(1 << 33), -(1 << 32), -1, 0, 1, 1 << 32, 1 << 33)]
+    steps = [e % (1 << 64) for e in edges] + [0x5A << 56, 0x6B << 56, 0x7F << 56, 0xE1 << 56, 3, (1 << 64) - 3] * 2
+    steps = (steps + [0] * 128)[:128]
+    rope = pkg.Rope(256)
+    rope.steps.copy_(torch.tensor([s - (1 << 64) if s >> 63 else s for s in steps]))
+    pool = Pool(0, "f16", 1, 256, 16, (16,))
+    q = np.zeros((1, 1, 256), np.float32)
+    q[..., :128] = 1.0                                     # (1, 0) turned is (cos, sin)
+    k = torch.zeros(1, 1, 256, device="cuda")
+    for pos in (1, 3, 5):
+        out = pkg.rope_append(pool.cache(pkg), tt(pool.table), tt(np.int32([pos])), k, k, q=tt(q), rope=rope)
+        turns = np.array([(pos * s % 2 ** 64) / 2.0 ** 64 for s in steps])
+        want = np.concatenate([np.cos(2 * np.pi * turns), np.sin(2 * np.pi * turns)])[None, None]
+        # 2 pi 2^-32 for the half of the angle that is left off; three roundings of the remainder of at most pi / 4
+        # (to 24 bits, the constant, their product: 2^-24 of it each); the series: half a 2^-24 for the result (at most
+        # 1) and, for the terms added to x or 1 before (together below 0.5, four roundings each), 1.5 times 2^-24
+        bound = 2 * np.pi * 2.0 ** -32 + 3 * np.pi / 4 * 2.0 ** -24 + 2 * 2.0 ** -24
+        check(out, want, np.full(want.shape, bound), "pos %d" % pos)
