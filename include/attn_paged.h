@@ -200,7 +200,13 @@ typedef struct {
  *                may run at once need workspaces of their own).
  * q and the softmax weights are carried in 16-bit parts (two of binary16, 22
  * bits, or three of bfloat16, 24), sums in 32 bits, so that the result has about
- * the accuracy of 32-bit arithmetic on the values the cache stands for.
+ * the accuracy of 32-bit arithmetic on the values the cache stands for. Two parts
+ * of binary16 (F16 and E4M3 caches) end at 2^-25: an element of q is carried to
+ * 2^-22 of itself or 2^-39 of its row's largest, and a weight times the V scale
+ * of its page to 2^-22 of itself or 2^-31 of the query row's largest such
+ * product, whichever is more. So rows whose product lies r < 2^-9 times below
+ * the largest count to 2^-31 / r of their part, which shows only in dimensions
+ * where the rows of larger products hold about 0.
  */
 attn_status attn_decode_paged(const attn_paged_cache *cache, const int32_t *block_table, int max_pages,
                               const int32_t *positions, const float *q, float *out, int n_seq, int n_q,

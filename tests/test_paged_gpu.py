@@ -935,3 +935,51 @@ def test_angles_at_every_border(pkg):
         # 1) and, for the terms added to x or 1 before (together below 0.5, four roundings each), 1.5 times 2^-24
         bound = 2 * np.pi * 2.0 ** -32 + 3 * np.pi / 4 * 2.0 ** -24 + 2 * 2.0 ** -24
         check(out, want, np.full(want.shape, bound), "pos %d" % pos)
+
+
+@pytest.mark.parametrize("spread", [0, 8, 20, 28])
+@pytest.mark.parametrize("hd,n_q,group", [(64, 1, 4), (128, 1, 8), (128, 3, 4), (256, 2, 8)])
+def test_weights_under_small_scales_by_dimension(pkg, spread, hd, n_q, group):
+    """Dimensions that only pages of a small V scale fill, beside pages of a scale 2^spread times as large
+    that hold 0 there. A row's weight times its V scale is carried to 2^-22 of itself or 2^-31 of the largest
+    such product (the f16 parts end at 2^-25, the largest lies at 2^6 or above), so that, with w the
+    normalised weights and d the error of a score, a dimension is off by at most
+        (e^2d - 1 + 2^-22 + 2^-21 + 2^-20) sum_j w_j |v_j|  +  2^-31 max_j(w_j vs_j) sum_j |code_j|,
+    2^-21 for the exponential and 2^-20 for the sums."""
+    page, ctx, n_kv = 16, 96, 2
+    pool = Pool(60 + spread, "e4m3", n_kv, hd, page, (ctx,))
+    rng = np.random.default_rng(spread)
+    small = pool.table[0, 1::2]
+    small = small[(small >= 0) & (small < pool.n_pages)]
+    large = pool.table[0, 0:ctx // page:2]
+    # scores of about 1, so that pages of both kinds weigh
+    kc = ref.to_e4m3(rng.standard_normal(pool.host[0].shape) * 20)
+    pool.host[0], pool.scale[0] = kc, np.full(pool.scale[0].shape, 2.0 ** -4)
+    codes = pool.host[1]
+    codes[large, :, :, hd // 2:] = 0
+    codes[small, :, :, hd // 2:] = ref.to_e4m3(rng.uniform(50, 400, codes[small, :, :, hd // 2:].shape))
+    pool.scale[1] = np.ones_like(pool.scale[1])
+    pool.scale[1][small] = 2.0 ** -spread
+    import torch
+    pool.dev = [tt(c).view(torch.float8_e4m3fn) for c in pool.host]
+    pool.dscale = [tt(c.astype(np.float32)) for c in pool.scale]
+    n_head = n_kv * group
+    q = rng.standard_normal((1, n_q, n_head, hd)).astype(np.float32)
+    out = pkg.paged_decode_attention(pool.cache(pkg), tt(pool.table), tt(np.int32([ctx - 1])), tt(q))
+    k, v = pool.rows(0)[0], pool.rows(1)[0]
+    vs = np.repeat(pool.scale[1][pool.table[0, :ctx // page]], page, 0)
+    want, bound = np.zeros(q.shape), np.zeros(q.shape)
+    for t in range(n_q):
+        seen = ctx - n_q + t + 1
+        for h in range(n_head):
+            x, kk, vv, s = q[0, t, h].astype(np.float64), k[:seen, h // group], v[:seen, h // group], vs[:seen, h // group]
+            sc = kk @ x * hd ** -0.5
+            mag = (np.abs(kk) @ np.abs(x)).max() * hd ** -0.5
+            d = mag * (2.0 ** -22 + (hd / 16 + 4) * 2.0 ** -23) + 2.0 ** -22 * np.abs(sc).max()
+            w = np.exp(sc - sc.max())
+            w /= w.sum()
+            want[0, t, h] = w @ vv
+            bound[0, t, h] = (math.expm1(2 * d) + 2.0 ** -22 + 2.0 ** -21 + 2.0 ** -20) * (w @ np.abs(vv)) + \
+                2.0 ** -31 * (w * s).max() * np.abs(vv / s[:, None]).sum(0)
+    check(out, want, bound, "spread %d" % spread)
+    assert pkg.attn_read_device_error() == 0
