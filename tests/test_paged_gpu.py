@@ -983,3 +983,39 @@ def test_weights_under_small_scales_by_dimension(pkg, spread, hd, n_q, group):
                 2.0 ** -31 * (w * s).max() * np.abs(vv / s[:, None]).sum(0)
     check(out, want, bound, "spread %d" % spread)
     assert pkg.attn_read_device_error() == 0
+
+
+def test_the_public_names_of_torch(pkg, monkeypatch):
+    """Where torch lacks the short ways to its allocator, device and stream, their public names give the same,
+    eagerly, on another stream and in a captured graph."""
+    import torch
+    pool = Pool(61, "e4m3", 2, 128, 64, (3000, 5))
+    cache, table, pos = pool.cache(pkg), tt(pool.table), tt(np.int32([2999, 4]))
+    q = tt(np.random.default_rng(1).standard_normal((2, 8, 128)).astype(np.float32))
+    want = pkg.paged_decode_attention(cache, table, pos, q)
+    short = {n: getattr(pkg, n) for n in ("_torch", "_alloc", "_free", "_device", "_raw_stream")}
+    try:
+        with monkeypatch.context() as m:
+            m.setattr(torch, "_C", object())
+            pkg._torch = None
+            pkg._torch_module()
+        assert pkg._device is torch.cuda.current_device and pkg._free is torch.cuda.caching_allocator_delete
+        assert pkg._alloc.__module__ == pkg._raw_stream.__module__ == pkg.__name__
+        assert torch.equal(pkg.paged_decode_attention(cache, table, pos, q), want)
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            got = pkg.paged_decode_attention(cache, table, pos, q)
+        side.synchronize()
+        assert torch.equal(got, want)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = pkg.paged_decode_attention(cache, table, pos, q)
+        got.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    finally:
+        for n, f in short.items():
+            setattr(pkg, n, f)
+    assert pkg.attn_read_device_error() == 0
