@@ -136,8 +136,13 @@ attn_status attn_rope_steps(int rot_dim, double base, int scaling, double factor
  *   q_out        float [n_tokens][n_head][head_dim], rotated: the q of
  *                attn_decode_paged. It may be q itself (F32, dense).
  *   rope         NULL: nothing is rotated (q is converted)
- * Angles and products are taken in 32 bits from the exact fixed-point angle;
- * each result is rounded once to the type it is stored in.
+ * Sines, cosines and products are taken in 32 bits from the exact fixed-point
+ * angle; each result is rounded once to the type it is stored in. E4M3: where a
+ * call brings a page more rows than a sweep of its threads takes (8 or more),
+ * the sines of up to three rows in four come from an earlier row's by 32-bit
+ * products (within 31 * 2^-24 instead of 8 * 2^-24 of a pair's magnitude), so that an
+ * element of K so near to the middle of two codes can take the other one
+ * than in an append of fewer rows.
  * E4M3: the new rows of a page and head set its scale to the smallest power of
  * two s (2^-60 .. 2^60) with |x| <= 448 s, or, where the page holds rows before
  * them, to the magnitude of the scale it has if that is larger. The rows

@@ -1019,3 +1019,45 @@ def test_the_public_names_of_torch(pkg, monkeypatch):
         for n, f in short.items():
             setattr(pkg, n, f)
     assert pkg.attn_read_device_error() == 0
+
+
+@pytest.mark.parametrize("hd,rot,page,n_kv,interleaved", [(128, 128, 64, 2, False), (64, 64, 1024, 1, True),
+                                                          (256, 64, 128, 8, False)])
+def test_a_prompt_at_once_or_row_by_row(pkg, hd, rot, page, n_kv, interleaved):
+    """The pages hold the same scales and V codes either way, where no row needs a larger scale than the first
+    of its page. K too, but for elements so near to the middle of two codes that the rotations' rounding decides:
+    a row by itself is turned by its own angle (a sine and cosine within 4.4 2^-24 + 2 pi 2^-32), of a page's rows three
+    in four by the row before's and a fixed step. As complex numbers both are off by 6.3 2^-24, each of three
+    products adds as much and 1.4 2^-24 of rounding, the rotation itself 1.4 2^-24: 31 2^-24 of the pair's magnitude,
+    which is at most sqrt 2 times the row's largest element -- 11 2^-22 of it."""
+    import torch
+    n = 2 * page + 7
+    x = np.random.default_rng(page).standard_normal((2, n, n_kv, hd)).astype(np.float32)
+    x[:, ::page] *= 4 / np.abs(x[:, ::page]).max(-1, keepdims=True)
+    x[:, ::page, :, 0] = 6                     # turned, at least 6 / sqrt 2; the other rows at most 2 sqrt 2
+    y = np.clip(x, -2, 2)
+    y[:, ::page] = x[:, ::page]
+    k, v = tt(y[0]), tt(y[1])
+    table = tt(np.arange(3, dtype=np.int32)[None])
+    rope = pkg.Rope(rot, interleaved=interleaved)
+    got = []
+    for steps in ([n], [1] * n):
+        pools = [torch.zeros(3, page, n_kv, hd, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        scales = [torch.zeros(3, n_kv, device="cuda") for _ in range(2)]
+        cache = pkg.PagedCache(*[p.view(torch.float8_e4m3fn) for p in pools], *scales)
+        at = 0
+        for m in steps:
+            pkg.rope_append(cache, table, tt(np.int32([at + m - 1])), k[at:at + m], v[at:at + m], rope=rope)
+            at += m
+        got.append([t.cpu().numpy() for t in pools + scales])
+    (ka, va, *sa), (kb, vb, *sb) = got
+    np.testing.assert_array_equal(va, vb)
+    np.testing.assert_array_equal(np.stack(sa), np.stack(sb))
+    a, b = (ref.VALUES[c.reshape(-1, n_kv, hd)[:n]] for c in (ka, kb))
+    scale = np.repeat(sa[0].astype(np.float64), page, 0)[:n, :, None]
+    freq = np.array([2 * math.pi * s / 2.0 ** 64 for s in pkg.attn_rope_steps(rot, 10000.0)])
+    want = ref.rotate(y[0].astype(np.float64), np.arange(n), freq, interleaved) / scale
+    far = np.abs(want - (a + b) / 2) > 11 * 2.0 ** -22 * np.abs(y[0]).max(-1, keepdims=True) / scale
+    assert not (far & (a != b)).any()
+    assert (np.abs(a - b) <= np.maximum(np.abs(want) * 2.0 ** -3 * (1 + 2.0 ** -4), 2.0 ** -9)).all()
+    assert pkg.attn_read_device_error() == 0
