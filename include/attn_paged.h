@@ -106,8 +106,9 @@ typedef struct {
  * attn_rope_steps -- host-only: the rotation of each pair per position, as a
  * fraction of a turn in 64-bit fixed point, steps[i] = round(2^64 f_i / 2 pi),
  * written to steps[0 .. rot_dim / 2) in host memory. Position times step
- * modulo 2^64 is the angle of that position without a loss that grows with
- * it: the angle is off by at most position * f_i * 2^-50 radians.
+ * modulo 2^64 is the angle of that position: the rounding of the step takes at
+ * most |position| * pi * 2^-64 radians (4e-10 at position 2^31) beside what f_i,
+ * computed in 64-bit floating point, is off by.
  *   rot_dim  as in attn_rope; base finite and >= 1; scaling ATTN_ROPE_*
  *   factor   > 0 and finite (not ATTN_ROPE_PLAIN), the enlarged base of
  *            ATTN_ROPE_BASE finite too; low_turns < high_turns and

@@ -483,3 +483,20 @@ def test_each_refusal_of_the_append_call(door, monkeypatch):
         with pytest.raises(ValueError):
             call()
         assert len(door.calls) == n
+
+
+@pytest.mark.parametrize("rot,base", [(128, 1e4), (128, 1e6), (96, 1e6), (256, 1e9), (64, 1e30)])
+def test_rope_steps_round_to_half_a_step(lib, rot, base):
+    """A step is the 64-bit floating-point f_i 2^64 / 2 pi to half a step, pi 2^-64 radians a position: more than
+    f_i 2^-50 where f_i lies below some 2e-4. f_i itself: the exponent's rounding (none where rot is a power of
+    two) moves it by 2^-53 times the logarithm of base^(2i / rot), power, 2 pi and two divisions by 2^-51 at most."""
+    getcontext().prec = 50
+    exact = rot & (rot - 1) == 0
+    over = 0
+    for i, step in enumerate(pkg.attn_rope_steps(rot, base)):
+        f = Decimal(base) ** (Decimal(-2 * i) / Decimal(rot))
+        own = Decimal(2) ** -51 + (0 if exact else -f.ln() * Decimal(2) ** -53)
+        off = abs(Decimal(step) * 2 * PI / Decimal(2) ** 64 - f)
+        assert off <= f * own + PI * Decimal(2) ** -64 * (1 + Decimal(2) ** -40), i
+        over += off > f * Decimal(2) ** -50
+    assert over > 0                            # the rounding to steps is what far positions of slow pairs lose
