@@ -116,8 +116,12 @@ void make_plan(const attn_paged_cache *c, int max_pages, int n_seq, int n_q, int
     // - where the last 16 would be half empty and 16 cost almost twice as much as 8: head_dim 256 (24, 40, 56 slots, 65000
     //   rows: 127.8 us with 16, 107.5 with 8; 183.9 and 163.7; 237.8 and 229.5), 128 up to 24 slots (64.3 and 61.0; 40
     //   slots 91.2 and 92.4), not 64 (43.1 and 47.5);
-    // - at head_dim 256 for short sequences, whose merges count most (28 sequences up to 1638 rows, 32 slots: 43.4 and
-    //   40.0; 60 of up to 4000, 16 slots: 138.0 and 142.2).
+    // - at head_dim 256 for short sequences, whose merges count most, up to the capacity where 8 slots cost nothing
+    //   even in a large call (1216, 1664, 2080, 2592, 4000 rows: 60 sequences, 8 KV heads, 32 slots 124.3 and 123.0, 149.6
+    //   and 151.7, 173.1 and 177.7, 200.8 and 209.2, 280.9 and 297.0; 16 slots 69.0 and 64.7, 79.9 and 76.9, 92.2 and 90.2,
+    //   104.5 and 105.7, 142.4 and 147.7). In small calls 8 slots gain past it too (28 sequences, 2 KV heads, 32 slots 24.6
+    //   and 21.5, 29.4 and 25.3, 30.9 and 28.9, 36.0 and 32.3, 44.3 and 41.7): where blocks have few rows, the first
+    //   rule takes them.
     const int64_t few = c->head_dim == 256 ? 1664 : 384;
     const bool half_empty = (need - 1) / 8 % 2 == 0;
     pl.slots = need <= 8 ? 8 : 16;
