@@ -39,7 +39,7 @@
 //
 // What bounds it. HBM where there are many rows (ragged batch above; 48 sequences of
 // 129 .. 4097 rows with a distance bias 57 us, 0.88 of the copy bandwidth; 131072 rows of
-// 8 KV heads 46.5 us, 0.85: 5 to 7 us of the last two are the chain before the first tile
+// 8 KV heads 47 us, 0.84: 5 to 7 us of the last two are the chain before the first tile
 // -- positions, table, page --, the merges, the joining kernel and uneven ends). Latency
 // where there are few: one sequence of 512 rows 6.2 us, 8192 rows of 4 KV heads 8.3; 4
 // draft rows of 4 sequences of up to 8400 rows, 32 slots of 256 dimensions a KV head, 19.5

@@ -15,9 +15,9 @@
 // scale grows, one sweep for the codes.
 //
 // What bounds it. HBM for prompts: 7370 bfloat16 tokens of 28 + 4 heads of 128 into e4m3
-// pages 30.4 us, 0.88 of the copy bandwidth (three fifths of the bytes are writes); 8399
-// float32 tokens of 16 + 2 heads of 256 into bfloat16 pages 51.5 us, 0.94. Launch latency for
-// a decode step: one token 3.5 us, 64 sequences of one 3.1 (a chain of position, table,
+// pages 30.3 us, 0.88 of the copy bandwidth (three fifths of the bytes are writes); 8399
+// float32 tokens of 16 + 2 heads of 256 into bfloat16 pages 51.2 us, 0.94. Launch latency for
+// a decode step: one token 3.6 us, 64 sequences of one 3.1 (a chain of position, table,
 // old scale and store).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
