@@ -36,6 +36,7 @@ struct DeviceState {
     unsigned *err_word = nullptr;                 // device address of g_attn_error_word
     void *ws = nullptr;                           // library-owned workspace
     size_t ws_bytes = 0;
+    bool ws_in_graph = false;                     // a captured call holds the workspace's address
     int fused_ok = -1;                            // the device holds a fused kernel's cluster (-1: not asked yet)
 };
 DeviceState g_dev[kMaxDevices];
@@ -91,22 +92,31 @@ cudaError_t device_state(int dev, DeviceState **out)
 }
 
 // Grow the library-owned workspace to `need` bytes; ok false: it would have to
-// grow while `stream` captures. Called with g_mu held and the device current.
+// grow while `stream` captures. A workspace that a captured call holds is left to
+// its graph, which may be replayed at any time. Called with g_mu held and the
+// device current.
 cudaError_t grow_workspace(DeviceState &d, size_t need, cudaStream_t stream, bool &ok)
 {
     ok = true;
-    if (d.ws_bytes >= need) return cudaSuccess;
+    if (d.ws_bytes >= need && d.ws_in_graph) return cudaSuccess;
     cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
     cudaError_t e = cudaStreamIsCapturing(stream, &cs);
     if (e != cudaSuccess) return e;
-    if (cs != cudaStreamCaptureStatusNone) {
+    const bool capturing = cs != cudaStreamCaptureStatusNone;
+    if (d.ws_bytes >= need) {
+        d.ws_in_graph = capturing;
+        return cudaSuccess;
+    }
+    if (capturing) {
         ok = false;
         return cudaSuccess;
     }
-    if (d.ws) {
-        e = cudaFree(d.ws);                       // synchronises with work using it
-        d.ws = nullptr;
-        d.ws_bytes = 0;
+    void *old = d.ws_in_graph ? nullptr : d.ws;
+    d.ws = nullptr;
+    d.ws_bytes = 0;
+    d.ws_in_graph = false;
+    if (old) {
+        e = cudaFree(old);                        // synchronises with work using it
         if (e != cudaSuccess) return e;
     }
     e = cudaMalloc(&d.ws, need);

@@ -145,7 +145,8 @@ typedef enum {
  * The split count comes from attn_split_heuristic(). The workspace is a
  * per-device buffer owned by the library; it grows (cudaMalloc) only outside
  * stream capture, so make one uncaptured call with the largest shape before
- * capturing. Calls that may run concurrently on different streams must use
+ * capturing. A buffer that a captured call holds stays where it is, beside the
+ * larger one, until the process exits. Calls that may run concurrently on different streams must use
  * attn_decode_ex with their own workspaces.
  * scale multiplies q·k (1/sqrt(head_dim) for standard attention).
  */
