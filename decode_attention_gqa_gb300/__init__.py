@@ -1,7 +1,7 @@
 """GB300 (sm_103a) split-KV grouped-query decode attention.
 
 Thin ctypes binding over ``libattn_decode.so`` (declared in
-``include/attn_decode.h`` and ``include/attn_paged.h``). Every ``attn_*``
+``include/attn_decode.h``, ``attn_paged.h``, ``attn_tree.h`` and ``attn_pages.h``). Every ``attn_*``
 function here has the name and argument order of the C entry point it calls and does argument marshalling only: pointers may
 be given as integers or as tensors (their ``data_ptr()`` is passed), streams as
 integers, ``torch.cuda.Stream`` objects or ``None`` (the current torch stream).
@@ -34,6 +34,10 @@ __all__ = [
     "ATTN_ROPE_PLAIN", "ATTN_ROPE_LINEAR", "ATTN_ROPE_BASE", "ATTN_ROPE_BANDS",
     "PagedCache", "Rope", "rope_append", "paged_decode_attention",
     "attn_rope_steps", "attn_rope_append", "attn_decode_paged", "attn_paged_plan",
+    "ATTN_DEVERR_BAD_REQUEST", "ATTN_DEVERR_NO_PAGE", "ATTN_DEVERR_SHARED_PAGE",
+    "PageBook", "tree_rules", "tree_decode_attention", "keep_rows", "copy_pages",
+    "attn_tree_rules", "attn_rope_append_tree", "attn_decode_tree", "attn_tree_plan", "attn_keep_rows",
+    "attn_pages_resize", "attn_pages_fork", "attn_pages_copy",
 ]
 
 ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_WORKSPACE, ATTN_ERR_CUDA = range(5)
@@ -45,6 +49,9 @@ ATTN_VARIANT_TC_TILE = 5
 ATTN_KV_BF16 = 0x10
 ATTN_KV_STABLE = 0x20
 ATTN_DEVERR_BAD_PAGE = 0x4
+ATTN_DEVERR_BAD_REQUEST = 0x8
+ATTN_DEVERR_NO_PAGE = 0x10
+ATTN_DEVERR_SHARED_PAGE = 0x20
 ATTN_TYPE_F32, ATTN_TYPE_F16, ATTN_TYPE_BF16, ATTN_TYPE_E4M3 = range(4)
 ATTN_ROPE_PLAIN, ATTN_ROPE_LINEAR, ATTN_ROPE_BASE, ATTN_ROPE_BANDS = range(4)
 
@@ -131,6 +138,25 @@ def load():
         lib.attn_paged_plan.restype = i32
         lib.attn_paged_plan.argtypes = [vp, i32, i32, i32, i32, i32, i32, i32, ctypes.POINTER(i32),
                                         ctypes.POINTER(sz)]
+        lib.attn_tree_rules.restype = i32
+        lib.attn_tree_rules.argtypes = [vp, vp, i32, i64, i32, vp, vp, vp]
+        lib.attn_rope_append_tree.restype = i32
+        lib.attn_rope_append_tree.argtypes = [vp, vp, i32, vp, vp, i32, i64, vp, vp, vp, i64, i64, i64,
+                                              i32, vp, i32, i32, vp, vp, vp]
+        lib.attn_decode_tree.restype = i32
+        lib.attn_decode_tree.argtypes = [vp, vp, i32, vp, vp, i32, i64, i32, vp, vp, i32, i32, f32, vp,
+                                         i32, vp, vp, i32, vp, sz, vp]
+        lib.attn_tree_plan.restype = i32
+        lib.attn_tree_plan.argtypes = [vp, i32, i32, i64, i32, i32, i32, i32, i32, ctypes.POINTER(i32),
+                                       ctypes.POINTER(sz)]
+        lib.attn_keep_rows.restype = i32
+        lib.attn_keep_rows.argtypes = [vp, vp, i32, vp, vp, vp, i32, i32, vp]
+        lib.attn_pages_resize.restype = i32
+        lib.attn_pages_resize.argtypes = [vp, i32, vp, i32, i32, vp, vp, i32, vp]
+        lib.attn_pages_fork.restype = i32
+        lib.attn_pages_fork.argtypes = [vp, i32, vp, i32, i32, i32, vp, vp, vp, i32, vp, vp]
+        lib.attn_pages_copy.restype = i32
+        lib.attn_pages_copy.argtypes = [vp, vp, i32, vp]
         _lib = lib
         return lib
 
@@ -417,6 +443,74 @@ def attn_decode_paged(cache, block_table, max_pages, positions, q, out, n_seq, n
            "attn_decode_paged")
 
 
+def attn_tree_rules(parents, cu_tokens, n_seq, n_tokens, max_nodes, mask, depths, stream=None):
+    """Masks and depths of the nodes of trees from their parents."""
+    _check(load().attn_tree_rules(_ptr(parents), _ptr(cu_tokens), n_seq, n_tokens, max_nodes, _ptr(mask),
+                                  _ptr(depths), _stream(stream)), "attn_tree_rules")
+
+
+def attn_rope_append_tree(cache, block_table, max_pages, positions, cu_tokens, n_seq, n_tokens, q, k_new,
+                          v_new, q_stride, k_stride, v_stride, in_type, q_out, out_type, n_head, rope=None,
+                          depths=None, stream=None):
+    """attn_rope_append with angles by depth and q_out of out_type."""
+    _check(load().attn_rope_append_tree(_struct(cache), _ptr(block_table), max_pages, _ptr(positions),
+                                        _ptr(cu_tokens), n_seq, n_tokens, _ptr(q), _ptr(k_new), _ptr(v_new),
+                                        q_stride, k_stride, v_stride, in_type, _ptr(q_out), out_type, n_head,
+                                        _struct(rope), _ptr(depths), _stream(stream)),
+           "attn_rope_append_tree")
+
+
+def attn_tree_plan(cache, max_pages, n_seq, n_tokens, max_nodes, q_type, n_head, n_splits=0, sm_count=0):
+    """(split count, workspace bytes) of the attn_decode_tree call with these arguments."""
+    p, ws = ctypes.c_int(0), ctypes.c_size_t(0)
+    _check(load().attn_tree_plan(_struct(cache), max_pages, n_seq, n_tokens, max_nodes, q_type, n_head,
+                                 n_splits, sm_count, ctypes.byref(p), ctypes.byref(ws)), "attn_tree_plan")
+    return p.value, ws.value
+
+
+def attn_decode_tree(cache, block_table, max_pages, positions, cu_tokens, n_seq, n_tokens, max_nodes, q, out,
+                     q_type, n_head, scale, mask=None, mask_words=0, depths=None, rules=None, n_splits=0,
+                     workspace=None, workspace_bytes=0, stream=None):
+    """Attention of the nodes of trees. `rules` is None or the (softcap, window, slopes, starts) of
+    attn_score_rules."""
+    if workspace is not None and not workspace_bytes and hasattr(workspace, "nbytes"):
+        workspace_bytes = workspace.nbytes
+    rules_p = None
+    if rules is not None:
+        softcap, window, slopes, starts = rules
+        rules = _rules(softcap, window, _ptr(slopes), _ptr(starts))
+        rules_p = ctypes.addressof(rules)
+    _check(load().attn_decode_tree(_struct(cache), _ptr(block_table), max_pages, _ptr(positions),
+                                   _ptr(cu_tokens), n_seq, n_tokens, max_nodes, _ptr(q), _ptr(out), q_type,
+                                   n_head, scale, _ptr(mask), mask_words, _ptr(depths), rules_p, n_splits,
+                                   _ptr(workspace), workspace_bytes, _stream(stream)), "attn_decode_tree")
+
+
+def attn_keep_rows(cache, block_table, max_pages, base, path, counts, n_seq, max_keep, stream=None):
+    """Move the kept rows behind base together."""
+    _check(load().attn_keep_rows(_struct(cache), _ptr(block_table), max_pages, _ptr(base), _ptr(path),
+                                 _ptr(counts), n_seq, max_keep, _stream(stream)), "attn_keep_rows")
+
+
+def attn_pages_resize(refs, n_pages, block_table, max_pages, page_size, have, want, n_seq, stream=None):
+    """Release and give out pages, from have to want rows."""
+    _check(load().attn_pages_resize(_ptr(refs), n_pages, _ptr(block_table), max_pages, page_size, _ptr(have),
+                                    _ptr(want), n_seq, _stream(stream)), "attn_pages_resize")
+
+
+def attn_pages_fork(refs, n_pages, block_table, max_pages, page_size, n_seq, src, dst, rows, n_fork, copies,
+                    stream=None):
+    """Share the pages of src with dst; what is left to copy goes to copies."""
+    _check(load().attn_pages_fork(_ptr(refs), n_pages, _ptr(block_table), max_pages, page_size, n_seq,
+                                  _ptr(src), _ptr(dst), _ptr(rows), n_fork, _ptr(copies), _stream(stream)),
+           "attn_pages_fork")
+
+
+def attn_pages_copy(cache, copies, n, stream=None):
+    """Copy rows of pages to other pages."""
+    _check(load().attn_pages_copy(_struct(cache), _ptr(copies), n, _stream(stream)), "attn_pages_copy")
+
+
 def _rules(softcap, window, slopes, starts):
     r = _RulesStruct(softcap, window, slopes, starts)
     if softcap and not r.softcap:
@@ -548,7 +642,7 @@ def _same_device(device):
         raise ValueError("the cache must be on the current CUDA device")
 
 
-def _in_type(dtype):
+def _in_type(dtype, name="k_new"):
     torch = _torch_module()
     if dtype is torch.bfloat16:
         return ATTN_TYPE_BF16
@@ -556,19 +650,20 @@ def _in_type(dtype):
         return ATTN_TYPE_F16
     if dtype is torch.float32:
         return ATTN_TYPE_F32
-    raise TypeError("k_new must be float32, float16 or bfloat16")
+    raise TypeError("%s must be float32, float16 or bfloat16" % name)
 
 
 def rope_append(cache, block_table, positions, k_new, v_new, q=None, q_out=None, rope=None,
-                cu_tokens=None, stream=None):
+                cu_tokens=None, stream=None, depths=None):
     """Convenience form of attn_rope_append for torch tensors: the sizes come from the shapes --
     k_new, v_new [n_tokens, n_kv_head, head_dim] and q [n_tokens, n_head, head_dim] (or None) of one
     type (float32, float16 or bfloat16), dense within a token and of any stride between tokens that
     do not overlap (a row repeated by expand is refused; pass its contiguous() copy);
     block_table int32 [n_seq, max_pages]; positions int32 [n_seq]; cu_tokens int32 [n_seq + 1], or
-    None for the same number of tokens in every sequence. `q_out` (float32) is allocated when not
-    given (on the current stream, so another `stream` needs it given). Returns q_out (None without
-    q)."""
+    None for the same number of tokens in every sequence; depths int32 [n_tokens] for the nodes of
+    trees (attn_rope_append_tree), or None. `q_out` (float32, or the type of q) is allocated as float32
+    when not given (on the current stream, so another `stream` needs it given). Returns q_out (None
+    without q)."""
     torch = _torch or _torch_module()
     i32, index, dt, hd = torch.int32, cache._index, k_new.dtype, cache.head_dim
     in_type = _in_type(dt)
@@ -589,7 +684,8 @@ def rope_append(cache, block_table, positions, k_new, v_new, q=None, q_out=None,
                   "block_table must be [n_seq, max_pages] and positions [n_seq]"),
                  (False, "k_new and v_new must be dense within a token")))
     qs = n_head = 0
-    qp = op = cp = None
+    out_type = ATTN_TYPE_F32
+    qp = op = cp = dp = None
     if q is not None:
         qshape, qst = q.shape, q.stride()
         if not (len(qshape) == 3 and qshape[0] == n_tokens and qshape[2] == hd and q.dtype is dt and
@@ -601,10 +697,12 @@ def rope_append(cache, block_table, positions, k_new, v_new, q=None, q_out=None,
             if stream is not None and _stream(stream) != _raw_stream(index):
                 raise ValueError("q_out must be given with a stream that is not the current one")
             q_out = torch.empty(qshape, dtype=torch.float32, device=cache.device)
-        elif not (q_out.shape == qshape and q_out.dtype is torch.float32 and q_out.get_device() == index and
+        elif not (q_out.shape == qshape and q_out.dtype in (torch.float32, dt) and q_out.get_device() == index and
                   q_out.is_contiguous()):
-            _refuse((("q_out", q_out, torch.float32, True),), cache.device,
+            _refuse((("q_out", q_out, dt if q_out.dtype is dt else torch.float32, True),), cache.device,
                     ((False, "q_out must have the shape of q"),))
+        if q_out.dtype is not torch.float32:
+            out_type = in_type
         qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -614,6 +712,11 @@ def rope_append(cache, block_table, positions, k_new, v_new, q=None, q_out=None,
             _refuse((("cu_tokens", cu_tokens, i32, True),), cache.device,
                     ((False, "cu_tokens must be [n_seq + 1]"),))
         cp = cu_tokens.data_ptr()
+    if depths is not None:
+        if not (depths.dtype is i32 and depths.get_device() == index and depths.shape == (n_tokens,) and
+                depths.is_contiguous()):
+            _refuse((("depths", depths, i32, True),), cache.device, ((False, "depths must be [n_tokens]"),))
+        dp = depths.data_ptr()
     rp = None
     if rope is not None:
         if rope._index != index:
@@ -627,9 +730,9 @@ def rope_append(cache, block_table, positions, k_new, v_new, q=None, q_out=None,
         if kst < n_kv * hd or vst < n_kv * hd or qs < n_head * hd:
             _refuse((), cache.device, [(st >= h * hd, "%s must not have tokens that overlap" % name) for name, st, h in
                                        (("k_new", kst, n_kv), ("v_new", vst, n_kv), ("q", qs, n_head))])
-    status = (_lib or load()).attn_rope_append(
+    status = (_lib or load()).attn_rope_append_tree(
         cache._address, block_table.data_ptr(), max_pages, positions.data_ptr(), cp, n_seq, n_tokens, qp,
-        k_new.data_ptr(), v_new.data_ptr(), qs, kst, vst, in_type, op, n_head, rp,
+        k_new.data_ptr(), v_new.data_ptr(), qs, kst, vst, in_type, op, out_type, n_head, rp, dp,
         _raw_stream(index) if stream is None else _stream(stream))
     if status:
         raise AttnError(status, "attn_rope_append")
@@ -706,3 +809,240 @@ def paged_decode_attention(cache, block_table, positions, q, scale=None, out=Non
     if status:
         raise AttnError(status, "attn_decode_paged")
     return out
+
+
+# ---------------------------------------------------------------------------
+# Drafted trees (include/attn_tree.h) and page bookkeeping (include/attn_pages.h).
+# ---------------------------------------------------------------------------
+def _ints(name, t, shape, index, device):
+    """The address of an int32 tensor of this shape on the device (None: None)."""
+    if t is None:
+        return None
+    if not (t.dtype is _torch.int32 and t.get_device() == index and t.shape == shape and t.is_contiguous()):
+        _refuse(((name, t, _torch.int32, True),), device,
+                ((False, "%s must be [%s]" % (name, ", ".join(str(n) for n in shape))),))
+    return t.data_ptr()
+
+
+def _current(t):
+    """The index of the current device, which `t` must be on."""
+    index = t.get_device()
+    if index < 0 or index != _device():
+        raise ValueError("the tensors must be on the current CUDA device")
+    return index
+
+
+def _nodes_of(cu_tokens, n_tokens, n_seq, max_nodes):
+    if cu_tokens is None:
+        if n_seq < 1 or n_tokens % n_seq:
+            raise ValueError("without cu_tokens every sequence has the same number of nodes")
+        return max(n_tokens // n_seq, 1) if max_nodes is None else max_nodes
+    if max_nodes is None:
+        raise ValueError("max_nodes belongs to cu_tokens")
+    return max_nodes
+
+
+def tree_rules(parents, cu_tokens=None, max_nodes=None, mask=None, depths=None, stream=None):
+    """Convenience form of attn_tree_rules for torch tensors: parents int32 [n_seq, n] (n nodes in every
+    sequence), or [n_tokens] with cu_tokens int32 [n_seq + 1] and max_nodes, which bounds the nodes of a
+    sequence. Returns (mask int32 [n_tokens, (max_nodes + 31) // 32], depths int32 [n_tokens]), allocated
+    when not given (on the current stream, so another `stream` needs them given)."""
+    torch = _torch or _torch_module()
+    index = _current(parents)
+    device, i32 = parents.device, torch.int32
+    if cu_tokens is None:
+        if parents.dim() != 2:
+            raise ValueError("parents must be [n_seq, n], or [n_tokens] with cu_tokens")
+        n_seq = parents.shape[0]
+        n_tokens = parents.numel()
+    else:
+        if parents.dim() != 1 or cu_tokens.dim() != 1 or cu_tokens.shape[0] < 1:
+            raise ValueError("parents must be [n_tokens] and cu_tokens [n_seq + 1]")
+        n_seq, n_tokens = cu_tokens.shape[0] - 1, parents.shape[0]
+    if cu_tokens is not None or n_seq:
+        max_nodes = _nodes_of(cu_tokens, n_tokens, n_seq, max_nodes)
+    else:
+        max_nodes = 1 if max_nodes is None else max_nodes
+    if stream is not None and (mask is None or depths is None) and _stream(stream) != _raw_stream(index):
+        raise ValueError("mask and depths must be given with a stream that is not the current one")
+    words = (max_nodes + 31) // 32
+    if mask is None:
+        mask = torch.empty((n_tokens, words), dtype=i32, device=device)
+    if depths is None:
+        depths = torch.empty(n_tokens, dtype=i32, device=device)
+    status = (_lib or load()).attn_tree_rules(
+        _ints("parents", parents, parents.shape, index, device),
+        _ints("cu_tokens", cu_tokens, (n_seq + 1,), index, device), n_seq, n_tokens, max_nodes,
+        _ints("mask", mask, (n_tokens, words), index, device), _ints("depths", depths, (n_tokens,), index, device),
+        _raw_stream(index) if stream is None else _stream(stream))
+    if status:
+        raise AttnError(status, "attn_tree_rules")
+    return mask, depths
+
+
+def tree_decode_attention(cache, block_table, positions, q, mask=None, depths=None, cu_tokens=None, max_nodes=None,
+                          scale=None, out=None, softcap=0.0, slopes=None, window=0, starts=None, n_splits=0,
+                          stream=None):
+    """Convenience form of attn_decode_tree for torch tensors: q float32, float16 or bfloat16
+    [n_tokens, n_head, head_dim], or [n_seq, n, n_head, head_dim] for n nodes in every sequence; mask int32
+    [n_tokens, words] and depths int32 [n_tokens] as tree_rules gives them, or None for chains; cu_tokens int32
+    [n_seq + 1] with max_nodes where sequences have different numbers of nodes; the rest as in
+    paged_decode_attention. Returns out, of the shape and type of q."""
+    torch = _torch or _torch_module()
+    i32, f32, index, hd, device = torch.int32, torch.float32, cache._index, cache.head_dim, cache.device
+    shape = q.shape
+    n_seq, max_pages = block_table.shape if block_table.dim() == 2 else (-1, 0)
+    if len(shape) == 3:
+        n_tokens, n_head, qd = shape
+    elif len(shape) == 4 and cu_tokens is None:
+        n_tokens, n_head, qd = shape[0] * shape[1], shape[2], shape[3]
+        if shape[0] != n_seq:
+            n_seq = -1
+    else:
+        raise ValueError("q must be [n_tokens, n_head, head_dim], or [n_seq, n, n_head, head_dim] without cu_tokens")
+    q_type = _in_type(q.dtype, "q")
+    if not (index >= 0 and index == _device() and n_seq >= 0 and qd == hd and q.get_device() == index and
+            q.is_contiguous() and
+            block_table.dtype is i32 and block_table.get_device() == index and block_table.is_contiguous() and
+            positions.dtype is i32 and positions.get_device() == index and positions.is_contiguous() and
+            positions.shape == (n_seq,)):
+        _refuse((("block_table", block_table, i32, True), ("positions", positions, i32, True),
+                 ("q", q, q.dtype, True)), device,
+                ((n_seq >= 0 and positions.shape == (n_seq,),
+                  "block_table must be [n_seq, max_pages], positions [n_seq] and q of as many sequences"),
+                 (False, "q and the cache disagree on head_dim")))
+    if out is None:
+        out = torch.empty_like(q)
+    elif not (out.shape == shape and out.dtype is q.dtype and out.get_device() == index and out.is_contiguous()):
+        _refuse((("out", out, q.dtype, True),), device, ((False, "out must have the shape of q"),))
+    if n_seq == 0 and n_tokens == 0:
+        return out
+    max_nodes = _nodes_of(cu_tokens, n_tokens, n_seq, max_nodes)
+    words = 0
+    if mask is not None:
+        words = mask.shape[1] if mask.dim() == 2 else -1
+        mask = _ints("mask", mask, (n_tokens, words), index, device)
+    rules = None
+    if softcap or window or slopes is not None or starts is not None:
+        if slopes is not None and not (slopes.dtype is f32 and slopes.get_device() == index and
+                                       slopes.shape == (n_head,) and slopes.is_contiguous()):
+            _refuse((("slopes", slopes, f32, True),), device, ((False, "slopes must be [n_head]"),))
+        kept = _rules(softcap, window, slopes.data_ptr() if slopes is not None else None,
+                      _ints("starts", starts, (n_seq,), index, device))
+        rules = ctypes.addressof(kept)
+    if n_tokens == 0:
+        return out
+    handle = _raw_stream(index)
+    if stream is not None and _stream(stream) != handle:
+        raise ValueError("stream must be the current stream (torch.cuda.stream selects one)")
+    key = (max_pages, n_seq, n_tokens, max_nodes, q_type, n_head, n_splits, "tree")
+    plan = cache._plans.get(key)
+    if plan is None:
+        if not (0 <= window < 1 << 31 and 0 <= n_splits < 1 << 31 and 0 < max_nodes < 1 << 31):
+            raise ValueError("window, n_splits and max_nodes must be non-negative 32-bit integers")
+        if len(cache._plans) >= 4096:
+            cache._plans.clear()
+        plan = cache._plans[key] = attn_tree_plan(cache, max_pages, n_seq, n_tokens, max_nodes, q_type, n_head,
+                                                  n_splits)
+    n_splits, need = plan
+    ws = _alloc(need, handle) if need else None
+    try:
+        status = (_lib or load()).attn_decode_tree(
+            cache._address, block_table.data_ptr(), max_pages, positions.data_ptr(),
+            _ints("cu_tokens", cu_tokens, (n_seq + 1,), index, device), n_seq, n_tokens, max_nodes, q.data_ptr(),
+            out.data_ptr(), q_type, n_head, hd ** -0.5 if scale is None else scale, mask, words,
+            _ints("depths", depths, (n_tokens,), index, device), rules, n_splits, ws, need, handle)
+    finally:
+        if need:
+            _free(ws)                   # for what follows on this stream
+    if status:
+        raise AttnError(status, "attn_decode_tree")
+    return out
+
+
+def keep_rows(cache, block_table, base, path, counts, stream=None):
+    """Convenience form of attn_keep_rows for torch tensors: row base[s] + path[s, i] of sequence s becomes row
+    base[s] + i for i < counts[s]; block_table int32 [n_seq, max_pages], base and counts int32 [n_seq], path
+    int32 [n_seq, max_keep]."""
+    _torch or _torch_module()
+    index, device = cache._index, cache.device
+    if index < 0 or index != _device():
+        _same_device(device)
+    if block_table.dim() != 2 or path.dim() != 2:
+        raise ValueError("block_table must be [n_seq, max_pages] and path [n_seq, max_keep]")
+    n_seq, max_keep = path.shape
+    max_pages = block_table.shape[1]
+    status = (_lib or load()).attn_keep_rows(
+        cache._address, _ints("block_table", block_table, (n_seq, max_pages), index, device), max_pages,
+        _ints("base", base, (n_seq,), index, device), _ints("path", path, (n_seq, max_keep), index, device),
+        _ints("counts", counts, (n_seq,), index, device), n_seq, max_keep,
+        _raw_stream(index) if stream is None else _stream(stream))
+    if status:
+        raise AttnError(status, "attn_keep_rows")
+
+
+def copy_pages(cache, copies, stream=None):
+    """Convenience form of attn_pages_copy for torch tensors: copies int32 [n, 4], as PageBook.fork gives them."""
+    _torch or _torch_module()
+    index, device = cache._index, cache.device
+    if index < 0 or index != _device():
+        _same_device(device)
+    n = copies.shape[0] if copies.dim() == 2 else -1
+    status = (_lib or load()).attn_pages_copy(cache._address, _ints("copies", copies, (n, 4), index, device), n,
+                                              _raw_stream(index) if stream is None else _stream(stream))
+    if status:
+        raise AttnError(status, "attn_pages_copy")
+
+
+class PageBook:
+    """The pages of a paged cache (or of the caches of all layers, where they use the same numbers): refs int32
+    [n_pages], how many block-table entries hold each page, and the block table int32 [n_seq, max_pages]. Holds
+    the tensors; its calls change them in place, on the device (include/attn_pages.h)."""
+
+    def __init__(self, refs, block_table, page_size):
+        torch = _torch_module()
+        if refs.device != block_table.device or refs.get_device() < 0:
+            raise ValueError("refs and block_table must be on the same CUDA device")
+        for name, t, dims in (("refs", refs, 1), ("block_table", block_table, 2)):
+            _on_device(name, t, torch.int32, refs.device)
+            _dense(name, t)
+            if t.dim() != dims:
+                raise ValueError("refs must be [n_pages] and block_table [n_seq, max_pages]")
+        self.refs, self.block_table, self.page_size = refs, block_table, page_size
+        self._index, self.device = refs.get_device(), refs.device
+
+    def _at(self, stream):
+        if self._index != _device():
+            raise ValueError("refs and block_table must be on the current CUDA device")
+        return _raw_stream(self._index) if stream is None else _stream(stream)
+
+    def resize(self, have, want, stream=None):
+        """attn_pages_resize: every sequence from have to want rows (int32 [n_seq])."""
+        handle = self._at(stream)
+        n_seq, max_pages = self.block_table.shape
+        status = (_lib or load()).attn_pages_resize(
+            self.refs.data_ptr(), self.refs.shape[0], self.block_table.data_ptr(), max_pages, self.page_size,
+            _ints("have", have, (n_seq,), self._index, self.device),
+            _ints("want", want, (n_seq,), self._index, self.device), n_seq, handle)
+        if status:
+            raise AttnError(status, "attn_pages_resize")
+
+    def fork(self, src, dst, rows, copies=None, stream=None):
+        """attn_pages_fork: sequence dst[i] takes the first rows[i] rows of src[i] (int32 [n_fork]). Returns
+        copies int32 [n_fork, 4] for copy_pages, allocated when not given (on the current stream, so another
+        `stream` needs it given)."""
+        handle = self._at(stream)
+        n = src.shape[0] if src.dim() == 1 else -1
+        if copies is None:
+            if stream is not None and handle != _raw_stream(self._index):
+                raise ValueError("copies must be given with a stream that is not the current one")
+            copies = _torch.empty((max(n, 0), 4), dtype=_torch.int32, device=self.device)
+        n_seq, max_pages = self.block_table.shape
+        status = (_lib or load()).attn_pages_fork(
+            self.refs.data_ptr(), self.refs.shape[0], self.block_table.data_ptr(), max_pages, self.page_size, n_seq,
+            _ints("src", src, (n,), self._index, self.device), _ints("dst", dst, (n,), self._index, self.device),
+            _ints("rows", rows, (n,), self._index, self.device), n,
+            _ints("copies", copies, (n, 4), self._index, self.device), handle)
+        if status:
+            raise AttnError(status, "attn_pages_fork")
+        return copies

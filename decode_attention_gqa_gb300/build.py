@@ -20,7 +20,8 @@ LIB = os.path.join(PKG, "libattn_decode.so")
 
 SOURCES = ["attn_api.cu", "attn_noalloc.cu"] + [
     "attn_kernels_hd%d_%s.cu" % (hd, t) for hd in (8, 64, 128, 256) for t in ("f16", "bf16")] + [
-    "attn_paged_api.cu", "attn_rope_append.cu"] + [
+    "attn_paged_api.cu", "attn_rope_append.cu", "attn_tree_api.cu", "attn_tree_rows.cu", "attn_tree.cu",
+    "attn_pages.cu"] + [
     "attn_paged_hd%d_%s.cu" % (hd, t) for hd in (64, 128, 256) for t in ("f16", "bf16", "e4m3")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -51,7 +52,8 @@ def _stale() -> bool:
         return True
     t = os.path.getmtime(LIB)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    deps += [os.path.join(ROOT, "include", h) for h in ("attn_decode.h", "attn_paged.h")]
+    deps += [os.path.join(ROOT, "include", h) for h in
+             ("attn_decode.h", "attn_paged.h", "attn_tree.h", "attn_pages.h")]
     deps.append(os.path.abspath(__file__))
     return any(os.path.getmtime(d) > t for d in deps)
 

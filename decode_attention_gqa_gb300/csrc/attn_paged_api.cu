@@ -8,59 +8,15 @@
 
 #include "attn_launch.h"
 #include "attn_paged.h"
+#include "attn_paged_check.h"
 #include "attn_paged_launch.h"
+#include "attn_tree.h"
 
 namespace {
 
+using namespace attn::check;
+
 constexpr int kMaxPagedSplits = 4096;
-constexpr int64_t kMaxRows = (int64_t)0x7fffffff - 16384;
-constexpr int64_t kMaxStrideBytes = (int64_t)1 << 40;
-
-bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-attn_status fail(cudaError_t e)
-{
-    attn::note_cuda_error(e);
-    return ATTN_ERR_CUDA;
-}
-
-int type_bytes(int t) { return t == ATTN_TYPE_F32 ? 4 : t == ATTN_TYPE_E4M3 ? 1 : 2; }
-
-struct Strides {
-    int64_t page, row, head;
-};
-
-// Everything about the pool but its pointers.
-attn_status check_cache_shape(const attn_paged_cache *c, int max_pages, Strides &st)
-{
-    if (!c || c->reserved != 0 || c->n_pages < 1 || c->n_kv_head < 1 || c->head_dim < 1 || max_pages < 1)
-        return ATTN_ERR_INVALID_ARG;
-    if (c->page_size < 16 || c->page_size > 1024 || c->page_size % 16 != 0) return ATTN_ERR_INVALID_ARG;
-    if (c->kv_type != ATTN_TYPE_F16 && c->kv_type != ATTN_TYPE_BF16 && c->kv_type != ATTN_TYPE_E4M3)
-        return ATTN_ERR_INVALID_ARG;
-    if (c->n_kv_head > 65535 || (int64_t)max_pages * c->page_size > kMaxRows) return ATTN_ERR_INVALID_ARG;
-    st = Strides{c->page_stride, c->row_stride, c->head_stride};
-    if (st.page == 0 && st.row == 0 && st.head == 0) {
-        st.head = c->head_dim;
-        st.row = (int64_t)c->n_kv_head * c->head_dim;
-        st.page = (int64_t)c->page_size * st.row;
-    }
-    const int64_t es = type_bytes(c->kv_type);
-    for (int64_t x : {st.page, st.row, st.head})
-        if (x < c->head_dim || x >= kMaxStrideBytes / es || x * es % 16 != 0) return ATTN_ERR_INVALID_ARG;
-    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return ATTN_ERR_UNSUPPORTED;
-    return ATTN_OK;
-}
-
-attn_status check_cache_pointers(const attn_paged_cache *c)
-{
-    if (!c || !c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return ATTN_ERR_INVALID_ARG;
-    const bool scales = c->kv_type == ATTN_TYPE_E4M3;
-    if (scales != (c->k_scale != nullptr) || scales != (c->v_scale != nullptr)) return ATTN_ERR_INVALID_ARG;
-    if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)) return ATTN_ERR_INVALID_ARG;
-    return ATTN_OK;
-}
-
 struct PagedPlan {
     attn::PagedShape shape{};
     int slots = 8, qgroups = 1, n_splits = 1;
@@ -75,8 +31,6 @@ attn_status check_heads(const attn_paged_cache *c, int n_seq, int n_q, int n_hea
     if (n_head / c->n_kv_head > 64) return ATTN_ERR_UNSUPPORTED;
     return ATTN_OK;
 }
-
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // How many blocks share the call's rows, per KV head and group of slots: as many as fill the SMs with
 // resident blocks once, since each takes an equal part of the rows that are there (the device divides them,
@@ -181,9 +135,21 @@ attn_status attn_rope_append(const attn_paged_cache *cache, const int32_t *block
                              int64_t k_stride, int64_t v_stride, int in_type, float *q_out, int n_head,
                              const attn_rope *rope, attn_stream_t stream)
 {
+    return attn_rope_append_tree(cache, block_table, max_pages, positions, cu_tokens, n_seq, n_tokens, q, k_new, v_new,
+                                 q_stride, k_stride, v_stride, in_type, q_out, ATTN_TYPE_F32, n_head, rope, nullptr,
+                                 stream);
+}
+
+attn_status attn_rope_append_tree(const attn_paged_cache *cache, const int32_t *block_table, int max_pages,
+                                  const int32_t *positions, const int32_t *cu_tokens, int n_seq, int64_t n_tokens,
+                                  const void *q, const void *k_new, const void *v_new, int64_t q_stride,
+                                  int64_t k_stride, int64_t v_stride, int in_type, void *q_out, int out_type,
+                                  int n_head, const attn_rope *rope, const int32_t *depths, attn_stream_t stream)
+{
     attn_status st = check_cache_pointers(cache);
     if (st != ATTN_OK) return st;
     if (in_type != ATTN_TYPE_F32 && in_type != ATTN_TYPE_F16 && in_type != ATTN_TYPE_BF16) return ATTN_ERR_INVALID_ARG;
+    if (out_type != ATTN_TYPE_F32 && out_type != in_type) return ATTN_ERR_INVALID_ARG;
     if (n_seq < 0 || n_seq > 65535 || n_tokens < 0 || n_tokens > kMaxRows) return ATTN_ERR_INVALID_ARG;
     if (n_seq == 0 && n_tokens != 0) return ATTN_ERR_INVALID_ARG;
     if (!cu_tokens && n_seq > 0 && n_tokens % n_seq != 0) return ATTN_ERR_INVALID_ARG;
@@ -191,7 +157,7 @@ attn_status attn_rope_append(const attn_paged_cache *cache, const int32_t *block
     if ((q != nullptr) != (q_out != nullptr) || (q && (n_head < 1 || n_head > 65535))) return ATTN_ERR_INVALID_ARG;
     for (const void *p : {q, k_new, v_new, static_cast<const void *>(q_out)})
         if (!aligned(p, 16)) return ATTN_ERR_INVALID_ARG;
-    for (const int32_t *p : {block_table, positions, cu_tokens})
+    for (const int32_t *p : {block_table, positions, cu_tokens, depths})
         if (!aligned(p, 4)) return ATTN_ERR_INVALID_ARG;
     if (rope && (!rope->steps || !aligned(rope->steps, 16) || rope->rot_dim < 16 || rope->rot_dim % 16 != 0 ||
                  rope->rot_dim > cache->head_dim || (rope->interleaved != 0 && rope->interleaved != 1) ||
@@ -208,7 +174,7 @@ attn_status attn_rope_append(const attn_paged_cache *cache, const int32_t *block
     if ((q && q_stride < q_dense) || k_stride < kv_dense || v_stride < kv_dense) return ATTN_ERR_INVALID_ARG;
     for (int64_t x : {q ? q_stride : kv_dense, k_stride, v_stride})
         if (x >= kMaxStrideBytes / es || x * es % 16 != 0) return ATTN_ERR_INVALID_ARG;
-    if (q && static_cast<const void *>(q_out) == q && (in_type != ATTN_TYPE_F32 || q_stride != q_dense))
+    if (q && static_cast<const void *>(q_out) == q && (in_type != out_type || q_stride != q_dense))
         return ATTN_ERR_INVALID_ARG;
     if (n_tokens == 0) return ATTN_OK;
 
@@ -231,6 +197,8 @@ attn_status attn_rope_append(const attn_paged_cache *cache, const int32_t *block
     a.table = block_table;
     a.positions = positions;
     a.cu = cu_tokens;
+    a.depths = depths;
+    a.q_in_type = out_type != ATTN_TYPE_F32;
     a.steps = rope ? rope->steps : nullptr;
     a.mscale = rope ? rope->mscale : 1.f;
     a.rot_dim = rope ? rope->rot_dim : 0;

@@ -108,16 +108,18 @@ cudaError_t launch_paged_hd256_e4m3(const PagedRequest &r);
 
 struct AppendArgs {
     const void *q, *k_new, *v_new;
-    float *q_out;
+    void *q_out;                                    // float, or the input's type (q_in_type)
     int64_t q_stride, k_stride, v_stride;           // elements between tokens
     void *k, *v;
     float *k_scale, *v_scale;
     int64_t page_stride, row_stride, head_stride;   // elements
     const int32_t *table, *positions, *cu;
+    const int32_t *depths;                          // of each token in its tree, or null: a chain
     const uint64_t *steps;                          // null: no rotation
     unsigned *err;
     float mscale;
     int rot_dim, interleaved;
+    bool q_in_type;
     int n_seq, n_head, n_kv_head;
     int64_t n_tokens;
     int64_t n_each;                                 // tokens per sequence when cu is null
@@ -140,6 +142,57 @@ struct AppendRequest {
 };
 
 cudaError_t launch_append(const AppendRequest &r);
+
+// Trees: rules from parents, and the rows that are kept.
+struct TreeRulesArgs {
+    const int32_t *parents, *cu;
+    uint32_t *mask;
+    int32_t *depths;
+    unsigned *err;
+    int64_t n_tokens, n_each;                       // n_each: nodes of a sequence when cu is null
+    int n_seq, max_nodes, words;
+};
+cudaError_t launch_tree_rules(const TreeRulesArgs &a, cudaStream_t stream);
+
+struct KeepArgs {
+    uint8_t *k, *v;
+    float *k_scale, *v_scale;
+    int64_t page_stride, row_stride, head_stride;   // bytes
+    const int32_t *table, *base, *path, *counts;
+    unsigned *err;
+    int n_seq, n_kv_head, max_keep, max_pages, n_pages, page_size;
+    int row_bytes;                                  // of one head: 64 .. 512
+    FastDiv by_page;
+};
+cudaError_t launch_keep_rows(const KeepArgs &a, bool e4m3, cudaStream_t stream);
+
+// Attention of trees.
+struct TreeArgs {
+    const void *q;            // [n_tokens][n_head][HD]
+    void *out;
+    const int32_t *positions, *cu, *table, *depths, *starts;
+    const uint32_t *mask;     // [n_tokens][words] or null
+    const float *k_scale, *v_scale, *slopes;
+    unsigned *err;
+    int q_type;
+    int64_t n_tokens;
+    int n_each;               // nodes of a sequence when cu is null
+    int n_seq, max_nodes, words;
+    int n_head, n_kv_head, group;
+    int max_pages, n_pages, page_size, cap, window;
+    float scale_log2;         // scale * log2 e
+    float softcap;            // 0: none
+    FastDiv by_page, by_group;
+};
+
+struct TreeRequest {
+    TreeArgs a;
+    const void *k, *v;
+    int64_t page_stride, row_stride, head_stride;   // elements
+    int head_dim, kv_type;
+    cudaStream_t stream;
+};
+cudaError_t launch_tree(const TreeRequest &r);
 
 // Implemented in attn_api.cu.
 // The current device's SM count and error word.

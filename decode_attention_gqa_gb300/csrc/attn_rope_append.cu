@@ -319,6 +319,7 @@ __device__ __forceinline__ void token_job(const AppendArgs &g, const Stage<HD, I
     for (int i = 0; i < D; ++i) fetch(i);                         // ... while the token's position is found
     Steps steps;
     steps.load(g.steps, u);
+    const int depth = g.depths ? ld_shared_by_all(g.depths + tok) : 0;
     const int s = g.cu ? warp_search(g.n_seq, at_tok, lane, [&](int i) { return cu_at(g, i); }) : div(g.by_each, at_tok);
     const int64_t end = cu_at(g, s + 1);
     const int64_t last = ld_shared_by_all(g.positions + s);
@@ -335,7 +336,9 @@ __device__ __forceinline__ void token_job(const AppendArgs &g, const Stage<HD, I
         }
     }
     Turn tr;
-    if (u.rot) make_turn(g, steps, pos, tr);
+    // a node of a tree turns by its depth behind the rows before the tree, not by its row
+    const int64_t at = g.depths && tok < end ? last + 1 - (end - cu_at(g, s)) + depth : pos;
+    if (u.rot) make_turn(g, steps, at, tr);
     const int n = tok < end ? g.iters : 0;                        // behind the last sequence: nothing
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
@@ -347,8 +350,10 @@ __device__ __forceinline__ void token_job(const AppendArgs &g, const Stage<HD, I
             float a[8], b[8];
             stage.values(i % D, u, a, b);
             if (u.rot && !is_v) turn(g, tr, a, b);
-            if (is_q) {
-                float *o = g.q_out + (tok * g.n_head + h) * HD;
+            if (is_q && sizeof(IN) == 2 && g.q_in_type) {
+                if constexpr (sizeof(IN) == 2) store_16bit<IN>(g, static_cast<IN *>(g.q_out) + (tok * g.n_head + h) * HD, u, a, b);
+            } else if (is_q) {
+                float *o = static_cast<float *>(g.q_out) + (tok * g.n_head + h) * HD;
                 uint32_t w[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(a[j]);
@@ -448,16 +453,17 @@ __device__ __forceinline__ void page_job(const AppendArgs &g, const Stage<HD, IN
     if (w0 == 0 && rows > TPB)
         for (int i = tid; i < g.rot_dim / 2; i += blockDim.x) angle(TPB, g.steps[i], by[i].x, by[i].y);
     // what the sweeps need now and then, out of the registers
-    __shared__ int64_t sm_tok, sm_base, sm_r0;
+    __shared__ int64_t sm_tok, sm_base, sm_r0, sm_first;
     if (tid == 0) {
         sm_tok = tok;
+        sm_first = first;
         sm_base = page * g.page_stride + kh * g.head_stride;
         sm_r0 = r0;
     }
     stage.template wait<0>();
     __syncthreads();
     if (!there) return;
-    const volatile int64_t &vtok = sm_tok, &vbase = sm_base, &vr0 = sm_r0;
+    const volatile int64_t &vtok = sm_tok, &vbase = sm_base, &vr0 = sm_r0, &vfirst = sm_first;
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
@@ -483,11 +489,11 @@ __device__ __forceinline__ void page_job(const AppendArgs &g, const Stage<HD, IN
                 stage.values(slot, u, a, b);
                 if (turned) {
                     // one row in four from its position, the others from the one before (three products of 32-bit
-                    // rounding at most)
-                    if (k % 4 == 0) {
+                    // rounding at most); nodes of a tree each from their own
+                    if (k % 4 == 0 || g.depths) {
                         Steps steps;
                         steps.load(sm_steps, u);
-                        make_turn(g, steps, vr0 + i, tr);
+                        make_turn(g, steps, g.depths ? vfirst + ld_shared_by_all(g.depths + vtok + i) : vr0 + i, tr);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) turn_pair(tr.c[j], tr.s[j], by[u.pair0 + j].x, by[u.pair0 + j].y);
