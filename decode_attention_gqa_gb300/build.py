@@ -20,9 +20,10 @@ LIB = os.path.join(PKG, "libattn_decode.so")
 
 SOURCES = ["attn_api.cu", "attn_noalloc.cu"] + [
     "attn_kernels_hd%d_%s.cu" % (hd, t) for hd in (8, 64, 128, 256) for t in ("f16", "bf16")] + [
-    "attn_paged_api.cu", "attn_rope_append.cu", "attn_tree_api.cu", "attn_tree_rows.cu", "attn_tree.cu",
+    "attn_paged_api.cu", "attn_rope_append.cu", "attn_tree_api.cu", "attn_tree_rows.cu",
     "attn_pages.cu"] + [
-    "attn_paged_hd%d_%s.cu" % (hd, t) for hd in (64, 128, 256) for t in ("f16", "bf16", "e4m3")]
+    "attn_%s_hd%d_%s.cu" % (k, hd, t) for k in ("paged", "tree") for hd in (64, 128, 256)
+    for t in ("f16", "bf16", "e4m3")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -168,20 +168,33 @@ cudaError_t launch_keep_rows(const KeepArgs &a, bool e4m3, cudaStream_t stream);
 
 // Attention of trees.
 struct TreeArgs {
-    const void *q;            // [n_tokens][n_head][HD]
+    const void *q;            // [n_tokens][n_head][HD] of q_type
     void *out;
-    const int32_t *positions, *cu, *table, *depths, *starts;
-    const uint32_t *mask;     // [n_tokens][words] or null
+    const void *v;            // the pool again, for rows that are added one by one
+    int64_t page_stride, row_stride, head_stride;   // elements
+    const int32_t *positions, *cu, *table, *starts; // of the launch's sequences
+    const int32_t *depths;    // of all tokens, or null
+    const uint32_t *mask;     // [n_tokens][words] or null: chains
     const float *k_scale, *v_scale, *slopes;
+    // Parts of units: row (rank * 2 + which) * unit_slots + slot in the unit, `which` 1 where the unit begins in
+    // this rank's places
+    float *ws_o;              // [rows][HD]
+    float2 *ws_ml;            // [rows]
+    int4 *ws_span;            // [n_seq]: first place, tiles, first token, places of a rank
     unsigned *err;
-    int q_type;
-    int64_t n_tokens;
-    int n_each;               // nodes of a sequence when cu is null
-    int n_seq, max_nodes, words;
+    int64_t n_tokens, n_each; // n_each: nodes of a sequence when cu is null
+    int64_t tok_end;          // tokens the joining kernel looks at
+    int q_type, n_seq, seq0;  // sequences of the launch (at most kPagedSeqs), the first one's number
+    int max_nodes, words;
     int n_head, n_kv_head, group;
     int max_pages, n_pages, page_size, cap, window;
-    float scale_log2;         // scale * log2 e
-    float softcap;            // 0: none
+    int ranks, min_share;     // blocks that share the tiles; the least a block takes
+    int unit_slots;           // (node, head) pairs a block serves at once: 128 or 256
+    int nslot, nraw;          // 16-bit and 8-bit tiles of the rings
+    int box_rows;             // rows of one TMA box
+    bool once;                // no other block reads the same rows
+    float qscale;             // scale * log2 e, or scale / softcap
+    float softcap, cap_log2;  // 0: none; softcap * log2 e
     FastDiv by_page, by_group;
 };
 
@@ -190,9 +203,19 @@ struct TreeRequest {
     const void *k, *v;
     int64_t page_stride, row_stride, head_stride;   // elements
     int head_dim, kv_type;
+    int parts;                // 16-bit parts of q and of the weights
     cudaStream_t stream;
 };
-cudaError_t launch_tree(const TreeRequest &r);
+constexpr int tree_tile(int head_dim) { return head_dim == 256 ? 64 : 128; }
+cudaError_t launch_tree_hd64_f16(const TreeRequest &r);
+cudaError_t launch_tree_hd64_bf16(const TreeRequest &r);
+cudaError_t launch_tree_hd64_e4m3(const TreeRequest &r);
+cudaError_t launch_tree_hd128_f16(const TreeRequest &r);
+cudaError_t launch_tree_hd128_bf16(const TreeRequest &r);
+cudaError_t launch_tree_hd128_e4m3(const TreeRequest &r);
+cudaError_t launch_tree_hd256_f16(const TreeRequest &r);
+cudaError_t launch_tree_hd256_bf16(const TreeRequest &r);
+cudaError_t launch_tree_hd256_e4m3(const TreeRequest &r);
 
 // Implemented in attn_api.cu.
 // The current device's SM count and error word.

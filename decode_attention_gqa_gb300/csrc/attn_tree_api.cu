@@ -34,14 +34,30 @@ attn_status check_call(const attn_paged_cache *c, int q_type, int n_head, int n_
 }
 
 struct TreePlan {
-    int n_splits = 1;
-    size_t workspace = 0;
+    int n_splits = 1, unit_slots = 128, min_share = 1, tile = 128;
+    size_t o_bytes = 0, ml_bytes = 0, workspace = 0;
 };
 
-void make_plan(int n_splits, int sm_count, TreePlan &pl)
+// A block an SM, each with an equal run of the tiles there are (the device counts them); fewer where the
+// capacity holds fewer. Up to 128 slots the two warpgroups of a block take tiles in turn: two at least.
+void make_plan(const attn_paged_cache *c, int max_pages, int n_seq, int max_nodes, int n_head, int n_splits, int sm_count,
+               TreePlan &pl)
 {
-    (void)sm_count;
-    pl.n_splits = n_splits > 0 ? n_splits : 1;
+    const int need = max_nodes * (n_head / c->n_kv_head);
+    pl.tile = attn::tree_tile(c->head_dim);
+    pl.unit_slots = c->head_dim == 256 || need <= 128 ? 128 : 256;
+    pl.min_share = c->head_dim != 256 && need <= 128 ? 2 : 1;
+    const int64_t units = (int64_t)c->n_kv_head * ((need + pl.unit_slots - 1) / pl.unit_slots);
+    const int64_t seqs = n_seq < attn::kPagedSeqs ? n_seq : attn::kPagedSeqs;
+    const int64_t tiles = ((int64_t)max_pages * c->page_size + pl.tile - 1) / pl.tile + 1;
+    const int64_t most = (tiles * units * seqs + pl.min_share - 1) / pl.min_share;
+    pl.n_splits = n_splits > 0 ? n_splits : (int)(most < sm_count ? most : sm_count);
+    if (pl.n_splits > 1) {
+        const size_t parts = (size_t)pl.n_splits * 2 * pl.unit_slots;
+        pl.o_bytes = align256(parts * c->head_dim * sizeof(float));
+        pl.ml_bytes = align256(parts * 2 * sizeof(float));
+        pl.workspace = pl.o_bytes + pl.ml_bytes + align256((size_t)seqs * 16);
+    }
 }
 
 } // namespace
@@ -88,7 +104,7 @@ attn_status attn_tree_plan(const attn_paged_cache *cache, int max_pages, int n_s
         if (e != cudaSuccess) return fail(e);
     }
     TreePlan pl;
-    make_plan(n_splits, sm_count, pl);
+    make_plan(cache, max_pages, n_seq, max_nodes, n_head, n_splits, sm_count, pl);
     if (n_splits_out) *n_splits_out = pl.n_splits;
     if (workspace_bytes_out) *workspace_bytes_out = pl.workspace;
     return ATTN_OK;
@@ -135,7 +151,7 @@ attn_status attn_decode_tree(const attn_paged_cache *cache, const int32_t *block
     cudaError_t e = attn::device_facts(&sm_count, &a.err);
     if (e != cudaSuccess) return fail(e);
     TreePlan pl;
-    make_plan(n_splits, sm_count, pl);
+    make_plan(cache, max_pages, n_seq, max_nodes, n_head, n_splits, sm_count, pl);
     if (pl.workspace > 0) {
         if (!workspace) {
             bool ok = false;
@@ -148,19 +164,24 @@ attn_status attn_decode_tree(const attn_paged_cache *cache, const int32_t *block
     }
     a.q = q;
     a.out = out;
-    a.positions = positions;
-    a.cu = cu_tokens;
-    a.table = block_table;
+    a.v = cache->v;
+    a.page_stride = cs.page;
+    a.row_stride = cs.row;
+    a.head_stride = cs.head;
     a.depths = depths;
-    a.starts = rules ? rules->starts : nullptr;
     a.mask = mask;
     a.k_scale = cache->k_scale;
     a.v_scale = cache->v_scale;
     a.slopes = rules ? rules->slopes : nullptr;
-    a.q_type = q_type;
+    if (pl.workspace > 0) {
+        uint8_t *ws = static_cast<uint8_t *>(workspace);
+        a.ws_o = reinterpret_cast<float *>(ws);
+        a.ws_ml = reinterpret_cast<float2 *>(ws + pl.o_bytes);
+        a.ws_span = reinterpret_cast<int4 *>(ws + pl.o_bytes + pl.ml_bytes);
+    }
     a.n_tokens = n_tokens;
-    a.n_each = cu_tokens ? 0 : (int)(n_tokens / n_seq);
-    a.n_seq = n_seq;
+    a.n_each = cu_tokens ? 0 : n_tokens / n_seq;
+    a.q_type = q_type;
     a.max_nodes = max_nodes;
     a.words = mask ? mask_words : 0;
     a.n_head = n_head;
@@ -170,9 +191,14 @@ attn_status attn_decode_tree(const attn_paged_cache *cache, const int32_t *block
     a.n_pages = cache->n_pages;
     a.page_size = cache->page_size;
     a.cap = max_pages * cache->page_size;
-    a.window = window;
-    a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    a.window = window > a.cap ? 0 : window;        // past the capacity it masks nothing
+    a.ranks = pl.n_splits;
+    a.min_share = pl.min_share;
+    a.unit_slots = pl.unit_slots;
+    a.once = (int64_t)max_nodes * a.group <= pl.unit_slots;
+    a.qscale = qscale;
     a.softcap = softcap;
+    a.cap_log2 = (float)((double)softcap * 1.4426950408889634);
     a.by_page = attn::fast_div((unsigned)cache->page_size);
     a.by_group = attn::fast_div((unsigned)a.group);
     r.k = cache->k;
@@ -182,9 +208,32 @@ attn_status attn_decode_tree(const attn_paged_cache *cache, const int32_t *block
     r.head_stride = cs.head;
     r.head_dim = cache->head_dim;
     r.kv_type = cache->kv_type;
+    // one part holds a 16-bit query, but for f16's in bfloat16
+    r.parts = q_type == ATTN_TYPE_F32 || (q_type == ATTN_TYPE_F16 && cache->kv_type == ATTN_TYPE_BF16) ? 2 : 1;
     r.stream = reinterpret_cast<cudaStream_t>(stream);
-    e = attn::launch_tree(r);
-    return e == cudaSuccess ? ATTN_OK : fail(e);
+    using Launch = cudaError_t (*)(const attn::TreeRequest &);
+    static const Launch table[3][3] = {
+        {attn::launch_tree_hd64_f16, attn::launch_tree_hd64_bf16, attn::launch_tree_hd64_e4m3},
+        {attn::launch_tree_hd128_f16, attn::launch_tree_hd128_bf16, attn::launch_tree_hd128_e4m3},
+        {attn::launch_tree_hd256_f16, attn::launch_tree_hd256_bf16, attn::launch_tree_hd256_e4m3}};
+    const Launch launch = table[cache->head_dim == 64 ? 0 : cache->head_dim == 128 ? 1 : 2][cache->kv_type - ATTN_TYPE_F16];
+    // places are counted in 32 bits: fewer sequences a launch where the capacity is huge
+    const int64_t units = (int64_t)cache->n_kv_head * (((int64_t)max_nodes * a.group + pl.unit_slots - 1) / pl.unit_slots);
+    const int64_t per_seq = (((int64_t)a.cap + pl.tile - 1) / pl.tile + 1) * units;
+    if (per_seq > 0x3fff0000) return ATTN_ERR_UNSUPPORTED;
+    const int batch = (int)(0x3fff0000 / per_seq < attn::kPagedSeqs ? 0x3fff0000 / per_seq : attn::kPagedSeqs);
+    for (int s0 = 0; s0 < n_seq; s0 += batch) {
+        a.n_seq = n_seq - s0 < batch ? n_seq - s0 : batch;
+        a.seq0 = s0;
+        a.positions = positions + s0;
+        a.cu = cu_tokens ? cu_tokens + s0 : nullptr;
+        a.table = block_table + (size_t)s0 * max_pages;
+        a.starts = rules && rules->starts ? rules->starts + s0 : nullptr;
+        a.tok_end = cu_tokens ? n_tokens : (s0 + a.n_seq) * a.n_each;
+        e = launch(r);
+        if (e != cudaSuccess) return fail(e);
+    }
+    return ATTN_OK;
 }
 
 attn_status attn_keep_rows(const attn_paged_cache *cache, const int32_t *block_table, int max_pages,

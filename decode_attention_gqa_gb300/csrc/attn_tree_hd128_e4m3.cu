@@ -1,0 +1,6 @@
+// Attention of trees for head_dim 128 over a e4m3 cache.
+#include "attn_tree.cuh"
+
+namespace attn {
+cudaError_t launch_tree_hd128_e4m3(const TreeRequest &r) { return launch_tree_for<128, E4m3>(r); }
+} // namespace attn

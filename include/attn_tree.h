@@ -76,7 +76,8 @@ attn_status attn_rope_append_tree(const attn_paged_cache *cache, const int32_t *
  *   mask       uint32 [n_tokens][mask_words], mask_words >= (max_nodes + 31) / 32, any
  *              bits (attn_tree_rules makes a tree's); bits at or past n_s are not
  *              looked at. NULL: a chain, node t sees nodes 0 .. t.
- *   depths     int32 [n_tokens], or NULL: node t has depth t. Only slopes and
+ *   depths     int32 [n_tokens], 0 .. max_nodes - 1 (others are taken as the
+ *              nearest of these), or NULL: node t has depth t. Only slopes and
  *              window look at it.
  *   rules      as in attn_decode_paged, with distances by position: query
  *              base_s + depth, cache row j < base_s at position j, node j at base_s + its
