@@ -176,11 +176,11 @@ struct TreeArgs {
     const int32_t *depths;    // of all tokens, or null
     const uint32_t *mask;     // [n_tokens][words] or null: chains
     const float *k_scale, *v_scale, *slopes;
-    // Parts of units: row (rank * 2 + which) * unit_slots + slot in the unit, `which` 1 where the unit begins in
-    // this rank's places
-    float *ws_o;              // [rows][HD]
-    float2 *ws_ml;            // [rows]
-    int4 *ws_span;            // [n_seq]: first place, tiles, first token, places of a rank
+    // Parts: block (rank * 2 + which) * units + unit of unit_slots slots, `which` 1 where the sequence begins in this
+    // rank's places
+    float *ws_o;              // [blocks][HD / 4][unit_slots][4]
+    float2 *ws_ml;            // [blocks][unit_slots]
+    int4 *ws_span;            // [units / n_kv_head][n_seq]: first place, tiles, first token, places of a rank
     unsigned *err;
     int64_t n_tokens, n_each; // n_each: nodes of a sequence when cu is null
     int64_t tok_end;          // tokens the joining kernel looks at
@@ -188,9 +188,12 @@ struct TreeArgs {
     int max_nodes, words;
     int n_head, n_kv_head, group;
     int max_pages, n_pages, page_size, cap, window;
-    int ranks, min_share;     // blocks that share the tiles; the least a block takes
+    int units;                // n_kv_head times what max_nodes has of unit_slots
+    int ranks, min_share;     // blocks that share a unit's tiles; the least a block takes
     int unit_slots;           // (node, head) pairs a block serves at once: 128 or 256
-    int nslot, nraw;          // 16-bit and 8-bit tiles of the rings
+    int q_parts;              // parts of q
+    uint32_t q_bytes;         // of Q in shared memory
+    int nk, nv, nrk, nrv;     // tiles of the rings of K and V, and of their 8-bit tiles that are converted
     int box_rows;             // rows of one TMA box
     bool once;                // no other block reads the same rows
     float qscale;             // scale * log2 e, or scale / softcap

@@ -19,14 +19,21 @@
 //
 // Parts. 16-bit queries and weights enter as one operand, f32 queries as two (the rounding, and the rounding of
 // what it left), and then the weights too: f16 over f16 and e4m3 caches (rows of q scaled by a power of two, so that nothing is
-// lost to f16's range), bf16 over bf16 caches.
+// lost to f16's range), bf16 over bf16 caches. 16-bit queries over an e4m3 cache are split into e4m3 parts instead --
+// two hold the 8 bits of a bfloat16, three the 11 of a binary16 -- so that K's codes enter the products as they
+// are, at twice the rate, and V alone is converted.
 //
-// Work. The tiles of all units -- (sequence, KV head, 128 or 256 slots) -- are laid end to end, and a block an
-// SM takes an equal run of them: what a block has of a unit is its output where it has all of it, else a part
-// (reference, sum, sum p v) for attn_tree_combine.
+// Work. A block serves one unit -- a KV head and 128 or 256 slots of it. The tiles that a unit has in all sequences are
+// laid end to end, and the unit's blocks (ranks; as many as make a block an SM) take equal runs of them:
+// what a block has of a sequence is its output where it has all of it, else a part (reference, sum, sum p v) for
+// attn_tree_combine. The KV heads of a rank run at the same time, so that the pieces of a row that they read are
+// asked of memory together (one row of blocks over all units in turn took 1.9 times as long over 32 sequences of up
+// to 32768 rows).
 //
-// Warps: 8 (4) of the softmax; 4 that convert an e4m3 tile to f16, and, in tiles that some slot does not see all
-// of, take infinities and NaN out of V (a weight of 0 would spread them); a producer (pages, TMA); an issuer.
+// Warps: 8 (4) of the softmax; 4 that convert e4m3 tiles to f16, and, in tiles that some slot does not see all
+// of, take infinities and NaN out of V (a weight of 0 would spread them); a producer of K and one of V (pages, TMA); an
+// issuer. What a single warp does for each tile takes some 8 cycles an instruction, and code that runs once is
+// fetched from L2 a line at a time: both are written for few instructions.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -40,7 +47,7 @@
 namespace attn {
 
 constexpr unsigned kErrBadTree = 0x8u;        // ATTN_DEVERR_BAD_REQUEST
-constexpr int kTreeDesc = 8;                  // tiles whose descriptors are kept: more than the rings hold
+constexpr int kTreeDesc = 8;                  // tiles whose descriptors are kept: K runs at most 5 tiles ahead of S, S 2 of P
 
 template <int HD_, typename KV_, int PARTS_>
 struct TreeCfg {
@@ -52,18 +59,27 @@ struct TreeCfg {
     static constexpr int TR = HD == 256 ? 64 : 128;            // cache rows of a tile
     static constexpr int NSLC = TR / 16;                       // 16-row slices
     static constexpr int TPG = 32 / NSLC;                      // tiles whose pages a warp looks up at once
-    static constexpr int SM_WARPS = 4 * NS, FIX = SM_WARPS, PROD = FIX + 4, MMA = PROD + 1;
-    static constexpr int THREADS = (MMA + 1) * 32;
-    static constexpr int NCH = HD / 64;                        // 128-byte chunks of a 16-bit row
-    static constexpr uint32_t QPART = 128u * HD * 2;           // a part of a tile of Q
+    static constexpr int SM_WARPS = 4 * NS, FIX = SM_WARPS;
+    // of a block of few slots the first warps have rows, those of the first scheduler: the issuer and the producers are
+    // with the others
+    static constexpr int PROD_V = FIX + 5, MMA = FIX + 6, PROD_K = FIX + 7;
+    // whole warpgroups where registers move between them: 512 threads of 128, of which the softmax takes 176 each, the
+    // converting warps 80, the last four (two have nothing to do) 72 -- 64512 of the block's 65536
+    static constexpr int THREADS = (PROD_K + 1) * 32;
+    // 8-bit K as it is (with q in 8-bit parts), or converted
+    static constexpr bool F8 = E8 && PARTS == 1, KCONV = E8 && !F8;
+    static constexpr int QES = F8 ? 1 : 2;                     // bytes of an element of a part of q
+    static constexpr uint32_t QPART = 128u * HD * QES;         // a part of a tile of Q
     static constexpr uint32_t SLOT = (uint32_t)TR * HD * 2;    // K or V of a tile, 16 bits
     static constexpr uint32_t RAW = (uint32_t)TR * HD;         // 8 bits
-    static constexpr int RCHB = HD < 128 ? HD : 128, RNCH = HD / RCHB;   // chunks of an 8-bit row
+    static constexpr uint32_t KSLOT = F8 ? RAW : SLOT;
+    // chunks of a row as they lie in shared memory: 128 bytes (64: 8-bit rows of 64 dimensions)
+    static constexpr int RCHB = HD < 128 ? HD : 128, RNCH = HD / RCHB, NCH = HD / 64;
     static constexpr uint32_t TM_S = 0, TM_O = 2 * TR, TM_COLS = 512;
     static constexpr uint32_t DATA = 224 * 1024;               // Q and the rings
     static constexpr uint32_t OFF_DESC = DATA;
     static constexpr uint32_t OFF_BAR = OFF_DESC + kTreeDesc * 96;
-    static constexpr int NBAR = 8 + 8 + 8 + 8 + 2 + 2 + 2 + 1;
+    static constexpr int NBAR = 39 + kTreeDesc;
     static constexpr uint32_t OFF_FLAG = OFF_BAR + NBAR * 8;   // TMEM slot, abort, share, total
     static constexpr uint32_t OFF_SEQ = OFF_FLAG + 16;         // before, first token, rows
     static constexpr uint32_t SMEM = OFF_SEQ + (3 * kPagedSeqs + 2) * 4;
@@ -81,11 +97,11 @@ struct __align__(16) TileInfo {
 };
 static_assert(sizeof(TileInfo) == 96, "its place in shared memory");
 
-// A block's share of a unit: sequence s, KV head hk, slots from m * 128 NS.. on; tiles [t0, t1) of its T
+// What a block has of a sequence: tiles [t0, t1) of its T
 struct TreeSeg {
-    int s, hk, m, t0, t1, T;
+    int s, t0, t1, T;
     int n, tok0, nkv, base, start;
-    int slots;                // of the unit, at most 256
+    int slots;                // of the unit in this sequence, at most 256
     bool pair;                // more than 128: both warpgroups on every tile
     int row0;                 // first row of tile 0
 };
@@ -132,6 +148,13 @@ __device__ __forceinline__ void tmem_ld2(uint32_t t, uint32_t &a, uint32_t &b)
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// The same with e4m3 operands.
+__device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
 // D += A B with A in tensor memory; issued by one thread.
 __device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc)
 {
@@ -140,9 +163,103 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, 
                  :: "r"(d), "r"(a), "l"(b), "r"(idesc) : "memory");
 }
 
+__device__ __forceinline__ uint32_t e4m3x4_of(float a, float b, float c, float d)
+{
+    uint16_t x, y;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(x) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(y) : "f"(d), "f"(c));
+    return (uint32_t)x | (uint32_t)y << 16;
+}
 __device__ __forceinline__ void sts128(uint32_t p, const uint4 &v)
 {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// mbarriers by their 32-bit shared addresses (as in attn_device.cuh otherwise)
+__device__ __forceinline__ void bar_init(uint32_t bar, unsigned count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar)
+{
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_arrive_expect_tx(uint32_t bar, unsigned bytes)
+{
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}"
+                 :: "r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, unsigned parity)
+{
+    unsigned ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+// Gives up after some 2^31 cycles, a second or more (by the SM's clock: reading %globaltimer takes longer than most
+// waits here).
+__device__ __forceinline__ bool bar_wait(uint32_t bar, unsigned parity)
+{
+    if (bar_try(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (true) {
+        if (bar_try(bar, parity)) return true;
+        if (clock64() - t0 > (1ll << 31)) return false;
+    }
+}
+__device__ __forceinline__ void bar_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ void tree_tma(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z, int w, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;"
+        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+// 1 / x to 2^-23 (division proper is a call, with registers saved around it)
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Pairs of f32 in one instruction
+__device__ __forceinline__ uint64_t pack2(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t x)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // Bits [a, b) of 32, for a and b of any size.
@@ -162,48 +279,63 @@ struct Tree {
     const TreeArgs &a;
     uint8_t *smem;
     uint32_t sm;
-    uint64_t *full, *empty, *ready, *raw_free;   // rings: full: TMA's; ready: converted or looked at; empty, raw_free: to be filled
-    uint64_t *s_full, *p_ready, *o_done, *q_ready;
-    volatile int *flags;                         // [0] TMEM address, [1] abort, [2] share, [3] total
-    int *before, *tok, *rows;
-    int nslot, nraw;
-    uint32_t off_slot, off_raw;
 
-    __device__ __forceinline__ Tree(const TreeArgs &args, uint8_t *base) : a(args), smem(base)
-    {
-        sm = smem_u32(smem);
-        full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
-        ready = full + 8;
-        empty = ready + 8;
-        raw_free = empty + 8;
-        s_full = raw_free + 8;
-        p_ready = s_full + 2;
-        o_done = p_ready + 2;
-        q_ready = o_done + 2;
-        flags = reinterpret_cast<volatile int *>(smem + C::OFF_FLAG);
-        before = reinterpret_cast<int *>(smem + C::OFF_SEQ);
-        tok = before + kPagedSeqs + 1;
-        rows = tok + kPagedSeqs + 1;
-        nslot = a.nslot;
-        nraw = a.nraw;
-        off_slot = (uint32_t)(a.unit_slots / 128) * PARTS * C::QPART;
-        off_raw = off_slot + nslot * C::SLOT;
-    }
+    __device__ __forceinline__ Tree(const TreeArgs &args, uint8_t *base) : a(args), smem(base), sm(smem_u32(base)) {}
 
-    __device__ __forceinline__ bool wait(uint64_t *bar, unsigned parity)
+    // Rings of tiles of K and of V. full: TMA's copies are there; ready: converted or looked at; empty, raw: to be
+    // filled again (16-bit tiles, and K's that are used as they are; 8-bit tiles that are converted)
+    __device__ __forceinline__ uint32_t bar(int i) const { return sm + C::OFF_BAR + 8 * i; }
+    __device__ __forceinline__ uint32_t full(bool v, int i) const { return bar(v * 16 + i); }
+    __device__ __forceinline__ uint32_t ready(bool v, int i) const { return bar(v * 16 + 4 + i); }
+    __device__ __forceinline__ uint32_t empty(bool v, int i) const { return bar(v * 16 + 8 + i); }
+    __device__ __forceinline__ uint32_t raw(bool v, int i) const { return bar(v * 16 + 12 + i); }
+    __device__ __forceinline__ uint32_t s_full(int i) const { return bar(32 + i); }
+    __device__ __forceinline__ uint32_t p_ready(int i) const { return bar(34 + i); }
+    __device__ __forceinline__ uint32_t o_done(int i) const { return bar(36 + i); }
+    __device__ __forceinline__ uint32_t q_ready() const { return bar(38); }
+    __device__ __forceinline__ uint32_t described(unsigned tile) const { return bar(39 + (tile & (kTreeDesc - 1))); }
+    // [0] tensor memory, [1] abort, [2] places of a rank, [3] of all
+    __device__ __forceinline__ volatile int *flags() const { return reinterpret_cast<volatile int *>(smem + C::OFF_FLAG); }
+    __device__ __forceinline__ int *before() const { return reinterpret_cast<int *>(smem + C::OFF_SEQ); }   // places before each sequence
+    __device__ __forceinline__ int *tok() const { return before() + kPagedSeqs + 1; }                        // first tokens
+    __device__ __forceinline__ int *rows() const { return tok() + kPagedSeqs + 1; }                          // rows
+    // Q, then V's tiles, K's, and the 8-bit ones that are converted
+    __device__ __forceinline__ uint32_t v_slot(int i) const { return sm + a.q_bytes + i * C::SLOT; }
+    __device__ __forceinline__ uint32_t k_slot(int i) const { return v_slot(a.nv) + i * C::KSLOT; }
+    __device__ __forceinline__ uint32_t raw_slot(bool v, int i) const { return k_slot(a.nk) + ((v ? 0 : a.nrv) + i) * C::RAW; }
+    // A place in a ring of n tiles, and the parity of what is waited for there
+    struct Ring {
+        int at;
+        unsigned phase;
+        __device__ __forceinline__ void next(int n)
+        {
+            if (++at == n) {
+                at = 0;
+                phase ^= 1;
+            }
+        }
+    };
+
+    __device__ __forceinline__ bool wait(uint32_t bar, unsigned parity)
     {
-        if (mbar_wait_bounded(bar, parity)) return true;
-        flags[1] = 1;
+        if (bar_wait(bar, parity)) return true;
+        flags()[1] = 1;
         atomicOr(a.err, kErrPipelineTimeout);
         return false;
     }
-    // by a whole warp
-    __device__ __forceinline__ bool wait_warp(uint64_t *bar, unsigned parity)
+    // by a whole warp: one lane asks
+    __device__ __forceinline__ bool wait_warp(uint32_t bar, unsigned parity)
     {
-        return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
+        int ok = 1;
+        if ((threadIdx.x & 31) == 0) ok = wait(bar, parity);
+        return __shfl_sync(0xffffffffu, ok, 0) != 0;
     }
 
     __device__ __forceinline__ TileInfo *tile_info(unsigned count) { return reinterpret_cast<TileInfo *>(smem + C::OFF_DESC) + (count & (kTreeDesc - 1)); }
+
+    // The block's unit: its KV head, and the first of its slots
+    __device__ __forceinline__ int hk() const { return blockIdx.x % a.n_kv_head; }
+    __device__ __forceinline__ int first_slot() const { return blockIdx.x / a.n_kv_head * a.unit_slots; }
 
     // Rows of a sequence that some node may see: [low, high)
     __device__ __forceinline__ int low_of(int base, int start) const
@@ -223,23 +355,19 @@ struct Tree {
         int lo = 0, hi = a.n_seq - 1;
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
-            if (before[mid + 1] > p) hi = mid;
+            if (before()[mid + 1] > p) hi = mid;
             else lo = mid + 1;
         }
         g.s = lo;
-        g.tok0 = tok[lo];
-        g.n = tok[lo + 1] - g.tok0;
-        g.nkv = rows[lo];
+        g.tok0 = tok()[lo];
+        g.n = tok()[lo + 1] - g.tok0;
+        g.nkv = rows()[lo];
         g.base = g.nkv - g.n;
         g.start = a.starts ? ld_dep(a.starts + lo) : 0;
-        const int all = g.n * a.group, units = (all + a.unit_slots - 1) / a.unit_slots;
-        g.T = (before[lo + 1] - before[lo]) / (units * a.n_kv_head);
-        const int x = p - before[lo], u = x / g.T;
-        g.t0 = x - u * g.T;
+        g.T = before()[lo + 1] - before()[lo];
+        g.t0 = p - before()[lo];
         g.t1 = min(g.T, g.t0 + end - p);
-        g.hk = u / units;
-        g.m = u - g.hk * units;
-        g.slots = min(all - g.m * a.unit_slots, a.unit_slots);
+        g.slots = min(g.n * a.group - first_slot(), a.unit_slots);
         g.pair = NS == 2 && g.slots > 128;
         g.row0 = min(low_of(g.base, g.start), g.nkv) / TR * TR;
         return p + g.t1 - g.t0;
@@ -266,18 +394,17 @@ struct Tree {
             }
             const int start = a.starts ? ld_dep(a.starts + s) : 0;
             int n = (int)max(c1 - c0, (int64_t)0);
-            tok[s] = (int)c0;
-            if (s == a.n_seq - 1) tok[s + 1] = (int)max(c1, c0);
-            const bool report = blockIdx.x == 0;
+            tok()[s] = (int)c0;
+            if (s == a.n_seq - 1) tok()[s + 1] = (int)max(c1, c0);
+            const bool report = (blockIdx.x | blockIdx.y) == 0;
             if (n > a.max_nodes) {
                 if (report) atomicOr(a.err, kErrBadTree);
                 n = 0;
             }
             if (n > 0 && (pos < -1 || pos >= a.cap) && report) atomicOr(a.err, kErrPositionClamped);
             const int nkv = min(max(pos, -1), a.cap - 1) + 1;
-            rows[s] = nkv;
-            const int units = (n * a.group + a.unit_slots - 1) / a.unit_slots * a.n_kv_head;
-            places[i] = tiles_of(n, nkv, start) * units;
+            rows()[s] = nkv;
+            if (n * a.group > first_slot()) places[i] = tiles_of(n, nkv, start);
             sum += places[i];
         }
         int upto = sum;
@@ -292,198 +419,180 @@ struct Tree {
         for (int i = 0; i < MOST; ++i) {
             const int s = lane * per + i;
             if (i >= per || s >= a.n_seq) continue;
-            before[s] = at;
+            before()[s] = at;
             at += places[i];
         }
         if (lane == 0) {
-            before[a.n_seq] = total;
-            flags[2] = max((total + a.ranks - 1) / a.ranks, a.min_share);
-            flags[3] = total;
+            before()[a.n_seq] = total;
+            flags()[2] = max((total + a.ranks - 1) / a.ranks, a.min_share);
+            flags()[3] = total;
         }
     }
 
-    // K and V of tiles in the order in which the tensor cores first need them: with `lag` 1 K of the next tile
-    // before V of this one.
-    struct Order {
-        int T, lag, m, v;
-        __device__ __forceinline__ Order(const TreeSeg &g) : T(g.t1 - g.t0), lag(g.pair ? 0 : 1), m(0), v(0) {}
-        // is_v, tile (from 0); false: no more
-        __device__ __forceinline__ bool next(bool &is_v, int &tile)
-        {
-            while (m < T + lag) {
-                if (v == 0) {
-                    v = 1;
-                    if (m < T) {
-                        is_v = false;
-                        tile = m;
-                        return true;
-                    }
-                }
-                v = 0;
-                const int x = m++ - lag;
-                if (x >= 0) {
-                    is_v = true;
-                    tile = x;
-                    return true;
-                }
-            }
-            return false;
-        }
-    };
-
     // -----------------------------------------------------------------------
-    // Producer warp: pages, descriptors, copies.
+    // Producer warps, one of K and one of V: pages, copies; K's writes the tiles' descriptors.
     // -----------------------------------------------------------------------
-    __device__ __forceinline__ void produce(const CUtensorMap *kmap, const CUtensorMap *vmap, int from, int end, int lane)
+    template <bool V>
+    __device__ __forceinline__ void produce(const CUtensorMap *map, int from, int end, int lane)
     {
+        constexpr bool CONV = V ? C::E8 : C::KCONV;
+        constexpr int NC = C::E8 ? C::RNCH : C::NCH, CB = C::E8 ? C::RCHB : 128, CW = C::E8 ? C::RCHB : 64;
         // lines that no other block reads are the first that L2 gives up
         uint64_t policy;
         if (a.once) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
         else asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
-        const int nring = C::E8 ? nraw : nslot;
-        uint64_t *free = C::E8 ? raw_free : empty;
-        int ring = 0;
-        unsigned phase = 1;                       // the ring is free at first
+        Ring ring{0, 1};                          // it is free at first
+        const int n = CONV ? (V ? a.nrv : a.nrk) : (V ? a.nv : a.nk);
         unsigned tiles = 0;                       // before the segment
-        const int BR = a.box_rows, per_box = BR / 16;
-        const int lt = lane / C::NSLC, ls = lane % C::NSLC;
+        const int BR = a.box_rows, lt = lane / C::NSLC, ls = lane % C::NSLC;
+        const bool leads = (ls & (BR / 16 - 1)) == 0;         // the first slice of a box
+        constexpr unsigned TILE_BITS = (1u << C::NSLC) - 1u;
         for (int p = from; p < end;) {
             TreeSeg g;
             p = segment(p, end, g);
             const int T = g.t1 - g.t0, low = low_of(g.base, g.start);
             const int32_t *table = a.table + (size_t)g.s * a.max_pages;
-            // lane l has slice l % NSLC of tile l / NSLC of a group; -2: nothing of its box is seen
+            // lane l has slice l % NSLC of tile l / NSLC of a group: its page (-2: nothing of its box is seen)
+            const int row0 = g.row0 + (g.t0 + lt) * TR + ls * 16;
             auto page_of = [&](int grp) {
-                const int t = grp * C::TPG + lt, r = g.row0 + (g.t0 + t) * TR + ls * 16, box = r & -BR;
-                return t < T && box < g.nkv && box + BR > low ? ld_dep(table + div(a.by_page, r)) : -2;
+                const int r = row0 + grp * (C::TPG * TR), box = r & -BR;
+                return grp * C::TPG + lt < T && box < g.nkv && box + BR > low ? ld_dep(table + div(a.by_page, r)) : -2;
             };
             auto scale_of = [&](int page) {
                 float2 f = make_float2(1.f, 1.f);
-                if (C::E8 && (unsigned)page < (unsigned)a.n_pages) {
-                    f.x = ld_dep(a.k_scale + (size_t)page * a.n_kv_head + g.hk);
-                    f.y = ld_dep(a.v_scale + (size_t)page * a.n_kv_head + g.hk);
+                if (C::E8 && !V && (unsigned)page < (unsigned)a.n_pages) {
+                    f.x = ld_dep(a.k_scale + (size_t)page * a.n_kv_head + hk());
+                    f.y = ld_dep(a.v_scale + (size_t)page * a.n_kv_head + hk());
                 }
                 return f;
             };
             // pages are asked for two groups ahead, scales one
-            int prev = -2, cur = page_of(0), next = page_of(1), far = page_of(2), grp = 0;
+            int cur = page_of(0), next = page_of(1), far = page_of(2);
             float2 f = scale_of(cur), fnext = scale_of(next);
-            const int seen_lo = max(g.start, a.window > 0 ? g.base + a.max_nodes - a.window : 0);
-            // A tile's descriptor goes over that of the tile kTreeDesc before it, whose V has left the rings.
-            auto describe = [&](int tile) {
+#pragma unroll 1
+            for (int t0 = 0, grp = 0; t0 < T; t0 += C::TPG, ++grp) {
                 const bool there = (unsigned)cur < (unsigned)a.n_pages;
-                const unsigned mine = __ballot_sync(0xffffffffu, there) >> (lt * C::NSLC) & ((1u << C::NSLC) - 1u);
-                if (lt != tile % C::TPG) return;
-                if (cur != -2 && !there) atomicOr(a.err, kErrBadPage);
-                TileInfo *d = tile_info(tiles + tile);
-                d->ks[ls] = f.x;
-                d->vs[ls] = f.y;
-                if (ls == 0) {
-                    const int r = g.row0 + (g.t0 + tile) * TR;
-                    d->row0 = r;
-                    d->edge = r < seen_lo || r + TR > g.base || mine != (1u << C::NSLC) - 1u;
-                    d->slices = mine;
-                    d->live = g.nkv - r;
-                    d->bad[0] = d->bad[1] = d->bad[2] = d->bad[3] = 0u;
-                }
-            };
-            Order order(g);
-            bool is_v;
-            int tile;
-            while (order.next(is_v, tile)) {
-                if (!is_v && tile / C::TPG != grp) {          // V of the tile before may still need the last group's
-                    ++grp;
-                    prev = cur;
-                    cur = next;
-                    f = fnext;
-                    next = far;
-                    far = page_of(grp + 2);
-                    fnext = scale_of(next);
-                }
-                const int src = tile / C::TPG == grp ? cur : prev;
-                int pages[C::NSLC];
+                const unsigned slices = __ballot_sync(0xffffffffu, there), boxes = __ballot_sync(0xffffffffu, there && leads);
+                const int r = row0 + grp * (C::TPG * TR), z = r - div(a.by_page, r) * a.page_size;
+                const unsigned negative = V ? 0u : __ballot_sync(0xffffffffu, f.x < 0.f);
+                const int count = min(C::TPG, T - t0);
+#pragma unroll 1
+                for (int i = 0; i < count; ++i) {
+                    if (!wait_warp(CONV ? raw(V, ring.at) : empty(V, ring.at), ring.phase)) return;
+                    const unsigned mine = slices >> (i * C::NSLC) & TILE_BITS;
+                    if (lt == i) {                             // a lane for each box
+                        if (there && leads) {
+                            const uint32_t to = (CONV ? raw_slot(V, ring.at) : V ? v_slot(ring.at) : k_slot(ring.at)) + ls * 16 * CB;
 #pragma unroll
-                for (int i = 0; i < C::NSLC; ++i) pages[i] = __shfl_sync(0xffffffffu, src, tile % C::TPG * C::NSLC + i);
-                bool ok = true;
-                unsigned bytes = 0;
-                if (lane == 0) {
-                    ok = wait(free + ring, phase);
-                    if (ok) {
-                        uint8_t *to = smem + (C::E8 ? off_raw + ring * C::RAW : off_slot + ring * C::SLOT);
-                        const CUtensorMap *map = is_v ? vmap : kmap;
-                        constexpr int NC = C::E8 ? C::RNCH : C::NCH, CB = C::E8 ? C::RCHB : 128, CW = C::E8 ? C::RCHB : 64;
-                        const int r0 = g.row0 + (g.t0 + tile) * TR;
-#pragma unroll
-                        for (int i = 0; i < C::NSLC; ++i) {
-                            if (i % per_box != 0 || (unsigned)pages[i] >= (unsigned)a.n_pages) continue;
-                            const int r = r0 + i * 16, z = r - div(a.by_page, r) * a.page_size;
-                            bytes += (unsigned)BR * HD * (C::E8 ? 1 : 2);
-#pragma unroll
-                            for (int c = 0; c < NC; ++c)
-                                tma_load_4d_once(to + c * (TR * CB) + i * 16 * CB, map, full + ring, c * CW, g.hk, z, pages[i], policy);
+                            for (int c = 0; c < NC; ++c) tree_tma(to + c * (TR * CB), map, full(V, ring.at), c * CW, hk(), z, cur, policy);
+                        }
+                        if (!V) {
+                            // the copies are on their way; the tile is whole once lane 0 has arrived too
+                            if (cur != -2 && !there) atomicOr(a.err, kErrBadPage);
+                            TileInfo *d = tile_info(tiles + i);
+                            d->ks[ls] = f.x;
+                            d->vs[ls] = f.y;
+                            if (ls == 0) {
+                                const int seen_lo = max(g.start, a.window > 0 ? g.base + a.max_nodes - a.window : 0);
+                                d->row0 = r;
+                                d->edge = (r < seen_lo || r + TR > g.base || mine != TILE_BITS ? 1 : 0) |
+                                          (negative >> (i * C::NSLC) & TILE_BITS ? 2 : 0);
+                                d->slices = mine;
+                                d->live = g.nkv - r;
+                                *reinterpret_cast<uint4 *>(d->bad) = make_uint4(0u, 0u, 0u, 0u);
+                            }
                         }
                     }
+                    __syncwarp();
+                    if (!V && lane == 0) bar_arrive(described(tiles + i));
+                    if (lane == 0)
+                        bar_arrive_expect_tx(full(V, ring.at), __popc(boxes >> (i * C::NSLC) & TILE_BITS) * (unsigned)BR * HD * (C::E8 ? 1 : 2));
+                    ring.next(n);
                 }
-                if (!__shfl_sync(0xffffffffu, (int)ok, 0)) return;
-                // the copies are on their way; the tile is whole once this thread has arrived too
-                if (!is_v) describe(tile);
-                __syncwarp();
-                if (lane == 0) mbar_arrive_expect_tx(full + ring, bytes);
-                if (++ring == nring) {
-                    ring = 0;
-                    phase ^= 1;
-                }
+                tiles += count;
+                cur = next;
+                f = fnext;
+                next = far;
+                far = page_of(grp + 3);
+                fnext = scale_of(next);
             }
-            tiles += T;
         }
     }
 
     // -----------------------------------------------------------------------
-    // Four warps that make a tile ready for the tensor cores.
+    // Four warps that make tiles ready for the tensor cores: of V, and of K where it is converted.
     // -----------------------------------------------------------------------
+    // A tile of codes to f16. A thread's units of 16 codes: one column, rows RSTEP (a multiple of 8) apart, so that the swizzle
+    // is the same for all; their loads go out before the first conversion.
+    template <bool V>
+    __device__ __forceinline__ bool convert(Ring &rr, Ring &sr, int tid)
+    {
+        constexpr int UPR = HD / 16, RSTEP = 128 / UPR, N = TR / RSTEP;
+        const int r = tid / UPR, u = tid % UPR, c = u >> 2, v = (u & 3) * 2;
+        if (!wait_warp(full(V, rr.at), rr.phase)) return false;
+        uint32_t src = raw_slot(V, rr.at);
+        if constexpr (C::RCHB == 128) src += (u >> 3) * (TR * 128) + r * 128 + ((u ^ r) & 7) * 16;
+        else src += r * 64 + (((u ^ (r >> 1)) & 3) << 4);
+        uint4 x[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) x[k] = lds128(src + k * RSTEP * C::RCHB);
+        if (!wait_warp(empty(V, sr.at), sr.phase)) return false;
+        // lanes of odd chunks write their second unit first: other banks than the even ones
+        const bool odd = c & 1;
+        const uint32_t dst = (V ? v_slot(sr.at) : k_slot(sr.at)) + c * (TR * 128) + r * 128;
+        const uint32_t dst0 = dst + (((v + odd) ^ (r & 7)) << 4), dst1 = dst + (((v + !odd) ^ (r & 7)) << 4);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            uint4 y0, y1;
+            e4m3x4_to_half4(x[k].x, y0.x, y0.y);
+            e4m3x4_to_half4(x[k].y, y0.z, y0.w);
+            e4m3x4_to_half4(x[k].z, y1.x, y1.y);
+            e4m3x4_to_half4(x[k].w, y1.z, y1.w);
+            sts128(dst0 + k * RSTEP * 128, odd ? y1 : y0);
+            sts128(dst1 + k * RSTEP * 128, odd ? y0 : y1);
+        }
+        return true;
+    }
+
     __device__ __forceinline__ void fix(int from, int end, int tid)
     {
-        int ring = 0, slot = 0;
-        unsigned phase = 0, sphase = 1, tiles = 0;
         const int lane = tid & 31;
+        Ring vr{0, 0}, vs{0, C::E8 ? 1u : 0u}, kr{0, 0}, ks{0, 1};
+        unsigned tiles = 0;
+        auto key = [&] {                                       // K of the next tile
+            if (!convert<false>(kr, ks, tid)) return false;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                bar_arrive(raw(false, kr.at));
+                bar_arrive(ready(false, ks.at));
+            }
+            kr.next(a.nrk);
+            ks.next(a.nk);
+            return true;
+        };
         for (int p = from; p < end;) {
             TreeSeg g;
             p = segment(p, end, g);
-            Order order(g);
-            bool is_v;
-            int tile;
-            while (order.next(is_v, tile)) {
-                if (!wait_warp(full + (C::E8 ? ring : slot), C::E8 ? phase : sphase ^ 1)) return;
-                TileInfo *d = tile_info(tiles + tile);
-                const volatile TileInfo *vd = d;
-                const bool look = is_v && vd->edge;
-                const uint32_t to = sm + off_slot + slot * C::SLOT;
+            const int T = g.t1 - g.t0;
+            // K before V, with both warpgroups on a tile each K of the next tile too
+            const int ahead = g.pair ? 0 : 1;
+            if (C::KCONV && ahead && !key()) return;
+#pragma unroll 1
+            for (int t = 0; t < T; ++t, ++tiles) {
+                if (C::KCONV && t + ahead < T && !key()) return;
                 if constexpr (C::E8) {
-                    if (!wait_warp(empty + slot, sphase)) return;
-                    const uint32_t raw = sm + off_raw + ring * C::RAW;
-                    constexpr int UPR = HD / 16;               // 16-byte units of a raw row
-#pragma unroll 4
-                    for (int i = tid; i < TR * UPR; i += 128) {
-                        const int r = i / UPR, u = i % UPR;
-                        uint32_t src;
-                        if constexpr (C::RCHB == 128) src = raw + (u >> 3) * (TR * 128) + r * 128 + ((u ^ r) & 7) * 16;
-                        else src = raw + r * 64 + (((u ^ (r >> 1)) & 3) << 4);
-                        const uint4 x = lds128(src);
-                        uint4 y0, y1;
-                        e4m3x4_to_half4(x.x, y0.x, y0.y);
-                        e4m3x4_to_half4(x.y, y0.z, y0.w);
-                        e4m3x4_to_half4(x.z, y1.x, y1.y);
-                        e4m3x4_to_half4(x.w, y1.z, y1.w);
-                        if (look) clean(d, r, y0, y1);
-                        const int c = u >> 2, v = (u & 3) * 2;
-                        const uint32_t dst = to + c * (TR * 128) + r * 128;
-                        // lanes of odd chunks write their second unit first: other banks than the even ones
-                        const bool odd = c & 1;
-                        sts128(dst + (((v + odd) ^ (r & 7)) << 4), odd ? y1 : y0);
-                        sts128(dst + (((v + !odd) ^ (r & 7)) << 4), odd ? y0 : y1);
-                    }
-                    fence_proxy_async_smem();
-                } else if (look) {
+                    if (!convert<true>(vr, vs, tid)) return;
+                } else {
+                    if (!wait_warp(full(true, vs.at), vs.phase)) return;
+                }
+                if (!wait_warp(described(tiles), tiles / kTreeDesc & 1)) return;
+                TileInfo *d = tile_info(tiles);
+                const bool look = static_cast<volatile TileInfo *>(d)->edge & 1;
+                if (look) {
+                    if (C::E8) asm volatile("bar.sync 2, 128;" ::: "memory");   // other warps' rows
+                    const uint32_t to = v_slot(vs.at);
+#pragma unroll 1
                     for (int i = tid; i < TR * (HD / 16); i += 128) {
                         const int r = i % TR, u = i / TR * 2;
                         const uint32_t at = to + (u >> 3) * (TR * 128) + r * 128;
@@ -494,23 +603,16 @@ struct Tree {
                             sts128(p1, y1);
                         }
                     }
-                    fence_proxy_async_smem();
                 }
+                if (C::E8 || look) fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    if (C::E8) mbar_arrive(raw_free + ring);
-                    mbar_arrive(ready + slot);
+                    if (C::E8) bar_arrive(raw(true, vr.at));
+                    bar_arrive(ready(true, vs.at));
                 }
-                if (C::E8 && ++ring == nraw) {
-                    ring = 0;
-                    phase ^= 1;
-                }
-                if (++slot == nslot) {
-                    slot = 0;
-                    sphase ^= 1;
-                }
+                if (C::E8) vr.next(a.nrv);
+                vs.next(a.nv);
             }
-            tiles += g.t1 - g.t0;
         }
     }
 
@@ -543,31 +645,34 @@ struct Tree {
     // -----------------------------------------------------------------------
     __device__ __forceinline__ void issue(uint32_t tm, int from, int end)
     {
-        int slot = 0;
-        unsigned phase = 0, cnt[2] = {0, 0}, done[2] = {0, 0}, segs = 0;   // items whose S, whose P V was issued, by stream
-        auto take = [&](int &got) {                            // the next entry of the ring
-            if (!wait(ready + slot, phase)) return false;
-            got = slot;
-            if (++slot == nslot) {
-                slot = 0;
-                phase ^= 1;
-            }
-            return true;
-        };
-        constexpr uint32_t id_s = umma_idesc<MT>(128, TR, 0, 0), id_o = umma_idesc<MT>(128, HD, 0, 1);
-        auto scores = [&](int qt, int b, int ks) {
-            const uint32_t k = sm + off_slot + ks * C::SLOT, q = sm + (uint32_t)qt * PARTS * C::QPART;
+        Ring kr{0, 0}, vr{0, 0};
+        unsigned segs = 0, seen = 0, done0 = 0, done1 = 0;     // items whose S (one stream), whose P V was issued, by stream
+        constexpr uint32_t id_s = C::F8 ? 1u << 4 | (uint32_t)(TR >> 3) << 17 | 8u << 24 : umma_idesc<MT>(128, TR, 0, 0);
+        constexpr uint32_t id_o = umma_idesc<MT>(128, HD, 0, 1);
+        auto scores = [&](int qt, int b) {
+            const uint32_t k = k_slot(kr.at), q = sm + (uint32_t)qt * a.q_parts * C::QPART, d = tm + C::TM_S + b * TR;
             tc_fence_after();
+            if constexpr (C::F8) {
+                // 32 codes a step; rows of 128 bytes (swizzle 2, 8 rows 1024 bytes apart) or 64 (4, 512)
+                constexpr uint32_t SW = C::RCHB == 128 ? 2 : 4, SBO = C::RCHB * 8;
+#pragma unroll 1
+                for (int x = 0; x < a.q_parts; ++x)
 #pragma unroll
-            for (int x = 0; x < PARTS; ++x)
+                    for (int kk = 0; kk < HD / 32; ++kk)
+                        umma_f8(d, umma_desc(q + x * C::QPART + (kk >> 2) * 16384 + (kk & 3) * 32, 16, SBO, SW),
+                                umma_desc(k + (kk >> 2) * (TR * 128) + (kk & 3) * 32, 16, SBO, SW), id_s, x + kk > 0);
+            } else {
 #pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk)
-                    umma_f16(tm + C::TM_S + b * TR, umma_desc(q + x * C::QPART + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024, 2),
-                             umma_desc(k + (kk >> 2) * (TR * 128) + (kk & 3) * 32, 16, 1024, 2), id_s, x + kk > 0);
-            umma_commit(s_full + b);
+                for (int x = 0; x < PARTS; ++x)
+#pragma unroll
+                    for (int kk = 0; kk < HD / 16; ++kk)
+                        umma_f16(d, umma_desc(q + x * C::QPART + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024, 2),
+                                 umma_desc(k + (kk >> 2) * (TR * 128) + (kk & 3) * 32, 16, 1024, 2), id_s, x + kk > 0);
+            }
+            bar_commit(s_full(b));
         };
-        auto values = [&](int w, int b, int vs) {
-            const uint32_t v = sm + off_slot + vs * C::SLOT;
+        auto values = [&](int w, int b) {
+            const uint32_t v = v_slot(vr.at);
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < TR / 16; ++kk)
@@ -575,35 +680,42 @@ struct Tree {
                 for (int x = 0; x < PARTS; ++x)
                     umma_f16_ts(tm + C::TM_O + w * HD, tm + C::TM_S + b * TR + 32 * (kk >> 1) + 16 * x + 8 * (kk & 1),
                                 umma_desc(v + kk * 2048, TR * 128, 1024, 2), id_o);
-            umma_commit(o_done + b);
+            bar_commit(o_done(b));
         };
         for (int p = from; p < end;) {
             TreeSeg g;
             p = segment(p, end, g);
-            if (!wait(q_ready, segs++ & 1)) return;
+            if (!wait(q_ready(), segs++ & 1)) return;
             const int T = g.t1 - g.t0, items = g.pair ? 2 * T : T;
-            int kslot = 0, vslot = 0, pw = 0, pb = 0;
+            int pw = 0, pb = 0;
+#pragma unroll 1
             for (int i = 0; i <= items; ++i) {
                 int w = 0, b = 0;
                 if (i < items) {
                     w = NS == 2 ? i & 1 : 0;
-                    b = NS == 2 ? w : (int)(cnt[0] & 1);
-                    if (!(g.pair && w == 1) && !take(kslot)) return;
-                    scores(g.pair ? w : 0, b, kslot);
-                    if (!g.pair || w == 1) umma_commit(empty + kslot);
+                    b = NS == 2 ? w : (int)(seen++ & 1);
+                    const bool fresh = !g.pair || w == 0, last = !g.pair || w == 1;
+                    if (fresh && !wait(C::KCONV ? ready(false, kr.at) : full(false, kr.at), kr.phase)) return;
+                    scores(g.pair ? w : 0, b);
+                    if (last) {
+                        bar_commit(empty(false, kr.at));
+                        kr.next(a.nk);
+                    }
                 }
                 if (i > 0) {                                   // the item before
-                    if (!wait(p_ready + pb, NS == 2 ? done[pw] & 1 : done[0] >> 1 & 1)) return;
-                    if (!(g.pair && pw == 1) && !take(vslot)) return;
-                    values(pw, pb, vslot);
-                    if (!g.pair || pw == 1) umma_commit(empty + vslot);
-                    ++done[pw];
+                    if (!wait(p_ready(pb), NS == 1 ? done0 >> 1 & 1 : pw ? done1 & 1 : done0 & 1)) return;
+                    const bool fresh = !g.pair || pw == 0, last = !g.pair || pw == 1;
+                    if (fresh && !wait(ready(true, vr.at), vr.phase)) return;
+                    values(pw, pb);
+                    if (last) {
+                        bar_commit(empty(true, vr.at));
+                        vr.next(a.nv);
+                    }
+                    if (pw) ++done1;
+                    else ++done0;
                 }
-                if (i < items) {
-                    pw = w;
-                    pb = b;
-                    ++cnt[w];
-                }
+                pw = w;
+                pb = b;
             }
         }
     }
@@ -613,126 +725,166 @@ struct Tree {
     // -----------------------------------------------------------------------
     struct Row {
         int t;                // node; -1: no slot
-        int x, low;           // position, first context row it sees
+        int h;                // head
+        int x;                // position
         float c;              // a score's factor (1 / q's scale, scale log2 e or scale / softcap)
-        float slope;
-        const uint32_t *mask;
-        int64_t at;           // of the output, in rows of HD
     };
+    __device__ __forceinline__ int64_t place_of(const TreeSeg &g, const Row &r) const   // of q and the output, in rows of HD
+    {
+        return (int64_t)(g.tok0 + r.t) * a.n_head + r.h;
+    }
 
     __device__ __forceinline__ int depth_of(const TreeSeg &g, int t) const
     {
         return a.depths ? min(max(ld_dep(a.depths + g.tok0 + t), 0), a.max_nodes - 1) : t;
     }
 
-    // Q of the warp's 32 slots: parts, K-major, swizzled. Every lane keeps its slot's factor.
-    __device__ __forceinline__ float stage_q(const TreeSeg &g, int w, int quad, int lane)
+    // Q of the warpgroup's slots: parts, K-major, swizzled; returns what undoes the power of two of the thread's row.
+    // The rows are copied as they are, 16 bytes a lane, to where their parts will stand -- a row of
+    // float is as long as its two 16-bit parts, one of 16 bits as one of those or as two 8-bit ones -- and a thread then
+    // turns its own row into its parts, in place. Where the two warpgroups share a tile of Q, each copies every other
+    // 32 units and turns every other unit of a row.
+    __device__ __forceinline__ uint32_t q_place(int qt, int row, int part, int u) const
     {
-        const int qt = g.pair ? w : 0, first = g.m * a.unit_slots + qt * 128 + quad * 32;
-        const int count = min(max(g.slots - qt * 128 - quad * 32, 0), 32);
-        const uint32_t to = sm + (uint32_t)qt * PARTS * C::QPART + quad * 32 * 128;
-        const bool both = NS == 1 || g.pair;                   // else a warpgroup writes every other row
-        constexpr int E = HD / 32;                             // elements of a lane: 2, 4, 8
-        constexpr int B = E == 8 ? 4 : 8;                      // rows on their way at a time
-        float inv = 1.f;
-#pragma unroll 1
-        for (int i0 = 0; i0 < count; i0 += B) {
-            float f[B][E];
-#pragma unroll
-            for (int y = 0; y < B; ++y) {
-                const int i = min(i0 + y, count - 1), slot = first + i, t = div(a.by_group, slot);
-                const int64_t row = ((int64_t)(g.tok0 + t) * a.n_head + g.hk * a.group + slot - t * a.group) * HD + lane * E;
-                load_q<E>(row, f[y]);
+        const uint32_t to = sm + (uint32_t)(qt * a.q_parts + part) * C::QPART;
+        if (C::F8 && HD == 64) return to + row * 64 + (((u ^ (row >> 1)) & 3) << 4);
+        return to + (u >> 3) * 16384 + row * 128 + (((u ^ row) & 7) << 4);
+    }
+    __device__ __forceinline__ float stage_q(const TreeSeg &g, const Row &r, int w, int quad, int lane)
+    {
+        const int qt = g.pair ? w : 0, my = quad * 32 + lane;
+        const bool half = NS == 2 && !g.pair;
+        const bool f32 = a.q_type == kTypeF32, f16 = std::is_same<MT, __half>::value;
+        const int lg = (HD == 64 ? 3 : HD == 128 ? 4 : 5) + f32;      // log2 of a row's 16-byte units
+        const int row_bytes = 16 << lg, su = half ? 2 : 1;
+#pragma unroll 4
+        for (int it = half ? w : 0; it < 1 << lg; it += su) {
+            const int i = it * 32 + lane, row = i >> lg, u = i & ((1 << lg) - 1);
+            const int t = __shfl_sync(0xffffffffu, r.t, row), h = __shfl_sync(0xffffffffu, r.h, row);
+            const uint32_t to = f32 || C::F8 ? q_place(qt, quad * 32 + row, u & 1, u >> 1) : q_place(qt, quad * 32 + row, 0, u);
+            if (t >= 0)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                             :: "r"(to), "l"(static_cast<const uint8_t *>(a.q) + ((int64_t)(g.tok0 + t) * a.n_head + h) * row_bytes + u * 16)
+                             : "memory");
+        }
+        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+        if (half) group_sync();
+        else __syncwarp();
+        if (!C::F8 && PARTS == 1 && a.q_type == (f16 ? kTypeF16 : kTypeBf16)) return 1.f;   // as it is
+
+        auto sixteen = [&](int part, int u, float (&f)[8]) {          // a unit of 16-bit elements
+            const uint4 x = lds128(q_place(qt, my, part, u));
+            if (a.q_type == kTypeF16) unpack8<__half>(x, f);
+            else unpack8<__nv_bfloat16>(x, f);
+        };
+        auto eight = [&](int u, float (&f)[8]) {                      // elements 8 u ..
+            if (!f32) {
+                if (C::F8) sixteen(u & 1, u >> 1, f);
+                else sixteen(0, u, f);
+                return;
             }
+            const uint4 x = lds128(q_place(qt, my, 0, u)), y = lds128(q_place(qt, my, 1, u));
+            f[0] = __uint_as_float(x.x); f[1] = __uint_as_float(x.y); f[2] = __uint_as_float(x.z); f[3] = __uint_as_float(x.w);
+            f[4] = __uint_as_float(y.x); f[5] = __uint_as_float(y.y); f[6] = __uint_as_float(y.z); f[7] = __uint_as_float(y.w);
+        };
+        float sc = 1.f, inv = 1.f;
+        if (f16) {
+            float m = 0.f;
+#pragma unroll 2
+            for (int u = 0; u < HD / 8; ++u) {
+                float f[8];
+                eight(u, f);
 #pragma unroll
-            for (int y = 0; y < B; ++y) {
-                const int i = i0 + y;
-                if (i >= count) break;
-                float m = 0.f;
+                for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
+            }
+            pow2_scale(m, sc, inv);
+            if (C::F8) {                                              // 2^7 .. 2^8: e4m3 ends at 448
+                sc *= 0.0078125f;
+                inv *= 128.f;
+            }
+        }
+        if (half) group_sync();                                       // the other warpgroup has read the row too
+        if constexpr (C::F8) {
+#pragma unroll 1
+            for (int u = half ? w : 0; u < HD / 16; u += su) {
+                float f[2][8];
+                sixteen(0, u, f[0]);
+                sixteen(1, u, f[1]);
 #pragma unroll
-                for (int e = 0; e < E; ++e) m = fmaxf(m, fabsf(f[y][e]));
-                m = warp_max(m);
-                float sc, iv;
-                if (std::is_same<MT, __half>::value) {
-                    pow2_scale(m, sc, iv);
-                } else {
-                    sc = iv = 1.f;
+                for (int e = 0; e < 16; ++e) f[e >> 3][e & 7] *= sc;
+#pragma unroll 1
+                for (int x = 0; x < a.q_parts; ++x) {
+                    uint4 y;
+                    uint32_t *yw = &y.x;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float *v = &f[e >> 1][(e & 1) * 4];
+                        yw[e] = e4m3x4_of(v[0], v[1], v[2], v[3]);
+                        uint32_t lo, hi;
+                        e4m3x4_to_half4(yw[e], lo, hi);
+                        const float2 b0 = kv2_to_float2<__half>(lo), b1 = kv2_to_float2<__half>(hi);
+                        v[0] -= b0.x; v[1] -= b0.y; v[2] -= b1.x; v[3] -= b1.y;
+                    }
+                    sts128(q_place(qt, my, x, u), y);
                 }
-                if (lane == i) inv = iv;
-                if (!both && (i & 1) != w) continue;
-#pragma unroll
-                for (int e = 0; e < E; ++e) f[y][e] *= sc;
-                const int d = lane * E, u = d >> 3;            // 16-byte unit of the row
-                const uint32_t at = to + (u >> 3) * 16384 + i * 128 + (((u & 7) ^ (i & 7)) << 4) + (d & 7) * 2;
+            }
+        } else {
+#pragma unroll 1
+            for (int u = half ? w : 0; u < HD / 8; u += su) {
+                float f[8];
+                eight(u, f);
 #pragma unroll
                 for (int x = 0; x < PARTS; ++x) {
-                    uint32_t h[E / 2];
+                    uint32_t h[4];
 #pragma unroll
-                    for (int e = 0; e < E / 2; ++e) {
-                        h[e] = float2_to_kv2<MT>(f[y][2 * e], f[y][2 * e + 1]);
+                    for (int e = 0; e < 4; ++e) {
+                        float &f0 = f[2 * e], &f1 = f[2 * e + 1];
+                        if (x == 0) {
+                            f0 *= sc;
+                            f1 *= sc;
+                        }
+                        h[e] = float2_to_kv2<MT>(f0, f1);
                         if (x + 1 < PARTS) {
                             const float2 b = kv2_to_float2<MT>(h[e]);
-                            f[y][2 * e] -= b.x;
-                            f[y][2 * e + 1] -= b.y;
+                            f0 -= b.x;
+                            f1 -= b.y;
                         }
                     }
-                    if constexpr (E == 2) asm volatile("st.shared.u32 [%0], %1;" :: "r"(at + x * C::QPART), "r"(h[0]) : "memory");
-                    else if constexpr (E == 4) asm volatile("st.shared.v2.u32 [%0], {%1, %2};" :: "r"(at + x * C::QPART), "r"(h[0]), "r"(h[1]) : "memory");
-                    else sts128(at + x * C::QPART, make_uint4(h[0], h[1], h[2], h[3]));
+                    sts128(q_place(qt, my, x, u), make_uint4(h[0], h[1], h[2], h[3]));
                 }
             }
         }
         return inv;
     }
 
-    template <int E>
-    __device__ __forceinline__ void load_q(int64_t i, float (&f)[E]) const
+    // tanh: near 0 its series (to x^9, remainder below 1e-8 of it at 1/4), elsewhere 1 - 2 / (1 + e^2x), to 2^-22
+    static __device__ __forceinline__ float tanh_of(float x)
     {
-        if (a.q_type == kTypeF32) {
-            const float *p = static_cast<const float *>(a.q) + i;
-            if constexpr (E == 2) {
-                const float2 v = ld_dep(reinterpret_cast<const float2 *>(p));
-                f[0] = v.x; f[1] = v.y;
-            } else {
-#pragma unroll
-                for (int e = 0; e < E; e += 4) {
-                    const float4 v = ld_dep(reinterpret_cast<const float4 *>(p + e));
-                    f[e] = v.x; f[e + 1] = v.y; f[e + 2] = v.z; f[e + 3] = v.w;
-                }
-            }
-        } else {
-            const uint16_t *p = static_cast<const uint16_t *>(a.q) + i;
-            uint32_t r[E / 2];
-            if constexpr (E == 2) {
-                r[0] = (uint32_t)ld_dep(reinterpret_cast<const int *>(p));
-            } else if constexpr (E == 4) {
-                asm volatile("ld.global.cg.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "l"(p) : "memory");
-            } else {
-                const uint4 v = ld_dep(reinterpret_cast<const uint4 *>(p));
-                r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
-            }
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e) {
-                const float2 v = a.q_type == kTypeF16 ? kv2_to_float2<__half>(r[e]) : kv2_to_float2<__nv_bfloat16>(r[e]);
-                f[2 * e] = v.x;
-                f[2 * e + 1] = v.y;
-            }
-        }
+        const float z = x * x;
+        float s = 2.1869489e-2f;                               // 62 / 2835
+        s = fmaf(s, z, -5.3968254e-2f);                        // 17 / 315
+        s = fmaf(s, z, 1.3333333e-1f);                         // 2 / 15
+        s = fmaf(s, z, -3.3333333e-1f);
+        s = fmaf(s * z, x, x);
+        const float e = ex2(2.f * kLog2e * x);                 // infinity: 1
+        const float l = 1.f - __fdividef(2.f, 1.f + e);
+        return fabsf(x) < 0.25f ? s : e < 1e30f ? l : x == x ? 1.f : x;
     }
 
     // Scores of 32 columns from tile row c0 on, with the rules, -inf where the slot does not see the row.
     __device__ __forceinline__ void ruled(const TreeSeg &g, const Row &r, const volatile TileInfo *d, int c0, uint32_t (&v)[32])
     {
         const int j0 = d->row0 + c0, y0 = j0 - g.base;
-        unsigned bits = bit_range(r.low - j0, g.base - j0);
+        unsigned bits = bit_range(low_of(r.x, g.start) - j0, g.base - j0);
         if (r.t >= 0 && y0 > -32 && y0 < g.n) {
             unsigned dr;
-            if (!r.mask) {
+            if (!a.mask) {
                 dr = bit_range(-y0, r.t + 1 - y0);
             } else {
                 const int w = y0 >> 5;                         // -1: before the first
-                const uint32_t lo = w >= 0 ? ld_mask(r.mask, w) : 0u;
-                const uint32_t hi = w + 1 < a.words ? ld_mask(r.mask, w + 1) : 0u;
+                const uint32_t *mask = a.mask + (int64_t)(g.tok0 + r.t) * a.words;
+                const uint32_t lo = w >= 0 ? ld_mask(mask, w) : 0u;
+                const uint32_t hi = w + 1 < a.words ? ld_mask(mask, w + 1) : 0u;
                 dr = __funnelshift_r(lo, hi, y0 & 31);
             }
             dr &= bit_range(max(-y0, g.start - j0), g.n - y0) & bit_range(-j0, 32);
@@ -746,14 +898,17 @@ struct Tree {
         if (r.t < 0) bits = 0u;
         const unsigned there = d->slices >> (c0 >> 4) & 3u;
         bits &= (there & 1u ? 0xffffu : 0u) | (there & 2u ? 0xffff0000u : 0u);
+        const float f0 = C::E8 ? r.c * d->ks[c0 >> 4] : r.c, f1 = C::E8 ? r.c * d->ks[(c0 >> 4) + 1] : r.c;
+        const bool cap = a.softcap > 0.f, slopes = a.slopes != nullptr;
+        const float slope = slopes ? ld_dep(a.slopes + r.h) * kLog2e : 0.f;
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
-            float s = __uint_as_float(v[c]) * (C::E8 ? r.c * d->ks[(c0 >> 4) + (c >> 4)] : r.c);
-            if (a.softcap > 0.f) s = a.cap_log2 * tanhf(s);
-            if (a.slopes) {
+            float s = __uint_as_float(v[c]) * (c < 16 ? f0 : f1);
+            if (cap) s = a.cap_log2 * tanh_of(s);
+            if (slopes) {
                 const int y = y0 + c;
                 const int x = y < 0 || y >= g.n ? j0 + c : g.base + depth_of(g, y);
-                s = fmaf(-r.slope, (float)(r.x - x), s);
+                s = fmaf(-slope, (float)(r.x - x), s);
             }
             v[c] = __float_as_uint(bits >> c & 1 ? s : -INFINITY);
         }
@@ -781,13 +936,13 @@ struct Tree {
     }
 
     // Rows of V that hold infinities or NaN: to the slots that see them, in the dimensions that do.
-    __device__ __noinline__ void add_bad(const TreeSeg &g, const volatile TileInfo *d, uint32_t s_at, uint32_t o, float ref)
+    __device__ __forceinline__ void add_bad(const TreeSeg &g, const volatile TileInfo *d, uint32_t s_at, uint32_t o, float ref)
     {
         for (int w = 0; w < (TR + 31) / 32; ++w)
             for (unsigned m = d->bad[w]; m; m &= m - 1) {
                 const int r = w * 32 + __ffs(m) - 1, j = d->row0 + r, pg = div(a.by_page, j);
                 const int page = ld_dep(a.table + (size_t)g.s * a.max_pages + pg);
-                const int64_t at = page * a.page_stride + (j - pg * a.page_size) * a.row_stride + g.hk * a.head_stride;
+                const int64_t at = page * a.page_stride + (j - pg * a.page_size) * a.row_stride + hk() * a.head_stride;
                 uint32_t sv, dummy;
                 tmem_ld2(s_at + (r & ~1), sv, dummy);
                 if (r & 1) sv = dummy;
@@ -822,26 +977,19 @@ struct Tree {
         const uint32_t o_at = tm + C::TM_O + w * HD + lanes;
         bool dead = false;
         unsigned cnt = 0, tiles = 0;                           // items of this stream; tiles before the segment
-        const bool rules = a.softcap > 0.f || a.slopes != nullptr;
+        const bool rules = a.softcap > 0.f || a.slopes != nullptr || a.qscale <= 0.f;
         for (int p = from; p < end;) {
             TreeSeg g;
             const int next = segment(p, end, g);
             const bool begins = g.t0 == 0, whole = begins && g.t1 == g.T;
             const int qt = g.pair ? w : 0;
-            const int in_unit = qt * 128 + quad * 32 + lane, slot = g.m * a.unit_slots + in_unit;
+            const int in_unit = qt * 128 + quad * 32 + lane, slot = first_slot() + in_unit;
             Row r;
             r.t = in_unit < g.slots ? div(a.by_group, slot) : -1;
             const bool any = qt * 128 + quad * 32 < g.slots;   // some slot in this warp
-            {
-                const float inv = any ? stage_q(g, w, quad, lane) : 1.f;
-                const int t = max(r.t, 0), h = g.hk * a.group + (r.t >= 0 ? slot - t * a.group : 0);
-                r.x = g.base + depth_of(g, t);
-                r.low = max(low_of(r.x, g.start), 0);
-                r.c = inv * a.qscale;
-                r.slope = a.slopes ? ld_dep(a.slopes + h) * kLog2e : 0.f;
-                r.mask = a.mask ? a.mask + (int64_t)(g.tok0 + t) * a.words : nullptr;
-                r.at = (int64_t)(g.tok0 + t) * a.n_head + h;
-            }
+            r.h = hk() * a.group + (r.t >= 0 ? slot - r.t * a.group : 0);
+            r.x = g.base + depth_of(g, max(r.t, 0));
+            r.c = stage_q(g, r, w, quad, lane) * a.qscale;
             fence_proxy_async_smem();                          // Q is read by the tensor cores
             if (any) {
                 uint32_t z[32];
@@ -853,8 +1001,9 @@ struct Tree {
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(q_ready);
+            if (lane == 0) bar_arrive(q_ready());
 
+            const float rc = rcp(r.c);
             float m = -INFINITY, l = 0.f;
             const int step = NS == 2 && !g.pair ? 2 : 1;
             for (int t = g.pair || NS == 1 ? 0 : w; t < g.t1 - g.t0; t += step) {
@@ -862,45 +1011,45 @@ struct Tree {
                 const unsigned par = NS == 2 ? cnt & 1 : cnt >> 1 & 1;
                 const uint32_t s_at = tm + C::TM_S + b * TR + lanes;
                 const volatile TileInfo *d = tile_info(tiles + t);
-                if (!dead) dead = !wait_warp(s_full + b, par);
+                if (!dead) dead = !wait_warp(s_full(b), par);
                 if (any && !dead) {
                     tc_fence_after();
-                    const bool edge = d->edge || rules;
+                    const bool slow = d->edge || rules;
                     float mx = -INFINITY;
+                    if (slow) {
 #pragma unroll 1
-                    for (int c = 0; c < TR; c += 32) {
-                        uint32_t v[32];
-                        tmem_ld32(s_at + c, v);
-                        tmem_wait_ld();
-                        if (edge) {
+                        for (int c = 0; c < TR; c += 32) {
+                            uint32_t v[32];
+                            tmem_ld32(s_at + c, v);
+                            tmem_wait_ld();
                             ruled(g, r, d, c, v);
                             tmem_st32(s_at + c, v);
+                            mx = fmaxf(mx, fmaxf(most16(v, 0) + shift_of(d, c >> 4), most16(v, 16) + shift_of(d, (c >> 4) + 1)));
                         }
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
+                        tmem_wait_st();
+                    } else {
+#pragma unroll 1
+                        for (int c = 0; c < TR; c += 64) {
+                            uint32_t v[2][32];
+                            tmem_ld32(s_at + c, v[0]);
+                            tmem_ld32(s_at + c + 32, v[1]);
+                            tmem_wait_ld();
                             float k = -INFINITY;
-                            if (edge || !C::E8) {
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) k = fmaxf(k, __uint_as_float(v[16 * h + i]));
-                                if (!edge) k = r.c >= 0.f ? k * r.c : lowest(v, h) * r.c;
-                            } else {
-                                const float f = r.c * d->ks[(c >> 4) + h];
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) k = fmaxf(k, __uint_as_float(v[16 * h + i]) * f);
-                            }
-                            if (C::E8) {
-                                const int e = (int)((__float_as_uint(d->vs[(c >> 4) + h]) >> 23) & 0xFFu) - 126;
-                                k += (float)min(max(e, -60), 61);
+                            for (int y = 0; y < 4; ++y) {
+                                float x = most16(v[y >> 1], (y & 1) * 16);
+                                if (C::E8) x = fmaf(x, d->ks[(c >> 4) + y], shift_of(d, (c >> 4) + y) * rc);
+                                k = fmaxf(k, x);
                             }
                             mx = fmaxf(mx, k);
                         }
+                        mx *= r.c;
                     }
-                    if (edge) tmem_wait_st();
                     const bool need = mx > m + TAU;
-                    const bool bad = d->edge && (d->bad[0] | d->bad[1] | d->bad[2] | d->bad[3]) != 0u;
+                    const bool bad = (d->edge & 1) && (d->bad[0] | d->bad[1] | d->bad[2] | d->bad[3]) != 0u;
                     if (__any_sync(0xffffffffu, need) || bad) {
                         // one S buffer a stream: S is complete, so is what was issued before it; two: O's last product is not
-                        if (NS == 1 && cnt > 0 && !wait_warp(o_done + (b ^ 1), (cnt - 1) >> 1 & 1)) dead = true;
+                        if (NS == 1 && cnt > 0 && !wait_warp(o_done((b ^ 1)), (cnt - 1) >> 1 & 1)) dead = true;
                         tc_fence_after();
                         if (!dead && __any_sync(0xffffffffu, need)) {
                             const float f = need ? ex2(m - mx) : 1.f;      // 0 while m is -inf
@@ -911,39 +1060,47 @@ struct Tree {
                         if (!dead && bad) add_bad(g, d, s_at, o_at, m == -INFINITY ? 0.f : m - OFF);
                     }
                     const float ref = m == -INFINITY ? 0.f : m - OFF;
+                    const uint64_t nref = pack2(-ref, -ref);
+                    uint64_t sum = pack2(0.f, 0.f);
 #pragma unroll 1
-                    for (int c = 0; c < TR; c += 32) {
-                        uint32_t v[32];
-                        tmem_ld32(s_at + c, v);
+                    for (int c = 0; c < TR; c += 64) {
+                        uint32_t v[2][32];
+                        tmem_ld32(s_at + c, v[0]);
+                        tmem_ld32(s_at + c + 32, v[1]);
                         tmem_wait_ld();
-                        float sum = 0.f;
-                        uint32_t h[PARTS][16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float f = edge ? 1.f : C::E8 ? r.c * d->ks[(c >> 4) + (i >> 3)] : r.c;
-                            float p0 = ex2(fmaf(__uint_as_float(v[2 * i]), f, -ref));
-                            float p1 = ex2(fmaf(__uint_as_float(v[2 * i + 1]), f, -ref));
-                            sum += p0 + p1;
-                            if (C::E8) {
-                                const float vs = d->vs[(c >> 4) + (i >> 3)];
-                                p0 *= vs;
-                                p1 *= vs;
+                        for (int y = 0; y < 2; ++y) {
+                            uint32_t h[PARTS][16];
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const int at = (c >> 4) + 2 * y + x;
+                                const float f = slow ? 1.f : C::E8 ? r.c * d->ks[at] : r.c, vs = C::E8 ? d->vs[at] : 1.f;
+                                const uint64_t f2 = pack2(f, f), vs2 = pack2(vs, vs);
+#pragma unroll
+                                for (int i = 8 * x; i < 8 * x + 8; ++i) {
+                                    const float2 s = unpack2(fma2(pack2(__uint_as_float(v[y][2 * i]), __uint_as_float(v[y][2 * i + 1])), f2, nref));
+                                    uint64_t p = pack2(ex2(s.x), ex2(s.y));
+                                    sum = add2(sum, p);
+                                    if (C::E8) p = mul2(p, vs2);
+                                    const float2 q = unpack2(p);
+                                    h[0][i] = float2_to_kv2<MT>(q.x, q.y);
+                                    if (PARTS == 2) {
+                                        const float2 b = kv2_to_float2<MT>(h[0][i]);
+                                        h[PARTS - 1][i] = float2_to_kv2<MT>(q.x - b.x, q.y - b.y);
+                                    }
+                                }
                             }
-                            h[0][i] = float2_to_kv2<MT>(p0, p1);
-                            if (PARTS == 2) {
-                                const float2 q = kv2_to_float2<MT>(h[0][i]);
-                                h[PARTS - 1][i] = float2_to_kv2<MT>(p0 - q.x, p1 - q.y);
-                            }
+#pragma unroll
+                            for (int x = 0; x < PARTS; ++x) tmem_st16(s_at + c + 32 * y + 16 * x, h[x]);
                         }
-                        l += sum;
-#pragma unroll
-                        for (int x = 0; x < PARTS; ++x) tmem_st16(s_at + c + 16 * x, h[x]);
                     }
+                    const float2 both = unpack2(sum);
+                    l += both.x + both.y;
                     tmem_wait_st();
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_ready + b);
+                if (lane == 0) bar_arrive(p_ready(b));
                 ++cnt;
             }
             // a slot whose every score is NaN keeps its NaN sum
@@ -953,12 +1110,19 @@ struct Tree {
             p = next;
         }
     }
-    static __device__ __forceinline__ float lowest(const uint32_t (&v)[32], int h)
+    static __device__ __forceinline__ float most16(const uint32_t (&v)[32], int at)
     {
-        float k = INFINITY;
+        float k = __uint_as_float(v[at]);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) k = fminf(k, __uint_as_float(v[16 * h + i]));
-        return k;
+        for (int i = 1; i < 15; i += 2) k = fmaxf(fmaxf(k, __uint_as_float(v[at + i])), __uint_as_float(v[at + i + 1]));
+        return fmaxf(k, __uint_as_float(v[at + 15]));
+    }
+    // log2 of a slice's V scale, rounded up: its exponent field
+    static __device__ __forceinline__ float shift_of(const volatile TileInfo *d, int slice)
+    {
+        if constexpr (!C::E8) return 0.f;
+        const int e = (int)((__float_as_uint(d->vs[slice]) >> 23) & 0xFFu) - 126;
+        return (float)min(max(e, -60), 61);
     }
 
     static __device__ __forceinline__ void group_sync() { asm volatile("bar.sync 1, %0;" :: "r"(C::SM_WARPS * 32) : "memory"); }
@@ -971,23 +1135,24 @@ struct Tree {
         const bool mine = g.pair || NS == 1 || g.t1 - g.t0 > w;    // this stream had an item
         if (mine && !dead) {
             const unsigned last = cnt - 1;
-            dead = !wait_warp(o_done + (NS == 2 ? w : (int)(last & 1)), NS == 2 ? last & 1 : last >> 1 & 1);
+            dead = !wait_warp(o_done((NS == 2 ? w : (int)(last & 1))), NS == 2 ? last & 1 : last >> 1 & 1);
         }
         tc_fence_after();
-        const size_t part = (size_t)(rank * 2 + (begins ? 1 : 0)) * a.unit_slots + (g.pair ? w : 0) * 128 + quad * 32 + lane;
+        const size_t block = ((size_t)(rank * 2 + (begins ? 1 : 0)) * gridDim.x + blockIdx.x) * a.unit_slots;
+        const int in_unit = (g.pair ? w : 0) * 128 + quad * 32 + lane;
         auto put = [&](int d, const float (&y)[32], float inv) {   // 32 dimensions from d on
             if (r.t < 0) return;
             if (!whole) {
-                float4 *o = reinterpret_cast<float4 *>(a.ws_o + part * HD + d);
+                float4 *o = reinterpret_cast<float4 *>(a.ws_o + block * HD) + (size_t)(d / 4) * a.unit_slots + in_unit;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                for (int i = 0; i < 8; ++i) o[i * a.unit_slots] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
             } else if (a.q_type == kTypeF32) {
-                float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + r.at * HD + d);
+                float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + place_of(g, r) * HD + d);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     o[i] = make_float4(y[4 * i] * inv, y[4 * i + 1] * inv, y[4 * i + 2] * inv, y[4 * i + 3] * inv);
             } else {
-                uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + r.at * HD + d);
+                uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + place_of(g, r) * HD + d);
                 const bool h = a.q_type == kTypeF16;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -1017,8 +1182,8 @@ struct Tree {
                 const float m1 = __uint_as_float(om), l1 = __uint_as_float(ol), M = fmaxf(m, m1);
                 const float f = m == -INFINITY ? 0.f : ex2(m - M), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
                 const float L = (m == -INFINITY ? 0.f : l * f) + (m1 == -INFINITY ? 0.f : l1 * f1);
-                const float inv = L == 0.f ? 0.f : 1.f / L;
-                if (!whole && w == 0 && r.t >= 0) a.ws_ml[part] = make_float2(M, L);
+                const float inv = L == 0.f ? 0.f : rcp(L);
+                if (!whole && w == 0 && r.t >= 0) a.ws_ml[block + in_unit] = make_float2(M, L);
 #pragma unroll 1
                 for (int d = w * (HD / 2); d < (w + 1) * (HD / 2); d += 32) {
                     uint32_t u[32], v[32];
@@ -1036,8 +1201,8 @@ struct Tree {
                 }
             }
         } else if (any && !dead) {
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            if (!whole && r.t >= 0) a.ws_ml[part] = make_float2(m, l);
+            const float inv = l == 0.f ? 0.f : rcp(l);
+            if (!whole && r.t >= 0) a.ws_ml[block + in_unit] = make_float2(m, l);
 #pragma unroll 1
             for (int d = 0; d < HD; d += 32) {
                 uint32_t u[32];
@@ -1062,22 +1227,18 @@ attn_tree_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constant
 {
     extern __shared__ __align__(1024) uint8_t smem[];      // the swizzle needs the alignment (launch: no static shared memory)
     Tree<C> x(a, smem);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = blockIdx.x;
-    if (warp == C::PROD) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = blockIdx.y;
+    if (warp == C::PROD_K) {
         if (lane == 0) {
-            for (int i = 0; i < 8; ++i) {
-                mbar_init(x.full + i, 1);
-                mbar_init(x.ready + i, 4);
-                mbar_init(x.empty + i, 1);
-                mbar_init(x.raw_free + i, 4);
-            }
+            for (int i = 0; i < 32; ++i) bar_init(x.bar(i), i & 4 ? 4 : 1);   // ready and raw: a lane of each converting warp
             for (int i = 0; i < 2; ++i) {
-                mbar_init(x.s_full + i, 1);
-                mbar_init(x.p_ready + i, 4);
-                mbar_init(x.o_done + i, 1);
+                bar_init(x.s_full(i), 1);
+                bar_init(x.p_ready(i), 4);
+                bar_init(x.o_done(i), 1);
             }
-            mbar_init(x.q_ready, C::SM_WARPS);
-            x.flags[1] = 0;
+            bar_init(x.q_ready(), C::SM_WARPS);
+            for (int i = 0; i < kTreeDesc; ++i) bar_init(x.described(i), 1);
+            x.flags()[1] = 0;
             fence_barrier_init();
             prefetch_tensormap(&kmap);
             prefetch_tensormap(&vmap);
@@ -1085,39 +1246,44 @@ attn_tree_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         __syncwarp();
         pdl_wait();
         x.count(lane);
-        if (rank == 0 && a.ranks > 1) {
+        if (rank == 0 && x.hk() == 0 && a.ranks > 1) {
             __syncwarp();
-            for (int s = lane; s < a.n_seq; s += 32) {
-                const int n = x.tok[s + 1] - x.tok[s], units = (n * a.group + a.unit_slots - 1) / a.unit_slots;
-                const int places = x.before[s + 1] - x.before[s];
-                a.ws_span[s] = make_int4(x.before[s], places ? places / (units * a.n_kv_head) : 0, x.tok[s], x.flags[2]);
-            }
+            for (int s = lane; s < a.n_seq; s += 32)
+                a.ws_span[blockIdx.x / a.n_kv_head * a.n_seq + s] =
+                    make_int4(x.before()[s], x.before()[s + 1] - x.before()[s], x.tok()[s], x.flags()[2]);
         }
     } else {
-        if (warp == C::MMA) tmem_alloc(reinterpret_cast<uint32_t *>(const_cast<int *>(x.flags)), C::TM_COLS);
+        if (warp == C::MMA) tmem_alloc(reinterpret_cast<uint32_t *>(const_cast<int *>(x.flags())), C::TM_COLS);
         pdl_wait();
     }
     pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tm = (uint32_t)x.flags[0];
-    const int share = x.flags[2], total = x.flags[3];
+    const uint32_t tm = (uint32_t)x.flags()[0];
+    const int share = x.flags()[2], total = x.flags()[3];
     const int64_t first = (int64_t)rank * share;
     const int from = (int)min(first, (int64_t)total), end = (int)min(first + share, (int64_t)total);
+    if constexpr (C::NS == 2) {
+        if (warp < C::SM_WARPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        else if (warp < C::FIX + 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    }
     if (warp < C::SM_WARPS) {
         x.softmax(tm, from, end, warp >> 2, warp & 3, lane, rank);
-    } else if (warp < C::PROD) {
+    } else if (warp < C::FIX + 4) {
         x.fix(from, end, tid - C::FIX * 32);
-    } else if (warp == C::PROD) {
-        x.produce(&kmap, &vmap, from, end, lane);
-    } else if (lane == 0) {
+    } else if (warp == C::PROD_K) {
+        x.template produce<false>(&kmap, from, end, lane);
+    } else if (warp == C::PROD_V) {
+        x.template produce<true>(&vmap, from, end, lane);
+    } else if (warp == C::MMA && lane == 0) {
         x.issue(tm, from, end);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (x.flags[1]) {                                      // after a timeout: copies and products under way end first
+    if (x.flags()[1]) {                                      // after a timeout: copies and products under way end first
         if (tid == 0) {
             const unsigned long long t0 = globaltimer_ns();
             while (globaltimer_ns() - t0 < 200000000ull) __nanosleep(1000);
@@ -1128,18 +1294,22 @@ attn_tree_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     if (warp == C::MMA) tmem_dealloc(tm, C::TM_COLS);
 }
 
-// Units that several blocks have tiles of: o = sum w oc / sum w S over their parts, w = 2^(mx - max mx). A warp for
-// a (node, head).
+// Units that several blocks have tiles of: o = sum w oc / sum w S over their parts, w = 2^(mx - max mx). A warp takes a
+// node, eight heads of a KV head and 16 dimensions: a part's slots lie next to each other for every four
+// dimensions, as the threads of the streaming kernel store them, so the lanes read whole sectors.
 template <int HD>
 __global__ void __launch_bounds__(128) attn_tree_combine(const TreeArgs a)
 {
-    constexpr int E = HD / 32;
     pdl_wait();
     const int lane = threadIdx.x & 31;
+    const int gq = (a.group + 7) / 8, per_tok = a.n_kv_head * gq * (HD / 16);
     const int64_t job = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int64_t tk = job / a.n_head;
-    const int h = (int)(job - tk * a.n_head), hk = h / a.group;
+    const int64_t tk = job / per_tok;
     if (tk >= a.tok_end) return;
+    int rest = (int)(job - tk * per_tok);
+    const int dq = rest % (HD / 16);
+    rest /= HD / 16;
+    const int hk = rest / gq, gh = (rest - hk * gq) * 8 + (lane & 7), d4 = dq * 4 + (lane >> 3);
     // its sequence: the last one that begins at or before it, of those that have places
     int s = -1;
     int4 sp = make_int4(0, 0, 0, 0);
@@ -1160,54 +1330,55 @@ __global__ void __launch_bounds__(128) attn_tree_combine(const TreeArgs a)
     if (s < 0) return;
     int64_t c1 = (int64_t)(a.seq0 + s + 1) * a.n_each;
     if (a.cu) c1 = min(max((int64_t)ld_dep(a.cu + s + 1), (int64_t)0), a.n_tokens);
-    if (tk >= c1) return;
-    const int t = (int)(tk - sp.z), slot = t * a.group + h - hk * a.group, n = (int)(c1 - sp.z);
-    const int units = (n * a.group + a.unit_slots - 1) / a.unit_slots, mu = slot / a.unit_slots;
-    const int p0 = sp.x + (hk * units + mu) * sp.y, r0 = p0 / sp.w, r1 = (p0 + sp.y - 1) / sp.w;
+    if (tk >= c1 || gh >= a.group) return;
+    const int slot = (int)(tk - sp.z) * a.group + gh, mu = slot / a.unit_slots;
+    if (mu > 0) {                                              // the unit's own places
+        const uint4 u = ld_dep(reinterpret_cast<const uint4 *>(a.ws_span + mu * a.n_seq + s));
+        sp = make_int4((int)u.x, (int)u.y, 0, (int)u.w);
+    }
+    const int r0 = sp.x / sp.w, r1 = (sp.x + sp.y - 1) / sp.w;
     if (r0 == r1) return;
+    const int unit = mu * a.n_kv_head + hk;
     const int in_unit = slot - mu * a.unit_slots;
-    float m = -INFINITY, S = 0.f, acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    float m = -INFINITY, S = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int BATCH = 4;
     for (int r = r0; r <= r1; r += BATCH) {
         float2 ml[BATCH];
-        float v[BATCH][E];
+        float4 v[BATCH];
 #pragma unroll
         for (int b = 0; b < BATCH; ++b) {
             const int x = min(r + b, r1);
-            const size_t row = ((size_t)x * 2 + (x == r0 && p0 >= x * sp.w ? 1 : 0)) * a.unit_slots + in_unit;
-            ml[b] = ld_dep(a.ws_ml + row);
-            const float *p = a.ws_o + row * HD + lane * E;
-            if constexpr (E == 2) {
-                const float2 y = ld_dep(reinterpret_cast<const float2 *>(p));
-                v[b][0] = y.x; v[b][1] = y.y;
-            } else {
-#pragma unroll
-                for (int e = 0; e < E; e += 4) {
-                    const float4 y = ld_dep(reinterpret_cast<const float4 *>(p + e));
-                    v[b][e] = y.x; v[b][e + 1] = y.y; v[b][e + 2] = y.z; v[b][e + 3] = y.w;
-                }
-            }
+            const size_t block = ((size_t)(x * 2 + (x == r0 ? 1 : 0)) * a.units + unit) * a.unit_slots;   // it begins in the first one's places
+            ml[b] = ld_dep(a.ws_ml + block + in_unit);
+            v[b] = ld_dep(reinterpret_cast<const float4 *>(a.ws_o + block * HD) + (size_t)d4 * a.unit_slots + in_unit);
         }
 #pragma unroll
         for (int b = 0; b < BATCH; ++b) {
             if (r + b > r1 || ml[b].x == -INFINITY) continue;
             const float M = fmaxf(m, ml[b].x), f = m == -INFINITY ? 0.f : ex2(m - M), w = ex2(ml[b].x - M);
             S = fmaf(S, f, w * ml[b].y);
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], f, w * v[b][e]);
+            acc.x = fmaf(acc.x, f, w * v[b].x);
+            acc.y = fmaf(acc.y, f, w * v[b].y);
+            acc.z = fmaf(acc.z, f, w * v[b].z);
+            acc.w = fmaf(acc.w, f, w * v[b].w);
             m = M;
         }
     }
     const float inv = S == 0.f ? 0.f : 1.f / S;
-    const int64_t at = (tk * a.n_head + h) * HD + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-        const float y0 = acc[e] * inv, y1 = acc[e + 1] * inv;
-        if (a.q_type == kTypeF32) *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + at + e) = make_float2(y0, y1);
-        else if (a.q_type == kTypeF16) *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + at + e) = float2_to_kv2<__half>(y0, y1);
-        else *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + at + e) = float2_to_kv2<__nv_bfloat16>(y0, y1);
+    const int64_t at = (tk * a.n_head + hk * a.group + gh) * HD + d4 * 4;
+    if (a.q_type == kTypeF32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    } else {
+        uint2 u;
+        if (a.q_type == kTypeF16) {
+            u.x = float2_to_kv2<__half>(acc.x * inv, acc.y * inv);
+            u.y = float2_to_kv2<__half>(acc.z * inv, acc.w * inv);
+        } else {
+            u.x = float2_to_kv2<__nv_bfloat16>(acc.x * inv, acc.y * inv);
+            u.y = float2_to_kv2<__nv_bfloat16>(acc.z * inv, acc.w * inv);
+        }
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) = u;
     }
 }
 
@@ -1226,25 +1397,35 @@ cudaError_t launch_tree_kernel(const TreeRequest &r)
     e = encode_paged_map(&vmap, r.v, (int)es, bf, C::HD, a.n_kv_head, a.page_size, a.n_pages, r.head_stride * es,
                          r.row_stride * es, r.page_stride * es, box_x, a.box_rows);
     if (e != cudaSuccess) return e;
-    // the rings share what Q leaves: 16-bit tiles alone, or three of them (two, where that is all) and 8-bit ones
-    const uint32_t left = C::DATA - (uint32_t)(a.unit_slots / 128) * C::PARTS * C::QPART;
-    if (!C::E8) {
-        a.nslot = (int)(left / C::SLOT);
-        a.nraw = 0;
+    // 8-bit parts hold 4 bits each: bfloat16 8, binary16 11
+    a.q_parts = C::F8 ? (a.q_type == kTypeBf16 ? 2 : 3) : C::PARTS;
+    a.q_bytes = (uint32_t)(a.unit_slots / 128) * a.q_parts * C::QPART;
+    // the rings share what Q leaves
+    auto few = [](int x) { return x > 4 ? 4 : x; };
+    const uint32_t left = C::DATA - a.q_bytes;
+    a.nrk = a.nrv = 0;
+    if (C::F8) {
+        a.nv = left >= 2 * C::SLOT + 4 * C::RAW ? 2 : 1;
+        const int raws = (int)((left - a.nv * C::SLOT) / C::RAW);
+        a.nk = few(raws / 2);
+        a.nrv = few(raws - a.nk);
+    } else if (C::E8) {
+        a.nk = a.nv = left >= 8 * C::SLOT ? 2 : 1;
+        a.nrk = a.nrv = few((int)((left - 2 * a.nk * C::SLOT) / (2 * C::RAW)));
+        if (a.nk + a.nrk > 5) a.nrk = 5 - a.nk;
     } else {
-        a.nslot = left >= 3 * C::SLOT + 2 * C::RAW ? 3 : 2;
-        a.nraw = (int)((left - a.nslot * C::SLOT) / C::RAW);
+        const int n = (int)(left / C::SLOT);
+        a.nk = few((n + (n == 3)) / 2);
+        a.nv = few(n - a.nk);
     }
-    if (a.nslot > 8) a.nslot = 8;
-    if (a.nraw > 6) a.nraw = 6;
     const void *fn = reinterpret_cast<const void *>(&attn_tree_stream<C>);
     e = ensure_smem_attr(fn, (int)C::SMEM);
     if (e != cudaSuccess) return e;
     void *args[] = {&kmap, &vmap, &a};
-    e = launch_pdl(fn, dim3((unsigned)a.ranks), dim3(C::THREADS), C::SMEM, r.stream, args);
+    e = launch_pdl(fn, dim3((unsigned)a.units, (unsigned)a.ranks), dim3(C::THREADS), C::SMEM, r.stream, args);
     if (e != cudaSuccess || a.ranks == 1) return e;
     const void *cf = reinterpret_cast<const void *>(&attn_tree_combine<C::HD>);
-    const int64_t blocks = (a.tok_end * a.n_head + 3) / 4;
+    const int64_t blocks = (a.tok_end * a.n_kv_head * ((a.group + 7) / 8) * (C::HD / 16) + 3) / 4;
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     void *cargs[] = {&a};
     return launch_pdl(cf, dim3((unsigned)blocks), dim3(128), 0, r.stream, cargs);

@@ -14,6 +14,8 @@ namespace {
 
 using namespace attn::check;
 
+constexpr int kMaxTreeSplits = 4096;
+
 attn_status check_trees(const int32_t *cu_tokens, int n_seq, int64_t n_tokens, int max_nodes)
 {
     if (n_seq < 0 || n_seq > 65535 || n_tokens < 0 || n_tokens > kMaxRows || max_nodes < 1 || max_nodes > 1024)
@@ -27,19 +29,21 @@ attn_status check_trees(const int32_t *cu_tokens, int n_seq, int64_t n_tokens, i
 attn_status check_call(const attn_paged_cache *c, int q_type, int n_head, int n_splits)
 {
     if (q_type != ATTN_TYPE_F32 && q_type != ATTN_TYPE_F16 && q_type != ATTN_TYPE_BF16) return ATTN_ERR_INVALID_ARG;
-    if (n_head < 1 || n_head > 65535 || n_head % c->n_kv_head != 0 || n_splits < 0 || n_splits > 4096)
+    if (n_head < 1 || n_head > 65535 || n_head % c->n_kv_head != 0 || n_splits < 0 || n_splits > kMaxTreeSplits)
         return ATTN_ERR_INVALID_ARG;
     if (n_head / c->n_kv_head > 64) return ATTN_ERR_UNSUPPORTED;
     return ATTN_OK;
 }
 
 struct TreePlan {
+    int64_t units = 1;
     int n_splits = 1, unit_slots = 128, min_share = 1, tile = 128;
     size_t o_bytes = 0, ml_bytes = 0, workspace = 0;
 };
 
-// A block an SM, each with an equal run of the tiles there are (the device counts them); fewer where the
-// capacity holds fewer. Up to 128 slots the two warpgroups of a block take tiles in turn: two at least.
+// As many blocks for each unit (KV head, 128 or 256 slots) as make a block an SM; where that leaves SMs without one
+// (units just over half of them), enough for four rounds of blocks, whose last is nearly full; no more than
+// there are tiles at full capacity. Up to 128 slots the two warpgroups of a block take tiles in turn: two at least.
 void make_plan(const attn_paged_cache *c, int max_pages, int n_seq, int max_nodes, int n_head, int n_splits, int sm_count,
                TreePlan &pl)
 {
@@ -47,16 +51,21 @@ void make_plan(const attn_paged_cache *c, int max_pages, int n_seq, int max_node
     pl.tile = attn::tree_tile(c->head_dim);
     pl.unit_slots = c->head_dim == 256 || need <= 128 ? 128 : 256;
     pl.min_share = c->head_dim != 256 && need <= 128 ? 2 : 1;
-    const int64_t units = (int64_t)c->n_kv_head * ((need + pl.unit_slots - 1) / pl.unit_slots);
+    const int64_t mus = (need + pl.unit_slots - 1) / pl.unit_slots;
+    pl.units = c->n_kv_head * mus;
     const int64_t seqs = n_seq < attn::kPagedSeqs ? n_seq : attn::kPagedSeqs;
-    const int64_t tiles = ((int64_t)max_pages * c->page_size + pl.tile - 1) / pl.tile + 1;
-    const int64_t most = (tiles * units * seqs + pl.min_share - 1) / pl.min_share;
-    pl.n_splits = n_splits > 0 ? n_splits : (int)(most < sm_count ? most : sm_count);
+    const int64_t tiles = ((int64_t)max_pages * c->page_size + pl.tile - 1) / pl.tile * seqs;
+    const int64_t most = (tiles + pl.min_share - 1) / pl.min_share;
+    int64_t P = sm_count / pl.units;
+    if (P * pl.units * 20 < (int64_t)sm_count * 17) P = 4 * (int64_t)sm_count / pl.units;
+    if (P > most) P = most;
+    if (P > kMaxTreeSplits) P = kMaxTreeSplits;
+    pl.n_splits = n_splits > 0 ? n_splits : P < 1 ? 1 : (int)P;
     if (pl.n_splits > 1) {
-        const size_t parts = (size_t)pl.n_splits * 2 * pl.unit_slots;
+        const size_t parts = (size_t)pl.n_splits * 2 * pl.units * pl.unit_slots;
         pl.o_bytes = align256(parts * c->head_dim * sizeof(float));
         pl.ml_bytes = align256(parts * 2 * sizeof(float));
-        pl.workspace = pl.o_bytes + pl.ml_bytes + align256((size_t)seqs * 16);
+        pl.workspace = pl.o_bytes + pl.ml_bytes + align256((size_t)(seqs * mus) * 16);
     }
 }
 
@@ -152,6 +161,7 @@ attn_status attn_decode_tree(const attn_paged_cache *cache, const int32_t *block
     if (e != cudaSuccess) return fail(e);
     TreePlan pl;
     make_plan(cache, max_pages, n_seq, max_nodes, n_head, n_splits, sm_count, pl);
+    if (pl.units > 0x7fffffff) return ATTN_ERR_UNSUPPORTED;
     if (pl.workspace > 0) {
         if (!workspace) {
             bool ok = false;
@@ -217,10 +227,9 @@ attn_status attn_decode_tree(const attn_paged_cache *cache, const int32_t *block
         {attn::launch_tree_hd128_f16, attn::launch_tree_hd128_bf16, attn::launch_tree_hd128_e4m3},
         {attn::launch_tree_hd256_f16, attn::launch_tree_hd256_bf16, attn::launch_tree_hd256_e4m3}};
     const Launch launch = table[cache->head_dim == 64 ? 0 : cache->head_dim == 128 ? 1 : 2][cache->kv_type - ATTN_TYPE_F16];
-    // places are counted in 32 bits: fewer sequences a launch where the capacity is huge
-    const int64_t units = (int64_t)cache->n_kv_head * (((int64_t)max_nodes * a.group + pl.unit_slots - 1) / pl.unit_slots);
-    const int64_t per_seq = (((int64_t)a.cap + pl.tile - 1) / pl.tile + 1) * units;
-    if (per_seq > 0x3fff0000) return ATTN_ERR_UNSUPPORTED;
+    a.units = (int)pl.units;
+    // tiles are counted in 32 bits: fewer sequences a launch where the capacity is huge
+    const int64_t per_seq = ((int64_t)a.cap + pl.tile - 1) / pl.tile + 1;
     const int batch = (int)(0x3fff0000 / per_seq < attn::kPagedSeqs ? 0x3fff0000 / per_seq : attn::kPagedSeqs);
     for (int s0 = 0; s0 < n_seq; s0 += batch) {
         a.n_seq = n_seq - s0 < batch ? n_seq - s0 : batch;

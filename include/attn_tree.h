@@ -83,9 +83,10 @@ attn_status attn_rope_append_tree(const attn_paged_cache *cache, const int32_t *
  *              base_s + depth, cache row j < base_s at position j, node j at base_s + its
  *              depth. starts masks rows (of nodes too), whatever their position.
  *   n_head     a multiple of n_kv_head, n_head / n_kv_head <= 64
- *   n_splits   blocks that share the call's work: each takes an equal part of the
- *              tiles of 128 rows of all (sequence, KV head, 128 or 256 (node, head)
- *              pairs); 0: attn_tree_plan's count, a block an SM
+ *   n_splits   blocks that share the call's rows, per KV head and 128 or 256 of its
+ *              (node, head) pairs: each takes an equal part of the tiles (128 rows, 64
+ *              at head_dim 256) of all sequences; 0: attn_tree_plan's count, which
+ *              fills the GPU once
  *   workspace  device buffer of the bytes attn_tree_plan reports, 256-byte
  *              aligned; NULL: the library-owned buffer (see attn_decode)
  * Rows that a node does not see never change its result, whatever they hold, and
@@ -96,7 +97,9 @@ attn_status attn_rope_append_tree(const attn_paged_cache *cache, const int32_t *
  * and E4M3 caches; of bfloat16, 16 bits, over BF16 ones); with 16-bit queries one
  * (F16 queries over a BF16 cache: two), so that a weight is rounded to the cache's
  * type (E4M3: binary16) before it meets V, which adds about as much as the
- * rounding of the result does.
+ * rounding of the result does. 16-bit queries over an E4M3 cache enter as two or
+ * three 8-bit parts that hold all their bits, but for what lies below 2^-17 of
+ * their row's largest.
  */
 attn_status attn_decode_tree(const attn_paged_cache *cache, const int32_t *block_table, int max_pages,
                              const int32_t *positions, const int32_t *cu_tokens, int n_seq, int64_t n_tokens,

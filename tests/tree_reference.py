@@ -52,8 +52,9 @@ def attend(q, sees, depths, k_rows, v_rows, scale, kv, src, softcap=0.0, slopes=
     """q: per sequence [n, n_head, hd]; sees, depths: per sequence as from `rules`; k_rows, v_rows: per sequence
     float64 [nkv, n_kv, hd], NaN where a page is not there. Returns per sequence (out, bound).
 
-    The bound. A score is q (in parts, off by at most HALF^parts of itself, 0 for one part of a type that holds it)
-    times exact cache values, summed in 32 bits in steps of 16 products: a step is off by at
+    The bound. A score is q (in parts, off by at most HALF^parts of itself, 0 for one part of a type that holds it;
+    16-bit queries over e4m3 caches in e4m3 parts that hold all their bits, but for what lies below 2^-17 of the row's
+    largest: e4m3's smallest step is 2^-9, the row's largest is brought to 2^7 or more, half a step is lost) times exact cache values, summed in 32 bits in steps of 16 products: a step is off by at
     most 2^-21 of the sum of magnitudes A (17 terms cut at 2^-25 of the largest, the sum at 2^-23), and there are
     parts * hd / 16; then a few 32-bit roundings of the score (2^-21 of it) and of the cap. An error d of every
     score moves each weight by a factor within e^(+-2d). A weight is off by HALF^parts of itself and 2^-21 (the
@@ -91,6 +92,7 @@ def attend(q, sees, depths, k_rows, v_rows, scale, kv, src, softcap=0.0, slopes=
                 kk, vv = k[rows, h // g], v[rows, h // g]
                 sc = kk @ qv * scale
                 mag = (np.abs(kk) @ np.abs(qv)).max() * abs(scale)
+                lost = 2.0 ** -17 * np.abs(qv).max() * np.abs(kk).sum(-1).max() * abs(scale) if kv == "e4m3" and src != "f32" else 0.0
                 if softcap:
                     sc = softcap * np.tanh(sc / softcap)
                 if slopes is not None:
@@ -99,7 +101,7 @@ def attend(q, sees, depths, k_rows, v_rows, scale, kv, src, softcap=0.0, slopes=
                 total = p.sum()
                 o[t, h] = p @ vv / total
                 seen = np.abs(sc[sc > sc.max() - 25]).max()
-                d = mag * (eps_q + pq * hd / 16 * 2.0 ** -21) + 2.0 ** -21 * (seen + softcap)
+                d = lost + mag * (eps_q + max(pq, 3) * hd / 16 * 2.0 ** -21) + 2.0 ** -21 * (seen + softcap)
                 mean = p @ np.abs(vv) / total
                 steps = pp * (-(-nkv // 16) + 8)
                 b[t, h] = (mean * (math.expm1(2 * d) + eps_p + 2.0 ** -21 + steps * 2.0 ** -21) * 1.01 +
