@@ -184,7 +184,7 @@ struct TreeArgs {
     unsigned *err;
     int64_t n_tokens, n_each; // n_each: nodes of a sequence when cu is null
     int64_t tok_end;          // tokens the joining kernel looks at
-    int q_type, n_seq, seq0;  // sequences of the launch (at most kPagedSeqs), the first one's number
+    int q_type, n_seq, seq0;  // sequences of the launch (at most kTreeSeqs), the first one's number
     int max_nodes, words;
     int n_head, n_kv_head, group;
     int max_pages, n_pages, page_size, cap, window;
@@ -209,6 +209,7 @@ struct TreeRequest {
     int parts;                // 16-bit parts of q and of the weights
     cudaStream_t stream;
 };
+constexpr int kTreeSeqs = 64;     // sequences one launch of the attention of trees takes
 constexpr int tree_tile(int head_dim) { return head_dim == 256 ? 64 : 128; }
 cudaError_t launch_tree_hd64_f16(const TreeRequest &r);
 cudaError_t launch_tree_hd64_bf16(const TreeRequest &r);

@@ -11,11 +11,11 @@
 // Tiles. A (node, head) pair of a KV head is a slot; 128 slots are the M rows of both products. S = Q K^T
 // (128 x TR, operands in shared memory) goes to tensor memory, a warpgroup turns it into P in place, one row a
 // thread, so that maxima and sums need no exchange, and O += P V takes P from tensor memory and V as an MN-major
-// operand from the tile TMA brought. With more than 128 slots a block serves 256: two tiles of Q, two
-// warpgroups, each with its S and O, over the same K and V. With up to 128, the two warpgroups take tiles in
-// turn, each with its own (reference, sum, O), joined at the end through tensor memory. Either way the tensor
-// cores work for one while the other is at its exponentials. head_dim 256 leaves tensor memory for one O:
-// one warpgroup, two S.
+// operand from the tile TMA brought. Up to 128 slots, the two warpgroups take tiles in turn: three (four) S in tensor memory,
+// one O, and one reference that a tile's warpgroup hands on to the next one's as soon as it knows the tile's
+// maxima. With more, a block serves 256 (head_dim up to 128): two tiles of Q over the same K and V, a warpgroup, an S and
+// an O for each. Either way the tensor cores work for one warpgroup while the other is at its exponentials. (With
+// an S and an O for each of two warpgroups on alternate tiles, a tile waited 3500 cycles for its S.)
 //
 // Parts. 16-bit queries and weights enter as one operand, f32 queries as two (the rounding, and the rounding of
 // what it left), and then the weights too: f16 over f16 and e4m3 caches (rows of q scaled by a power of two, so that nothing is
@@ -30,7 +30,7 @@
 // asked of memory together (one row of blocks over all units in turn took 1.9 times as long over 32 sequences of up
 // to 32768 rows).
 //
-// Warps: 8 (4) of the softmax; 4 that convert e4m3 tiles to f16, and, in tiles that some slot does not see all
+// Warps: 8 of the softmax; 4 that convert e4m3 tiles to f16, and, in tiles that some slot does not see all
 // of, take infinities and NaN out of V (a weight of 0 would spread them); a producer of K and one of V (pages, TMA); an
 // issuer. What a single warp does for each tile takes some 8 cycles an instruction, and code that runs once is
 // fetched from L2 a line at a time: both are written for few instructions.
@@ -47,7 +47,7 @@
 namespace attn {
 
 constexpr unsigned kErrBadTree = 0x8u;        // ATTN_DEVERR_BAD_REQUEST
-constexpr int kTreeDesc = 8;                  // tiles whose descriptors are kept: K runs at most 5 tiles ahead of S, S 2 of P
+constexpr int kTreeDesc = 8;                  // tiles whose descriptors are kept: K runs at most 4 tiles ahead of S, S 3 of P
 
 template <int HD_, typename KV_, int PARTS_>
 struct TreeCfg {
@@ -55,11 +55,12 @@ struct TreeCfg {
     using KV = KV_;
     using MT = typename PagedMma<KV>::T;
     static constexpr bool E8 = std::is_same<KV, E4m3>::value;
-    static constexpr int NS = HD == 256 ? 1 : 2;               // warpgroups at the softmax
+    static constexpr bool PAIR = HD <= 128;                    // whether tensor memory holds two O
+    static constexpr int NB = HD == 256 ? 4 : 3;               // S of the warpgroups in turn
     static constexpr int TR = HD == 256 ? 64 : 128;            // cache rows of a tile
     static constexpr int NSLC = TR / 16;                       // 16-row slices
     static constexpr int TPG = 32 / NSLC;                      // tiles whose pages a warp looks up at once
-    static constexpr int SM_WARPS = 4 * NS, FIX = SM_WARPS;
+    static constexpr int SM_WARPS = 8, FIX = SM_WARPS;
     // of a block of few slots the first warps have rows, those of the first scheduler: the issuer and the producers are
     // with the others
     static constexpr int PROD_V = FIX + 5, MMA = FIX + 6, PROD_K = FIX + 7;
@@ -75,16 +76,17 @@ struct TreeCfg {
     static constexpr uint32_t KSLOT = F8 ? RAW : SLOT;
     // chunks of a row as they lie in shared memory: 128 bytes (64: 8-bit rows of 64 dimensions)
     static constexpr int RCHB = HD < 128 ? HD : 128, RNCH = HD / RCHB, NCH = HD / 64;
-    static constexpr uint32_t TM_S = 0, TM_O = 2 * TR, TM_COLS = 512;
+    static constexpr uint32_t TM_COLS = 512;                   // O first, then the S
     static constexpr uint32_t DATA = 224 * 1024;               // Q and the rings
     static constexpr uint32_t OFF_DESC = DATA;
-    static constexpr uint32_t OFF_BAR = OFF_DESC + kTreeDesc * 96;
-    static constexpr int NBAR = 39 + kTreeDesc;
+    static constexpr uint32_t OFF_BAR = OFF_DESC + kTreeDesc * 128;
+    static constexpr int NBAR = 50 + kTreeDesc;
     static constexpr uint32_t OFF_FLAG = OFF_BAR + NBAR * 8;   // TMEM slot, abort, share, total
     static constexpr uint32_t OFF_SEQ = OFF_FLAG + 16;         // before, first token, rows
-    static constexpr uint32_t SMEM = OFF_SEQ + (3 * kPagedSeqs + 2) * 4;
+    static constexpr uint32_t OFF_REF = OFF_SEQ + (3 * kTreeSeqs + 2) * 4;   // references of 128 slots
+    static constexpr uint32_t SMEM = OFF_REF + 128 * 4;
     static_assert(SMEM <= 227 * 1024, "shared memory");
-    static_assert(2 * TR + NS * HD <= 512, "tensor memory");
+    static_assert(NB * TR + HD <= 512 && (!PAIR || 2 * TR + 2 * HD <= 512), "tensor memory");
 };
 
 struct __align__(16) TileInfo {
@@ -93,16 +95,17 @@ struct __align__(16) TileInfo {
     unsigned slices;          // 16-row slices that are there
     int live;                 // rows of it that belong to the sequence
     unsigned bad[4];          // rows with an infinity or NaN in V that was taken out (edge tiles)
-    float ks[8], vs[8];
+    float ks[8], vs[8];       // scales of its slices
+    float lv[8];              // log2 of the V scales, rounded up
 };
-static_assert(sizeof(TileInfo) == 96, "its place in shared memory");
+static_assert(sizeof(TileInfo) == 128, "its place in shared memory");
 
 // What a block has of a sequence: tiles [t0, t1) of its T
 struct TreeSeg {
     int s, t0, t1, T;
     int n, tok0, nkv, base, start;
     int slots;                // of the unit in this sequence, at most 256
-    bool pair;                // more than 128: both warpgroups on every tile
+    bool pair;                // more than 128: a tile of Q for each warpgroup
     int row0;                 // first row of tile 0
 };
 
@@ -145,9 +148,24 @@ __device__ __forceinline__ void tmem_ld2(uint32_t t, uint32_t &a, uint32_t &b)
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];\n\ttcgen05.wait::ld.sync.aligned;"
                  : "=r"(a), "=r"(b) : "r"(t) : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Waits for the loads issued before, of which r is one: nothing that uses r comes before it.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :: "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
 // The same with e4m3 operands.
 __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
 {
@@ -273,7 +291,7 @@ __device__ __forceinline__ unsigned bit_range(int a, int b)
 
 template <class C>
 struct Tree {
-    static constexpr int HD = C::HD, PARTS = C::PARTS, TR = C::TR, NS = C::NS;
+    static constexpr int HD = C::HD, PARTS = C::PARTS, TR = C::TR;
     using MT = typename C::MT;
 
     const TreeArgs &a;
@@ -290,19 +308,43 @@ struct Tree {
     __device__ __forceinline__ uint32_t empty(bool v, int i) const { return bar(v * 16 + 8 + i); }
     __device__ __forceinline__ uint32_t raw(bool v, int i) const { return bar(v * 16 + 12 + i); }
     __device__ __forceinline__ uint32_t s_full(int i) const { return bar(32 + i); }
-    __device__ __forceinline__ uint32_t p_ready(int i) const { return bar(34 + i); }
-    __device__ __forceinline__ uint32_t o_done(int i) const { return bar(36 + i); }
-    __device__ __forceinline__ uint32_t q_ready() const { return bar(38); }
-    __device__ __forceinline__ uint32_t described(unsigned tile) const { return bar(39 + (tile & (kTreeDesc - 1))); }
+    __device__ __forceinline__ uint32_t p_ready(int i) const { return bar(36 + i); }
+    __device__ __forceinline__ uint32_t o_done(int i) const { return bar(40 + i); }
+    __device__ __forceinline__ uint32_t ref_known(int quad) const { return bar(44 + quad); }
+    __device__ __forceinline__ uint32_t q_ready() const { return bar(48); }
+    __device__ __forceinline__ uint32_t described(unsigned tile) const { return bar(50 + (tile & (kTreeDesc - 1))); }
+    __device__ __forceinline__ uint32_t met() const { return bar(49); }
     // [0] tensor memory, [1] abort, [2] places of a rank, [3] of all
     __device__ __forceinline__ volatile int *flags() const { return reinterpret_cast<volatile int *>(smem + C::OFF_FLAG); }
     __device__ __forceinline__ int *before() const { return reinterpret_cast<int *>(smem + C::OFF_SEQ); }   // places before each sequence
-    __device__ __forceinline__ int *tok() const { return before() + kPagedSeqs + 1; }                        // first tokens
-    __device__ __forceinline__ int *rows() const { return tok() + kPagedSeqs + 1; }                          // rows
+    __device__ __forceinline__ int *tok() const { return before() + kTreeSeqs + 1; }                         // first tokens
+    __device__ __forceinline__ int *rows() const { return tok() + kTreeSeqs + 1; }                          // rows
     // Q, then V's tiles, K's, and the 8-bit ones that are converted
     __device__ __forceinline__ uint32_t v_slot(int i) const { return sm + a.q_bytes + i * C::SLOT; }
     __device__ __forceinline__ uint32_t k_slot(int i) const { return v_slot(a.nv) + i * C::KSLOT; }
     __device__ __forceinline__ uint32_t raw_slot(bool v, int i) const { return k_slot(a.nk) + ((v ? 0 : a.nrv) + i) * C::RAW; }
+    // Tensor memory: O of a warpgroup (of both, where they take tiles in turn), and S
+    static __device__ __forceinline__ uint32_t o_col(bool pair, int w) { return pair ? w * HD : 0; }
+    static __device__ __forceinline__ uint32_t s_col(bool pair, int b) { return (pair ? 2 * HD : HD) + b * TR; }
+    // The S of a segment's tile t for warpgroup w, and how often it was used before in the segment. `Uses` keeps the
+    // parities of all segments before.
+    struct Uses {
+        unsigned odd = 0;
+        static __device__ __forceinline__ int buffer(bool pair, int w, int t) { return pair ? w : t % C::NB; }
+        __device__ __forceinline__ unsigned parity(bool pair, int w, int t) const
+        {
+            return (odd >> buffer(pair, w, t) ^ (pair ? t : t / C::NB)) & 1;
+        }
+        __device__ __forceinline__ void end(bool pair, int T)
+        {
+            if (pair) {
+                odd ^= T & 1 ? 3u : 0u;
+            } else {
+#pragma unroll
+                for (int b = 0; b < C::NB; ++b) odd ^= ((unsigned)(T + C::NB - 1 - b) / C::NB & 1) << b;
+            }
+        }
+    };
     // A place in a ring of n tiles, and the parity of what is waited for there
     struct Ring {
         int at;
@@ -322,6 +364,14 @@ struct Tree {
         flags()[1] = 1;
         atomicOr(a.err, kErrPipelineTimeout);
         return false;
+    }
+    // All warps of the softmax; gives up like every wait.
+    unsigned meetings = 0;
+    __device__ __forceinline__ bool group_sync()
+    {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) bar_arrive(met());
+        return wait_warp(met(), meetings++ & 1);
     }
     // by a whole warp: one lane asks
     __device__ __forceinline__ bool wait_warp(uint32_t bar, unsigned parity)
@@ -368,7 +418,7 @@ struct Tree {
         g.t0 = p - before()[lo];
         g.t1 = min(g.T, g.t0 + end - p);
         g.slots = min(g.n * a.group - first_slot(), a.unit_slots);
-        g.pair = NS == 2 && g.slots > 128;
+        g.pair = C::PAIR && g.slots > 128;
         g.row0 = min(low_of(g.base, g.start), g.nkv) / TR * TR;
         return p + g.t1 - g.t0;
     }
@@ -378,7 +428,7 @@ struct Tree {
     // -----------------------------------------------------------------------
     __device__ __forceinline__ void count(int lane)
     {
-        constexpr int MOST = kPagedSeqs / 32;
+        constexpr int MOST = kTreeSeqs / 32;
         const int per = (a.n_seq + 31) / 32;
         int places[MOST], sum = 0;
 #pragma unroll
@@ -492,6 +542,7 @@ struct Tree {
                             TileInfo *d = tile_info(tiles + i);
                             d->ks[ls] = f.x;
                             d->vs[ls] = f.y;
+                            d->lv[ls] = (float)min(max((int)(__float_as_uint(f.y) >> 23 & 0xFFu) - 126, -60), 61);   // its exponent field
                             if (ls == 0) {
                                 const int seen_lo = max(g.start, a.window > 0 ? g.base + a.max_nodes - a.window : 0);
                                 d->row0 = r;
@@ -524,10 +575,11 @@ struct Tree {
     // -----------------------------------------------------------------------
     // A tile of codes to f16. A thread's units of 16 codes: one column, rows RSTEP (a multiple of 8) apart, so that the swizzle
     // is the same for all; their loads go out before the first conversion.
+    static constexpr int UPR = HD / 16, RSTEP = 128 / UPR, NU = TR / RSTEP;
     template <bool V>
     __device__ __forceinline__ bool convert(Ring &rr, Ring &sr, int tid)
     {
-        constexpr int UPR = HD / 16, RSTEP = 128 / UPR, N = TR / RSTEP;
+        constexpr int N = NU;
         const int r = tid / UPR, u = tid % UPR, c = u >> 2, v = (u & 3) * 2;
         if (!wait_warp(full(V, rr.at), rr.phase)) return false;
         uint32_t src = raw_slot(V, rr.at);
@@ -575,9 +627,10 @@ struct Tree {
             TreeSeg g;
             p = segment(p, end, g);
             const int T = g.t1 - g.t0;
-            // K before V, with both warpgroups on a tile each K of the next tile too
-            const int ahead = g.pair ? 0 : 1;
-            if (C::KCONV && ahead && !key()) return;
+            // K as far before V as S is before P V
+            const int ahead = g.pair ? 0 : C::NB - 1;
+            for (int t = 0; C::KCONV && t < min(ahead, T); ++t)
+                if (!key()) return;
 #pragma unroll 1
             for (int t = 0; t < T; ++t, ++tiles) {
                 if (C::KCONV && t + ahead < T && !key()) return;
@@ -589,14 +642,12 @@ struct Tree {
                 if (!wait_warp(described(tiles), tiles / kTreeDesc & 1)) return;
                 TileInfo *d = tile_info(tiles);
                 const bool look = static_cast<volatile TileInfo *>(d)->edge & 1;
-                if (look) {
-                    if (C::E8) asm volatile("bar.sync 2, 128;" ::: "memory");   // other warps' rows
-                    const uint32_t to = v_slot(vs.at);
+                if (look) {                                    // the units that this thread has written, where it has
+                    const int u = tid % UPR * 2;
+                    const uint32_t to = v_slot(vs.at) + (u >> 3) * (TR * 128);
 #pragma unroll 1
-                    for (int i = tid; i < TR * (HD / 16); i += 128) {
-                        const int r = i % TR, u = i / TR * 2;
-                        const uint32_t at = to + (u >> 3) * (TR * 128) + r * 128;
-                        const uint32_t p0 = at + ((u & 7 ^ (r & 7)) << 4), p1 = at + (((u + 1) & 7 ^ (r & 7)) << 4);
+                    for (int r = tid / UPR; r < TR; r += RSTEP) {
+                        const uint32_t p0 = to + r * 128 + (((u ^ r) & 7) << 4), p1 = to + r * 128 + ((((u + 1) ^ r) & 7) << 4);
                         uint4 y0 = lds128(p0), y1 = lds128(p1);
                         if (clean(d, r, y0, y1)) {
                             sts128(p0, y0);
@@ -641,82 +692,87 @@ struct Tree {
     }
 
     // -----------------------------------------------------------------------
-    // Issuer: one thread.
+    // Issuer: a warp, so that what is the same in all lanes (descriptors, addresses) stays in uniform registers; one lane
+    // issues.
     // -----------------------------------------------------------------------
-    __device__ __forceinline__ void issue(uint32_t tm, int from, int end)
+    __device__ __forceinline__ void issue(uint32_t tm_any, int from, int end)
     {
+        const uint32_t tm = __shfl_sync(0xffffffffu, tm_any, 0);
+        const bool one = elect_one();
         Ring kr{0, 0}, vr{0, 0};
-        unsigned segs = 0, seen = 0, done0 = 0, done1 = 0;     // items whose S (one stream), whose P V was issued, by stream
+        unsigned segs = 0;
+        Uses uses;
         constexpr uint32_t id_s = C::F8 ? 1u << 4 | (uint32_t)(TR >> 3) << 17 | 8u << 24 : umma_idesc<MT>(128, TR, 0, 0);
         constexpr uint32_t id_o = umma_idesc<MT>(128, HD, 0, 1);
-        auto scores = [&](int qt, int b) {
-            const uint32_t k = k_slot(kr.at), q = sm + (uint32_t)qt * a.q_parts * C::QPART, d = tm + C::TM_S + b * TR;
+        // rows of 128 bytes (swizzle 2, 8 rows 1024 bytes apart) or 64 (8-bit, head_dim 64: 4, 512)
+        constexpr uint32_t SW = C::F8 && HD == 64 ? 4 : 2, SBO = SW == 4 ? 512 : 1024;
+        constexpr int KK = C::F8 ? HD / 32 : HD / 16;          // steps of 32 bytes of a row
+        const uint64_t q0 = umma_desc(sm, 16, SBO, SW), k0 = umma_desc(k_slot(0), 16, SBO, SW);
+        const uint64_t v0 = umma_desc(v_slot(0), TR * 128, 1024, 2);
+        auto scores = [&](int qt, int b, uint32_t d, bool last) {
+            const uint64_t k = k0 + (uint32_t)kr.at * (C::KSLOT >> 4);
+            uint64_t q = q0 + (uint32_t)(qt * a.q_parts) * (C::QPART >> 4);
             tc_fence_after();
-            if constexpr (C::F8) {
-                // 32 codes a step; rows of 128 bytes (swizzle 2, 8 rows 1024 bytes apart) or 64 (4, 512)
-                constexpr uint32_t SW = C::RCHB == 128 ? 2 : 4, SBO = C::RCHB * 8;
+            if (one) {
 #pragma unroll 1
-                for (int x = 0; x < a.q_parts; ++x)
+                for (int x = 0; x < a.q_parts; ++x) {
 #pragma unroll
-                    for (int kk = 0; kk < HD / 32; ++kk)
-                        umma_f8(d, umma_desc(q + x * C::QPART + (kk >> 2) * 16384 + (kk & 3) * 32, 16, SBO, SW),
-                                umma_desc(k + (kk >> 2) * (TR * 128) + (kk & 3) * 32, 16, SBO, SW), id_s, x + kk > 0);
-            } else {
-#pragma unroll
-                for (int x = 0; x < PARTS; ++x)
-#pragma unroll
-                    for (int kk = 0; kk < HD / 16; ++kk)
-                        umma_f16(d, umma_desc(q + x * C::QPART + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024, 2),
-                                 umma_desc(k + (kk >> 2) * (TR * 128) + (kk & 3) * 32, 16, 1024, 2), id_s, x + kk > 0);
+                    for (int kk = 0; kk < KK; ++kk) {
+                        const uint64_t qa = q + ((kk >> 2) * 16384 + (kk & 3) * 32) / 16, kb = k + ((kk >> 2) * (TR * 128) + (kk & 3) * 32) / 16;
+                        if constexpr (C::F8) umma_f8(d, qa, kb, id_s, x + kk > 0);
+                        else umma_f16(d, qa, kb, id_s, x + kk > 0);
+                    }
+                    q += C::QPART >> 4;
+                }
+                bar_commit(s_full(b));
+                if (last) bar_commit(empty(false, kr.at));
             }
-            bar_commit(s_full(b));
+            __syncwarp();
         };
-        auto values = [&](int w, int b) {
-            const uint32_t v = v_slot(vr.at);
+        auto values = [&](uint32_t o, int b, uint32_t s, bool last) {
+            const uint64_t v = v0 + (uint32_t)vr.at * (C::SLOT >> 4);
             tc_fence_after();
+            if (one) {
 #pragma unroll
-            for (int kk = 0; kk < TR / 16; ++kk)
+                for (int kk = 0; kk < TR / 16; ++kk)
 #pragma unroll
-                for (int x = 0; x < PARTS; ++x)
-                    umma_f16_ts(tm + C::TM_O + w * HD, tm + C::TM_S + b * TR + 32 * (kk >> 1) + 16 * x + 8 * (kk & 1),
-                                umma_desc(v + kk * 2048, TR * 128, 1024, 2), id_o);
-            bar_commit(o_done(b));
+                    for (int x = 0; x < PARTS; ++x) umma_f16_ts(o, s + 32 * (kk >> 1) + 16 * x + 8 * (kk & 1), v + kk * 128, id_o);
+                bar_commit(o_done(b));
+                if (last) bar_commit(empty(true, vr.at));
+            }
+            __syncwarp();
         };
         for (int p = from; p < end;) {
             TreeSeg g;
             p = segment(p, end, g);
-            if (!wait(q_ready(), segs++ & 1)) return;
-            const int T = g.t1 - g.t0, items = g.pair ? 2 * T : T;
-            int pw = 0, pb = 0;
+            if (!wait_warp(q_ready(), segs++ & 1)) return;
+            const bool pair = __shfl_sync(0xffffffffu, g.pair, 0);
+            const int T = __shfl_sync(0xffffffffu, g.t1 - g.t0, 0);
+            // S of a tile some tiles before P V of one: as many as there are S; of two warpgroups in turn, one
+            const int items = pair ? 2 * T : T, ahead = pair ? 1 : C::NB - 1;
 #pragma unroll 1
-            for (int i = 0; i <= items; ++i) {
-                int w = 0, b = 0;
+            for (int i = 0; i < items + ahead; ++i) {
                 if (i < items) {
-                    w = NS == 2 ? i & 1 : 0;
-                    b = NS == 2 ? w : (int)(seen++ & 1);
-                    const bool fresh = !g.pair || w == 0, last = !g.pair || w == 1;
-                    if (fresh && !wait(C::KCONV ? ready(false, kr.at) : full(false, kr.at), kr.phase)) return;
-                    scores(g.pair ? w : 0, b);
-                    if (last) {
-                        bar_commit(empty(false, kr.at));
-                        kr.next(a.nk);
-                    }
+                    const int w = pair ? i & 1 : 0, x = pair ? i >> 1 : i, b = Uses::buffer(pair, w, x);
+                    if (w == 0 && !wait_warp(C::KCONV ? ready(false, kr.at) : full(false, kr.at), kr.phase)) return;
+                    // S goes over the P of a product that may still read it: products of other shapes need not end in order
+                    const int over = x - (pair ? 1 : C::NB);
+                    if (over >= 0 && !wait_warp(o_done(b), uses.parity(pair, w, over))) return;
+                    const bool last = !pair || w == 1;         // user of this K
+                    scores(w, b, tm + s_col(pair, b), last);
+                    if (last) kr.next(a.nk);
                 }
-                if (i > 0) {                                   // the item before
-                    if (!wait(p_ready(pb), NS == 1 ? done0 >> 1 & 1 : pw ? done1 & 1 : done0 & 1)) return;
-                    const bool fresh = !g.pair || pw == 0, last = !g.pair || pw == 1;
-                    if (fresh && !wait(ready(true, vr.at), vr.phase)) return;
-                    values(pw, pb);
-                    if (last) {
-                        bar_commit(empty(true, vr.at));
-                        vr.next(a.nv);
-                    }
-                    if (pw) ++done1;
-                    else ++done0;
+                const int j = i - ahead;
+                if (j >= 0) {
+                    const int w = pair ? j & 1 : 0, x = pair ? j >> 1 : j, b = Uses::buffer(pair, w, x);
+                    if (!wait_warp(p_ready(b), uses.parity(pair, w, x))) return;
+                    if (w == 0 && !wait_warp(ready(true, vr.at), vr.phase)) return;
+                    const bool last = !pair || w == 1;
+                    values(tm + o_col(pair, w), b, tm + s_col(pair, b), last);
+                    if (last) vr.next(a.nv);
                 }
-                pw = w;
-                pb = b;
             }
+            uses.end(pair, T);
         }
     }
 
@@ -753,7 +809,7 @@ struct Tree {
     __device__ __forceinline__ float stage_q(const TreeSeg &g, const Row &r, int w, int quad, int lane)
     {
         const int qt = g.pair ? w : 0, my = quad * 32 + lane;
-        const bool half = NS == 2 && !g.pair;
+        const bool half = !g.pair;
         const bool f32 = a.q_type == kTypeF32, f16 = std::is_same<MT, __half>::value;
         const int lg = (HD == 64 ? 3 : HD == 128 ? 4 : 5) + f32;      // log2 of a row's 16-byte units
         const int row_bytes = 16 << lg, su = half ? 2 : 1;
@@ -771,112 +827,128 @@ struct Tree {
         if (half) group_sync();
         else __syncwarp();
         if (!C::F8 && PARTS == 1 && a.q_type == (f16 ? kTypeF16 : kTypeBf16)) return 1.f;   // as it is
-
-        auto sixteen = [&](int part, int u, float (&f)[8]) {          // a unit of 16-bit elements
-            const uint4 x = lds128(q_place(qt, my, part, u));
-            if (a.q_type == kTypeF16) unpack8<__half>(x, f);
-            else unpack8<__nv_bfloat16>(x, f);
-        };
-        auto eight = [&](int u, float (&f)[8]) {                      // elements 8 u ..
-            if (!f32) {
-                if (C::F8) sixteen(u & 1, u >> 1, f);
-                else sixteen(0, u, f);
-                return;
-            }
-            const uint4 x = lds128(q_place(qt, my, 0, u)), y = lds128(q_place(qt, my, 1, u));
-            f[0] = __uint_as_float(x.x); f[1] = __uint_as_float(x.y); f[2] = __uint_as_float(x.z); f[3] = __uint_as_float(x.w);
-            f[4] = __uint_as_float(y.x); f[5] = __uint_as_float(y.y); f[6] = __uint_as_float(y.z); f[7] = __uint_as_float(y.w);
-        };
+        const bool bf = a.q_type == kTypeBf16;
+        const int mine = r.t >= 0 ? HD / 8 : 0;                       // units of 8 elements
         float sc = 1.f, inv = 1.f;
         if (f16) {
-            float m = 0.f;
-#pragma unroll 2
-            for (int u = 0; u < HD / 8; ++u) {
-                float f[8];
-                eight(u, f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
+            // the largest magnitude, by the bits: they order as the numbers do
+            uint32_t m = 0;
+            if (f32) {
+#pragma unroll 4
+                for (int u = 0; u < 2 * mine; ++u) {
+                    const uint4 x = lds128(q_place(qt, my, u & 1, u >> 1));
+                    m = max(max(m, x.x & 0x7fffffffu), max(max(x.y & 0x7fffffffu, x.z & 0x7fffffffu), x.w & 0x7fffffffu));
+                }
+            } else {
+#pragma unroll 4
+                for (int u = 0; u < mine; ++u) {
+                    const uint4 x = lds128(C::F8 ? q_place(qt, my, u & 1, u >> 1) : q_place(qt, my, 0, u));
+                    m = __vmaxu2(__vmaxu2(m, x.x & 0x7fff7fffu), __vmaxu2(__vmaxu2(x.y & 0x7fff7fffu, x.z & 0x7fff7fffu), x.w & 0x7fff7fffu));
+                }
+                m = max(m >> 16, m & 0xffffu);
+                m = bf ? m << 16 : __float_as_uint(kv2_to_float2<__half>(m).x);
             }
-            pow2_scale(m, sc, inv);
+            pow2_scale(__uint_as_float(m), sc, inv);
             if (C::F8) {                                              // 2^7 .. 2^8: e4m3 ends at 448
                 sc *= 0.0078125f;
                 inv *= 128.f;
             }
         }
         if (half) group_sync();                                       // the other warpgroup has read the row too
+        auto pair_of = [&](uint32_t w) {                              // two elements, scaled
+            const float2 x = bf ? kv2_to_float2<__nv_bfloat16>(w) : kv2_to_float2<__half>(w);
+            return make_float2(x.x * sc, x.y * sc);
+        };
         if constexpr (C::F8) {
 #pragma unroll 1
-            for (int u = half ? w : 0; u < HD / 16; u += su) {
-                float f[2][8];
-                sixteen(0, u, f[0]);
-                sixteen(1, u, f[1]);
+            for (int u = half ? w : 0; u < mine / 2; u += su) {       // 16 elements
+                const uint4 x = lds128(q_place(qt, my, 0, u)), y = lds128(q_place(qt, my, 1, u));
+                const uint32_t in[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                __half2 h[8];                                         // exact: 11 bits, and 2^8 is far from f16's limits
 #pragma unroll
-                for (int e = 0; e < 16; ++e) f[e >> 3][e & 7] *= sc;
+                for (int e = 0; e < 8; ++e) {
+                    const float2 f = pair_of(in[e]);
+                    h[e] = __floats2half2_rn(f.x, f.y);
+                }
 #pragma unroll 1
-                for (int x = 0; x < a.q_parts; ++x) {
-                    uint4 y;
-                    uint32_t *yw = &y.x;
+                for (int part = 0; part < a.q_parts; ++part) {
+                    uint32_t c[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float *v = &f[e >> 1][(e & 1) * 4];
-                        yw[e] = e4m3x4_of(v[0], v[1], v[2], v[3]);
-                        uint32_t lo, hi;
-                        e4m3x4_to_half4(yw[e], lo, hi);
-                        const float2 b0 = kv2_to_float2<__half>(lo), b1 = kv2_to_float2<__half>(hi);
-                        v[0] -= b0.x; v[1] -= b0.y; v[2] -= b1.x; v[3] -= b1.y;
+                        uint16_t lo, hi;
+                        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(*reinterpret_cast<uint32_t *>(&h[2 * e])));
+                        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(*reinterpret_cast<uint32_t *>(&h[2 * e + 1])));
+                        c[e] = (uint32_t)lo | (uint32_t)hi << 16;
+                        uint32_t b0, b1;
+                        e4m3x4_to_half4(c[e], b0, b1);
+                        h[2 * e] = __hsub2(h[2 * e], *reinterpret_cast<__half2 *>(&b0));
+                        h[2 * e + 1] = __hsub2(h[2 * e + 1], *reinterpret_cast<__half2 *>(&b1));
                     }
-                    sts128(q_place(qt, my, x, u), y);
+                    sts128(q_place(qt, my, part, u), make_uint4(c[0], c[1], c[2], c[3]));
                 }
             }
         } else {
 #pragma unroll 1
-            for (int u = half ? w : 0; u < HD / 8; u += su) {
-                float f[8];
-                eight(u, f);
+            for (int u = half ? w : 0; u < mine; u += su) {
+                const uint4 x = lds128(q_place(qt, my, 0, u));
+                float2 f[4];
+                if (f32) {
+                    const uint4 y = lds128(q_place(qt, my, 1, u));
+                    f[0] = make_float2(__uint_as_float(x.x) * sc, __uint_as_float(x.y) * sc);
+                    f[1] = make_float2(__uint_as_float(x.z) * sc, __uint_as_float(x.w) * sc);
+                    f[2] = make_float2(__uint_as_float(y.x) * sc, __uint_as_float(y.y) * sc);
+                    f[3] = make_float2(__uint_as_float(y.z) * sc, __uint_as_float(y.w) * sc);
+                } else {
+                    f[0] = pair_of(x.x);
+                    f[1] = pair_of(x.y);
+                    f[2] = pair_of(x.z);
+                    f[3] = pair_of(x.w);
+                }
 #pragma unroll
-                for (int x = 0; x < PARTS; ++x) {
+                for (int part = 0; part < PARTS; ++part) {
                     uint32_t h[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float &f0 = f[2 * e], &f1 = f[2 * e + 1];
-                        if (x == 0) {
-                            f0 *= sc;
-                            f1 *= sc;
-                        }
-                        h[e] = float2_to_kv2<MT>(f0, f1);
-                        if (x + 1 < PARTS) {
+                        h[e] = float2_to_kv2<MT>(f[e].x, f[e].y);
+                        if (part + 1 < PARTS) {
                             const float2 b = kv2_to_float2<MT>(h[e]);
-                            f0 -= b.x;
-                            f1 -= b.y;
+                            f[e].x -= b.x;
+                            f[e].y -= b.y;
                         }
                     }
-                    sts128(q_place(qt, my, x, u), make_uint4(h[0], h[1], h[2], h[3]));
+                    sts128(q_place(qt, my, part, u), make_uint4(h[0], h[1], h[2], h[3]));
                 }
             }
         }
         return inv;
     }
 
-    // tanh: near 0 its series (to x^9, remainder below 1e-8 of it at 1/4), elsewhere 1 - 2 / (1 + e^2x), to 2^-22
-    static __device__ __forceinline__ float tanh_of(float x)
+    // tanh near 0, |x| < 0.4: its series to x^11 (what follows is below 2^-23 of it)
+    static __device__ __forceinline__ float tanh_small(float x)
     {
         const float z = x * x;
-        float s = 2.1869489e-2f;                               // 62 / 2835
+        float s = -8.8632355e-3f;                              // 1382 / 155925
+        s = fmaf(s, z, 2.1869489e-2f);                         // 62 / 2835
         s = fmaf(s, z, -5.3968254e-2f);                        // 17 / 315
         s = fmaf(s, z, 1.3333333e-1f);                         // 2 / 15
         s = fmaf(s, z, -3.3333333e-1f);
-        s = fmaf(s * z, x, x);
-        const float e = ex2(2.f * kLog2e * x);                 // infinity: 1
-        const float l = 1.f - __fdividef(2.f, 1.f + e);
-        return fabsf(x) < 0.25f ? s : e < 1e30f ? l : x == x ? 1.f : x;
+        return fmaf(s * z, x, x);
+    }
+    // elsewhere 1 - 2 / (1 + e^2x), to 2^-22
+    static __device__ __forceinline__ float tanh_of(float x)
+    {
+        const float e = ex2(2.f * kLog2e * x);
+        const float l = e < 1e30f ? fmaf(-2.f, rcp(1.f + e), 1.f) : 1.f;
+        return fabsf(x) < 0.4f ? tanh_small(x) : x == x ? l : x;
     }
 
-    // Scores of 32 columns from tile row c0 on, with the rules, -inf where the slot does not see the row.
-    __device__ __forceinline__ void ruled(const TreeSeg &g, const Row &r, const volatile TileInfo *d, int c0, uint32_t (&v)[32])
+    // The rows of 32 from tile row c0 on that the thread's node sees.
+    __device__ __forceinline__ unsigned seen_bits(const TreeSeg &g, const Row &r, const volatile TileInfo *d, int c0) const
     {
+        if (r.t < 0) return 0u;
         const int j0 = d->row0 + c0, y0 = j0 - g.base;
         unsigned bits = bit_range(low_of(r.x, g.start) - j0, g.base - j0);
-        if (r.t >= 0 && y0 > -32 && y0 < g.n) {
+        if (y0 > -32 && y0 < g.n) {
             unsigned dr;
             if (!a.mask) {
                 dr = bit_range(-y0, r.t + 1 - y0);
@@ -887,7 +959,7 @@ struct Tree {
                 const uint32_t hi = w + 1 < a.words ? ld_mask(mask, w + 1) : 0u;
                 dr = __funnelshift_r(lo, hi, y0 & 31);
             }
-            dr &= bit_range(max(-y0, g.start - j0), g.n - y0) & bit_range(-j0, 32);
+            dr &= bit_range(max(-y0, g.start - j0), g.n - y0);
             if (a.window > 0 && a.window < a.max_nodes)
                 for (unsigned m = dr; m; m &= m - 1) {
                     const int c = __ffs(m) - 1;
@@ -895,23 +967,51 @@ struct Tree {
                 }
             bits |= dr;
         }
-        if (r.t < 0) bits = 0u;
         const unsigned there = d->slices >> (c0 >> 4) & 3u;
-        bits &= (there & 1u ? 0xffffu : 0u) | (there & 2u ? 0xffff0000u : 0u);
+        return bits & ((there & 1u ? 0xffffu : 0u) | (there & 2u ? 0xffff0000u : 0u));
+    }
+
+    // Scores of those 32 with the rules, -inf where the node does not see the row.
+    __device__ __forceinline__ void ruled(const TreeSeg &g, const Row &r, const volatile TileInfo *d, int c0, uint32_t (&v)[32]) const
+    {
         const float f0 = C::E8 ? r.c * d->ks[c0 >> 4] : r.c, f1 = C::E8 ? r.c * d->ks[(c0 >> 4) + 1] : r.c;
-        const bool cap = a.softcap > 0.f, slopes = a.slopes != nullptr;
-        const float slope = slopes ? ld_dep(a.slopes + r.h) * kLog2e : 0.f;
+        float s[32];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-            float s = __uint_as_float(v[c]) * (c < 16 ? f0 : f1);
-            if (cap) s = a.cap_log2 * tanh_of(s);
-            if (slopes) {
-                const int y = y0 + c;
-                const int x = y < 0 || y >= g.n ? j0 + c : g.base + depth_of(g, y);
-                s = fmaf(-slope, (float)(r.x - x), s);
+        for (int c = 0; c < 32; ++c) s[c] = __uint_as_float(v[c]) * (c < 16 ? f0 : f1);
+        if (a.softcap > 0.f) {
+            float k = 0.f;
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) k = fmaxf(fmaxf(k, fabsf(s[c])), fabsf(s[c + 1]));
+            if (__all_sync(0xffffffffu, k < 0.4f)) {           // a cap is seldom come near
+#pragma unroll
+                for (int c = 0; c < 32; ++c) s[c] = a.cap_log2 * tanh_small(s[c]);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) s[c] = a.cap_log2 * tanh_of(s[c]);
             }
-            v[c] = __float_as_uint(bits >> c & 1 ? s : -INFINITY);
         }
+        if (a.slopes) {
+            const float slope = ld_dep(a.slopes + r.h) * kLog2e;
+            const int j0 = d->row0 + c0, y0 = j0 - g.base;
+            if (y0 <= -32 || y0 >= g.n) {
+                const int x0 = r.x - j0;
+#pragma unroll
+                for (int c = 0; c < 32; ++c) s[c] = fmaf(-slope, (float)(x0 - c), s[c]);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const int y = y0 + c;
+                    s[c] = fmaf(-slope, (float)(r.x - (y < 0 || y >= g.n ? j0 + c : g.base + depth_of(g, y))), s[c]);
+                }
+            }
+        }
+        if (d->edge & 1) {
+            const unsigned bits = seen_bits(g, r, d, c0);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) s[c] = bits >> c & 1 ? s[c] : -INFINITY;
+        }
+#pragma unroll
+        for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(s[c]);
     }
     static __device__ __forceinline__ uint32_t ld_mask(const uint32_t *m, int w)
     {
@@ -927,7 +1027,7 @@ struct Tree {
         for (int c = 0; c < HD; c += 32) {
             uint32_t v[32];
             tmem_ld32(o + c, v);
-            tmem_wait_ld();
+            tmem_wait_ld(v);
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
             tmem_st32(o + c, v);
@@ -951,7 +1051,7 @@ struct Tree {
                 for (int c = 0; c < HD; c += 32) {
                     uint32_t v[32];
                     tmem_ld32(o + c, v);
-                    tmem_wait_ld();
+                    tmem_wait_ld(v);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         float x;
@@ -964,6 +1064,7 @@ struct Tree {
                         }
                         if (sees && !(fabsf(x) < INFINITY)) v[i] = __float_as_uint(fmaf(p, x, __uint_as_float(v[i])));
                     }
+                    __syncwarp();
                     tmem_st32(o + c, v);
                 }
                 tmem_wait_st();
@@ -974,16 +1075,20 @@ struct Tree {
     {
         constexpr float TAU = 8.f, OFF = 7.f;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        const uint32_t o_at = tm + C::TM_O + w * HD + lanes;
+        const int my = quad * 32 + lane;
+        volatile float *refs = reinterpret_cast<volatile float *>(smem + C::OFF_REF);
         bool dead = false;
-        unsigned cnt = 0, tiles = 0;                           // items of this stream; tiles before the segment
+        unsigned tiles = 0, refs_odd = 0;                      // tiles before the segment; parity of the references handed on
+        Uses uses;
         const bool rules = a.softcap > 0.f || a.slopes != nullptr || a.qscale <= 0.f;
         for (int p = from; p < end;) {
             TreeSeg g;
             const int next = segment(p, end, g);
             const bool begins = g.t0 == 0, whole = begins && g.t1 == g.T;
-            const int qt = g.pair ? w : 0;
-            const int in_unit = qt * 128 + quad * 32 + lane, slot = first_slot() + in_unit;
+            const bool pair = g.pair;
+            const int T = g.t1 - g.t0, qt = pair ? w : 0;
+            const int in_unit = qt * 128 + my, slot = first_slot() + in_unit;
+            const uint32_t o_at = tm + o_col(pair, w) + lanes;
             Row r;
             r.t = in_unit < g.slots ? div(a.by_group, slot) : -1;
             const bool any = qt * 128 + quad * 32 < g.slots;   // some slot in this warp
@@ -991,7 +1096,8 @@ struct Tree {
             r.x = g.base + depth_of(g, max(r.t, 0));
             r.c = stage_q(g, r, w, quad, lane) * a.qscale;
             fence_proxy_async_smem();                          // Q is read by the tensor cores
-            if (any) {
+            __syncwarp();                                      // rows without a slot had nothing to turn
+            if (any && (pair || w == 0)) {
                 uint32_t z[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) z[i] = 0u;
@@ -1005,13 +1111,12 @@ struct Tree {
 
             const float rc = rcp(r.c);
             float m = -INFINITY, l = 0.f;
-            const int step = NS == 2 && !g.pair ? 2 : 1;
-            for (int t = g.pair || NS == 1 ? 0 : w; t < g.t1 - g.t0; t += step) {
-                const int b = NS == 2 ? w : (int)(cnt & 1);
-                const unsigned par = NS == 2 ? cnt & 1 : cnt >> 1 & 1;
-                const uint32_t s_at = tm + C::TM_S + b * TR + lanes;
+#pragma unroll 1
+            for (int t = pair ? 0 : w; t < T; t += pair ? 1 : 2) {
+                const int b = Uses::buffer(pair, w, t);
+                const uint32_t s_at = tm + s_col(pair, b) + lanes;
                 const volatile TileInfo *d = tile_info(tiles + t);
-                if (!dead) dead = !wait_warp(s_full(b), par);
+                if (!dead) dead = !wait_warp(s_full(b), uses.parity(pair, w, t));
                 if (any && !dead) {
                     tc_fence_after();
                     const bool slow = d->edge || rules;
@@ -1021,79 +1126,81 @@ struct Tree {
                         for (int c = 0; c < TR; c += 32) {
                             uint32_t v[32];
                             tmem_ld32(s_at + c, v);
-                            tmem_wait_ld();
+                            tmem_wait_ld(v);
                             ruled(g, r, d, c, v);
+                            __syncwarp();
                             tmem_st32(s_at + c, v);
-                            mx = fmaxf(mx, fmaxf(most16(v, 0) + shift_of(d, c >> 4), most16(v, 16) + shift_of(d, (c >> 4) + 1)));
+                            float k0 = most16(v, 0), k1 = most16(v, 16);
+                            if (C::E8) {
+                                k0 += d->lv[c >> 4];
+                                k1 += d->lv[(c >> 4) + 1];
+                            }
+                            mx = fmaxf(mx, fmaxf(k0, k1));
                         }
                         tmem_wait_st();
                     } else {
-#pragma unroll 1
-                        for (int c = 0; c < TR; c += 64) {
-                            uint32_t v[2][32];
-                            tmem_ld32(s_at + c, v[0]);
-                            tmem_ld32(s_at + c + 32, v[1]);
-                            tmem_wait_ld();
-                            float k = -INFINITY;
+                        auto most = [&](const uint32_t (&v)[32], int c) {
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                float x = most16(v[y >> 1], (y & 1) * 16);
-                                if (C::E8) x = fmaf(x, d->ks[(c >> 4) + y], shift_of(d, (c >> 4) + y) * rc);
-                                k = fmaxf(k, x);
+                            for (int y = 0; y < 2; ++y) {
+                                float k = most16(v, 16 * y);
+                                if (C::E8) k = fmaf(k, d->ks[(c >> 4) + y], d->lv[(c >> 4) + y] * rc);
+                                mx = fmaxf(mx, k);
                             }
-                            mx = fmaxf(mx, k);
-                        }
+                        };
+                        by_32(s_at, most);
                         mx *= r.c;
                     }
+                    // the reference: that of the tile before, or a new one
+                    const float own = m;
+                    if (!pair && t > 0) {
+                        dead = !wait_warp(ref_known(quad), (refs_odd ^ (t - 1)) & 1);
+                        m = refs[my];
+                    }
                     const bool need = mx > m + TAU;
+                    const float before = m;
+                    if (need) m = mx;
+                    if (!pair) {
+                        refs[my] = m;
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(ref_known(quad));
+                    }
                     const bool bad = (d->edge & 1) && (d->bad[0] | d->bad[1] | d->bad[2] | d->bad[3]) != 0u;
                     if (__any_sync(0xffffffffu, need) || bad) {
-                        // one S buffer a stream: S is complete, so is what was issued before it; two: O's last product is not
-                        if (NS == 1 && cnt > 0 && !wait_warp(o_done((b ^ 1)), (cnt - 1) >> 1 & 1)) dead = true;
+                        // O stands still from the product before (of a pair's warpgroup: issued before this S) to this one
+                        if (!pair && t > 0 && !dead)
+                            dead = !wait_warp(o_done(Uses::buffer(pair, w, t - 1)), uses.parity(pair, w, t - 1));
                         tc_fence_after();
-                        if (!dead && __any_sync(0xffffffffu, need)) {
-                            const float f = need ? ex2(m - mx) : 1.f;      // 0 while m is -inf
-                            if (need) m = mx;
-                            l *= f;
-                            scale_o(o_at, f);
-                        }
+                        if (!dead && __any_sync(0xffffffffu, need)) scale_o(o_at, need ? ex2(before - m) : 1.f);   // 0 from -inf
                         if (!dead && bad) add_bad(g, d, s_at, o_at, m == -INFINITY ? 0.f : m - OFF);
                     }
+                    if (own != m) l *= ex2(own - m);
                     const float ref = m == -INFINITY ? 0.f : m - OFF;
                     const uint64_t nref = pack2(-ref, -ref);
                     uint64_t sum = pack2(0.f, 0.f);
-#pragma unroll 1
-                    for (int c = 0; c < TR; c += 64) {
-                        uint32_t v[2][32];
-                        tmem_ld32(s_at + c, v[0]);
-                        tmem_ld32(s_at + c + 32, v[1]);
-                        tmem_wait_ld();
+                    by_32(s_at, [&](const uint32_t (&v)[32], int c) {
+                        uint32_t h[PARTS][16];
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            uint32_t h[PARTS][16];
+                        for (int x = 0; x < 2; ++x) {
+                            const int at = (c >> 4) + x;
+                            const float f = slow ? 1.f : C::E8 ? r.c * d->ks[at] : r.c, vs = C::E8 ? d->vs[at] : 1.f;
+                            const uint64_t f2 = pack2(f, f), vs2 = pack2(vs, vs);
 #pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const int at = (c >> 4) + 2 * y + x;
-                                const float f = slow ? 1.f : C::E8 ? r.c * d->ks[at] : r.c, vs = C::E8 ? d->vs[at] : 1.f;
-                                const uint64_t f2 = pack2(f, f), vs2 = pack2(vs, vs);
-#pragma unroll
-                                for (int i = 8 * x; i < 8 * x + 8; ++i) {
-                                    const float2 s = unpack2(fma2(pack2(__uint_as_float(v[y][2 * i]), __uint_as_float(v[y][2 * i + 1])), f2, nref));
-                                    uint64_t p = pack2(ex2(s.x), ex2(s.y));
-                                    sum = add2(sum, p);
-                                    if (C::E8) p = mul2(p, vs2);
-                                    const float2 q = unpack2(p);
-                                    h[0][i] = float2_to_kv2<MT>(q.x, q.y);
-                                    if (PARTS == 2) {
-                                        const float2 b = kv2_to_float2<MT>(h[0][i]);
-                                        h[PARTS - 1][i] = float2_to_kv2<MT>(q.x - b.x, q.y - b.y);
-                                    }
+                            for (int i = 8 * x; i < 8 * x + 8; ++i) {
+                                const float2 s = unpack2(fma2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2, nref));
+                                uint64_t p = pack2(ex2(s.x), ex2(s.y));
+                                sum = add2(sum, p);
+                                if (C::E8) p = mul2(p, vs2);
+                                const float2 q = unpack2(p);
+                                h[0][i] = float2_to_kv2<MT>(q.x, q.y);
+                                if (PARTS == 2) {
+                                    const float2 y = kv2_to_float2<MT>(h[0][i]);
+                                    h[PARTS - 1][i] = float2_to_kv2<MT>(q.x - y.x, q.y - y.y);
                                 }
                             }
-#pragma unroll
-                            for (int x = 0; x < PARTS; ++x) tmem_st16(s_at + c + 32 * y + 16 * x, h[x]);
                         }
-                    }
+#pragma unroll
+                        for (int x = 0; x < PARTS; ++x) tmem_st16(s_at + c + 16 * x, h[x]);
+                    });
                     const float2 both = unpack2(sum);
                     l += both.x + both.y;
                     tmem_wait_st();
@@ -1101,13 +1208,40 @@ struct Tree {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) bar_arrive(p_ready(b));
-                ++cnt;
             }
+            // every product of the segment is done
+            {
+                // (A barrier's parity tells a phase from the one before only: the warpgroup without the last tile may not
+                // know yet that the last tile's S was free for it.)
+                const int last = T - 1, over = last - C::NB;
+                if (!pair && over >= 0 && !dead) dead = !wait_warp(o_done(Uses::buffer(pair, w, over)), uses.parity(pair, w, over));
+                if (!dead) dead = !wait_warp(o_done(Uses::buffer(pair, w, last)), uses.parity(pair, w, last));
+            }
+            uses.end(pair, T);
+            if (any && !pair) refs_odd ^= T & 1;
             // a slot whose every score is NaN keeps its NaN sum
-            const float mref = m == -INFINITY && l != 0.f ? 0.f : m - OFF;
-            finish(tm, g, r, w, quad, lane, cnt, whole, begins, rank, mref, l, any, dead);
-            tiles += g.t1 - g.t0;
+            finish(tm, g, r, w, quad, lane, whole, begins, rank, m == -INFINITY && l != 0.f ? 0.f : m - OFF, l, any, dead);
+            tiles += T;
             p = next;
+        }
+    }
+    // f(32 columns, the first one's number) for a tile's columns, the next 32 on their way meanwhile. Two copies of f, not
+    // one for each 32: code that does not stay in the schedulers' instruction caches, four roles of it, runs three times
+    // as long.
+    template <class F>
+    static __device__ __forceinline__ void by_32(uint32_t s_at, F f)
+    {
+        uint32_t u[32], v[32];
+        tmem_ld32(s_at, u);
+        tmem_wait_ld(u);
+#pragma unroll 1
+        for (int c = 0; c < TR; c += 64) {
+            tmem_ld32(s_at + c + 32, v);
+            f(u, c);
+            tmem_wait_ld(v);
+            if (c + 64 < TR) tmem_ld32(s_at + c + 64, u);
+            f(v, c + 32);
+            tmem_wait_ld(u);
         }
     }
     static __device__ __forceinline__ float most16(const uint32_t (&v)[32], int at)
@@ -1117,26 +1251,13 @@ struct Tree {
         for (int i = 1; i < 15; i += 2) k = fmaxf(fmaxf(k, __uint_as_float(v[at + i])), __uint_as_float(v[at + i + 1]));
         return fmaxf(k, __uint_as_float(v[at + 15]));
     }
-    // log2 of a slice's V scale, rounded up: its exponent field
-    static __device__ __forceinline__ float shift_of(const volatile TileInfo *d, int slice)
-    {
-        if constexpr (!C::E8) return 0.f;
-        const int e = (int)((__float_as_uint(d->vs[slice]) >> 23) & 0xFFu) - 126;
-        return (float)min(max(e, -60), 61);
-    }
 
-    static __device__ __forceinline__ void group_sync() { asm volatile("bar.sync 1, %0;" :: "r"(C::SM_WARPS * 32) : "memory"); }
-
-    // The end of a segment: the output, or the block's part of it.
-    __device__ __forceinline__ void finish(uint32_t tm, const TreeSeg &g, const Row &r, int w, int quad, int lane, unsigned cnt,
-                                           bool whole, bool begins, int rank, float m, float l, bool any, bool &dead)
+    // The end of a segment: the output, or the block's part of it. Warpgroups in turn share O, and write half of its dimensions
+    // each.
+    __device__ __forceinline__ void finish(uint32_t tm, const TreeSeg &g, const Row &r, int w, int quad, int lane, bool whole,
+                                           bool begins, int rank, float m, float l, bool any, bool dead)
     {
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        const bool mine = g.pair || NS == 1 || g.t1 - g.t0 > w;    // this stream had an item
-        if (mine && !dead) {
-            const unsigned last = cnt - 1;
-            dead = !wait_warp(o_done((NS == 2 ? w : (int)(last & 1))), NS == 2 ? last & 1 : last >> 1 & 1);
-        }
         tc_fence_after();
         const size_t block = ((size_t)(rank * 2 + (begins ? 1 : 0)) * gridDim.x + blockIdx.x) * a.unit_slots;
         const int in_unit = (g.pair ? w : 0) * 128 + quad * 32 + lane;
@@ -1166,52 +1287,42 @@ struct Tree {
                 }
             }
         };
-        if (NS == 2 && !g.pair) {
-            // the other warpgroup's reference and sum, through this thread's lane of tensor memory
-            const uint32_t box = tm + C::TM_S + lanes;
+        int d0 = 0, d1 = HD;
+        float f = 1.f;                                         // what O is to be multiplied by
+        if (!g.pair) {
+            // the other warpgroup's reference and sum, through this thread's lane of tensor memory; O has the larger reference
+            const uint32_t box = tm + s_col(false, 0) + lanes;
             if (any) {
-                tmem_st2(box + w * TR, __float_as_uint(m), __float_as_uint(l));
+                tmem_st2(box + 2 * w, __float_as_uint(m), __float_as_uint(l));
                 tmem_wait_st();
             }
             tc_fence_before();
             group_sync();
             tc_fence_after();
-            if (any && !dead) {
+            if (any) {
                 uint32_t om, ol;
-                tmem_ld2(box + (w ^ 1) * TR, om, ol);
+                tmem_ld2(box + 2 * (w ^ 1), om, ol);
                 const float m1 = __uint_as_float(om), l1 = __uint_as_float(ol), M = fmaxf(m, m1);
-                const float f = m == -INFINITY ? 0.f : ex2(m - M), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
-                const float L = (m == -INFINITY ? 0.f : l * f) + (m1 == -INFINITY ? 0.f : l1 * f1);
-                const float inv = L == 0.f ? 0.f : rcp(L);
-                if (!whole && w == 0 && r.t >= 0) a.ws_ml[block + in_unit] = make_float2(M, L);
-#pragma unroll 1
-                for (int d = w * (HD / 2); d < (w + 1) * (HD / 2); d += 32) {
-                    uint32_t u[32], v[32];
-                    tmem_ld32(tm + C::TM_O + w * HD + lanes + d, u);
-                    tmem_ld32(tm + C::TM_O + (w ^ 1) * HD + lanes + d, v);
-                    tmem_wait_ld();
-                    float y[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        float x = m == -INFINITY ? 0.f : __uint_as_float(u[i]) * f;
-                        if (m1 != -INFINITY) x = fmaf(__uint_as_float(v[i]), f1, x);
-                        y[i] = x;
-                    }
-                    put(d, y, inv);
-                }
+                l = (m == -INFINITY ? 0.f : l * ex2(m - M)) + (m1 == -INFINITY ? 0.f : l1 * ex2(m1 - M));
+                m = M;
             }
-        } else if (any && !dead) {
-            const float inv = l == 0.f ? 0.f : rcp(l);
-            if (!whole && r.t >= 0) a.ws_ml[block + in_unit] = make_float2(m, l);
+            d0 = w * (HD / 2);
+            d1 = d0 + HD / 2;
+        }
+        if (any && !dead) {
+            if (!whole && r.t >= 0 && d0 == 0) a.ws_ml[block + in_unit] = make_float2(m, l);
+            if (whole) f = l == 0.f ? 0.f : rcp(l);
+            const uint32_t o = tm + o_col(g.pair, w) + lanes;
 #pragma unroll 1
-            for (int d = 0; d < HD; d += 32) {
+            for (int d = d0; d < d1; d += 32) {
                 uint32_t u[32];
-                tmem_ld32(tm + C::TM_O + w * HD + lanes + d, u);
-                tmem_wait_ld();
+                tmem_ld32(o + d, u);
+                tmem_wait_ld(u);
                 float y[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(u[i]);
-                put(d, y, inv);
+                put(d, y, f);
+                __syncwarp();
             }
         }
         // the next segment's Q and zeros go over what the other warpgroup reads, and over what its products read
@@ -1231,12 +1342,14 @@ attn_tree_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     if (warp == C::PROD_K) {
         if (lane == 0) {
             for (int i = 0; i < 32; ++i) bar_init(x.bar(i), i & 4 ? 4 : 1);   // ready and raw: a lane of each converting warp
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 4; ++i) {
                 bar_init(x.s_full(i), 1);
                 bar_init(x.p_ready(i), 4);
                 bar_init(x.o_done(i), 1);
+                bar_init(x.ref_known(i), 1);
             }
             bar_init(x.q_ready(), C::SM_WARPS);
+            bar_init(x.met(), C::SM_WARPS);
             for (int i = 0; i < kTreeDesc; ++i) bar_init(x.described(i), 1);
             x.flags()[1] = 0;
             fence_barrier_init();
@@ -1264,10 +1377,10 @@ attn_tree_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     const int share = x.flags()[2], total = x.flags()[3];
     const int64_t first = (int64_t)rank * share;
     const int from = (int)min(first, (int64_t)total), end = (int)min(first + share, (int64_t)total);
-    if constexpr (C::NS == 2) {
+    {
         if (warp < C::SM_WARPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
-        else if (warp < C::FIX + 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        else if (warp < C::FIX + 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     }
     if (warp < C::SM_WARPS) {
         x.softmax(tm, from, end, warp >> 2, warp & 3, lane, rank);
@@ -1277,7 +1390,7 @@ attn_tree_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         x.template produce<false>(&kmap, from, end, lane);
     } else if (warp == C::PROD_V) {
         x.template produce<true>(&vmap, from, end, lane);
-    } else if (warp == C::MMA && lane == 0) {
+    } else if (warp == C::MMA) {
         x.issue(tm, from, end);
     }
     __syncwarp();
@@ -1412,7 +1525,7 @@ cudaError_t launch_tree_kernel(const TreeRequest &r)
     } else if (C::E8) {
         a.nk = a.nv = left >= 8 * C::SLOT ? 2 : 1;
         a.nrk = a.nrv = few((int)((left - 2 * a.nk * C::SLOT) / (2 * C::RAW)));
-        if (a.nk + a.nrk > 5) a.nrk = 5 - a.nk;
+        if (a.nk + a.nrk > 4) a.nrk = 4 - a.nk;
     } else {
         const int n = (int)(left / C::SLOT);
         a.nk = few((n + (n == 3)) / 2);

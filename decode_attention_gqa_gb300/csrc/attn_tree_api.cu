@@ -50,10 +50,10 @@ void make_plan(const attn_paged_cache *c, int max_pages, int n_seq, int max_node
     const int need = max_nodes * (n_head / c->n_kv_head);
     pl.tile = attn::tree_tile(c->head_dim);
     pl.unit_slots = c->head_dim == 256 || need <= 128 ? 128 : 256;
-    pl.min_share = c->head_dim != 256 && need <= 128 ? 2 : 1;
+    pl.min_share = pl.unit_slots == 128 ? 2 : 1;
     const int64_t mus = (need + pl.unit_slots - 1) / pl.unit_slots;
     pl.units = c->n_kv_head * mus;
-    const int64_t seqs = n_seq < attn::kPagedSeqs ? n_seq : attn::kPagedSeqs;
+    const int64_t seqs = n_seq < attn::kTreeSeqs ? n_seq : attn::kTreeSeqs;
     const int64_t tiles = ((int64_t)max_pages * c->page_size + pl.tile - 1) / pl.tile * seqs;
     const int64_t most = (tiles + pl.min_share - 1) / pl.min_share;
     int64_t P = sm_count / pl.units;
@@ -230,7 +230,7 @@ attn_status attn_decode_tree(const attn_paged_cache *cache, const int32_t *block
     a.units = (int)pl.units;
     // tiles are counted in 32 bits: fewer sequences a launch where the capacity is huge
     const int64_t per_seq = ((int64_t)a.cap + pl.tile - 1) / pl.tile + 1;
-    const int batch = (int)(0x3fff0000 / per_seq < attn::kPagedSeqs ? 0x3fff0000 / per_seq : attn::kPagedSeqs);
+    const int batch = (int)(0x3fff0000 / per_seq < attn::kTreeSeqs ? 0x3fff0000 / per_seq : attn::kTreeSeqs);
     for (int s0 = 0; s0 < n_seq; s0 += batch) {
         a.n_seq = n_seq - s0 < batch ? n_seq - s0 : batch;
         a.seq0 = s0;
