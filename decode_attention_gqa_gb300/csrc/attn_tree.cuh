@@ -202,6 +202,10 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar)
 {
     asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" :: "r"(bar) : "memory");
 }
+__device__ __forceinline__ void bar_arrive(uint32_t bar, unsigned count)
+{
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0], %1;\n\t}" :: "r"(bar), "r"(count) : "memory");
+}
 __device__ __forceinline__ void bar_arrive_expect_tx(uint32_t bar, unsigned bytes)
 {
     asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}"
@@ -216,14 +220,21 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, unsigned parity)
                  : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
-// Gives up after some 2^31 cycles, a second or more (by the SM's clock: reading %globaltimer takes longer than most
-// waits here).
+// By a whole warp, every lane for itself: one lane's wait that the others are told of takes 330 cycles even where there
+// is nothing to wait for, this 40. Gives up after some 2^31 cycles, a second or more. LAZY: a wait that is
+// seldom short and may end some 100 cycles late; what it executes meanwhile is not taken from the scheduler's other warps.
+template <bool LAZY>
 __device__ __forceinline__ bool bar_wait(uint32_t bar, unsigned parity)
 {
     if (bar_try(bar, parity)) return true;
     const long long t0 = clock64();
+#pragma unroll 1
     while (true) {
-        if (bar_try(bar, parity)) return true;
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i) {
+            if (LAZY) __nanosleep(32);
+            if (bar_try(bar, parity)) return true;
+        }
         if (clock64() - t0 > (1ll << 31)) return false;
     }
 }
@@ -358,27 +369,30 @@ struct Tree {
         }
     };
 
+    template <bool LAZY = false>
     __device__ __forceinline__ bool wait(uint32_t bar, unsigned parity)
     {
-        if (bar_wait(bar, parity)) return true;
+        if (bar_wait<LAZY>(bar, parity)) return true;
         flags()[1] = 1;
         atomicOr(a.err, kErrPipelineTimeout);
         return false;
     }
     // All warps of the softmax; gives up like every wait.
     unsigned meetings = 0;
-    __device__ __forceinline__ bool group_sync()
+    __device__ __forceinline__ bool group_sync(bool lazy = false)
     {
         __syncwarp();
         if ((threadIdx.x & 31) == 0) bar_arrive(met());
-        return wait_warp(met(), meetings++ & 1);
+        const unsigned parity = meetings++ & 1;
+        return lazy ? wait_warp<true>(met(), parity) : wait_warp(met(), parity);
     }
-    // by a whole warp: one lane asks
+    // by a whole warp
+    template <bool LAZY = false>
     __device__ __forceinline__ bool wait_warp(uint32_t bar, unsigned parity)
     {
-        int ok = 1;
-        if ((threadIdx.x & 31) == 0) ok = wait(bar, parity);
-        return __shfl_sync(0xffffffffu, ok, 0) != 0;
+        const bool ok = wait<LAZY>(bar, parity);
+        __syncwarp();
+        return ok;
     }
 
     __device__ __forceinline__ TileInfo *tile_info(unsigned count) { return reinterpret_cast<TileInfo *>(smem + C::OFF_DESC) + (count & (kTreeDesc - 1)); }
@@ -528,7 +542,7 @@ struct Tree {
                 const int count = min(C::TPG, T - t0);
 #pragma unroll 1
                 for (int i = 0; i < count; ++i) {
-                    if (!wait_warp(CONV ? raw(V, ring.at) : empty(V, ring.at), ring.phase)) return;
+                    if (!wait_warp<true>(CONV ? raw(V, ring.at) : empty(V, ring.at), ring.phase)) return;
                     const unsigned mine = slices >> (i * C::NSLC) & TILE_BITS;
                     if (lt == i) {                             // a lane for each box
                         if (there && leads) {
@@ -580,19 +594,18 @@ struct Tree {
     __device__ __forceinline__ bool convert(Ring &rr, Ring &sr, int tid)
     {
         constexpr int N = NU;
-        const int r = tid / UPR, u = tid % UPR, c = u >> 2, v = (u & 3) * 2;
-        if (!wait_warp(full(V, rr.at), rr.phase)) return false;
+        // lanes of odd chunks take the next row of a pair: their units fall into other banks than those of the even ones
+        const int u = tid % UPR, c = u >> 2, v = (u & 3) * 2, r = tid / UPR ^ (c & 1);
+        if (!wait_warp<true>(full(V, rr.at), rr.phase)) return false;
         uint32_t src = raw_slot(V, rr.at);
         if constexpr (C::RCHB == 128) src += (u >> 3) * (TR * 128) + r * 128 + ((u ^ r) & 7) * 16;
         else src += r * 64 + (((u ^ (r >> 1)) & 3) << 4);
         uint4 x[N];
 #pragma unroll
         for (int k = 0; k < N; ++k) x[k] = lds128(src + k * RSTEP * C::RCHB);
-        if (!wait_warp(empty(V, sr.at), sr.phase)) return false;
-        // lanes of odd chunks write their second unit first: other banks than the even ones
-        const bool odd = c & 1;
+        if (!wait_warp<true>(empty(V, sr.at), sr.phase)) return false;
         const uint32_t dst = (V ? v_slot(sr.at) : k_slot(sr.at)) + c * (TR * 128) + r * 128;
-        const uint32_t dst0 = dst + (((v + odd) ^ (r & 7)) << 4), dst1 = dst + (((v + !odd) ^ (r & 7)) << 4);
+        const uint32_t dst0 = dst + ((v ^ (r & 7)) << 4), dst1 = dst + (((v + 1) ^ (r & 7)) << 4);
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             uint4 y0, y1;
@@ -600,8 +613,8 @@ struct Tree {
             e4m3x4_to_half4(x[k].y, y0.z, y0.w);
             e4m3x4_to_half4(x[k].z, y1.x, y1.y);
             e4m3x4_to_half4(x[k].w, y1.z, y1.w);
-            sts128(dst0 + k * RSTEP * 128, odd ? y1 : y0);
-            sts128(dst1 + k * RSTEP * 128, odd ? y0 : y1);
+            sts128(dst0 + k * RSTEP * 128, y0);
+            sts128(dst1 + k * RSTEP * 128, y1);
         }
         return true;
     }
@@ -628,7 +641,7 @@ struct Tree {
             p = segment(p, end, g);
             const int T = g.t1 - g.t0;
             // K as far before V as S is before P V
-            const int ahead = g.pair ? 0 : C::NB - 1;
+            const int ahead = g.pair ? 0 : C::NB - 2;
             for (int t = 0; C::KCONV && t < min(ahead, T); ++t)
                 if (!key()) return;
 #pragma unroll 1
@@ -637,7 +650,7 @@ struct Tree {
                 if constexpr (C::E8) {
                     if (!convert<true>(vr, vs, tid)) return;
                 } else {
-                    if (!wait_warp(full(true, vs.at), vs.phase)) return;
+                    if (!wait_warp<true>(full(true, vs.at), vs.phase)) return;
                 }
                 if (!wait_warp(described(tiles), tiles / kTreeDesc & 1)) return;
                 TileInfo *d = tile_info(tiles);
@@ -646,7 +659,7 @@ struct Tree {
                     const int u = tid % UPR * 2;
                     const uint32_t to = v_slot(vs.at) + (u >> 3) * (TR * 128);
 #pragma unroll 1
-                    for (int r = tid / UPR; r < TR; r += RSTEP) {
+                    for (int r = tid / UPR ^ (u >> 3 & 1); r < TR; r += RSTEP) {
                         const uint32_t p0 = to + r * 128 + (((u ^ r) & 7) << 4), p1 = to + r * 128 + ((((u + 1) ^ r) & 7) << 4);
                         uint4 y0 = lds128(p0), y1 = lds128(p1);
                         if (clean(d, r, y0, y1)) {
@@ -745,11 +758,12 @@ struct Tree {
         for (int p = from; p < end;) {
             TreeSeg g;
             p = segment(p, end, g);
-            if (!wait_warp(q_ready(), segs++ & 1)) return;
+            if (!wait_warp<true>(q_ready(), segs++ & 1)) return;
             const bool pair = __shfl_sync(0xffffffffu, g.pair, 0);
             const int T = __shfl_sync(0xffffffffu, g.t1 - g.t0, 0);
-            // S of a tile some tiles before P V of one: as many as there are S; of two warpgroups in turn, one
-            const int items = pair ? 2 * T : T, ahead = pair ? 1 : C::NB - 1;
+            // S of a tile one or two items before P V of one, so that the product which last read where it goes is not
+            // the one that was just issued (or, a pair's, is all the tensor cores have to do)
+            const int items = pair ? 2 * T : T, ahead = pair ? 1 : C::NB - 2;
 #pragma unroll 1
             for (int i = 0; i < items + ahead; ++i) {
                 if (i < items) {
@@ -1091,7 +1105,8 @@ struct Tree {
             const uint32_t o_at = tm + o_col(pair, w) + lanes;
             Row r;
             r.t = in_unit < g.slots ? div(a.by_group, slot) : -1;
-            const bool any = qt * 128 + quad * 32 < g.slots;   // some slot in this warp
+            const bool any = qt * 128 + quad * 32 < g.slots;   // some slot in this warp; warps of its group without one
+            const int idle = 4 - (min(g.slots - qt * 128, 128) + 31) / 32;
             r.h = hk() * a.group + (r.t >= 0 ? slot - r.t * a.group : 0);
             r.x = g.base + depth_of(g, max(r.t, 0));
             r.c = stage_q(g, r, w, quad, lane) * a.qscale;
@@ -1112,7 +1127,7 @@ struct Tree {
             const float rc = rcp(r.c);
             float m = -INFINITY, l = 0.f;
 #pragma unroll 1
-            for (int t = pair ? 0 : w; t < T; t += pair ? 1 : 2) {
+            for (int t = pair ? 0 : w; any && t < T; t += pair ? 1 : 2) {
                 const int b = Uses::buffer(pair, w, t);
                 const uint32_t s_at = tm + s_col(pair, b) + lanes;
                 const volatile TileInfo *d = tile_info(tiles + t);
@@ -1207,15 +1222,15 @@ struct Tree {
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(p_ready(b));
+                if (lane == 0) bar_arrive(p_ready(b), quad ? 1 : 1 + idle);   // for the warps without a slot too
             }
             // every product of the segment is done
             {
                 // (A barrier's parity tells a phase from the one before only: the warpgroup without the last tile may not
                 // know yet that the last tile's S was free for it.)
                 const int last = T - 1, over = last - C::NB;
-                if (!pair && over >= 0 && !dead) dead = !wait_warp(o_done(Uses::buffer(pair, w, over)), uses.parity(pair, w, over));
-                if (!dead) dead = !wait_warp(o_done(Uses::buffer(pair, w, last)), uses.parity(pair, w, last));
+                if (!pair && over >= 0 && !dead && any) dead = !wait_warp(o_done(Uses::buffer(pair, w, over)), uses.parity(pair, w, over));
+                if (!dead && any) dead = !wait_warp(o_done(Uses::buffer(pair, w, last)), uses.parity(pair, w, last));
             }
             uses.end(pair, T);
             if (any && !pair) refs_odd ^= T & 1;
@@ -1297,7 +1312,7 @@ struct Tree {
                 tmem_wait_st();
             }
             tc_fence_before();
-            group_sync();
+            group_sync(!any);
             tc_fence_after();
             if (any) {
                 uint32_t om, ol;
@@ -1327,7 +1342,7 @@ struct Tree {
         }
         // the next segment's Q and zeros go over what the other warpgroup reads, and over what its products read
         tc_fence_before();
-        group_sync();
+        group_sync(!any);
         tc_fence_after();
     }
 };
