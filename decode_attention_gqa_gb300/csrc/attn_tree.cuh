@@ -64,8 +64,8 @@ struct TreeCfg {
     // of a block of few slots the first warps have rows, those of the first scheduler: the issuer and the producers are
     // with the others
     static constexpr int PROD_V = FIX + 5, MMA = FIX + 6, PROD_K = FIX + 7;
-    // whole warpgroups where registers move between them: 512 threads of 128, of which the softmax takes 176 each, the
-    // converting warps 80, the last four (two have nothing to do) 72 -- 64512 of the block's 65536
+    // whole warpgroups where registers move between them: 512 threads of 128, of which the softmax takes 184 each and
+    // the others 72: the block's 65536
     static constexpr int THREADS = (PROD_K + 1) * 32;
     // 8-bit K as it is (with q in 8-bit parts), or converted
     static constexpr bool F8 = E8 && PARTS == 1, KCONV = E8 && !F8;
@@ -160,34 +160,33 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32])
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ bool elect_one()
+__device__ __forceinline__ uint32_t elect_one()
 {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
+    return p;
 }
-// The same with e4m3 operands.
-__device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+// Products by a warp, of which the lane with `one` issues: no branch.
+template <bool F8>
+__device__ __forceinline__ void umma_ss(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+    if constexpr (F8)                                          // e4m3 operands
+        asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+                     "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+                     "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one) : "memory");
 }
-// D += A B with A in tensor memory; issued by one thread.
-__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc)
+// D += A B with A in tensor memory.
+__device__ __forceinline__ void umma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, 0, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 :: "r"(d), "r"(a), "l"(b), "r"(idesc) : "memory");
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.eq.u32 p, 0, 0;\n\tsetp.ne.b32 e, %4, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(one) : "memory");
 }
 
-__device__ __forceinline__ uint32_t e4m3x4_of(float a, float b, float c, float d)
-{
-    uint16_t x, y;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(x) : "f"(b), "f"(a));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(y) : "f"(d), "f"(c));
-    return (uint32_t)x | (uint32_t)y << 16;
-}
 __device__ __forceinline__ void sts128(uint32_t p, const uint4 &v)
 {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -201,10 +200,6 @@ __device__ __forceinline__ void bar_init(uint32_t bar, unsigned count)
 __device__ __forceinline__ void bar_arrive(uint32_t bar)
 {
     asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" :: "r"(bar) : "memory");
-}
-__device__ __forceinline__ void bar_arrive(uint32_t bar, unsigned count)
-{
-    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0], %1;\n\t}" :: "r"(bar), "r"(count) : "memory");
 }
 __device__ __forceinline__ void bar_arrive_expect_tx(uint32_t bar, unsigned bytes)
 {
@@ -220,27 +215,11 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, unsigned parity)
                  : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
-// By a whole warp, every lane for itself: one lane's wait that the others are told of takes 330 cycles even where there
-// is nothing to wait for, this 40. Gives up after some 2^31 cycles, a second or more. LAZY: a wait that is
-// seldom short and may end some 100 cycles late; what it executes meanwhile is not taken from the scheduler's other warps.
-template <bool LAZY>
-__device__ __forceinline__ bool bar_wait(uint32_t bar, unsigned parity)
+__device__ __forceinline__ void bar_commit(uint32_t one, uint32_t bar)
 {
-    if (bar_try(bar, parity)) return true;
-    const long long t0 = clock64();
-#pragma unroll 1
-    while (true) {
-#pragma unroll 1
-        for (int i = 0; i < 64; ++i) {
-            if (LAZY) __nanosleep(32);
-            if (bar_try(bar, parity)) return true;
-        }
-        if (clock64() - t0 > (1ll << 31)) return false;
-    }
-}
-__device__ __forceinline__ void bar_commit(uint32_t bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+                 :: "r"(bar), "r"(one) : "memory");
 }
 __device__ __forceinline__ void tree_tma(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z, int w, uint64_t policy)
 {
@@ -369,30 +348,44 @@ struct Tree {
         }
     };
 
+    // By a whole warp, every lane for itself: one lane's wait that the others are told of takes 330 cycles even where there
+    // is nothing to wait for, this 40. Gives up after some 2^31 cycles, a second or more; the abort flag then ends
+    // every wait of the block, no more tiles are asked for, and the warps run through what is left and write nothing: no
+    // branch around what follows, which would keep it out of the uniform registers. LAZY: a wait that is seldom short and may end some
+    // 100 cycles late; what it executes meanwhile is not taken from the scheduler's other warps.
     template <bool LAZY = false>
-    __device__ __forceinline__ bool wait(uint32_t bar, unsigned parity)
+    __device__ __forceinline__ void wait(uint32_t bar, unsigned parity)
     {
-        if (bar_wait<LAZY>(bar, parity)) return true;
-        flags()[1] = 1;
-        atomicOr(a.err, kErrPipelineTimeout);
-        return false;
+        if (!bar_try(bar, parity)) {
+            const long long t0 = clock64();
+#pragma unroll 1
+            while (true) {
+                bool done = false;
+#pragma unroll 1
+                for (int i = 0; i < 64 && !done; ++i) {
+                    if (LAZY) __nanosleep(32);
+                    done = bar_try(bar, parity);
+                }
+                if (done || flags()[1]) break;
+                if (clock64() - t0 > (1ll << 31)) {
+                    flags()[1] = 1;
+                    atomicOr(a.err, kErrPipelineTimeout);
+                    break;
+                }
+            }
+        }
+        __syncwarp();
     }
-    // All warps of the softmax; gives up like every wait.
+    __device__ __forceinline__ bool ended() const { return __any_sync(0xffffffffu, flags()[1]); }
+    // All warps of the softmax
     unsigned meetings = 0;
-    __device__ __forceinline__ bool group_sync(bool lazy = false)
+    __device__ __forceinline__ void group_sync(bool lazy = false)
     {
         __syncwarp();
         if ((threadIdx.x & 31) == 0) bar_arrive(met());
         const unsigned parity = meetings++ & 1;
-        return lazy ? wait_warp<true>(met(), parity) : wait_warp(met(), parity);
-    }
-    // by a whole warp
-    template <bool LAZY = false>
-    __device__ __forceinline__ bool wait_warp(uint32_t bar, unsigned parity)
-    {
-        const bool ok = wait<LAZY>(bar, parity);
-        __syncwarp();
-        return ok;
+        if (lazy) wait<true>(met(), parity);
+        else wait(met(), parity);
     }
 
     __device__ __forceinline__ TileInfo *tile_info(unsigned count) { return reinterpret_cast<TileInfo *>(smem + C::OFF_DESC) + (count & (kTreeDesc - 1)); }
@@ -542,7 +535,8 @@ struct Tree {
                 const int count = min(C::TPG, T - t0);
 #pragma unroll 1
                 for (int i = 0; i < count; ++i) {
-                    if (!wait_warp<true>(CONV ? raw(V, ring.at) : empty(V, ring.at), ring.phase)) return;
+                    wait<true>(CONV ? raw(V, ring.at) : empty(V, ring.at), ring.phase);
+                    if (ended()) return;
                     const unsigned mine = slices >> (i * C::NSLC) & TILE_BITS;
                     if (lt == i) {                             // a lane for each box
                         if (there && leads) {
@@ -591,19 +585,19 @@ struct Tree {
     // is the same for all; their loads go out before the first conversion.
     static constexpr int UPR = HD / 16, RSTEP = 128 / UPR, NU = TR / RSTEP;
     template <bool V>
-    __device__ __forceinline__ bool convert(Ring &rr, Ring &sr, int tid)
+    __device__ __forceinline__ void convert(Ring &rr, Ring &sr, int tid)
     {
         constexpr int N = NU;
         // lanes of odd chunks take the next row of a pair: their units fall into other banks than those of the even ones
         const int u = tid % UPR, c = u >> 2, v = (u & 3) * 2, r = tid / UPR ^ (c & 1);
-        if (!wait_warp<true>(full(V, rr.at), rr.phase)) return false;
+        wait<true>(full(V, rr.at), rr.phase);
         uint32_t src = raw_slot(V, rr.at);
         if constexpr (C::RCHB == 128) src += (u >> 3) * (TR * 128) + r * 128 + ((u ^ r) & 7) * 16;
         else src += r * 64 + (((u ^ (r >> 1)) & 3) << 4);
         uint4 x[N];
 #pragma unroll
         for (int k = 0; k < N; ++k) x[k] = lds128(src + k * RSTEP * C::RCHB);
-        if (!wait_warp<true>(empty(V, sr.at), sr.phase)) return false;
+        wait<true>(empty(V, sr.at), sr.phase);
         const uint32_t dst = (V ? v_slot(sr.at) : k_slot(sr.at)) + c * (TR * 128) + r * 128;
         const uint32_t dst0 = dst + ((v ^ (r & 7)) << 4), dst1 = dst + (((v + 1) ^ (r & 7)) << 4);
 #pragma unroll
@@ -616,7 +610,6 @@ struct Tree {
             sts128(dst0 + k * RSTEP * 128, y0);
             sts128(dst1 + k * RSTEP * 128, y1);
         }
-        return true;
     }
 
     __device__ __forceinline__ void fix(int from, int end, int tid)
@@ -625,7 +618,7 @@ struct Tree {
         Ring vr{0, 0}, vs{0, C::E8 ? 1u : 0u}, kr{0, 0}, ks{0, 1};
         unsigned tiles = 0;
         auto key = [&] {                                       // K of the next tile
-            if (!convert<false>(kr, ks, tid)) return false;
+            convert<false>(kr, ks, tid);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -634,25 +627,23 @@ struct Tree {
             }
             kr.next(a.nrk);
             ks.next(a.nk);
-            return true;
         };
         for (int p = from; p < end;) {
             TreeSeg g;
             p = segment(p, end, g);
             const int T = g.t1 - g.t0;
             // K as far before V as S is before P V
-            const int ahead = g.pair ? 0 : C::NB - 2;
-            for (int t = 0; C::KCONV && t < min(ahead, T); ++t)
-                if (!key()) return;
+            const int ahead = !C::KCONV || g.pair ? 0 : C::NB - 2;
 #pragma unroll 1
-            for (int t = 0; t < T; ++t, ++tiles) {
-                if (C::KCONV && t + ahead < T && !key()) return;
+            for (int t = -ahead; t < T; ++t) {
+                if (C::KCONV && t + ahead < T) key();
+                if (t < 0) continue;
                 if constexpr (C::E8) {
-                    if (!convert<true>(vr, vs, tid)) return;
+                    convert<true>(vr, vs, tid);
                 } else {
-                    if (!wait_warp<true>(full(true, vs.at), vs.phase)) return;
+                    wait<true>(full(true, vs.at), vs.phase);
                 }
-                if (!wait_warp(described(tiles), tiles / kTreeDesc & 1)) return;
+                wait(described(tiles), tiles / kTreeDesc & 1);
                 TileInfo *d = tile_info(tiles);
                 const bool look = static_cast<volatile TileInfo *>(d)->edge & 1;
                 if (look) {                                    // the units that this thread has written, where it has
@@ -676,6 +667,7 @@ struct Tree {
                 }
                 if (C::E8) vr.next(a.nrv);
                 vs.next(a.nv);
+                ++tiles;
             }
         }
     }
@@ -711,7 +703,7 @@ struct Tree {
     __device__ __forceinline__ void issue(uint32_t tm_any, int from, int end)
     {
         const uint32_t tm = __shfl_sync(0xffffffffu, tm_any, 0);
-        const bool one = elect_one();
+        const uint32_t one = elect_one();
         Ring kr{0, 0}, vr{0, 0};
         unsigned segs = 0;
         Uses uses;
@@ -726,39 +718,31 @@ struct Tree {
             const uint64_t k = k0 + (uint32_t)kr.at * (C::KSLOT >> 4);
             uint64_t q = q0 + (uint32_t)(qt * a.q_parts) * (C::QPART >> 4);
             tc_fence_after();
-            if (one) {
 #pragma unroll 1
-                for (int x = 0; x < a.q_parts; ++x) {
+            for (int x = 0; x < a.q_parts; ++x) {
 #pragma unroll
-                    for (int kk = 0; kk < KK; ++kk) {
-                        const uint64_t qa = q + ((kk >> 2) * 16384 + (kk & 3) * 32) / 16, kb = k + ((kk >> 2) * (TR * 128) + (kk & 3) * 32) / 16;
-                        if constexpr (C::F8) umma_f8(d, qa, kb, id_s, x + kk > 0);
-                        else umma_f16(d, qa, kb, id_s, x + kk > 0);
-                    }
-                    q += C::QPART >> 4;
-                }
-                bar_commit(s_full(b));
-                if (last) bar_commit(empty(false, kr.at));
+                for (int kk = 0; kk < KK; ++kk)
+                    umma_ss<C::F8>(one, d, q + ((kk >> 2) * 16384 + (kk & 3) * 32) / 16, k + ((kk >> 2) * (TR * 128) + (kk & 3) * 32) / 16,
+                                   id_s, x + kk > 0);
+                q += C::QPART >> 4;
             }
-            __syncwarp();
+            bar_commit(one, s_full(b));
+            if (last) bar_commit(one, empty(false, kr.at));
         };
         auto values = [&](uint32_t o, int b, uint32_t s, bool last) {
             const uint64_t v = v0 + (uint32_t)vr.at * (C::SLOT >> 4);
             tc_fence_after();
-            if (one) {
 #pragma unroll
-                for (int kk = 0; kk < TR / 16; ++kk)
+            for (int kk = 0; kk < TR / 16; ++kk)
 #pragma unroll
-                    for (int x = 0; x < PARTS; ++x) umma_f16_ts(o, s + 32 * (kk >> 1) + 16 * x + 8 * (kk & 1), v + kk * 128, id_o);
-                bar_commit(o_done(b));
-                if (last) bar_commit(empty(true, vr.at));
-            }
-            __syncwarp();
+                for (int x = 0; x < PARTS; ++x) umma_ts(one, o, s + 32 * (kk >> 1) + 16 * x + 8 * (kk & 1), v + kk * 128, id_o);
+            bar_commit(one, o_done(b));
+            if (last) bar_commit(one, empty(true, vr.at));
         };
         for (int p = from; p < end;) {
             TreeSeg g;
             p = segment(p, end, g);
-            if (!wait_warp<true>(q_ready(), segs++ & 1)) return;
+            wait<true>(q_ready(), segs++ & 1);
             const bool pair = __shfl_sync(0xffffffffu, g.pair, 0);
             const int T = __shfl_sync(0xffffffffu, g.t1 - g.t0, 0);
             // S of a tile one or two items before P V of one, so that the product which last read where it goes is not
@@ -768,10 +752,10 @@ struct Tree {
             for (int i = 0; i < items + ahead; ++i) {
                 if (i < items) {
                     const int w = pair ? i & 1 : 0, x = pair ? i >> 1 : i, b = Uses::buffer(pair, w, x);
-                    if (w == 0 && !wait_warp(C::KCONV ? ready(false, kr.at) : full(false, kr.at), kr.phase)) return;
+                    if (w == 0) wait(C::KCONV ? ready(false, kr.at) : full(false, kr.at), kr.phase);
                     // S goes over the P of a product that may still read it: products of other shapes need not end in order
                     const int over = x - (pair ? 1 : C::NB);
-                    if (over >= 0 && !wait_warp(o_done(b), uses.parity(pair, w, over))) return;
+                    if (over >= 0) wait(o_done(b), uses.parity(pair, w, over));
                     const bool last = !pair || w == 1;         // user of this K
                     scores(w, b, tm + s_col(pair, b), last);
                     if (last) kr.next(a.nk);
@@ -779,8 +763,8 @@ struct Tree {
                 const int j = i - ahead;
                 if (j >= 0) {
                     const int w = pair ? j & 1 : 0, x = pair ? j >> 1 : j, b = Uses::buffer(pair, w, x);
-                    if (!wait_warp(p_ready(b), uses.parity(pair, w, x))) return;
-                    if (w == 0 && !wait_warp(ready(true, vr.at), vr.phase)) return;
+                    wait(p_ready(b), uses.parity(pair, w, x));
+                    if (w == 0) wait(ready(true, vr.at), vr.phase);
                     const bool last = !pair || w == 1;
                     values(tm + o_col(pair, w), b, tm + s_col(pair, b), last);
                     if (last) vr.next(a.nv);
@@ -1091,7 +1075,6 @@ struct Tree {
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const int my = quad * 32 + lane;
         volatile float *refs = reinterpret_cast<volatile float *>(smem + C::OFF_REF);
-        bool dead = false;
         unsigned tiles = 0, refs_odd = 0;                      // tiles before the segment; parity of the references handed on
         Uses uses;
         const bool rules = a.softcap > 0.f || a.slopes != nullptr || a.qscale <= 0.f;
@@ -1131,10 +1114,11 @@ struct Tree {
                 const int b = Uses::buffer(pair, w, t);
                 const uint32_t s_at = tm + s_col(pair, b) + lanes;
                 const volatile TileInfo *d = tile_info(tiles + t);
-                if (!dead) dead = !wait_warp(s_full(b), uses.parity(pair, w, t));
-                if (any && !dead) {
+                wait(s_full(b), uses.parity(pair, w, t));
+                {
                     tc_fence_after();
-                    const bool slow = d->edge || rules;
+                    const int edge = __shfl_sync(0xffffffffu, d->edge, 0);
+                    const bool slow = edge || rules;
                     float mx = -INFINITY;
                     if (slow) {
 #pragma unroll 1
@@ -1168,7 +1152,7 @@ struct Tree {
                     // the reference: that of the tile before, or a new one
                     const float own = m;
                     if (!pair && t > 0) {
-                        dead = !wait_warp(ref_known(quad), (refs_odd ^ (t - 1)) & 1);
+                        wait(ref_known(quad), (refs_odd ^ (t - 1)) & 1);
                         m = refs[my];
                     }
                     const bool need = mx > m + TAU;
@@ -1179,14 +1163,13 @@ struct Tree {
                         __syncwarp();
                         if (lane == 0) bar_arrive(ref_known(quad));
                     }
-                    const bool bad = (d->edge & 1) && (d->bad[0] | d->bad[1] | d->bad[2] | d->bad[3]) != 0u;
+                    const bool bad = (edge & 1) && __any_sync(0xffffffffu, d->bad[0] | d->bad[1] | d->bad[2] | d->bad[3]) && !ended();
                     if (__any_sync(0xffffffffu, need) || bad) {
                         // O stands still from the product before (of a pair's warpgroup: issued before this S) to this one
-                        if (!pair && t > 0 && !dead)
-                            dead = !wait_warp(o_done(Uses::buffer(pair, w, t - 1)), uses.parity(pair, w, t - 1));
+                        if (!pair && t > 0) wait(o_done(Uses::buffer(pair, w, t - 1)), uses.parity(pair, w, t - 1));
                         tc_fence_after();
-                        if (!dead && __any_sync(0xffffffffu, need)) scale_o(o_at, need ? ex2(before - m) : 1.f);   // 0 from -inf
-                        if (!dead && bad) add_bad(g, d, s_at, o_at, m == -INFINITY ? 0.f : m - OFF);
+                        if (__any_sync(0xffffffffu, need)) scale_o(o_at, need ? ex2(before - m) : 1.f);   // 0 from -inf
+                        if (bad) add_bad(g, d, s_at, o_at, m == -INFINITY ? 0.f : m - OFF);
                     }
                     if (own != m) l *= ex2(own - m);
                     const float ref = m == -INFINITY ? 0.f : m - OFF;
@@ -1222,20 +1205,20 @@ struct Tree {
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(p_ready(b), quad ? 1 : 1 + idle);   // for the warps without a slot too
+                if (lane <= (quad ? 0 : idle)) bar_arrive(p_ready(b));   // for the warps without a slot too
             }
             // every product of the segment is done
             {
                 // (A barrier's parity tells a phase from the one before only: the warpgroup without the last tile may not
                 // know yet that the last tile's S was free for it.)
                 const int last = T - 1, over = last - C::NB;
-                if (!pair && over >= 0 && !dead && any) dead = !wait_warp(o_done(Uses::buffer(pair, w, over)), uses.parity(pair, w, over));
-                if (!dead && any) dead = !wait_warp(o_done(Uses::buffer(pair, w, last)), uses.parity(pair, w, last));
+                if (!pair && over >= 0 && any) wait(o_done(Uses::buffer(pair, w, over)), uses.parity(pair, w, over));
+                if (any) wait(o_done(Uses::buffer(pair, w, last)), uses.parity(pair, w, last));
             }
             uses.end(pair, T);
             if (any && !pair) refs_odd ^= T & 1;
             // a slot whose every score is NaN keeps its NaN sum
-            finish(tm, g, r, w, quad, lane, whole, begins, rank, m == -INFINITY && l != 0.f ? 0.f : m - OFF, l, any, dead);
+            finish(tm, g, r, w, quad, lane, whole, begins, rank, m == -INFINITY && l != 0.f ? 0.f : m - OFF, l, any);
             tiles += T;
             p = next;
         }
@@ -1270,7 +1253,7 @@ struct Tree {
     // The end of a segment: the output, or the block's part of it. Warpgroups in turn share O, and write half of its dimensions
     // each.
     __device__ __forceinline__ void finish(uint32_t tm, const TreeSeg &g, const Row &r, int w, int quad, int lane, bool whole,
-                                           bool begins, int rank, float m, float l, bool any, bool dead)
+                                           bool begins, int rank, float m, float l, bool any)
     {
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         tc_fence_after();
@@ -1324,7 +1307,7 @@ struct Tree {
             d0 = w * (HD / 2);
             d1 = d0 + HD / 2;
         }
-        if (any && !dead) {
+        if (any && !ended()) {
             if (!whole && r.t >= 0 && d0 == 0) a.ws_ml[block + in_unit] = make_float2(m, l);
             if (whole) f = l == 0.f ? 0.f : rcp(l);
             const uint32_t o = tm + o_col(g.pair, w) + lanes;
@@ -1393,9 +1376,8 @@ attn_tree_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     const int64_t first = (int64_t)rank * share;
     const int from = (int)min(first, (int64_t)total), end = (int)min(first + share, (int64_t)total);
     {
-        if (warp < C::SM_WARPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
-        else if (warp < C::FIX + 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (warp < C::SM_WARPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     }
     if (warp < C::SM_WARPS) {
         x.softmax(tm, from, end, warp >> 2, warp & 3, lane, rank);
