@@ -32,7 +32,7 @@
 //
 // Warps: 8 of the softmax; 4 that convert e4m3 tiles to f16, and, in tiles that some slot does not see all
 // of, take infinities and NaN out of V (a weight of 0 would spread them); a producer of K and one of V (pages, TMA); an
-// issuer. What a single warp does for each tile takes some 8 cycles an instruction, and code that runs once is
+// issuer of each product. What a single warp does for each tile takes some 8 cycles an instruction, and code that runs once is
 // fetched from L2 a line at a time: both are written for few instructions.
 #pragma once
 
@@ -61,11 +61,10 @@ struct TreeCfg {
     static constexpr int NSLC = TR / 16;                       // 16-row slices
     static constexpr int TPG = 32 / NSLC;                      // tiles whose pages a warp looks up at once
     static constexpr int SM_WARPS = 8, FIX = SM_WARPS;
-    // of a block of few slots the first warps have rows, those of the first scheduler: the issuer and the producers are
-    // with the others
-    static constexpr int PROD_V = FIX + 5, MMA = FIX + 6, PROD_K = FIX + 7;
-    // whole warpgroups where registers move between them: 512 threads of 128, of which the softmax takes 184 each and
-    // the others 72: the block's 65536
+    // of a block of few slots the first warps have rows, those of the first scheduler: the issuers are with the others
+    static constexpr int PROD_V = FIX + 4, MMA_O = FIX + 5, MMA_S = FIX + 6, PROD_K = FIX + 7;
+    // whole warpgroups where registers move between them: 512 threads of 128, of which the softmax takes 176 each and
+    // the others 80: the block's 65536
     static constexpr int THREADS = (PROD_K + 1) * 32;
     // 8-bit K as it is (with q in 8-bit parts), or converted
     static constexpr bool F8 = E8 && PARTS == 1, KCONV = E8 && !F8;
@@ -138,6 +137,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t *r)
                  :: "r"(t), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
                     "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
                  : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t t, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "r"(t), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
 }
 __device__ __forceinline__ void tmem_st2(uint32_t t, uint32_t a, uint32_t b)
 {
@@ -632,8 +636,8 @@ struct Tree {
             TreeSeg g;
             p = segment(p, end, g);
             const int T = g.t1 - g.t0;
-            // K as far before V as S is before P V
-            const int ahead = !C::KCONV || g.pair ? 0 : C::NB - 2;
+            // K as far before V as S may be before P V
+            const int ahead = !C::KCONV || g.pair ? 0 : C::NB - 1;
 #pragma unroll 1
             for (int t = -ahead; t < T; ++t) {
                 if (C::KCONV && t + ahead < T) key();
@@ -697,80 +701,90 @@ struct Tree {
     }
 
     // -----------------------------------------------------------------------
-    // Issuer: a warp, so that what is the same in all lanes (descriptors, addresses) stays in uniform registers; one lane
-    // issues.
+    // Issuers, one of S = Q K^T and one of O += P V: warps, so that what is the same in all lanes (descriptors, addresses)
+    // stays in uniform registers; one lane issues. (One warp for both was what the tensor cores waited for:
+    // 2000 cycles a tile, half of them for barriers.)
     // -----------------------------------------------------------------------
-    __device__ __forceinline__ void issue(uint32_t tm_any, int from, int end)
+    __device__ __forceinline__ void issue_s(uint32_t tm_any, int from, int end)
     {
         const uint32_t tm = __shfl_sync(0xffffffffu, tm_any, 0);
         const uint32_t one = elect_one();
-        Ring kr{0, 0}, vr{0, 0};
-        unsigned segs = 0;
-        Uses uses;
+        Ring kr{0, 0};
+        unsigned segs = 0, used = 0;                           // used: bit b, whether S number b was used an odd number of times
         constexpr uint32_t id_s = C::F8 ? 1u << 4 | (uint32_t)(TR >> 3) << 17 | 8u << 24 : umma_idesc<MT>(128, TR, 0, 0);
-        constexpr uint32_t id_o = umma_idesc<MT>(128, HD, 0, 1);
         // rows of 128 bytes (swizzle 2, 8 rows 1024 bytes apart) or 64 (8-bit, head_dim 64: 4, 512)
         constexpr uint32_t SW = C::F8 && HD == 64 ? 4 : 2, SBO = SW == 4 ? 512 : 1024;
         constexpr int KK = C::F8 ? HD / 32 : HD / 16;          // steps of 32 bytes of a row
         const uint64_t q0 = umma_desc(sm, 16, SBO, SW), k0 = umma_desc(k_slot(0), 16, SBO, SW);
-        const uint64_t v0 = umma_desc(v_slot(0), TR * 128, 1024, 2);
-        auto scores = [&](int qt, int b, uint32_t d, bool last) {
-            const uint64_t k = k0 + (uint32_t)kr.at * (C::KSLOT >> 4);
-            uint64_t q = q0 + (uint32_t)(qt * a.q_parts) * (C::QPART >> 4);
-            tc_fence_after();
-#pragma unroll 1
-            for (int x = 0; x < a.q_parts; ++x) {
-#pragma unroll
-                for (int kk = 0; kk < KK; ++kk)
-                    umma_ss<C::F8>(one, d, q + ((kk >> 2) * 16384 + (kk & 3) * 32) / 16, k + ((kk >> 2) * (TR * 128) + (kk & 3) * 32) / 16,
-                                   id_s, x + kk > 0);
-                q += C::QPART >> 4;
-            }
-            bar_commit(one, s_full(b));
-            if (last) bar_commit(one, empty(false, kr.at));
-        };
-        auto values = [&](uint32_t o, int b, uint32_t s, bool last) {
-            const uint64_t v = v0 + (uint32_t)vr.at * (C::SLOT >> 4);
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < TR / 16; ++kk)
-#pragma unroll
-                for (int x = 0; x < PARTS; ++x) umma_ts(one, o, s + 32 * (kk >> 1) + 16 * x + 8 * (kk & 1), v + kk * 128, id_o);
-            bar_commit(one, o_done(b));
-            if (last) bar_commit(one, empty(true, vr.at));
-        };
         for (int p = from; p < end;) {
             TreeSeg g;
             p = segment(p, end, g);
-            wait<true>(q_ready(), segs++ & 1);
             const bool pair = __shfl_sync(0xffffffffu, g.pair, 0);
-            const int T = __shfl_sync(0xffffffffu, g.t1 - g.t0, 0);
-            // S of a tile one or two items before P V of one, so that the product which last read where it goes is not
-            // the one that was just issued (or, a pair's, is all the tensor cores have to do)
-            const int items = pair ? 2 * T : T, ahead = pair ? 1 : C::NB - 2;
+            const int T = __shfl_sync(0xffffffffu, g.t1 - g.t0, 0), users = pair ? 2 : 1;
+            wait<true>(q_ready(), segs++ & 1);
+            int b = 0;
 #pragma unroll 1
-            for (int i = 0; i < items + ahead; ++i) {
-                if (i < items) {
-                    const int w = pair ? i & 1 : 0, x = pair ? i >> 1 : i, b = Uses::buffer(pair, w, x);
-                    if (w == 0) wait(C::KCONV ? ready(false, kr.at) : full(false, kr.at), kr.phase);
-                    // S goes over the P of a product that may still read it: products of other shapes need not end in order
-                    const int over = x - (pair ? 1 : C::NB);
-                    if (over >= 0) wait(o_done(b), uses.parity(pair, w, over));
-                    const bool last = !pair || w == 1;         // user of this K
-                    scores(w, b, tm + s_col(pair, b), last);
-                    if (last) kr.next(a.nk);
+            for (int t = 0; t < T; ++t) {
+                wait(C::KCONV ? ready(false, kr.at) : full(false, kr.at), kr.phase);
+                const uint64_t k = k0 + (uint32_t)kr.at * (C::KSLOT >> 4);
+#pragma unroll 1
+                for (int w = 0; w < users; ++w) {
+                    // S goes over the P of a product that may still read it
+                    wait(o_done(b), ~used >> b & 1);
+                    used ^= 1u << b;
+                    tc_fence_after();
+                    const uint32_t d = tm + s_col(pair, b);
+                    uint64_t q = q0 + (uint32_t)(w * a.q_parts) * (C::QPART >> 4);
+#pragma unroll 1
+                    for (int x = 0; x < a.q_parts; ++x) {
+#pragma unroll
+                        for (int kk = 0; kk < KK; ++kk)
+                            umma_ss<C::F8>(one, d, q + ((kk >> 2) * 16384 + (kk & 3) * 32) / 16,
+                                           k + ((kk >> 2) * (TR * 128) + (kk & 3) * 32) / 16, id_s, x + kk > 0);
+                        q += C::QPART >> 4;
+                    }
+                    bar_commit(one, s_full(b));
+                    if (++b == (pair ? 2 : C::NB)) b = 0;
                 }
-                const int j = i - ahead;
-                if (j >= 0) {
-                    const int w = pair ? j & 1 : 0, x = pair ? j >> 1 : j, b = Uses::buffer(pair, w, x);
-                    wait(p_ready(b), uses.parity(pair, w, x));
-                    if (w == 0) wait(ready(true, vr.at), vr.phase);
-                    const bool last = !pair || w == 1;
-                    values(tm + o_col(pair, w), b, tm + s_col(pair, b), last);
-                    if (last) vr.next(a.nv);
-                }
+                bar_commit(one, empty(false, kr.at));
+                kr.next(a.nk);
             }
-            uses.end(pair, T);
+        }
+    }
+    __device__ __forceinline__ void issue_o(uint32_t tm_any, int from, int end)
+    {
+        const uint32_t tm = __shfl_sync(0xffffffffu, tm_any, 0);
+        const uint32_t one = elect_one();
+        Ring vr{0, 0};
+        unsigned used = 0;
+        constexpr uint32_t id_o = umma_idesc<MT>(128, HD, 0, 1);
+        const uint64_t v0 = umma_desc(v_slot(0), TR * 128, 1024, 2);
+        for (int p = from; p < end;) {
+            TreeSeg g;
+            p = segment(p, end, g);
+            const bool pair = __shfl_sync(0xffffffffu, g.pair, 0);
+            const int T = __shfl_sync(0xffffffffu, g.t1 - g.t0, 0), users = pair ? 2 : 1;
+            int b = 0;
+#pragma unroll 1
+            for (int t = 0; t < T; ++t) {
+                wait(ready(true, vr.at), vr.phase);
+                const uint64_t v = v0 + (uint32_t)vr.at * (C::SLOT >> 4);
+#pragma unroll 1
+                for (int w = 0; w < users; ++w) {
+                    wait(p_ready(b), used >> b & 1);
+                    used ^= 1u << b;
+                    tc_fence_after();
+                    const uint32_t s = tm + s_col(pair, b), o = tm + o_col(pair, w);
+#pragma unroll
+                    for (int kk = 0; kk < TR / 16; ++kk)
+#pragma unroll
+                        for (int x = 0; x < PARTS; ++x) umma_ts(one, o, s + 32 * (kk >> 1) + 16 * x + 8 * (kk & 1), v + kk * 128, id_o);
+                    bar_commit(one, o_done(b));
+                    if (++b == (pair ? 2 : C::NB)) b = 0;
+                }
+                bar_commit(one, empty(true, vr.at));
+                vr.next(a.nv);
+            }
         }
     }
 
@@ -1036,7 +1050,9 @@ struct Tree {
     // Rows of V that hold infinities or NaN: to the slots that see them, in the dimensions that do.
     __device__ __forceinline__ void add_bad(const TreeSeg &g, const volatile TileInfo *d, uint32_t s_at, uint32_t o, float ref)
     {
-        for (int w = 0; w < (TR + 31) / 32; ++w)
+#pragma unroll 1
+        for (int w = 0; w < TR / 32; ++w)
+#pragma unroll 1
             for (unsigned m = d->bad[w]; m; m &= m - 1) {
                 const int r = w * 32 + __ffs(m) - 1, j = d->row0 + r, pg = div(a.by_page, j);
                 const int page = ld_dep(a.table + (size_t)g.s * a.max_pages + pg);
@@ -1046,6 +1062,7 @@ struct Tree {
                 if (r & 1) sv = dummy;
                 const float s = __uint_as_float(sv), p = ex2(s - ref);
                 const bool sees = s != -INFINITY;
+#pragma unroll 1
                 for (int c = 0; c < HD; c += 32) {
                     uint32_t v[32];
                     tmem_ld32(o + c, v);
@@ -1195,9 +1212,12 @@ struct Tree {
                                     h[PARTS - 1][i] = float2_to_kv2<MT>(q.x - y.x, q.y - y.y);
                                 }
                             }
+                            if (PARTS == 2) {                  // in turn: all of both parts do not fit into the registers
+                                tmem_st8(s_at + c + 8 * x, h[0] + 8 * x);
+                                tmem_st8(s_at + c + 16 + 8 * x, h[PARTS - 1] + 8 * x);
+                            }
                         }
-#pragma unroll
-                        for (int x = 0; x < PARTS; ++x) tmem_st16(s_at + c + 16 * x, h[x]);
+                        if (PARTS == 1) tmem_st16(s_at + c, h[0]);
                     });
                     const float2 both = unpack2(sum);
                     l += both.x + both.y;
@@ -1364,7 +1384,7 @@ attn_tree_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                     make_int4(x.before()[s], x.before()[s + 1] - x.before()[s], x.tok()[s], x.flags()[2]);
         }
     } else {
-        if (warp == C::MMA) tmem_alloc(reinterpret_cast<uint32_t *>(const_cast<int *>(x.flags())), C::TM_COLS);
+        if (warp == C::MMA_S) tmem_alloc(reinterpret_cast<uint32_t *>(const_cast<int *>(x.flags())), C::TM_COLS);
         pdl_wait();
     }
     pdl_launch_dependents();
@@ -1376,8 +1396,8 @@ attn_tree_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     const int64_t first = (int64_t)rank * share;
     const int from = (int)min(first, (int64_t)total), end = (int)min(first + share, (int64_t)total);
     {
-        if (warp < C::SM_WARPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp < C::SM_WARPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     }
     if (warp < C::SM_WARPS) {
         x.softmax(tm, from, end, warp >> 2, warp & 3, lane, rank);
@@ -1387,8 +1407,10 @@ attn_tree_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         x.template produce<false>(&kmap, from, end, lane);
     } else if (warp == C::PROD_V) {
         x.template produce<true>(&vmap, from, end, lane);
-    } else if (warp == C::MMA) {
-        x.issue(tm, from, end);
+    } else if (warp == C::MMA_S) {
+        x.issue_s(tm, from, end);
+    } else if (warp == C::MMA_O) {
+        x.issue_o(tm, from, end);
     }
     __syncwarp();
     tc_fence_before();
@@ -1401,7 +1423,7 @@ attn_tree_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         __syncthreads();
     }
     tc_fence_after();
-    if (warp == C::MMA) tmem_dealloc(tm, C::TM_COLS);
+    if (warp == C::MMA_S) tmem_dealloc(tm, C::TM_COLS);
 }
 
 // Units that several blocks have tiles of: o = sum w oc / sum w S over their parts, w = 2^(mx - max mx). A warp takes a
