@@ -3,7 +3,8 @@
 // Mathematics. For a node t at position x over the cache rows j it sees -- all before its tree, and the
 // tree's own as its mask has them --
 //     s_j = rules(scale q.k_j),  o = sum_j p_j v_j / sum_j p_j,  p_j = 2^(s_j log2 e - m),
-// one pass with a running reference m that moves when a score passes it by 8. An e4m3 cache holds codes
+// one pass with a running reference m, an integer, that moves when a score passes it by 8 (what was weighed
+// before is then multiplied by a power of two). An e4m3 cache holds codes
 // with one scale per page and KV head: the K scale multiplies a page's scores, the V scale p; the
 // reference follows s + log2 of the V scale (rounded up), so that p times the scale stays in the 16-bit
 // range whatever the scales are; sum p is f32.
@@ -265,6 +266,14 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t mul_kv2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    if constexpr (std::is_same<T, __half>::value) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
@@ -1047,8 +1056,9 @@ struct Tree {
         tmem_wait_st();
     }
 
-    // Rows of V that hold infinities or NaN: to the slots that see them, in the dimensions that do.
-    __device__ __forceinline__ void add_bad(const TreeSeg &g, const volatile TileInfo *d, uint32_t s_at, uint32_t o, float ref)
+    // Rows of V that hold infinities or NaN: to the slots that see them, in the dimensions that do. (A weight changes
+    // neither.)
+    __device__ __forceinline__ void add_bad(const TreeSeg &g, const volatile TileInfo *d, uint32_t s_at, uint32_t o)
     {
 #pragma unroll 1
         for (int w = 0; w < TR / 32; ++w)
@@ -1060,8 +1070,7 @@ struct Tree {
                 uint32_t sv, dummy;
                 tmem_ld2(s_at + (r & ~1), sv, dummy);
                 if (r & 1) sv = dummy;
-                const float s = __uint_as_float(sv), p = ex2(s - ref);
-                const bool sees = s != -INFINITY;
+                const bool sees = __uint_as_float(sv) != -INFINITY;
 #pragma unroll 1
                 for (int c = 0; c < HD; c += 32) {
                     uint32_t v[32];
@@ -1077,7 +1086,7 @@ struct Tree {
                         } else {
                             x = kv2_to_float2<MT>((uint32_t)static_cast<const uint16_t *>(a.v)[at + c + i]).x;
                         }
-                        if (sees && !(fabsf(x) < INFINITY)) v[i] = __float_as_uint(fmaf(p, x, __uint_as_float(v[i])));
+                        if (sees && !(fabsf(x) < INFINITY)) v[i] = __float_as_uint(x + __uint_as_float(v[i]));
                     }
                     __syncwarp();
                     tmem_st32(o + c, v);
@@ -1124,7 +1133,6 @@ struct Tree {
             __syncwarp();
             if (lane == 0) bar_arrive(q_ready());
 
-            const float rc = rcp(r.c);
             float m = -INFINITY, l = 0.f;
 #pragma unroll 1
             for (int t = pair ? 0 : w; any && t < T; t += pair ? 1 : 2) {
@@ -1132,96 +1140,103 @@ struct Tree {
                 const uint32_t s_at = tm + s_col(pair, b) + lanes;
                 const volatile TileInfo *d = tile_info(tiles + t);
                 wait(s_full(b), uses.parity(pair, w, t));
-                {
-                    tc_fence_after();
-                    const int edge = __shfl_sync(0xffffffffu, d->edge, 0);
-                    const bool slow = edge || rules;
-                    float mx = -INFINITY;
-                    if (slow) {
+                tc_fence_after();
+                const int edge = __shfl_sync(0xffffffffu, d->edge, 0);
+                const bool slow = edge || rules;
+                if (slow) {                                    // the rules first
 #pragma unroll 1
-                        for (int c = 0; c < TR; c += 32) {
-                            uint32_t v[32];
-                            tmem_ld32(s_at + c, v);
-                            tmem_wait_ld(v);
-                            ruled(g, r, d, c, v);
-                            __syncwarp();
-                            tmem_st32(s_at + c, v);
-                            float k0 = most16(v, 0), k1 = most16(v, 16);
-                            if (C::E8) {
-                                k0 += d->lv[c >> 4];
-                                k1 += d->lv[(c >> 4) + 1];
-                            }
-                            mx = fmaxf(mx, fmaxf(k0, k1));
-                        }
-                        tmem_wait_st();
-                    } else {
-                        auto most = [&](const uint32_t (&v)[32], int c) {
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                float k = most16(v, 16 * y);
-                                if (C::E8) k = fmaf(k, d->ks[(c >> 4) + y], d->lv[(c >> 4) + y] * rc);
-                                mx = fmaxf(mx, k);
-                            }
-                        };
-                        by_32(s_at, most);
-                        mx *= r.c;
-                    }
-                    // the reference: that of the tile before, or a new one
-                    const float own = m;
-                    if (!pair && t > 0) {
-                        wait(ref_known(quad), (refs_odd ^ (t - 1)) & 1);
-                        m = refs[my];
-                    }
-                    const bool need = mx > m + TAU;
-                    const float before = m;
-                    if (need) m = mx;
-                    if (!pair) {
-                        refs[my] = m;
+                    for (int c = 0; c < TR; c += 32) {
+                        uint32_t v[32];
+                        tmem_ld32(s_at + c, v);
+                        tmem_wait_ld(v);
+                        ruled(g, r, d, c, v);
                         __syncwarp();
-                        if (lane == 0) bar_arrive(ref_known(quad));
+                        tmem_st32(s_at + c, v);
                     }
-                    const bool bad = (edge & 1) && __any_sync(0xffffffffu, d->bad[0] | d->bad[1] | d->bad[2] | d->bad[3]) && !ended();
-                    if (__any_sync(0xffffffffu, need) || bad) {
+                    tmem_wait_st();
+                    if ((edge & 1) && __any_sync(0xffffffffu, d->bad[0] | d->bad[1] | d->bad[2] | d->bad[3]) && !ended()) {
                         // O stands still from the product before (of a pair's warpgroup: issued before this S) to this one
                         if (!pair && t > 0) wait(o_done(Uses::buffer(pair, w, t - 1)), uses.parity(pair, w, t - 1));
                         tc_fence_after();
-                        if (__any_sync(0xffffffffu, need)) scale_o(o_at, need ? ex2(before - m) : 1.f);   // 0 from -inf
-                        if (bad) add_bad(g, d, s_at, o_at, m == -INFINITY ? 0.f : m - OFF);
+                        add_bad(g, d, s_at, o_at);
                     }
-                    if (own != m) l *= ex2(own - m);
+                }
+                // P, by the reference as it is: that of the tile before may be larger by now, which is seen to at the end
+                const float before = m;
+                const float c = slow ? 1.f : r.c;
+                uint64_t sum[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[i] = pack2(0.f, 0.f);
+                auto gather = [&] {
+                    const float2 both = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+                    l += both.x + both.y;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sum[i] = pack2(0.f, 0.f);
+                };
+                uint32_t u[32], v[32];
+                tmem_ld32(s_at, u);
+                tmem_ld32(s_at + 32, v);
+#pragma unroll 1
+                for (int at = 0; at < TR; at += 64) {
+                    float f[4], vs[4], k[4];
+                    if constexpr (C::E8) {
+                        const uint32_t info = sm + C::OFF_DESC + ((tiles + t) & (kTreeDesc - 1)) * 128 + at / 4;
+                        const uint4 x = lds128(info + 32), y = lds128(info + 64), z = lds128(info + 96);
+                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w}, zs[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            f[i] = slow ? 1.f : c * __uint_as_float(xs[i]);
+                            vs[i] = __uint_as_float(ys[i]);
+                            k[i] = __uint_as_float(zs[i]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) f[i] = c, vs[i] = 1.f, k[i] = 0.f;
+                    }
+                    tmem_wait_ld(u);
+                    tmem_wait_ld(v);
+                    k[0] = fmaf(most16(u, 0), f[0], k[0]);
+                    k[1] = fmaf(most16(u, 16), f[1], k[1]);
+                    k[2] = fmaf(most16(v, 0), f[2], k[2]);
+                    k[3] = fmaf(most16(v, 16), f[3], k[3]);
+                    const float mx = fmaxf(fmaxf(k[0], k[1]), fmaxf(k[2], k[3]));
+                    if (__any_sync(0xffffffffu, mx > m + TAU)) {
+                        const float M = mx > m + TAU ? ceilf(mx) : m, fac = M == m ? 1.f : ex2(m - M);   // 0 from -inf
+                        gather();
+                        l *= fac;
+                        m = M;
+                        if (at) scale_p(s_at, at, fac);
+                    }
                     const float ref = m == -INFINITY ? 0.f : m - OFF;
                     const uint64_t nref = pack2(-ref, -ref);
-                    uint64_t sum = pack2(0.f, 0.f);
-                    by_32(s_at, [&](const uint32_t (&v)[32], int c) {
-                        uint32_t h[PARTS][16];
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const int at = (c >> 4) + x;
-                            const float f = slow ? 1.f : C::E8 ? r.c * d->ks[at] : r.c, vs = C::E8 ? d->vs[at] : 1.f;
-                            const uint64_t f2 = pack2(f, f), vs2 = pack2(vs, vs);
-#pragma unroll
-                            for (int i = 8 * x; i < 8 * x + 8; ++i) {
-                                const float2 s = unpack2(fma2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2, nref));
-                                uint64_t p = pack2(ex2(s.x), ex2(s.y));
-                                sum = add2(sum, p);
-                                if (C::E8) p = mul2(p, vs2);
-                                const float2 q = unpack2(p);
-                                h[0][i] = float2_to_kv2<MT>(q.x, q.y);
-                                if (PARTS == 2) {
-                                    const float2 y = kv2_to_float2<MT>(h[0][i]);
-                                    h[PARTS - 1][i] = float2_to_kv2<MT>(q.x - y.x, q.y - y.y);
-                                }
-                            }
-                            if (PARTS == 2) {                  // in turn: all of both parts do not fit into the registers
-                                tmem_st8(s_at + c + 8 * x, h[0] + 8 * x);
-                                tmem_st8(s_at + c + 16 + 8 * x, h[PARTS - 1] + 8 * x);
-                            }
-                        }
-                        if (PARTS == 1) tmem_st16(s_at + c, h[0]);
-                    });
-                    const float2 both = unpack2(sum);
-                    l += both.x + both.y;
-                    tmem_wait_st();
+                    weights(u, s_at + at, nref, f, vs, sum);
+                    if (at + 64 < TR) tmem_ld32(s_at + at + 64, u);
+                    weights(v, s_at + at + 32, nref, f + 2, vs + 2, sum);
+                    if (at + 64 < TR) tmem_ld32(s_at + at + 96, v);
+                }
+                gather();
+                tmem_wait_st();
+                // O and P by one reference, the larger
+                float mo = pair ? before : m;                  // O's
+                if (!pair && t > 0) {
+                    wait(ref_known(quad), (refs_odd ^ (t - 1)) & 1);
+                    mo = refs[my];
+                }
+                if (__any_sync(0xffffffffu, m != mo)) {
+                    const float M = fmaxf(m, mo), fac = m == M ? 1.f : ex2(m - M);
+                    if (__any_sync(0xffffffffu, m != M)) scale_p(s_at, TR, fac);
+                    l *= fac;
+                    if (__any_sync(0xffffffffu, mo != M)) {
+                        if (!pair) wait(o_done(Uses::buffer(pair, w, t - 1)), uses.parity(pair, w, t - 1));
+                        tc_fence_after();
+                        scale_o(o_at, mo == M ? 1.f : fmaxf(ex2(mo - M), 1.17549435e-38f));   // not 0: it may hold infinities
+                    }
+                    m = M;
+                }
+                if (!pair) {
+                    refs[my] = m;
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(ref_known(quad));
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -1243,24 +1258,50 @@ struct Tree {
             p = next;
         }
     }
-    // f(32 columns, the first one's number) for a tile's columns, the next 32 on their way meanwhile. Two copies of f, not
-    // one for each 32: code that does not stay in the schedulers' instruction caches, four roles of it, runs three times
-    // as long.
-    template <class F>
-    static __device__ __forceinline__ void by_32(uint32_t s_at, F f)
+    // 32 scores to weights, into the same columns; their sums.
+    static __device__ __forceinline__ void weights(const uint32_t (&v)[32], uint32_t at, uint64_t nref, const float *f, const float *vs,
+                                                   uint64_t (&sum)[4])
     {
-        uint32_t u[32], v[32];
-        tmem_ld32(s_at, u);
-        tmem_wait_ld(u);
-#pragma unroll 1
-        for (int c = 0; c < TR; c += 64) {
-            tmem_ld32(s_at + c + 32, v);
-            f(u, c);
-            tmem_wait_ld(v);
-            if (c + 64 < TR) tmem_ld32(s_at + c + 64, u);
-            f(v, c + 32);
-            tmem_wait_ld(u);
+        uint32_t h[PARTS][16];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const uint64_t f2 = pack2(f[x], f[x]), vs2 = pack2(vs[x], vs[x]);
+#pragma unroll
+            for (int i = 8 * x; i < 8 * x + 8; ++i) {
+                const float2 s = unpack2(fma2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2, nref));
+                uint64_t p = pack2(ex2(s.x), ex2(s.y));
+                sum[i & 3] = add2(sum[i & 3], p);
+                if (C::E8) p = mul2(p, vs2);
+                const float2 q = unpack2(p);
+                h[0][i] = float2_to_kv2<MT>(q.x, q.y);
+                if (PARTS == 2) {
+                    const float2 y = kv2_to_float2<MT>(h[0][i]);
+                    h[PARTS - 1][i] = float2_to_kv2<MT>(q.x - y.x, q.y - y.y);
+                }
+            }
+            if (PARTS == 2) {                                  // in turn: all of both parts do not fit into the registers
+                tmem_st8(at + 8 * x, h[0] + 8 * x);
+                tmem_st8(at + 16 + 8 * x, h[PARTS - 1] + 8 * x);
+            }
         }
+        if (PARTS == 1) tmem_st16(at, h[0]);
+    }
+    // The weights of the first n columns times f, a power of two; whole warps.
+    static __device__ __forceinline__ void scale_p(uint32_t s_at, int n, float f)
+    {
+        const uint32_t f2 = float2_to_kv2<MT>(f, f);
+        tmem_wait_st();
+#pragma unroll 1
+        for (int c = 0; c < n; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(s_at + c, v);
+            tmem_wait_ld(v);
+#pragma unroll
+            for (int i = 0; i < 16 * PARTS; ++i) v[i] = mul_kv2<MT>(v[i], f2);
+#pragma unroll
+            for (int x = 0; x < PARTS; ++x) tmem_st16(s_at + c + 16 * x, v + 16 * x);
+        }
+        tmem_wait_st();
     }
     static __device__ __forceinline__ float most16(const uint32_t (&v)[32], int at)
     {
