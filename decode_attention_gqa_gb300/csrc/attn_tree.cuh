@@ -646,7 +646,7 @@ struct Tree {
             p = segment(p, end, g);
             const int T = g.t1 - g.t0;
             // K as far before V as S may be before P V
-            const int ahead = !C::KCONV || g.pair ? 0 : C::NB - 1;
+            const int ahead = !C::KCONV || g.pair ? 0 : min(a.nk, C::NB) - 1;
 #pragma unroll 1
             for (int t = -ahead; t < T; ++t) {
                 if (C::KCONV && t + ahead < T) key();
@@ -832,17 +832,18 @@ struct Tree {
         const int qt = g.pair ? w : 0, my = quad * 32 + lane;
         const bool half = !g.pair;
         const bool f32 = a.q_type == kTypeF32, f16 = std::is_same<MT, __half>::value;
-        const int lg = (HD == 64 ? 3 : HD == 128 ? 4 : 5) + f32;      // log2 of a row's 16-byte units
-        const int row_bytes = 16 << lg, su = half ? 2 : 1;
-#pragma unroll 4
-        for (int it = half ? w : 0; it < 1 << lg; it += su) {
-            const int i = it * 32 + lane, row = i >> lg, u = i & ((1 << lg) - 1);
-            const int t = __shfl_sync(0xffffffffu, r.t, row), h = __shfl_sync(0xffffffffu, r.h, row);
+        const int lg = (HD == 64 ? 3 : HD == 128 ? 4 : 5) + f32, last = (1 << lg) - 1;   // log2 of a row's 16-byte units
+        const int su = half ? 2 : 1, rows = min(max(g.slots - qt * 128 - quad * 32, 0), 32);
+        const int mine_at = r.t * a.n_head + r.h;                     // after the sequence's first token
+        const uint8_t *src = static_cast<const uint8_t *>(a.q) + ((int64_t)g.tok0 * a.n_head << lg) * 16;
+#pragma unroll 1
+        for (int it = half ? w : 0; it * 32 < rows << lg; it += su) {
+            const int i = it * 32 + lane, row = i >> lg, u = i & last;
+            const int at = __shfl_sync(0xffffffffu, mine_at, row);
             const uint32_t to = f32 || C::F8 ? q_place(qt, quad * 32 + row, u & 1, u >> 1) : q_place(qt, quad * 32 + row, 0, u);
-            if (t >= 0)
+            if (row < rows)
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
-                             :: "r"(to), "l"(static_cast<const uint8_t *>(a.q) + ((int64_t)(g.tok0 + t) * a.n_head + h) * row_bytes + u * 16)
-                             : "memory");
+                             :: "r"(to), "l"(src + (((int64_t)at << lg) + u) * 16) : "memory");
         }
         asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
         if (half) group_sync();
@@ -1242,14 +1243,11 @@ struct Tree {
                 __syncwarp();
                 if (lane <= (quad ? 0 : idle)) bar_arrive(p_ready(b));   // for the warps without a slot too
             }
-            // every product of the segment is done
-            {
-                // (A barrier's parity tells a phase from the one before only: the warpgroup without the last tile may not
-                // know yet that the last tile's S was free for it.)
-                const int last = T - 1, over = last - C::NB;
-                if (!pair && over >= 0 && any) wait(o_done(Uses::buffer(pair, w, over)), uses.parity(pair, w, over));
-                if (any) wait(o_done(Uses::buffer(pair, w, last)), uses.parity(pair, w, last));
-            }
+            // Every product of the segment is done. A barrier's parity tells a phase from those next to it only, so each wait
+            // is for one that the warp knows to be the last or the one under way: the warpgroup's own last tile's first
+            // (the other's last tile may have used the same S as a product that is still under way, and may be done too).
+            if (any && !pair && T > 1) wait(o_done(Uses::buffer(pair, w, T - 2)), uses.parity(pair, w, T - 2));
+            if (any) wait(o_done(Uses::buffer(pair, w, T - 1)), uses.parity(pair, w, T - 1));
             uses.end(pair, T);
             if (any && !pair) refs_odd ^= T & 1;
             // a slot whose every score is NaN keeps its NaN sum
@@ -1583,8 +1581,9 @@ cudaError_t launch_tree_kernel(const TreeRequest &r)
         a.nk = few(raws / 2);
         a.nrv = few(raws - a.nk);
     } else if (C::E8) {
-        a.nk = a.nv = left >= 8 * C::SLOT ? 2 : 1;
-        a.nrk = a.nrv = few((int)((left - 2 * a.nk * C::SLOT) / (2 * C::RAW)));
+        a.nk = left >= 5 * C::SLOT ? 2 : 1;                           // K of a tile is converted before V of the one before
+        a.nv = left >= 8 * C::SLOT ? 2 : 1;
+        a.nrk = a.nrv = few((int)((left - (a.nk + a.nv) * C::SLOT) / (2 * C::RAW)));
         if (a.nk + a.nrk > 4) a.nrk = 4 - a.nk;
     } else {
         const int n = (int)(left / C::SLOT);
