@@ -176,10 +176,10 @@ struct TreeArgs {
     const int32_t *depths;    // of all tokens, or null
     const uint32_t *mask;     // [n_tokens][words] or null: chains
     const float *k_scale, *v_scale, *slopes;
-    // Parts: block (rank * 2 + which) * units + unit of unit_slots slots, `which` 1 where the sequence begins in this
+    // Parts: block (rank * 2 + which) * units + unit of kTreeSlots slots, `which` 1 where the sequence begins in this
     // rank's places
-    float *ws_o;              // [blocks][HD / 4][unit_slots][4]
-    float2 *ws_ml;            // [blocks][unit_slots]
+    float *ws_o;              // [blocks][HD / 4][kTreeSlots][4]
+    float2 *ws_ml;            // [blocks][kTreeSlots]
     int4 *ws_span;            // [units / n_kv_head][n_seq]: first place, tiles, first token, places of a rank
     unsigned *err;
     int64_t n_tokens, n_each; // n_each: nodes of a sequence when cu is null
@@ -188,9 +188,8 @@ struct TreeArgs {
     int max_nodes, words;
     int n_head, n_kv_head, group;
     int max_pages, n_pages, page_size, cap, window;
-    int units;                // n_kv_head times what max_nodes has of unit_slots
-    int ranks, min_share;     // blocks that share a unit's tiles; the least a block takes
-    int unit_slots;           // (node, head) pairs a block serves at once: 128 or 256
+    int units;                // n_kv_head times what max_nodes has of kTreeSlots
+    int ranks;                // blocks that share a unit's tiles
     int q_parts;              // parts of q
     uint32_t q_bytes;         // of Q in shared memory
     int nk, nv, nrk, nrv;     // tiles of the rings of K and V, and of their 8-bit tiles that are converted
@@ -210,6 +209,7 @@ struct TreeRequest {
     cudaStream_t stream;
 };
 constexpr int kTreeSeqs = 64;     // sequences one launch of the attention of trees takes
+constexpr int kTreeSlots = 128;         // (node, head) pairs of a KV head that a block serves
 constexpr int tree_tile(int head_dim) { return head_dim == 256 ? 64 : 128; }
 cudaError_t launch_tree_hd64_f16(const TreeRequest &r);
 cudaError_t launch_tree_hd64_bf16(const TreeRequest &r);

@@ -12,11 +12,11 @@
 // Tiles. A (node, head) pair of a KV head is a slot; 128 slots are the M rows of both products. S = Q K^T
 // (128 x TR, operands in shared memory) goes to tensor memory, a warpgroup turns it into P in place, one row a
 // thread, so that maxima and sums need no exchange, and O += P V takes P from tensor memory and V as an MN-major
-// operand from the tile TMA brought. Up to 128 slots, the two warpgroups take tiles in turn: three (four) S in tensor memory,
-// one O, and one reference that a tile's warpgroup hands on to the next one's as soon as it knows the tile's
-// maxima. With more, a block serves 256 (head_dim up to 128): two tiles of Q over the same K and V, a warpgroup, an S and
-// an O for each. Either way the tensor cores work for one warpgroup while the other is at its exponentials. (With
-// an S and an O for each of two warpgroups on alternate tiles, a tile waited 3500 cycles for its S.)
+// operand from the tile TMA brought. The two warpgroups take tiles in turn: three (four) S in tensor memory, one O, and one
+// reference that a tile's warpgroup hands on to the next one's, so that the tensor cores work for one warpgroup while the
+// other is at its exponentials. (With an S and an O for each of two warpgroups on alternate tiles, a tile waited 3500 cycles
+// for its S. Blocks of 256 slots, two tiles of Q over the same K and V, read half as much of L2 and took 1.1 to 1.25 times as
+// long, 448 slots over 8192 rows 35 us and not 28: a warpgroup waited for its own products.)
 //
 // Parts. 16-bit queries and weights enter as one operand, f32 queries as two (the rounding, and the rounding of
 // what it left), and then the weights too: f16 over f16 and e4m3 caches (rows of q scaled by a power of two, so that nothing is
@@ -24,7 +24,7 @@
 // two hold the 8 bits of a bfloat16, three the 11 of a binary16 -- so that K's codes enter the products as they
 // are, at twice the rate, and V alone is converted.
 //
-// Work. A block serves one unit -- a KV head and 128 or 256 slots of it. The tiles that a unit has in all sequences are
+// Work. A block serves one unit -- a KV head and 128 slots of it. The tiles that a unit has in all sequences are
 // laid end to end, and the unit's blocks (ranks; as many as make a block an SM) take equal runs of them:
 // what a block has of a sequence is its output where it has all of it, else a part (reference, sum, sum p v) for
 // attn_tree_combine. The KV heads of a rank run at the same time, so that the pieces of a row that they read are
@@ -56,7 +56,6 @@ struct TreeCfg {
     using KV = KV_;
     using MT = typename PagedMma<KV>::T;
     static constexpr bool E8 = std::is_same<KV, E4m3>::value;
-    static constexpr bool PAIR = HD <= 128;                    // whether tensor memory holds two O
     static constexpr int NB = HD == 256 ? 4 : 3;               // S of the warpgroups in turn
     static constexpr int TR = HD == 256 ? 64 : 128;            // cache rows of a tile
     static constexpr int NSLC = TR / 16;                       // 16-row slices
@@ -86,7 +85,7 @@ struct TreeCfg {
     static constexpr uint32_t OFF_REF = OFF_SEQ + (3 * kTreeSeqs + 2) * 4;   // references of 128 slots
     static constexpr uint32_t SMEM = OFF_REF + 128 * 4;
     static_assert(SMEM <= 227 * 1024, "shared memory");
-    static_assert(NB * TR + HD <= 512 && (!PAIR || 2 * TR + 2 * HD <= 512), "tensor memory");
+    static_assert(NB * TR + HD <= 512, "tensor memory");
 };
 
 struct __align__(16) TileInfo {
@@ -104,8 +103,7 @@ static_assert(sizeof(TileInfo) == 128, "its place in shared memory");
 struct TreeSeg {
     int s, t0, t1, T;
     int n, tok0, nkv, base, start;
-    int slots;                // of the unit in this sequence, at most 256
-    bool pair;                // more than 128: a tile of Q for each warpgroup
+    int slots;                // of the unit in this sequence, at most 128
     int row0;                 // first row of tile 0
 };
 
@@ -326,26 +324,18 @@ struct Tree {
     __device__ __forceinline__ uint32_t v_slot(int i) const { return sm + a.q_bytes + i * C::SLOT; }
     __device__ __forceinline__ uint32_t k_slot(int i) const { return v_slot(a.nv) + i * C::KSLOT; }
     __device__ __forceinline__ uint32_t raw_slot(bool v, int i) const { return k_slot(a.nk) + ((v ? 0 : a.nrv) + i) * C::RAW; }
-    // Tensor memory: O of a warpgroup (of both, where they take tiles in turn), and S
-    static __device__ __forceinline__ uint32_t o_col(bool pair, int w) { return pair ? w * HD : 0; }
-    static __device__ __forceinline__ uint32_t s_col(bool pair, int b) { return (pair ? 2 * HD : HD) + b * TR; }
-    // The S of a segment's tile t for warpgroup w, and how often it was used before in the segment. `Uses` keeps the
-    // parities of all segments before.
+    // Tensor memory: O, and S number b
+    static __device__ __forceinline__ uint32_t s_col(int b) { return HD + b * TR; }
+    // The S of a segment's tile t, and how often it was used before in the segment. `Uses` keeps the parities of all
+    // segments before.
     struct Uses {
         unsigned odd = 0;
-        static __device__ __forceinline__ int buffer(bool pair, int w, int t) { return pair ? w : t % C::NB; }
-        __device__ __forceinline__ unsigned parity(bool pair, int w, int t) const
+        static __device__ __forceinline__ int buffer(int t) { return t % C::NB; }
+        __device__ __forceinline__ unsigned parity(int t) const { return (odd >> buffer(t) ^ t / C::NB) & 1; }
+        __device__ __forceinline__ void end(int T)
         {
-            return (odd >> buffer(pair, w, t) ^ (pair ? t : t / C::NB)) & 1;
-        }
-        __device__ __forceinline__ void end(bool pair, int T)
-        {
-            if (pair) {
-                odd ^= T & 1 ? 3u : 0u;
-            } else {
 #pragma unroll
-                for (int b = 0; b < C::NB; ++b) odd ^= ((unsigned)(T + C::NB - 1 - b) / C::NB & 1) << b;
-            }
+            for (int b = 0; b < C::NB; ++b) odd ^= ((unsigned)(T + C::NB - 1 - b) / C::NB & 1) << b;
         }
     };
     // A place in a ring of n tiles, and the parity of what is waited for there
@@ -405,7 +395,7 @@ struct Tree {
 
     // The block's unit: its KV head, and the first of its slots
     __device__ __forceinline__ int hk() const { return blockIdx.x % a.n_kv_head; }
-    __device__ __forceinline__ int first_slot() const { return blockIdx.x / a.n_kv_head * a.unit_slots; }
+    __device__ __forceinline__ int first_slot() const { return blockIdx.x / a.n_kv_head * kTreeSlots; }
 
     // Rows of a sequence that some node may see: [low, high)
     __device__ __forceinline__ int low_of(int base, int start) const
@@ -437,8 +427,7 @@ struct Tree {
         g.T = before()[lo + 1] - before()[lo];
         g.t0 = p - before()[lo];
         g.t1 = min(g.T, g.t0 + end - p);
-        g.slots = min(g.n * a.group - first_slot(), a.unit_slots);
-        g.pair = C::PAIR && g.slots > 128;
+        g.slots = min(g.n * a.group - first_slot(), kTreeSlots);
         g.row0 = min(low_of(g.base, g.start), g.nkv) / TR * TR;
         return p + g.t1 - g.t0;
     }
@@ -494,7 +483,7 @@ struct Tree {
         }
         if (lane == 0) {
             before()[a.n_seq] = total;
-            flags()[2] = max((total + a.ranks - 1) / a.ranks, a.min_share);
+            flags()[2] = max((total + a.ranks - 1) / a.ranks, 2);         // a tile for each warpgroup
             flags()[3] = total;
         }
     }
@@ -646,7 +635,7 @@ struct Tree {
             p = segment(p, end, g);
             const int T = g.t1 - g.t0;
             // K as far before V as S may be before P V
-            const int ahead = !C::KCONV || g.pair ? 0 : min(a.nk, C::NB) - 1;
+            const int ahead = C::KCONV ? min(a.nk, C::NB) - 1 : 0;
 #pragma unroll 1
             for (int t = -ahead; t < T; ++t) {
                 if (C::KCONV && t + ahead < T) key();
@@ -728,33 +717,29 @@ struct Tree {
         for (int p = from; p < end;) {
             TreeSeg g;
             p = segment(p, end, g);
-            const bool pair = __shfl_sync(0xffffffffu, g.pair, 0);
-            const int T = __shfl_sync(0xffffffffu, g.t1 - g.t0, 0), users = pair ? 2 : 1;
+            const int T = __shfl_sync(0xffffffffu, g.t1 - g.t0, 0);
             wait<true>(q_ready(), segs++ & 1);
             int b = 0;
 #pragma unroll 1
             for (int t = 0; t < T; ++t) {
                 wait(C::KCONV ? ready(false, kr.at) : full(false, kr.at), kr.phase);
+                // S goes over the P of a product that may still read it
+                wait(o_done(b), ~used >> b & 1);
+                used ^= 1u << b;
+                tc_fence_after();
                 const uint64_t k = k0 + (uint32_t)kr.at * (C::KSLOT >> 4);
+                const uint32_t d = tm + s_col(b);
+                uint64_t q = q0;
 #pragma unroll 1
-                for (int w = 0; w < users; ++w) {
-                    // S goes over the P of a product that may still read it
-                    wait(o_done(b), ~used >> b & 1);
-                    used ^= 1u << b;
-                    tc_fence_after();
-                    const uint32_t d = tm + s_col(pair, b);
-                    uint64_t q = q0 + (uint32_t)(w * a.q_parts) * (C::QPART >> 4);
-#pragma unroll 1
-                    for (int x = 0; x < a.q_parts; ++x) {
+                for (int x = 0; x < a.q_parts; ++x) {
 #pragma unroll
-                        for (int kk = 0; kk < KK; ++kk)
-                            umma_ss<C::F8>(one, d, q + ((kk >> 2) * 16384 + (kk & 3) * 32) / 16,
-                                           k + ((kk >> 2) * (TR * 128) + (kk & 3) * 32) / 16, id_s, x + kk > 0);
-                        q += C::QPART >> 4;
-                    }
-                    bar_commit(one, s_full(b));
-                    if (++b == (pair ? 2 : C::NB)) b = 0;
+                    for (int kk = 0; kk < KK; ++kk)
+                        umma_ss<C::F8>(one, d, q + ((kk >> 2) * 16384 + (kk & 3) * 32) / 16, k + ((kk >> 2) * (TR * 128) + (kk & 3) * 32) / 16,
+                                       id_s, x + kk > 0);
+                    q += C::QPART >> 4;
                 }
+                bar_commit(one, s_full(b));
+                if (++b == C::NB) b = 0;
                 bar_commit(one, empty(false, kr.at));
                 kr.next(a.nk);
             }
@@ -771,26 +756,22 @@ struct Tree {
         for (int p = from; p < end;) {
             TreeSeg g;
             p = segment(p, end, g);
-            const bool pair = __shfl_sync(0xffffffffu, g.pair, 0);
-            const int T = __shfl_sync(0xffffffffu, g.t1 - g.t0, 0), users = pair ? 2 : 1;
+            const int T = __shfl_sync(0xffffffffu, g.t1 - g.t0, 0);
             int b = 0;
 #pragma unroll 1
             for (int t = 0; t < T; ++t) {
                 wait(ready(true, vr.at), vr.phase);
+                wait(p_ready(b), used >> b & 1);
+                used ^= 1u << b;
+                tc_fence_after();
                 const uint64_t v = v0 + (uint32_t)vr.at * (C::SLOT >> 4);
-#pragma unroll 1
-                for (int w = 0; w < users; ++w) {
-                    wait(p_ready(b), used >> b & 1);
-                    used ^= 1u << b;
-                    tc_fence_after();
-                    const uint32_t s = tm + s_col(pair, b), o = tm + o_col(pair, w);
+                const uint32_t s = tm + s_col(b);
 #pragma unroll
-                    for (int kk = 0; kk < TR / 16; ++kk)
+                for (int kk = 0; kk < TR / 16; ++kk)
 #pragma unroll
-                        for (int x = 0; x < PARTS; ++x) umma_ts(one, o, s + 32 * (kk >> 1) + 16 * x + 8 * (kk & 1), v + kk * 128, id_o);
-                    bar_commit(one, o_done(b));
-                    if (++b == (pair ? 2 : C::NB)) b = 0;
-                }
+                    for (int x = 0; x < PARTS; ++x) umma_ts(one, tm, s + 32 * (kk >> 1) + 16 * x + 8 * (kk & 1), v + kk * 128, id_o);
+                bar_commit(one, o_done(b));
+                if (++b == C::NB) b = 0;
                 bar_commit(one, empty(true, vr.at));
                 vr.next(a.nv);
             }
@@ -819,35 +800,33 @@ struct Tree {
     // Q of the warpgroup's slots: parts, K-major, swizzled; returns what undoes the power of two of the thread's row.
     // The rows are copied as they are, 16 bytes a lane, to where their parts will stand -- a row of
     // float is as long as its two 16-bit parts, one of 16 bits as one of those or as two 8-bit ones -- and a thread then
-    // turns its own row into its parts, in place. Where the two warpgroups share a tile of Q, each copies every other
-    // 32 units and turns every other unit of a row.
-    __device__ __forceinline__ uint32_t q_place(int qt, int row, int part, int u) const
+    // turns its own row into its parts, in place. Each of the two warpgroups copies every other 32 units and turns every other
+    // unit of a row.
+    __device__ __forceinline__ uint32_t q_place(int row, int part, int u) const
     {
-        const uint32_t to = sm + (uint32_t)(qt * a.q_parts + part) * C::QPART;
+        const uint32_t to = sm + (uint32_t)part * C::QPART;
         if (C::F8 && HD == 64) return to + row * 64 + (((u ^ (row >> 1)) & 3) << 4);
         return to + (u >> 3) * 16384 + row * 128 + (((u ^ row) & 7) << 4);
     }
     __device__ __forceinline__ float stage_q(const TreeSeg &g, const Row &r, int w, int quad, int lane)
     {
-        const int qt = g.pair ? w : 0, my = quad * 32 + lane;
-        const bool half = !g.pair;
+        const int my = quad * 32 + lane;
         const bool f32 = a.q_type == kTypeF32, f16 = std::is_same<MT, __half>::value;
         const int lg = (HD == 64 ? 3 : HD == 128 ? 4 : 5) + f32, last = (1 << lg) - 1;   // log2 of a row's 16-byte units
-        const int su = half ? 2 : 1, rows = min(max(g.slots - qt * 128 - quad * 32, 0), 32);
+        const int rows = min(max(g.slots - quad * 32, 0), 32);
         const int mine_at = r.t * a.n_head + r.h;                     // after the sequence's first token
         const uint8_t *src = static_cast<const uint8_t *>(a.q) + ((int64_t)g.tok0 * a.n_head << lg) * 16;
 #pragma unroll 1
-        for (int it = half ? w : 0; it * 32 < rows << lg; it += su) {
+        for (int it = w; it * 32 < rows << lg; it += 2) {
             const int i = it * 32 + lane, row = i >> lg, u = i & last;
             const int at = __shfl_sync(0xffffffffu, mine_at, row);
-            const uint32_t to = f32 || C::F8 ? q_place(qt, quad * 32 + row, u & 1, u >> 1) : q_place(qt, quad * 32 + row, 0, u);
+            const uint32_t to = f32 || C::F8 ? q_place(quad * 32 + row, u & 1, u >> 1) : q_place(quad * 32 + row, 0, u);
             if (row < rows)
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
                              :: "r"(to), "l"(src + (((int64_t)at << lg) + u) * 16) : "memory");
         }
         asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-        if (half) group_sync();
-        else __syncwarp();
+        group_sync();
         if (!C::F8 && PARTS == 1 && a.q_type == (f16 ? kTypeF16 : kTypeBf16)) return 1.f;   // as it is
         const bool bf = a.q_type == kTypeBf16;
         const int mine = r.t >= 0 ? HD / 8 : 0;                       // units of 8 elements
@@ -858,13 +837,13 @@ struct Tree {
             if (f32) {
 #pragma unroll 4
                 for (int u = 0; u < 2 * mine; ++u) {
-                    const uint4 x = lds128(q_place(qt, my, u & 1, u >> 1));
+                    const uint4 x = lds128(q_place(my, u & 1, u >> 1));
                     m = max(max(m, x.x & 0x7fffffffu), max(max(x.y & 0x7fffffffu, x.z & 0x7fffffffu), x.w & 0x7fffffffu));
                 }
             } else {
 #pragma unroll 4
                 for (int u = 0; u < mine; ++u) {
-                    const uint4 x = lds128(C::F8 ? q_place(qt, my, u & 1, u >> 1) : q_place(qt, my, 0, u));
+                    const uint4 x = lds128(C::F8 ? q_place(my, u & 1, u >> 1) : q_place(my, 0, u));
                     m = __vmaxu2(__vmaxu2(m, x.x & 0x7fff7fffu), __vmaxu2(__vmaxu2(x.y & 0x7fff7fffu, x.z & 0x7fff7fffu), x.w & 0x7fff7fffu));
                 }
                 m = max(m >> 16, m & 0xffffu);
@@ -876,15 +855,15 @@ struct Tree {
                 inv *= 128.f;
             }
         }
-        if (half) group_sync();                                       // the other warpgroup has read the row too
+        group_sync();                                                 // the other warpgroup has read the row too
         auto pair_of = [&](uint32_t w) {                              // two elements, scaled
             const float2 x = bf ? kv2_to_float2<__nv_bfloat16>(w) : kv2_to_float2<__half>(w);
             return make_float2(x.x * sc, x.y * sc);
         };
         if constexpr (C::F8) {
 #pragma unroll 1
-            for (int u = half ? w : 0; u < mine / 2; u += su) {       // 16 elements
-                const uint4 x = lds128(q_place(qt, my, 0, u)), y = lds128(q_place(qt, my, 1, u));
+            for (int u = w; u < mine / 2; u += 2) {       // 16 elements
+                const uint4 x = lds128(q_place(my, 0, u)), y = lds128(q_place(my, 1, u));
                 const uint32_t in[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
                 __half2 h[8];                                         // exact: 11 bits, and 2^8 is far from f16's limits
 #pragma unroll
@@ -906,16 +885,16 @@ struct Tree {
                         h[2 * e] = __hsub2(h[2 * e], *reinterpret_cast<__half2 *>(&b0));
                         h[2 * e + 1] = __hsub2(h[2 * e + 1], *reinterpret_cast<__half2 *>(&b1));
                     }
-                    sts128(q_place(qt, my, part, u), make_uint4(c[0], c[1], c[2], c[3]));
+                    sts128(q_place(my, part, u), make_uint4(c[0], c[1], c[2], c[3]));
                 }
             }
         } else {
 #pragma unroll 1
-            for (int u = half ? w : 0; u < mine; u += su) {
-                const uint4 x = lds128(q_place(qt, my, 0, u));
+            for (int u = w; u < mine; u += 2) {
+                const uint4 x = lds128(q_place(my, 0, u));
                 float2 f[4];
                 if (f32) {
-                    const uint4 y = lds128(q_place(qt, my, 1, u));
+                    const uint4 y = lds128(q_place(my, 1, u));
                     f[0] = make_float2(__uint_as_float(x.x) * sc, __uint_as_float(x.y) * sc);
                     f[1] = make_float2(__uint_as_float(x.z) * sc, __uint_as_float(x.w) * sc);
                     f[2] = make_float2(__uint_as_float(y.x) * sc, __uint_as_float(y.y) * sc);
@@ -938,7 +917,7 @@ struct Tree {
                             f[e].y -= b.y;
                         }
                     }
-                    sts128(q_place(qt, my, part, u), make_uint4(h[0], h[1], h[2], h[3]));
+                    sts128(q_place(my, part, u), make_uint4(h[0], h[1], h[2], h[3]));
                 }
             }
         }
@@ -1109,20 +1088,18 @@ struct Tree {
             TreeSeg g;
             const int next = segment(p, end, g);
             const bool begins = g.t0 == 0, whole = begins && g.t1 == g.T;
-            const bool pair = g.pair;
-            const int T = g.t1 - g.t0, qt = pair ? w : 0;
-            const int in_unit = qt * 128 + my, slot = first_slot() + in_unit;
-            const uint32_t o_at = tm + o_col(pair, w) + lanes;
+            const int T = g.t1 - g.t0, slot = first_slot() + my;
+            const uint32_t o_at = tm + lanes;
             Row r;
-            r.t = in_unit < g.slots ? div(a.by_group, slot) : -1;
-            const bool any = qt * 128 + quad * 32 < g.slots;   // some slot in this warp; warps of its group without one
-            const int idle = 4 - (min(g.slots - qt * 128, 128) + 31) / 32;
+            r.t = my < g.slots ? div(a.by_group, slot) : -1;
+            const bool any = quad * 32 < g.slots;   // some slot in this warp; warps of its group without one
+            const int idle = 4 - (g.slots + 31) / 32;
             r.h = hk() * a.group + (r.t >= 0 ? slot - r.t * a.group : 0);
             r.x = g.base + depth_of(g, max(r.t, 0));
             r.c = stage_q(g, r, w, quad, lane) * a.qscale;
             fence_proxy_async_smem();                          // Q is read by the tensor cores
             __syncwarp();                                      // rows without a slot had nothing to turn
-            if (any && (pair || w == 0)) {
+            if (any && w == 0) {
                 uint32_t z[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) z[i] = 0u;
@@ -1136,11 +1113,11 @@ struct Tree {
 
             float m = -INFINITY, l = 0.f;
 #pragma unroll 1
-            for (int t = pair ? 0 : w; any && t < T; t += pair ? 1 : 2) {
-                const int b = Uses::buffer(pair, w, t);
-                const uint32_t s_at = tm + s_col(pair, b) + lanes;
+            for (int t = w; any && t < T; t += 2) {
+                const int b = Uses::buffer(t);
+                const uint32_t s_at = tm + s_col(b) + lanes;
                 const volatile TileInfo *d = tile_info(tiles + t);
-                wait(s_full(b), uses.parity(pair, w, t));
+                wait(s_full(b), uses.parity(t));
                 tc_fence_after();
                 const int edge = __shfl_sync(0xffffffffu, d->edge, 0);
                 const bool slow = edge || rules;
@@ -1156,14 +1133,13 @@ struct Tree {
                     }
                     tmem_wait_st();
                     if ((edge & 1) && __any_sync(0xffffffffu, d->bad[0] | d->bad[1] | d->bad[2] | d->bad[3]) && !ended()) {
-                        // O stands still from the product before (of a pair's warpgroup: issued before this S) to this one
-                        if (!pair && t > 0) wait(o_done(Uses::buffer(pair, w, t - 1)), uses.parity(pair, w, t - 1));
+                        // O stands still from the product before to this one
+                        if (t > 0) wait(o_done(Uses::buffer(t - 1)), uses.parity(t - 1));
                         tc_fence_after();
                         add_bad(g, d, s_at, o_at);
                     }
                 }
                 // P, by the reference as it is: that of the tile before may be larger by now, which is seen to at the end
-                const float before = m;
                 const float c = slow ? 1.f : r.c;
                 uint64_t sum[4];
 #pragma unroll
@@ -1218,8 +1194,8 @@ struct Tree {
                 gather();
                 tmem_wait_st();
                 // O and P by one reference, the larger
-                float mo = pair ? before : m;                  // O's
-                if (!pair && t > 0) {
+                float mo = m;                                  // O's
+                if (t > 0) {
                     wait(ref_known(quad), (refs_odd ^ (t - 1)) & 1);
                     mo = refs[my];
                 }
@@ -1228,17 +1204,15 @@ struct Tree {
                     if (__any_sync(0xffffffffu, m != M)) scale_p(s_at, TR, fac);
                     l *= fac;
                     if (__any_sync(0xffffffffu, mo != M)) {
-                        if (!pair) wait(o_done(Uses::buffer(pair, w, t - 1)), uses.parity(pair, w, t - 1));
+                        wait(o_done(Uses::buffer(t - 1)), uses.parity(t - 1));
                         tc_fence_after();
                         scale_o(o_at, mo == M ? 1.f : fmaxf(ex2(mo - M), 1.17549435e-38f));   // not 0: it may hold infinities
                     }
                     m = M;
                 }
-                if (!pair) {
-                    refs[my] = m;
-                    __syncwarp();
-                    if (lane == 0) bar_arrive(ref_known(quad));
-                }
+                refs[my] = m;
+                __syncwarp();
+                if (lane == 0) bar_arrive(ref_known(quad));
                 tc_fence_before();
                 __syncwarp();
                 if (lane <= (quad ? 0 : idle)) bar_arrive(p_ready(b));   // for the warps without a slot too
@@ -1246,10 +1220,10 @@ struct Tree {
             // Every product of the segment is done. A barrier's parity tells a phase from those next to it only, so each wait
             // is for one that the warp knows to be the last or the one under way: the warpgroup's own last tile's first
             // (the other's last tile may have used the same S as a product that is still under way, and may be done too).
-            if (any && !pair && T > 1) wait(o_done(Uses::buffer(pair, w, T - 2)), uses.parity(pair, w, T - 2));
-            if (any) wait(o_done(Uses::buffer(pair, w, T - 1)), uses.parity(pair, w, T - 1));
-            uses.end(pair, T);
-            if (any && !pair) refs_odd ^= T & 1;
+            if (any && T > 1) wait(o_done(Uses::buffer(T - 2)), uses.parity(T - 2));
+            if (any) wait(o_done(Uses::buffer(T - 1)), uses.parity(T - 1));
+            uses.end(T);
+            if (any) refs_odd ^= T & 1;
             // a slot whose every score is NaN keeps its NaN sum
             finish(tm, g, r, w, quad, lane, whole, begins, rank, m == -INFINITY && l != 0.f ? 0.f : m - OFF, l, any);
             tiles += T;
@@ -1309,21 +1283,20 @@ struct Tree {
         return fmaxf(k, __uint_as_float(v[at + 15]));
     }
 
-    // The end of a segment: the output, or the block's part of it. Warpgroups in turn share O, and write half of its dimensions
-    // each.
+    // The end of a segment: the output, or the block's part of it; each warpgroup writes half of the dimensions.
     __device__ __forceinline__ void finish(uint32_t tm, const TreeSeg &g, const Row &r, int w, int quad, int lane, bool whole,
                                            bool begins, int rank, float m, float l, bool any)
     {
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         tc_fence_after();
-        const size_t block = ((size_t)(rank * 2 + (begins ? 1 : 0)) * gridDim.x + blockIdx.x) * a.unit_slots;
-        const int in_unit = (g.pair ? w : 0) * 128 + quad * 32 + lane;
+        const size_t block = ((size_t)(rank * 2 + (begins ? 1 : 0)) * gridDim.x + blockIdx.x) * kTreeSlots;
+        const int in_unit = quad * 32 + lane;
         auto put = [&](int d, const float (&y)[32], float inv) {   // 32 dimensions from d on
             if (r.t < 0) return;
             if (!whole) {
-                float4 *o = reinterpret_cast<float4 *>(a.ws_o + block * HD) + (size_t)(d / 4) * a.unit_slots + in_unit;
+                float4 *o = reinterpret_cast<float4 *>(a.ws_o + block * HD) + (size_t)(d / 4) * kTreeSlots + in_unit;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i * a.unit_slots] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                for (int i = 0; i < 8; ++i) o[i * kTreeSlots] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
             } else if (a.q_type == kTypeF32) {
                 float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + place_of(g, r) * HD + d);
 #pragma unroll
@@ -1344,32 +1317,28 @@ struct Tree {
                 }
             }
         };
-        int d0 = 0, d1 = HD;
-        float f = 1.f;                                         // what O is to be multiplied by
-        if (!g.pair) {
-            // the other warpgroup's reference and sum, through this thread's lane of tensor memory; O has the larger reference
-            const uint32_t box = tm + s_col(false, 0) + lanes;
-            if (any) {
-                tmem_st2(box + 2 * w, __float_as_uint(m), __float_as_uint(l));
-                tmem_wait_st();
-            }
-            tc_fence_before();
-            group_sync(!any);
-            tc_fence_after();
-            if (any) {
-                uint32_t om, ol;
-                tmem_ld2(box + 2 * (w ^ 1), om, ol);
-                const float m1 = __uint_as_float(om), l1 = __uint_as_float(ol), M = fmaxf(m, m1);
-                l = (m == -INFINITY ? 0.f : l * ex2(m - M)) + (m1 == -INFINITY ? 0.f : l1 * ex2(m1 - M));
-                m = M;
-            }
-            d0 = w * (HD / 2);
-            d1 = d0 + HD / 2;
+        // the other warpgroup's reference and sum, through this thread's lane of tensor memory; O has the larger reference
+        const uint32_t box = tm + s_col(0) + lanes;
+        if (any) {
+            tmem_st2(box + 2 * w, __float_as_uint(m), __float_as_uint(l));
+            tmem_wait_st();
         }
+        tc_fence_before();
+        group_sync(!any);
+        tc_fence_after();
+        if (any) {
+            uint32_t om, ol;
+            tmem_ld2(box + 2 * (w ^ 1), om, ol);
+            const float m1 = __uint_as_float(om), l1 = __uint_as_float(ol), M = fmaxf(m, m1);
+            l = (m == -INFINITY ? 0.f : l * ex2(m - M)) + (m1 == -INFINITY ? 0.f : l1 * ex2(m1 - M));
+            m = M;
+        }
+        const int d0 = w * (HD / 2), d1 = d0 + HD / 2;
+        float f = 1.f;                                         // what O is to be multiplied by
         if (any && !ended()) {
             if (!whole && r.t >= 0 && d0 == 0) a.ws_ml[block + in_unit] = make_float2(m, l);
             if (whole) f = l == 0.f ? 0.f : rcp(l);
-            const uint32_t o = tm + o_col(g.pair, w) + lanes;
+            const uint32_t o = tm + lanes;
 #pragma unroll 1
             for (int d = d0; d < d1; d += 32) {
                 uint32_t u[32];
@@ -1502,7 +1471,7 @@ __global__ void __launch_bounds__(128) attn_tree_combine(const TreeArgs a)
     int64_t c1 = (int64_t)(a.seq0 + s + 1) * a.n_each;
     if (a.cu) c1 = min(max((int64_t)ld_dep(a.cu + s + 1), (int64_t)0), a.n_tokens);
     if (tk >= c1 || gh >= a.group) return;
-    const int slot = (int)(tk - sp.z) * a.group + gh, mu = slot / a.unit_slots;
+    const int slot = (int)(tk - sp.z) * a.group + gh, mu = slot / kTreeSlots;
     if (mu > 0) {                                              // the unit's own places
         const uint4 u = ld_dep(reinterpret_cast<const uint4 *>(a.ws_span + mu * a.n_seq + s));
         sp = make_int4((int)u.x, (int)u.y, 0, (int)u.w);
@@ -1510,7 +1479,7 @@ __global__ void __launch_bounds__(128) attn_tree_combine(const TreeArgs a)
     const int r0 = sp.x / sp.w, r1 = (sp.x + sp.y - 1) / sp.w;
     if (r0 == r1) return;
     const int unit = mu * a.n_kv_head + hk;
-    const int in_unit = slot - mu * a.unit_slots;
+    const int in_unit = slot - mu * kTreeSlots;
     float m = -INFINITY, S = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int BATCH = 4;
@@ -1520,9 +1489,9 @@ __global__ void __launch_bounds__(128) attn_tree_combine(const TreeArgs a)
 #pragma unroll
         for (int b = 0; b < BATCH; ++b) {
             const int x = min(r + b, r1);
-            const size_t block = ((size_t)(x * 2 + (x == r0 ? 1 : 0)) * a.units + unit) * a.unit_slots;   // it begins in the first one's places
+            const size_t block = ((size_t)(x * 2 + (x == r0 ? 1 : 0)) * a.units + unit) * kTreeSlots;   // it begins in the first one's places
             ml[b] = ld_dep(a.ws_ml + block + in_unit);
-            v[b] = ld_dep(reinterpret_cast<const float4 *>(a.ws_o + block * HD) + (size_t)d4 * a.unit_slots + in_unit);
+            v[b] = ld_dep(reinterpret_cast<const float4 *>(a.ws_o + block * HD) + (size_t)d4 * kTreeSlots + in_unit);
         }
 #pragma unroll
         for (int b = 0; b < BATCH; ++b) {
@@ -1570,7 +1539,7 @@ cudaError_t launch_tree_kernel(const TreeRequest &r)
     if (e != cudaSuccess) return e;
     // 8-bit parts hold 4 bits each: bfloat16 8, binary16 11
     a.q_parts = C::F8 ? (a.q_type == kTypeBf16 ? 2 : 3) : C::PARTS;
-    a.q_bytes = (uint32_t)(a.unit_slots / 128) * a.q_parts * C::QPART;
+    a.q_bytes = (uint32_t)a.q_parts * C::QPART;
     // the rings share what Q leaves
     auto few = [](int x) { return x > 4 ? 4 : x; };
     const uint32_t left = C::DATA - a.q_bytes;

@@ -37,32 +37,30 @@ attn_status check_call(const attn_paged_cache *c, int q_type, int n_head, int n_
 
 struct TreePlan {
     int64_t units = 1;
-    int n_splits = 1, unit_slots = 128, min_share = 1, tile = 128;
+    int n_splits = 1, tile = 128;
     size_t o_bytes = 0, ml_bytes = 0, workspace = 0;
 };
 
-// As many blocks for each unit (KV head, 128 or 256 slots) as make a block an SM; where that leaves SMs without one
+// As many blocks for each unit (KV head, 128 slots) as make a block an SM; where that leaves SMs without one
 // (units just over half of them), enough for four rounds of blocks, whose last is nearly full; no more than
-// there are tiles at full capacity. Up to 128 slots the two warpgroups of a block take tiles in turn: two at least.
+// there are pairs of tiles at full capacity: the two warpgroups of a block take tiles in turn.
 void make_plan(const attn_paged_cache *c, int max_pages, int n_seq, int max_nodes, int n_head, int n_splits, int sm_count,
                TreePlan &pl)
 {
     const int need = max_nodes * (n_head / c->n_kv_head);
     pl.tile = attn::tree_tile(c->head_dim);
-    pl.unit_slots = c->head_dim == 256 || need <= 128 ? 128 : 256;
-    pl.min_share = pl.unit_slots == 128 ? 2 : 1;
-    const int64_t mus = (need + pl.unit_slots - 1) / pl.unit_slots;
+    const int64_t mus = (need + attn::kTreeSlots - 1) / attn::kTreeSlots;
     pl.units = c->n_kv_head * mus;
     const int64_t seqs = n_seq < attn::kTreeSeqs ? n_seq : attn::kTreeSeqs;
     const int64_t tiles = ((int64_t)max_pages * c->page_size + pl.tile - 1) / pl.tile * seqs;
-    const int64_t most = (tiles + pl.min_share - 1) / pl.min_share;
+    const int64_t most = (tiles + 1) / 2;
     int64_t P = sm_count / pl.units;
     if (P * pl.units * 20 < (int64_t)sm_count * 17) P = 4 * (int64_t)sm_count / pl.units;
     if (P > most) P = most;
     if (P > kMaxTreeSplits) P = kMaxTreeSplits;
     pl.n_splits = n_splits > 0 ? n_splits : P < 1 ? 1 : (int)P;
     if (pl.n_splits > 1) {
-        const size_t parts = (size_t)pl.n_splits * 2 * pl.units * pl.unit_slots;
+        const size_t parts = (size_t)pl.n_splits * 2 * pl.units * attn::kTreeSlots;
         pl.o_bytes = align256(parts * c->head_dim * sizeof(float));
         pl.ml_bytes = align256(parts * 2 * sizeof(float));
         pl.workspace = pl.o_bytes + pl.ml_bytes + align256((size_t)(seqs * mus) * 16);
@@ -203,9 +201,7 @@ attn_status attn_decode_tree(const attn_paged_cache *cache, const int32_t *block
     a.cap = max_pages * cache->page_size;
     a.window = window > a.cap ? 0 : window;        // past the capacity it masks nothing
     a.ranks = pl.n_splits;
-    a.min_share = pl.min_share;
-    a.unit_slots = pl.unit_slots;
-    a.once = (int64_t)max_nodes * a.group <= pl.unit_slots;
+    a.once = (int64_t)max_nodes * a.group <= attn::kTreeSlots;
     a.qscale = qscale;
     a.softcap = softcap;
     a.cap_log2 = (float)((double)softcap * 1.4426950408889634);

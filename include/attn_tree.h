@@ -83,7 +83,7 @@ attn_status attn_rope_append_tree(const attn_paged_cache *cache, const int32_t *
  *              base_s + depth, cache row j < base_s at position j, node j at base_s + its
  *              depth. starts masks rows (of nodes too), whatever their position.
  *   n_head     a multiple of n_kv_head, n_head / n_kv_head <= 64
- *   n_splits   blocks that share the call's rows, per KV head and 128 or 256 of its
+ *   n_splits   blocks that share the call's rows, per KV head and 128 of its
  *              (node, head) pairs: each takes an equal part of the tiles (128 rows, 64
  *              at head_dim 256) of all sequences; 0: attn_tree_plan's count, which
  *              fills the GPU once
