@@ -48,6 +48,7 @@
 namespace attn {
 
 constexpr unsigned kErrBadTree = 0x8u;        // ATTN_DEVERR_BAD_REQUEST
+constexpr int kTreeTurn = 7;                  // what another sequence costs a block, in tiles
 constexpr int kTreeDesc = 8;                  // tiles whose descriptors are kept: K runs at most 4 tiles ahead of S, S 3 of P
 
 template <int HD_, typename KV_, int PARTS_>
@@ -80,9 +81,9 @@ struct TreeCfg {
     static constexpr uint32_t OFF_DESC = DATA;
     static constexpr uint32_t OFF_BAR = OFF_DESC + kTreeDesc * 128;
     static constexpr int NBAR = 50 + kTreeDesc;
-    static constexpr uint32_t OFF_FLAG = OFF_BAR + NBAR * 8;   // TMEM slot, abort, share, total
-    static constexpr uint32_t OFF_SEQ = OFF_FLAG + 16;         // before, first token, rows
-    static constexpr uint32_t OFF_REF = OFF_SEQ + (3 * kTreeSeqs + 2) * 4;   // references of 128 slots
+    static constexpr uint32_t OFF_FLAG = OFF_BAR + NBAR * 8;   // TMEM slot, abort, share, the block's first tile and the one behind it
+    static constexpr uint32_t OFF_SEQ = OFF_FLAG + 32;         // before, first token, places before, rows
+    static constexpr uint32_t OFF_REF = OFF_SEQ + (4 * kTreeSeqs + 4) * 4;   // references of 128 slots
     static constexpr uint32_t SMEM = OFF_REF + 128 * 4;
     static_assert(SMEM <= 227 * 1024, "shared memory");
     static_assert(NB * TR + HD <= 512, "tensor memory");
@@ -315,11 +316,12 @@ struct Tree {
     __device__ __forceinline__ uint32_t q_ready() const { return bar(48); }
     __device__ __forceinline__ uint32_t described(unsigned tile) const { return bar(50 + (tile & (kTreeDesc - 1))); }
     __device__ __forceinline__ uint32_t met() const { return bar(49); }
-    // [0] tensor memory, [1] abort, [2] places of a rank, [3] of all
+    // [0] tensor memory, [1] abort, [2] places of a rank, [3], [4] its first tile and the one behind its last
     __device__ __forceinline__ volatile int *flags() const { return reinterpret_cast<volatile int *>(smem + C::OFF_FLAG); }
-    __device__ __forceinline__ int *before() const { return reinterpret_cast<int *>(smem + C::OFF_SEQ); }   // places before each sequence
+    __device__ __forceinline__ int *before() const { return reinterpret_cast<int *>(smem + C::OFF_SEQ); }   // tiles before each sequence
     __device__ __forceinline__ int *tok() const { return before() + kTreeSeqs + 1; }                         // first tokens
-    __device__ __forceinline__ int *rows() const { return tok() + kTreeSeqs + 1; }                          // rows
+    __device__ __forceinline__ int *place() const { return tok() + kTreeSeqs + 1; }                         // place of its first tile
+    __device__ __forceinline__ int *rows() const { return place() + kTreeSeqs + 1; }                        // rows
     // Q, then V's tiles, K's, and the 8-bit ones that are converted
     __device__ __forceinline__ uint32_t v_slot(int i) const { return sm + a.q_bytes + i * C::SLOT; }
     __device__ __forceinline__ uint32_t k_slot(int i) const { return v_slot(a.nv) + i * C::KSLOT; }
@@ -409,7 +411,7 @@ struct Tree {
         return max((nkv + TR - 1) / TR - lo, 1);
     }
 
-    // The segment that begins at place p (of the block's, up to `end`), and the place behind it.
+    // The segment that begins at tile p (of the block's, up to `end`), and the tile behind it.
     __device__ __forceinline__ int segment(int p, int end, TreeSeg &g) const
     {
         int lo = 0, hi = a.n_seq - 1;
@@ -433,16 +435,19 @@ struct Tree {
     }
 
     // -----------------------------------------------------------------------
-    // Rows, tiles and places of every sequence; by one warp.
+    // Rows, tiles and places of every sequence, and the block's tiles; by one warp. A sequence's tiles have a place each, and
+    // kTreeTurn places lie between one sequence and the next: what a block spends on another sequence (its Q, its output, the
+    // pipeline's filling) is the time of as many tiles. (Without them, 4 sequences in blocks of 13 tiles: those with
+    // two of the sequences took 60 thousand cycles, the others 42.)
     // -----------------------------------------------------------------------
     __device__ __forceinline__ void count(int lane)
     {
         constexpr int MOST = kTreeSeqs / 32;
         const int per = (a.n_seq + 31) / 32;
-        int places[MOST], sum = 0;
+        int tiles[MOST], sum = 0, there = 0;                   // there: sequences with tiles
 #pragma unroll
         for (int i = 0; i < MOST; ++i) {
-            places[i] = 0;
+            tiles[i] = 0;
             const int s = lane * per + i;
             if (i >= per || s >= a.n_seq) continue;
             const int pos = ld_dep(a.positions + s);
@@ -463,28 +468,49 @@ struct Tree {
             if (n > 0 && (pos < -1 || pos >= a.cap) && report) atomicOr(a.err, kErrPositionClamped);
             const int nkv = min(max(pos, -1), a.cap - 1) + 1;
             rows()[s] = nkv;
-            if (n * a.group > first_slot()) places[i] = tiles_of(n, nkv, start);
-            sum += places[i];
+            if (n * a.group > first_slot()) tiles[i] = tiles_of(n, nkv, start);
+            sum += tiles[i];
+            there += tiles[i] > 0;
         }
-        int upto = sum;
+        int upto = sum, seqs = there;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, upto, off);
-            if (lane >= off) upto += y;
+            const int y = __shfl_up_sync(0xffffffffu, upto, off), z = __shfl_up_sync(0xffffffffu, seqs, off);
+            if (lane >= off) {
+                upto += y;
+                seqs += z;
+            }
         }
-        const int total = __shfl_sync(0xffffffffu, upto, 31);
-        int at = upto - sum;
+        const int total = __shfl_sync(0xffffffffu, upto, 31), turns = max(__shfl_sync(0xffffffffu, seqs, 31) - 1, 0);
+        int at = upto - sum, turn = seqs - there;
 #pragma unroll
         for (int i = 0; i < MOST; ++i) {
             const int s = lane * per + i;
             if (i >= per || s >= a.n_seq) continue;
             before()[s] = at;
-            at += places[i];
+            place()[s] = at + turn * kTreeTurn;
+            at += tiles[i];
+            turn += tiles[i] > 0;
         }
+        const int places = total + turns * kTreeTurn, share = max((places + a.ranks - 1) / a.ranks, 2);   // a tile for each warpgroup
         if (lane == 0) {
             before()[a.n_seq] = total;
-            flags()[2] = max((total + a.ranks - 1) / a.ranks, 2);         // a tile for each warpgroup
-            flags()[3] = total;
+            flags()[2] = share;
+        }
+        __syncwarp();
+        if (lane < 2) {                                        // tiles before the block's first place, and the one behind its last
+            const int64_t p = (int64_t)(blockIdx.y + lane) * share;
+            int x = total;
+            if (p < places) {
+                int lo = 0, hi = a.n_seq - 1;                  // the last sequence whose place is at most p (0: the first)
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (place()[mid] <= p) lo = mid;
+                    else hi = mid - 1;
+                }
+                x = min(before()[lo] + max((int)p - place()[lo], 0), before()[lo + 1]);
+            }
+            flags()[3 + lane] = x;
         }
     }
 
@@ -983,7 +1009,7 @@ struct Tree {
             float k = 0.f;
 #pragma unroll
             for (int c = 0; c < 32; c += 2) k = fmaxf(fmaxf(k, fabsf(s[c])), fabsf(s[c + 1]));
-            if (__all_sync(0xffffffffu, k < 0.4f)) {           // a cap is seldom come near
+            if (__all_sync(0xffffffffu, k < 0.4f || r.t < 0)) {   // a cap is seldom come near; nothing is known of rows without a slot
 #pragma unroll
                 for (int c = 0; c < 32; ++c) s[c] = a.cap_log2 * tanh_small(s[c]);
             } else {
@@ -1176,7 +1202,7 @@ struct Tree {
                     k[1] = fmaf(most16(u, 16), f[1], k[1]);
                     k[2] = fmaf(most16(v, 0), f[2], k[2]);
                     k[3] = fmaf(most16(v, 16), f[3], k[3]);
-                    const float mx = fmaxf(fmaxf(k[0], k[1]), fmaxf(k[2], k[3]));
+                    const float mx = r.t < 0 ? -INFINITY : fmaxf(fmaxf(k[0], k[1]), fmaxf(k[2], k[3]));
                     if (__any_sync(0xffffffffu, mx > m + TAU)) {
                         const float M = mx > m + TAU ? ceilf(mx) : m, fac = M == m ? 1.f : ex2(m - M);   // 0 from -inf
                         gather();
@@ -1389,7 +1415,7 @@ attn_tree_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             __syncwarp();
             for (int s = lane; s < a.n_seq; s += 32)
                 a.ws_span[blockIdx.x / a.n_kv_head * a.n_seq + s] =
-                    make_int4(x.before()[s], x.before()[s + 1] - x.before()[s], x.tok()[s], x.flags()[2]);
+                    make_int4(x.place()[s], x.before()[s + 1] - x.before()[s], x.tok()[s], x.flags()[2]);
         }
     } else {
         if (warp == C::MMA_S) tmem_alloc(reinterpret_cast<uint32_t *>(const_cast<int *>(x.flags())), C::TM_COLS);
@@ -1400,9 +1426,7 @@ attn_tree_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = (uint32_t)x.flags()[0];
-    const int share = x.flags()[2], total = x.flags()[3];
-    const int64_t first = (int64_t)rank * share;
-    const int from = (int)min(first, (int64_t)total), end = (int)min(first + share, (int64_t)total);
+    const int from = x.flags()[3], end = x.flags()[4];
     {
         if (warp < C::SM_WARPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
