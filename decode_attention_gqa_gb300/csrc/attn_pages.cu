@@ -13,6 +13,7 @@ namespace {
 constexpr int kBookThreads = 1024;
 constexpr int kMaxResize = 8192, kMaxForks = 4096;
 constexpr int kBookCluster = 16;
+constexpr int kMaxBookSeqs = 65536;
 
 struct BookArgs {
     int32_t *refs, *table;
@@ -234,27 +235,49 @@ __device__ __forceinline__ bool fork_at(const BookArgs &g, int i, int &src, int 
            rows <= g.max_pages * g.page_size;
 }
 
+// Sequences that a fork may not end in: dst of two forks, or of one and src of another. Every block finds them by itself.
+struct Taken {
+    unsigned src[kMaxBookSeqs / 32], once[kMaxBookSeqs / 32], twice[kMaxBookSeqs / 32];
+
+    __device__ __forceinline__ void fill(const BookArgs &g)
+    {
+        for (int i = threadIdx.x; i * 32 < g.n_seq; i += kBookThreads) src[i] = once[i] = twice[i] = 0u;
+        __syncthreads();
+        for (int i = threadIdx.x; i < g.n; i += kBookThreads) {
+            int s, d, rows;
+            if (!fork_at(g, i, s, d, rows)) continue;
+            atomicOr(src + s / 32, 1u << s % 32);
+            const unsigned bit = 1u << d % 32;
+            if (atomicOr(once + d / 32, bit) & bit) atomicOr(twice + d / 32, bit);
+        }
+        __syncthreads();
+    }
+    __device__ __forceinline__ bool has(int d) const { return (src[d / 32] | twice[d / 32]) >> d % 32 & 1u; }
+};
+
 // Block 0 gives out the pages that the forks end in; the others share the full ones, which are held already, so
 // that no count that block 0 looks for changes to or from 0 under it.
 __global__ void __launch_bounds__(kBookThreads) fork_kernel(const BookArgs g)
 {
     __shared__ int sm[32];
-    __shared__ int which[kMaxForks];
+    __shared__ uint16_t which[kMaxForks];
+    __shared__ Taken taken;
     pdl_wait();
     const int tid = threadIdx.x;
+    taken.fill(g);
     if (blockIdx.x == 0) {
         int need = 0;
         for (int i0 = 0; i0 < g.n; i0 += kBookThreads) {
             const int i = i0 + tid;
             int src, dst, rows, x = 0;
             if (i < g.n) {
-                if (fork_at(g, i, src, dst, rows)) x = rows - div(g.by_page, rows) * g.page_size > 0;
+                if (fork_at(g, i, src, dst, rows) && !taken.has(dst)) x = rows - div(g.by_page, rows) * g.page_size > 0;
                 else atomicOr(g.err, ATTN_DEVERR_BAD_REQUEST);
                 if (!x) g.copies[i] = make_int4(-1, -1, 0, 0);
             }
             int total;
             const int before = need + block_scan(x, sm, total);
-            if (x) which[before] = i;
+            if (x) which[before] = (uint16_t)i;
             need += total;
         }
         __syncthreads();
@@ -279,7 +302,7 @@ __global__ void __launch_bounds__(kBookThreads) fork_kernel(const BookArgs g)
     const int warps = (gridDim.x - 1) * (kBookThreads / 32);
     for (int i = (blockIdx.x - 1) * (kBookThreads / 32) + (tid >> 5); i < g.n; i += warps) {
         int src, dst, rows;
-        if (!fork_at(g, i, src, dst, rows)) continue;
+        if (!fork_at(g, i, src, dst, rows) || taken.has(dst)) continue;
         const int full = div(g.by_page, rows);
         for (int e = tid & 31; e < full; e += 32) {
             int p = ld_dep(g.table + (size_t)src * g.max_pages + e);

@@ -49,14 +49,13 @@ attn_status attn_pages_resize(int32_t *refs, int n_pages, int32_t *block_table, 
  * it gets a page of its own, the lowest-numbered free one, by i, into which
  * attn_pages_copy brings the rows.
  *   src, dst, rows  int32 [n_fork], n_fork <= 4096. dst[i] holds no page before (its
- *                   entries are not looked at, and those past the rows not written);
- *                   no sequence is dst twice, or dst and src.
+ *                   entries are not looked at, and those past the rows not written)
  *   copies          int32 [n_fork][4], 16-byte aligned, written: (source page, page,
  *                   rows to copy, 0), or (-1, -1, 0, 0) where there is nothing to
  *                   copy -- the pages attn_pages_copy takes, for every layer's cache
  * A src or dst outside [0, n_seq), equal ones, or rows outside
  * [0, max_pages * page_size] set ATTN_DEVERR_BAD_REQUEST, and that fork is
- * skipped; an entry of src that is no page is shared as -1 (ATTN_DEVERR_BAD_PAGE); no
+ * skipped; so are, of the others, all whose dst is dst of another or src of one. An entry of src that is no page is shared as -1 (ATTN_DEVERR_BAD_PAGE); no
  * free page: the entry is -1 (ATTN_DEVERR_NO_PAGE).
  */
 attn_status attn_pages_fork(int32_t *refs, int n_pages, int32_t *block_table, int max_pages, int page_size,

@@ -134,6 +134,26 @@ def test_forks_that_are_none_are_skipped(pkg):
     same(b, refs, table)
 
 
+def test_forks_that_end_in_the_same_sequence_or_in_a_source(pkg):
+    """None of two with one dst, none whose dst is the src of another; an impossible fork counts for neither."""
+    refs, table = np.zeros(40, np.int32), np.full((70, 3), -1, np.int32)
+    have = np.zeros(70, np.int32)
+    have[:3] = 40, 48, 17
+    b = book(pkg, refs, table, 16)
+    b.resize(tt(np.zeros(70, np.int32)), tt(have))
+    tree.resize(refs, table, 16, [0] * 70, have)
+    pkg.attn_read_device_error()
+    src = np.int32([0, 1, 2, 1, 69, 0, 2, 0, 1])
+    dst = np.int32([3, 3, 4, 69, 5, 33, 33, 65, 65])
+    rows = np.int32([40, 20, 17, 48, 5, 40, 1, 20, 49])               # the last is none, so the one before it is
+    copies = b.fork(tt(src), tt(dst), tt(rows))
+    want, err = tree.fork(refs, table, 16, src, dst, rows)
+    assert err & 8 and pkg.attn_read_device_error() == err
+    np.testing.assert_array_equal(copies.cpu().numpy(), want)
+    same(b, refs, table)
+    assert (table[[3, 33, 69]] == -1).all() and (table[[4, 65], 0] >= 0).all()
+
+
 @pytest.mark.parametrize("kv", ["e4m3", "f16", "bf16"])
 @pytest.mark.parametrize("order", ["rows", "heads", "joint"])
 @pytest.mark.parametrize("hd,n_kv,page", [(64, 1, 16), (128, 3, 48), (256, 8, 64)])

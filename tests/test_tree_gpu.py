@@ -372,6 +372,29 @@ def test_long_context(pkg):
         assert float((out - want).norm() / want.norm()) < tol
 
 
+@pytest.mark.parametrize("kv,hd,nodes", [("bf16", 64, 9), ("f16", 128, 5), ("e4m3", 128, 16), ("bf16", 256, 20)])
+def test_many_runs_over_many_tiles(pkg, kv, hd, nodes):
+    """Warps that are late or early where one sequence ends and the next begins: equal bits from every run, and no wait
+    that gave up. Two KV heads, groups of 7: one or two units, some warps of them without a row."""
+    import torch
+    rng = np.random.default_rng(hd)
+    n_seq, page, ctx = 5, 64, 2048
+    per = ctx // page
+    shape = (n_seq * per, page, 2, hd)
+    vals = [rng.standard_normal(shape).astype(np.float32) for _ in range(2)]
+    k, v = (tt(x).to(torch.float8_e4m3fn if kv == "e4m3" else dtype(kv)) for x in vals)
+    scales = [torch.ones((n_seq * per, 2), device="cuda") for _ in range(2)] if kv == "e4m3" else []
+    cache = pkg.PagedCache(k, v, *scales)
+    table = tt(rng.permutation(n_seq * per).astype(np.int32).reshape(n_seq, per))
+    pos = tt(np.int32([ctx - 1, 700, 100, ctx - 130, 1291]))
+    q = tt(rng.standard_normal((n_seq * nodes, 14, hd)).astype(np.float32)).to(dtype("bf16" if kv == "bf16" else "f16"))
+    pkg.attn_read_device_error()
+    first = pkg.tree_decode_attention(cache, table, pos, q, n_splits=3)
+    for _ in range(60):
+        assert torch.equal(pkg.tree_decode_attention(cache, table, pos, q, n_splits=3), first)
+    assert pkg.attn_read_device_error() == 0
+
+
 def test_a_query_of_nan_stays_alone(pkg):
     import torch
     for src in ("f32", "f16"):

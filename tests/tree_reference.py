@@ -157,9 +157,11 @@ def fork(refs, table, page, src, dst, rows):
     n_seq, cap = table.shape[0], table.shape[1] * page
     copies, err = np.zeros((len(src), 4), np.int32), 0
     free = iter(np.flatnonzero(refs == 0).tolist())
+    ok = [0 <= f < n_seq and 0 <= t < n_seq and f != t and 0 <= r <= cap for f, t, r in zip(src, dst, rows)]
+    sources, ends = ([int(x) for x, y in zip(a, ok) if y] for a in (src, dst))
     for i, (f, t, r) in enumerate(zip(src, dst, rows)):
         copies[i] = (-1, -1, 0, 0)
-        if not (0 <= f < n_seq and 0 <= t < n_seq and f != t and 0 <= r <= cap):
+        if not ok[i] or t in sources or ends.count(t) > 1:
             err |= 8
             continue
         for e in range(r // page):
