@@ -1486,9 +1486,12 @@ __global__ void __launch_bounds__(128) attn_tree_combine(const TreeArgs a)
     // its sequence: the last one that begins at or before it, of those that have places
     int s = -1;
     int4 sp = make_int4(0, 0, 0, 0);
+    int64_t c1 = 0;                                            // the token behind its last
     for (int i0 = 0; i0 < a.n_seq; i0 += 32) {
         int4 q = make_int4(0, 0, 0x7fffffff, 0);
+        int upto = 0;
         if (i0 + lane < a.n_seq) {
+            if (a.cu) upto = ld_dep(a.cu + i0 + lane + 1);
             const uint4 u = ld_dep(reinterpret_cast<const uint4 *>(a.ws_span + i0 + lane));
             q = make_int4((int)u.x, (int)u.y, (int)u.z, (int)u.w);
         }
@@ -1498,11 +1501,11 @@ __global__ void __launch_bounds__(128) attn_tree_combine(const TreeArgs a)
             s = i0 + l;
             sp = make_int4(__shfl_sync(0xffffffffu, q.x, l), __shfl_sync(0xffffffffu, q.y, l), __shfl_sync(0xffffffffu, q.z, l),
                            __shfl_sync(0xffffffffu, q.w, l));
+            c1 = __shfl_sync(0xffffffffu, upto, l);
         }
     }
     if (s < 0) return;
-    int64_t c1 = (int64_t)(a.seq0 + s + 1) * a.n_each;
-    if (a.cu) c1 = min(max((int64_t)ld_dep(a.cu + s + 1), (int64_t)0), a.n_tokens);
+    c1 = a.cu ? min(c1, a.n_tokens) : (int64_t)(a.seq0 + s + 1) * a.n_each;
     if (tk >= c1 || gh >= a.group) return;
     const int slot = (int)(tk - sp.z) * a.group + gh, mu = slot / kTreeSlots;
     if (mu > 0) {                                              // the unit's own places
@@ -1515,7 +1518,7 @@ __global__ void __launch_bounds__(128) attn_tree_combine(const TreeArgs a)
     const int in_unit = slot - mu * kTreeSlots;
     float m = -INFINITY, S = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int BATCH = 4;
+    constexpr int BATCH = 8;
     for (int r = r0; r <= r1; r += BATCH) {
         float2 ml[BATCH];
         float4 v[BATCH];
