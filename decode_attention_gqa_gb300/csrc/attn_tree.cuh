@@ -26,8 +26,8 @@
 //
 // Work. A block serves one unit -- a KV head and 128 slots of it. The tiles that a unit has in all sequences are
 // laid end to end, and the unit's blocks (ranks; as many as make a block an SM) take equal runs of them, the turn to another
-// sequence counted as some more: what a block has of a sequence is its output where it has all of it, else a part (reference, sum, sum p v) for
-// attn_tree_combine. The KV heads of a rank run at the same time, so that the pieces of a row that they read are
+// sequence counted as some more: what a block has of a sequence is its output where it has all of it, else a part
+// (reference, sum, sum p v) for attn_tree_combine. The KV heads of a rank run at the same time, so that the pieces of a row that they read are
 // asked of memory together (one row of blocks over all units in turn took 1.9 times as long over 32 sequences of up
 // to 32768 rows).
 //
@@ -37,8 +37,8 @@
 // fetched from L2 a line at a time: both are written for few instructions.
 //
 // Measured (calls in a graph, the joining kernel among them): 32 sequences of 17 .. 32768 rows, trees of 5 to 16 nodes, 32/8 heads
-// of 128, e4m3, bf16 queries 213 us (1.09 GB, 5110 GB/s, 0.75 of a copy's rate); 8192 rows, 64 nodes, 28/4 heads 25.9 us; 4
-// sequences of up to 8400 rows, trees of 33 to 60 nodes, 16/2 heads of 256, capped scores, a window of 4096, bf16 34.8 us; 512
+// of 128, e4m3, bf16 queries 217 us (1.09 GB, 5020 GB/s, 0.74 of a copy's rate); 8192 rows, 64 nodes, 28/4 heads 25.2 us; 4
+// sequences of up to 8400 rows, trees of 33 to 60 nodes, 16/2 heads of 256, capped scores, a window of 4096, bf16 31.4 us; 512
 // rows, 8 nodes, 8/2 heads, f32 queries 15.6 us. Over long rows no unit alone bounds it: a tile of 128 rows and 128 slots takes
 // some 1600 cycles, the tensor cores 1170 of them (every slot of 128, with a node or not), a warpgroup half of its
 // 3200 for each of its own, converting V 880; with half the products, without the exponentials, the sums or the
@@ -959,23 +959,56 @@ struct Tree {
         return inv;
     }
 
-    // tanh near 0, |x| < 0.4: its series to x^11 (what follows is below 2^-23 of it)
-    static __device__ __forceinline__ float tanh_small(float x)
+    // tanh: near 0, |x| < 0.4, its series to x^11 (what follows is below 2^-23 of it); elsewhere 1 - 2 / (1 + e^2x), to 2^-22
+    static __device__ __forceinline__ float tanh_of(float x)
     {
-        const float z = x * x;
+        const float e = ex2(2.f * kLog2e * x), z = x * x;
+        const float l = e < 1e30f ? fmaf(-2.f, rcp(1.f + e), 1.f) : 1.f;
         float s = -8.8632355e-3f;                              // 1382 / 155925
         s = fmaf(s, z, 2.1869489e-2f);                         // 62 / 2835
         s = fmaf(s, z, -5.3968254e-2f);                        // 17 / 315
         s = fmaf(s, z, 1.3333333e-1f);                         // 2 / 15
         s = fmaf(s, z, -3.3333333e-1f);
-        return fmaf(s * z, x, x);
+        return fabsf(x) < 0.4f ? fmaf(s * z, x, x) : x == x ? l : x;
     }
-    // elsewhere 1 - 2 / (1 + e^2x), to 2^-22
-    static __device__ __forceinline__ float tanh_of(float x)
+    // 32 products, 16 with each factor, to capped scores: the series alone, in pairs, where no row with a slot leaves its range
+    // (a cap is seldom come near, and nothing is known of rows without a slot)
+    __device__ __forceinline__ void cap(const Row &r, uint32_t (&v)[32], float f0, float f1) const
     {
-        const float e = ex2(2.f * kLog2e * x);
-        const float l = e < 1e30f ? fmaf(-2.f, rcp(1.f + e), 1.f) : 1.f;
-        return fabsf(x) < 0.4f ? tanh_small(x) : x == x ? l : x;
+        uint64_t x[16];
+        float k = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float f = i < 8 ? f0 : f1;
+            x[i] = mul2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), pack2(f, f));
+            const float2 y = unpack2(x[i]);
+            k = fmaxf(fmaxf(k, fabsf(y.x)), fabsf(y.y));
+        }
+        if (__all_sync(0xffffffffu, k < 0.4f || r.t < 0)) {
+            auto both = [](float c) { return pack2(c, c); };
+            const uint64_t most = both(a.cap_log2);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint64_t z = mul2(x[i], x[i]), y = mul2(x[i], most);
+                uint64_t s = fma2(both(-8.8632355e-3f), z, both(2.1869489e-2f));
+                s = fma2(s, z, both(-5.3968254e-2f));
+                s = fma2(s, z, both(1.3333333e-1f));
+                s = fma2(s, z, both(-3.3333333e-1f));
+                x[i] = fma2(mul2(s, z), y, y);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float2 y = unpack2(x[i]);
+                x[i] = pack2(a.cap_log2 * tanh_of(y.x), a.cap_log2 * tanh_of(y.y));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float2 y = unpack2(x[i]);
+            v[2 * i] = __float_as_uint(y.x);
+            v[2 * i + 1] = __float_as_uint(y.y);
+        }
     }
 
     // The rows of 32 from tile row c0 on that the thread's node sees.
@@ -1010,22 +1043,14 @@ struct Tree {
     // Scores of those 32 with the rules, -inf where the node does not see the row.
     __device__ __forceinline__ void ruled(const TreeSeg &g, const Row &r, const volatile TileInfo *d, int c0, uint32_t (&v)[32]) const
     {
-        const float f0 = C::E8 ? r.c * d->ks[c0 >> 4] : r.c, f1 = C::E8 ? r.c * d->ks[(c0 >> 4) + 1] : r.c;
+        float f0 = C::E8 ? r.c * d->ks[c0 >> 4] : r.c, f1 = C::E8 ? r.c * d->ks[(c0 >> 4) + 1] : r.c;
+        if (a.softcap > 0.f) {
+            cap(r, v, f0, f1);
+            f0 = f1 = 1.f;
+        }
         float s[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c) s[c] = __uint_as_float(v[c]) * (c < 16 ? f0 : f1);
-        if (a.softcap > 0.f) {
-            float k = 0.f;
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) k = fmaxf(fmaxf(k, fabsf(s[c])), fabsf(s[c + 1]));
-            if (__all_sync(0xffffffffu, k < 0.4f || r.t < 0)) {   // a cap is seldom come near; nothing is known of rows without a slot
-#pragma unroll
-                for (int c = 0; c < 32; ++c) s[c] = a.cap_log2 * tanh_small(s[c]);
-            } else {
-#pragma unroll
-                for (int c = 0; c < 32; ++c) s[c] = a.cap_log2 * tanh_of(s[c]);
-            }
-        }
         if (a.slopes) {
             const float slope = ld_dep(a.slopes + r.h) * kLog2e;
             const int j0 = d->row0 + c0, y0 = j0 - g.base;
@@ -1118,7 +1143,10 @@ struct Tree {
         volatile float *refs = reinterpret_cast<volatile float *>(smem + C::OFF_REF);
         unsigned tiles = 0, refs_odd = 0;                      // tiles before the segment; parity of the references handed on
         Uses uses;
-        const bool rules = a.softcap > 0.f || a.slopes != nullptr || a.qscale <= 0.f;
+        // Over 16-bit caches, tiles with nothing but a cap are capped on their way to weights, others with rules before (31.4 us
+        // and not 33.5 for the heads of 256 dimensions above; over e4m3 the branch cost tiles without rules 4 %).
+        const bool capped = !C::E8 && a.softcap > 0.f && !a.slopes && a.qscale > 0.f;
+        const bool rules = !capped && (a.softcap > 0.f || a.slopes != nullptr || a.qscale <= 0.f);
         for (int p = from; p < end;) {
             TreeSeg g;
             const int next = segment(p, end, g);
@@ -1207,6 +1235,12 @@ struct Tree {
                     }
                     tmem_wait_ld(u);
                     tmem_wait_ld(v);
+                    if (capped && !slow) {
+                        cap(r, u, f[0], f[1]);
+                        cap(r, v, f[2], f[3]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) f[i] = 1.f;
+                    }
                     k[0] = fmaf(most16(u, 0), f[0], k[0]);
                     k[1] = fmaf(most16(u, 16), f[1], k[1]);
                     k[2] = fmaf(most16(v, 0), f[2], k[2]);
