@@ -395,6 +395,31 @@ def test_many_runs_over_many_tiles(pkg, kv, hd, nodes):
     assert pkg.attn_read_device_error() == 0
 
 
+def test_two_calls_at_once(pkg):
+    """On two streams, each with its own trees over one cache: the bits of the calls alone."""
+    import torch
+    rng = np.random.default_rng(5)
+    n_seq, page, per = 4, 32, 40
+    shape = (n_seq * per, page, 2, 128)
+    k, v = (tt(rng.standard_normal(shape).astype(np.float32)).half() for _ in range(2))
+    cache = pkg.PagedCache(k, v)
+    table = tt(rng.permutation(n_seq * per).astype(np.int32).reshape(n_seq, per))
+    calls = [(tt(np.int32(p)), tt(rng.standard_normal((n_seq, n, 8, 128)).astype(np.float32)).half())
+             for p, n in (([1279, 500, 64, 900], 6), ([1000, 31, 1200, 77], 30))]
+    alone = [pkg.tree_decode_attention(cache, table, p, q) for p, q in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[], []]
+    for _ in range(20):
+        for i, (p, q) in enumerate(calls):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(pkg.tree_decode_attention(cache, table, p, q))
+    torch.cuda.synchronize()
+    for want, outs in zip(alone, got):
+        assert all(torch.equal(x, want) for x in outs)
+    assert pkg.attn_read_device_error() == 0
+
+
 def test_a_query_of_nan_stays_alone(pkg):
     import torch
     for src in ("f32", "f16"):

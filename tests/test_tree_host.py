@@ -143,6 +143,24 @@ def test_bookkeeping_refuses_wrong_arguments(lib):
     assert lib.attn_pages_copy(_addr(_cache()), None, 0, None) == OK
 
 
+def test_bookkeeping_of_more_pages_than_it_counts_is_refused(lib):
+    assert _resize(lib, n_pages=(1 << 30) + 1) == UNSUPPORTED
+    assert _fork(lib, n_pages=(1 << 31) - 1) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("hd,nodes,splits,workspace", [
+    # 8 KV heads, groups of 4: 128 slots hold 32 nodes; an SM a block, 152 of them
+    (128, 32, 19, 19 * 2 * 8 * 128 * (128 + 2) * 4 + 256),
+    (128, 33, 9, 9 * 2 * 16 * 128 * (128 + 2) * 4 + 256),
+    (256, 200, 10, 10 * 2 * 56 * 128 * (256 + 2) * 4 + 256),     # 56 units: two rounds' worth would leave a quarter idle: four rounds
+])
+def test_plan_fills_the_sms(hd, nodes, splits, workspace):
+    """152 SMs, two sequences of up to 65536 rows."""
+    c = _cache(head_dim=hd, n_kv_head=8)
+    got = pkg.attn_tree_plan(ctypes.addressof(c), 65536 // c.page_size, 2, 2 * nodes, nodes, F16, 32, sm_count=152)
+    assert tuple(got) == (splits, workspace)
+
+
 def test_plan_refuses_what_the_call_does():
     def plan(cache=None, max_pages=8, n_seq=1, n_tokens=4, most=4, q_type=F32, n_head=8, P=0):
         c = cache or _cache()
