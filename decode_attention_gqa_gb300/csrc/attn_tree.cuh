@@ -32,9 +32,10 @@
 // to 32768 rows).
 //
 // Warps: 8 of the softmax; 4 that convert e4m3 tiles to f16, and, in tiles that some slot does not see all
-// of, take infinities and NaN out of V (a weight of 0 would spread them); a producer of K and one of V (pages, TMA); an
-// issuer of each product. What a single warp does for each tile takes some 8 cycles an instruction, and code that runs once is
-// fetched from L2 a line at a time: both are written for few instructions.
+// of, take infinities and NaN out of V (a weight of 0 would spread them; where a block's part of the sequence ends, the
+// softmax gives them to the slots that see them); a producer of K and one of V (pages, TMA); an issuer of each product. What a
+// single warp does for each tile takes some 8 cycles an instruction, and code that runs once is fetched from L2 a line at a
+// time: both are written for few instructions.
 //
 // Measured (calls in a graph, the joining kernel among them): 32 sequences of 17 .. 32768 rows, trees of 5 to 16 nodes, 32/8 heads
 // of 128, e4m3, bf16 queries 217 us (1.09 GB, 5020 GB/s, 0.74 of a copy's rate); 8192 rows, 64 nodes, 28/4 heads 25.2 us; 4
@@ -90,7 +91,7 @@ struct TreeCfg {
     static constexpr uint32_t OFF_DESC = DATA;
     static constexpr uint32_t OFF_BAR = OFF_DESC + kTreeDesc * 128;
     static constexpr int NBAR = 50 + kTreeDesc;
-    static constexpr uint32_t OFF_FLAG = OFF_BAR + NBAR * 8;   // TMEM slot, abort, share, the block's first tile and the one behind it
+    static constexpr uint32_t OFF_FLAG = OFF_BAR + NBAR * 8;   // TMEM slot, abort, share, the block's first tile and the one behind it, wild segments
     static constexpr uint32_t OFF_SEQ = OFF_FLAG + 32;         // before, first token, places before, rows
     static constexpr uint32_t OFF_REF = OFF_SEQ + (4 * kTreeSeqs + 4) * 4;   // references of 128 slots
     static constexpr uint32_t SMEM = OFF_REF + 128 * 4;
@@ -103,7 +104,7 @@ struct __align__(16) TileInfo {
     int edge;                 // some slot does not see all of it
     unsigned slices;          // 16-row slices that are there
     int live;                 // rows of it that belong to the sequence
-    unsigned bad[4];          // rows with an infinity or NaN in V that was taken out (edge tiles)
+    unsigned unused[4];       // the scales in 16-byte loads
     float ks[8], vs[8];       // scales of its slices
     float lv[8];              // log2 of the V scales, rounded up
 };
@@ -325,7 +326,8 @@ struct Tree {
     __device__ __forceinline__ uint32_t q_ready() const { return bar(48); }
     __device__ __forceinline__ uint32_t described(unsigned tile) const { return bar(50 + (tile & (kTreeDesc - 1))); }
     __device__ __forceinline__ uint32_t met() const { return bar(49); }
-    // [0] tensor memory, [1] abort, [2] places of a rank, [3], [4] its first tile and the one behind its last
+    // [0] tensor memory, [1] abort, [2] places of a rank, [3], [4] its first tile and the one behind its last, [5] segments (bit
+    // i: the i-th, modulo 32) of whose V infinities or NaN were taken out
     __device__ __forceinline__ volatile int *flags() const { return reinterpret_cast<volatile int *>(smem + C::OFF_FLAG); }
     __device__ __forceinline__ int *before() const { return reinterpret_cast<int *>(smem + C::OFF_SEQ); }   // tiles before each sequence
     __device__ __forceinline__ int *tok() const { return before() + kTreeSeqs + 1; }                         // first tokens
@@ -595,7 +597,6 @@ struct Tree {
                                           (negative >> (i * C::NSLC) & TILE_BITS ? 2 : 0);
                                 d->slices = mine;
                                 d->live = g.nkv - r;
-                                *reinterpret_cast<uint4 *>(d->bad) = make_uint4(0u, 0u, 0u, 0u);
                             }
                         }
                     }
@@ -653,7 +654,7 @@ struct Tree {
     {
         const int lane = tid & 31;
         Ring vr{0, 0}, vs{0, C::E8 ? 1u : 0u}, kr{0, 0}, ks{0, 1};
-        unsigned tiles = 0;
+        unsigned tiles = 0, segs = 0;
         auto key = [&] {                                       // K of the next tile
             convert<false>(kr, ks, tid);
             fence_proxy_async_smem();
@@ -665,7 +666,7 @@ struct Tree {
             kr.next(a.nrk);
             ks.next(a.nk);
         };
-        for (int p = from; p < end;) {
+        for (int p = from; p < end; ++segs) {
             TreeSeg g;
             p = segment(p, end, g);
             const int T = g.t1 - g.t0;
@@ -686,15 +687,18 @@ struct Tree {
                 if (look) {                                    // the units that this thread has written, where it has
                     const int u = tid % UPR * 2;
                     const uint32_t to = v_slot(vs.at) + (u >> 3) * (TR * 128);
+                    bool wild = false;
 #pragma unroll 1
                     for (int r = tid / UPR ^ (u >> 3 & 1); r < TR; r += RSTEP) {
                         const uint32_t p0 = to + r * 128 + (((u ^ r) & 7) << 4), p1 = to + r * 128 + ((((u + 1) ^ r) & 7) << 4);
                         uint4 y0 = lds128(p0), y1 = lds128(p1);
-                        if (clean(d, r, y0, y1)) {
+                        if (clean(d, r, y0, y1, wild)) {
                             sts128(p0, y0);
                             sts128(p1, y1);
                         }
                     }
+                    // before V is ready, behind whose products the softmax looks
+                    if (wild) atomicOr(reinterpret_cast<unsigned *>(const_cast<int *>(flags())) + 5, 1u << (segs & 31));
                 }
                 if (C::E8 || look) fence_proxy_async_smem();
                 __syncwarp();
@@ -710,8 +714,8 @@ struct Tree {
     }
 
     // Sixteen elements of V of tile row r: what belongs to no row of the sequence, and infinities and NaN, become 0.
-    // Whether anything changed.
-    static __device__ __forceinline__ bool clean(TileInfo *d, int r, uint4 &y0, uint4 &y1)
+    // Whether anything changed; wild: whether there was an infinity or NaN.
+    static __device__ __forceinline__ bool clean(const TileInfo *d, int r, uint4 &y0, uint4 &y1, bool &wild)
     {
         const volatile TileInfo *vd = d;
         if (r >= vd->live || !(vd->slices >> (r >> 4) & 1)) {
@@ -729,7 +733,7 @@ struct Tree {
             found = found || keep != 0xffffffffu;
             *w[i] &= keep;
         }
-        if (found) atomicOr(&d->bad[r >> 5], 1u << (r & 31));
+        wild = wild || found;
         return found;
     }
 
@@ -1011,11 +1015,11 @@ struct Tree {
         }
     }
 
-    // The rows of 32 from tile row c0 on that the thread's node sees.
-    __device__ __forceinline__ unsigned seen_bits(const TreeSeg &g, const Row &r, const volatile TileInfo *d, int c0) const
+    // Of the 32 rows from j0 on those that the thread's node sees; there: the two 16-row slices of them that are.
+    __device__ __forceinline__ unsigned seen_bits(const TreeSeg &g, const Row &r, int j0, unsigned there) const
     {
         if (r.t < 0) return 0u;
-        const int j0 = d->row0 + c0, y0 = j0 - g.base;
+        const int y0 = j0 - g.base;
         unsigned bits = bit_range(low_of(r.x, g.start) - j0, g.base - j0);
         if (y0 > -32 && y0 < g.n) {
             unsigned dr;
@@ -1036,7 +1040,6 @@ struct Tree {
                 }
             bits |= dr;
         }
-        const unsigned there = d->slices >> (c0 >> 4) & 3u;
         return bits & ((there & 1u ? 0xffffu : 0u) | (there & 2u ? 0xffff0000u : 0u));
     }
 
@@ -1067,7 +1070,7 @@ struct Tree {
             }
         }
         if (d->edge & 1) {
-            const unsigned bits = seen_bits(g, r, d, c0);
+            const unsigned bits = seen_bits(g, r, d->row0 + c0, d->slices >> (c0 >> 4) & 3u);
 #pragma unroll
             for (int c = 0; c < 32; ++c) s[c] = bits >> c & 1 ? s[c] : -INFINITY;
         }
@@ -1096,43 +1099,61 @@ struct Tree {
         tmem_wait_st();
     }
 
-    // Rows of V that hold infinities or NaN: to the slots that see them, in the dimensions that do. (A weight changes
-    // neither.)
-    __device__ __forceinline__ void add_bad(const TreeSeg &g, const volatile TileInfo *d, uint32_t s_at, uint32_t o)
+    // At the end of a segment, when its products are done: infinities and NaN that were taken out of V, added to half w of O's
+    // dimensions of the slots that see their rows. (A weight changes neither. Where every slot sees a tile they were left in and
+    // are in O already; once more is the same.) By a scan of the segment, 32 rows at a time: it is seldom done. (A note of the rows
+    // with each tile, for its softmax, needs a wait for V in every tile with an edge: 2 to 4 % of a call.)
+    __device__ __forceinline__ void add_wild(const TreeSeg &g, const Row &r, uint32_t o, int w, int lane)
     {
+        const uint32_t EXP = C::E8 ? 0x7F7F7F7Fu : std::is_same<MT, __half>::value ? 0x7C007C00u : 0x7F807F80u;
+        constexpr int ES = C::E8 ? 1 : 2;
+        const int low = low_of(g.base, g.start), end = min(g.row0 + g.t1 * TR, g.nkv);
 #pragma unroll 1
-        for (int w = 0; w < TR / 32; ++w)
+        for (int j0 = g.row0 + g.t0 * TR; j0 < end; j0 += 32) {
+            const int j = j0 + lane, pg = div(a.by_page, j);
+            const int page = j >= low && j < end ? ld_dep(a.table + (size_t)g.s * a.max_pages + pg) : -1;
+            const bool there = (unsigned)page < (unsigned)a.n_pages;
+            const uint8_t *row = static_cast<const uint8_t *>(a.v) +
+                                 (page * a.page_stride + (j - pg * a.page_size) * a.row_stride + hk() * a.head_stride + w * (HD / 2)) * ES;
+            bool wild = false;
 #pragma unroll 1
-            for (unsigned m = d->bad[w]; m; m &= m - 1) {
-                const int r = w * 32 + __ffs(m) - 1, j = d->row0 + r, pg = div(a.by_page, j);
-                const int page = ld_dep(a.table + (size_t)g.s * a.max_pages + pg);
-                const int64_t at = page * a.page_stride + (j - pg * a.page_size) * a.row_stride + hk() * a.head_stride;
-                uint32_t sv, dummy;
-                tmem_ld2(s_at + (r & ~1), sv, dummy);
-                if (r & 1) sv = dummy;
-                const bool sees = __uint_as_float(sv) != -INFINITY;
+            for (int u = 0; there && u < HD / 2 * ES; u += 16) {
+                const uint4 x = ld_dep(reinterpret_cast<const uint4 *>(row + u));
+                const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    wild = wild || (C::E8 ? __vcmpeq4(y[i] & EXP, EXP) : __vcmpeq2(y[i] & EXP, EXP)) != 0;
+            }
+            const unsigned seen = seen_bits(g, r, j0, 3u);
+            __syncwarp();
 #pragma unroll 1
-                for (int c = 0; c < HD; c += 32) {
+            for (unsigned m = __ballot_sync(0xffffffffu, wild); m; m &= m - 1) {
+                const int at = __ffs(m) - 1;
+                const uint8_t *from = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(row), at));
+                const bool sees = seen >> at & 1;
+#pragma unroll 1
+                for (int c = 0; c < HD / 2; c += 32) {
                     uint32_t v[32];
-                    tmem_ld32(o + c, v);
+                    tmem_ld32(o + w * (HD / 2) + c, v);
                     tmem_wait_ld(v);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         float x;
                         if constexpr (C::E8) {
                             uint32_t lo, hi;
-                            e4m3x4_to_half4((uint32_t)static_cast<const uint8_t *>(a.v)[at + c + i], lo, hi);
+                            e4m3x4_to_half4((uint32_t)from[c + i], lo, hi);
                             x = kv2_to_float2<__half>(lo).x;
                         } else {
-                            x = kv2_to_float2<MT>((uint32_t)static_cast<const uint16_t *>(a.v)[at + c + i]).x;
+                            x = kv2_to_float2<MT>((uint32_t)reinterpret_cast<const uint16_t *>(from)[c + i]).x;
                         }
                         if (sees && !(fabsf(x) < INFINITY)) v[i] = __float_as_uint(x + __uint_as_float(v[i]));
                     }
                     __syncwarp();
-                    tmem_st32(o + c, v);
+                    tmem_st32(o + w * (HD / 2) + c, v);
                 }
                 tmem_wait_st();
             }
+        }
     }
 
     __device__ __forceinline__ void softmax(uint32_t tm, int from, int end, int w, int quad, int lane, int rank)
@@ -1141,7 +1162,7 @@ struct Tree {
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const int my = quad * 32 + lane;
         volatile float *refs = reinterpret_cast<volatile float *>(smem + C::OFF_REF);
-        unsigned tiles = 0, refs_odd = 0;                      // tiles before the segment; parity of the references handed on
+        unsigned tiles = 0, segs = 0, refs_odd = 0;            // tiles and segments before this one; parity of the references handed on
         Uses uses;
         // Over 16-bit caches, tiles with nothing but a cap are capped on their way to weights, others with rules before (31.4 us
         // and not 33.5 for the heads of 256 dimensions above; over e4m3 the branch cost tiles without rules 4 %).
@@ -1195,12 +1216,6 @@ struct Tree {
                         tmem_st32(s_at + c, v);
                     }
                     tmem_wait_st();
-                    if ((edge & 1) && __any_sync(0xffffffffu, d->bad[0] | d->bad[1] | d->bad[2] | d->bad[3]) && !ended()) {
-                        // O stands still from the product before to this one
-                        if (t > 0) wait(o_done(Uses::buffer(t - 1)), uses.parity(t - 1));
-                        tc_fence_after();
-                        add_bad(g, d, s_at, o_at);
-                    }
                 }
                 // P, by the reference as it is: that of the tile before may be larger by now, which is seen to at the end
                 const float c = slow ? 1.f : r.c;
@@ -1293,8 +1308,17 @@ struct Tree {
             if (any) wait(o_done(Uses::buffer(T - 1)), uses.parity(T - 1));
             uses.end(T);
             if (any) refs_odd ^= T & 1;
+            const unsigned wild = 1u << (segs++ & 31);
+            const bool is_wild = __any_sync(0xffffffffu, flags()[5] & wild);
+            if (is_wild && any && !ended()) {
+                tc_fence_after();
+                add_wild(g, r, o_at, w, lane);
+            }
             // a slot whose every score is NaN keeps its NaN sum
             finish(tm, g, r, w, quad, lane, whole, begins, rank, m == -INFINITY && l != 0.f ? 0.f : m - OFF, l, any);
+            // for the segment 32 behind: V is never that far ahead
+            if (is_wild && w == 0 && quad == 0 && lane == 0)
+                atomicAnd(reinterpret_cast<unsigned *>(const_cast<int *>(flags())) + 5, ~wild);
             tiles += T;
             p = next;
         }
@@ -1447,6 +1471,7 @@ attn_tree_stream(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             bar_init(x.met(), C::SM_WARPS);
             for (int i = 0; i < kTreeDesc; ++i) bar_init(x.described(i), 1);
             x.flags()[1] = 0;
+            x.flags()[5] = 0;
             fence_barrier_init();
             prefetch_tensormap(&kmap);
             prefetch_tensormap(&vmap);

@@ -264,6 +264,53 @@ def test_unseen_infinities_and_nan(pkg, kv, src, hd):
             assert bool(out[t].isfinite().all()) == (depths[0][t] >= 2), (t, depths[0][t])
 
 
+@pytest.mark.parametrize("src", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("kv", ["e4m3", "f16", "bf16"])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_infinities_and_nan_in_v_alone(pkg, kv, src, hd):
+    """K is finite, V is not in some dimensions of two nodes and of a row beside `starts`: those dimensions of the nodes
+    that see them, and nothing else, with equal bits from every run. Over many tiles, as parts and as a whole."""
+    import torch
+    ctx, nodes, n_head, n_words = (1300, 37, 2100), (20, 9, 33), 8, 2
+    pool = Pool(21, kv, 2, hd, 32, ctx)
+    parents, sees, depths, mask = setup(9, nodes, n_words)
+    rng = np.random.default_rng(3)
+    starts = [5, 0, 900]
+    put = [(0, 1280 + 4, 3, 5), (0, 1280 + 11, hd - 1, hd), (1, 28 + 2, 8, 9), (2, 2067 + 13, 0, 2), (2, 900, 30, 34)]
+    k, v = pool.rows(0), pool.rows(1)
+    for i, (s, row, d0, d1) in enumerate(put):
+        p, o = int(pool.table[s, row // 32]), row % 32
+        d = pool.dev[1].view(torch.uint8) if kv == "e4m3" else pool.dev[1]
+        d[p, o, :, d0:d1] = 0x7F if kv == "e4m3" else (math.nan if i == 1 else math.inf)
+        v[s][row, :, d0:d1] = 0.0
+    t, cu = sum(nodes), np.cumsum((0,) + nodes)
+    wild = np.zeros((t, hd), bool)                                # what cannot be finite
+    for s, row, d0, d1 in put:
+        y = row - (ctx[s] - nodes[s])
+        who = [cu[s] + x for x in range(nodes[s]) if y < 0 or y in sees[s][x]]
+        assert who
+        wild[who, d0:d1] = True
+    for s, row, d0, d1 in put[:4]:                                # nobody sees all of them, some see one alone
+        assert not wild[cu[s]:cu[s + 1], d0].all()
+    q = tt(rng.standard_normal((t, n_head, hd)).astype(np.float32)).to(dtype(src))
+    qh = q.double().cpu().numpy()
+    want, bound = (np.concatenate(x) for x in tree.attend(
+        [qh[cu[s]:cu[s + 1]] for s in range(3)], sees, depths, k, v, hd ** -0.5, kv, src, vmax=vmax_of(pool, v), starts=starts))
+    a = [pool.cache(pkg), tt(pool.table), tt(np.int32(ctx) - 1), q]
+    kw = dict(mask=tt(mask), depths=tt(flat(depths)), cu_tokens=tt(cu.astype(np.int32)), max_nodes=max(nodes),
+              starts=tt(np.int32(starts)))
+    bits = torch.int32 if src == "f32" else torch.int16
+    there = tt(wild)[:, None, :].expand(t, n_head, hd)
+    pkg.attn_read_device_error()
+    for P in (1, 0, 2, 7):
+        first = pkg.tree_decode_attention(*a, n_splits=P, **kw)
+        assert bool((first.isfinite() == ~there).all())
+        check(torch.where(there, torch.zeros_like(first), first), np.where(wild[:, None], 0.0, want), bound, "P=%d" % P)
+        for _ in range(10):
+            assert torch.equal(pkg.tree_decode_attention(*a, n_splits=P, **kw).view(bits), first.view(bits))
+    assert pkg.attn_read_device_error() == 0
+
+
 @pytest.mark.parametrize("kv", ["e4m3", "f16"])
 def test_pages_that_are_not_there(pkg, kv):
     pool = Pool(9, kv, 2, 128, 32, (200, 70, 40))
