@@ -924,6 +924,8 @@ def tree_decode_attention(cache, block_table, positions, q, mask=None, depths=No
         mask = _ints("mask", mask, (n_tokens, words), index, device)
     rules = None
     if softcap or window or slopes is not None or starts is not None:
+        if not 0 <= window < 1 << 31:                     # the plan does not know it
+            raise ValueError("window must be a non-negative 32-bit integer")
         if slopes is not None and not (slopes.dtype is f32 and slopes.get_device() == index and
                                        slopes.shape == (n_head,) and slopes.is_contiguous()):
             _refuse((("slopes", slopes, f32, True),), device, ((False, "slopes must be [n_head]"),))
@@ -938,8 +940,8 @@ def tree_decode_attention(cache, block_table, positions, q, mask=None, depths=No
     key = (max_pages, n_seq, n_tokens, max_nodes, q_type, n_head, n_splits, "tree")
     plan = cache._plans.get(key)
     if plan is None:
-        if not (0 <= window < 1 << 31 and 0 <= n_splits < 1 << 31 and 0 < max_nodes < 1 << 31):
-            raise ValueError("window, n_splits and max_nodes must be non-negative 32-bit integers")
+        if not (0 <= n_splits < 1 << 31 and 0 < max_nodes < 1 << 31):
+            raise ValueError("n_splits and max_nodes must be non-negative 32-bit integers")
         if len(cache._plans) >= 4096:
             cache._plans.clear()
         plan = cache._plans[key] = attn_tree_plan(cache, max_pages, n_seq, n_tokens, max_nodes, q_type, n_head,

@@ -10,7 +10,7 @@ import pytest
 import decode_attention_gqa_gb300 as pkg
 import tree_reference as tree
 from decode_attention_gqa_gb300 import build as cuda_build
-from test_paged_host import CACHE_FAULTS, _addr, _cache
+from test_paged_host import CACHE_FAULTS, _addr, _cache, _pool_and_ids, door     # noqa: F401  (door is a fixture)
 
 INVALID, UNSUPPORTED, OK = pkg.ATTN_ERR_INVALID_ARG, pkg.ATTN_ERR_UNSUPPORTED, pkg.ATTN_OK
 F32, F16, BF16, E4M3 = range(4)
@@ -195,6 +195,23 @@ def test_torch_forms_refuse_before_any_call():
             pkg.tree_decode_attention(cache, table, pos, *args, **kw)
     with pytest.raises(ValueError):
         pkg.rope_append(cache, table, pos, torch.zeros(2, 2, 64), torch.zeros(2, 2, 64), depths=torch.zeros(2, **i32))
+
+
+def test_a_window_is_refused_whatever_was_called_before(door):     # noqa: F811
+    """The plan does not depend on the window, so a call of the same shape must not let one past 32 bits through, which would
+    arrive as another: 2^32 as none."""
+    import torch
+    cache, table, pos = _pool_and_ids()
+    q = torch.zeros(3, 4, 64)
+    for _ in range(2):
+        n = len(door.calls)
+        for window in (2 ** 31, 2 ** 32, 2 ** 32 + 16, -1, -2 ** 32):
+            with pytest.raises(ValueError, match="window"):
+                pkg.tree_decode_attention(cache, table, pos, q, window=window)
+        assert len(door.calls) == n
+        pkg.tree_decode_attention(cache, table, pos, q)
+        pkg.tree_decode_attention(cache, table, pos, q, window=2 ** 31 - 1)
+        assert door.calls[-1][0] == "attn_decode_tree"
 
 
 def test_headers_and_binding_agree(lib):
