@@ -1,5 +1,8 @@
 // attn_pages.cu -- the page bookkeeping of include/attn_pages.h: its C ABI, the kernels that release and
 // give out pages and share them between sequences, and the copy of pages.
+#include <map>
+#include <mutex>
+
 #include "attn_device.cuh"
 #include "attn_launch.h"
 #include "attn_pages.h"
@@ -226,6 +229,34 @@ __global__ void __launch_bounds__(kBookThreads) resize_kernel(const BookArgs g)
     }
 }
 
+// Blocks of the resizing cluster: 16, or where the current device (a share of one) holds no such cluster, the largest power of
+// two below that it holds. The kernel takes any number. Asked once per device.
+cudaError_t resize_blocks(const void *fn, unsigned *blocks)
+{
+    static std::mutex mu;
+    static std::map<int, unsigned> known;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    const auto it = known.find(dev);
+    if (it != known.end()) {
+        *blocks = it->second;
+        return cudaSuccess;
+    }
+    constexpr int smem = (2 * kMaxResize + 1) * 4;             // of the most sequences
+    e = ensure_smem_attr(fn, smem);
+    if (e != cudaSuccess) return e;
+    unsigned n = kBookCluster;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+        (void)cudaGetLastError();
+        n = 8;                                                 // the largest portable one
+    }
+    while (n > 1 && cluster_slots(fn, dim3(kBookThreads), smem, n) < 1) n /= 2;
+    known[dev] = *blocks = n;
+    return cudaSuccess;
+}
+
 __device__ __forceinline__ bool fork_at(const BookArgs &g, int i, int &src, int &dst, int &rows)
 {
     src = ld_dep(g.a + i);
@@ -420,12 +451,10 @@ attn_status attn_pages_resize(int32_t *refs, int n_pages, int32_t *block_table, 
     g.n_seq = g.n = n_seq;
     g.by_page = fast_div((unsigned)page_size);
     const void *fn = reinterpret_cast<const void *>(&resize_kernel);
-    e = ensure_smem_attr(fn, (2 * kMaxResize + 1) * 4);
+    unsigned blocks = 0;
+    e = resize_blocks(fn, &blocks);
     if (e != cudaSuccess) return fail(e);
     void *args[] = {&g};
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return fail(e);
-    constexpr unsigned blocks = kBookCluster;
     e = launch_pdl_cluster(fn, dim3(blocks), dim3(kBookThreads), (2 * (size_t)n_seq + 1) * 4, reinterpret_cast<cudaStream_t>(stream),
                            args, blocks);
     return e == cudaSuccess ? ATTN_OK : fail(e);

@@ -1,12 +1,20 @@
 """GPU: the page bookkeeping against the restatement in tree_reference.py: tables and counts are equal to the
 last entry, copied pages to the last bit."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
+
+if __name__ == "__main__":
+    sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 import tree_reference as tree
 from test_paged_gpu import Pool, pkg, tt        # noqa: F401  (pkg is the fixture)
 
 pytestmark = pytest.mark.gpu
+CUDA_INCLUDE = "/usr/local/cuda/include"
 
 
 def book(pkg, refs, table, page):
@@ -39,6 +47,39 @@ def test_resize(pkg, n_seq, n_pages, max_pages, page):
         same(b, refs, table)
         assert pkg.attn_read_device_error() == err
         have = want
+
+
+SMALLER = """
+#include <cuda_runtime.h>
+static int asked = 0;
+extern "C" int times_asked() { return asked; }
+namespace attn {
+int cluster_slots(const void *, dim3, size_t, unsigned cluster_x) { ++asked; return cluster_x <= %d ? 1 : 0; }
+}
+"""
+
+
+@pytest.mark.parametrize("most", [0, 1, 2, 8])
+def test_resize_where_no_cluster_of_16_blocks_fits(most, tmp_path):
+    """As on a share of a device: the question how many clusters it holds is answered by a library that is loaded before
+    (0: by nobody), the same steps give the same tables, and it is asked once per size."""
+    shim = tmp_path / "shim.so"
+    (tmp_path / "shim.cpp").write_text(SMALLER % most)
+    subprocess.run(["g++", "-shared", "-fPIC", "-I", CUDA_INCLUDE, str(tmp_path / "shim.cpp"), "-o", str(shim)], check=True)
+    res = subprocess.run([sys.executable, __file__, str(shim)], capture_output=True, text=True, timeout=300,
+                         cwd=os.path.dirname(os.path.abspath(__file__)))
+    assert res.returncode == 0, res.stdout + res.stderr
+    assert res.stdout.split() == ["asked", str({0: 4, 1: 4, 2: 4, 8: 2}[most])]
+
+
+def _resize_with(shim):
+    import ctypes
+    lib = ctypes.CDLL(shim, mode=ctypes.RTLD_GLOBAL)
+    import decode_attention_gqa_gb300 as package
+    package.load()
+    for shape in ((1, 5, 9, 16), (33, 300, 20, 64), (1500, 20011, 16, 16), (40, 16385, 500, 1024)):
+        test_resize(package, *shape)
+    print("asked", lib.times_asked())
 
 
 def test_resize_out_of_range(pkg):
@@ -217,3 +258,7 @@ def test_bookkeeping_in_a_graph_and_on_a_stream_of_the_callers(pkg):
         h = w
         h[7:] = r
     pkg.attn_read_device_error()
+
+
+if __name__ == "__main__":
+    _resize_with(sys.argv[1])
