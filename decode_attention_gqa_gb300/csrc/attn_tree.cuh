@@ -410,6 +410,9 @@ struct Tree {
     __device__ __forceinline__ int hk() const { return blockIdx.x % a.n_kv_head; }
     __device__ __forceinline__ int first_slot() const { return blockIdx.x / a.n_kv_head * kTreeSlots; }
 
+    // First row that is not masked; not below 0, so that differences to rows fit into 32 bits
+    __device__ __forceinline__ int start_of(int s) const { return a.starts ? max(ld_dep(a.starts + s), 0) : 0; }
+
     // Rows of a sequence that some node may see: [low, high)
     __device__ __forceinline__ int low_of(int base, int start) const
     {
@@ -436,7 +439,7 @@ struct Tree {
         g.n = tok()[lo + 1] - g.tok0;
         g.nkv = rows()[lo];
         g.base = g.nkv - g.n;
-        g.start = a.starts ? ld_dep(a.starts + lo) : 0;
+        g.start = start_of(lo);
         g.T = before()[lo + 1] - before()[lo];
         g.t0 = p - before()[lo];
         g.t1 = min(g.T, g.t0 + end - p);
@@ -467,7 +470,7 @@ struct Tree {
                 c0 = min(max((int64_t)ld_dep(a.cu + s), (int64_t)0), a.n_tokens);
                 c1 = min(max((int64_t)ld_dep(a.cu + s + 1), (int64_t)0), a.n_tokens);
             }
-            const int start = a.starts ? ld_dep(a.starts + s) : 0;
+            const int start = start_of(s);
             int n = (int)max(c1 - c0, (int64_t)0);
             tok()[s] = (int)c0;
             if (s == a.n_seq - 1) tok()[s + 1] = (int)max(c1, c0);

@@ -199,6 +199,24 @@ def test_score_rules(pkg, kv, hd, src, rules, group):
     tree_check(pkg, pool, nodes, 2 * group, src, chain=True, **r)
 
 
+@pytest.mark.parametrize("kv,hd", [("e4m3", 128), ("f16", 64), ("bf16", 256)])
+def test_starts_before_the_first_row_mask_nothing(pkg, kv, hd):
+    """Down to the smallest 32-bit number, as one may write where there is no start."""
+    import torch
+    ctx, nodes = (700, 300, 40, 515), (20, 33, 12, 7)
+    pool = Pool(23, kv, 2, hd, 32, ctx)
+    parents, sees, depths, mask = setup(4, nodes, 2)
+    rng = np.random.default_rng(2)
+    q = tt(rng.standard_normal((sum(nodes), 6, hd)).astype(np.float32))
+    a = [pool.cache(pkg), tt(pool.table), tt(np.int32(ctx) - 1), q]
+    cu = tt(np.cumsum((0,) + nodes).astype(np.int32))
+    for kw in (dict(mask=tt(mask), depths=tt(flat(depths))), {}):
+        kw.update(cu_tokens=cu, max_nodes=33, n_splits=3)
+        plain = pkg.tree_decode_attention(*a, **kw)
+        for starts in ([-1] * 4, [-2 ** 31] * 4, [-2 ** 31 + 1, -2 ** 31 + 600, -2 ** 30, 0]):
+            assert torch.equal(pkg.tree_decode_attention(*a, starts=tt(np.int32(starts)), **kw), plain)
+
+
 @pytest.mark.parametrize("src", ["f32", "bf16"])
 @pytest.mark.parametrize("kv", ["e4m3", "f16", "bf16"])
 def test_masks_of_any_bits_and_rows_that_see_nothing(pkg, kv, src):
