@@ -199,7 +199,8 @@ attn_status attn_decode_tree(const attn_paged_cache *cache, const int32_t *block
     a.n_pages = cache->n_pages;
     a.page_size = cache->page_size;
     a.cap = max_pages * cache->page_size;
-    a.window = window > a.cap ? 0 : window;        // past the capacity it masks nothing
+    // past every distance it masks nothing: a node may be as deep as max_nodes - 1 behind the last row
+    a.window = window >= a.cap + max_nodes ? 0 : window;
     a.ranks = pl.n_splits;
     a.once = (int64_t)max_nodes * a.group <= attn::kTreeSlots;
     a.qscale = qscale;

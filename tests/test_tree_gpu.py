@@ -200,6 +200,27 @@ def test_score_rules(pkg, kv, hd, src, rules, group):
 
 
 @pytest.mark.parametrize("kv,hd", [("e4m3", 128), ("f16", 64), ("bf16", 256)])
+def test_windows_and_nodes_deeper_than_the_capacity(pkg, kv, hd):
+    """A node's position may lie past the cache's last row, so a window longer than the cache can mask some of it."""
+    import torch
+    pool = Pool(24, kv, 1, hd, 16, (64, 50))                      # 64 rows of capacity
+    depths = [[0, 70, 1023, 7], [5, 900, 33]]
+    sees = [[[0], [0, 1], [0, 1, 2], [3, 0]], [[0], [1, 0], [0, 2]]]
+    mask = np.concatenate([tree.words(s, 32) for s in sees])
+    cu = np.int32([0, 4, 7])
+    q = tt(np.random.default_rng(3).standard_normal((7, 4, hd)).astype(np.float32))
+    qh = q.double().cpu().numpy()
+    k, v = pool.rows(0), pool.rows(1)
+    for window in (64, 65, 66, 90, 1000, 1064, 1083, 1084, 1087, 1088, 2 ** 31 - 1):
+        want, bound = tree.attend([qh[:4], qh[4:]], sees, depths, k, v, hd ** -0.5, kv, "f32", vmax=vmax_of(pool, v),
+                                  window=window)
+        for P in (1, 2):
+            out = pkg.tree_decode_attention(pool.cache(pkg), tt(pool.table), tt(np.int32([63, 49])), q, mask=tt(mask),
+                                            depths=tt(flat(depths)), cu_tokens=tt(cu), max_nodes=1024, window=window, n_splits=P)
+            check(out, np.concatenate(want), np.concatenate(bound), "window %d" % window)
+
+
+@pytest.mark.parametrize("kv,hd", [("e4m3", 128), ("f16", 64), ("bf16", 256)])
 def test_starts_before_the_first_row_mask_nothing(pkg, kv, hd):
     """Down to the smallest 32-bit number, as one may write where there is no start."""
     import torch
