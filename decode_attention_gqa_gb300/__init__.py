@@ -921,6 +921,8 @@ def tree_decode_attention(cache, block_table, positions, q, mask=None, depths=No
     words = 0
     if mask is not None:
         words = mask.shape[1] if mask.dim() == 2 else -1
+        if words < (max_nodes + 31) // 32:                # none has no address, which stands for chains
+            raise ValueError("mask must be [n_tokens, words] with a bit for each of max_nodes nodes")
         mask = _ints("mask", mask, (n_tokens, words), index, device)
     rules = None
     if softcap or window or slopes is not None or starts is not None:

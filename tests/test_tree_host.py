@@ -214,6 +214,20 @@ def test_a_window_is_refused_whatever_was_called_before(door):     # noqa: F811
         assert door.calls[-1][0] == "attn_decode_tree"
 
 
+def test_a_mask_of_too_few_words_is_refused(door):                # noqa: F811
+    """One of no words has no address, and would stand for chains."""
+    import torch
+    cache, table, pos = _pool_and_ids()
+    i32 = dict(dtype=torch.int32)
+    depths = torch.zeros(33, **i32)
+    for mask in (torch.zeros(33, 0, **i32), torch.zeros(33, 1, **i32), torch.zeros(33, **i32)):
+        with pytest.raises(ValueError, match="mask"):
+            pkg.tree_decode_attention(cache, table, pos, torch.zeros(33, 4, 64), mask=mask, depths=depths)
+    assert not door.calls
+    pkg.tree_decode_attention(cache, table, pos, torch.zeros(33, 4, 64), mask=torch.zeros(33, 2, **i32), depths=depths)
+    assert door.calls[-1][1][13] and door.calls[-1][1][14] == 2
+
+
 def test_headers_and_binding_agree(lib):
     text = "".join(open(cuda_build.ROOT + "/include/%s.h" % h).read() for h in ("attn_tree", "attn_pages"))
     for name, value in re.findall(r"#define (ATTN_\w+) (0x[0-9A-Fa-f]+)u", text):
