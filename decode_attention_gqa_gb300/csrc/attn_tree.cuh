@@ -850,6 +850,22 @@ struct Tree {
         if (C::F8 && HD == 64) return to + row * 64 + (((u ^ (row >> 1)) & 3) << 4);
         return to + (u >> 3) * 16384 + row * 128 + (((u ^ row) & 7) << 4);
     }
+    // One part of q's own type: copied only
+    __device__ __forceinline__ bool as_it_is() const
+    {
+        return !C::F8 && PARTS == 1 && a.q_type == (std::is_same<MT, __half>::value ? kTypeF16 : kTypeBf16);
+    }
+    // Whether the thread's row of such a Q is finite
+    __device__ __forceinline__ bool finite_q(int my) const
+    {
+        uint32_t m = 0;
+#pragma unroll 4
+        for (int u = 0; u < HD / 8; ++u) {
+            const uint4 x = lds128(q_place(my, 0, u));
+            m = __vmaxu2(__vmaxu2(m, x.x & 0x7fff7fffu), __vmaxu2(__vmaxu2(x.y & 0x7fff7fffu, x.z & 0x7fff7fffu), x.w & 0x7fff7fffu));
+        }
+        return max(m >> 16, m & 0xffffu) < (std::is_same<MT, __half>::value ? 0x7C00u : 0x7F80u);
+    }
     __device__ __forceinline__ float stage_q(const TreeSeg &g, const Row &r, int w, int quad, int lane)
     {
         const int my = quad * 32 + lane;
@@ -869,7 +885,7 @@ struct Tree {
         }
         asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
         group_sync();
-        if (!C::F8 && PARTS == 1 && a.q_type == (f16 ? kTypeF16 : kTypeBf16)) return 1.f;   // as it is
+        if (as_it_is()) return 1.f;
         const bool bf = a.q_type == kTypeBf16;
         const int mine = r.t >= 0 ? HD / 8 : 0;                       // units of 8 elements
         float sc = 1.f, inv = 1.f;
@@ -896,6 +912,8 @@ struct Tree {
                 sc *= 0.0078125f;
                 inv *= 128.f;
             }
+            // a row with an infinity or NaN: every score NaN (8-bit parts end at 448, and one 16-bit part of -inf hides rows)
+            if (m >= 0x7f800000u) inv = __uint_as_float(0x7fffffffu);
         }
         group_sync();                                                 // the other warpgroup has read the row too
         auto pair_of = [&](uint32_t w) {                              // two elements, scaled
@@ -1197,6 +1215,8 @@ struct Tree {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive(q_ready());
+            // while the first S is made (stage_q sees to it where it looks at the row itself)
+            if (as_it_is() && r.t >= 0 && !finite_q(my)) r.c = __uint_as_float(0x7fffffffu);
 
             float m = -INFINITY, l = 0.f;
 #pragma unroll 1

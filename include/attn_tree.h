@@ -91,7 +91,9 @@ attn_status attn_rope_append_tree(const attn_paged_cache *cache, const int32_t *
  *              aligned; NULL: the library-owned buffer (see attn_decode)
  * Rows that a node does not see never change its result, whatever they hold, and
  * neither do pages that are not there (ATTN_DEVERR_BAD_PAGE). Rows that
- * are seen are taken to hold finite values, as in attn_decode_paged.
+ * are seen are taken to hold finite values, as in attn_decode_paged. A query with an
+ * infinity or NaN gives NaN (0 where it sees nothing), and changes no other (with
+ * a softcap: none beyond its accuracy).
  * Scores, softmax statistics and sums are 32 bits. q and the weights enter the
  * products in 16-bit parts: with F32 queries two each (of binary16, 22 bits, over F16
  * and E4M3 caches; of bfloat16, 16 bits, over BF16 ones); with 16-bit queries one

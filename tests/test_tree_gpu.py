@@ -525,6 +525,51 @@ def test_a_query_of_nan_stays_alone(pkg):
         assert bool(out[3, 1].isnan().all()) and not bool(out[5, 0].isfinite().all())
 
 
+@pytest.mark.parametrize("src", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("kv", ["e4m3", "f16", "bf16"])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_queries_that_are_not_finite_give_nan(pkg, kv, src, hd):
+    """Infinities of either sign and NaN, alone in a row: NaN in all of its dimensions whatever the signs of K (keys of one sign
+    make every score +inf or -inf), 0 where it sees no row, and the bits of the call without them elsewhere. With a cap the
+    rows of a warp decide together which of two forms of tanh they take, each within the reference's bound of the result: so
+    the other rows differ by twice that at most."""
+    import torch
+    ctx, n = 300, 12
+    pool = Pool(25, kv, 1, hd, 16, (ctx,))
+    if kv == "e4m3":
+        pool.dev[0].view(torch.uint8).bitwise_and_(0x7F)
+    else:
+        pool.dev[0].abs_()
+    parents, sees, depths, mask = setup(3, (n,), 1)
+    q = np.random.default_rng(1).standard_normal((n, 4, hd)).astype(np.float32)
+    a = [pool.cache(pkg), tt(pool.table), tt(np.int32([ctx - 1]))]
+    kw = dict(mask=tt(mask), depths=tt(flat(depths)))
+    wild = q.copy()
+    put = [(0, 0, 0, -math.inf), (1, 3, hd - 1, math.inf), (4, 1, 7, math.nan), (7, 0, 40, -math.inf), (7, 1, 41, math.inf),
+           (11, 2, hd // 2, -math.inf)]
+    keep = torch.ones(n, 4, dtype=torch.bool, device="cuda")
+    for t, h, d, x in put:
+        wild[t, h, d] = x
+        keep[t, h] = False
+    k, v = ([np.abs(x) if i == 0 else x for x in pool.rows(i)] for i in range(2))
+    bound = tree.attend([tt(q).to(dtype(src)).double().cpu().numpy()], sees, depths, k, v, hd ** -0.5, kv, src,
+                        vmax=vmax_of(pool, v), softcap=20.0)[1][0]
+    for extra in ({}, dict(softcap=20.0), dict(slopes=tt(np.full(4, 0.01, np.float32))), dict(starts=tt(np.int32([ctx - 1])))):
+        for P in (0, 1, 3):
+            clean, out = (pkg.tree_decode_attention(*a, tt(x).to(dtype(src)), n_splits=P, **kw, **extra) for x in (q, wild))
+            assert bool(clean.isfinite().all())
+            if "softcap" in extra:
+                off = (out.double() - clean.double()).abs().cpu().numpy()
+                assert (off <= 2 * bound)[keep.cpu().numpy()].all()
+            else:
+                assert torch.equal(out[keep], clean[keep]), (P, extra)
+            for t, h, _, _ in put:
+                if "starts" not in extra or n - 1 in sees[0][t]:
+                    assert bool(out[t, h].isnan().all()), (t, h, P, extra)
+                else:
+                    assert bool((out[t, h] == 0).all()), (t, h, P, extra)
+
+
 def test_same_bits_again_from_any_workspace_and_in_graphs(pkg):
     import torch
     pool = Pool(18, "e4m3", 2, 128, 64, (900, 333, 40))
