@@ -435,7 +435,7 @@ attn_status attn_pages_resize(int32_t *refs, int n_pages, int32_t *block_table, 
     if (st != ATTN_OK) return st;
     if (!aligned(have, 4) || !aligned(want, 4)) return ATTN_ERR_INVALID_ARG;
     if (n_seq > 0 && (!refs || !block_table || !have || !want)) return ATTN_ERR_INVALID_ARG;
-    if (n_seq > kMaxResize) return ATTN_ERR_UNSUPPORTED;
+    if (n_seq > kMaxResize || (int64_t)n_seq * max_pages > 0x7fffffff) return ATTN_ERR_UNSUPPORTED;   // 32 bits count the entries
     if (n_seq == 0) return ATTN_OK;
     BookArgs g{};
     int sms = 0;

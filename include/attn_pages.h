@@ -34,7 +34,7 @@ extern "C" {
  * free pages, those just released among them. want[s] = 0 frees a sequence.
  *   have, want  int32 [n_seq]; values outside [0, max_pages * page_size] are
  *               clamped (ATTN_DEVERR_POSITION_CLAMPED)
- *   n_seq       at most 8192
+ *   n_seq       at most 8192, n_seq * max_pages below 2^31
  * An entry to release that is no held page of the pool sets ATTN_DEVERR_BAD_PAGE
  * (an entry of -1, of a page that was not to be had, is passed over), too few free
  * pages ATTN_DEVERR_NO_PAGE, and a sequence that is cut to a row inside a page with

@@ -148,6 +148,12 @@ def test_bookkeeping_of_more_pages_than_it_counts_is_refused(lib):
     assert _fork(lib, n_pages=(1 << 31) - 1) == UNSUPPORTED
 
 
+def test_resizing_a_table_of_more_entries_than_it_counts_is_refused(lib):
+    """What all sequences ask for is summed in 32 bits."""
+    assert _resize(lib, n_seq=8192, max_pages=1 << 18) == UNSUPPORTED
+    assert _resize(lib, n_seq=17, max_pages=(1 << 27) - 1025) == UNSUPPORTED
+
+
 @pytest.mark.parametrize("hd,nodes,splits,workspace", [
     # 8 KV heads, groups of 4: 128 slots hold 32 nodes; an SM a block, 152 of them
     (128, 32, 19, 19 * 2 * 8 * 128 * (128 + 2) * 4 + 256),
