@@ -367,8 +367,9 @@ struct Tree {
     // By a whole warp, every lane for itself: one lane's wait that the others are told of takes 330 cycles even where there
     // is nothing to wait for, this 40. Gives up after some 2^31 cycles, a second or more; the abort flag then ends
     // every wait of the block, no more tiles are asked for, and the warps run through what is left and write nothing: no
-    // branch around what follows, which would keep it out of the uniform registers. LAZY: a wait that is seldom short and may end some
-    // 100 cycles late; what it executes meanwhile is not taken from the scheduler's other warps.
+    // branch around what follows, which would keep it out of the uniform registers. (The joining kernel does not know and joins
+    // what the workspace holds; the error word tells.) LAZY: a wait that is seldom short and may end some 100 cycles late; what it
+    // executes meanwhile is not taken from the scheduler's other warps.
     template <bool LAZY = false>
     __device__ __forceinline__ void wait(uint32_t bar, unsigned parity)
     {
