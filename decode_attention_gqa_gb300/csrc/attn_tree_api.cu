@@ -41,8 +41,8 @@ struct TreePlan {
     size_t o_bytes = 0, ml_bytes = 0, workspace = 0;
 };
 
-// As many blocks for each unit (KV head, 128 slots) as make a block an SM; where that leaves SMs without one
-// (units just over half of them), enough for four rounds of blocks, whose last is nearly full; no more than
+// As many blocks for each unit (KV head, 128 slots) as make a block an SM; where that leaves more than 15 % of the SMs without
+// one (units just over half of them), enough for four rounds of blocks, whose last is nearly full; no more than
 // there are pairs of tiles at full capacity: the two warpgroups of a block take tiles in turn.
 void make_plan(const attn_paged_cache *c, int max_pages, int n_seq, int max_nodes, int n_head, int n_splits, int sm_count,
                TreePlan &pl)

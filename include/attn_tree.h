@@ -85,8 +85,9 @@ attn_status attn_rope_append_tree(const attn_paged_cache *cache, const int32_t *
  *   n_head     a multiple of n_kv_head, n_head / n_kv_head <= 64
  *   n_splits   blocks that share the call's rows, per KV head and 128 of its
  *              (node, head) pairs: each takes an equal part of the tiles (128 rows, 64
- *              at head_dim 256) of all sequences; 0: attn_tree_plan's count, which
- *              fills the GPU once
+ *              at head_dim 256) of all sequences; 0: attn_tree_plan's count: as
+ *              many as make a block an SM, or, where that leaves more than 15 % of
+ *              the SMs without one, up to four blocks an SM, in turn
  *   workspace  device buffer of the bytes attn_tree_plan reports, 256-byte
  *              aligned; NULL: the library-owned buffer (see attn_decode)
  * Rows that a node does not see never change its result, whatever they hold, and

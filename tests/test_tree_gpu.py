@@ -425,6 +425,20 @@ def test_blocks_that_cross_many_sequences(pkg, kv, hd, src, n_kv, group):
     tree_check(pkg, pool, nodes, n_kv * group, src, splits=(0, 1, 2, 3, 7, 61))
 
 
+def test_four_rounds_of_blocks(pkg):
+    """Units just over half of the SMs: with a block an SM almost half would have none, so that each unit's tiles are shared
+    by as many blocks as make four rounds."""
+    import torch
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    n_kv, group = 8, 8
+    units = sms // 2 // n_kv * n_kv + n_kv
+    nodes = (units // n_kv) * 128 // group
+    pool = Pool(26, "f16", n_kv, 64, 64, (1700, 900, 300))
+    P = pkg.attn_tree_plan(pool.cache(pkg), pool.max_pages, 3, nodes + 4, nodes, pkg.ATTN_TYPE_BF16, n_kv * group)[0]
+    assert P == 4 * sms // units and P * units > 3 * sms
+    tree_check(pkg, pool, (nodes, 1, 3), n_kv * group, "bf16", splits=(0,))
+
+
 def test_long_context(pkg):
     """A long cache: rows by a plain 64-bit form on the GPU."""
     import torch
