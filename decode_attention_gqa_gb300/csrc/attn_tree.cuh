@@ -25,11 +25,11 @@
 // are, at twice the rate, and V alone is converted.
 //
 // Work. A block serves one unit -- a KV head and 128 slots of it. The tiles that a unit has in all sequences are
-// laid end to end, and the unit's blocks (ranks; as many as make a block an SM, or four rounds of blocks where one would leave
-// too many SMs idle) take equal runs of them, the turn to another sequence counted as some more: what a block has of a sequence is its output where it has all of it, else a part
-// (reference, sum, sum p v) for attn_tree_combine. The KV heads of a rank run at the same time, so that the pieces of a row that they read are
-// asked of memory together (one row of blocks over all units in turn took 1.9 times as long over 32 sequences of up
-// to 32768 rows).
+// laid end to end, and the unit's blocks (ranks; as many as make a block an SM, or four rounds of blocks where one would
+// leave too many SMs idle) take equal runs of them, the turn to another sequence counted as some more: what a block has
+// of a sequence is its output where it has all of it, else a part (reference, sum, sum p v) for attn_tree_combine. The
+// KV heads of a rank run at the same time, so that the pieces of a row that they read are asked of memory together (one
+// row of blocks over all units in turn took 1.9 times as long over 32 sequences of up to 32768 rows).
 //
 // Warps: 8 of the softmax; 4 that convert e4m3 tiles to f16, and, in tiles that some slot does not see all
 // of, take infinities and NaN out of V (a weight of 0 would spread them; where a block's part of the sequence ends, the

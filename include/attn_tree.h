@@ -53,7 +53,8 @@ attn_status attn_tree_rules(const int32_t *parents, const int32_t *cu_tokens, in
  * attn_keep_rows moves it to the row of its depth.
  *   depths    int32 [n_tokens], or NULL: a chain, as attn_rope_append
  *   q_out     [n_tokens][n_head][head_dim] of out_type
- *   out_type  ATTN_TYPE_F32, or in_type: rounded once
+ *   out_type  ATTN_TYPE_F32, or in_type: rounded once; of in_type, q_out may be q
+ *             itself (dense)
  * E4M3: each row's angle is computed from its position.
  */
 attn_status attn_rope_append_tree(const attn_paged_cache *cache, const int32_t *block_table, int max_pages,

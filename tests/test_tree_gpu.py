@@ -683,6 +683,31 @@ def test_append_of_trees(pkg, kv, src, out, interleaved):
                 assert (err <= np.abs(host) * tree.HALF[kv] + sl.max() + 2.0 ** -25)[live].all()
 
 
+@pytest.mark.parametrize("kv", ["e4m3", "f16", "bf16"])
+@pytest.mark.parametrize("src", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_of_trees_in_place(pkg, kv, src, interleaved):
+    """q_out may be q itself, where they are of one type: the bits of the call with another."""
+    import torch
+    for hd, n_head, past, nodes in ((128, 6, (5, 31, 0), (7, 40, 1)), (64, 32, (100,), (700,)), (256, 1, (63, 2), (5, 90))):
+        parents, sees, depths, mask = setup(hd, nodes, 32)
+        ctx, t = [a + b for a, b in zip(past, nodes)], sum(nodes)
+        rng = np.random.default_rng(hd)
+        q, kn, vn = (tt(rng.standard_normal((t + 1, h, hd)).astype(np.float32)).to(dtype(src)) for h in (n_head, 2, 2))
+        cu = tt(np.cumsum((0,) + nodes).astype(np.int32))
+        dep = tt(np.concatenate([flat(depths), np.int32([3])]))
+        outs = []
+        for q_out in (torch.empty_like(q), q.clone()):
+            pool = Pool(hd, kv, 2, hd, 32, ctx)
+            q_out[t:] = q[t:]
+            given = q_out if outs else q
+            got = pkg.rope_append(pool.cache(pkg), tt(pool.table), tt(np.int32(ctx) - 1), kn, vn, q=given, q_out=q_out,
+                                  rope=pkg.Rope(hd, interleaved=interleaved), cu_tokens=cu, depths=dep)
+            assert got is q_out
+            outs.append((q_out, pool.dev[0].view(torch.uint8), pool.dev[1].view(torch.uint8)))
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(*outs))
+
+
 def test_a_tree_that_is_a_chain_appends_the_same(pkg):
     """Depths 0, 1, ...: the bits of the call without depths (16-bit caches: every row's angle is its own there too)."""
     import torch
