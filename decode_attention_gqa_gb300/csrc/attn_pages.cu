@@ -356,7 +356,7 @@ struct CopyArgs {
     int64_t page_stride, row_stride, head_stride;              // bytes
     const int4 *copies;
     unsigned *err;
-    int n, n_pages, page_size, n_kv_head, units;               // 16-byte units of a head's row
+    int n_pages, page_size, n_kv_head, units;                  // 16-byte units of a head's row
     bool heads_outer;                                          // a head's rows lie together
     FastDiv by_units, by_heads, by_rows;
 };
@@ -516,7 +516,6 @@ attn_status attn_pages_copy(const attn_paged_cache *cache, const int32_t *copies
     g.row_stride = cs.row * es;
     g.head_stride = cs.head * es;
     g.copies = reinterpret_cast<const int4 *>(copies);
-    g.n = n;
     g.n_pages = cache->n_pages;
     g.page_size = cache->page_size;
     g.n_kv_head = cache->n_kv_head;
