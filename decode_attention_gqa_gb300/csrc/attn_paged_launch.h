@@ -205,7 +205,7 @@ struct TreeRequest {
     const void *k, *v;
     int64_t page_stride, row_stride, head_stride;   // elements
     int head_dim, kv_type;
-    int parts;                // 16-bit parts of q and of the weights
+    int parts, weight_parts;  // 16-bit parts of q and of the weights
     cudaStream_t stream;
 };
 constexpr int kTreeSeqs = 64;     // sequences one launch of the attention of trees takes

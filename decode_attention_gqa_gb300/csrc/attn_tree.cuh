@@ -18,11 +18,12 @@
 // for its S. Blocks of 256 slots, two tiles of Q over the same K and V, read half as much of L2 and took 1.1 to 1.25 times as
 // long, 448 slots over 8192 rows 35 us and not 28: a warpgroup waited for its own products.)
 //
-// Parts. 16-bit queries and weights enter as one operand, f32 queries as two (the rounding, and the rounding of
-// what it left), and then the weights too: f16 over f16 and e4m3 caches (rows of q scaled by a power of two, so that nothing is
-// lost to f16's range), bf16 over bf16 caches. 16-bit queries over an e4m3 cache are split into e4m3 parts instead --
-// two hold the 8 bits of a bfloat16, three the 11 of a binary16 -- so that K's codes enter the products as they
-// are, at twice the rate, and V alone is converted.
+// Parts. 16-bit queries enter as one operand, f32 queries as two (the rounding, and the rounding of what it left), and
+// then the weights too: f16 over f16 and e4m3 caches (rows of q scaled by a power of two, so that nothing is lost to
+// f16's range), bf16 over bf16 caches. The weights of 16-bit queries are two as well where the result has as many bits as
+// one of them (queries of the cache's type), else one. 16-bit queries over an e4m3 cache are split into e4m3 parts
+// instead -- two hold the 8 bits of a bfloat16, three the 11 of a binary16 -- so that K's codes enter the products as
+// they are, at twice the rate, and V alone is converted.
 //
 // Work. A block serves one unit -- a KV head and 128 slots of it. The tiles that a unit has in all sequences are
 // laid end to end, and the unit's blocks (ranks; as many as make a block an SM, or four rounds of blocks where one would
@@ -61,9 +62,10 @@ constexpr unsigned kErrBadTree = 0x8u;        // ATTN_DEVERR_BAD_REQUEST
 constexpr int kTreeTurn = 7;                  // what another sequence costs a block, in tiles
 constexpr int kTreeDesc = 8;                  // tiles whose descriptors are kept: K runs at most 4 tiles ahead of S, S 3 of P
 
-template <int HD_, typename KV_, int PARTS_>
+// PARTS: of q; PP: of the weights
+template <int HD_, typename KV_, int PARTS_, int PP_>
 struct TreeCfg {
-    static constexpr int HD = HD_, PARTS = PARTS_;
+    static constexpr int HD = HD_, PARTS = PARTS_, PP = PP_;
     using KV = KV_;
     using MT = typename PagedMma<KV>::T;
     static constexpr bool E8 = std::is_same<KV, E4m3>::value;
@@ -303,7 +305,7 @@ __device__ __forceinline__ unsigned bit_range(int a, int b)
 
 template <class C>
 struct Tree {
-    static constexpr int HD = C::HD, PARTS = C::PARTS, TR = C::TR;
+    static constexpr int HD = C::HD, PARTS = C::PARTS, PP = C::PP, TR = C::TR;
     using MT = typename C::MT;
 
     const TreeArgs &a;
@@ -812,7 +814,7 @@ struct Tree {
 #pragma unroll
                 for (int kk = 0; kk < TR / 16; ++kk)
 #pragma unroll
-                    for (int x = 0; x < PARTS; ++x) umma_ts(one, tm, s + 32 * (kk >> 1) + 16 * x + 8 * (kk & 1), v + kk * 128, id_o);
+                    for (int x = 0; x < PP; ++x) umma_ts(one, tm, s + 32 * (kk >> 1) + 16 * x + 8 * (kk & 1), v + kk * 128, id_o);
                 bar_commit(one, o_done(b));
                 if (++b == C::NB) b = 0;
                 bar_commit(one, empty(true, vr.at));
@@ -1351,7 +1353,7 @@ struct Tree {
     static __device__ __forceinline__ void weights(const uint32_t (&v)[32], uint32_t at, uint64_t nref, const float *f, const float *vs,
                                                    uint64_t (&sum)[4])
     {
-        uint32_t h[PARTS][16];
+        uint32_t h[PP][16];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const uint64_t f2 = pack2(f[x], f[x]), vs2 = pack2(vs[x], vs[x]);
@@ -1363,17 +1365,17 @@ struct Tree {
                 if (C::E8) p = mul2(p, vs2);
                 const float2 q = unpack2(p);
                 h[0][i] = float2_to_kv2<MT>(q.x, q.y);
-                if (PARTS == 2) {
+                if (PP == 2) {
                     const float2 y = kv2_to_float2<MT>(h[0][i]);
-                    h[PARTS - 1][i] = float2_to_kv2<MT>(q.x - y.x, q.y - y.y);
+                    h[PP - 1][i] = float2_to_kv2<MT>(q.x - y.x, q.y - y.y);
                 }
             }
-            if (PARTS == 2) {                                  // in turn: all of both parts do not fit into the registers
+            if (PP == 2) {                                  // in turn: all of both parts do not fit into the registers
                 tmem_st8(at + 8 * x, h[0] + 8 * x);
-                tmem_st8(at + 16 + 8 * x, h[PARTS - 1] + 8 * x);
+                tmem_st8(at + 16 + 8 * x, h[PP - 1] + 8 * x);
             }
         }
-        if (PARTS == 1) tmem_st16(at, h[0]);
+        if (PP == 1) tmem_st16(at, h[0]);
     }
     // The weights of the first n columns times f, a power of two; whole warps.
     static __device__ __forceinline__ void scale_p(uint32_t s_at, int n, float f)
@@ -1386,9 +1388,9 @@ struct Tree {
             tmem_ld32(s_at + c, v);
             tmem_wait_ld(v);
 #pragma unroll
-            for (int i = 0; i < 16 * PARTS; ++i) v[i] = mul_kv2<MT>(v[i], f2);
+            for (int i = 0; i < 16 * PP; ++i) v[i] = mul_kv2<MT>(v[i], f2);
 #pragma unroll
-            for (int x = 0; x < PARTS; ++x) tmem_st16(s_at + c + 16 * x, v + 16 * x);
+            for (int x = 0; x < PP; ++x) tmem_st16(s_at + c + 16 * x, v + 16 * x);
         }
         tmem_wait_st();
     }
@@ -1694,7 +1696,12 @@ cudaError_t launch_tree_kernel(const TreeRequest &r)
 template <int HD, typename KV>
 cudaError_t launch_tree_for(const TreeRequest &r)
 {
-    return r.parts == 2 ? launch_tree_kernel<TreeCfg<HD, KV, 2>>(r) : launch_tree_kernel<TreeCfg<HD, KV, 1>>(r);
+    if (r.parts == 2) return launch_tree_kernel<TreeCfg<HD, KV, 2, 2>>(r);
+    if constexpr (!std::is_same<KV, E4m3>::value)
+        if (r.weight_parts == 2) return launch_tree_kernel<TreeCfg<HD, KV, 1, 2>>(r);
+    if constexpr (!std::is_same<KV, __nv_bfloat16>::value)    // bfloat16 queries over a bfloat16 cache take the form above
+        return launch_tree_kernel<TreeCfg<HD, KV, 1, 1>>(r);
+    return cudaErrorInvalidValue;
 }
 
 } // namespace attn

@@ -98,12 +98,15 @@ attn_status attn_rope_append_tree(const attn_paged_cache *cache, const int32_t *
  * a softcap: none beyond its accuracy).
  * Scores, softmax statistics and sums are 32 bits. q and the weights enter the
  * products in 16-bit parts: with F32 queries two each (of binary16, 22 bits, over F16
- * and E4M3 caches; of bfloat16, 16 bits, over BF16 ones); with 16-bit queries one
- * (F16 queries over a BF16 cache: two), so that a weight is rounded to the cache's
- * type (E4M3: binary16) before it meets V, which adds about as much as the
- * rounding of the result does. 16-bit queries over an E4M3 cache enter as two or
+ * and E4M3 caches; of bfloat16, 16 bits, over BF16 ones, fewer than the 24 that
+ * attn_decode_paged carries there). 16-bit queries enter as they are (F16 over a
+ * BF16 cache: two parts), their weights as two parts where the query has the
+ * cache's type, or is F16 over a BF16 cache, else as one of binary16: 11 bits,
+ * which beside the rounding of a BF16 result adds 1 % and beside that of an F16
+ * one (over E4M3) two fifths. 16-bit queries over an E4M3 cache enter as two or
  * three 8-bit parts that hold all their bits, but for what lies below 2^-17 of
- * their row's largest.
+ * their row's largest. So the queries' type chooses: F32 ones give weights and
+ * results more bits, at up to 2.5 times the time.
  */
 attn_status attn_decode_tree(const attn_paged_cache *cache, const int32_t *block_table, int max_pages,
                              const int32_t *positions, const int32_t *cu_tokens, int n_seq, int64_t n_tokens,

@@ -160,6 +160,16 @@ def test_trees_of_many_sizes(pkg, kv, hd, n, group, ctx):
     tree_check(pkg, pool, (n,), group, src, splits=(0, 3), what="%s %d" % (kv, hd))
 
 
+@pytest.mark.parametrize("kv", ["f16", "bf16"])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("rules", [{}, dict(softcap=30.0, window=300), dict(slopes=[0.01, 0.5, 0.1, 0.02, 0.3, 1.0])])
+def test_weights_carry_more_bits_than_a_result_of_the_caches_type(pkg, monkeypatch, kv, hd, rules):
+    """Queries of a 16-bit cache's type: the bound for weights in two parts."""
+    monkeypatch.setattr(tree, "parts_of", lambda a, b: (1, 2, kv))
+    pool = Pool(27, kv, 2, hd, 32, (2, 40, 129, 700, 1300, 260))
+    tree_check(pkg, pool, (2, 7, 1, 33, 20, 5), 6, kv, splits=(0, 1, 3), **rules)
+
+
 @pytest.mark.parametrize("kv,hd,src", [("e4m3", 128, "f32"), ("f16", 64, "f16"), ("bf16", 256, "bf16"), ("e4m3", 128, "bf16")])
 def test_chains_and_a_padded_batch(pkg, kv, hd, src):
     pool = Pool(5, kv, 2, hd, 32, (0, 5, 70, 300, 133))
