@@ -190,6 +190,7 @@ struct TreeArgs {
     int max_pages, n_pages, page_size, cap, window;
     int units;                // n_kv_head times what max_nodes has of kTreeSlots
     int ranks;                // blocks that share a unit's tiles
+    int fold;                 // tree_fold
     int q_parts;              // parts of q
     uint32_t q_bytes;         // of Q in shared memory
     int nk, nv, nrk, nrv;     // tiles of the rings of K and V, and of their 8-bit tiles that are converted
@@ -211,6 +212,13 @@ struct TreeRequest {
 constexpr int kTreeSeqs = 64;     // sequences one launch of the attention of trees takes
 constexpr int kTreeSlots = 128;         // (node, head) pairs of a KV head that a block serves
 constexpr int tree_tile(int head_dim) { return head_dim == 256 ? 64 : 128; }
+// 16-bit parts of q: one holds a 16-bit query, but for f16's in bfloat16
+constexpr int tree_parts(int q_type, int kv_type) { return q_type == kTypeF32 || (q_type == kTypeF16 && kv_type == kTypeBf16) ? 2 : 1; }
+// Tiles, a power of two of them, after which O is added to a sum in the workspace (see "Sums" in attn_tree.cuh)
+constexpr int tree_fold(int head_dim, int q_type, int kv_type)
+{
+    return tree_parts(q_type, kv_type) == 1 ? 1 << 30 : (q_type == kTypeF16 ? 16384 : 2048) / tree_tile(head_dim);
+}
 cudaError_t launch_tree_hd64_f16(const TreeRequest &r);
 cudaError_t launch_tree_hd64_bf16(const TreeRequest &r);
 cudaError_t launch_tree_hd64_e4m3(const TreeRequest &r);

@@ -25,6 +25,12 @@
 // instead -- two hold the 8 bits of a bfloat16, three the 11 of a binary16 -- so that K's codes enter the products as
 // they are, at twice the rate, and V alone is converted.
 //
+// Sums. At each step of 16 rows the tensor cores cut an accumulator off at 24 bits, always towards 0: over 30000 rows in one
+// block 7e-5 of the result was lost, over 131072 3e-4. For f32 queries O is added to a sum in the workspace every 2048
+// rows, at the place of the block's part (32 sequences of up to 32768 rows of 128, e4m3: 7.7e-5 of the result before, 4.6e-6 now,
+// 375 and 386 us; every 1024 rows 2.5e-6 and 411 us, every 512 1.4e-6 and 432 us). Results of 16 bits are rounded at 2^-12 or
+// 2^-9 of themselves; their sums run on (f16 queries over bf16, whose parts are the same code: every 16384 rows).
+//
 // Work. A block serves one unit -- a KV head and 128 slots of it. The tiles that a unit has in all sequences are
 // laid end to end, and the unit's blocks (ranks; as many as make a block an SM, or four rounds of blocks where one would
 // leave too many SMs idle) take equal runs of them, the turn to another sequence counted as some more: what a block has
@@ -1180,9 +1186,10 @@ struct Tree {
         }
     }
 
+    static constexpr float OFF = 7.f;                          // a weight at the reference is 2^7
     __device__ __forceinline__ void softmax(uint32_t tm, int from, int end, int w, int quad, int lane, int rank)
     {
-        constexpr float TAU = 8.f, OFF = 7.f;
+        constexpr float TAU = 8.f;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const int my = quad * 32 + lane;
         volatile float *refs = reinterpret_cast<volatile float *>(smem + C::OFF_REF);
@@ -1221,7 +1228,7 @@ struct Tree {
             // while the first S is made (stage_q sees to it where it looks at the row itself)
             if (as_it_is() && r.t >= 0 && !finite_q(my)) r.c = __uint_as_float(0x7fffffffu);
 
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY, l = 0.f, mm = -INFINITY;      // mm: reference of the sums on the way
 #pragma unroll 1
             for (int t = w; any && t < T; t += 2) {
                 const int b = Uses::buffer(t);
@@ -1323,6 +1330,12 @@ struct Tree {
                 refs[my] = m;
                 __syncwarp();
                 if (lane == 0) bar_arrive(ref_known(quad));
+                if (PARTS == 2 && t > 0 && (t & (a.fold - 1)) == 0) {   // the first warpgroup's
+                    wait(o_done(Uses::buffer(t - 1)), uses.parity(t - 1));
+                    tc_fence_after();
+                    fold(o_at, part_of(rank, begins), my, r.t >= 0, t == a.fold ? -1.f : mm == m ? 1.f : fmaxf(ex2(mm - m), 1.17549435e-38f));
+                    mm = m;
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane <= (quad ? 0 : idle)) bar_arrive(p_ready(b));   // for the warps without a slot too
@@ -1341,7 +1354,8 @@ struct Tree {
                 add_wild(g, r, o_at, w, lane);
             }
             // a slot whose every score is NaN keeps its NaN sum
-            finish(tm, g, r, w, quad, lane, whole, begins, rank, m == -INFINITY && l != 0.f ? 0.f : m - OFF, l, any);
+            finish(tm, g, r, w, quad, lane, whole, begins, rank, m == -INFINITY && l != 0.f ? 0.f : m - OFF, l, any,
+                   PARTS == 2 && T > a.fold, mm);
             // for the segment 32 behind: V is never that far ahead
             if (is_wild && w == 0 && quad == 0 && lane == 0)
                 atomicAnd(reinterpret_cast<unsigned *>(const_cast<int *>(flags())) + 5, ~wild);
@@ -1402,13 +1416,51 @@ struct Tree {
         return fmaxf(k, __uint_as_float(v[at + 15]));
     }
 
-    // The end of a segment: the output, or the block's part of it; each warpgroup writes half of the dimensions.
+    // Place of the block's part of a sequence in the workspace, in slots; of one that it has all of, for sums on the way.
+    __device__ __forceinline__ size_t part_of(int rank, bool begins) const
+    {
+        return ((size_t)(a.ranks == 1 ? 0 : rank * 2 + (begins ? 1 : 0)) * gridDim.x + blockIdx.x) * kTreeSlots;
+    }
+    // O of the slots to their sums on the way, those times f first (f < 0: there are none yet); O is 0 then.
+    __device__ __forceinline__ void fold(uint32_t o, size_t block, int my, bool mine, float f)
+    {
+        float4 *to = reinterpret_cast<float4 *>(a.ws_o + block * HD) + my;
+#pragma unroll 1
+        for (int c = 0; c < HD; c += 32, to += 8 * kTreeSlots) {
+            uint32_t v[32];
+            tmem_ld32(o + c, v);
+            float4 x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (mine && f >= 0.f) x[i] = ld_dep(to + i * kTreeSlots);
+            }
+            tmem_wait_ld(v);
+            if (mine) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float *y = reinterpret_cast<const float *>(v) + 4 * i;
+                    to[i * kTreeSlots] = f < 0.f ? make_float4(y[0], y[1], y[2], y[3])
+                                                 : make_float4(fmaf(x[i].x, f, y[0]), fmaf(x[i].y, f, y[1]), fmaf(x[i].z, f, y[2]),
+                                                               fmaf(x[i].w, f, y[3]));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0u;
+            __syncwarp();
+            tmem_st32(o + c, v);
+        }
+        tmem_wait_st();
+    }
+
+    // The end of a segment: the output, or the block's part of it; each warpgroup writes half of the dimensions. folded: there are
+    // sums on the way, by reference mm (of the first warpgroup).
     __device__ __forceinline__ void finish(uint32_t tm, const TreeSeg &g, const Row &r, int w, int quad, int lane, bool whole,
-                                           bool begins, int rank, float m, float l, bool any)
+                                           bool begins, int rank, float m, float l, bool any, bool folded, float mm)
     {
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         tc_fence_after();
-        const size_t block = ((size_t)(rank * 2 + (begins ? 1 : 0)) * gridDim.x + blockIdx.x) * kTreeSlots;
+        const size_t block = part_of(rank, begins);
         const int in_unit = quad * 32 + lane;
         auto put = [&](int d, const float (&y)[32], float inv) {   // 32 dimensions from d on
             if (r.t < 0) return;
@@ -1440,6 +1492,7 @@ struct Tree {
         const uint32_t box = tm + s_col(0) + lanes;
         if (any) {
             tmem_st2(box + 2 * w, __float_as_uint(m), __float_as_uint(l));
+            if (folded && w == 0) tmem_st2(box + 4, __float_as_uint(mm), 0u);
             tmem_wait_st();
         }
         tc_fence_before();
@@ -1451,6 +1504,13 @@ struct Tree {
             const float m1 = __uint_as_float(om), l1 = __uint_as_float(ol), M = fmaxf(m, m1);
             l = (m == -INFINITY ? 0.f : l * ex2(m - M)) + (m1 == -INFINITY ? 0.f : l1 * ex2(m1 - M));
             m = M;
+        }
+        float fold_f = 0.f;                                    // what the sums on the way are to be multiplied by
+        if (any && folded) {
+            uint32_t om, none;
+            tmem_ld2(box + 4, om, none);
+            mm = __uint_as_float(om) - OFF;
+            fold_f = mm == m ? 1.f : fmaxf(ex2(mm - m), 1.17549435e-38f);
         }
         const int d0 = w * (HD / 2), d1 = d0 + HD / 2;
         float f = 1.f;                                         // what O is to be multiplied by
@@ -1466,6 +1526,17 @@ struct Tree {
                 float y[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(u[i]);
+                if (folded && r.t >= 0) {
+                    const float4 *from = reinterpret_cast<const float4 *>(a.ws_o + block * HD) + (size_t)(d / 4) * kTreeSlots + in_unit;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 x = ld_dep(from + i * kTreeSlots);
+                        y[4 * i] = fmaf(x.x, fold_f, y[4 * i]);
+                        y[4 * i + 1] = fmaf(x.y, fold_f, y[4 * i + 1]);
+                        y[4 * i + 2] = fmaf(x.z, fold_f, y[4 * i + 2]);
+                        y[4 * i + 3] = fmaf(x.w, fold_f, y[4 * i + 3]);
+                    }
+                }
                 put(d, y, f);
                 __syncwarp();
             }

@@ -44,8 +44,8 @@ struct TreePlan {
 // As many blocks for each unit (KV head, 128 slots) as make a block an SM; where that leaves more than 15 % of the SMs without
 // one (units just over half of them), enough for four rounds of blocks, whose last is nearly full; no more than
 // there are pairs of tiles at full capacity: the two warpgroups of a block take tiles in turn.
-void make_plan(const attn_paged_cache *c, int max_pages, int n_seq, int max_nodes, int n_head, int n_splits, int sm_count,
-               TreePlan &pl)
+void make_plan(const attn_paged_cache *c, int max_pages, int n_seq, int max_nodes, int q_type, int n_head, int n_splits,
+               int sm_count, TreePlan &pl)
 {
     const int need = max_nodes * (n_head / c->n_kv_head);
     pl.tile = attn::tree_tile(c->head_dim);
@@ -64,6 +64,8 @@ void make_plan(const attn_paged_cache *c, int max_pages, int n_seq, int max_node
         pl.o_bytes = align256(parts * c->head_dim * sizeof(float));
         pl.ml_bytes = align256(parts * 2 * sizeof(float));
         pl.workspace = pl.o_bytes + pl.ml_bytes + align256((size_t)(seqs * mus) * 16);
+    } else if (((int64_t)max_pages * c->page_size + pl.tile - 1) / pl.tile > attn::tree_fold(c->head_dim, q_type, c->kv_type)) {
+        pl.workspace = pl.o_bytes = align256((size_t)pl.units * attn::kTreeSlots * c->head_dim * sizeof(float));
     }
 }
 
@@ -111,7 +113,7 @@ attn_status attn_tree_plan(const attn_paged_cache *cache, int max_pages, int n_s
         if (e != cudaSuccess) return fail(e);
     }
     TreePlan pl;
-    make_plan(cache, max_pages, n_seq, max_nodes, n_head, n_splits, sm_count, pl);
+    make_plan(cache, max_pages, n_seq, max_nodes, q_type, n_head, n_splits, sm_count, pl);
     if (n_splits_out) *n_splits_out = pl.n_splits;
     if (workspace_bytes_out) *workspace_bytes_out = pl.workspace;
     return ATTN_OK;
@@ -158,7 +160,7 @@ attn_status attn_decode_tree(const attn_paged_cache *cache, const int32_t *block
     cudaError_t e = attn::device_facts(&sm_count, &a.err);
     if (e != cudaSuccess) return fail(e);
     TreePlan pl;
-    make_plan(cache, max_pages, n_seq, max_nodes, n_head, n_splits, sm_count, pl);
+    make_plan(cache, max_pages, n_seq, max_nodes, q_type, n_head, n_splits, sm_count, pl);
     if (pl.units > 0x7fffffff) return ATTN_ERR_UNSUPPORTED;
     if (pl.workspace > 0) {
         if (!workspace) {
@@ -202,6 +204,7 @@ attn_status attn_decode_tree(const attn_paged_cache *cache, const int32_t *block
     // past every distance it masks nothing: a node may be as deep as max_nodes - 1 behind the last row
     a.window = window >= a.cap + max_nodes ? 0 : window;
     a.ranks = pl.n_splits;
+    a.fold = attn::tree_fold(cache->head_dim, q_type, cache->kv_type);
     a.once = (int64_t)max_nodes * a.group <= attn::kTreeSlots;
     a.qscale = qscale;
     a.softcap = softcap;
@@ -215,8 +218,7 @@ attn_status attn_decode_tree(const attn_paged_cache *cache, const int32_t *block
     r.head_stride = cs.head;
     r.head_dim = cache->head_dim;
     r.kv_type = cache->kv_type;
-    // one part holds a 16-bit query, but for f16's in bfloat16
-    r.parts = q_type == ATTN_TYPE_F32 || (q_type == ATTN_TYPE_F16 && cache->kv_type == ATTN_TYPE_BF16) ? 2 : 1;
+    r.parts = attn::tree_parts(q_type, cache->kv_type);
     // One part of a weight carries as many bits as a result of the cache's own 16-bit type: both roundings together are off by
     // 1.4 times the result's own, by up to 2.2 where few rows weigh. Two parts leave the result's; over e4m3, where they take
     // a quarter of the time more (32 sequences of up to 32768 rows 222 -> 279 us; over 16 bits 0 to 17 %), one is kept.

@@ -482,6 +482,50 @@ def test_long_context(pkg):
         assert float((out - want).norm() / want.norm()) < tol
 
 
+@pytest.mark.parametrize("kv,hd", [("e4m3", 128), ("f16", 64), ("f16", 256), ("bf16", 128), ("e4m3", 256)])
+@pytest.mark.parametrize("P", [1, 2, 5])
+def test_long_runs_of_one_block_keep_their_bits(pkg, kv, hd, P):
+    """Rows are added up on the tensor cores, which cut a sum off at 24 bits at each step (16 rows of a part): half a unit of
+    2^-23 .. 2^-24 of it on average, always towards 0. Over 2048 rows these are 256 steps, in which a sum of terms of random sign
+    grows as the square root: 256 * 2 / 3 * 2^-24 = 1.0e-5 of the result. Beside it 1e-6, or 5e-6 for the 16 bits of q and
+    weights over bf16."""
+    import torch
+    n_seq, n_kv, n, ctx, page = 3, 2, 6, 30011, 64
+    per = -(-ctx // page)
+    rng = np.random.default_rng(3)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    dt = torch.float8_e4m3fn if kv == "e4m3" else dtype(kv)
+    pools = [torch.randn(n_seq * per, page, n_kv, hd, device="cuda", generator=g).to(dt) for _ in range(2)]
+    one = [torch.ones(n_seq * per, n_kv, device="cuda")] * 2 if kv == "e4m3" else []
+    table = tt(rng.permutation(n_seq * per).astype(np.int32).reshape(n_seq, per))
+    q = torch.randn(n_seq, n, 3 * n_kv, hd, device="cuda", generator=g)
+    pos = np.int32([ctx - 1, 2000, 17000])
+    out = pkg.tree_decode_attention(pkg.PagedCache(*pools, *one), table, tt(pos), q, n_splits=P)
+    for s in range(n_seq):
+        rows = int(pos[s]) + 1
+        k, v = (p[table[s].long()].double().reshape(-1, n_kv, hd)[:rows] for p in pools)
+        ok = torch.arange(rows, device="cuda")[None] <= rows - n + torch.arange(n, device="cuda")[:, None]
+        sc = torch.einsum("tkgd,nkd->tkgn", q[s].double().view(n, n_kv, 3, hd), k) / math.sqrt(hd)
+        p = torch.softmax(torch.where(ok[:, None, None], sc, -math.inf), -1)
+        want = torch.einsum("tkgn,nkd->tkgd", p, v).reshape(n, 3 * n_kv, hd)
+        off = float((out[s] - want).norm() / want.norm())
+        assert off < 1.0e-5 + (5e-6 if kv == "bf16" else 1e-6), (s, off)
+
+
+@pytest.mark.parametrize("kv,hd,page", [("e4m3", 128, 64), ("e4m3", 64, 48), ("f16", 256, 128), ("bf16", 128, 16), ("e4m3", 256, 32)])
+def test_runs_of_many_tiles(pkg, kv, hd, page):
+    """Sums that are put by and taken up again, at references that move (page scales, slopes), in sequences that a block has all
+    of and in parts, with infinities among them."""
+    ctx, nodes = (7003, 40, 5200, 2049, 4100), (7, 9, 3, 1, 20)
+    pool = Pool(28, kv, 1, hd, page, ctx)
+    for splits in ((1, 2), (3, 7)):
+        tree_check(pkg, pool, nodes, 3, "f32", splits=splits)
+    tree_check(pkg, pool, nodes, 3, "f32", splits=(1, 3), slopes=[0.05, 0.002, -0.004], starts=[3000, 0, 17, 1, 2047])
+    if kv == "bf16":
+        tree_check(pkg, pool, nodes, 3, "f16", splits=(1, 2))
+
+
 @pytest.mark.parametrize("kv,hd,nodes", [("bf16", 64, 9), ("f16", 128, 5), ("e4m3", 128, 16), ("bf16", 256, 20)])
 def test_many_runs_over_many_tiles(pkg, kv, hd, nodes):
     """Warps that are late or early where one sequence ends and the next begins: equal bits from every run, and no wait

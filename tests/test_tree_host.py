@@ -167,6 +167,18 @@ def test_plan_fills_the_sms(hd, nodes, splits, workspace):
     assert tuple(got) == (splits, workspace)
 
 
+@pytest.mark.parametrize("kv,q,hd,rows,workspace", [
+    (E4M3, F32, 128, 4096, 16 * 128 * 128 * 4), (E4M3, F32, 128, 2048, 0), (F16, F32, 256, 2112, 16 * 128 * 256 * 4),
+    (BF16, F32, 64, 2176, 16 * 128 * 64 * 4), (E4M3, F16, 128, 65536, 0), (BF16, BF16, 128, 65536, 0), (BF16, F16, 128, 16384, 0),
+    (BF16, F16, 128, 32768, 16 * 128 * 128 * 4)])
+def test_plan_of_one_split_has_room_for_sums_on_the_way(kv, q, hd, rows, workspace):
+    """8 KV heads, 33 nodes of groups of 4: 16 units, a sum of 128 rows of f32 each where more rows than 2048 are added up
+    (f16 queries over bf16: 16384)."""
+    c = _cache(head_dim=hd, n_kv_head=8, kv_type=kv, page_size=64)
+    got = pkg.attn_tree_plan(ctypes.addressof(c), rows // 64, 2, 66, 33, q, 32, 1, sm_count=152)
+    assert tuple(got) == (1, workspace)
+
+
 def test_plan_refuses_what_the_call_does():
     def plan(cache=None, max_pages=8, n_seq=1, n_tokens=4, most=4, q_type=F32, n_head=8, P=0):
         c = cache or _cache()
