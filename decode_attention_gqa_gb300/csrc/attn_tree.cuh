@@ -780,14 +780,15 @@ struct Tree {
                 tc_fence_after();
                 const uint64_t k = k0 + (uint32_t)kr.at * (C::KSLOT >> 4);
                 const uint32_t d = tm + s_col(b);
-                uint64_t q = q0;
+                // the last part first: a sum is cut off at 24 bits at each step, of which those of the small parts cost nothing then
+                uint64_t q = q0 + (a.q_parts - 1) * (C::QPART >> 4);
 #pragma unroll 1
                 for (int x = 0; x < a.q_parts; ++x) {
 #pragma unroll
                     for (int kk = 0; kk < KK; ++kk)
                         umma_ss<C::F8>(one, d, q + ((kk >> 2) * 16384 + (kk & 3) * 32) / 16, k + ((kk >> 2) * (TR * 128) + (kk & 3) * 32) / 16,
                                        id_s, x + kk > 0);
-                    q += C::QPART >> 4;
+                    q -= C::QPART >> 4;
                 }
                 bar_commit(one, s_full(b));
                 if (++b == C::NB) b = 0;
