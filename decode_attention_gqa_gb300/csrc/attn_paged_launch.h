@@ -177,7 +177,7 @@ struct TreeArgs {
     const uint32_t *mask;     // [n_tokens][words] or null: chains
     const float *k_scale, *v_scale, *slopes;
     // Parts: block (rank * 2 + which) * units + unit of kTreeSlots slots, `which` 1 where the sequence begins in this
-    // rank's places
+    // rank's places. On the way to a part, or to an output, sums of f32 queries' (one rank: block `unit`)
     float *ws_o;              // [blocks][HD / 4][kTreeSlots][4]
     float2 *ws_ml;            // [blocks][kTreeSlots]
     int4 *ws_span;            // [units / n_kv_head][n_seq]: first place, tiles, first token, places of a rank

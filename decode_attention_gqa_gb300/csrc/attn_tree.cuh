@@ -45,9 +45,9 @@
 // time: both are written for few instructions.
 //
 // Measured (calls in a graph, the joining kernel among them): 32 sequences of 17 .. 32768 rows, trees of 5 to 16 nodes, 32/8 heads
-// of 128, e4m3, bf16 queries 217 us (1.09 GB, 5020 GB/s, 0.74 of a copy's rate); 8192 rows, 64 nodes, 28/4 heads 25.2 us; 4
-// sequences of up to 8400 rows, trees of 33 to 60 nodes, 16/2 heads of 256, capped scores, a window of 4096, bf16 31.4 us; 512
-// rows, 8 nodes, 8/2 heads, f32 queries 15.6 us. Over long rows no unit alone bounds it: a tile of 128 rows and 128 slots takes
+// of 128, e4m3, bf16 queries 215 us (1.09 GB, 5070 GB/s, 0.75 of a copy's rate); 8192 rows, 64 nodes, 28/4 heads 24.9 us; 4
+// sequences of up to 8400 rows, trees of 33 to 60 nodes, 16/2 heads of 256, capped scores, a window of 4096, bf16 35.1 us; 512
+// rows, 8 nodes, 8/2 heads, f32 queries 16.3 us. Over long rows no unit alone bounds it: a tile of 128 rows and 128 slots takes
 // some 1600 cycles, the tensor cores 1170 of them (every slot of 128, with a node or not), a warpgroup half of its
 // 3200 for each of its own, converting V 880; with half the products, without the exponentials, the sums or the
 // conversion it took 1 to 4 % less. Short calls are chains: 2500 cycles to the first table entry, 5000 for Q, a tile's
@@ -1197,7 +1197,8 @@ struct Tree {
         unsigned tiles = 0, segs = 0, refs_odd = 0;            // tiles and segments before this one; parity of the references handed on
         Uses uses;
         // Over 16-bit caches, tiles with nothing but a cap are capped on their way to weights, others with rules before (31.4 us
-        // and not 33.5 for the heads of 256 dimensions above; over e4m3 the branch cost tiles without rules 4 %).
+        // and not 33.5 for the heads of 256 dimensions above with weights in one part; over e4m3 the branch cost tiles without
+        // rules 4 %).
         const bool capped = !C::E8 && a.softcap > 0.f && !a.slopes && a.qscale > 0.f;
         const bool rules = !capped && (a.softcap > 0.f || a.slopes != nullptr || a.qscale <= 0.f);
         for (int p = from; p < end;) {

@@ -90,16 +90,17 @@ attn_status attn_rope_append_tree(const attn_paged_cache *cache, const int32_t *
  *              many as make a block an SM, or, where that leaves more than 15 % of
  *              the SMs without one, up to four blocks an SM, in turn
  *   workspace  device buffer of the bytes attn_tree_plan reports, 256-byte
- *              aligned; NULL: the library-owned buffer (see attn_decode)
+ *              aligned; NULL: the library-owned buffer (see attn_decode). One split
+ *              needs some too where F32 queries may have more than 2048 rows
  * Rows that a node does not see never change its result, whatever they hold, and
  * neither do pages that are not there (ATTN_DEVERR_BAD_PAGE). Rows that
  * are seen are taken to hold finite values, as in attn_decode_paged. A query with an
  * infinity or NaN gives NaN (0 where it sees nothing), and changes no other (with
  * a softcap: none beyond its accuracy).
- * Scores, softmax statistics and sums are 32 bits; the tensor cores, which add the
- * rows up, cut a sum off at 24 bits at every 16 rows, so that F32 results are
- * within some 5e-6 of themselves (no more than 2048 rows are added up so) and
- * those of 16 bits, in 32 bits, within 1e-4 for 30000 rows in one block. q and the weights enter the
+ * Scores, softmax statistics and sums are 32 bits. The tensor cores, which add the
+ * rows up, cut a sum off at 24 bits at every 16 rows: with F32 queries no more than
+ * 2048 rows are added up so (some 5e-6 of the result), with 16-bit ones all that a
+ * block has of a sequence (1e-4 of it after 30000 rows). q and the weights enter the
  * products in 16-bit parts: with F32 queries two each (of binary16, 22 bits, over F16
  * and E4M3 caches; of bfloat16, 16 bits, over BF16 ones, fewer than the 24 that
  * attn_decode_paged carries there). 16-bit queries enter as they are (F16 over a
@@ -109,7 +110,7 @@ attn_status attn_rope_append_tree(const attn_paged_cache *cache, const int32_t *
  * one (over E4M3) two fifths. 16-bit queries over an E4M3 cache enter as two or
  * three 8-bit parts that hold all their bits, but for what lies below 2^-17 of
  * their row's largest. So the queries' type chooses: F32 ones give weights and
- * results more bits, at up to 2.5 times the time.
+ * results more bits, at up to 1.8 times the time.
  */
 attn_status attn_decode_tree(const attn_paged_cache *cache, const int32_t *block_table, int max_pages,
                              const int32_t *positions, const int32_t *cu_tokens, int n_seq, int64_t n_tokens,
