@@ -688,6 +688,66 @@ def test_same_bits_again_from_any_workspace_and_in_graphs(pkg):
         assert all(torch.equal(o, want) for o in outs)
 
 
+@pytest.mark.parametrize("kv,hd", [("e4m3", 128), ("bf16", 64), ("f16", 256)])
+@pytest.mark.parametrize("P", [1, 4])
+def test_sums_on_the_way_in_any_workspace_and_in_graphs(pkg, kv, hd, P):
+    """Float32 queries over more rows than one sum takes: equal bits from every run, from workspaces that held anything and the
+    library's own, and from graphs on two streams at once; a workspace that is too small is refused, one of a split too."""
+    import torch
+    ctx, nodes = (9001, 300, 2177, 4500), (20, 1, 33, 7)
+    pool = Pool(29, kv, 2, hd, 64, ctx)
+    parents, sees, depths, mask = setup(3, nodes, 2)
+    t, cu = sum(nodes), np.cumsum((0,) + nodes).astype(np.int32)
+    q = tt(np.random.default_rng(1).standard_normal((t, 6, hd)).astype(np.float32))
+    cache, table, pos = pool.cache(pkg), tt(pool.table), tt(np.int32(ctx) - 1)
+    dm, dd, dcu = tt(mask), tt(flat(depths)), tt(cu)
+
+    def call(out=None):
+        return pkg.tree_decode_attention(cache, table, pos, q, mask=dm, depths=dd, cu_tokens=dcu, max_nodes=33, n_splits=P, out=out)
+    pkg.attn_read_device_error()
+    first = call()
+    assert all(torch.equal(call(), first) for _ in range(30))
+    shape = (cache, table, table.shape[1], pos, dcu, 4, t, 33, q)
+    rest = (pkg.ATTN_TYPE_F32, 6, hd ** -0.5, dm, 2, dd)
+    need = pkg.attn_tree_plan(cache, table.shape[1], 4, t, 33, pkg.ATTN_TYPE_F32, 6, P)[1]
+    assert need > 0
+    for fill in (0, 0x7F, 0xFF):
+        ws = torch.full((need + 256,), fill, dtype=torch.uint8, device="cuda")
+        out = torch.empty_like(q)
+        pkg.attn_decode_tree(*shape, out, *rest, n_splits=P, workspace=ws, workspace_bytes=need)
+        assert torch.equal(out, first)
+        assert bool((ws[need:] == fill).all())
+    with pytest.raises(pkg.AttnError) as e:
+        pkg.attn_decode_tree(*shape, out, *rest, n_splits=P, workspace=ws, workspace_bytes=need - 256)
+    assert e.value.status == pkg.ATTN_ERR_WORKSPACE
+    out = torch.empty_like(q)
+    pkg.attn_decode_tree(*shape, out, *rest, n_splits=P)          # the library's own
+    assert torch.equal(out, first)
+    outs, graphs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        o = torch.empty_like(q)
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            call(o)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            call(o)
+        outs.append(o)
+        graphs.append(g)
+    for shift in (0, 2100):
+        pos.copy_(tt(np.int32(ctx) - 1 - np.int32([shift, 0, 0, shift])))
+        want = call()
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for s, g in zip(streams, graphs):
+                with torch.cuda.stream(s):
+                    g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want) for o in outs)
+    assert pkg.attn_read_device_error() == 0
+
+
 # ---------------------------------------------------------------------------
 # The append at a tree's depths.
 # ---------------------------------------------------------------------------
