@@ -377,8 +377,8 @@ struct Tree {
     // every wait of the block, no more tiles are asked for, and the warps run through what is left and write nothing: no
     // branch around what follows, which would keep it out of the uniform registers. (The joining kernel does not know and joins
     // what the workspace holds; the error word tells.) LAZY: a wait that is seldom short and may end some 100 cycles late; what it
-    // executes meanwhile is not taken from the scheduler's other warps.
-    template <bool LAZY = false>
+    // executes meanwhile is not taken from the scheduler's other warps. LIMIT: its logarithm, in cycles.
+    template <bool LAZY = false, int LIMIT = 31>
     __device__ __forceinline__ void wait(uint32_t bar, unsigned parity)
     {
         if (!bar_try(bar, parity)) {
@@ -392,7 +392,7 @@ struct Tree {
                     done = bar_try(bar, parity);
                 }
                 if (done || flags()[1]) break;
-                if (clock64() - t0 > (1ll << 31)) {
+                if (clock64() - t0 > (1ll << LIMIT)) {
                     flags()[1] = 1;
                     atomicOr(a.err, kErrPipelineTimeout);
                     break;
@@ -409,7 +409,9 @@ struct Tree {
         __syncwarp();
         if ((threadIdx.x & 31) == 0) bar_arrive(met());
         const unsigned parity = meetings++ & 1;
-        if (lazy) wait<true>(met(), parity);
+        // warps without a slot wait for all of the block's work on a sequence, which may take seconds; those that do it give up
+        // for them too
+        if (lazy) wait<true, 38>(met(), parity);
         else wait(met(), parity);
     }
 

@@ -513,6 +513,26 @@ def test_long_runs_of_one_block_keep_their_bits(pkg, kv, hd, P):
         assert off < 1.0e-5 + (5e-6 if kv == "bf16" else 1e-6), (s, off)
 
 
+def test_a_block_may_take_seconds(pkg):
+    """One block over 2^27 rows (1.6 s; pages that stand in the table many times): warps without a slot wait longer than a wait
+    may take otherwise. Each row has its weight 2^14 times, so that the result is the one of 2^13 rows; 2^22 additions to a
+    32-bit sum of weights, each off by 2^-24 at most, may leave a quarter of it."""
+    import torch
+    page, n_pages, hd = 1024, 8, 128
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    k, v = (torch.randn(n_pages, page, 1, hd, device="cuda", generator=g).to(torch.float8_e4m3fn) for _ in range(2))
+    one = torch.ones(n_pages, 1, device="cuda")
+    table = torch.arange(2 ** 17, device="cuda", dtype=torch.int32)[None] % n_pages
+    q = torch.randn(1, 1, hd, device="cuda", generator=g)
+    pkg.attn_read_device_error()
+    out = pkg.tree_decode_attention(pkg.PagedCache(k, v, one, one), table, tt(np.int32([2 ** 27 - 1])), q, n_splits=1)
+    assert pkg.attn_read_device_error() == 0
+    sc = k.double().reshape(-1, hd) @ q[0, 0].double() / math.sqrt(hd)
+    want = torch.softmax(sc, 0) @ v.double().reshape(-1, hd)
+    assert float((out[0, 0] - want).norm() / want.norm()) < 0.25
+
+
 @pytest.mark.parametrize("kv,hd,page", [("e4m3", 128, 64), ("e4m3", 64, 48), ("f16", 256, 128), ("bf16", 128, 16), ("e4m3", 256, 32)])
 def test_runs_of_many_tiles(pkg, kv, hd, page):
     """Sums that are put by and taken up again, at references that move (page scales, slopes), in sequences that a block has all
